@@ -49,6 +49,8 @@ extern "C" {
 #define NDQ_ERR_DEVICE_FAULT 12      /* a kernel gave up on a bounded wait */
 #define NDQ_ERR_BAD_COUNT 13         /* batched tensor count < 0 */
 #define NDQ_ERR_TOO_MANY_TENSORS 14  /* no-allocation batch larger than its table */
+#define NDQ_ERR_BAD_ARG 15           /* a size or option outside its documented range */
+#define NDQ_ERR_MISALIGNED 16        /* a pointer or stride off its documented boundary */
 
 /* Output element types: the ONNX TensorProto data-type numbers of the four
  * output types DequantizePacked supports ("Signature and storage"). */
@@ -56,6 +58,10 @@ extern "C" {
 #define NDQ_FLOAT16 10
 #define NDQ_DOUBLE 11
 #define NDQ_BFLOAT16 16
+
+/* Cache code types (again the ONNX data-type numbers). */
+#define NDQ_INT8 3
+#define NDQ_FLOAT8E4M3FN 17
 
 /* Format identifiers: a closed enumeration.  0..26 are the 27 fixed GGUF
  * profiles of "Quantization formats", in the specification's table order;
@@ -312,6 +318,150 @@ int ndq_dequantize_packed_batched(const ndq_tensor_desc *descs, int n, void *wor
  * anything is enqueued; n < 0 returns NDQ_ERR_BAD_COUNT; otherwise the same
  * validation and errors as ndq_dequantize_packed_batched (minus workspace). */
 int ndq_dequantize_packed_batched_noalloc(const ndq_tensor_desc *descs, int n, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Serving operators: what a generation step over packed weights needs        */
+/* beside its products.  (No counterpart on the pages.)  A step calls         */
+/* ndq_kv_plan, then for every layer ndq_matmul_packed[_batched] (+           */
+/* ndq_lora_add), ndq_kv_append and ndq_attention_kv8.  Like the calls above  */
+/* they allocate nothing, validate on the host before any launch and run      */
+/* asynchronously on `stream`; lengths, tables and slots stay on the device   */
+/* and are never read by the host.                                            */
+/* ------------------------------------------------------------------------ */
+
+/* A key/value cache in 8-bit codes with one binary32 scale for each block of
+ * block_size tokens and head.  Block b, head h holds block_size x head_dim
+ * codes at byte ((b * kv_heads + h) * block_size) * head_dim of k and of v
+ * (token-major; 16-byte-aligned bases), standing for code * scale with scale
+ * k_scale / v_scale [b * kv_heads + h], 0 or in [2^-100, 2^100].
+ *   code_type   NDQ_FLOAT8E4M3FN or NDQ_INT8
+ *   block_size  16, 32, 64 or 128
+ *   head_dim    64 or 128
+ *   num_blocks  1 .. 2^31 - 1
+ * Block ids are int32; byte offsets are 64-bit. */
+typedef struct ndq_kv_cache {
+    void *k;
+    void *v;
+    float *k_scale;
+    float *v_scale;
+    int64_t num_blocks;
+    int32_t kv_heads;
+    int32_t block_size;
+    int32_t head_dim;
+    int32_t code_type;
+} ndq_kv_cache;
+
+/* Block tables and slot maps of one step, from request lengths.
+ *   cached, fresh   device int32 [n_req]: tokens request r holds in the cache
+ *                   and brings in this step (negative counts as 0)
+ *   free_blocks     device int32 stack of free block ids; *free_count (device
+ *                   int32, at most the stack's allocated length) of them are
+ *                   valid, the last on top
+ *   block_table     device int32 [n_req, table_width], row-major; row r holds
+ *                   the ids of its first ceil(cached / block_size) blocks and
+ *                   receives those of the blocks that the fresh tokens open
+ * Outputs (device):
+ *   q_start     int32 [n_req + 1]  exclusive prefix sums of fresh
+ *   kv_len      int32 [n_req]      cached + fresh
+ *   positions   int32 [n_tokens]   position of each fresh token (-1: padding)
+ *   slots       int64 [n_tokens]   block * block_size + position % block_size
+ *   free_left   int32 [1]          *free_count minus the blocks needed;
+ *                                  negative: that many were missing
+ * Blocks are taken from the top of the stack in request order: the i-th one
+ * is free_blocks[*free_count - 1 - i], or -1 when the stack is used up.  A
+ * token whose block is -1, or lies beyond table_width, has slot -1.  Tokens
+ * are those of request 0, then 1, ...; when the requests bring fewer than
+ * n_tokens, the rest of positions and slots is -1; when they bring more,
+ * tokens from n_tokens on are left out, with the table entries of blocks
+ * that start there.  The table is written in place and the stack is not
+ * popped: the next step starts from free_left (a second call with the same
+ * inputs writes the same values).  free_left must not alias free_count.
+ * The sum of the lengths must stay below 2^31.  n_req or n_tokens of 0 is
+ * valid (q_start[0] = 0 and free_left are still written). */
+int ndq_kv_plan(const int32_t *cached, const int32_t *fresh, int64_t n_req, int block_size,
+                const int32_t *free_blocks, const int32_t *free_count, int32_t *block_table, int64_t table_width,
+                int32_t *q_start, int32_t *kv_len, int32_t *positions, int64_t *slots, int64_t n_tokens,
+                int32_t *free_left, void *stream);
+
+/* Write new key and value rows into the cache.
+ *   k, v       device rows [n_tokens, kv_heads, head_dim] of in_dtype
+ *              (NDQ_BFLOAT16 or NDQ_FLOAT16); rows are k_stride / v_stride
+ *              elements apart, heads dense; bases and rows 16-byte aligned
+ *   slots      device int64 [n_tokens], as ndq_kv_plan writes them; a slot
+ *              outside [0, num_blocks * block_size) skips its token
+ * Tokens of one block are adjacent in the call, in slot order.  For each
+ * block they fall in, head and each of k and v, in binary32:
+ *   fresh = min(max(amax / Q, 2^-100), 2^100)  with amax the largest finite
+ *           magnitude of the block's new values and Q = 448 (E4M3) or 127
+ *           (INT8); 0 when amax is 0
+ *   s     = max(fresh, old), old the block's scale, or 0 when its first new
+ *           token sits at the block's start
+ *   code  = x / s rounded to nearest even and saturated (0 when s is 0); NaN
+ *           becomes the NaN code in E4M3 and 0 in INT8
+ * and when s > old > 0 the codes c of the block's earlier tokens become
+ * (c * old) / s, rounded the same way.  n_tokens of 0 is valid. */
+int ndq_kv_append(const ndq_kv_cache *cache, const void *k, const void *v, int in_dtype, int64_t k_stride,
+                  int64_t v_stride, const int64_t *slots, int64_t n_tokens, void *stream);
+
+/* Causal attention over the cache:
+ *   out[t, h] = sum_j softmax_j(scale * q[t, h] . K_j) V_j
+ * for the tokens j of t's request that t sees.  Request r has the queries
+ * q_start[r] .. q_start[r + 1] - 1 and kv_len[r] tokens, its queries being
+ * the last of them: query i of n sits at position kv_len[r] - n + i and sees
+ * the positions up to its own, with window > 0 only the last `window` of
+ * those.  Query heads h read cache head h / (q_heads / kv_heads).
+ *   q          device [n_tokens, q_heads, head_dim] of dtype (NDQ_BFLOAT16 or
+ *              NDQ_FLOAT16), rows q_stride elements apart, heads dense, base
+ *              and rows 16-byte aligned
+ *   block_table, table_width   as for ndq_kv_plan; tokens of an id outside
+ *              [0, num_blocks) are not seen
+ *   kv_len     device int32 [n_req] (at most table_width * block_size each,
+ *              which is at most 2^30)
+ *   q_start    device int32 [n_req + 1], or NULL when every request has
+ *              exactly one query (n_tokens == n_req)
+ *              (n_tokens * q_heads below 2^31)
+ *   max_q      an upper bound of the queries of one request (host); queries
+ *              beyond it are not computed
+ *   out        device [n_tokens, q_heads, head_dim] of dtype, dense
+ *   lse        NULL, or device binary32 [n_tokens, q_heads]: the natural
+ *              logarithm of the softmax denominator, -inf for an empty row
+ *   workspace  device buffer of ndq_attention_workspace_bytes(head_dim)
+ *              bytes, 16-byte aligned, zeroed once before its first use and
+ *              not shared by calls that may overlap (each call leaves its
+ *              counters zero again)
+ * A query that sees nothing gives 0.  What is not seen has no influence,
+ * whatever its codes stand for.  Scores, softmax statistics and sums are
+ * binary32; query values and softmax weights enter the tensor cores as
+ * binary16 scaled by powers of two (the codes are exact there).  Repeated
+ * calls give identical bits. */
+size_t ndq_attention_workspace_bytes(int head_dim);
+int ndq_attention_kv8(const ndq_kv_cache *cache, const void *q, int dtype, int64_t n_tokens, int q_heads,
+                      int64_t q_stride, const int32_t *block_table, int64_t table_width, const int32_t *kv_len,
+                      const int32_t *q_start, int64_t n_req, int64_t max_q, float scale, int64_t window, void *out,
+                      float *lse, void *workspace, size_t ws_bytes, void *stream);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *   y[m] = base[m] + scales[a] * (x[m] A[a]^T) B[a]^T,   a = index[m]
+ *   x       device bfloat16 [M, K], dense
+ *   lora_a  device bfloat16 [n_adapters, max_rank, K], dense
+ *   lora_b  device bfloat16 [n_adapters, N, max_rank], dense
+ *   ranks   device int32 [n_adapters] (0 .. max_rank; values beyond an
+ *           adapter's rank are not read into any result)
+ *   scales  device binary32 [n_adapters]
+ *   index   device int32 [M]; a row whose index is outside
+ *           [0, n_adapters) gets y = base
+ *   base, y device [M, N] of dtype (NDQ_FLOAT or NDQ_BFLOAT16), dense; they
+ *           may be the same buffer, and otherwise must not overlap
+ *   workspace  device buffer of ndq_lora_workspace_bytes(...) bytes, 16-byte
+ *           aligned; not shared by calls that may overlap
+ * 1 <= max_rank <= 128.  Products are exact and sums binary32 in a fixed
+ * order; y is rounded once.  Rows of one adapter run fastest when adjacent,
+ * any order is right.  M, N, K or n_adapters of 0 is valid. */
+size_t ndq_lora_workspace_bytes(int64_t M, int64_t max_rank, int64_t K);
+int ndq_lora_add(const void *x_bf16, int64_t M, int64_t K, const void *lora_a, const void *lora_b,
+                 int64_t n_adapters, int64_t max_rank, int64_t N, const int32_t *ranks, const float *scales,
+                 const int32_t *index, const void *base, int dtype, void *y, void *workspace, size_t ws_bytes,
+                 void *stream);
 
 /* Failure-path check (not part of the pages' contract): makes the NEXT decode
  * launch issued by the calling host thread (ndq_dequantize_packed or a

@@ -30,8 +30,10 @@ STATUS = {
     4: "NDQ_ERR_BAD_RANK", 5: "NDQ_ERR_NEGATIVE_DIM", 6: "NDQ_ERR_NOT_BLOCK_ALIGNED",
     7: "NDQ_ERR_LENGTH_MISMATCH", 8: "NDQ_ERR_OVERFLOW", 9: "NDQ_ERR_BAD_DTYPE", 10: "NDQ_ERR_WORKSPACE",
     11: "NDQ_ERR_CUDA", 12: "NDQ_ERR_DEVICE_FAULT", 13: "NDQ_ERR_BAD_COUNT", 14: "NDQ_ERR_TOO_MANY_TENSORS",
+    15: "NDQ_ERR_BAD_ARG", 16: "NDQ_ERR_MISALIGNED",
 }
 NDQ_FLOAT, NDQ_FLOAT16, NDQ_DOUBLE, NDQ_BFLOAT16 = 1, 10, 11, 16
+NDQ_INT8, NDQ_FLOAT8E4M3FN = 3, 17
 NDQ_MAX_RANK = 8
 NDQ_NUM_FORMATS = 36
 NDQ_NOALLOC_MAX_TENSORS = 1024
@@ -60,6 +62,14 @@ class ndq_matmul_desc(ctypes.Structure):
     ]
 
 
+class ndq_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("num_blocks", ctypes.c_int64), ("kv_heads", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("code_type", ctypes.c_int32),
+    ]
+
+
 _c = ctypes
 _lib.ndq_format_from_name.argtypes = [_c.c_char_p]
 _lib.ndq_format_from_name.restype = _c.c_int
@@ -84,6 +94,17 @@ _lib.ndq_matmul_packed.argtypes = [_c.c_int, _c.c_int64, _c.c_int64, _c.c_void_p
                                    _c.c_int64, _c.c_int, _c.c_int, _c.c_void_p, _c.c_void_p]
 _lib.ndq_matmul_packed_batched.argtypes = [_c.POINTER(ndq_matmul_desc), _c.c_int, _c.c_int64, _c.c_void_p,
                                            _c.c_int64, _c.c_int, _c.c_int, _c.c_void_p]
+_p, _i64 = _c.c_void_p, _c.c_int64
+_lib.ndq_kv_plan.argtypes = [_p, _p, _i64, _c.c_int, _p, _p, _p, _i64, _p, _p, _p, _p, _i64, _p, _p]
+_lib.ndq_kv_append.argtypes = [_c.POINTER(ndq_kv_cache), _p, _p, _c.c_int, _i64, _i64, _p, _i64, _p]
+_lib.ndq_attention_workspace_bytes.argtypes = [_c.c_int]
+_lib.ndq_attention_workspace_bytes.restype = _c.c_size_t
+_lib.ndq_attention_kv8.argtypes = [_c.POINTER(ndq_kv_cache), _p, _c.c_int, _i64, _c.c_int, _i64, _p, _i64, _p, _p, _i64,
+                                   _i64, _c.c_float, _i64, _p, _p, _p, _c.c_size_t, _p]
+_lib.ndq_lora_workspace_bytes.argtypes = [_i64, _i64, _i64]
+_lib.ndq_lora_workspace_bytes.restype = _c.c_size_t
+_lib.ndq_lora_add.argtypes = [_p, _i64, _i64, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _c.c_int, _p, _p, _c.c_size_t,
+                              _p]
 
 # Every symbol the header declares (checked by the CPU tests).
 EXPORTS = (
@@ -91,6 +112,8 @@ EXPORTS = (
     "ndq_status_string", "ndq_payload_geometry", "ndq_dequantize_packed", "ndq_batched_workspace_bytes",
     "ndq_dequantize_packed_batched", "ndq_get_device_fault", "ndq_dequantize_packed_batched_noalloc",
     "ndq_matmul_packed", "ndq_test_withhold_copy", "ndq_matmul_packed_batched",
+    "ndq_kv_plan", "ndq_kv_append", "ndq_attention_workspace_bytes", "ndq_attention_kv8",
+    "ndq_lora_workspace_bytes", "ndq_lora_add",
 )
 
 
@@ -306,3 +329,234 @@ def matmul_packed_batched(items, K: int, x, out_dtype=None, stream=None, weight_
 
 def get_device_fault() -> int:
     return ndq_get_device_fault()
+
+
+# ---- serving operators ------------------------------------------------------
+def ndq_kv_plan(cached: int, fresh: int, n_req: int, block_size: int, free_blocks: int, free_count: int,
+                block_table: int, table_width: int, q_start: int, kv_len: int, positions: int, slots: int,
+                n_tokens: int, free_left: int, stream: int = 0) -> int:
+    """Raw call (device pointers as integers); returns the status code."""
+    return _lib.ndq_kv_plan(cached, fresh, n_req, block_size, free_blocks, free_count, block_table, table_width,
+                            q_start, kv_len, positions, slots, n_tokens, free_left, stream)
+
+
+def ndq_kv_append(cache, k: int, v: int, in_dtype: int, k_stride: int, v_stride: int, slots: int, n_tokens: int,
+                  stream: int = 0) -> int:
+    """Raw call; `cache` is an ndq_kv_cache; returns the status code."""
+    return _lib.ndq_kv_append(cache, k, v, in_dtype, k_stride, v_stride, slots, n_tokens, stream)
+
+
+def ndq_attention_workspace_bytes(head_dim: int) -> int:
+    return _lib.ndq_attention_workspace_bytes(head_dim)
+
+
+def ndq_attention_kv8(cache, q: int, dtype: int, n_tokens: int, q_heads: int, q_stride: int, block_table: int,
+                      table_width: int, kv_len: int, q_start: int, n_req: int, max_q: int, scale: float, window: int,
+                      out: int, lse: int, workspace: int, ws_bytes: int, stream: int = 0) -> int:
+    """Raw call; `cache` is an ndq_kv_cache; returns the status code."""
+    return _lib.ndq_attention_kv8(cache, q, dtype, n_tokens, q_heads, q_stride, block_table, table_width, kv_len,
+                                  q_start, n_req, max_q, scale, window, out, lse, workspace, ws_bytes, stream)
+
+
+def ndq_lora_workspace_bytes(M: int, max_rank: int, K: int) -> int:
+    return _lib.ndq_lora_workspace_bytes(M, max_rank, K)
+
+
+def ndq_lora_add(x: int, M: int, K: int, lora_a: int, lora_b: int, n_adapters: int, max_rank: int, N: int, ranks: int,
+                 scales: int, index: int, base: int, dtype: int, y: int, workspace: int, ws_bytes: int,
+                 stream: int = 0) -> int:
+    """Raw call; returns the status code."""
+    return _lib.ndq_lora_add(x, M, K, lora_a, lora_b, n_adapters, max_rank, N, ranks, scales, index, base, dtype, y,
+                             workspace, ws_bytes, stream)
+
+
+def _check(name, x, dtype, shape, device):
+    if x.dtype != dtype or x.shape != shape or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+class KvCache:
+    """An 8-bit key/value cache: codes k, v [blocks, kv_heads, block_size,
+    head_dim] (torch.float8_e4m3fn or torch.int8) and binary32 scales k_scale,
+    v_scale [blocks, kv_heads].  Keeps the tensors and their C descriptor."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        torch = _torch()
+        code = {torch.float8_e4m3fn: NDQ_FLOAT8E4M3FN, torch.int8: NDQ_INT8}.get(k.dtype)
+        if code is None or k.dim() != 4 or not k.is_cuda:
+            raise ValueError("k must be a 4-D CUDA tensor of torch.float8_e4m3fn or torch.int8 codes")
+        _check("k", k, k.dtype, k.shape, k.device)
+        _check("v", v, k.dtype, k.shape, k.device)
+        _check("k_scale", k_scale, torch.float32, k.shape[:2], k.device)
+        _check("v_scale", v_scale, torch.float32, k.shape[:2], k.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_blocks, self.kv_heads, self.block_size, self.head_dim = k.shape
+        self.device = k.device
+        self.desc = ndq_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.num_blocks,
+                                 self.kv_heads, self.block_size, self.head_dim, code)
+
+    @classmethod
+    def empty(cls, num_blocks: int, kv_heads: int, block_size: int, head_dim: int, dtype=None, device="cuda"):
+        """A cache of uninitialised blocks (kv_append writes codes and scales)."""
+        torch = _torch()
+        shape = (num_blocks, kv_heads, block_size, head_dim)
+        dtype = dtype or torch.float8_e4m3fn
+        k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+        ks, vs = (torch.empty(shape[:2], dtype=torch.float32, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+
+class KvPlan:
+    """Outputs of kv_plan: q_start [R + 1], kv_len [R], positions [T] (int32),
+    slots [T] (int64), free_left [1] (int32)."""
+    __slots__ = ("q_start", "kv_len", "positions", "slots", "free_left")
+
+    def __init__(self, q_start, kv_len, positions, slots, free_left):
+        self.q_start, self.kv_len, self.positions, self.slots, self.free_left = q_start, kv_len, positions, slots, free_left
+
+
+def kv_plan_buffers(n_req: int, n_tokens: int, device="cuda") -> KvPlan:
+    """Output buffers of kv_plan for n_req requests and up to n_tokens tokens."""
+    torch = _torch()
+    i32 = dict(dtype=torch.int32, device=device)
+    return KvPlan(torch.empty(n_req + 1, **i32), torch.empty(n_req, **i32), torch.empty(n_tokens, **i32),
+                  torch.empty(n_tokens, dtype=torch.int64, device=device), torch.empty(1, **i32))
+
+
+def kv_plan(cached, fresh, block_size: int, free_blocks, free_count, block_table, out=None, n_tokens=None, stream=None):
+    """Block tables and slot maps of one step (see ndq_kv_plan): cached, fresh
+    [R], free_blocks [F], free_count [1] and block_table [R, width] are CUDA
+    int32 tensors; block_table is written in place.  `out` holds the outputs,
+    or `n_tokens` says how many tokens to allow for.  Returns the KvPlan."""
+    torch = _torch()
+    i32 = torch.int32
+    if (cached.dtype != i32 or fresh.dtype != i32 or free_blocks.dtype != i32 or free_count.dtype != i32
+            or block_table.dtype != i32):
+        raise ValueError("kv_plan takes int32 tensors")
+    R = cached.shape[0]
+    if fresh.shape[0] != R or block_table.dim() != 2 or block_table.shape[0] != R or free_count.numel() != 1:
+        raise ValueError("cached [R], fresh [R], block_table [R, width] and free_count [1] must agree")
+    if not (cached.is_contiguous() and fresh.is_contiguous() and free_blocks.is_contiguous()
+            and block_table.is_contiguous()):
+        raise ValueError("kv_plan takes contiguous tensors")
+    if out is None:
+        if n_tokens is None:
+            raise ValueError("kv_plan needs `out` or `n_tokens`")
+        out = kv_plan_buffers(R, n_tokens, cached.device)
+    elif out.q_start.shape[0] != R + 1 or out.kv_len.shape[0] != R or out.positions.shape != out.slots.shape:
+        raise ValueError("out does not fit the requests")
+    rc = _lib.ndq_kv_plan(cached.data_ptr(), fresh.data_ptr(), R, block_size, free_blocks.data_ptr(),
+                          free_count.data_ptr(), block_table.data_ptr(), block_table.shape[1], out.q_start.data_ptr(),
+                          out.kv_len.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(), out.slots.shape[0],
+                          out.free_left.data_ptr(), _stream_handle(stream))
+    if rc:
+        raise NdqError(rc, "kv_plan")
+    return out
+
+
+def _row_stride(name, x, heads, dim):
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}]")
+    st = x.stride()
+    if st[2] != 1 or (st[1] != dim and heads > 1):
+        raise ValueError(f"{name} must have dense heads")
+    return st[0] if x.shape[0] > 1 else heads * dim
+
+
+def kv_append(cache: KvCache, k, v, slots, stream=None) -> None:
+    """Quantise the rows k, v [T, kv_heads, head_dim] (bfloat16 or float16;
+    token strides of any multiple of 8) into `cache` at slots [T] (int64, as
+    kv_plan writes them)."""
+    torch = _torch()
+    ks, vs = (_row_stride(n, x, cache.kv_heads, cache.head_dim) for n, x in (("k", k), ("v", v)))
+    T = k.shape[0]
+    if k.dtype != v.dtype or v.shape[0] != T or slots.dtype != torch.int64 or slots.shape != (T,) or not slots.is_contiguous():
+        raise ValueError("k and v must have the same type and tokens, and slots one int64 for each")
+    rc = _lib.ndq_kv_append(cache.desc, k.data_ptr(), v.data_ptr(), out_dtype_code(k.dtype), ks, vs, slots.data_ptr(), T,
+                            _stream_handle(stream))
+    if rc:
+        raise NdqError(rc, "kv_append")
+
+
+def attention_workspace(n_req: int, n_tokens: int, q_heads: int, cache: KvCache, max_q: int = 1):
+    """A workspace for attention_kv8 calls on `cache`, of any size: zeroed
+    here, left reusable by every call.  (The sizes are accepted so that a
+    caller need not know that they do not matter.)"""
+    torch = _torch()
+    return torch.zeros(ndq_attention_workspace_bytes(cache.head_dim), dtype=torch.uint8, device=cache.device)
+
+
+def attention_kv8(q, cache: KvCache, block_table, kv_len, q_start=None, max_q=None, scale=None, window: int = 0,
+                  out=None, lse=None, workspace=None, stream=None):
+    """Causal attention of q [T, q_heads, head_dim] (bfloat16 or float16) over
+    `cache` (see ndq_attention_kv8): block_table [R, width], kv_len [R] and
+    q_start [R + 1] are CUDA int32 tensors, q_start None when every request has
+    one query.  max_q bounds the queries of one request (default: T, or 1).
+    Returns out [T, q_heads, head_dim]; lse [T, q_heads] is written if given."""
+    torch = _torch()
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, q_heads, head_dim]")
+    T, H, D = q.shape
+    qs = _row_stride("q", q, H, cache.head_dim)
+    R = kv_len.shape[0]
+    if (block_table.dtype != torch.int32 or kv_len.dtype != torch.int32 or block_table.dim() != 2
+            or block_table.shape[0] != R or not block_table.is_contiguous() or not kv_len.is_contiguous()):
+        raise ValueError("block_table must be int32 [R, width] and kv_len int32 [R]")
+    if q_start is not None and (q_start.dtype != torch.int32 or q_start.shape != (R + 1,) or not q_start.is_contiguous()):
+        raise ValueError("q_start must be int32 [R + 1]")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape and type")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()):
+        raise ValueError("lse must be float32 [tokens, q_heads]")
+    if workspace is None:
+        workspace = attention_workspace(R, T, H, cache)
+    rc = _lib.ndq_attention_kv8(
+        cache.desc, q.data_ptr(), out_dtype_code(q.dtype), T, H, qs, block_table.data_ptr(), block_table.shape[1],
+        kv_len.data_ptr(), None if q_start is None else q_start.data_ptr(), R,
+        max_q if max_q is not None else (1 if q_start is None else T), D ** -0.5 if scale is None else scale, window,
+        out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _stream_handle(stream))
+    if rc:
+        raise NdqError(rc, "attention_kv8")
+    return out
+
+
+def lora_workspace(M: int, n_adapters: int, max_rank: int, K: int, device="cuda"):
+    """A workspace for lora_add calls of up to M rows, max_rank and K."""
+    torch = _torch()
+    return torch.empty(ndq_lora_workspace_bytes(M, max_rank, K), dtype=torch.uint8, device=device)
+
+
+def lora_add(x, lora_a, lora_b, ranks, scales, index, base, out=None, workspace=None, stream=None):
+    """base + scales[a] * (x A[a]^T) B[a]^T for each row's adapter a = index[m]
+    (see ndq_lora_add): x bfloat16 [M, K], lora_a bfloat16 [n, rank, K], lora_b
+    bfloat16 [n, N, rank], ranks int32 [n], scales float32 [n], index int32 [M],
+    base float32 or bfloat16 [M, N].  out may be base.  Returns out."""
+    torch = _torch()
+    M, K = x.shape
+    nA, rank = lora_a.shape[0], lora_a.shape[1]
+    N = lora_b.shape[1]
+    bf16 = torch.bfloat16
+    if (x.dtype != bf16 or lora_a.dtype != bf16 or lora_b.dtype != bf16 or lora_a.shape != (nA, rank, K)
+            or lora_b.shape != (nA, N, rank) or base.shape != (M, N) or ranks.shape != (nA,) or scales.shape != (nA,)
+            or index.shape != (M,) or ranks.dtype != torch.int32 or index.dtype != torch.int32
+            or scales.dtype != torch.float32):
+        raise ValueError("lora_add: x [M, K], lora_a [n, r, K], lora_b [n, N, r] bfloat16, ranks [n], index [M] int32, "
+                         "scales [n] float32, base [M, N]")
+    if out is None:
+        out = torch.empty_like(base)
+    if out.dtype != base.dtype or out.shape != base.shape:
+        raise ValueError("out must have base's shape and type")
+    if not (x.is_contiguous() and lora_a.is_contiguous() and lora_b.is_contiguous() and base.is_contiguous()
+            and out.is_contiguous() and ranks.is_contiguous() and scales.is_contiguous() and index.is_contiguous()):
+        raise ValueError("lora_add takes contiguous tensors")
+    if workspace is None:
+        workspace = lora_workspace(M, nA, rank, K, x.device)
+    rc = _lib.ndq_lora_add(x.data_ptr(), M, K, lora_a.data_ptr(), lora_b.data_ptr(), nA, rank, N, ranks.data_ptr(),
+                           scales.data_ptr(), index.data_ptr(), base.data_ptr(), out_dtype_code(base.dtype),
+                           out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
+    if rc:
+        raise NdqError(rc, "lora_add")
+    return out

@@ -218,6 +218,8 @@ const char* ndq_status_string(int status) {
         case NDQ_ERR_DEVICE_FAULT: return "device fault (bounded wait expired)";
         case NDQ_ERR_BAD_COUNT: return "bad tensor count";
         case NDQ_ERR_TOO_MANY_TENSORS: return "more tensors than the no-allocation launch table holds";
+        case NDQ_ERR_BAD_ARG: return "size or option out of range";
+        case NDQ_ERR_MISALIGNED: return "misaligned pointer or stride";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,121 @@
+// ndq_attn.cuh -- what the attention kernels share: number conversions and
+// the reading of a request's lengths.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "ndq_serve.h"
+
+namespace ndq {
+namespace {
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// Two 16-bit input values to binary32.
+template <bool BF16>
+__device__ __forceinline__ void widen2(uint32_t w, float& a, float& b) {
+    if constexpr (BF16) {
+        a = __uint_as_float(w << 16);
+        b = __uint_as_float(w & 0xffff0000u);
+    } else {
+        asm("{\n.reg .f16 l, h;\nmov.b32 {l, h}, %2;\ncvt.f32.f16 %0, l;\ncvt.f32.f16 %1, h;\n}" : "=f"(a), "=f"(b) : "r"(w));
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two outputs, rounded once.
+template <bool BF16>
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+    if constexpr (BF16) {
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    } else {
+        return pack_half2(lo, hi);
+    }
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four codes to binary16 pairs (bytes 0, 1) and (2, 3); every code is exact.
+template <bool E4M3>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if constexpr (E4M3) {
+        asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    } else {
+        // c + 128 under the exponent of 1024, then minus 1152
+        const uint32_t u = w ^ 0x80808080u;
+        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+    }
+}
+
+// Bit 7 of every byte that is an E4M3 NaN code (0x7f, 0xff).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// The powers of two that bring a row of queries with the largest magnitude
+// amax to about 2^10 and back: in binary16 every bfloat16 or binary16 value of
+// the row above 2^-24 of the largest is then exact.  (0, infinity, NaN: 1.)
+__device__ __forceinline__ void row_scale(float amax, float& up, float& down) {
+    const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu);
+    if (e == 0xff || amax == 0.0f) {
+        up = down = 1.0f;
+        return;
+    }
+    int s = e - 127 - 10;  // amax in [2^(s + 10), 2^(s + 11))
+    s = s < -126 ? -126 : s;
+    up = __uint_as_float(static_cast<uint32_t>(127 - s) << 23);
+    down = __uint_as_float(static_cast<uint32_t>(127 + s) << 23);
+}
+
+// A cache scale as f * 2^e with f in [1, 2) (0: as 1, its codes count for
+// nothing or are scaled by f = 0), and 2^-e.
+__device__ __forceinline__ void split_scale(float s, float& f, float& e, float& inv) {
+    const uint32_t b = __float_as_uint(s);
+    if (!(s > 0.0f)) {  // zero (or NaN, which stays one)
+        f = s;
+        e = 0.0f;
+        inv = 1.0f;
+        return;
+    }
+    f = __uint_as_float((b & 0x007fffffu) | 0x3f800000u);
+    e = static_cast<float>(static_cast<int>(b >> 23) - 127);
+    inv = __uint_as_float((254u - (b >> 23)) << 23);
+}
+
+// Request r's first query row, queries and tokens, kept inside the buffers
+// whatever the device arrays hold.
+__device__ __forceinline__ void attn_request(const AttnParams& p, int64_t r, int64_t& q0, int32_t& n, int32_t& kv) {
+    int64_t a = r, b = r + 1;
+    if (p.q_start) {
+        a = p.q_start[r];
+        b = p.q_start[r + 1];
+        a = a < 0 ? 0 : (a > p.n_tokens ? p.n_tokens : a);
+        b = b < a ? a : (b > p.n_tokens ? p.n_tokens : b);
+    }
+    q0 = a;
+    n = static_cast<int32_t>(b - a < p.max_q ? b - a : p.max_q);
+    const int64_t most = p.width << p.c.bs_log2;
+    int64_t len = p.kv_len[r];
+    len = len < 0 ? 0 : (len > most ? most : len);
+    kv = static_cast<int32_t>(len);
+}
+
+}  // namespace
+}  // namespace ndq

@@ -1,0 +1,348 @@
+// ndq_kv.cu -- block tables and slot maps from request lengths, and the
+// append of new key/value rows to the 8-bit cache.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "ndq_serve.h"
+
+namespace ndq {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Block tables and slot maps.
+//
+// With F(r) the fresh tokens and N(r) = ceil(kv_len / bs) - ceil(cached / bs)
+// the blocks request r opens, the token t belongs to the request r with
+// sum_{<r} F <= t < sum_{<=r} F, and block b of r is the
+// (sum_{<r} N + b - ceil(cached / bs))-th one taken from the free stack.
+//
+// One launch: a CTA owns kPlanTokens tokens, scans the requests in chunks
+// that fit shared memory until it has passed its last token, and finds each
+// token's request by bisection in the chunk's prefix sums.  Every CTA repeats
+// the scan (8 bytes a request from L2): that costs less than a second launch
+// or a chained scan up to tens of thousands of requests.  CTA 0 scans all of
+// them and writes the per-request outputs.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 256;
+constexpr int kPlanPer = 8;                             // requests per thread and chunk
+constexpr int kPlanChunk = kPlanThreads * kPlanPer;     // requests per chunk
+constexpr int kPlanTokens = kPlanThreads * 4;           // tokens per CTA
+
+// Exclusive prefix of (a, b) over the CTA's threads, and the totals.
+__device__ __forceinline__ void scan_pair(uint32_t& a, uint32_t& b, uint32_t& ta, uint32_t& tb, uint2* sh) {
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const uint32_t a0 = a, b0 = b;
+#pragma unroll
+    for (uint32_t d = 1; d < 32; d <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, a, d), y = __shfl_up_sync(0xffffffffu, b, d);
+        if (lane >= d) {
+            a += x;
+            b += y;
+        }
+    }
+    if (lane == 31u) sh[warp] = make_uint2(a, b);
+    __syncthreads();
+    uint32_t pa = 0, pb = 0;
+    ta = tb = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kPlanThreads / 32; ++w) {
+        if (w == warp) {
+            pa = ta;
+            pb = tb;
+        }
+        ta += sh[w].x;
+        tb += sh[w].y;
+    }
+    a += pa - a0;
+    b += pb - b0;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const PlanParams p) {
+    __shared__ uint32_t s_q[kPlanChunk + 1];  // first token of each request of the chunk
+    __shared__ uint32_t s_n[kPlanChunk];      // blocks taken before it
+    __shared__ uint2 s_w[kPlanThreads / 32];
+    const uint32_t tid = threadIdx.x, bl = static_cast<uint32_t>(p.bs_log2), bs = 1u << bl;
+    const uint32_t t0 = blockIdx.x * kPlanTokens;
+    const uint32_t n_tokens = static_cast<uint32_t>(p.n_tokens);
+    const uint32_t t1 = t0 + kPlanTokens < n_tokens ? t0 + kPlanTokens : n_tokens;
+    const int32_t count = *p.free_count;
+    uint32_t run_q = 0, run_n = 0;
+    for (int64_t r0 = 0; r0 < p.n_req && (blockIdx.x == 0 || run_q < t1); r0 += kPlanChunk) {
+        const int64_t rt = r0 + static_cast<int64_t>(tid) * kPlanPer;
+        uint32_t q[kPlanPer], nb[kPlanPer], kv[kPlanPer], sq = 0, sn = 0;
+#pragma unroll
+        for (int i = 0; i < kPlanPer; ++i) {
+            int32_t c = 0, f = 0;
+            if (rt + i < p.n_req) {
+                c = p.cached[rt + i];
+                f = p.fresh[rt + i];
+            }
+            const uint32_t cu = c > 0 ? static_cast<uint32_t>(c) : 0u, fu = f > 0 ? static_cast<uint32_t>(f) : 0u;
+            q[i] = sq;
+            nb[i] = sn;
+            kv[i] = cu + fu;
+            sq += fu;
+            sn += ((cu + fu + bs - 1u) >> bl) - ((cu + bs - 1u) >> bl);
+        }
+        uint32_t tq, tn;
+        __syncthreads();  // the previous chunk's tokens are done with s_q, s_n and s_w
+        scan_pair(sq, sn, tq, tn, s_w);
+#pragma unroll
+        for (int i = 0; i < kPlanPer; ++i) {
+            const uint32_t j = tid * kPlanPer + i;
+            q[i] += run_q + sq;
+            s_q[j] = q[i];
+            s_n[j] = run_n + sn + nb[i];
+            if (blockIdx.x == 0 && rt + i < p.n_req) {
+                p.q_start[rt + i] = static_cast<int32_t>(q[i]);
+                p.kv_len[rt + i] = static_cast<int32_t>(kv[i]);
+            }
+        }
+        if (tid == 0) s_q[kPlanChunk] = run_q + tq;
+        __syncthreads();
+        const uint32_t end = run_q + tq;
+        for (uint32_t t = t0 + tid; t < t1; t += kPlanThreads) {
+            if (t < run_q || t >= end) continue;
+            uint32_t lo = 0, hi = kPlanChunk;  // the last request that starts at or before t
+            while (hi - lo > 1u) {
+                const uint32_t mid = (lo + hi) >> 1;
+                if (s_q[mid] <= t) lo = mid;
+                else hi = mid;
+            }
+            const int64_t r = r0 + lo;
+            const int32_t c = p.cached[r];
+            const uint32_t cu = c > 0 ? static_cast<uint32_t>(c) : 0u;
+            const uint32_t pos = cu + (t - s_q[lo]), blk = pos >> bl, had = (cu + bs - 1u) >> bl;
+            int32_t id = -1;
+            if (blk < p.width) {
+                if (blk >= had) {
+                    const uint32_t i = static_cast<uint32_t>(count - 1) - (s_n[lo] + blk - had);
+                    if (count > 0 && i < static_cast<uint32_t>(count)) id = p.free_blocks[i];
+                    if ((pos & (bs - 1u)) == 0u) p.table[r * p.width + blk] = id;
+                } else {
+                    id = p.table[r * p.width + blk];
+                }
+            }
+            p.positions[t] = static_cast<int32_t>(pos);
+            p.slots[t] = id >= 0 ? (static_cast<int64_t>(id) << bl) + (pos & (bs - 1u)) : -1;
+        }
+        run_q = end;
+        run_n += tn;
+    }
+    for (uint32_t t = t0 + tid; t < t1; t += kPlanThreads)  // padding past the last request's tokens
+        if (t >= run_q) {
+            p.positions[t] = -1;
+            p.slots[t] = -1;
+        }
+    if (blockIdx.x == 0 && tid == 0) {
+        p.q_start[p.n_req] = static_cast<int32_t>(run_q);
+        *p.free_left = count - static_cast<int32_t>(run_n);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Append: quantise new rows into the cache, one scale per block and head.
+//
+// A run is the adjacent tokens of the call that fall in one block.  One warp
+// takes a run for one head and one of K and V: the run's largest magnitude
+// gives the scale, then the rows are divided by it, rounded and stored.
+// ---------------------------------------------------------------------------
+constexpr int kAppendWarps = 4;
+constexpr int kAppendHeld = 16;  // passes of rows kept in registers between the two sweeps
+
+template <bool BF16>
+__device__ __forceinline__ float2 widen(uint32_t w) {
+    if constexpr (BF16)
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Four values over s, rounded to nearest even and saturated: the codes.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t encode4(float4 v, float s) {
+    if (!(s > 0.0f)) return 0u;
+    v.x = __fdiv_rn(v.x, s);
+    v.y = __fdiv_rn(v.y, s);
+    v.z = __fdiv_rn(v.z, s);
+    v.w = __fdiv_rn(v.w, s);
+    if constexpr (E4M3) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v.x, v.y), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v.z, v.w), __NV_SATFINITE, __NV_E4M3);
+        return lo | (hi << 16);
+    } else {
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float c = fminf(fmaxf(f[i], -127.0f), 127.0f);  // (NaN: -127 here, replaced below)
+            const int q = f[i] == f[i] ? __float2int_rn(c) : 0;
+            w |= (static_cast<uint32_t>(q) & 0xffu) << (8 * i);
+        }
+        return w;
+    }
+}
+
+template <bool E4M3>
+__device__ __forceinline__ float4 decode4(uint32_t w) {
+    if constexpr (E4M3) {
+        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3);
+        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
+        const float2 x = __half22float2(__half2(a)), y = __half22float2(__half2(b));
+        return make_float4(x.x, x.y, y.x, y.y);
+    } else {
+        return make_float4(static_cast<float>(static_cast<int8_t>(w)), static_cast<float>(static_cast<int8_t>(w >> 8)),
+                           static_cast<float>(static_cast<int8_t>(w >> 16)),
+                           static_cast<float>(static_cast<int8_t>(w >> 24)));
+    }
+}
+
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a <= FLT_MAX ? a : 0.0f;
+}
+
+// win: tokens a warp searches for runs that start among them.
+template <int D, bool E4M3, bool BF16>
+__global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendParams p, int win) {
+    constexpr int LPR = D / 4;       // lanes per row, four values each
+    constexpr int RPP = 32 / LPR;    // rows per pass of the warp
+    constexpr float kQmax = E4M3 ? 448.0f : 127.0f;
+    const uint32_t lane = threadIdx.x & 31u;
+    const int units = 2 * p.c.heads;
+    const int64_t wid = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
+    const int64_t w0 = wid / units * win;
+    if (w0 >= p.n_tokens) return;
+    const int u = static_cast<int>(wid % units), h = u >> 1;
+    const bool is_v = u & 1;
+    const int bl = p.c.bs_log2, bs = 1 << bl;
+    const int64_t limit = p.c.num_blocks << bl;
+    const uint16_t* in = (is_v ? p.v : p.k) + static_cast<int64_t>(h) * D;
+    const int64_t stride = is_v ? p.v_stride : p.k_stride;
+    uint8_t* codes = is_v ? p.c.v : p.c.k;
+    float* scales = is_v ? p.c.vs : p.c.ks;
+    const int64_t wend = w0 + win < p.n_tokens ? w0 + win : p.n_tokens;
+    // which tokens of the window start a run (lane i: token w0 + i; win <= 32)
+    bool lead = false;
+    int64_t slot = -1;
+    if (w0 + lane < wend) {
+        slot = p.slots[w0 + lane];
+        const int64_t before = w0 + lane > 0 ? p.slots[w0 + lane - 1] : -1;
+        lead = slot >= 0 && slot < limit && (before < 0 || (before >> bl) != (slot >> bl));
+    }
+    uint32_t leads = __ballot_sync(0xffffffffu, lead);
+    const uint32_t row = lane / LPR, col = (lane % LPR) * 4;
+    while (leads) {
+        const int li = __ffs(leads) - 1;
+        leads &= leads - 1;
+        const int64_t t0 = w0 + li;
+        const int64_t s0 = __shfl_sync(0xffffffffu, slot, li);
+        const int64_t blk = s0 >> bl;
+        // the run's length: up to bs tokens of the same block
+        int cnt = 0;
+        for (int i0 = 0; i0 < bs; i0 += 32) {
+            const int64_t t = t0 + i0 + lane;
+            const bool same = t < p.n_tokens && (p.slots[t] >> bl) == blk;
+            const uint32_t m = __ballot_sync(0xffffffffu, same);
+            const int k = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+            cnt += k;
+            if (k < 32) break;
+        }
+        if (cnt > bs) cnt = bs;
+        const int n_old = static_cast<int>(s0 & (bs - 1));
+        const int64_t unit = blk * p.c.heads + h;
+        const float old = n_old > 0 ? scales[unit] : 0.0f;
+        uint2 held[kAppendHeld];
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kAppendHeld; ++i) {
+            const int r = i * RPP + row;
+            held[i] = make_uint2(0u, 0u);
+            if (r < cnt) held[i] = *reinterpret_cast<const uint2*>(in + (t0 + r) * stride + col);
+        }
+#pragma unroll
+        for (int i = 0; i < kAppendHeld; ++i) {
+            const float2 a = widen<BF16>(held[i].x), b = widen<BF16>(held[i].y);
+            amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(a.x), finite_abs(a.y)), fmaxf(finite_abs(b.x), finite_abs(b.y))));
+        }
+#pragma unroll 4
+        for (int r = kAppendHeld * RPP + row; r < cnt; r += RPP) {
+            const uint2 w = *reinterpret_cast<const uint2*>(in + (t0 + r) * stride + col);
+            const float2 a = widen<BF16>(w.x), b = widen<BF16>(w.y);
+            amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(a.x), finite_abs(a.y)), fmaxf(finite_abs(b.x), finite_abs(b.y))));
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+        float fresh = 0.0f;
+        if (amax > 0.0f) fresh = fminf(fmaxf(__fdiv_rn(amax, kQmax), 0x1p-100f), 0x1p100f);
+        const float s = fmaxf(old, fresh);
+        uint8_t* out = codes + (unit << bl) * D + col;
+        if (old > 0.0f && s > old) {  // the earlier tokens' codes under the grown scale
+#pragma unroll 4
+            for (int r = row; r < n_old; r += RPP) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(out + r * D);
+                float4 v = decode4<E4M3>(*w);
+                v.x = __fmul_rn(v.x, old);
+                v.y = __fmul_rn(v.y, old);
+                v.z = __fmul_rn(v.z, old);
+                v.w = __fmul_rn(v.w, old);
+                *w = encode4<E4M3>(v, s);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAppendHeld; ++i) {
+            const int r = i * RPP + row;
+            if (r < cnt) {
+                const float2 a = widen<BF16>(held[i].x), b = widen<BF16>(held[i].y);
+                const int o = static_cast<int>(p.slots[t0 + r] & (bs - 1));
+                *reinterpret_cast<uint32_t*>(out + o * D) = encode4<E4M3>(make_float4(a.x, a.y, b.x, b.y), s);
+            }
+        }
+#pragma unroll 4
+        for (int r = kAppendHeld * RPP + row; r < cnt; r += RPP) {
+            const uint2 w = *reinterpret_cast<const uint2*>(in + (t0 + r) * stride + col);
+            const float2 a = widen<BF16>(w.x), b = widen<BF16>(w.y);
+            const int o = static_cast<int>(p.slots[t0 + r] & (bs - 1));
+            *reinterpret_cast<uint32_t*>(out + o * D) = encode4<E4M3>(make_float4(a.x, a.y, b.x, b.y), s);
+        }
+        __syncwarp();  // every lane has read the old scale
+        if (lane == 0) scales[unit] = s;
+    }
+}
+
+template <int D, bool E4M3>
+int append_typed(const AppendParams& p, bool bf16, void* stream) {
+    const int64_t units = 2 * static_cast<int64_t>(p.c.heads);
+    // One token per warp while every warp can be resident at once (a step's
+    // latency); 16 per warp for prompts, where only one token in a block
+    // starts a run and the others would cost an idle warp each.
+    const int win = p.n_tokens * units <= 152 * 48 ? 1 : 16;
+    const int64_t warps = (p.n_tokens + win - 1) / win * units;
+    const unsigned grid = static_cast<unsigned>((warps + kAppendWarps - 1) / kAppendWarps);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (bf16) k_kv_append<D, E4M3, true><<<grid, kAppendWarps * 32, 0, st>>>(p, win);
+    else k_kv_append<D, E4M3, false><<<grid, kAppendWarps * 32, 0, st>>>(p, win);
+    return static_cast<int>(cudaGetLastError());
+}
+
+}  // namespace
+
+int launch_kv_plan(const PlanParams& p, void* stream) {
+    const int64_t tiles = (p.n_tokens + kPlanTokens - 1) / kPlanTokens;
+    k_kv_plan<<<static_cast<unsigned>(tiles > 0 ? tiles : 1), kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return static_cast<int>(cudaGetLastError());
+}
+
+int launch_kv_append(const AppendParams& p, int head_dim, bool e4m3, bool bf16, void* stream) {
+    if (head_dim == 64)
+        return e4m3 ? append_typed<64, true>(p, bf16, stream) : append_typed<64, false>(p, bf16, stream);
+    return e4m3 ? append_typed<128, true>(p, bf16, stream) : append_typed<128, false>(p, bf16, stream);
+}
+
+}  // namespace ndq

@@ -1,0 +1,99 @@
+// ndq_serve.h -- launch descriptors of the serving operators (block tables,
+// 8-bit cache append, attention over that cache, low-rank adapters), shared
+// by the host ABI (ndq_serve_api.cpp) and their kernels.  Not part of the
+// public ABI.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+namespace ndq {
+
+struct PlanParams {
+    const int32_t* cached;
+    const int32_t* fresh;
+    const int32_t* free_blocks;
+    const int32_t* free_count;
+    int32_t* table;
+    int32_t* q_start;
+    int32_t* kv_len;
+    int32_t* positions;
+    int64_t* slots;
+    int32_t* free_left;
+    int64_t n_req;
+    int64_t n_tokens;
+    int64_t width;
+    int32_t bs_log2;
+};
+int launch_kv_plan(const PlanParams& p, void* stream);
+
+// The cache as the kernels see it.
+struct KvCache {
+    uint8_t* k;
+    uint8_t* v;
+    float* ks;
+    float* vs;
+    int64_t num_blocks;
+    int32_t heads;
+    int32_t bs_log2;
+};
+
+struct AppendParams {
+    KvCache c;
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t k_stride;
+    int64_t v_stride;
+    const int64_t* slots;
+    int64_t n_tokens;
+};
+int launch_kv_append(const AppendParams& p, int head_dim, bool e4m3, bool bf16, void* stream);
+
+// CTAs of an attention launch at most, and the workspace: one arrival counter
+// per CTA (zero between calls), then two partial results per CTA.
+constexpr int kAttnMaxCtas = 512;
+constexpr int kAttnRows = 16;  // (query, head) rows of one partial
+constexpr size_t attn_slot_floats(int head_dim) { return static_cast<size_t>(kAttnRows) * (head_dim + 2); }
+constexpr size_t attn_workspace_bytes(int head_dim) {
+    return kAttnMaxCtas * 4u + 2u * kAttnMaxCtas * attn_slot_floats(head_dim) * 4u;
+}
+
+struct AttnParams {
+    KvCache c;
+    const uint16_t* q;
+    void* out;
+    float* lse;
+    const int32_t* table;
+    const int32_t* kv_len;
+    const int32_t* q_start;  // or nullptr: one query per request
+    uint32_t* counters;
+    float* parts;
+    int64_t n_tokens;
+    int64_t n_req;
+    int64_t q_stride;
+    int64_t width;
+    int64_t window;  // 0: none
+    int64_t max_q;
+    int32_t q_heads;
+    int32_t group;   // query heads per cache head
+    float scale_log2;  // scale * log2(e)
+    int32_t prompt_rows;  // > 0: requests with at least this many rows are left to the prompt kernel
+};
+int launch_attention(const AttnParams& p, int head_dim, bool e4m3, bool bf16, void* stream);
+
+struct LoraParams {
+    const uint16_t* x;
+    const uint16_t* a;
+    const uint16_t* b;
+    const int32_t* ranks;
+    const float* scales;
+    const int32_t* index;
+    const void* base;
+    void* y;
+    float* t;  // workspace
+    int64_t M, K, N, nA, rmax;
+};
+size_t lora_workspace_bytes(int64_t M, int64_t rmax, int64_t K);
+int launch_lora(const LoraParams& p, bool out_f32, void* stream);
+
+}  // namespace ndq
