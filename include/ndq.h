@@ -454,7 +454,8 @@ int ndq_attention_kv8(const ndq_kv_cache *cache, const void *q, int dtype, int64
  *           may be the same buffer, and otherwise must not overlap
  *   workspace  device buffer of ndq_lora_workspace_bytes(...) bytes, 16-byte
  *           aligned; not shared by calls that may overlap
- * 1 <= max_rank <= 128.  Products are exact and sums binary32 in a fixed
+ * 1 <= max_rank <= 128, M * max_rank below 2^31.  A workspace sized for some
+ * M, max_rank and K serves smaller ones.  Products are exact and sums binary32 in a fixed
  * order; y is rounded once.  Rows of one adapter run fastest when adjacent,
  * any order is right.  M, N, K or n_adapters of 0 is valid. */
 size_t ndq_lora_workspace_bytes(int64_t M, int64_t max_rank, int64_t K);

@@ -370,6 +370,13 @@ def ndq_lora_add(x: int, M: int, K: int, lora_a: int, lora_b: int, n_adapters: i
                              workspace, ws_bytes, stream)
 
 
+def _raw_stream(stream, device) -> int:
+    # (the handle alone: building a torch.cuda.Stream for each call costs microseconds)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
+
+
 def _check(name, x, dtype, shape, device):
     if x.dtype != dtype or x.shape != shape or not x.is_contiguous() or x.device != device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
@@ -448,7 +455,7 @@ def kv_plan(cached, fresh, block_size: int, free_blocks, free_count, block_table
     rc = _lib.ndq_kv_plan(cached.data_ptr(), fresh.data_ptr(), R, block_size, free_blocks.data_ptr(),
                           free_count.data_ptr(), block_table.data_ptr(), block_table.shape[1], out.q_start.data_ptr(),
                           out.kv_len.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(), out.slots.shape[0],
-                          out.free_left.data_ptr(), _stream_handle(stream))
+                          out.free_left.data_ptr(), _raw_stream(stream, cached.device))
     if rc:
         raise NdqError(rc, "kv_plan")
     return out
@@ -473,7 +480,7 @@ def kv_append(cache: KvCache, k, v, slots, stream=None) -> None:
     if k.dtype != v.dtype or v.shape[0] != T or slots.dtype != torch.int64 or slots.shape != (T,) or not slots.is_contiguous():
         raise ValueError("k and v must have the same type and tokens, and slots one int64 for each")
     rc = _lib.ndq_kv_append(cache.desc, k.data_ptr(), v.data_ptr(), out_dtype_code(k.dtype), ks, vs, slots.data_ptr(), T,
-                            _stream_handle(stream))
+                            _raw_stream(stream, k.device))
     if rc:
         raise NdqError(rc, "kv_append")
 
@@ -517,7 +524,7 @@ def attention_kv8(q, cache: KvCache, block_table, kv_len, q_start=None, max_q=No
         kv_len.data_ptr(), None if q_start is None else q_start.data_ptr(), R,
         max_q if max_q is not None else (1 if q_start is None else T), D ** -0.5 if scale is None else scale, window,
         out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        _stream_handle(stream))
+        _raw_stream(stream, q.device))
     if rc:
         raise NdqError(rc, "attention_kv8")
     return out
@@ -556,7 +563,7 @@ def lora_add(x, lora_a, lora_b, ranks, scales, index, base, out=None, workspace=
         workspace = lora_workspace(M, nA, rank, K, x.device)
     rc = _lib.ndq_lora_add(x.data_ptr(), M, K, lora_a.data_ptr(), lora_b.data_ptr(), nA, rank, N, ranks.data_ptr(),
                            scales.data_ptr(), index.data_ptr(), base.data_ptr(), out_dtype_code(base.dtype),
-                           out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
+                           out.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, x.device))
     if rc:
         raise NdqError(rc, "lora_add")
     return out

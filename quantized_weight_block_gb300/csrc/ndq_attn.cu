@@ -21,11 +21,15 @@
 // codes come through a ring of asynchronous copies in shared memory that is
 // private to the lane which consumes them (the copies only hide latency:
 // nothing is exchanged), are widened to binary16 in registers (exact) and go
-// through mma.sync m16n8k16: S = Q K^T with the head dimension permuted so
-// that a lane's 16-byte copy is its operand, then O += P V with the
-// accumulator layout of S as the operand of P.  (With 16 rows the tensor
-// cores have next to nothing to do; tcgen05 would want the codes widened
-// through shared memory first, four times the traffic of the copy itself.)
+// through mma.sync m16n8k16 with the tokens on the 16-row side and 8 (or
+// twice 8) query rows on the other: S^T = K Q^T with the head dimension
+// permuted so that a lane's 16-byte copy is its operand, then O^T += V^T P^T
+// with P^T transposed in registers (movmatrix).  A code is widened once for
+// all the rows.  (With so few rows the tensor cores have next to nothing to
+// do; tcgen05 would want the codes widened through shared memory first, four
+// times the traffic of the copy itself.)  The running maximum moves only when
+// a score passes it by 8 (weights up to 2^8: far from binary16's limit), so
+// most tiles need no exchange between lanes at all.
 //
 // Scales.  K's scale multiplies a tile's scores.  V's scale f * 2^e (f in
 // [1, 2)) joins the exponent, t = s + e, so that the weights 2^(t - m) f
@@ -46,16 +50,12 @@ constexpr int kRowWarps = 8;
 constexpr int kRowThreads = kRowWarps * 32;
 constexpr int kRowTile = 16;                       // tokens per warp tile
 constexpr int kRowUnit = kRowWarps * kRowTile;     // tokens per unit of work
-constexpr int kRowStages = 3;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -91,6 +91,7 @@ struct Req {
     int32_t tiles; // row tiles per cache head
 };
 
+template <int ROWS>
 __device__ __forceinline__ Req request(const AttnParams& p, int64_t r) {
     Req x;
     attn_request(p, r, x.q0, x.n, x.kv);
@@ -101,34 +102,41 @@ __device__ __forceinline__ Req request(const AttnParams& p, int64_t r) {
         x.lo = first > 0 ? static_cast<int32_t>(first) & ~(kRowTile - 1) : 0;
     }
     x.units = x.kv > x.lo ? (x.kv - x.lo + kRowUnit - 1) / kRowUnit : 1;
-    x.tiles = static_cast<int32_t>((static_cast<int64_t>(x.n) * p.group + kAttnRows - 1) / kAttnRows);
+    x.tiles = (x.n * p.group + ROWS - 1) / ROWS;
     return x;
 }
 
-template <int D, bool HALF>
+// NT: n-tiles of 8 rows.  Two CTAs on an SM where the accumulators (NT D / 8
+// registers) leave room, else one with a deeper ring.
+template <int D, int NT>
 struct RowSmem {
-    static constexpr int kRows = HALF ? 8 : 16;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kCtas = NT * D <= 128 ? 2 : 1;
+    static constexpr int kStages = D == 64 ? 6 : (kCtas == 2 ? 3 : 6);
     static constexpr int kStage = 2 * kRowTile * D;                          // one warp's K and V tile
-    static constexpr int kRing = kRowWarps * kRowStages * kStage;
+    static constexpr int kRing = kRowWarps * kStages * kStage;
     static constexpr int kMerge = kRowWarps * kRows * (D + 4) * 4;           // one partial per warp
     static constexpr int kBytes = kRing > kMerge ? kRing : kMerge;
 };
 
-template <int D, bool E4M3, bool BF16, bool HALF>
-__global__ void __launch_bounds__(kRowThreads, HALF ? 2 : 1) k_attn_rows(const AttnParams p) {
-    using Sm = RowSmem<D, HALF>;
-    constexpr int kRows = Sm::kRows;
-    constexpr int KS = D / 16;       // k-steps of a score
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int D, bool E4M3, bool BF16, int NT>
+__global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_rows(const AttnParams p) {
+    using Sm = RowSmem<D, NT>;
+    constexpr int kRows = Sm::kRows, ST = Sm::kStages;
+    constexpr int KS = D / 16;       // k-steps of a score, m-tiles of a head
     constexpr int KC = D / 64;       // 16-byte pieces of a token's K per lane
-    constexpr int VB = D / 8;        // bytes of a token's V per lane; n-tiles of a head
-    constexpr int OR = HALF ? 2 : 4;
+    constexpr int VB = D / 8;        // bytes of a token's V per lane
     constexpr uint64_t kSlot = kAttnRows * (D + 2);  // attn_slot_floats(D)
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ uint64_t s_sum[kRowWarps];
     __shared__ int64_t s_r, s_base;
-    __shared__ float s_sc[kRowWarps][kRowStages][2];
-    __shared__ int32_t s_id[kRowWarps][kRowStages];
-    __shared__ float s_m[kRowWarps][kAttnRows], s_l[kRowWarps][kAttnRows];
+    __shared__ float s_m[kRowWarps][kRows], s_l[kRowWarps][kRows];
     __shared__ uint32_t s_last;
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
     const int bl = p.c.bs_log2;
@@ -139,7 +147,7 @@ __global__ void __launch_bounds__(kRowThreads, HALF ? 2 : 1) k_attn_rows(const A
     for (int64_t i = 0; i < per; ++i) {
         const int64_t r = tid * per + i;
         if (r < p.n_req) {
-            const Req x = request(p, r);
+            const Req x = request<kRows>(p, r);
             mine += static_cast<uint64_t>(x.tiles) * p.c.heads * x.units;
         }
     }
@@ -170,9 +178,9 @@ __global__ void __launch_bounds__(kRowThreads, HALF ? 2 : 1) k_attn_rows(const A
     int64_t r = s_r;
     uint64_t base = static_cast<uint64_t>(s_base);  // first unit of request r
 
-    const uint32_t my_ring = smem_u32(ring) + warp * kRowStages * Sm::kStage + lane * 16;
+    const uint32_t my_ring = smem_u32(ring) + warp * ST * Sm::kStage + lane * 16;
     while (u < u_end) {
-        const Req x = request(p, r);
+        const Req x = request<kRows>(p, r);
         const uint64_t ru = static_cast<uint64_t>(x.tiles) * p.c.heads * x.units;
         if (u >= base + ru) {
             base += ru;
@@ -184,16 +192,67 @@ __global__ void __launch_bounds__(kRowThreads, HALF ? 2 : 1) k_attn_rows(const A
         const int32_t cb = static_cast<int32_t>(x.units - ca < u_end - u ? x.units : ca + (u_end - u));
         const int32_t h = static_cast<int32_t>(hj / x.tiles), j = static_cast<int32_t>(hj % x.tiles);
 
-        // the rows of this tile: row i is (query, head) = divmod(16 j + i, group)
-        const int32_t row0 = j * kAttnRows;
+        // the tokens some row of the tile sees / every row sees; row i of the
+        // tile is (query, head) = divmod(row0 + i, group)
+        const int32_t row0 = j * kRows;
         const int32_t rows_left = x.n * p.group - row0;
-        const int32_t nrows = rows_left < kAttnRows ? rows_left : kAttnRows;
-        uint32_t qf[KS][4];
-        float frow[2];
-        int32_t see_lo[2], see_hi[2];  // the tokens rows g and g + 8 see
+        const int32_t nrows = rows_left < kRows ? rows_left : kRows;
+        const int32_t qa = row0 / p.group, qb = (row0 + nrows - 1) / p.group;
+        const int64_t any_hi = static_cast<int64_t>(x.kv) - x.n + qb + 1, all_hi = static_cast<int64_t>(x.kv) - x.n + qa + 1;
+        const int64_t any_lo = p.window > 0 ? all_hi - p.window : 0, all_lo = p.window > 0 ? any_hi - p.window : 0;
+
+        // this warp's tiles: base token x.lo + 16 (8 c + warp), c = ca .. cb - 1
+        int32_t tok = x.lo + ca * kRowUnit + static_cast<int32_t>(warp) * kRowTile;
+        const int64_t seg_end = static_cast<int64_t>(x.lo) + static_cast<int64_t>(cb) * kRowUnit;
+        const int64_t tok_end = seg_end < any_hi ? seg_end : any_hi;
+        while (tok + kRowTile <= any_lo && tok < tok_end) tok += kRowUnit;
+        const int32_t ntile = tok < tok_end ? static_cast<int32_t>((tok_end - tok + kRowUnit - 1) / kRowUnit) : 0;
+        const int32_t* table = p.table + r * p.width;
+        // lane i holds the block id (-1: none) of tile 32 b + i
+        auto ids_of = [&](int32_t b) -> int32_t {
+            const int32_t i = 32 * b + static_cast<int32_t>(lane);
+            if (i >= ntile) return -1;
+            const int32_t id = table[(tok + i * kRowUnit) >> bl];
+            return id >= 0 && id < p.c.num_blocks ? id : -1;
+        };
+        int32_t ids = ids_of(0), ids_next = -1;
+        auto issue = [&](int32_t i, int32_t id) {  // tile i into stage i % ST
+            if (id >= 0) {
+                const uint64_t unit = static_cast<uint64_t>(id) * p.c.heads + static_cast<uint32_t>(h);
+                const uint64_t off = ((unit << bl) + ((tok + i * kRowUnit) & ((1 << bl) - 1))) * D;
+                const uint8_t* k = p.c.k + off + g * D + t * 16;
+                const uint8_t* v = p.c.v + off + 2 * t * D + g * VB;
+                const uint32_t d = my_ring + static_cast<uint32_t>(i % ST) * Sm::kStage;
 #pragma unroll
-        for (int half = 0; half < (HALF ? 1 : 2); ++half) {
-            const int32_t i = static_cast<int32_t>(g) + 8 * half;
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int c = 0; c < KC; ++c) cp_async16(d + (a * KC + c) * 512, k + a * 8 * D + c * 64);
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {  // tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+                    const uint8_t* src = v + ((a >> 1) * 8 + (a & 1)) * D;
+                    if constexpr (D == 128) cp_async16(d + (2 * KC + a) * 512, src);
+                    else cp_async8(d + 2 * KC * 512 + a * 256 - lane * 8, src);
+                }
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) issue(i, __shfl_sync(0xffffffffu, ids, i));
+        float ks_l = 0.0f, vs_l = 0.0f;  // lane i: the scales of tile 32 b + i
+        auto scales_of = [&](int32_t id) {
+            if (id >= 0) {
+                const uint64_t unit = static_cast<uint64_t>(id) * p.c.heads + static_cast<uint32_t>(h);
+                ks_l = p.c.ks[unit];
+                vs_l = p.c.vs[unit];
+            }
+        };
+        scales_of(ids);
+
+        uint32_t qf[NT][KS][2];
+        float frow[NT][2];  // rows 8 nt + 2 t and + 1: what turns a sum of products into a base-2 score, but for K's scale
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int32_t i = 8 * nt + static_cast<int32_t>(g);
             const bool ok = i < nrows;
             const int32_t qi = (row0 + (ok ? i : 0)) / p.group, qh = (row0 + (ok ? i : 0)) % p.group;
             const uint16_t* src = p.q + (x.q0 + qi) * p.q_stride + static_cast<int64_t>(h * p.group + qh) * D + t * 16;
@@ -214,165 +273,134 @@ __global__ void __launch_bounds__(kRowThreads, HALF ? 2 : 1) k_attn_rows(const A
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             float up, down;
             row_scale(amax, up, down);
-            frow[half] = down * p.scale_log2;
+            down *= p.scale_log2;
+            frow[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+            frow[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                qf[s][half] = pack_half2(v[s * 4] * up, v[s * 4 + 1] * up);
-                qf[s][half + 2] = pack_half2(v[s * 4 + 2] * up, v[s * 4 + 3] * up);
+                qf[nt][s][0] = pack_half2(v[s * 4] * up, v[s * 4 + 1] * up);
+                qf[nt][s][1] = pack_half2(v[s * 4 + 2] * up, v[s * 4 + 3] * up);
             }
-            const int64_t pos = static_cast<int64_t>(x.kv) - x.n + qi;
-            see_hi[half] = ok && pos >= 0 ? static_cast<int32_t>(pos) + 1 : 0;
-            see_lo[half] = p.window > 0 && pos + 1 > p.window ? static_cast<int32_t>(pos + 1 - p.window) : 0;
         }
-        if constexpr (HALF) {
-#pragma unroll
-            for (int s = 0; s < KS; ++s) qf[s][1] = qf[s][3] = 0u;
-            frow[1] = 0.0f;
-            see_lo[1] = see_hi[1] = 0;
-        }
-        // the tokens some row of the tile sees / every row sees
-        const int32_t qa = row0 / p.group, qb = (row0 + nrows - 1) / p.group;
-        int64_t any_hi = static_cast<int64_t>(x.kv) - x.n + qb + 1, all_hi = static_cast<int64_t>(x.kv) - x.n + qa + 1;
-        int64_t any_lo = 0, all_lo = 0;
-        if (p.window > 0) {
-            any_lo = all_hi - p.window;
-            all_lo = any_hi - p.window;
-        }
-
-        float o[VB][OR];
-#pragma unroll
-        for (int s = 0; s < VB; ++s)
-#pragma unroll
-            for (int e = 0; e < OR; ++e) o[s][e] = 0.0f;
-        float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
-
-        // this warp's tiles: base token x.lo + 16 (8 c + warp), c = ca .. cb - 1
-        int32_t tok = x.lo + ca * kRowUnit + static_cast<int32_t>(warp) * kRowTile;
-        const int64_t seg_end = static_cast<int64_t>(x.lo) + static_cast<int64_t>(cb) * kRowUnit;
-        const int64_t tok_end = seg_end < any_hi ? seg_end : any_hi;
-        while (tok + kRowTile <= any_lo && tok < tok_end) tok += kRowUnit;
-        const int32_t ntile = tok < tok_end ? static_cast<int32_t>((tok_end - tok + kRowUnit - 1) / kRowUnit) : 0;
-        const int32_t* table = p.table + r * p.width;
-        const uint64_t head_off = static_cast<uint64_t>(h);
-
-        // tile i of this warp into stage i % kRowStages; its block id was loaded a tile earlier
-        auto block_of = [&](int32_t i) -> int32_t {
-            if (i >= ntile) return -1;
-            const int32_t id = table[(tok + i * kRowUnit) >> bl];
-            return id >= 0 && id < p.c.num_blocks ? id : -1;
+        // the tokens row i of the tile sees: [lo, hi)
+        auto sees = [&](int32_t i, int32_t& lo, int32_t& hi) {
+            const int64_t pos = static_cast<int64_t>(x.kv) - x.n + (row0 + i) / p.group;
+            hi = i < nrows && pos >= 0 ? static_cast<int32_t>(pos) + 1 : 0;
+            lo = p.window > 0 && pos + 1 > p.window ? static_cast<int32_t>(pos + 1 - p.window) : 0;
         };
-        auto issue = [&](int32_t i, int32_t id) {
-            const uint32_t st = static_cast<uint32_t>(i % kRowStages);
-            if (i < ntile && id >= 0) {
-                const uint64_t unit = static_cast<uint64_t>(id) * p.c.heads + head_off;
-                const uint64_t off = ((unit << bl) + ((tok + i * kRowUnit) & ((1 << bl) - 1))) * D;
-                const uint8_t* k = p.c.k + off + t * 16;
-                const uint8_t* v = p.c.v + off + g * VB;
-                const uint32_t d = my_ring + st * Sm::kStage;
+
+        float o[NT][KS][4];  // O^T: m-tile s rows are head positions VB g + 2 s, + 1; columns rows 8 nt + 2 t, + 1
 #pragma unroll
-                for (int a = 0; a < 2; ++a)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < KC; ++c) cp_async16(d + (a * KC + c) * 512, k + (a * 8 + g) * D + c * 64);
+            for (int s = 0; s < KS; ++s) o[nt][s][0] = o[nt][s][1] = o[nt][s][2] = o[nt][s][3] = 0.0f;
+        float mx[NT][2], ms[NT][2], sum[NT][2];
 #pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    const uint32_t vt = (a >> 1) * 8 + 2 * t + (a & 1);
-                    if constexpr (D == 128) cp_async16(d + (2 * KC + a) * 512, v + vt * D);
-                    else cp_async8(d + 2 * KC * 512 + a * 256 - lane * 8, v + vt * D);
-                }
-                if (lane == 0) {
-                    cp_async4(smem_u32(&s_sc[warp][st][0]), p.c.ks + unit);
-                    cp_async4(smem_u32(&s_sc[warp][st][1]), p.c.vs + unit);
-                }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mx[nt][e] = -INFINITY;
+                ms[nt][e] = sum[nt][e] = 0.0f;
             }
-            if (lane == 0) s_id[warp][st] = id;
-            cp_commit();
-        };
-        int32_t next_id = block_of(0);
-#pragma unroll
-        for (int i = 0; i < kRowStages - 1; ++i) {
-            const int32_t id = next_id;
-            next_id = block_of(i + 1);
-            issue(i, id);
-        }
+
         for (int32_t i = 0; i < ntile; ++i) {
-            __syncwarp();  // every lane has read what the stage about to be refilled held
-            {
-                const int32_t id = next_id;
-                next_id = block_of(i + kRowStages);
-                issue(i + kRowStages - 1, id);
+            const int32_t i32 = i & 31;
+            if (i32 == 0) {
+                if (i > 0) {
+                    ids = ids_next;
+                    scales_of(ids);
+                }
+                ids_next = ids_of((i >> 5) + 1);
             }
-            cp_wait<kRowStages - 1>();
-            __syncwarp();
-            const uint32_t st = static_cast<uint32_t>(i % kRowStages);
-            if (s_id[warp][st] < 0) continue;
-            const float ks = s_sc[warp][st][0];
+            {
+                const int32_t q = i + ST - 1;
+                issue(q, __shfl_sync(0xffffffffu, (q >> 5) == (i >> 5) ? ids : ids_next, q & 31));
+            }
+            cp_wait<ST - 1>();
+            if (__shfl_sync(0xffffffffu, ids, i32) < 0) continue;
+            const float ks = __shfl_sync(0xffffffffu, ks_l, i32);
             float vf, ve, vinv;
-            split_scale(s_sc[warp][st][1], vf, ve, vinv);
-            const uint32_t d = my_ring + st * Sm::kStage;
-            // scores of 16 tokens
-            float sc[2][4];
+            split_scale(__shfl_sync(0xffffffffu, vs_l, i32), vf, ve, vinv);
+            const uint32_t d = my_ring + static_cast<uint32_t>(i % ST) * Sm::kStage;
+            // scores: sc[nt][0..1] token g, rows 2 t, 2 t + 1; [2..3] token g + 8
+            float sc[NT][4];
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                sc[a][0] = sc[a][1] = sc[a][2] = sc[a][3] = 0.0f;
+            for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
 #pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    const uint4 w = lds128(d + (a * KC + c) * 512);
-                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            for (int c = 0; c < KC; ++c) {
+                const uint4 w0 = lds128(d + c * 512), w1 = lds128(d + (KC + c) * 512);
+                const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        uint32_t b0, b1;
-                        widen4<E4M3>(ww[s], b0, b1);
-                        mma16816(sc[a], qf[c * 4 + s], b0, b1);
-                    }
+                for (int s = 0; s < 4; ++s) {
+                    uint32_t a[4];
+                    widen4<E4M3>(x0[s], a[0], a[2]);
+                    widen4<E4M3>(x1[s], a[1], a[3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], a, qf[nt][c * 4 + s][0], qf[nt][c * 4 + s][1]);
                 }
             }
             const int32_t tb = tok + i * kRowUnit;
             const bool masked = tb + kRowTile > all_hi || tb < all_lo;
-            float tv[2][4];
-            const float f0 = frow[0] * ks, f1 = HALF ? 0.0f : frow[1] * ks;
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                tv[a][0] = __fmaf_rn(sc[a][0], f0, ve);
-                tv[a][1] = __fmaf_rn(sc[a][1], f0, ve);
-                if constexpr (!HALF) {
-                    tv[a][2] = __fmaf_rn(sc[a][2], f1, ve);
-                    tv[a][3] = __fmaf_rn(sc[a][3], f1, ve);
-                }
-            }
+            uint32_t hidden = 0u;  // bit 4 nt + e: score e is not seen
             if (masked) {
 #pragma unroll
-                for (int a = 0; a < 2; ++a)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < OR; ++e) {
-                        const int32_t pos = tb + a * 8 + 2 * static_cast<int32_t>(t) + (e & 1);
-                        if (pos < see_lo[e >> 1] || pos >= see_hi[e >> 1]) tv[a][e] = -INFINITY;
+                    for (int e = 0; e < 2; ++e) {
+                        int32_t lo, hi;
+                        sees(8 * nt + 2 * static_cast<int32_t>(t) + e, lo, hi);
+                        const int32_t pos = tb + static_cast<int32_t>(g);
+                        if (pos < lo || pos >= hi) hidden |= 1u << (4 * nt + e);
+                        if (pos + 8 < lo || pos + 8 >= hi) hidden |= 4u << (4 * nt + e);
                     }
             }
-            uint32_t pf[4] = {0u, 0u, 0u, 0u};
+            // exponents relative to the running maximum
+            float ex[NT][4];
+            bool grow = false;
 #pragma unroll
-            for (int half = 0; half < (HALF ? 1 : 2); ++half) {
-                float tm = fmaxf(fmaxf(tv[0][2 * half], tv[0][2 * half + 1]), fmaxf(tv[1][2 * half], tv[1][2 * half + 1]));
-                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
-                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
-                const float mn = fmaxf(mx[half], tm);
-                if (__any_sync(0xffffffffu, mn > mx[half])) {
-                    const float al = mn > mx[half] ? exp2_fast(mx[half] - mn) : 1.0f;  // (mn finite where it grew)
-                    sum[half] *= al;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int s = 0; s < VB; ++s) {
-                        o[s][2 * half] *= al;
-                        o[s][2 * half + 1] *= al;
-                    }
-                    mx[half] = mn;
+                for (int e = 0; e < 4; ++e) {
+                    const float y = __fmaf_rn(sc[nt][e], frow[nt][e & 1] * ks, ve - ms[nt][e & 1]);
+                    ex[nt][e] = (hidden >> (4 * nt + e)) & 1u ? -INFINITY : y;
+                    grow |= ex[nt][e] > (mx[nt][e & 1] == -INFINITY ? -INFINITY : 8.0f);
                 }
-                const float ms = mn == -INFINITY ? 0.0f : mn;
-                const float p0 = exp2_fast(tv[0][2 * half] - ms), p1 = exp2_fast(tv[0][2 * half + 1] - ms);
-                const float p2 = exp2_fast(tv[1][2 * half] - ms), p3 = exp2_fast(tv[1][2 * half + 1] - ms);
-                sum[half] = __fmaf_rn((p0 + p1) + (p2 + p3), vinv, sum[half]);
-                pf[half] = pack_half2(p0 * vf, p1 * vf);
-                pf[half + 2] = pack_half2(p2 * vf, p3 * vf);
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float tm = fmaxf(ex[nt][e], ex[nt][e + 2]);
+                        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 4));
+                        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 8));
+                        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
+                        // (relative to ms: the new maximum is ms + tm where it grew)
+                        if (mx[nt][e] == -INFINITY ? tm > -INFINITY : tm > 0.0f) {
+                            const float mn = ms[nt][e] + tm;
+                            const float al = mx[nt][e] == -INFINITY ? 0.0f : exp2_fast(-tm);
+                            sum[nt][e] *= al;
+#pragma unroll
+                            for (int s = 0; s < KS; ++s) {
+                                o[nt][s][e] *= al;
+                                o[nt][s][e + 2] *= al;
+                            }
+                            ex[nt][e] -= tm;
+                            ex[nt][e + 2] -= tm;
+                            mx[nt][e] = ms[nt][e] = mn;
+                        }
+                    }
             }
-            // O += P V
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float p0 = exp2_fast(ex[nt][0]), p1 = exp2_fast(ex[nt][1]);
+                const float p2 = exp2_fast(ex[nt][2]), p3 = exp2_fast(ex[nt][3]);
+                sum[nt][0] = __fmaf_rn(p0 + p2, vinv, sum[nt][0]);
+                sum[nt][1] = __fmaf_rn(p1 + p3, vinv, sum[nt][1]);
+                pf[nt][0] = transpose8x8(pack_half2(p0 * vf, p1 * vf));
+                pf[nt][1] = transpose8x8(pack_half2(p2 * vf, p3 * vf));
+            }
+            // O^T += V^T P^T
             uint32_t vw[4][VB / 4];
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
@@ -388,10 +416,10 @@ __global__ void __launch_bounds__(kRowThreads, HALF ? 2 : 1) k_attn_rows(const A
                     vw[a][1] = w.y;
                 }
             }
-            bool odd_nan = false;
             if (masked) {
                 // a token that no row sees contributes nothing, whatever it
                 // holds; one that only some rows see may hold NaN codes
+                bool odd = false;
 #pragma unroll
                 for (int a = 0; a < 4; ++a) {
                     const int32_t pos = tb + (a >> 1) * 8 + 2 * static_cast<int32_t>(t) + (a & 1);
@@ -399,90 +427,89 @@ __global__ void __launch_bounds__(kRowThreads, HALF ? 2 : 1) k_attn_rows(const A
 #pragma unroll
                     for (int w = 0; w < VB / 4; ++w) {
                         if (dead) vw[a][w] = 0u;
-                        if constexpr (E4M3) odd_nan |= nan_bytes(vw[a][w]) != 0u;
+                        if constexpr (E4M3) odd |= nan_bytes(vw[a][w]) != 0u;
                     }
                 }
-                odd_nan = E4M3 && __any_sync(0xffffffffu, odd_nan);
-            }
-            if (E4M3 && odd_nan) {
-                // NaN codes count only for the rows that see them: a product of
-                // "sees" with "is NaN" marks those outputs, the codes become 0
-                uint32_t seen[4];
+                if (E4M3 && __any_sync(0xffffffffu, odd)) {
+                    // NaN codes count only for the rows that see them: a product of
+                    // "is NaN" with "sees" marks those outputs, the codes become 0
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        int32_t lo, hi;
+                        sees(8 * nt + static_cast<int32_t>(g), lo, hi);
+                        uint32_t seen[2];
 #pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        const int32_t pos = tb + a * 8 + 2 * static_cast<int32_t>(t);
-                        const uint32_t x0 = pos >= see_lo[half] && pos < see_hi[half] ? 0x3c00u : 0u;
-                        const uint32_t x1 = pos + 1 >= see_lo[half] && pos + 1 < see_hi[half] ? 0x3c000000u : 0u;
-                        seen[half + 2 * a] = x0 | x1;
+                        for (int a = 0; a < 2; ++a) {
+                            const int32_t pos = tb + a * 8 + 2 * static_cast<int32_t>(t);
+                            seen[a] = (pos >= lo && pos < hi ? 0x3c00u : 0u) | (pos + 1 >= lo && pos + 1 < hi ? 0x3c000000u : 0u);
+                        }
+#pragma unroll
+                        for (int s = 0; s < KS; ++s) {
+                            uint32_t n[4];  // [position 2 s, 2 s + 1 of the lane's bytes] x [tokens 2 t.., 2 t + 8..]
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int byte = 2 * s + (e & 1), w = byte >> 2, sh = 8 * (byte & 3) + 7, a = e & 2;
+                                n[e] = ((nan_bytes(vw[a][w]) >> sh) & 1u) * 0x3c00u | ((nan_bytes(vw[a + 1][w]) >> sh) & 1u) * 0x3c000000u;
+                            }
+                            float cnt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            mma16816(cnt, n, seen[0], seen[1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (cnt[e] > 0.0f) o[nt][s][e] = __int_as_float(0x7fffffff);
+                        }
                     }
 #pragma unroll
-                for (int s = 0; s < VB; ++s) {
-                    const int w = s >> 2, b = s & 3;
-                    uint32_t n[4];
+                    for (int a = 0; a < 4; ++a)
 #pragma unroll
-                    for (int a = 0; a < 4; ++a) n[a] = (nan_bytes(vw[a][w]) >> (8 * b + 7)) & 1u;
-                    float cnt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma16816(cnt, seen, n[0] * 0x3c00u | n[1] * 0x3c000000u, n[2] * 0x3c00u | n[3] * 0x3c000000u);
-#pragma unroll
-                    for (int e = 0; e < OR; ++e)
-                        if (cnt[e] > 0.0f) o[s][e] = __int_as_float(0x7fffffff);
+                        for (int w = 0; w < VB / 4; ++w) vw[a][w] &= ~((nan_bytes(vw[a][w]) >> 7) * 0xffu);
                 }
-#pragma unroll
-                for (int a = 0; a < 4; ++a)
-#pragma unroll
-                    for (int w = 0; w < VB / 4; ++w) vw[a][w] &= ~((nan_bytes(vw[a][w]) >> 7) * 0xffu);
             }
-            float dummy[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int w = 0; w < VB / 4; ++w) {
-                // bytes of two tokens side by side: (token 0, token 1) pairs of the four head positions of the word
+                // (token, next token) pairs of the word's four head positions
                 const uint32_t x01 = __byte_perm(vw[0][w], vw[1][w], 0x5140), y01 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
                 const uint32_t x23 = __byte_perm(vw[2][w], vw[3][w], 0x5140), y23 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-                uint32_t b[4][2];
-                widen4<E4M3>(x01, b[0][0], b[1][0]);
-                widen4<E4M3>(y01, b[2][0], b[3][0]);
-                widen4<E4M3>(x23, b[0][1], b[1][1]);
-                widen4<E4M3>(y23, b[2][1], b[3][1]);
+                uint32_t a0[4], a1[4];
+                widen4<E4M3>(x01, a0[0], a0[1]);
+                widen4<E4M3>(x23, a0[2], a0[3]);
+                widen4<E4M3>(y01, a1[0], a1[1]);
+                widen4<E4M3>(y23, a1[2], a1[3]);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    if constexpr (HALF) {
-                        float c[4] = {o[w * 4 + s][0], o[w * 4 + s][1], dummy[0], dummy[1]};
-                        mma16816(c, pf, b[s][0], b[s][1]);
-                        o[w * 4 + s][0] = c[0];
-                        o[w * 4 + s][1] = c[1];
-                    } else {
-                        mma16816(o[w * 4 + s], pf, b[s][0], b[s][1]);
-                    }
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma16816(o[nt][2 * w], a0, pf[nt][0], pf[nt][1]);
+                    mma16816(o[nt][2 * w + 1], a1, pf[nt][0], pf[nt][1]);
                 }
             }
         }
         cp_wait<0>();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 1);
-            sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 2);
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], 4);
+                sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], 8);
+                sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], 16);
+            }
 
         // join the warps: row i's maximum, sum and values over the 8 warps in order
         __syncthreads();  // the ring is free
         float* part = reinterpret_cast<float*>(ring);
         constexpr int PS = D + 4;
 #pragma unroll
-        for (int half = 0; half < (HALF ? 1 : 2); ++half) {
-            if (t == 0) {
-                s_m[warp][g + 8 * half] = mx[half];
-                s_l[warp][g + 8 * half] = sum[half];
-            }
-            // lane (g, t) holds head positions 2 t D/8 .. of row g: o[s][0] at 2 t VB + s, o[s][1] at (2 t + 1) VB + s
-            float* dst = part + (warp * kRows + g + 8 * half) * PS + 2 * t * VB;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int s = 0; s < VB; ++s) {
-                dst[s] = o[s][2 * half];
-                dst[VB + s] = o[s][2 * half + 1];
+            for (int e = 0; e < 2; ++e) {
+                const int32_t row = 8 * nt + 2 * static_cast<int32_t>(t) + e;
+                if (g == 0) {
+                    s_m[warp][row] = mx[nt][e];
+                    s_l[warp][row] = sum[nt][e];
+                }
+                float* dst = part + (static_cast<int32_t>(warp) * kRows + row) * PS + g * VB;
+#pragma unroll
+                for (int s = 0; s < KS; s += 2)
+                    *reinterpret_cast<float4*>(dst + 2 * s) =
+                        make_float4(o[nt][s][e], o[nt][s][e + 2], o[nt][s + 1][e], o[nt][s + 1][e + 2]);
             }
-        }
         __syncthreads();
         constexpr int TPR = kRowThreads / kRows;  // threads per row
         constexpr int EPT = D / TPR;              // head positions per thread
@@ -529,16 +556,20 @@ __global__ void __launch_bounds__(kRowThreads, HALF ? 2 : 1) k_attn_rows(const A
                 L = 0.0f;
 #pragma unroll
                 for (int e = 0; e < EPT; ++e) acc[e] = 0.0f;
-                for (uint64_t c = c0; c <= c1; ++c)
-                    M = fmaxf(M, __ldcg(p.parts + (2 * c + (c == c0 ? 1 : 0)) * kSlot + row));
+                for (uint64_t c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.parts + (2 * c + (c == c0 ? 1 : 0)) * kSlot + row));
+#pragma unroll 4
                 for (uint64_t c = c0; c <= c1; ++c) {
                     const float* q = p.parts + (2 * c + (c == c0 ? 1 : 0)) * kSlot;
                     const float mw = __ldcg(q + row), lw = __ldcg(q + kAttnRows + row);
-                    const float f = mw == -INFINITY ? (lw == lw ? 0.0f : 1.0f) : exp2_fast(mw - M);
-                    if (f == 0.0f) continue;
-                    L = __fmaf_rn(lw, f, L);
+                    float v[EPT];
 #pragma unroll
-                    for (int e = 0; e < EPT; ++e) acc[e] = __fmaf_rn(__ldcg(q + 2 * kAttnRows + row * D + d0 + e), f, acc[e]);
+                    for (int e = 0; e < EPT; ++e) v[e] = __ldcg(q + 2 * kAttnRows + row * D + d0 + e);
+                    const float f = mw == -INFINITY ? (lw == lw ? 0.0f : 1.0f) : exp2_fast(mw - M);
+                    if (f != 0.0f) {
+                        L = __fmaf_rn(lw, f, L);
+#pragma unroll
+                        for (int e = 0; e < EPT; ++e) acc[e] = __fmaf_rn(v[e], f, acc[e]);
+                    }
                 }
             }
         }
@@ -560,30 +591,26 @@ __global__ void __launch_bounds__(kRowThreads, HALF ? 2 : 1) k_attn_rows(const A
 
 constexpr int kMaxDevices = 64;
 
-template <int D, bool E4M3, bool BF16, bool HALF>
-int launch_rows(const AttnParams& p, int sms, void* stream) {
-    using Sm = RowSmem<D, HALF>;
-    const auto fn = k_attn_rows<D, E4M3, BF16, HALF>;
+template <int D, bool E4M3, bool BF16, int NT>
+int launch_rows(const AttnParams& p, int dev, int sms, void* stream) {
+    using Sm = RowSmem<D, NT>;
+    const auto fn = k_attn_rows<D, E4M3, BF16, NT>;
     static bool ready[kMaxDevices];  // (concurrent first calls set the same attribute)
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return static_cast<int>(e);
-    if (dev < 0 || dev >= kMaxDevices) return static_cast<int>(cudaErrorInvalidDevice);
     if (!ready[dev]) {
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kBytes);
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kBytes);
         if (e != cudaSuccess) return static_cast<int>(e);
         ready[dev] = true;
     }
-    int grid = sms * (HALF ? 2 : 1);
+    int grid = sms * Sm::kCtas;
     if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
     fn<<<grid, kRowThreads, Sm::kBytes, static_cast<cudaStream_t>(stream)>>>(p);
     return static_cast<int>(cudaGetLastError());
 }
 
 template <int D, bool E4M3, bool BF16>
-int launch_typed(const AttnParams& p, int sms, void* stream) {
-    if (p.max_q * p.group <= 8) return launch_rows<D, E4M3, BF16, true>(p, sms, stream);
-    return launch_rows<D, E4M3, BF16, false>(p, sms, stream);
+int launch_typed(const AttnParams& p, int dev, int sms, void* stream) {
+    if (p.max_q * p.group <= 8) return launch_rows<D, E4M3, BF16, 1>(p, dev, sms, stream);
+    return launch_rows<D, E4M3, BF16, 2>(p, dev, sms, stream);
 }
 
 }  // namespace
@@ -602,11 +629,11 @@ int launch_attention(const AttnParams& p, int head_dim, bool e4m3, bool bf16, vo
     }
     const int sms = sms_of[dev];
     if (head_dim == 64) {
-        if (e4m3) return bf16 ? launch_typed<64, true, true>(p, sms, stream) : launch_typed<64, true, false>(p, sms, stream);
-        return bf16 ? launch_typed<64, false, true>(p, sms, stream) : launch_typed<64, false, false>(p, sms, stream);
+        if (e4m3) return bf16 ? launch_typed<64, true, true>(p, dev, sms, stream) : launch_typed<64, true, false>(p, dev, sms, stream);
+        return bf16 ? launch_typed<64, false, true>(p, dev, sms, stream) : launch_typed<64, false, false>(p, dev, sms, stream);
     }
-    if (e4m3) return bf16 ? launch_typed<128, true, true>(p, sms, stream) : launch_typed<128, true, false>(p, sms, stream);
-    return bf16 ? launch_typed<128, false, true>(p, sms, stream) : launch_typed<128, false, false>(p, sms, stream);
+    if (e4m3) return bf16 ? launch_typed<128, true, true>(p, dev, sms, stream) : launch_typed<128, true, false>(p, dev, sms, stream);
+    return bf16 ? launch_typed<128, false, true>(p, dev, sms, stream) : launch_typed<128, false, false>(p, dev, sms, stream);
 }
 
 }  // namespace ndq

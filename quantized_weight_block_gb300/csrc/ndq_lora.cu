@@ -1,5 +1,32 @@
 // ndq_lora.cu -- low-rank adapters of many requests beside a shared
-// projection: y[m] = base[m] + scale * (x[m] A^T) B^T.
+// projection:
+//
+//     t[m, j] = scale[a] * sum_k x[m, k] A[a, j, k]          (shrink, j < rank)
+//     y[m, n] = base[m, n] + sum_j t[m, j] B[a, n, j]        (expand),  a = index[m]
+//
+// Two kernels, t in binary32 in the workspace; the second is launched
+// programmatically behind the first and reads what does not depend on it
+// before it waits.  There are two pairs:
+//
+// * few rows (k_lora_shrink_rows, k_lora_expand_rows): bound by the latency
+//   of one pass over the adapters' weights.  A CTA takes one row and
+//   kShrinkJ ranks over all of K; a thread of the expansion one or more
+//   outputs.
+// * many rows (k_lora_shrink_tile, k_lora_expand_tile): tiles of 32 rows on
+//   the tensor cores (mma.sync m16n8k16: the operator is bound by reading x
+//   and base and writing y, and its products need a fraction of even that
+//   rate).  A tile goes through the adapters of its rows one by one, with the
+//   other adapters' rows as zeros, so any row order is right and adjacent
+//   rows of one adapter cost one pass.  x and the weights are bfloat16, so
+//   the shrink's products are exact; t enters the expansion as a sum of
+//   bfloat16 parts: three for a binary32 result (2^-24 of t is left), two
+//   for a bfloat16 one (2^-16, under the result's own rounding of 2^-9).
+//   Operands are loaded from global memory in the order of the fragments:
+//   the k-index is permuted so that a lane's 16-byte load is its part of two
+//   k-steps, the output columns so that a lane holds 16 adjacent ones.
+//
+// Any other alignment (K or max_rank not a multiple of 8, buffers off 16
+// bytes) takes the few-row kernels with scalar loads.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -11,62 +38,506 @@
 namespace ndq {
 namespace {
 
-__device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+constexpr int kShrinkJ = 4;          // ranks per CTA of k_lora_shrink_rows
+constexpr int kLoraThreads = 256;
+constexpr int kLoraWarps = kLoraThreads / 32;
+constexpr int kTileRows = 32;        // rows of a tensor-core tile
+constexpr int kMaxSplit = 8;         // K splits of k_lora_shrink_tile at most
 
-// t[m, j] = scale * sum_k x[m, k] A[a, j, k]: a warp per (m, j).
-__global__ void __launch_bounds__(256) k_lora_shrink(const LoraParams p) {
-    const int64_t wid = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t m = wid / p.rmax, j = wid % p.rmax;
-    const uint32_t lane = threadIdx.x & 31u;
-    if (m >= p.M) return;
-    const int32_t a = p.index[m];
-    if (a < 0 || a >= p.nA || j >= p.ranks[a]) return;
-    const uint16_t* x = p.x + m * p.K;
-    const uint16_t* w = p.a + (static_cast<int64_t>(a) * p.rmax + j) * p.K;
-    float s = 0.0f;
-    for (int64_t k = lane; k < p.K; k += 32) s = __fmaf_rn(bf(x[k]), bf(w[k]), s);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (lane == 0) p.t[m * p.rmax + j] = __fmul_rn(s, p.scales[a]);
+__device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ int32_t rank_of(const LoraParams& p, int32_t a) {
+    if (a < 0 || a >= p.nA) return 0;
+    const int32_t r = p.ranks[a];
+    return r < 0 ? 0 : (r < p.rmax ? r : static_cast<int32_t>(p.rmax));
 }
 
-// y[m, n] = base[m, n] + sum_j t[m, j] B[a, n, j]: a thread per output.
-template <bool F32>
-__global__ void __launch_bounds__(256) k_lora_expand(const LoraParams p) {
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (n >= p.N) return;
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& w, float s) {
+    s = __fmaf_rn(bf_lo(x.x), bf_lo(w.x), s);
+    s = __fmaf_rn(bf_hi(x.x), bf_hi(w.x), s);
+    s = __fmaf_rn(bf_lo(x.y), bf_lo(w.y), s);
+    s = __fmaf_rn(bf_hi(x.y), bf_hi(w.y), s);
+    s = __fmaf_rn(bf_lo(x.z), bf_lo(w.z), s);
+    s = __fmaf_rn(bf_hi(x.z), bf_hi(w.z), s);
+    s = __fmaf_rn(bf_lo(x.w), bf_lo(w.w), s);
+    return __fmaf_rn(bf_hi(x.w), bf_hi(w.w), s);
+}
+
+// ---- few rows ----------------------------------------------------------------
+
+// One row and kShrinkJ ranks; the CTA's threads split K.
+template <bool VEC>
+__global__ void __launch_bounds__(kLoraThreads) k_lora_shrink_rows(const LoraParams p) {
+    __shared__ float s_part[kLoraWarps][kShrinkJ];
+    pdl_launch();
+    const int32_t groups = static_cast<int32_t>((p.rmax + kShrinkJ - 1) / kShrinkJ);
+    const int64_t m = blockIdx.x / groups;
+    const int32_t j0 = static_cast<int32_t>(blockIdx.x % groups) * kShrinkJ;
+    const int32_t a = p.index[m];
+    const int32_t r = rank_of(p, a);
+    if (j0 >= r) return;
+    const uint16_t* x = p.x + m * p.K;
+    const uint16_t* w = p.a + (static_cast<int64_t>(a) * p.rmax + j0) * p.K;
+    const int32_t nj = r - j0 < kShrinkJ ? r - j0 : kShrinkJ;
+    float s[kShrinkJ] = {};
+    if constexpr (VEC) {
+        const int64_t K8 = p.K >> 3;
+#pragma unroll 2
+        for (int64_t i = threadIdx.x; i < K8; i += kLoraThreads) {
+            const uint4 xv = reinterpret_cast<const uint4*>(x)[i];
+            uint4 wv[kShrinkJ];
+#pragma unroll
+            for (int j = 0; j < kShrinkJ; ++j)
+                wv[j] = j < nj ? __ldg(reinterpret_cast<const uint4*>(w + j * p.K) + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int j = 0; j < kShrinkJ; ++j) s[j] = dot8(xv, wv[j], s[j]);
+        }
+    } else {
+        for (int64_t k = threadIdx.x; k < p.K; k += kLoraThreads) {
+            const float xv = bf(x[k]);
+#pragma unroll
+            for (int j = 0; j < kShrinkJ; ++j)
+                if (j < nj) s[j] = __fmaf_rn(xv, bf(w[j * p.K + k]), s[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kShrinkJ; ++j)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s[j] = __fadd_rn(s[j], __shfl_xor_sync(0xffffffffu, s[j], d));
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    if (lane == 0) {
+#pragma unroll
+        for (int j = 0; j < kShrinkJ; ++j) s_part[warp][j] = s[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < nj) {
+        float v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kLoraWarps; ++q) v = __fadd_rn(v, s_part[q][threadIdx.x]);
+        p.t[m * p.rmax + j0 + threadIdx.x] = __fmul_rn(v, p.scales[a]);
+    }
+}
+
+// An output per thread; the weights of the first 16 ranks and base are
+// fetched before the wait for t.
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(kLoraThreads) k_lora_expand_rows(const LoraParams p) {
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * kLoraThreads + threadIdx.x;
+    const bool in = n < p.N;
+    bool waited = false;
     for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
         const int32_t a = p.index[m];
+        const int32_t r = rank_of(p, a);
         const int64_t o = m * p.N + n;
-        float s = 0.0f;
-        if (a >= 0 && a < p.nA) {
-            int32_t r = p.ranks[a];
-            r = r < p.rmax ? r : static_cast<int32_t>(p.rmax);
-            const uint16_t* w = p.b + (static_cast<int64_t>(a) * p.N + n) * p.rmax;
-            for (int32_t j = 0; j < r; ++j) s = __fmaf_rn(p.t[m * p.rmax + j], bf(w[j]), s);
+        float b = 0.0f;
+        if (in) {
+            if constexpr (F32) b = static_cast<const float*>(p.base)[o];
+            else b = bf(static_cast<const uint16_t*>(p.base)[o]);
         }
-        if constexpr (F32)
-            static_cast<float*>(p.y)[o] = __fadd_rn(static_cast<const float*>(p.base)[o], s);
-        else
-            static_cast<__nv_bfloat16*>(p.y)[o] =
-                __float2bfloat16_rn(__fadd_rn(bf(static_cast<const uint16_t*>(p.base)[o]), s));
+        const uint16_t* w = p.b + (static_cast<int64_t>(a) * p.N + n) * p.rmax;  // (not read where r is 0)
+        const float* t = p.t + m * p.rmax;
+        float s = 0.0f;
+        if constexpr (VEC) {
+            uint4 v[2] = {};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (in && 8 * i < r) v[i] = __ldg(reinterpret_cast<const uint4*>(w) + i);
+            if (!waited) pdl_wait();
+            waited = true;
+            for (int32_t j0 = 0; j0 < r; j0 += 16) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int32_t j = j0 + 8 * i + e;
+                        const float wv = (e & 1) ? bf_hi(c[e >> 1]) : bf_lo(c[e >> 1]);
+                        if (j < r) s = __fmaf_rn(__ldcg(t + j), wv, s);
+                    }
+                    if (in && j0 + 16 + 8 * i < r) v[i] = __ldg(reinterpret_cast<const uint4*>(w + j0 + 16) + i);
+                }
+            }
+        } else {
+            if (!waited) pdl_wait();
+            waited = true;
+            if (in)
+                for (int32_t j = 0; j < r; ++j) s = __fmaf_rn(__ldcg(t + j), bf(w[j]), s);
+        }
+        if (in) {
+            if constexpr (F32) static_cast<float*>(p.y)[o] = __fadd_rn(b, s);
+            else static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(__fadd_rn(b, s));
+        }
     }
+    if (!waited) pdl_wait();
+}
+
+// ---- many rows -----------------------------------------------------------------
+
+__device__ __forceinline__ void mma_bf16_16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The next adapter of a tile after `prev` (rows' adapters in s_a; lanes are
+// rows), or INT32_MAX: ascending, so each comes once.
+__device__ __forceinline__ int32_t next_adapter(int32_t mine, int32_t prev) {
+    int32_t c = mine > prev ? mine : INT32_MAX;
+    return __reduce_min_sync(0xffffffffu, c);
+}
+
+// Sums t over a K split: CTA (tile, split), NT = max_rank / 8 rounded up.
+// Warps take every eighth 32-k step; their sums are joined in warp order.
+template <int NT>
+__global__ void __launch_bounds__(kLoraThreads, NT <= 8 ? 2 : 1) k_lora_shrink_tile(const LoraParams p, int splits) {
+    extern __shared__ __align__(16) float s_sum[];  // [warps][32][NT * 8 + 4]
+    constexpr int LD = NT * 8 + 4;
+    pdl_launch();
+    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kTileRows;
+    const int32_t split = static_cast<int32_t>(blockIdx.y);
+    int32_t mine = -1;
+    if (m0 + lane < p.M) {
+        mine = p.index[m0 + lane];
+        if (mine < 0 || mine >= p.nA) mine = -1;
+    }
+    const int64_t steps = (p.K + 31) / 32;
+    const int64_t st0 = steps * split / splits, st1 = steps * (split + 1) / splits;
+    for (int32_t a = next_adapter(mine, -1); a != INT32_MAX; a = next_adapter(mine, a)) {
+        const int32_t r = rank_of(p, a);
+        if (r == 0) continue;
+        bool live[4];  // rows g, g + 8, g + 16, g + 24 of this adapter
+#pragma unroll
+        for (int i = 0; i < 4; ++i) live[i] = __shfl_sync(0xffffffffu, mine, static_cast<int>(g) + 8 * i) == a;
+        float acc[2][NT][4] = {};
+        const uint16_t* x = p.x + (m0 + g) * p.K + t * 8;
+        const uint16_t* w = p.a + (static_cast<int64_t>(a) * p.rmax + g) * p.K + t * 8;
+#pragma unroll 1
+        for (int64_t st = st0 + warp; st < st1; st += kLoraWarps) {
+            const int64_t k = st * 32;
+            const bool in = k + t * 8 < p.K;
+            uint4 xv[4], wv[NT];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                xv[i] = in && live[i] ? __ldg(reinterpret_cast<const uint4*>(x + 8 * i * p.K + k)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                wv[n] = in && 8 * n + static_cast<int>(g) < r ? __ldg(reinterpret_cast<const uint4*>(w + 8 * n * p.K + k))
+                                                             : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t a0[4] = {xv[0].x, xv[1].x, xv[0].y, xv[1].y}, a1[4] = {xv[0].z, xv[1].z, xv[0].w, xv[1].w};
+                const uint32_t c0[4] = {xv[2].x, xv[3].x, xv[2].y, xv[3].y}, c1[4] = {xv[2].z, xv[3].z, xv[2].w, xv[3].w};
+                const uint32_t* f = h == 0 ? (a0) : (c0);
+                const uint32_t* e = h == 0 ? (a1) : (c1);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (8 * n >= r) continue;
+                    mma_bf16_16816(acc[h][n], f, wv[n].x, wv[n].y);
+                    mma_bf16_16816(acc[h][n], e, wv[n].z, wv[n].w);
+                }
+            }
+        }
+        __syncthreads();  // the previous adapter's sums are read
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float* d = s_sum + (warp * kTileRows + 16 * h + g) * LD + 8 * n + 2 * t;
+                d[0] = acc[h][n][0];
+                d[1] = acc[h][n][1];
+                d[8 * LD] = acc[h][n][2];
+                d[8 * LD + 1] = acc[h][n][3];
+            }
+        __syncthreads();
+        const float sc = p.scales[a];
+        for (int32_t i = static_cast<int32_t>(tid); i < kTileRows * NT * 8; i += kLoraThreads) {
+            const int32_t row = i / (NT * 8), j = i % (NT * 8);
+            if (j >= r || m0 + row >= p.M) continue;
+            const int32_t ra = p.index[m0 + row];
+            if (ra != a) continue;
+            float v = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kLoraWarps; ++q) v = __fadd_rn(v, s_sum[(q * kTileRows + row) * LD + j]);
+            p.t[(static_cast<int64_t>(split) * p.M + m0 + row) * p.rmax + j] = __fmul_rn(v, sc);
+        }
+    }
+}
+
+// y of 32 rows by `chunks` x 512 columns: each warp 64 adjacent columns at a
+// time.  t's parts are laid out as A fragments in shared memory.
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(kLoraThreads, 2) k_lora_expand_tile(const LoraParams p, int splits, int chunks, int groups) {
+    constexpr int PARTS = F32 ? 3 : 2;
+    extern __shared__ __align__(16) uint8_t s_raw[];
+    uint4* s_t = reinterpret_cast<uint4*>(s_raw);  // [k-step pair][part][half of the rows][k-step][lane]
+    __shared__ int32_t s_a[kTileRows];
+    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x / groups) * kTileRows;
+    int32_t mine = -1;
+    if (m0 + lane < p.M) {
+        mine = p.index[m0 + lane];
+        if (mine < 0 || mine >= p.nA) mine = -1;
+    }
+    if (warp == 0) s_a[lane] = mine;
+    const int64_t cbase = (static_cast<int64_t>(blockIdx.x % groups) * chunks * kLoraWarps + warp) * 64;
+    const int32_t first = next_adapter(mine, -1);
+    const bool one = first == INT32_MAX || next_adapter(mine, first) == INT32_MAX;  // a single adapter: lay t out once
+    pdl_wait();
+    __syncthreads();
+    // lays adapter a's t out: rows of other adapters and ranks beyond r as zeros
+    auto lay = [&](int32_t a, int32_t r) {
+        const int32_t pairs = (r + 31) / 32;
+        for (int32_t i = static_cast<int32_t>(tid); i < pairs * 2 * 2 * 32; i += kLoraThreads) {
+            const int32_t ln = i & 31, ks = (i >> 5) & 1, half = (i >> 6) & 1, pr = i >> 7;
+            const int32_t gg = ln >> 2, tt = ln & 3;
+            float v[2][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int32_t row = 16 * half + gg + 8 * e;
+                const bool ok = s_a[row] == a;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int32_t j = 32 * pr + 8 * tt + 4 * ks + c;
+                    float s = 0.0f;
+                    if (ok && j < r)
+                        for (int32_t q = 0; q < splits; ++q)
+                            s = __fadd_rn(s, __ldcg(p.t + (static_cast<int64_t>(q) * p.M + m0 + row) * p.rmax + j));
+                    v[e][c] = s;
+                }
+            }
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+                uint4 f;
+                f.x = pack_bf16(v[0][0], v[0][1]);
+                f.y = pack_bf16(v[1][0], v[1][1]);
+                f.z = pack_bf16(v[0][2], v[0][3]);
+                f.w = pack_bf16(v[1][2], v[1][3]);
+                s_t[(((pr * PARTS + part) * 2 + half) * 2 + ks) * 32 + ln] = f;
+                v[0][0] = __fsub_rn(v[0][0], bf_lo(f.x));
+                v[0][1] = __fsub_rn(v[0][1], bf_hi(f.x));
+                v[1][0] = __fsub_rn(v[1][0], bf_lo(f.y));
+                v[1][1] = __fsub_rn(v[1][1], bf_hi(f.y));
+                v[0][2] = __fsub_rn(v[0][2], bf_lo(f.z));
+                v[0][3] = __fsub_rn(v[0][3], bf_hi(f.z));
+                v[1][2] = __fsub_rn(v[1][2], bf_lo(f.w));
+                v[1][3] = __fsub_rn(v[1][3], bf_hi(f.w));
+            }
+        }
+    };
+    if (one && first != INT32_MAX) {
+        lay(first, rank_of(p, first));
+        __syncthreads();
+    }
+    for (int c = 0; c < chunks; ++c) {
+        const int64_t n0 = cbase + static_cast<int64_t>(c) * kLoraWarps * 64;
+        // this lane's outputs: rows g + 8 i, columns n0 + 16 t + 0 .. 15 (n-tile e: columns 2 e, 2 e + 1)
+        float acc[2][8][4] = {};
+        for (int32_t a = first; a != INT32_MAX; a = next_adapter(mine, a)) {
+            const int32_t r = rank_of(p, a);
+            if (!one) {
+                __syncthreads();
+                lay(a, r);
+                __syncthreads();
+            }
+            for (int32_t pr = 0; 32 * pr < r; ++pr) {
+                uint4 wv[8];
+                // column of B's fragment n-tile e, index g: n0 + 16 (g / 2) + 2 e + g % 2
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int64_t n = n0 + 16 * (g >> 1) + 2 * e + (g & 1u);
+                    const int32_t j = 32 * pr + 8 * static_cast<int32_t>(t);
+                    wv[e] = make_uint4(0u, 0u, 0u, 0u);
+                    if (n < p.N && j < r) {
+                        wv[e] = __ldg(reinterpret_cast<const uint4*>(p.b + (static_cast<int64_t>(a) * p.N + n) * p.rmax + j));
+                        if (j + 8 > r) {  // ranks beyond the adapter's: not 0 * garbage
+                            const int32_t left = r - j;
+                            wv[e].x = left >= 2 ? wv[e].x : wv[e].x & 0xffffu;
+                            wv[e].y = left >= 4 ? wv[e].y : (left >= 3 ? wv[e].y & 0xffffu : 0u);
+                            wv[e].z = left >= 6 ? wv[e].z : (left >= 5 ? wv[e].z & 0xffffu : 0u);
+                            wv[e].w = left >= 7 ? wv[e].w & 0xffffu : 0u;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint4 f0 = s_t[(((pr * PARTS + part) * 2 + half) * 2 + 0) * 32 + lane];
+                        const uint4 f1 = s_t[(((pr * PARTS + part) * 2 + half) * 2 + 1) * 32 + lane];
+                        const uint32_t a0[4] = {f0.x, f0.y, f0.z, f0.w}, a1[4] = {f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            mma_bf16_16816(acc[half][e], a0, wv[e].x, wv[e].y);
+                            mma_bf16_16816(acc[half][e], a1, wv[e].z, wv[e].w);
+                        }
+                    }
+            }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int64_t m = m0 + 16 * half + g + 8 * i, n = n0 + 16 * t;
+                if (m >= p.M) continue;
+                const int64_t o = m * p.N + n;
+                if constexpr (F32) {
+                    const float* b = static_cast<const float*>(p.base) + o;
+                    float* y = static_cast<float*>(p.y) + o;
+                    if constexpr (VEC) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (n + 4 * e < p.N) {
+                                float4 v = *reinterpret_cast<const float4*>(b + 4 * e);
+                                v.x = __fadd_rn(v.x, acc[half][2 * e][2 * i]);
+                                v.y = __fadd_rn(v.y, acc[half][2 * e][2 * i + 1]);
+                                v.z = __fadd_rn(v.z, acc[half][2 * e + 1][2 * i]);
+                                v.w = __fadd_rn(v.w, acc[half][2 * e + 1][2 * i + 1]);
+                                *reinterpret_cast<float4*>(y + 4 * e) = v;
+                            }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (n + e < p.N) y[e] = __fadd_rn(b[e], acc[half][e >> 1][2 * i + (e & 1)]);
+                    }
+                } else {
+                    const uint16_t* b = static_cast<const uint16_t*>(p.base) + o;
+                    uint16_t* y = static_cast<uint16_t*>(p.y) + o;
+                    if constexpr (VEC) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (n + 8 * e < p.N) {
+                                uint4 v = *reinterpret_cast<const uint4*>(b + 8 * e);
+                                uint32_t* u = &v.x;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    u[q] = pack_bf16(__fadd_rn(bf_lo(u[q]), acc[half][4 * e + q][2 * i]),
+                                                     __fadd_rn(bf_hi(u[q]), acc[half][4 * e + q][2 * i + 1]));
+                                *reinterpret_cast<uint4*>(y + 8 * e) = v;
+                            }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (n + e < p.N)
+                                y[e] = static_cast<uint16_t>(pack_bf16(__fadd_rn(bf(b[e]), acc[half][e >> 1][2 * i + (e & 1)]), 0.0f));
+                    }
+                }
+            }
+    }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Rows from which the tensor-core tiles are taken (rule: where a 32-row tile
+// is worth its pass over the adapters of its rows).
+constexpr int64_t kTileMinRows = 96;
+
+// K splits: enough CTAs for two on each SM, at least 512 of K each.
+int shrink_splits(int64_t M, int64_t K) {
+    const int64_t tiles = (M + kTileRows - 1) / kTileRows;
+    int64_t s = (2 * 152 + tiles - 1) / tiles;
+    if (s > K / 512) s = K / 512;
+    if (s > kMaxSplit) s = kMaxSplit;
+    return s < 1 ? 1 : static_cast<int>(s);
+}
+
+cudaLaunchConfig_t behind(cudaLaunchAttribute* attr, dim3 grid, size_t smem, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kLoraThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <int NT>
+cudaError_t shrink_tile(const LoraParams& p, int splits, cudaStream_t st) {
+    constexpr int smem = kLoraWarps * kTileRows * (NT * 8 + 4) * 4;
+    if constexpr (smem > 48 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(k_lora_shrink_tile<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    const dim3 grid(static_cast<unsigned>((p.M + kTileRows - 1) / kTileRows), static_cast<unsigned>(splits));
+    k_lora_shrink_tile<NT><<<grid, kLoraThreads, smem, st>>>(p, splits);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t lora_workspace_bytes(int64_t M, int64_t rmax, int64_t) {
-    return static_cast<size_t>(M > 0 ? M : 1) * static_cast<size_t>(rmax) * 4u + 16u;
+// Room for any M' <= M: M' * splits is at most 8 M' and, splits being
+// (304 + tiles - 1) / tiles, at most 32 (304 + tiles).
+size_t lora_workspace_bytes(int64_t M, int64_t rmax, int64_t K) {
+    if (M < 1) M = 1;
+    int64_t s = K / 512 < kMaxSplit ? K / 512 : kMaxSplit;
+    if (s < 1) s = 1;
+    const int64_t bound = kTileRows * (2 * 152 + (M + kTileRows - 1) / kTileRows);
+    const int64_t rows = M * s < bound || bound < M ? M * s : bound;
+    return static_cast<size_t>(rows) * static_cast<size_t>(rmax) * 4u + 16u;
 }
 
 int launch_lora(const LoraParams& p, bool out_f32, void* stream) {
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (p.nA > 0)
-        k_lora_shrink<<<static_cast<unsigned>((p.M * p.rmax + 7) / 8), 256, 0, st>>>(p);
-    const dim3 grid(static_cast<unsigned>((p.N + 255) / 256), static_cast<unsigned>(p.M < 65535 ? p.M : 65535));
-    if (out_f32) k_lora_expand<true><<<grid, 256, 0, st>>>(p);
-    else k_lora_expand<false><<<grid, 256, 0, st>>>(p);
-    return static_cast<int>(cudaGetLastError());
+    const bool vec_a = p.K % 8 == 0 && aligned16(p.x) && aligned16(p.a);
+    const bool vec_b = p.rmax % 8 == 0 && aligned16(p.b);
+    cudaLaunchAttribute attr[1];
+    if (p.M >= kTileMinRows && vec_a && vec_b && p.nA > 0) {
+        const int splits = shrink_splits(p.M, p.K);
+        cudaError_t e;
+        if (p.rmax <= 8) e = shrink_tile<1>(p, splits, st);
+        else if (p.rmax <= 16) e = shrink_tile<2>(p, splits, st);
+        else if (p.rmax <= 32) e = shrink_tile<4>(p, splits, st);
+        else if (p.rmax <= 64) e = shrink_tile<8>(p, splits, st);
+        else e = shrink_tile<16>(p, splits, st);
+        if (e != cudaSuccess) return static_cast<int>(e);
+        const bool vec_y = p.N % (out_f32 ? 4 : 8) == 0 && aligned16(p.base) && aligned16(p.y);
+        const int64_t tiles = (p.M + kTileRows - 1) / kTileRows, cols = (p.N + kLoraWarps * 64 - 1) / (kLoraWarps * 64);
+        // column chunks per CTA: t is laid out once for all of them, as long as every SM has two CTAs
+        int64_t chunks = tiles * cols / (4 * 152);
+        chunks = chunks < 1 ? 1 : (chunks > 8 ? 8 : chunks);
+        const int64_t groups = (cols + chunks - 1) / chunks;
+        const size_t smem = static_cast<size_t>((p.rmax + 31) / 32) * (out_f32 ? 3 : 2) * 4 * 32 * 16;
+        cudaLaunchConfig_t cfg = behind(attr, dim3(static_cast<unsigned>(tiles * groups)), smem, st);
+        const int ch = static_cast<int>(chunks), cg = static_cast<int>(groups);
+        if (out_f32) e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, true>, p, splits, ch, cg)
+                               : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, false>, p, splits, ch, cg);
+        else e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, true>, p, splits, ch, cg)
+                       : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, false>, p, splits, ch, cg);
+        return static_cast<int>(e);
+    }
+    if (p.nA > 0) {
+        const int64_t groups = (p.rmax + kShrinkJ - 1) / kShrinkJ;
+        const unsigned grid = static_cast<unsigned>(p.M * groups);  // (the host keeps M * max_rank below 2^31)
+        if (vec_a) k_lora_shrink_rows<true><<<grid, kLoraThreads, 0, st>>>(p);
+        else k_lora_shrink_rows<false><<<grid, kLoraThreads, 0, st>>>(p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return static_cast<int>(e);
+    }
+    const dim3 grid(static_cast<unsigned>((p.N + kLoraThreads - 1) / kLoraThreads),
+                    static_cast<unsigned>(p.M < 65535 ? p.M : 65535));
+    cudaLaunchConfig_t cfg = behind(attr, grid, 0, st);
+    if (p.nA == 0) cfg.numAttrs = 0;  // nothing of this call to run behind
+    cudaError_t e;
+    if (out_f32) e = vec_b ? cudaLaunchKernelEx(&cfg, k_lora_expand_rows<true, true>, p)
+                           : cudaLaunchKernelEx(&cfg, k_lora_expand_rows<true, false>, p);
+    else e = vec_b ? cudaLaunchKernelEx(&cfg, k_lora_expand_rows<false, true>, p)
+                   : cudaLaunchKernelEx(&cfg, k_lora_expand_rows<false, false>, p);
+    return static_cast<int>(e);
 }
 
 }  // namespace ndq

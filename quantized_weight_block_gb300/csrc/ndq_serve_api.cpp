@@ -176,7 +176,7 @@ int ndq_lora_add(const void* x_bf16, int64_t M, int64_t K, const void* lora_a, c
     if (M < 0 || K < 0 || N < 0 || n_adapters < 0) return NDQ_ERR_NEGATIVE_DIM;
     if (dtype != NDQ_FLOAT && dtype != NDQ_BFLOAT16) return NDQ_ERR_BAD_DTYPE;
     if (max_rank < 1 || max_rank > 128 || M > INT32_MAX / 2 || K > INT32_MAX / 2 || N > INT32_MAX / 2 ||
-        n_adapters > INT32_MAX / 2)
+        n_adapters > INT32_MAX / 2 || M > INT32_MAX / max_rank)
         return NDQ_ERR_BAD_ARG;
     if (M == 0 || N == 0) return NDQ_OK;
     if (!base || !y || !index) return NDQ_ERR_NULL;
