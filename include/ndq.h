@@ -426,9 +426,9 @@ int ndq_kv_append(const ndq_kv_cache *cache, const void *k, const void *v, int i
  *   lse        NULL, or device binary32 [n_tokens, q_heads]: the natural
  *              logarithm of the softmax denominator, -inf for an empty row
  *   workspace  device buffer of ndq_attention_workspace_bytes(head_dim)
- *              bytes, 16-byte aligned, zeroed once before its first use and
- *              not shared by calls that may overlap (each call leaves its
- *              counters zero again)
+ *              bytes, 16-byte aligned, its first 4096 bytes zeroed once before
+ *              its first use (each call leaves them zero), not shared by
+ *              calls that may overlap
  * A query that sees nothing gives 0.  What is not seen has no influence,
  * whatever its codes stand for.  Scores, softmax statistics and sums are
  * binary32; query values and softmax weights enter the tensor cores as

@@ -486,11 +486,13 @@ def kv_append(cache: KvCache, k, v, slots, stream=None) -> None:
 
 
 def attention_workspace(n_req: int, n_tokens: int, q_heads: int, cache: KvCache, max_q: int = 1):
-    """A workspace for attention_kv8 calls on `cache`, of any size: zeroed
-    here, left reusable by every call.  (The sizes are accepted so that a
-    caller need not know that they do not matter.)"""
+    """A workspace for attention_kv8 calls on `cache`, of any size: its
+    counters are zeroed here and left so by every call.  (The sizes are
+    accepted so that a caller need not know that they do not matter.)"""
     torch = _torch()
-    return torch.zeros(ndq_attention_workspace_bytes(cache.head_dim), dtype=torch.uint8, device=cache.device)
+    ws = torch.empty(ndq_attention_workspace_bytes(cache.head_dim), dtype=torch.uint8, device=cache.device)
+    ws[:4096].zero_()
+    return ws
 
 
 def attention_kv8(q, cache: KvCache, block_table, kv_len, q_start=None, max_q=None, scale=None, window: int = 0,

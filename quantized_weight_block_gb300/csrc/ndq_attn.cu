@@ -615,7 +615,7 @@ int launch_typed(const AttnParams& p, int dev, int sms, void* stream) {
 
 }  // namespace
 
-int launch_attention(const AttnParams& p, int head_dim, bool e4m3, bool bf16, void* stream) {
+int launch_attention(AttnParams p, int head_dim, bool e4m3, bool bf16, void* stream) {
     static int sms_of[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -628,6 +628,15 @@ int launch_attention(const AttnParams& p, int head_dim, bool e4m3, bool bf16, vo
         sms_of[dev] = sms;
     }
     const int sms = sms_of[dev];
+    if (p.max_q > p.n_tokens) p.max_q = p.n_tokens;
+    // Requests with more than 16 rows go to the prompt kernel, which is not
+    // launched when there can be none; the others to this one.  (The host does
+    // not know the lengths, so this one always runs.)
+    if (p.max_q * p.group > kAttnRows) {
+        p.prompt_rows = kAttnRows + 1;
+        const int rc = launch_attention_prompt(p, head_dim, e4m3, bf16, dev, sms, stream);
+        if (rc != 0) return rc;
+    }
     if (head_dim == 64) {
         if (e4m3) return bf16 ? launch_typed<64, true, true>(p, dev, sms, stream) : launch_typed<64, true, false>(p, dev, sms, stream);
         return bf16 ? launch_typed<64, false, true>(p, dev, sms, stream) : launch_typed<64, false, false>(p, dev, sms, stream);

@@ -1,0 +1,758 @@
+// ndq_attn_prompt.cu -- attention over the 8-bit cache, many rows per request
+// (prompt chunks): the tcgen05 kernel k_attn_prompt.
+//
+// The rows of a request that share a cache head (its tokens times the group's
+// heads) are cut into units of 256, two tiles of 128.  A CTA takes one unit
+// (or, when there are too few units to fill the GPU, one of `splits` equal
+// parts of its tokens) and goes through the tokens 128 at a time.  Bound by
+// arithmetic: 4 D operations per row and token in the products and one
+// exponential per row and token beside them.
+//
+// Roles, joined by mbarriers only:
+// * warps 8-11 (converters) load the codes of 128 tokens straight into
+//   registers, one tile ahead, widen them to binary16 (exact) and store them
+//   as 128-byte-swizzled operands, K and V each in a ring of two; they also
+//   publish each 16-token group's constants (a group lies in one block);
+// * warp 12 issues the MMAs: S_i = Q_i K^T into tensor memory, and
+//   O_i += P_i V with P_i read from tensor memory; V is used as it lies
+//   (tokens by head positions, an operand contiguous along N);
+// * warps 0-3 and 4-7 (one thread per row of tile 0 / 1) turn S into P in
+//   place, keep the row's maximum and sum, and write the result.
+// The two tiles alternate, so that the tensor cores multiply for one while
+// the other's exponentials are taken.
+//
+// Scales as in ndq_attn.cu: t = s ks + log2(vs), P = 2^(t - m), the
+// denominator sums P / vs per group; Q is scaled by a power of two per row.
+// The maximum m moves only when a row passes it by 8, so O in tensor memory
+// is rescaled rarely; P is then at most 2^8.
+//
+// What a tile's rows do not all see is masked per element.  Tokens that no
+// row of the CTA sees enter as zeros; a NaN code of V that only some rows see
+// is taken out of the product and put into those rows at the end.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ndq_attn.cuh"
+#include "ndq_mma.cuh"
+
+namespace ndq {
+namespace {
+
+constexpr int kPrConv = 4;                      // converter warps
+constexpr int kPrConvWarp = 8;
+constexpr int kPrMmaWarp = kPrConvWarp + kPrConv;
+constexpr int kPrThreads = (kPrMmaWarp + 1) * 32;
+constexpr int kPrTokens = 128;                  // tokens of a K / V tile
+constexpr int kPrGroups = kPrTokens / 16;
+constexpr uint32_t kPrFault = 8u;               // bit of the device fault word
+
+struct PrShared {
+    uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
+    uint64_t sfull[2], pfull[2], odone[2];
+    float4 cst[4][kPrGroups];  // per group: K's scale, log2 of V's scale, 1 / V's scale
+    uint32_t tmem;
+    uint32_t fault;
+    uint32_t nan;   // V has NaN codes in a tile that some rows see only part of
+    uint32_t last;
+    int64_t r, base;
+    uint64_t sum[kPrThreads / 32];
+};
+
+template <int D>
+struct PrSmem {
+    static constexpr uint32_t kTile = kPrTokens * D * 2;  // K, V or Q tile
+    static constexpr uint32_t kBytes = 1024 + 6 * kTile + sizeof(PrShared);
+};
+
+// MN-major operand (N contiguous, 128-byte swizzle): 64 columns of N 128 rows
+// apart in memory (`lead` bytes to the next 64), 8 rows of K 1024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lead) {
+    uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(lead >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+// D[tmem] (+)= A[tmem] B: A is binary16 pairs, 8 columns per k-step of 16.
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bd, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bd), "r"(idesc), "r"(acc));
+}
+
+// 32 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
+        "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+        "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(a)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(a)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// A request's units of 256 rows (0: left to the other kernel).
+__device__ __forceinline__ int64_t prompt_tiles(const AttnParams& p, int64_t r, int64_t& q0, int32_t& n, int32_t& kv) {
+    attn_request(p, r, q0, n, kv);
+    const int64_t rows = static_cast<int64_t>(n) * p.group;
+    return rows < p.prompt_rows ? 0 : (rows + kPromptRows - 1) / kPromptRows;
+}
+
+template <int D, bool E4M3, bool BF16>
+__global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_constant__ AttnParams p) {
+    using Sm = PrSmem<D>;
+    constexpr uint32_t kTile = Sm::kTile;
+    constexpr uint32_t kAtom = kPrTokens * 128;  // 64 head positions of a tile's 128 rows
+    constexpr uint32_t kO = 256;                 // tensor-memory columns: S0, S1 at 0, 128; O0, O1 at 256, 256 + D
+    extern __shared__ __align__(1024) uint8_t pr_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pr_raw) + 1023u) & ~uintptr_t(1023));
+    uint8_t* sK = base;
+    uint8_t* sV = base + 2 * kTile;
+    uint8_t* sQ = base + 4 * kTile;
+    PrShared& S = *reinterpret_cast<PrShared*>(base + 6 * kTile);
+    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
+    const int bl = p.c.bs_log2;
+
+    // which unit: blockIdx.x counts (unit, split), units ordered by request,
+    // then row tile (the last, longest, first), then head
+    const uint64_t unit = blockIdx.x / static_cast<uint32_t>(p.splits);
+    const uint32_t split = blockIdx.x % static_cast<uint32_t>(p.splits);
+    {
+        const int64_t per = (p.n_req + kPrThreads - 1) / kPrThreads;
+        int64_t q0;
+        int32_t n, kv;
+        uint64_t mine = 0;
+        for (int64_t i = 0; i < per; ++i) {
+            const int64_t r = tid * per + i;
+            if (r < p.n_req) mine += static_cast<uint64_t>(prompt_tiles(p, r, q0, n, kv)) * p.c.heads;
+        }
+        uint64_t incl = mine;
+#pragma unroll
+        for (uint32_t d = 1; d < 32; d <<= 1) {
+            const uint64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += y;
+        }
+        if (lane == 31u) S.sum[warp] = incl;
+        __syncthreads();
+        uint64_t total = 0, before = incl - mine;
+        for (uint32_t w = 0; w < kPrThreads / 32; ++w) {
+            if (w < warp) before += S.sum[w];
+            total += S.sum[w];
+        }
+        if (unit >= total) return;
+        if (before <= unit && unit < before + mine) {
+            S.r = tid * per;
+            S.base = static_cast<int64_t>(before);
+        }
+    }
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.kfull[i], kPrConv);
+            mbar_init(&S.vfull[i], kPrConv);
+            mbar_init(&S.kfree[i], 1);
+            mbar_init(&S.vfree[i], 1);
+            mbar_init(&S.sfull[i], 1);
+            mbar_init(&S.odone[i], 1);
+            mbar_init(&S.pfull[i], 4);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        S.fault = 0u;
+        S.nan = 0u;
+        S.last = 0u;
+    }
+    if (warp == kPrMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&S.tmem)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    __syncthreads();
+    int64_t r = S.r, q0 = 0;
+    int32_t n = 0, kv = 0;
+    uint64_t left = unit - static_cast<uint64_t>(S.base);
+    int64_t tiles = prompt_tiles(p, r, q0, n, kv);
+    while (left >= static_cast<uint64_t>(tiles) * p.c.heads) {
+        left -= static_cast<uint64_t>(tiles) * p.c.heads;
+        ++r;
+        tiles = prompt_tiles(p, r, q0, n, kv);
+    }
+    const int32_t h = static_cast<int32_t>(left % p.c.heads);
+    const int32_t row0 = static_cast<int32_t>(tiles - 1 - left / p.c.heads) * kPromptRows;
+    const int32_t rows_left = n * p.group - row0;
+    const int32_t nrows = rows_left < kPromptRows ? rows_left : kPromptRows;
+    const int32_t nact = nrows > 128 ? 2 : 1;  // row tiles in use
+    // tokens that some row / every row of the CTA sees
+    const int64_t first_pos = static_cast<int64_t>(kv) - n + row0 / p.group;
+    const int64_t last_pos = static_cast<int64_t>(kv) - n + (row0 + nrows - 1) / p.group;
+    const int64_t any_hi = last_pos + 1;
+    const int64_t any_lo = p.window > 0 && first_pos + 1 > p.window ? first_pos + 1 - p.window : 0;
+    const int64_t cta_hi = first_pos + 1;
+    const int64_t cta_lo = p.window > 0 ? last_pos + 1 - p.window : 0;
+    const int64_t lo16 = any_lo & ~int64_t(15);
+    const int64_t all_tiles = any_hi > lo16 ? (any_hi - lo16 + kPrTokens - 1) / kPrTokens : 0;
+    const int64_t j0 = all_tiles * split / p.splits;
+    const int32_t nt = static_cast<int32_t>(all_tiles * (split + 1) / p.splits - j0);
+    const int32_t tok0 = static_cast<int32_t>(lo16 + j0 * kPrTokens);  // first token of this CTA's tiles
+
+    // Q: one row per softmax thread, scaled, as a 128-byte-swizzled operand
+    const uint32_t wg = warp >> 2, wrow = tid & 127u;
+    float frow = 0.0f;
+    int32_t see_lo = 0, see_hi = 0;
+    int64_t at = 0;  // index of the row's output
+    bool has_row = false;
+    if (warp < kPrConvWarp) {
+        const int32_t i = static_cast<int32_t>(wg * 128u + wrow);
+        has_row = i < nrows;
+        const int32_t qi = (row0 + (has_row ? i : 0)) / p.group, qh = h * p.group + (row0 + (has_row ? i : 0)) % p.group;
+        at = (q0 + qi) * p.q_heads + qh;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (q0 + qi) * p.q_stride + static_cast<int64_t>(qh) * D);
+        float amax = 0.0f;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+            const uint4 w = has_row ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float a, b;
+                widen2<BF16>(ww[e], a, b);
+                amax = max3(amax, fabsf(a), fabsf(b));
+            }
+        }
+        float up, down;
+        row_scale(amax, up, down);
+        if (p.scale_log2 < 0.0f) {  // (a negative scale goes into Q: K's scale then keeps the order of scores)
+            up = -up;
+            down = -down;
+        }
+        frow = down * p.scale_log2;
+        uint8_t* dst = sQ + wg * kTile;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+            const uint4 w = has_row ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float a, b;
+                widen2<BF16>(ww[e], a, b);
+                o[e] = pack_half2(a * up, b * up);
+            }
+            *reinterpret_cast<uint4*>(dst + (c >> 3) * kAtom + sw128(wrow, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        const int64_t pos = static_cast<int64_t>(kv) - n + qi;
+        see_hi = has_row && pos >= 0 ? static_cast<int32_t>(pos) + 1 : 0;
+        see_lo = p.window > 0 && pos + 1 > p.window ? static_cast<int32_t>(pos + 1 - p.window) : 0;
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    float mx = -INFINITY, sum = 0.0f;
+
+    if (warp >= kPrConvWarp && warp < kPrMmaWarp) {
+        // ---- converters: groups cw and cw + 4 of every tile
+        constexpr int LPR = D / 8, RPI = 32 / LPR, ITS = 16 / RPI;  // lanes per row, rows per load, loads per group
+        const uint32_t cw = warp - kPrConvWarp;
+        const uint32_t lrow = lane / LPR, piece = lane % LPR;
+        const int32_t* table = p.table + r * p.width;
+        // lane i: group cw + 4 (i & 1) of tile 16 b + i / 2
+        auto ids_of = [&](int32_t b) -> int32_t {
+            const int32_t j = 16 * b + static_cast<int32_t>(lane >> 1);
+            const int64_t tk = static_cast<int64_t>(tok0) + static_cast<int64_t>(j) * kPrTokens + (cw + 4 * (lane & 1u)) * 16;
+            if (j >= nt || tk >= any_hi) return -1;
+            const int32_t id = table[tk >> bl];
+            return id >= 0 && id < p.c.num_blocks ? id : -1;
+        };
+        int32_t ids = ids_of(0), ids_next = ids_of(1);
+        float ks_l = 0.0f, vs_l = 0.0f;
+        auto scales_of = [&]() {
+            if (ids >= 0) {
+                const uint64_t u = static_cast<uint64_t>(ids) * p.c.heads + static_cast<uint32_t>(h);
+                ks_l = p.c.ks[u];
+                vs_l = p.c.vs[u];
+            }
+        };
+        scales_of();
+        uint2 kr[2][ITS], vr[2][ITS];
+        // the codes of tile j: rows outside what the CTA sees as zeros
+        auto load = [&](const uint8_t* codes, int32_t j, uint2 (&d)[2][ITS], int32_t set) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int32_t id = __shfl_sync(0xffffffffu, set, 2 * (j & 15) + q);
+                const int64_t tk = static_cast<int64_t>(tok0) + static_cast<int64_t>(j) * kPrTokens + (cw + 4 * q) * 16 + lrow;
+                const uint64_t u = static_cast<uint64_t>(id < 0 ? 0 : id) * p.c.heads + static_cast<uint32_t>(h);
+                const uint8_t* src = codes + ((u << bl) + (static_cast<uint64_t>(tk) & ((1u << bl) - 1u))) * D + piece * 8;
+#pragma unroll
+                for (int i = 0; i < ITS; ++i) {
+                    const int64_t tt = tk + i * RPI;
+                    d[q][i] = make_uint2(0u, 0u);
+                    if (id >= 0 && tt < any_hi && tt >= any_lo) d[q][i] = __ldg(reinterpret_cast<const uint2*>(src + i * RPI * D));
+                }
+            }
+        };
+        auto store = [&](uint8_t* tile, uint2 (&d)[2][ITS]) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < ITS; ++i) {
+                    uint4 o;
+                    widen4<E4M3>(d[q][i].x, o.x, o.y);
+                    widen4<E4M3>(d[q][i].y, o.z, o.w);
+                    *reinterpret_cast<uint4*>(tile + (piece >> 3) * kAtom + sw128((cw + 4 * q) * 16 + i * RPI + lrow, piece & 7u)) = o;
+                }
+        };
+        bool ok = true;
+        if (nt > 0) load(p.c.k, 0, kr, ids);
+        for (int32_t j = 0; j < nt && ok; ++j) {
+            if ((j & 15) == 0 && j > 0) {
+                ids = ids_next;
+                ids_next = ids_of((j >> 4) + 1);
+                scales_of();
+            }
+            load(p.c.v, j, vr, ids);
+            const uint32_t st = static_cast<uint32_t>(j & 1), ph = static_cast<uint32_t>(((j >> 1) - 1) & 1);
+            // the groups' constants (ring of four: the tile four before is out of use once K's stage is free)
+            float vsg[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int src = 2 * (j & 15) + q;
+                const int32_t id = __shfl_sync(0xffffffffu, ids, src);
+                const float ks = __shfl_sync(0xffffffffu, ks_l, src), vs = __shfl_sync(0xffffffffu, vs_l, src);
+                vsg[q] = id < 0 ? 0.0f : vs;
+                float4 c = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);  // a missing block: weight 0
+                if (id >= 0) {
+                    float f, e, inv;
+                    split_scale(vs, f, e, inv);
+                    float lg;
+                    asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(vs == 0.0f ? 1.0f : f));
+                    c = make_float4(ks, e + lg, vs == 0.0f ? 1.0f : __fdiv_rn(1.0f, vs), 0.0f);
+                }
+                if (j >= 2 && q == 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.kfree[st], ph));
+                if (!ok) break;
+                if (lane == 0) S.cst[j & 3][cw + 4 * q] = c;
+            }
+            if (!ok) break;
+            store(sK + st * kTile, kr);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.kfull[st]);
+            if (j + 1 < nt) load(p.c.k, j + 1, kr, ((j + 1) & 15) == 0 ? ids_next : ids);
+            if (j >= 2) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.vfree[st], ph));
+            if (!ok) break;
+            // a block of V of scale 0 counts as zeros
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (vsg[q] == 0.0f) {
+#pragma unroll
+                    for (int i = 0; i < ITS; ++i) vr[q][i] = make_uint2(0u, 0u);
+                }
+            if constexpr (E4M3) {
+                const int64_t tb = static_cast<int64_t>(tok0) + static_cast<int64_t>(j) * kPrTokens;
+                if (tb + kPrTokens > cta_hi || tb < cta_lo) {  // some rows see only part of this tile
+                    bool odd = false;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int i = 0; i < ITS; ++i) {
+                            const uint32_t nx = nan_bytes(vr[q][i].x), ny = nan_bytes(vr[q][i].y);
+                            odd |= (nx | ny) != 0u;
+                            vr[q][i].x &= ~((nx >> 7) * 0xffu);
+                            vr[q][i].y &= ~((ny >> 7) * 0xffu);
+                        }
+                    if (odd) S.nan = 1u;
+                }
+            }
+            store(sV + st * kTile, vr);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.vfull[st]);
+        }
+        if (!ok && lane == 0) atomicOr(&S.fault, 1u);
+    } else if (warp == kPrMmaWarp) {
+        // ---- MMA issue
+        constexpr uint32_t kIdQ = (1u << 4) | ((kPrTokens >> 3) << 17) | ((128u >> 4) << 24);
+        constexpr uint32_t kIdP = (1u << 4) | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
+        bool ok = true;
+        int32_t issued[2] = {0, 0};  // PV products of each row tile
+        int32_t scored[2] = {0, 0};  // score products of each row tile
+        auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(b, parity)); };
+        auto scores = [&](int32_t i, int32_t j) {  // S_i = Q_i K_j^T
+            const uint32_t a0 = smem_addr(sQ + i * kTile), b0 = smem_addr(sK + (j & 1) * kTile);
+            if (elect_one()) {
+#pragma unroll
+                for (uint32_t s = 0; s < D / 16; ++s)
+                    mma_bf16(tmem + 128u * i, mma_sdesc(a0 + (s >> 2) * kAtom + (s & 3u) * 32u),
+                             mma_sdesc(b0 + (s >> 2) * kAtom + (s & 3u) * 32u), kIdQ, s > 0 ? 1u : 0u);
+                mma_commit(&S.sfull[i]);
+                if (i == nact - 1) mma_commit(&S.kfree[j & 1]);
+            }
+            __syncwarp();
+            ++scored[i];
+        };
+        if (nt > 0) {
+            ok = wait(&S.kfull[0], 0u);
+            if (ok) {
+                tc_fence_after();
+                for (int32_t i = 0; i < nact; ++i) scores(i, 0);
+            }
+        }
+        for (int32_t j = 0; j < nt && ok; ++j) {
+            ok = wait(&S.vfull[j & 1], static_cast<uint32_t>((j >> 1) & 1));
+            for (int32_t i = 0; i < nact && ok; ++i) {
+                ok = wait(&S.pfull[i], static_cast<uint32_t>(j & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t b0 = smem_addr(sV + (j & 1) * kTile);
+                if (elect_one()) {
+#pragma unroll
+                    for (uint32_t s = 0; s < kPrTokens / 16; ++s)
+                        mma_ts(tmem + kO + D * i, tmem + 128u * i + 8u * s, sdesc_mn(b0 + s * 2048u, kAtom), kIdP,
+                               j > 0 || s > 0 ? 1u : 0u);
+                    mma_commit(&S.odone[i]);
+                    if (i == nact - 1) mma_commit(&S.vfree[j & 1]);
+                }
+                __syncwarp();
+                ++issued[i];
+                if (j + 1 < nt) {
+                    if (i == 0) {
+                        ok = wait(&S.kfull[(j + 1) & 1], static_cast<uint32_t>(((j + 1) >> 1) & 1));
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    scores(i, j + 1);
+                }
+            }
+        }
+        // no MMA may still run when tensor memory is given back
+        for (int32_t i = 0; i < 2; ++i) {
+            if (scored[i] > 0) ok = wait(&S.sfull[i], static_cast<uint32_t>((scored[i] - 1) & 1)) && ok;
+            if (issued[i] > 0) ok = wait(&S.odone[i], static_cast<uint32_t>((issued[i] - 1) & 1)) && ok;
+        }
+        if (!ok && lane == 0) atomicOr(&S.fault, 1u);
+    } else if (static_cast<int32_t>(wg) < nact) {
+        // ---- softmax: one row per thread
+        const uint32_t tS = tmem + 128u * wg + ((32u * (warp & 3u)) << 16), tO = tmem + kO + D * wg + ((32u * (warp & 3u)) << 16);
+        const int32_t wrow0 = row0 + 128 * static_cast<int32_t>(wg);
+        const int32_t wrows = nrows - 128 * static_cast<int32_t>(wg) < 128 ? nrows - 128 * static_cast<int32_t>(wg) : 128;
+        const int64_t all_hi = static_cast<int64_t>(kv) - n + wrow0 / p.group + 1;
+        const int64_t all_lo = p.window > 0 ? static_cast<int64_t>(kv) - n + (wrow0 + wrows - 1) / p.group + 1 - p.window : 0;
+        float ms = 0.0f;
+        bool ok = true;
+        for (int32_t j = 0; j < nt; ++j) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.sfull[wg], static_cast<uint32_t>(j & 1)));
+            if (!ok) break;
+            tc_fence_after();
+            const int32_t tb = tok0 + j * kPrTokens;
+            const bool masked = tb + kPrTokens > all_hi || tb < all_lo;
+            const float4* cst = S.cst[j & 3];
+            // the row's largest score of the tile
+            float tm = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t v[32];
+                tmem_ld32(tS + 32 * c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float4 k = cst[2 * c + q];
+                    float m = -INFINITY;
+                    if (!masked) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) m = max3(m, __uint_as_float(v[16 * q + e]), __uint_as_float(v[16 * q + e + 1]));
+                    } else {
+                        const int32_t pos = tb + 32 * c + 16 * q;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            m = fmaxf(m, pos + e >= see_lo && pos + e < see_hi ? __uint_as_float(v[16 * q + e]) : -INFINITY);
+                    }
+                    // (m is -inf where nothing is seen: not times a scale of 0)
+                    if (m > -INFINITY) tm = fmaxf(tm, __fmaf_rn(m, frow * k.x, k.y));
+                }
+            }
+            const bool grow = tm > (mx == -INFINITY ? -INFINITY : mx + 8.0f);
+            if (__any_sync(0xffffffffu, grow)) {
+                const float al = !grow ? 1.0f : (mx == -INFINITY ? 0.0f : exp2_fast(mx - tm));
+                if (j > 0) {  // the product before this one is done with O
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((j - 1) & 1)));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(tO + 32 * c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
+                        tmem_st32(tO + 32 * c, v);
+                    }
+                }
+                sum *= al;
+                if (grow) mx = ms = tm;
+            }
+            // weights, in place
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t v[32], w[16];
+                tmem_ld32(tS + 32 * c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float4 k = cst[2 * c + q];
+                    const uint64_t f2 = pair(frow * k.x, frow * k.x), c2 = pair(k.y - ms, k.y - ms);
+                    uint64_t s2 = 0;
+                    const int32_t pos = tb + 32 * c + 16 * q;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        float a, b;
+                        unpair(pair_fma(pair(__uint_as_float(v[16 * q + e]), __uint_as_float(v[16 * q + e + 1])), f2, c2), a, b);
+                        if (masked) {
+                            if (pos + e < see_lo || pos + e >= see_hi) a = -INFINITY;
+                            if (pos + e + 1 < see_lo || pos + e + 1 >= see_hi) b = -INFINITY;
+                        }
+                        a = exp2_fast(a);
+                        b = exp2_fast(b);
+                        s2 = pair_add(s2, pair(a, b));
+                        w[8 * q + e / 2] = pack_half2(a, b);
+                    }
+                    float a, b;
+                    unpair(s2, a, b);
+                    sum = __fmaf_rn(a + b, k.z, sum);
+                }
+                tmem_st16(tS + 16 * c, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.pfull[wg]);
+        }
+        if (ok && nt > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((nt - 1) & 1)));
+            tc_fence_after();
+        }
+        if (!ok && lane == 0) atomicOr(&S.fault, 1u);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const bool fault = S.fault != 0u;
+    if (fault && tid == 0) atomicOr(p.fault, kPrFault);
+
+    if (!fault && warp < kPrConvWarp && static_cast<int32_t>(wg) < nact) {
+        const uint32_t tO = tmem + kO + D * wg + ((32u * (warp & 3u)) << 16);
+        // head positions that this row sees as NaN although the product left them out
+        uint32_t bad[D / 32] = {};
+        if (E4M3 && S.nan != 0u) {
+            const int32_t* table = p.table + r * p.width;
+            for (int32_t j = 0; j < nt; ++j) {
+                const int64_t tb = static_cast<int64_t>(tok0) + static_cast<int64_t>(j) * kPrTokens;
+                if (tb + kPrTokens <= cta_hi && tb >= cta_lo) continue;
+                const int64_t a = tb > see_lo ? tb : see_lo, b = tb + kPrTokens < see_hi ? tb + kPrTokens : see_hi;
+                for (int64_t tk = a; tk < b; ++tk) {
+                    const int32_t id = table[tk >> bl];
+                    if (id < 0 || id >= p.c.num_blocks) continue;
+                    const uint64_t u = static_cast<uint64_t>(id) * p.c.heads + static_cast<uint32_t>(h);
+                    if (p.c.vs[u] == 0.0f) continue;
+                    const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                        p.c.v + ((u << bl) + (static_cast<uint64_t>(tk) & ((1u << bl) - 1u))) * D);
+#pragma unroll
+                    for (int w = 0; w < D / 4; ++w) {
+                        const uint32_t x = nan_bytes(v[w]) >> 7;
+                        bad[w / 8] |= ((x & 1u) | (x >> 7 & 2u) | (x >> 14 & 4u) | (x >> 21 & 8u)) << (4 * (w % 8));
+                    }
+                }
+            }
+        }
+        const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == sum ? 0.0f : sum);
+        float* slot = p.parts + static_cast<uint64_t>(blockIdx.x) * NDQ_PROMPT_SLOT(D);
+        const uint32_t prow = wg * 128u + wrow;
+        if (p.splits > 1) {
+            slot[prow] = mx;
+            slot[kPromptRows + prow] = sum;
+        }
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            if (nt > 0) {
+                tmem_ld32(tO + 32 * c, v);
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = 0u;
+            }
+            if (E4M3 && S.nan != 0u) {
+                uint32_t bc = 0u;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q)
+                    if (q == c) bc = bad[q];
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (bc >> e & 1u) v[e] = 0x7fffffffu;
+            }
+            if (p.splits > 1) {
+                float4* d = reinterpret_cast<float4*>(slot + 2 * kPromptRows);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    d[(8 * c + e) * kPromptRows + prow] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                                                     __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+            } else if (has_row) {
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + 32 * c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        // (a row that saw nothing gives 0, whatever the product left)
+                        o[q] = sum == 0.0f ? 0u : narrow2<BF16>(__uint_as_float(v[8 * e + 2 * q]) * inv, __uint_as_float(v[8 * e + 2 * q + 1]) * inv);
+                    dst[e] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+        }
+        if (p.splits == 1 && p.lse && has_row)
+            p.lse[at] = sum > 0.0f ? (mx + log2f(sum)) * 0.6931471805599453f : (sum == sum ? -INFINITY : sum);
+    }
+    tc_fence_before();
+    if (p.splits > 1) {
+        // the last part of the unit to arrive joins them in order
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            const uint32_t seen = atomicAdd(p.counters + unit, 1u);
+            S.last = seen == static_cast<uint32_t>(p.splits - 1);
+            if (S.last) p.counters[unit] = 0u;
+            __threadfence();
+        }
+        __syncthreads();
+        if (S.last && !fault && warp < kPrConvWarp && has_row) {
+            const uint32_t prow = wg * 128u + wrow;
+            const float* first = p.parts + unit * static_cast<uint64_t>(p.splits) * NDQ_PROMPT_SLOT(D);
+            float M = -INFINITY, L = 0.0f;
+            for (int s = 0; s < p.splits; ++s) M = fmaxf(M, __ldcg(first + s * NDQ_PROMPT_SLOT(D) + prow));
+            auto weight = [&](int s, float& l) {
+                const float m = __ldcg(first + s * NDQ_PROMPT_SLOT(D) + prow);
+                l = __ldcg(first + s * NDQ_PROMPT_SLOT(D) + kPromptRows + prow);
+                return m == -INFINITY ? (l == l ? 0.0f : 1.0f) : exp2_fast(m - M);
+            };
+            for (int s = 0; s < p.splits; ++s) {
+                float l;
+                const float f = weight(s, l);
+                if (f != 0.0f) L = __fmaf_rn(l, f, L);
+            }
+            const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : (L == L ? 0.0f : L);
+            for (int c = 0; c < D / 8; ++c) {
+                float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+                for (int s = 0; s < p.splits; ++s) {
+                    float l;
+                    const float f = weight(s, l);
+                    if (f == 0.0f) continue;
+                    const float4* q = reinterpret_cast<const float4*>(first + s * NDQ_PROMPT_SLOT(D) + 2 * kPromptRows);
+                    const float4 x = __ldcg(q + (2 * c) * kPromptRows + prow), y = __ldcg(q + (2 * c + 1) * kPromptRows + prow);
+                    a.x = __fmaf_rn(x.x, f, a.x);
+                    a.y = __fmaf_rn(x.y, f, a.y);
+                    a.z = __fmaf_rn(x.z, f, a.z);
+                    a.w = __fmaf_rn(x.w, f, a.w);
+                    b.x = __fmaf_rn(y.x, f, b.x);
+                    b.y = __fmaf_rn(y.y, f, b.y);
+                    b.z = __fmaf_rn(y.z, f, b.z);
+                    b.w = __fmaf_rn(y.w, f, b.w);
+                }
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + 8 * c) =
+                    make_uint4(narrow2<BF16>(a.x * inv, a.y * inv), narrow2<BF16>(a.z * inv, a.w * inv),
+                               narrow2<BF16>(b.x * inv, b.y * inv), narrow2<BF16>(b.z * inv, b.w * inv));
+            }
+            if (p.lse) p.lse[at] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : (L == L ? -INFINITY : L);
+        }
+    }
+    __syncthreads();
+    if (warp == kPrMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+template <int D, bool E4M3, bool BF16>
+int launch_typed(const AttnParams& p, unsigned grid, int dev, void* stream) {
+    const auto fn = k_attn_prompt<D, E4M3, BF16>;
+    static bool ready[64];  // (concurrent first calls set the same attribute)
+    if (!ready[dev]) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(PrSmem<D>::kBytes));
+        if (e != cudaSuccess) return static_cast<int>(e);
+        ready[dev] = true;
+    }
+    fn<<<grid, kPrThreads, PrSmem<D>::kBytes, static_cast<cudaStream_t>(stream)>>>(p);
+    return static_cast<int>(cudaGetLastError());
+}
+
+}  // namespace
+
+int launch_attention_prompt(AttnParams p, int head_dim, bool e4m3, bool bf16, int dev, int sms, void* stream) {
+    const IqGrids* grids = nullptr;
+    int e = device_symbols(dev, &p.fault, &grids);
+    if (e != 0) return e;
+    // units at most: a request's last unit may be partial, and has at least prompt_rows rows
+    const int64_t rows = p.n_tokens * p.group;
+    const int64_t reqs = rows / p.prompt_rows < p.n_req ? rows / p.prompt_rows : p.n_req;
+    const int64_t units = (rows / kPromptRows + reqs) * p.c.heads;
+    if (units == 0) return 0;
+    // too few units to fill the GPU: split their tokens, four tiles to a part at least
+    const int64_t most = (p.width << p.c.bs_log2) / (4 * 128);
+    int64_t splits = (sms < kPromptMaxParts ? sms : kPromptMaxParts) / units;
+    if (splits > kPromptMaxSplits) splits = kPromptMaxSplits;
+    if (splits > most) splits = most;
+    if (splits < 1) splits = 1;
+    p.splits = static_cast<int32_t>(splits);
+    if (units * splits > INT32_MAX) return static_cast<int>(cudaErrorInvalidValue);
+    const unsigned grid = static_cast<unsigned>(units * splits);
+    if (head_dim == 64) {
+        if (e4m3) return bf16 ? launch_typed<64, true, true>(p, grid, dev, stream) : launch_typed<64, true, false>(p, grid, dev, stream);
+        return bf16 ? launch_typed<64, false, true>(p, grid, dev, stream) : launch_typed<64, false, false>(p, grid, dev, stream);
+    }
+    if (e4m3) return bf16 ? launch_typed<128, true, true>(p, grid, dev, stream) : launch_typed<128, true, false>(p, grid, dev, stream);
+    return bf16 ? launch_typed<128, false, true>(p, grid, dev, stream) : launch_typed<128, false, false>(p, grid, dev, stream);
+}
+
+}  // namespace ndq

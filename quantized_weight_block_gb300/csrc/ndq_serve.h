@@ -49,13 +49,22 @@ struct AppendParams {
 };
 int launch_kv_append(const AppendParams& p, int head_dim, bool e4m3, bool bf16, void* stream);
 
-// CTAs of an attention launch at most, and the workspace: one arrival counter
-// per CTA (zero between calls), then two partial results per CTA.
+// The attention workspace: arrival counters (zero between calls), then partial
+// results.  Few rows: CTAs of a launch at most, each leaving up to two
+// partials of 16 rows.  Prompts: units of 256 rows whose tokens are split over
+// at most one CTA per SM in all, each leaving one partial.
 constexpr int kAttnMaxCtas = 512;
-constexpr int kAttnRows = 16;  // (query, head) rows of one partial
+constexpr size_t kAttnCounterBytes = 4096;
+constexpr int kAttnRows = 16;
+constexpr int kPromptRows = 256;
+constexpr int kPromptMaxSplits = 16;
+constexpr int kPromptMaxParts = 192;  // (units * splits <= SMs when splits > 1)
 constexpr size_t attn_slot_floats(int head_dim) { return static_cast<size_t>(kAttnRows) * (head_dim + 2); }
+#define NDQ_PROMPT_SLOT(D) (static_cast<size_t>(ndq::kPromptRows) * ((D) + 2))
 constexpr size_t attn_workspace_bytes(int head_dim) {
-    return kAttnMaxCtas * 4u + 2u * kAttnMaxCtas * attn_slot_floats(head_dim) * 4u;
+    return kAttnCounterBytes + 4u * (2u * kAttnMaxCtas * attn_slot_floats(head_dim) > kPromptMaxParts * NDQ_PROMPT_SLOT(head_dim)
+                                         ? 2u * kAttnMaxCtas * attn_slot_floats(head_dim)
+                                         : kPromptMaxParts * NDQ_PROMPT_SLOT(head_dim));
 }
 
 struct AttnParams {
@@ -77,9 +86,12 @@ struct AttnParams {
     int32_t q_heads;
     int32_t group;   // query heads per cache head
     float scale_log2;  // scale * log2(e)
+    unsigned int* fault;  // device fault word (set by the launcher)
+    int32_t splits;       // prompts: CTAs per unit (set by the launcher)
     int32_t prompt_rows;  // > 0: requests with at least this many rows are left to the prompt kernel
 };
-int launch_attention(const AttnParams& p, int head_dim, bool e4m3, bool bf16, void* stream);
+int launch_attention_prompt(AttnParams p, int head_dim, bool e4m3, bool bf16, int dev, int sms, void* stream);
+int launch_attention(AttnParams p, int head_dim, bool e4m3, bool bf16, void* stream);
 
 struct LoraParams {
     const uint16_t* x;

@@ -148,7 +148,7 @@ int ndq_attention_kv8(const ndq_kv_cache* cache, const void* q, int dtype, int64
     p.kv_len = kv_len;
     p.q_start = q_start;
     p.counters = static_cast<uint32_t*>(workspace);
-    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ndq::kAttnMaxCtas * 4u);
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ndq::kAttnCounterBytes);
     p.n_tokens = n_tokens;
     p.n_req = n_req;
     p.q_stride = q_stride;
