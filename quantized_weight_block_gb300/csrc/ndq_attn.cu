@@ -98,8 +98,8 @@ __device__ __forceinline__ Req request(const AttnParams& p, int64_t r) {
     if (p.prompt_rows > 0 && static_cast<int64_t>(x.n) * p.group >= p.prompt_rows) x.n = 0;  // the other kernel's
     x.lo = 0;
     if (p.window > 0) {
-        const int64_t first = static_cast<int64_t>(x.kv) - x.n + 1 - p.window;
-        x.lo = first > 0 ? static_cast<int32_t>(first) & ~(kRowTile - 1) : 0;
+        const int32_t first = x.kv - x.n + 1 - p.window;
+        x.lo = first > 0 ? first & ~(kRowTile - 1) : 0;
     }
     x.units = x.kv > x.lo ? (x.kv - x.lo + kRowUnit - 1) / kRowUnit : 1;
     x.tiles = (x.n * p.group + ROWS - 1) / ROWS;
@@ -198,15 +198,15 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         const int32_t rows_left = x.n * p.group - row0;
         const int32_t nrows = rows_left < kRows ? rows_left : kRows;
         const int32_t qa = row0 / p.group, qb = (row0 + nrows - 1) / p.group;
-        const int64_t any_hi = static_cast<int64_t>(x.kv) - x.n + qb + 1, all_hi = static_cast<int64_t>(x.kv) - x.n + qa + 1;
-        const int64_t any_lo = p.window > 0 ? all_hi - p.window : 0, all_lo = p.window > 0 ? any_hi - p.window : 0;
+        const int32_t any_hi = x.kv - x.n + qb + 1, all_hi = x.kv - x.n + qa + 1;
+        const int32_t any_lo = p.window > 0 ? all_hi - p.window : 0, all_lo = p.window > 0 ? any_hi - p.window : 0;
 
         // this warp's tiles: base token x.lo + 16 (8 c + warp), c = ca .. cb - 1
         int32_t tok = x.lo + ca * kRowUnit + static_cast<int32_t>(warp) * kRowTile;
-        const int64_t seg_end = static_cast<int64_t>(x.lo) + static_cast<int64_t>(cb) * kRowUnit;
-        const int64_t tok_end = seg_end < any_hi ? seg_end : any_hi;
+        const int32_t seg_end = x.lo + cb * kRowUnit;
+        const int32_t tok_end = seg_end < any_hi ? seg_end : any_hi;
         while (tok + kRowTile <= any_lo && tok < tok_end) tok += kRowUnit;
-        const int32_t ntile = tok < tok_end ? static_cast<int32_t>((tok_end - tok + kRowUnit - 1) / kRowUnit) : 0;
+        const int32_t ntile = tok < tok_end ? (tok_end - tok + kRowUnit - 1) / kRowUnit : 0;
         const int32_t* table = p.table + r * p.width;
         // lane i holds the block id (-1: none) of tile 32 b + i
         auto ids_of = [&](int32_t b) -> int32_t {
@@ -284,9 +284,9 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         }
         // the tokens row i of the tile sees: [lo, hi)
         auto sees = [&](int32_t i, int32_t& lo, int32_t& hi) {
-            const int64_t pos = static_cast<int64_t>(x.kv) - x.n + (row0 + i) / p.group;
-            hi = i < nrows && pos >= 0 ? static_cast<int32_t>(pos) + 1 : 0;
-            lo = p.window > 0 && pos + 1 > p.window ? static_cast<int32_t>(pos + 1 - p.window) : 0;
+            const int32_t pos = x.kv - x.n + (row0 + i) / p.group;
+            hi = i < nrows && pos >= 0 ? pos + 1 : 0;
+            lo = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
         };
 
         float o[NT][KS][4];  // O^T: m-tile s rows are head positions VB g + 2 s, + 1; columns rows 8 nt + 2 t, + 1

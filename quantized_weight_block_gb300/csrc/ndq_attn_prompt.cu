@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "ndq_attn.cuh"
 #include "ndq_mma.cuh"
@@ -45,7 +46,10 @@ namespace {
 constexpr int kPrConv = 4;                      // converter warps
 constexpr int kPrConvWarp = 8;
 constexpr int kPrMmaWarp = kPrConvWarp + kPrConv;
-constexpr int kPrThreads = (kPrMmaWarp + 1) * 32;
+constexpr int kPrThreads = 512;                 // four warpgroups; warps 13-15 idle
+// Registers per thread after the split by warpgroup: launched with 128 each,
+// 256 * 168 + 128 * 128 + 128 * 48 = 512 * 128.
+constexpr int kPrLaunchRegs = 128;
 constexpr int kPrTokens = 128;                  // tokens of a K / V tile
 constexpr int kPrGroups = kPrTokens / 16;
 constexpr uint32_t kPrFault = 8u;               // bit of the device fault word
@@ -108,17 +112,24 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* v) {
         "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(a)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
-        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(a)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+// Barriers by number: every thread of the roles that meet there, and no other.
+template <int ID, int THREADS>
+__device__ __forceinline__ void meet() { asm volatile("barrier.cta.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory"); }
+constexpr int kMeetAll = 1, kMeetEnd = 2, kMeetRows = 3;
+
+template <int N>
+__device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
     uint64_t r;
@@ -228,29 +239,27 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     const int32_t nrows = rows_left < kPromptRows ? rows_left : kPromptRows;
     const int32_t nact = nrows > 128 ? 2 : 1;  // row tiles in use
     // tokens that some row / every row of the CTA sees
-    const int64_t first_pos = static_cast<int64_t>(kv) - n + row0 / p.group;
-    const int64_t last_pos = static_cast<int64_t>(kv) - n + (row0 + nrows - 1) / p.group;
-    const int64_t any_hi = last_pos + 1;
-    const int64_t any_lo = p.window > 0 && first_pos + 1 > p.window ? first_pos + 1 - p.window : 0;
-    const int64_t cta_hi = first_pos + 1;
-    const int64_t cta_lo = p.window > 0 ? last_pos + 1 - p.window : 0;
-    const int64_t lo16 = any_lo & ~int64_t(15);
-    const int64_t all_tiles = any_hi > lo16 ? (any_hi - lo16 + kPrTokens - 1) / kPrTokens : 0;
-    const int64_t j0 = all_tiles * split / p.splits;
-    const int32_t nt = static_cast<int32_t>(all_tiles * (split + 1) / p.splits - j0);
-    const int32_t tok0 = static_cast<int32_t>(lo16 + j0 * kPrTokens);  // first token of this CTA's tiles
+    const int32_t first_pos = kv - n + row0 / p.group, last_pos = kv - n + (row0 + nrows - 1) / p.group;
+    const int32_t any_hi = last_pos + 1, cta_hi = first_pos + 1;
+    const int32_t any_lo = p.window > 0 && first_pos + 1 > p.window ? first_pos + 1 - p.window : 0;
+    const int32_t cta_lo = p.window > 0 ? last_pos + 1 - p.window : 0;
+    const int32_t lo16 = any_lo & ~15;
+    const int32_t all_tiles = any_hi > lo16 ? (any_hi - lo16 + kPrTokens - 1) / kPrTokens : 0;
+    const int32_t j0 = all_tiles * static_cast<int32_t>(split) / p.splits;
+    const int32_t nt = all_tiles * static_cast<int32_t>(split + 1) / p.splits - j0;
+    const int32_t tok0 = lo16 + j0 * kPrTokens;  // first token of this CTA's tiles
 
     // Q: one row per softmax thread, scaled, as a 128-byte-swizzled operand
     const uint32_t wg = warp >> 2, wrow = tid & 127u;
     float frow = 0.0f;
     int32_t see_lo = 0, see_hi = 0;
-    int64_t at = 0;  // index of the row's output
+    int32_t at = 0;  // index of the row's output (n_tokens * q_heads is below 2^31)
     bool has_row = false;
     if (warp < kPrConvWarp) {
         const int32_t i = static_cast<int32_t>(wg * 128u + wrow);
         has_row = i < nrows;
         const int32_t qi = (row0 + (has_row ? i : 0)) / p.group, qh = h * p.group + (row0 + (has_row ? i : 0)) % p.group;
-        at = (q0 + qi) * p.q_heads + qh;
+        at = static_cast<int32_t>((q0 + qi) * p.q_heads) + qh;
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (q0 + qi) * p.q_stride + static_cast<int64_t>(qh) * D);
         float amax = 0.0f;
 #pragma unroll
@@ -285,9 +294,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             }
             *reinterpret_cast<uint4*>(dst + (c >> 3) * kAtom + sw128(wrow, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        const int64_t pos = static_cast<int64_t>(kv) - n + qi;
-        see_hi = has_row && pos >= 0 ? static_cast<int32_t>(pos) + 1 : 0;
-        see_lo = p.window > 0 && pos + 1 > p.window ? static_cast<int32_t>(pos + 1 - p.window) : 0;
+        const int32_t pos = kv - n + qi;
+        see_hi = has_row && pos >= 0 ? pos + 1 : 0;
+        see_lo = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
         fence_proxy_async_smem();
     }
     tc_fence_before();
@@ -298,6 +307,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
 
     if (warp >= kPrConvWarp && warp < kPrMmaWarp) {
         // ---- converters: groups cw and cw + 4 of every tile
+        regs_less<128>();
         constexpr int LPR = D / 8, RPI = 32 / LPR, ITS = 16 / RPI;  // lanes per row, rows per load, loads per group
         const uint32_t cw = warp - kPrConvWarp;
         const uint32_t lrow = lane / LPR, piece = lane % LPR;
@@ -305,7 +315,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         // lane i: group cw + 4 (i & 1) of tile 16 b + i / 2
         auto ids_of = [&](int32_t b) -> int32_t {
             const int32_t j = 16 * b + static_cast<int32_t>(lane >> 1);
-            const int64_t tk = static_cast<int64_t>(tok0) + static_cast<int64_t>(j) * kPrTokens + (cw + 4 * (lane & 1u)) * 16;
+            const int32_t tk = tok0 + j * kPrTokens + static_cast<int32_t>(cw + 4 * (lane & 1u)) * 16;
             if (j >= nt || tk >= any_hi) return -1;
             const int32_t id = table[tk >> bl];
             return id >= 0 && id < p.c.num_blocks ? id : -1;
@@ -326,14 +336,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int32_t id = __shfl_sync(0xffffffffu, set, 2 * (j & 15) + q);
-                const int64_t tk = static_cast<int64_t>(tok0) + static_cast<int64_t>(j) * kPrTokens + (cw + 4 * q) * 16 + lrow;
+                const int32_t g0 = tok0 + j * kPrTokens + static_cast<int32_t>(cw + 4 * q) * 16, tk = g0 + static_cast<int32_t>(lrow);
                 const uint64_t u = static_cast<uint64_t>(id < 0 ? 0 : id) * p.c.heads + static_cast<uint32_t>(h);
-                const uint8_t* src = codes + ((u << bl) + (static_cast<uint64_t>(tk) & ((1u << bl) - 1u))) * D + piece * 8;
+                const uint8_t* src = codes + ((u << bl) + (static_cast<uint32_t>(tk) & ((1u << bl) - 1u))) * D + piece * 8;
+                if (id >= 0 && g0 + 16 <= any_hi && g0 >= any_lo) {
 #pragma unroll
-                for (int i = 0; i < ITS; ++i) {
-                    const int64_t tt = tk + i * RPI;
-                    d[q][i] = make_uint2(0u, 0u);
-                    if (id >= 0 && tt < any_hi && tt >= any_lo) d[q][i] = __ldg(reinterpret_cast<const uint2*>(src + i * RPI * D));
+                    for (int i = 0; i < ITS; ++i) d[q][i] = __ldg(reinterpret_cast<const uint2*>(src + i * RPI * D));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < ITS; ++i) {
+                        const int32_t tt = tk + i * RPI;
+                        d[q][i] = make_uint2(0u, 0u);
+                        if (id >= 0 && tt < any_hi && tt >= any_lo) d[q][i] = __ldg(reinterpret_cast<const uint2*>(src + i * RPI * D));
+                    }
                 }
             }
         };
@@ -394,7 +409,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     for (int i = 0; i < ITS; ++i) vr[q][i] = make_uint2(0u, 0u);
                 }
             if constexpr (E4M3) {
-                const int64_t tb = static_cast<int64_t>(tok0) + static_cast<int64_t>(j) * kPrTokens;
+                const int32_t tb = tok0 + j * kPrTokens;
                 if (tb + kPrTokens > cta_hi || tb < cta_lo) {  // some rows see only part of this tile
                     bool odd = false;
 #pragma unroll
@@ -415,7 +430,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             if (lane == 0) mbar_arrive(&S.vfull[st]);
         }
         if (!ok && lane == 0) atomicOr(&S.fault, 1u);
-    } else if (warp == kPrMmaWarp) {
+        tc_fence_before();
+        meet<kMeetAll, kPrThreads>();
+        return;
+    }
+    if (warp >= kPrMmaWarp) {
+        regs_less<48>();
+        if (warp != kPrMmaWarp) {  // (only there to make the warpgroup whole)
+            meet<kMeetAll, kPrThreads>();
+            return;
+        }
         // ---- MMA issue
         constexpr uint32_t kIdQ = (1u << 4) | ((kPrTokens >> 3) << 17) | ((128u >> 4) << 24);
         constexpr uint32_t kIdP = (1u << 4) | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
@@ -475,16 +499,66 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             if (scored[i] > 0) ok = wait(&S.sfull[i], static_cast<uint32_t>((scored[i] - 1) & 1)) && ok;
             if (issued[i] > 0) ok = wait(&S.odone[i], static_cast<uint32_t>((issued[i] - 1) & 1)) && ok;
         }
-        if (!ok && lane == 0) atomicOr(&S.fault, 1u);
-    } else if (static_cast<int32_t>(wg) < nact) {
+        if (!ok && lane == 0) {
+            atomicOr(&S.fault, 1u);
+            atomicOr(p.fault, kPrFault);
+        }
+        tc_fence_before();
+        meet<kMeetAll, kPrThreads>();
+        meet<kMeetEnd, 256 + 32>();  // the rows are read out of tensor memory
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        return;
+    }
+    regs_more<168>();
+    if (static_cast<int32_t>(wg) < nact) {
         // ---- softmax: one row per thread
         const uint32_t tS = tmem + 128u * wg + ((32u * (warp & 3u)) << 16), tO = tmem + kO + D * wg + ((32u * (warp & 3u)) << 16);
         const int32_t wrow0 = row0 + 128 * static_cast<int32_t>(wg);
         const int32_t wrows = nrows - 128 * static_cast<int32_t>(wg) < 128 ? nrows - 128 * static_cast<int32_t>(wg) : 128;
-        const int64_t all_hi = static_cast<int64_t>(kv) - n + wrow0 / p.group + 1;
-        const int64_t all_lo = p.window > 0 ? static_cast<int64_t>(kv) - n + (wrow0 + wrows - 1) / p.group + 1 - p.window : 0;
+        const int32_t all_hi = kv - n + wrow0 / p.group + 1;
+        const int32_t all_lo = p.window > 0 ? kv - n + (wrow0 + wrows - 1) / p.group + 1 - p.window : 0;
         float ms = 0.0f;
         bool ok = true;
+        uint32_t w[kPrTokens / 2];  // the row's weights of the tile, in pairs
+        // The weights relative to ms, their sum and the largest exponent.
+        auto weigh = [&](auto mask, const float4* cst, int32_t tb, float& ts, float& top) {
+            constexpr bool kMasked = decltype(mask)::value;
+            uint32_t v[2][32];
+            ts = 0.0f;
+            top = -INFINITY;
+            tmem_ld32(tS, v[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                tmem_wait_ld();
+                if (c < 3) tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
+                const uint32_t* x = v[c & 1];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float4 k = cst[2 * c + q];
+                    const uint64_t f2 = pair(frow * k.x, frow * k.x), c2 = pair(k.y - ms, k.y - ms);
+                    uint64_t s2 = 0;
+                    const int32_t pos = tb + 32 * c + 16 * q;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        float a, b;
+                        unpair(pair_fma(pair(__uint_as_float(x[16 * q + e]), __uint_as_float(x[16 * q + e + 1])), f2, c2), a, b);
+                        if constexpr (kMasked) {
+                            if (pos + e < see_lo || pos + e >= see_hi) a = -INFINITY;
+                            if (pos + e + 1 < see_lo || pos + e + 1 >= see_hi) b = -INFINITY;
+                        }
+                        top = max3(top, a, b);
+                        a = exp2_fast(a);
+                        b = exp2_fast(b);
+                        s2 = pair_add(s2, pair(a, b));
+                        w[16 * c + 8 * q + e / 2] = pack_half2(a, b);
+                    }
+                    float a, b;
+                    unpair(s2, a, b);
+                    ts = __fmaf_rn(a + b, k.z, ts);
+                }
+            }
+        };
         for (int32_t j = 0; j < nt; ++j) {
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.sfull[wg], static_cast<uint32_t>(j & 1)));
             if (!ok) break;
@@ -492,35 +566,18 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             const int32_t tb = tok0 + j * kPrTokens;
             const bool masked = tb + kPrTokens > all_hi || tb < all_lo;
             const float4* cst = S.cst[j & 3];
-            // the row's largest score of the tile
-            float tm = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t v[32];
-                tmem_ld32(tS + 32 * c, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float4 k = cst[2 * c + q];
-                    float m = -INFINITY;
-                    if (!masked) {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) m = max3(m, __uint_as_float(v[16 * q + e]), __uint_as_float(v[16 * q + e + 1]));
-                    } else {
-                        const int32_t pos = tb + 32 * c + 16 * q;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            m = fmaxf(m, pos + e >= see_lo && pos + e < see_hi ? __uint_as_float(v[16 * q + e]) : -INFINITY);
-                    }
-                    // (m is -inf where nothing is seen: not times a scale of 0)
-                    if (m > -INFINITY) tm = fmaxf(tm, __fmaf_rn(m, frow * k.x, k.y));
-                }
-            }
-            const bool grow = tm > (mx == -INFINITY ? -INFINITY : mx + 8.0f);
-            if (__any_sync(0xffffffffu, grow)) {
-                const float al = !grow ? 1.0f : (mx == -INFINITY ? 0.0f : exp2_fast(mx - tm));
-                if (j > 0) {  // the product before this one is done with O
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((j - 1) & 1)));
+            float ts, top;
+            bool waited = false;
+            // (again when a row passed its maximum by 8: always for the first tile that it sees, rarely later)
+            for (int again = 0; again < 3; ++again) {
+                if (masked) weigh(std::true_type{}, cst, tb, ts, top);
+                else weigh(std::false_type{}, cst, tb, ts, top);
+                const bool grow = top > (mx == -INFINITY ? -INFINITY : 8.0f);
+                if (!__any_sync(0xffffffffu, grow)) break;
+                const float al = !grow ? 1.0f : (mx == -INFINITY ? 0.0f : exp2_fast(-top));
+                if (j > 0) {  // O moves to the new maximum once the product before this one is done with it
+                    if (!waited) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((j - 1) & 1)));
+                    waited = true;
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -532,41 +589,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                         for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
                         tmem_st32(tO + 32 * c, v);
                     }
+                    tmem_wait_st();
                 }
                 sum *= al;
-                if (grow) mx = ms = tm;
+                if (grow) mx = ms = ms + top;
             }
-            // weights, in place
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t v[32], w[16];
-                tmem_ld32(tS + 32 * c, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float4 k = cst[2 * c + q];
-                    const uint64_t f2 = pair(frow * k.x, frow * k.x), c2 = pair(k.y - ms, k.y - ms);
-                    uint64_t s2 = 0;
-                    const int32_t pos = tb + 32 * c + 16 * q;
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float a, b;
-                        unpair(pair_fma(pair(__uint_as_float(v[16 * q + e]), __uint_as_float(v[16 * q + e + 1])), f2, c2), a, b);
-                        if (masked) {
-                            if (pos + e < see_lo || pos + e >= see_hi) a = -INFINITY;
-                            if (pos + e + 1 < see_lo || pos + e + 1 >= see_hi) b = -INFINITY;
-                        }
-                        a = exp2_fast(a);
-                        b = exp2_fast(b);
-                        s2 = pair_add(s2, pair(a, b));
-                        w[8 * q + e / 2] = pack_half2(a, b);
-                    }
-                    float a, b;
-                    unpair(s2, a, b);
-                    sum = __fmaf_rn(a + b, k.z, sum);
-                }
-                tmem_st16(tS + 16 * c, w);
-            }
+            if (!ok) break;
+            sum += ts;
+            tmem_st32(tS, w);
+            tmem_st32(tS + 32, w + 32);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -579,28 +610,28 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         if (!ok && lane == 0) atomicOr(&S.fault, 1u);
     }
     tc_fence_before();
-    __syncthreads();
+    meet<kMeetAll, kPrThreads>();
     tc_fence_after();
     const bool fault = S.fault != 0u;
     if (fault && tid == 0) atomicOr(p.fault, kPrFault);
 
-    if (!fault && warp < kPrConvWarp && static_cast<int32_t>(wg) < nact) {
+    if (!fault && static_cast<int32_t>(wg) < nact) {
         const uint32_t tO = tmem + kO + D * wg + ((32u * (warp & 3u)) << 16);
         // head positions that this row sees as NaN although the product left them out
         uint32_t bad[D / 32] = {};
         if (E4M3 && S.nan != 0u) {
             const int32_t* table = p.table + r * p.width;
             for (int32_t j = 0; j < nt; ++j) {
-                const int64_t tb = static_cast<int64_t>(tok0) + static_cast<int64_t>(j) * kPrTokens;
+                const int32_t tb = tok0 + j * kPrTokens;
                 if (tb + kPrTokens <= cta_hi && tb >= cta_lo) continue;
-                const int64_t a = tb > see_lo ? tb : see_lo, b = tb + kPrTokens < see_hi ? tb + kPrTokens : see_hi;
-                for (int64_t tk = a; tk < b; ++tk) {
+                const int32_t a = tb > see_lo ? tb : see_lo, b = tb + kPrTokens < see_hi ? tb + kPrTokens : see_hi;
+                for (int32_t tk = a; tk < b; ++tk) {
                     const int32_t id = table[tk >> bl];
                     if (id < 0 || id >= p.c.num_blocks) continue;
                     const uint64_t u = static_cast<uint64_t>(id) * p.c.heads + static_cast<uint32_t>(h);
                     if (p.c.vs[u] == 0.0f) continue;
                     const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                        p.c.v + ((u << bl) + (static_cast<uint64_t>(tk) & ((1u << bl) - 1u))) * D);
+                        p.c.v + ((u << bl) + (static_cast<uint32_t>(tk) & ((1u << bl) - 1u))) * D);
 #pragma unroll
                     for (int w = 0; w < D / 4; ++w) {
                         const uint32_t x = nan_bytes(v[w]) >> 7;
@@ -642,7 +673,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     d[(8 * c + e) * kPromptRows + prow] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
                                                                      __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
             } else if (has_row) {
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + 32 * c);
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(at) * D + 32 * c);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint32_t o[4];
@@ -658,18 +689,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             p.lse[at] = sum > 0.0f ? (mx + log2f(sum)) * 0.6931471805599453f : (sum == sum ? -INFINITY : sum);
     }
     tc_fence_before();
+    meet<kMeetEnd, 256 + 32>();
     if (p.splits > 1) {
         // the last part of the unit to arrive joins them in order
         __threadfence();
-        __syncthreads();
+        meet<kMeetRows, 256>();
         if (tid == 0) {
             const uint32_t seen = atomicAdd(p.counters + unit, 1u);
             S.last = seen == static_cast<uint32_t>(p.splits - 1);
             if (S.last) p.counters[unit] = 0u;
             __threadfence();
         }
-        __syncthreads();
-        if (S.last && !fault && warp < kPrConvWarp && has_row) {
+        meet<kMeetRows, 256>();
+        if (S.last && !fault && has_row) {
             const uint32_t prow = wg * 128u + wrow;
             const float* first = p.parts + unit * static_cast<uint64_t>(p.splits) * NDQ_PROMPT_SLOT(D);
             float M = -INFINITY, L = 0.0f;
@@ -702,15 +734,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     b.z = __fmaf_rn(y.z, f, b.z);
                     b.w = __fmaf_rn(y.w, f, b.w);
                 }
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + 8 * c) =
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(at) * D + 8 * c) =
                     make_uint4(narrow2<BF16>(a.x * inv, a.y * inv), narrow2<BF16>(a.z * inv, a.w * inv),
                                narrow2<BF16>(b.x * inv, b.y * inv), narrow2<BF16>(b.z * inv, b.w * inv));
             }
             if (p.lse) p.lse[at] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : (L == L ? -INFINITY : L);
         }
     }
-    __syncthreads();
-    if (warp == kPrMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 template <int D, bool E4M3, bool BF16>
@@ -721,6 +751,11 @@ int launch_typed(const AttnParams& p, unsigned grid, int dev, void* stream) {
         const cudaError_t e =
             cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(PrSmem<D>::kBytes));
         if (e != cudaSuccess) return static_cast<int>(e);
+        // the register split draws on what the block is launched with
+        cudaFuncAttributes attr;
+        const cudaError_t e2 = cudaFuncGetAttributes(&attr, fn);
+        if (e2 != cudaSuccess) return static_cast<int>(e2);
+        if (attr.numRegs != kPrLaunchRegs) return static_cast<int>(cudaErrorInvalidKernelImage);
         ready[dev] = true;
     }
     fn<<<grid, kPrThreads, PrSmem<D>::kBytes, static_cast<cudaStream_t>(stream)>>>(p);

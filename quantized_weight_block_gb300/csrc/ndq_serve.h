@@ -81,7 +81,7 @@ struct AttnParams {
     int64_t n_req;
     int64_t q_stride;
     int64_t width;
-    int64_t window;  // 0: none
+    int32_t window;  // 0: none (at most 2^30, so positions and windows add up in 32 bits)
     int64_t max_q;
     int32_t q_heads;
     int32_t group;   // query heads per cache head

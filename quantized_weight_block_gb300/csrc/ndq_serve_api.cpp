@@ -153,7 +153,7 @@ int ndq_attention_kv8(const ndq_kv_cache* cache, const void* q, int dtype, int64
     p.n_req = n_req;
     p.q_stride = q_stride;
     p.width = table_width;
-    p.window = window;
+    p.window = window > (INT64_C(1) << 30) ? 0 : static_cast<int32_t>(window);  // (no table is that long)
     p.max_q = q_start ? max_q : 1;
     p.q_heads = q_heads;
     p.group = q_heads / cache->kv_heads;
