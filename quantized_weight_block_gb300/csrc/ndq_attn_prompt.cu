@@ -9,10 +9,11 @@
 // exponential per row and token beside them.
 //
 // Roles, joined by mbarriers only:
-// * warps 8-11 (converters) load the codes of 128 tokens straight into
-//   registers, one tile ahead, widen them to binary16 (exact) and store them
-//   as 128-byte-swizzled operands, K and V each in a ring of two; they also
-//   publish each 16-token group's constants (a group lies in one block);
+// * warp 13 (loader) brings the codes of 128 tokens, K and V, into shared
+//   memory by bulk copies of 16 tokens (which lie in one block), two tiles
+//   ahead, and publishes each 16-token group's scales;
+// * warps 8-11 (converters) widen them to binary16 (exact) and store them as
+//   128-byte-swizzled operands, K in a ring of two, V in one stage;
 // * warp 12 issues the MMAs: S_i = Q_i K^T into tensor memory, and
 //   O_i += P_i V with P_i read from tensor memory; V is used as it lies
 //   (tokens by head positions, an operand contiguous along N);
@@ -46,18 +47,22 @@ namespace {
 constexpr int kPrConv = 4;                      // converter warps
 constexpr int kPrConvWarp = 8;
 constexpr int kPrMmaWarp = kPrConvWarp + kPrConv;
-constexpr int kPrThreads = 512;                 // four warpgroups; warps 13-15 idle
+constexpr int kPrLoadWarp = kPrMmaWarp + 1;
+constexpr int kPrRaw = 4;                       // staged tiles of codes: K and V of two tiles
+constexpr int kPrCst = 8;                       // tiles of group constants
+constexpr int kPrThreads = 512;                 // four warpgroups; warps 14 and 15 idle
 // Registers per thread after the split by warpgroup: launched with 128 each,
-// 256 * 168 + 128 * 128 + 128 * 48 = 512 * 128.
+// 256 * 176 + 128 * 96 + 128 * 64 = 512 * 128.
 constexpr int kPrLaunchRegs = 128;
 constexpr int kPrTokens = 128;                  // tokens of a K / V tile
 constexpr int kPrGroups = kPrTokens / 16;
 constexpr uint32_t kPrFault = 8u;               // bit of the device fault word
 
 struct PrShared {
-    uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
+    uint64_t rawfull[kPrRaw], rawfree[kPrRaw];
+    uint64_t kfull[2], kfree[2], vfull, vfree;
     uint64_t sfull[2], pfull[2], odone[2];
-    float4 cst[4][kPrGroups];  // per group: K's scale, log2 of V's scale, 1 / V's scale
+    float4 cst[kPrCst][kPrGroups];  // per group: K's scale, log2 of V's scale, 1 / V's scale
     uint32_t tmem;
     uint32_t fault;
     uint32_t nan;   // V has NaN codes in a tile that some rows see only part of
@@ -69,7 +74,7 @@ struct PrShared {
 template <int D>
 struct PrSmem {
     static constexpr uint32_t kTile = kPrTokens * D * 2;  // K, V or Q tile
-    static constexpr uint32_t kBytes = 1024 + 6 * kTile + sizeof(PrShared);
+    static constexpr uint32_t kBytes = 1024 + 7 * kTile + sizeof(PrShared);  // 2 Q, 2 K, 1 V, 4 tiles of codes
 };
 
 // MN-major operand (N contiguous, 128-byte swizzle): 64 columns of N 128 rows
@@ -112,7 +117,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* v) {
         "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(a)
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The wait for the loads before it names their registers, so that nothing that
+// uses them can be moved ahead of it.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t* v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
+                   "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+                   "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Barriers by number: every thread of the roles that meet there, and no other.
@@ -167,8 +182,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pr_raw) + 1023u) & ~uintptr_t(1023));
     uint8_t* sK = base;
     uint8_t* sV = base + 2 * kTile;
-    uint8_t* sQ = base + 4 * kTile;
-    PrShared& S = *reinterpret_cast<PrShared*>(base + 6 * kTile);
+    uint8_t* sRaw = base + 3 * kTile;
+    uint8_t* sQ = base + 5 * kTile;
+    PrShared& S = *reinterpret_cast<PrShared*>(base + 7 * kTile);
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
     const int bl = p.c.bs_log2;
 
@@ -205,11 +221,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         }
     }
     if (tid == 0) {
+        for (int i = 0; i < kPrRaw; ++i) {
+            mbar_init(&S.rawfull[i], 1);
+            mbar_init(&S.rawfree[i], kPrConv);
+        }
+        mbar_init(&S.vfull, kPrConv);
+        mbar_init(&S.vfree, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.kfull[i], kPrConv);
-            mbar_init(&S.vfull[i], kPrConv);
             mbar_init(&S.kfree[i], 1);
-            mbar_init(&S.vfree[i], 1);
             mbar_init(&S.sfull[i], 1);
             mbar_init(&S.odone[i], 1);
             mbar_init(&S.pfull[i], 4);
@@ -307,127 +327,73 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
 
     if (warp >= kPrConvWarp && warp < kPrMmaWarp) {
         // ---- converters: groups cw and cw + 4 of every tile
-        regs_less<128>();
+        regs_less<96>();
         constexpr int LPR = D / 8, RPI = 32 / LPR, ITS = 16 / RPI;  // lanes per row, rows per load, loads per group
         const uint32_t cw = warp - kPrConvWarp;
         const uint32_t lrow = lane / LPR, piece = lane % LPR;
-        const int32_t* table = p.table + r * p.width;
-        // lane i: group cw + 4 (i & 1) of tile 16 b + i / 2
-        auto ids_of = [&](int32_t b) -> int32_t {
-            const int32_t j = 16 * b + static_cast<int32_t>(lane >> 1);
-            const int32_t tk = tok0 + j * kPrTokens + static_cast<int32_t>(cw + 4 * (lane & 1u)) * 16;
-            if (j >= nt || tk >= any_hi) return -1;
-            const int32_t id = table[tk >> bl];
-            return id >= 0 && id < p.c.num_blocks ? id : -1;
-        };
-        int32_t ids = ids_of(0), ids_next = ids_of(1);
-        float ks_l = 0.0f, vs_l = 0.0f;
-        auto scales_of = [&]() {
-            if (ids >= 0) {
-                const uint64_t u = static_cast<uint64_t>(ids) * p.c.heads + static_cast<uint32_t>(h);
-                ks_l = p.c.ks[u];
-                vs_l = p.c.vs[u];
-            }
-        };
-        scales_of();
-        uint2 kr[2][ITS], vr[2][ITS];
-        // the codes of tile j: rows outside what the CTA sees as zeros
-        auto load = [&](const uint8_t* codes, int32_t j, uint2 (&d)[2][ITS], int32_t set) {
+        bool ok = true;
+        // one tile of codes to an operand; rows outside what the CTA sees, and groups of weight 0, as zeros
+        auto convert = [&](const uint8_t* raw, uint8_t* tile, int32_t j, bool is_v) {
+            const int32_t tb = tok0 + j * kPrTokens;
+            const bool part = tb + kPrTokens > cta_hi || tb < cta_lo;  // some rows see only part of this tile
+            uint2 x[2][ITS];  // (all loads before the first store: the compiler must assume that they alias)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < ITS; ++i)
+                    x[q][i] = *reinterpret_cast<const uint2*>(raw + ((cw + 4 * q) * 16 + i * RPI + lrow) * D + piece * 8);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int32_t id = __shfl_sync(0xffffffffu, set, 2 * (j & 15) + q);
-                const int32_t g0 = tok0 + j * kPrTokens + static_cast<int32_t>(cw + 4 * q) * 16, tk = g0 + static_cast<int32_t>(lrow);
-                const uint64_t u = static_cast<uint64_t>(id < 0 ? 0 : id) * p.c.heads + static_cast<uint32_t>(h);
-                const uint8_t* src = codes + ((u << bl) + (static_cast<uint32_t>(tk) & ((1u << bl) - 1u))) * D + piece * 8;
-                if (id >= 0 && g0 + 16 <= any_hi && g0 >= any_lo) {
+                const float4 c = S.cst[j % kPrCst][cw + 4 * q];
+                if (c.w == 0.0f && (is_v || c.y == -INFINITY)) {
 #pragma unroll
-                    for (int i = 0; i < ITS; ++i) d[q][i] = __ldg(reinterpret_cast<const uint2*>(src + i * RPI * D));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < ITS; ++i) {
-                        const int32_t tt = tk + i * RPI;
-                        d[q][i] = make_uint2(0u, 0u);
-                        if (id >= 0 && tt < any_hi && tt >= any_lo) d[q][i] = __ldg(reinterpret_cast<const uint2*>(src + i * RPI * D));
-                    }
+                    for (int i = 0; i < ITS; ++i) x[q][i] = make_uint2(0u, 0u);
                 }
             }
-        };
-        auto store = [&](uint8_t* tile, uint2 (&d)[2][ITS]) {
+            if (part) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int i = 0; i < ITS; ++i) {
+                        const int32_t tk = tb + static_cast<int32_t>((cw + 4 * q) * 16 + i * RPI + lrow);
+                        if (tk >= any_hi || tk < any_lo) x[q][i] = make_uint2(0u, 0u);
+                        if (E4M3 && is_v) {  // NaN codes that only some rows see: see the end of the kernel
+                            const uint32_t nx = nan_bytes(x[q][i].x), ny = nan_bytes(x[q][i].y);
+                            if ((nx | ny) != 0u) S.nan = 1u;
+                            x[q][i].x &= ~((nx >> 7) * 0xffu);
+                            x[q][i].y &= ~((ny >> 7) * 0xffu);
+                        }
+                    }
+            }
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
                 for (int i = 0; i < ITS; ++i) {
                     uint4 o;
-                    widen4<E4M3>(d[q][i].x, o.x, o.y);
-                    widen4<E4M3>(d[q][i].y, o.z, o.w);
+                    widen4<E4M3>(x[q][i].x, o.x, o.y);
+                    widen4<E4M3>(x[q][i].y, o.z, o.w);
                     *reinterpret_cast<uint4*>(tile + (piece >> 3) * kAtom + sw128((cw + 4 * q) * 16 + i * RPI + lrow, piece & 7u)) = o;
                 }
+            fence_proxy_async_smem();
+            __syncwarp();
         };
-        bool ok = true;
-        if (nt > 0) load(p.c.k, 0, kr, ids);
-        for (int32_t j = 0; j < nt && ok; ++j) {
-            if ((j & 15) == 0 && j > 0) {
-                ids = ids_next;
-                ids_next = ids_of((j >> 4) + 1);
-                scales_of();
-            }
-            load(p.c.v, j, vr, ids);
-            const uint32_t st = static_cast<uint32_t>(j & 1), ph = static_cast<uint32_t>(((j >> 1) - 1) & 1);
-            // the groups' constants (ring of four: the tile four before is out of use once K's stage is free)
-            float vsg[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int src = 2 * (j & 15) + q;
-                const int32_t id = __shfl_sync(0xffffffffu, ids, src);
-                const float ks = __shfl_sync(0xffffffffu, ks_l, src), vs = __shfl_sync(0xffffffffu, vs_l, src);
-                vsg[q] = id < 0 ? 0.0f : vs;
-                float4 c = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);  // a missing block: weight 0
-                if (id >= 0) {
-                    float f, e, inv;
-                    split_scale(vs, f, e, inv);
-                    float lg;
-                    asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(vs == 0.0f ? 1.0f : f));
-                    c = make_float4(ks, e + lg, vs == 0.0f ? 1.0f : __fdiv_rn(1.0f, vs), 0.0f);
-                }
-                if (j >= 2 && q == 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.kfree[st], ph));
-                if (!ok) break;
-                if (lane == 0) S.cst[j & 3][cw + 4 * q] = c;
-            }
+        auto wait = [&](uint64_t* b, int32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(b, static_cast<uint32_t>(parity & 1))); };
+        for (int32_t j = 0; j < nt; ++j) {
+            const uint32_t st = static_cast<uint32_t>(j & 1), rs = 2 * st;
+            ok = wait(&S.rawfull[rs], j >> 1) && (j < 2 || wait(&S.kfree[st], (j >> 1) - 1));
             if (!ok) break;
-            store(sK + st * kTile, kr);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.kfull[st]);
-            if (j + 1 < nt) load(p.c.k, j + 1, kr, ((j + 1) & 15) == 0 ? ids_next : ids);
-            if (j >= 2) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.vfree[st], ph));
-            if (!ok) break;
-            // a block of V of scale 0 counts as zeros
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                if (vsg[q] == 0.0f) {
-#pragma unroll
-                    for (int i = 0; i < ITS; ++i) vr[q][i] = make_uint2(0u, 0u);
-                }
-            if constexpr (E4M3) {
-                const int32_t tb = tok0 + j * kPrTokens;
-                if (tb + kPrTokens > cta_hi || tb < cta_lo) {  // some rows see only part of this tile
-                    bool odd = false;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int i = 0; i < ITS; ++i) {
-                            const uint32_t nx = nan_bytes(vr[q][i].x), ny = nan_bytes(vr[q][i].y);
-                            odd |= (nx | ny) != 0u;
-                            vr[q][i].x &= ~((nx >> 7) * 0xffu);
-                            vr[q][i].y &= ~((ny >> 7) * 0xffu);
-                        }
-                    if (odd) S.nan = 1u;
-                }
+            convert(sRaw + rs * (kTile / 2), sK + st * kTile, j, false);
+            if (lane == 0) {
+                mbar_arrive(&S.kfull[st]);
+                mbar_arrive(&S.rawfree[rs]);
             }
-            store(sV + st * kTile, vr);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.vfull[st]);
+            ok = wait(&S.rawfull[rs + 1], j >> 1) && (j < 1 || wait(&S.vfree, j - 1));
+            if (!ok) break;
+            convert(sRaw + (rs + 1) * (kTile / 2), sV, j, true);
+            if (lane == 0) {
+                mbar_arrive(&S.vfull);
+                mbar_arrive(&S.rawfree[rs + 1]);
+            }
         }
         if (!ok && lane == 0) atomicOr(&S.fault, 1u);
         tc_fence_before();
@@ -435,7 +401,62 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         return;
     }
     if (warp >= kPrMmaWarp) {
-        regs_less<48>();
+        regs_less<64>();
+        if (warp == kPrLoadWarp) {
+            // ---- loader: lane 8 i + g holds group g of tile 4 b + i
+            const int32_t* table = p.table + r * p.width;
+            const uint32_t gl = lane & 7u;
+            auto ids_of = [&](int32_t b) -> int32_t {
+                const int32_t j = 4 * b + static_cast<int32_t>(lane >> 3);
+                const int32_t tk = tok0 + j * kPrTokens + static_cast<int32_t>(gl) * 16;
+                if (j >= nt || tk >= any_hi) return -1;
+                const int32_t id = table[tk >> bl];
+                return id >= 0 && id < p.c.num_blocks ? id : -1;
+            };
+            bool ok = true;
+            int32_t ids = -1, ids_next = ids_of(0), issued = 0;
+            uint64_t off = 0;
+            float4 c = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
+            for (int32_t j = 0; j < nt && ok; ++j) {
+                if ((j & 3) == 0) {
+                    ids = ids_next;
+                    ids_next = ids_of((j >> 2) + 1);
+                    c = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);  // a missing block: weight 0
+                    if (ids >= 0) {
+                        const uint64_t u = static_cast<uint64_t>(ids) * p.c.heads + static_cast<uint32_t>(h);
+                        const int32_t tk = tok0 + (j + static_cast<int32_t>(lane >> 3)) * kPrTokens + static_cast<int32_t>(gl) * 16;
+                        off = ((u << bl) + (static_cast<uint32_t>(tk) & ((1u << bl) - 1u))) * D;
+                        const float vs = p.c.vs[u];
+                        float f, e, inv, lg;
+                        split_scale(vs, f, e, inv);
+                        asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(vs == 0.0f ? 1.0f : f));
+                        // (a block of V of scale 0 counts as zeros)
+                        c = make_float4(p.c.ks[u], e + lg, vs == 0.0f ? 1.0f : __fdiv_rn(1.0f, vs), vs == 0.0f ? 0.0f : 1.0f);
+                    }
+                }
+                const bool mine = static_cast<int32_t>(lane >> 3) == (j & 3);
+                const uint32_t n16 = __popc(__ballot_sync(0xffffffffu, mine && ids >= 0));
+                for (int32_t half = 0; half < 2; ++half) {  // K, V
+                    const uint32_t rs = static_cast<uint32_t>(2 * (j & 1) + half);
+                    if (j >= 2) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.rawfree[rs], static_cast<uint32_t>(((j >> 1) - 1) & 1)));
+                    if (!ok) break;
+                    if (half == 0 && mine) S.cst[j % kPrCst][gl] = c;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(&S.rawfull[rs], n16 * 16u * D);
+                    __syncwarp();
+                    if (mine && ids >= 0)
+                        bulk_load(sRaw + rs * (kTile / 2) + gl * 16u * D, (half ? p.c.v : p.c.k) + off, 16u * D, &S.rawfull[rs]);
+                    ++issued;
+                }
+            }
+            if (!ok) {  // its own copies in flight land before the block ends
+                if (lane == 0) atomicOr(&S.fault, 1u);
+                for (int32_t i = issued > kPrRaw ? issued - kPrRaw : 0; i < issued; ++i)
+                    mbar_wait_bounded(&S.rawfull[i & 3], static_cast<uint32_t>((i >> 2) & 1));
+            }
+            meet<kMeetAll, kPrThreads>();
+            return;
+        }
         if (warp != kPrMmaWarp) {  // (only there to make the warpgroup whole)
             meet<kMeetAll, kPrThreads>();
             return;
@@ -468,19 +489,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             }
         }
         for (int32_t j = 0; j < nt && ok; ++j) {
-            ok = wait(&S.vfull[j & 1], static_cast<uint32_t>((j >> 1) & 1));
+            ok = wait(&S.vfull, static_cast<uint32_t>(j & 1));
             for (int32_t i = 0; i < nact && ok; ++i) {
                 ok = wait(&S.pfull[i], static_cast<uint32_t>(j & 1));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t b0 = smem_addr(sV + (j & 1) * kTile);
+                const uint32_t b0 = smem_addr(sV);
                 if (elect_one()) {
 #pragma unroll
                     for (uint32_t s = 0; s < kPrTokens / 16; ++s)
                         mma_ts(tmem + kO + D * i, tmem + 128u * i + 8u * s, sdesc_mn(b0 + s * 2048u, kAtom), kIdP,
                                j > 0 || s > 0 ? 1u : 0u);
                     mma_commit(&S.odone[i]);
-                    if (i == nact - 1) mma_commit(&S.vfree[j & 1]);
+                    if (i == nact - 1) mma_commit(&S.vfree);
                 }
                 __syncwarp();
                 ++issued[i];
@@ -510,7 +531,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
         return;
     }
-    regs_more<168>();
+    regs_more<176>();
     if (static_cast<int32_t>(wg) < nact) {
         // ---- softmax: one row per thread
         const uint32_t tS = tmem + 128u * wg + ((32u * (warp & 3u)) << 16), tO = tmem + kO + D * wg + ((32u * (warp & 3u)) << 16);
@@ -526,11 +547,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             constexpr bool kMasked = decltype(mask)::value;
             uint32_t v[2][32];
             ts = 0.0f;
-            top = -INFINITY;
+            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             tmem_ld32(tS, v[0]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                tmem_wait_ld();
+                tmem_wait_ld32(v[c & 1]);
                 if (c < 3) tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
                 const uint32_t* x = v[c & 1];
 #pragma unroll
@@ -547,7 +568,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                             if (pos + e < see_lo || pos + e >= see_hi) a = -INFINITY;
                             if (pos + e + 1 < see_lo || pos + e + 1 >= see_hi) b = -INFINITY;
                         }
-                        top = max3(top, a, b);
+                        tops[(e / 2) & 3] = max3(tops[(e / 2) & 3], a, b);
                         a = exp2_fast(a);
                         b = exp2_fast(b);
                         s2 = pair_add(s2, pair(a, b));
@@ -558,6 +579,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     ts = __fmaf_rn(a + b, k.z, ts);
                 }
             }
+            top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
         };
         for (int32_t j = 0; j < nt; ++j) {
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.sfull[wg], static_cast<uint32_t>(j & 1)));
@@ -565,7 +587,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             tc_fence_after();
             const int32_t tb = tok0 + j * kPrTokens;
             const bool masked = tb + kPrTokens > all_hi || tb < all_lo;
-            const float4* cst = S.cst[j & 3];
+            const float4* cst = S.cst[j % kPrCst];
             float ts, top;
             bool waited = false;
             // (again when a row passed its maximum by 8: always for the first tile that it sees, rarely later)
@@ -584,7 +606,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t v[32];
                         tmem_ld32(tO + 32 * c, v);
-                        tmem_wait_ld();
+                        tmem_wait_ld32(v);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
                         tmem_st32(tO + 32 * c, v);
@@ -652,7 +674,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             uint32_t v[32];
             if (nt > 0) {
                 tmem_ld32(tO + 32 * c, v);
-                tmem_wait_ld();
+                tmem_wait_ld32(v);
             } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = 0u;
