@@ -10,10 +10,10 @@
 //
 // Roles, joined by mbarriers only:
 // * warp 13 (loader) brings the codes of 128 tokens, K and V, into shared
-//   memory by bulk copies of 16 tokens (which lie in one block), two tiles
+//   memory by bulk copies of 16 tokens (which lie in one block), a tile
 //   ahead, and publishes each 16-token group's scales;
 // * warps 8-11 (converters) widen them to binary16 (exact) and store them as
-//   128-byte-swizzled operands, K in a ring of two, V in one stage;
+//   128-byte-swizzled operands, K and V each in a ring of two;
 // * warp 12 issues the MMAs: S_i = Q_i K^T into tensor memory, and
 //   O_i += P_i V with P_i read from tensor memory; V is used as it lies
 //   (tokens by head positions, an operand contiguous along N);
@@ -48,7 +48,7 @@ constexpr int kPrConv = 4;                      // converter warps
 constexpr int kPrConvWarp = 8;
 constexpr int kPrMmaWarp = kPrConvWarp + kPrConv;
 constexpr int kPrLoadWarp = kPrMmaWarp + 1;
-constexpr int kPrRaw = 4;                       // staged tiles of codes: K and V of two tiles
+constexpr int kPrRaw = 2;                       // staged tiles of codes: one of K, one of V
 constexpr int kPrCst = 8;                       // tiles of group constants
 constexpr int kPrThreads = 512;                 // four warpgroups; warps 14 and 15 idle
 // Registers per thread after the split by warpgroup: launched with 128 each,
@@ -60,7 +60,7 @@ constexpr uint32_t kPrFault = 8u;               // bit of the device fault word
 
 struct PrShared {
     uint64_t rawfull[kPrRaw], rawfree[kPrRaw];
-    uint64_t kfull[2], kfree[2], vfull, vfree;
+    uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
     uint64_t sfull[2], pfull[2], odone[2];
     float4 cst[kPrCst][kPrGroups];  // per group: K's scale, log2 of V's scale, 1 / V's scale
     uint32_t tmem;
@@ -74,7 +74,7 @@ struct PrShared {
 template <int D>
 struct PrSmem {
     static constexpr uint32_t kTile = kPrTokens * D * 2;  // K, V or Q tile
-    static constexpr uint32_t kBytes = 1024 + 7 * kTile + sizeof(PrShared);  // 2 Q, 2 K, 1 V, 4 tiles of codes
+    static constexpr uint32_t kBytes = 1024 + 7 * kTile + sizeof(PrShared);  // 2 Q, 2 K, 2 V, 2 tiles of codes
 };
 
 // MN-major operand (N contiguous, 128-byte swizzle): 64 columns of N 128 rows
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pr_raw) + 1023u) & ~uintptr_t(1023));
     uint8_t* sK = base;
     uint8_t* sV = base + 2 * kTile;
-    uint8_t* sRaw = base + 3 * kTile;
+    uint8_t* sRaw = base + 4 * kTile;
     uint8_t* sQ = base + 5 * kTile;
     PrShared& S = *reinterpret_cast<PrShared*>(base + 7 * kTile);
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
@@ -225,9 +225,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             mbar_init(&S.rawfull[i], 1);
             mbar_init(&S.rawfree[i], kPrConv);
         }
-        mbar_init(&S.vfull, kPrConv);
-        mbar_init(&S.vfree, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.vfull[i], kPrConv);
+            mbar_init(&S.vfree[i], 1);
             mbar_init(&S.kfull[i], kPrConv);
             mbar_init(&S.kfree[i], 1);
             mbar_init(&S.sfull[i], 1);
@@ -379,20 +379,20 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         };
         auto wait = [&](uint64_t* b, int32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(b, static_cast<uint32_t>(parity & 1))); };
         for (int32_t j = 0; j < nt; ++j) {
-            const uint32_t st = static_cast<uint32_t>(j & 1), rs = 2 * st;
-            ok = wait(&S.rawfull[rs], j >> 1) && (j < 2 || wait(&S.kfree[st], (j >> 1) - 1));
+            const uint32_t st = static_cast<uint32_t>(j & 1);
+            ok = wait(&S.rawfull[0], j) && (j < 2 || wait(&S.kfree[st], (j >> 1) - 1));
             if (!ok) break;
-            convert(sRaw + rs * (kTile / 2), sK + st * kTile, j, false);
+            convert(sRaw, sK + st * kTile, j, false);
             if (lane == 0) {
                 mbar_arrive(&S.kfull[st]);
-                mbar_arrive(&S.rawfree[rs]);
+                mbar_arrive(&S.rawfree[0]);
             }
-            ok = wait(&S.rawfull[rs + 1], j >> 1) && (j < 1 || wait(&S.vfree, j - 1));
+            ok = wait(&S.rawfull[1], j) && (j < 2 || wait(&S.vfree[st], (j >> 1) - 1));
             if (!ok) break;
-            convert(sRaw + (rs + 1) * (kTile / 2), sV, j, true);
+            convert(sRaw + kTile / 2, sV + st * kTile, j, true);
             if (lane == 0) {
-                mbar_arrive(&S.vfull);
-                mbar_arrive(&S.rawfree[rs + 1]);
+                mbar_arrive(&S.vfull[st]);
+                mbar_arrive(&S.rawfree[1]);
             }
         }
         if (!ok && lane == 0) atomicOr(&S.fault, 1u);
@@ -437,8 +437,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 const bool mine = static_cast<int32_t>(lane >> 3) == (j & 3);
                 const uint32_t n16 = __popc(__ballot_sync(0xffffffffu, mine && ids >= 0));
                 for (int32_t half = 0; half < 2; ++half) {  // K, V
-                    const uint32_t rs = static_cast<uint32_t>(2 * (j & 1) + half);
-                    if (j >= 2) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.rawfree[rs], static_cast<uint32_t>(((j >> 1) - 1) & 1)));
+                    const uint32_t rs = static_cast<uint32_t>(half);
+                    if (j >= 1) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.rawfree[rs], static_cast<uint32_t>((j - 1) & 1)));
                     if (!ok) break;
                     if (half == 0 && mine) S.cst[j % kPrCst][gl] = c;
                     __syncwarp();
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             if (!ok) {  // its own copies in flight land before the block ends
                 if (lane == 0) atomicOr(&S.fault, 1u);
                 for (int32_t i = issued > kPrRaw ? issued - kPrRaw : 0; i < issued; ++i)
-                    mbar_wait_bounded(&S.rawfull[i & 3], static_cast<uint32_t>((i >> 2) & 1));
+                    mbar_wait_bounded(&S.rawfull[i & 1], static_cast<uint32_t>((i >> 1) & 1));
             }
             meet<kMeetAll, kPrThreads>();
             return;
@@ -464,17 +464,20 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         // ---- MMA issue
         constexpr uint32_t kIdQ = (1u << 4) | ((kPrTokens >> 3) << 17) | ((128u >> 4) << 24);
         constexpr uint32_t kIdP = (1u << 4) | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
+        // descriptors of the first stages: the address field counts 16 bytes, and
+        // no operand crosses its 2^14 (shared memory ends at 2^18 bytes)
+        const uint64_t dq = mma_sdesc(smem_addr(sQ)), dk = mma_sdesc(smem_addr(sK)), dv = sdesc_mn(smem_addr(sV), kAtom);
         bool ok = true;
         int32_t issued[2] = {0, 0};  // PV products of each row tile
         int32_t scored[2] = {0, 0};  // score products of each row tile
         auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(b, parity)); };
         auto scores = [&](int32_t i, int32_t j) {  // S_i = Q_i K_j^T
-            const uint32_t a0 = smem_addr(sQ + i * kTile), b0 = smem_addr(sK + (j & 1) * kTile);
+            const uint64_t a0 = dq + static_cast<uint32_t>(i) * (kTile >> 4), b0 = dk + static_cast<uint32_t>(j & 1) * (kTile >> 4);
             if (elect_one()) {
 #pragma unroll
                 for (uint32_t s = 0; s < D / 16; ++s)
-                    mma_bf16(tmem + 128u * i, mma_sdesc(a0 + (s >> 2) * kAtom + (s & 3u) * 32u),
-                             mma_sdesc(b0 + (s >> 2) * kAtom + (s & 3u) * 32u), kIdQ, s > 0 ? 1u : 0u);
+                    mma_bf16(tmem + 128u * i, a0 + (((s >> 2) * kAtom + (s & 3u) * 32u) >> 4),
+                             b0 + (((s >> 2) * kAtom + (s & 3u) * 32u) >> 4), kIdQ, s > 0 ? 1u : 0u);
                 mma_commit(&S.sfull[i]);
                 if (i == nact - 1) mma_commit(&S.kfree[j & 1]);
             }
@@ -489,19 +492,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             }
         }
         for (int32_t j = 0; j < nt && ok; ++j) {
-            ok = wait(&S.vfull, static_cast<uint32_t>(j & 1));
+            ok = wait(&S.vfull[j & 1], static_cast<uint32_t>((j >> 1) & 1));
             for (int32_t i = 0; i < nact && ok; ++i) {
                 ok = wait(&S.pfull[i], static_cast<uint32_t>(j & 1));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t b0 = smem_addr(sV);
+                const uint64_t b0 = dv + static_cast<uint32_t>(j & 1) * (kTile >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (uint32_t s = 0; s < kPrTokens / 16; ++s)
-                        mma_ts(tmem + kO + D * i, tmem + 128u * i + 8u * s, sdesc_mn(b0 + s * 2048u, kAtom), kIdP,
+                        mma_ts(tmem + kO + D * i, tmem + 128u * i + 8u * s, b0 + s * (2048u >> 4), kIdP,
                                j > 0 || s > 0 ? 1u : 0u);
                     mma_commit(&S.odone[i]);
-                    if (i == nact - 1) mma_commit(&S.vfree);
+                    if (i == nact - 1) mma_commit(&S.vfree[j & 1]);
                 }
                 __syncwarp();
                 ++issued[i];
