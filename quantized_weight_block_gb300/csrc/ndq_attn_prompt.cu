@@ -107,6 +107,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* v) {
           "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(a));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(a));
+}
 __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -129,6 +136,14 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t* v) {
                  : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t* v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
 
 // Barriers by number: every thread of the roles that meet there, and no other.
 template <int ID, int THREADS>
@@ -548,41 +563,41 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         // The weights relative to ms, their sum and the largest exponent.
         auto weigh = [&](auto mask, const float4* cst, int32_t tb, float& ts, float& top) {
             constexpr bool kMasked = decltype(mask)::value;
-            uint32_t v[2][32];
+            uint32_t v[2][16];
             ts = 0.0f;
-            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            tmem_ld32(tS, v[0]);
+            float tops[2] = {-INFINITY, -INFINITY};
+            tmem_ld16(tS, v[0]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                tmem_wait_ld32(v[c & 1]);
-                if (c < 3) tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
-                const uint32_t* x = v[c & 1];
+            for (int q = 0; q < kPrGroups; ++q) {  // a group of 16 tokens; the next one's scores load meanwhile
+                tmem_wait_ld16(v[q & 1]);
+                if (q + 1 < kPrGroups) tmem_ld16(tS + 16 * (q + 1), v[(q + 1) & 1]);
+                const uint32_t* x = v[q & 1];
+                const float4 k = cst[q];
+                const uint64_t f2 = pair(frow * k.x, frow * k.x), c2 = pair(k.y - ms, k.y - ms);
+                const int32_t pos = tb + 16 * q;
+                float y[16];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float4 k = cst[2 * c + q];
-                    const uint64_t f2 = pair(frow * k.x, frow * k.x), c2 = pair(k.y - ms, k.y - ms);
-                    uint64_t s2 = 0;
-                    const int32_t pos = tb + 32 * c + 16 * q;
+                for (int e = 0; e < 16; e += 2)
+                    unpair(pair_fma(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f2, c2), y[e], y[e + 1]);
+                if constexpr (kMasked) {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float a, b;
-                        unpair(pair_fma(pair(__uint_as_float(x[16 * q + e]), __uint_as_float(x[16 * q + e + 1])), f2, c2), a, b);
-                        if constexpr (kMasked) {
-                            if (pos + e < see_lo || pos + e >= see_hi) a = -INFINITY;
-                            if (pos + e + 1 < see_lo || pos + e + 1 >= see_hi) b = -INFINITY;
-                        }
-                        tops[(e / 2) & 3] = max3(tops[(e / 2) & 3], a, b);
-                        a = exp2_fast(a);
-                        b = exp2_fast(b);
-                        s2 = pair_add(s2, pair(a, b));
-                        w[16 * c + 8 * q + e / 2] = pack_half2(a, b);
-                    }
-                    float a, b;
-                    unpair(s2, a, b);
-                    ts = __fmaf_rn(a + b, k.z, ts);
+                    for (int e = 0; e < 16; ++e)
+                        if (pos + e < see_lo || pos + e >= see_hi) y[e] = -INFINITY;
                 }
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) tops[(e >> 1) & 1] = max3(tops[(e >> 1) & 1], y[e], y[e + 1]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] = exp2_fast(y[e]);
+                uint64_t s2[2] = {pair(y[0], y[1]), pair(y[2], y[3])};
+#pragma unroll
+                for (int e = 4; e < 16; e += 2) s2[(e >> 1) & 1] = pair_add(s2[(e >> 1) & 1], pair(y[e], y[e + 1]));
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) w[8 * q + e / 2] = pack_half2(y[e], y[e + 1]);
+                float a, b;
+                unpair(pair_add(s2[0], s2[1]), a, b);
+                ts = __fmaf_rn(a + b, k.z, ts);
             }
-            top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
+            top = fmaxf(tops[0], tops[1]);
         };
         for (int32_t j = 0; j < nt; ++j) {
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.sfull[wg], static_cast<uint32_t>(j & 1)));

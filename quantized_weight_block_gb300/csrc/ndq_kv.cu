@@ -149,9 +149,16 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const PlanParams p) {
 // ---------------------------------------------------------------------------
 // Append: quantise new rows into the cache, one scale per block and head.
 //
-// A run is the adjacent tokens of the call that fall in one block.  One warp
-// takes a run for one head and one of K and V: the run's largest magnitude
-// gives the scale, then the rows are divided by it, rounded and stored.
+// A run is the adjacent tokens of the call that fall in one block.  Its
+// largest magnitude, for one head and one of K and V, gives the scale; then
+// its rows are divided by it, rounded and stored.  Bound by reading the rows
+// and writing the codes once; a run's rows stay in registers between the two
+// sweeps (up to 16 passes of them, more are read again from the cache).
+//
+// The quotient x / s is not formed: with y a reciprocal of s off by a few
+// units, x y (1 - 2^-21) and x y (1 + 2^-21) enclose it, and where both round
+// to the same code, that is the code.  Only the others (one in thousands)
+// take the division.
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
 constexpr int kAppendHeld = 16;  // passes of rows kept in registers between the two sweeps
@@ -189,6 +196,32 @@ __device__ __forceinline__ uint32_t encode4(float4 v, float s) {
     }
 }
 
+// The codes of four values as four numbers already divided: no special cases.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t round4(float a, float b, float c, float d) {
+    if constexpr (E4M3) {
+        uint32_t r;
+        asm("{\n.reg .b16 l, h;\ncvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\ncvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\nmov.b32 %0, {l, h};\n}"
+            : "=r"(r)
+            : "f"(a), "f"(b), "f"(c), "f"(d));
+        return r;
+    } else {
+        // to nearest even by adding 1.5 * 2^23: the low byte is the code (|quotient| < 128)
+        constexpr float kBig = 12582912.0f;
+        const uint32_t ab = __byte_perm(__float_as_uint(__fadd_rn(a, kBig)), __float_as_uint(__fadd_rn(b, kBig)), 0x0040);
+        const uint32_t cd = __byte_perm(__float_as_uint(__fadd_rn(c, kBig)), __float_as_uint(__fadd_rn(d, kBig)), 0x0040);
+        return __byte_perm(ab, cd, 0x5410);
+    }
+}
+
+// encode4 for finite values of at most Q s: lo and hi enclose 1 / s.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t encode4_fast(float4 v, float s, float lo, float hi) {
+    const uint32_t a = round4<E4M3>(__fmul_rn(v.x, lo), __fmul_rn(v.y, lo), __fmul_rn(v.z, lo), __fmul_rn(v.w, lo));
+    const uint32_t b = round4<E4M3>(__fmul_rn(v.x, hi), __fmul_rn(v.y, hi), __fmul_rn(v.z, hi), __fmul_rn(v.w, hi));
+    return a == b ? a : encode4<E4M3>(v, s);
+}
+
 template <bool E4M3>
 __device__ __forceinline__ float4 decode4(uint32_t w) {
     if constexpr (E4M3) {
@@ -208,18 +241,20 @@ __device__ __forceinline__ float finite_abs(float x) {
     return a <= FLT_MAX ? a : 0.0f;
 }
 
-// win: tokens a warp searches for runs that start among them.
-template <int D, bool E4M3, bool BF16>
+// TEAM warps work on a run together.  win (at most 32): the tokens a team
+// searches for runs that start among them.
+template <int D, bool E4M3, bool BF16, int TEAM>
 __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendParams p, int win) {
-    constexpr int LPR = D / 4;       // lanes per row, four values each
-    constexpr int RPP = 32 / LPR;    // rows per pass of the warp
+    constexpr int LPR = D / 4;              // lanes per row, four values each
+    constexpr int RPP = TEAM * 32 / LPR;    // rows per pass of the team
     constexpr float kQmax = E4M3 ? 448.0f : 127.0f;
-    const uint32_t lane = threadIdx.x & 31u;
+    __shared__ float s_max[kAppendWarps];
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const int units = 2 * p.c.heads;
-    const int64_t wid = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
-    const int64_t w0 = wid / units * win;
+    const int64_t team = TEAM == 1 ? static_cast<int64_t>(blockIdx.x) * kAppendWarps + warp : blockIdx.x;
+    const int64_t w0 = team / units * win;
     if (w0 >= p.n_tokens) return;
-    const int u = static_cast<int>(wid % units), h = u >> 1;
+    const int u = static_cast<int>(team % units), h = u >> 1;
     const bool is_v = u & 1;
     const int bl = p.c.bs_log2, bs = 1 << bl;
     const int64_t limit = p.c.num_blocks << bl;
@@ -228,7 +263,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
     uint8_t* codes = is_v ? p.c.v : p.c.k;
     float* scales = is_v ? p.c.vs : p.c.ks;
     const int64_t wend = w0 + win < p.n_tokens ? w0 + win : p.n_tokens;
-    // which tokens of the window start a run (lane i: token w0 + i; win <= 32)
+    // which tokens of the window start a run (lane i: token w0 + i)
     bool lead = false;
     int64_t slot = -1;
     if (w0 + lane < wend) {
@@ -237,7 +272,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
         lead = slot >= 0 && slot < limit && (before < 0 || (before >> bl) != (slot >> bl));
     }
     uint32_t leads = __ballot_sync(0xffffffffu, lead);
-    const uint32_t row = lane / LPR, col = (lane % LPR) * 4;
+    const uint32_t idx = TEAM == 1 ? lane : threadIdx.x;
+    const int row = static_cast<int>(idx / LPR), col = static_cast<int>(idx % LPR) * 4;
     while (leads) {
         const int li = __ffs(leads) - 1;
         leads &= leads - 1;
@@ -260,6 +296,18 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
         const float old = n_old > 0 ? scales[unit] : 0.0f;
         uint2 held[kAppendHeld];
         float amax = 0.0f;
+        bool odd = false;  // an infinity or NaN among the values
+        auto look = [&](const uint2& w) {
+            const float2 a = widen<BF16>(w.x), b = widen<BF16>(w.y);
+            const float m = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y)));
+            // (the sum is NaN or infinite if one of them is)
+            if (!(fabsf(a.x) + fabsf(a.y) + (fabsf(b.x) + fabsf(b.y)) <= FLT_MAX)) {
+                odd = true;
+                amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(a.x), finite_abs(a.y)), fmaxf(finite_abs(b.x), finite_abs(b.y))));
+            } else {
+                amax = fmaxf(amax, m);
+            }
+        };
 #pragma unroll
         for (int i = 0; i < kAppendHeld; ++i) {
             const int r = i * RPP + row;
@@ -267,21 +315,29 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
             if (r < cnt) held[i] = *reinterpret_cast<const uint2*>(in + (t0 + r) * stride + col);
         }
 #pragma unroll
-        for (int i = 0; i < kAppendHeld; ++i) {
-            const float2 a = widen<BF16>(held[i].x), b = widen<BF16>(held[i].y);
-            amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(a.x), finite_abs(a.y)), fmaxf(finite_abs(b.x), finite_abs(b.y))));
-        }
+        for (int i = 0; i < kAppendHeld; ++i)
+            if (i * RPP < cnt) look(held[i]);
 #pragma unroll 4
-        for (int r = kAppendHeld * RPP + row; r < cnt; r += RPP) {
-            const uint2 w = *reinterpret_cast<const uint2*>(in + (t0 + r) * stride + col);
-            const float2 a = widen<BF16>(w.x), b = widen<BF16>(w.y);
-            amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(a.x), finite_abs(a.y)), fmaxf(finite_abs(b.x), finite_abs(b.y))));
-        }
+        for (int r = kAppendHeld * RPP + row; r < cnt; r += RPP) look(*reinterpret_cast<const uint2*>(in + (t0 + r) * stride + col));
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+        if constexpr (TEAM > 1) {  // (also: every thread has read the old scale before it is written)
+            __syncthreads();
+            if (lane == 0) s_max[warp] = amax;
+            odd = __syncthreads_or(odd);
+#pragma unroll
+            for (int w = 0; w < TEAM; ++w) amax = fmaxf(amax, s_max[w]);
+        } else {
+            odd = __any_sync(0xffffffffu, odd);
+        }
         float fresh = 0.0f;
         if (amax > 0.0f) fresh = fminf(fmaxf(__fdiv_rn(amax, kQmax), 0x1p-100f), 0x1p100f);
         const float s = fmaxf(old, fresh);
+        // (a scale cut off at 2^100 leaves values beyond Q s: to be saturated)
+        const bool fast = !odd && s > 0.0f && s < 0x1p100f;
+        const float y = fast ? __fdividef(1.0f, s) : 0.0f;
+        const float lo = __fmul_rn(y, 1.0f - 0x1p-21f), hi = __fmul_rn(y, 1.0f + 0x1p-21f);
+        auto encode = [&](const float4& v) { return fast ? encode4_fast<E4M3>(v, s, lo, hi) : encode4<E4M3>(v, s); };
         uint8_t* out = codes + (unit << bl) * D + col;
         if (old > 0.0f && s > old) {  // the earlier tokens' codes under the grown scale
 #pragma unroll 4
@@ -295,39 +351,40 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
                 *w = encode4<E4M3>(v, s);
             }
         }
+        auto put = [&](const uint2& w, int r) {
+            const float2 a = widen<BF16>(w.x), b = widen<BF16>(w.y);
+            const int o = static_cast<int>(p.slots[t0 + r] & (bs - 1));
+            *reinterpret_cast<uint32_t*>(out + o * D) = encode(make_float4(a.x, a.y, b.x, b.y));
+        };
 #pragma unroll
         for (int i = 0; i < kAppendHeld; ++i) {
             const int r = i * RPP + row;
-            if (r < cnt) {
-                const float2 a = widen<BF16>(held[i].x), b = widen<BF16>(held[i].y);
-                const int o = static_cast<int>(p.slots[t0 + r] & (bs - 1));
-                *reinterpret_cast<uint32_t*>(out + o * D) = encode4<E4M3>(make_float4(a.x, a.y, b.x, b.y), s);
-            }
+            if (r < cnt) put(held[i], r);
         }
 #pragma unroll 4
-        for (int r = kAppendHeld * RPP + row; r < cnt; r += RPP) {
-            const uint2 w = *reinterpret_cast<const uint2*>(in + (t0 + r) * stride + col);
-            const float2 a = widen<BF16>(w.x), b = widen<BF16>(w.y);
-            const int o = static_cast<int>(p.slots[t0 + r] & (bs - 1));
-            *reinterpret_cast<uint32_t*>(out + o * D) = encode4<E4M3>(make_float4(a.x, a.y, b.x, b.y), s);
-        }
+        for (int r = kAppendHeld * RPP + row; r < cnt; r += RPP) put(*reinterpret_cast<const uint2*>(in + (t0 + r) * stride + col), r);
         __syncwarp();  // every lane has read the old scale
-        if (lane == 0) scales[unit] = s;
+        if (idx == 0) scales[unit] = s;
     }
 }
 
 template <int D, bool E4M3>
 int append_typed(const AppendParams& p, bool bf16, void* stream) {
     const int64_t units = 2 * static_cast<int64_t>(p.c.heads);
-    // One token per warp while every warp can be resident at once (a step's
-    // latency); 16 per warp for prompts, where only one token in a block
-    // starts a run and the others would cost an idle warp each.
-    const int win = p.n_tokens * units <= 152 * 48 ? 1 : 16;
-    const int64_t warps = (p.n_tokens + win - 1) / win * units;
-    const unsigned grid = static_cast<unsigned>((warps + kAppendWarps - 1) / kAppendWarps);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (bf16) k_kv_append<D, E4M3, true><<<grid, kAppendWarps * 32, 0, st>>>(p, win);
-    else k_kv_append<D, E4M3, false><<<grid, kAppendWarps * 32, 0, st>>>(p, win);
+    // A warp per token, head and K or V while all of them are resident at once
+    // (a step: latency).  More tokens are prompts, whose runs are blocks: a
+    // CTA per 32 tokens works on the runs that start there.
+    if (p.n_tokens * units <= 152 * 48) {
+        const unsigned grid = static_cast<unsigned>((p.n_tokens * units + kAppendWarps - 1) / kAppendWarps);
+        if (bf16) k_kv_append<D, E4M3, true, 1><<<grid, kAppendWarps * 32, 0, st>>>(p, 1);
+        else k_kv_append<D, E4M3, false, 1><<<grid, kAppendWarps * 32, 0, st>>>(p, 1);
+    } else {
+        const int win = p.c.bs_log2 > 4 ? 32 : 16;  // (blocks of 16 would give two or three runs to a window of 32)
+        const unsigned grid = static_cast<unsigned>((p.n_tokens + win - 1) / win * units);
+        if (bf16) k_kv_append<D, E4M3, true, kAppendWarps><<<grid, kAppendWarps * 32, 0, st>>>(p, win);
+        else k_kv_append<D, E4M3, false, kAppendWarps><<<grid, kAppendWarps * 32, 0, st>>>(p, win);
+    }
     return static_cast<int>(cudaGetLastError());
 }
 

@@ -12,8 +12,8 @@
 //   of one pass over the adapters' weights.  A CTA takes one row and
 //   kShrinkJ ranks over all of K; a thread of the expansion one or more
 //   outputs.
-// * many rows (k_lora_shrink_tile, k_lora_expand_tile): tiles of 32 rows on
-//   the tensor cores (mma.sync m16n8k16: the operator is bound by reading x
+// * many rows (k_lora_shrink_tile, k_lora_expand_tile): tiles of 64 and 32
+//   rows on the tensor cores (mma.sync m16n8k16: the operator is bound by reading x
 //   and base and writing y, and its products need a fraction of even that
 //   rate).  A tile goes through the adapters of its rows one by one, with the
 //   other adapters' rows as zeros, so any row order is right and adjacent
@@ -21,9 +21,10 @@
 //   the shrink's products are exact; t enters the expansion as a sum of
 //   bfloat16 parts: three for a binary32 result (2^-24 of t is left), two
 //   for a bfloat16 one (2^-16, under the result's own rounding of 2^-9).
-//   Operands are loaded from global memory in the order of the fragments:
-//   the k-index is permuted so that a lane's 16-byte load is its part of two
-//   k-steps, the output columns so that a lane holds 16 adjacent ones.
+//   The expansion's weights are loaded from global memory in the order of the
+//   fragments: the k-index is permuted so that a lane's 16-byte load is its
+//   part of two k-steps, the output columns so that a lane holds 8 adjacent
+//   ones.
 //
 // Any other alignment (K or max_rank not a multiple of 8, buffers off 16
 // bytes) takes the few-row kernels with scalar loads.
@@ -197,89 +198,151 @@ __device__ __forceinline__ int32_t next_adapter(int32_t mine, int32_t prev) {
     return __reduce_min_sync(0xffffffffu, c);
 }
 
-// Sums t over a K split: CTA (tile, split), NT = max_rank / 8 rounded up.
-// Warps take every eighth 32-k step; their sums are joined in warp order.
+// Sums t over a K split: CTA (tile of 64 rows, split), NT = max_rank / 8 rounded
+// up.  x and the adapter's rows of A come through a ring of asynchronous
+// copies in shared memory, 64 of K a stage, 16-byte pieces exchanged by row
+// so that ldmatrix reads without conflicts.  Warp w takes rows 16 (w % 4)
+// and half w / 4 of each stage; the halves are added at the end.
+constexpr int kShrinkRows = 64;
+constexpr int kShrinkK = 64;
 template <int NT>
-__global__ void __launch_bounds__(kLoraThreads, NT <= 8 ? 2 : 1) k_lora_shrink_tile(const LoraParams p, int splits) {
-    extern __shared__ __align__(16) float s_sum[];  // [warps][32][NT * 8 + 4]
-    constexpr int LD = NT * 8 + 4;
+struct ShrinkSmem {
+    static constexpr int kStages = NT <= 8 ? 6 : 4;
+    static constexpr int kStage = (kShrinkRows + NT * 8) * kShrinkK * 2;
+    static constexpr int kBytes = kStages * kStage;  // (at least the 64 x NT * 8 sums at the end)
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t* r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kLoraThreads, 2) k_lora_shrink_tile(const LoraParams p, int splits) {
+    using Sm = ShrinkSmem<NT>;
+    constexpr int ST = Sm::kStages;
+    extern __shared__ __align__(128) uint8_t s_ring[];
+    __shared__ int32_t s_a[kShrinkRows];
     pdl_launch();
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kTileRows;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kShrinkRows;
     const int32_t split = static_cast<int32_t>(blockIdx.y);
-    int32_t mine = -1;
-    if (m0 + lane < p.M) {
-        mine = p.index[m0 + lane];
-        if (mine < 0 || mine >= p.nA) mine = -1;
+    if (tid < kShrinkRows) {
+        int32_t a = -1;
+        if (m0 + tid < p.M) {
+            a = p.index[m0 + tid];
+            if (a >= p.nA) a = -1;
+        }
+        s_a[tid] = a;
     }
-    const int64_t steps = (p.K + 31) / 32;
-    const int64_t st0 = steps * split / splits, st1 = steps * (split + 1) / splits;
-    for (int32_t a = next_adapter(mine, -1); a != INT32_MAX; a = next_adapter(mine, a)) {
+    __syncthreads();
+    const int32_t mine0 = s_a[lane], mine1 = s_a[lane + 32];
+    auto next = [&](int32_t prev) {  // the tile's adapters in ascending order
+        const int32_t c0 = mine0 > prev ? mine0 : INT32_MAX, c1 = mine1 > prev ? mine1 : INT32_MAX;
+        return __reduce_min_sync(0xffffffffu, c0 < c1 ? c0 : c1);
+    };
+    const int32_t steps = static_cast<int32_t>((p.K + kShrinkK - 1) / kShrinkK);
+    const int32_t st0 = static_cast<int32_t>(static_cast<int64_t>(steps) * split / splits);
+    const int32_t n = static_cast<int32_t>(static_cast<int64_t>(steps) * (split + 1) / splits) - st0;
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(s_ring));
+    const uint32_t piece = tid & 7u, crow = tid >> 3;  // this thread copies piece `piece` of rows crow, crow + 32, ...
+    const uint32_t mrow = 16u * (warp & 3u), khalf = warp >> 2;
+    for (int32_t a = next(-1); a != INT32_MAX; a = next(a)) {
         const int32_t r = rank_of(p, a);
         if (r == 0) continue;
-        bool live[4];  // rows g, g + 8, g + 16, g + 24 of this adapter
+        const bool live0 = s_a[crow] == a, live1 = s_a[crow + 32] == a;
+        const uint16_t* x = p.x + (m0 + crow) * p.K + piece * 8;
+        const uint16_t* w = p.a + (static_cast<int64_t>(a) * p.rmax + crow) * p.K + piece * 8;
+        auto issue = [&](int32_t i) {
+            if (i < n) {
+                const int64_t k = static_cast<int64_t>(st0 + i) * kShrinkK;
+                const bool in = k + piece * 8 < p.K;  // (K is a multiple of 8)
+                const uint32_t d = ring + static_cast<uint32_t>(i % ST) * Sm::kStage + crow * 128u + ((piece ^ (crow & 7u)) << 4);
+                cp_async16(d, live0 && in ? x + k : p.x, live0 && in ? 16u : 0u);
+                cp_async16(d + 32u * 128u, live1 && in ? x + 32 * p.K + k : p.x, live1 && in ? 16u : 0u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) live[i] = __shfl_sync(0xffffffffu, mine, static_cast<int>(g) + 8 * i) == a;
-        float acc[2][NT][4] = {};
-        const uint16_t* x = p.x + (m0 + g) * p.K + t * 8;
-        const uint16_t* w = p.a + (static_cast<int64_t>(a) * p.rmax + g) * p.K + t * 8;
-#pragma unroll 1
-        for (int64_t st = st0 + warp; st < st1; st += kLoraWarps) {
-            const int64_t k = st * 32;
-            const bool in = k + t * 8 < p.K;
-            uint4 xv[4], wv[NT];
+                for (int q = 0; q < (NT + 3) / 4; ++q) {
+                    const int32_t j = static_cast<int32_t>(crow) + 32 * q;
+                    if (j < NT * 8) {
+                        const bool ok = in && j < r;
+                        cp_async16(d + (kShrinkRows + 32u * q) * 128u, ok ? w + static_cast<int64_t>(32 * q) * p.K + k : p.a, ok ? 16u : 0u);
+                    }
+                }
+            }
+            cp_commit();
+        };
+        float acc[NT][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                xv[i] = in && live[i] ? __ldg(reinterpret_cast<const uint4*>(x + 8 * i * p.K + k)) : make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+        __syncthreads();  // the ring and the previous adapter's sums are free
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                wv[n] = in && 8 * n + static_cast<int>(g) < r ? __ldg(reinterpret_cast<const uint4*>(w + 8 * n * p.K + k))
-                                                             : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < ST - 1; ++i) issue(i);
+        for (int32_t i = 0; i < n; ++i) {
+            cp_wait<ST - 2>();
+            __syncthreads();  // stage i is there, and every warp is done with stage i - 1
+            issue(i + ST - 1);
+            const uint32_t sx = ring + static_cast<uint32_t>(i % ST) * Sm::kStage, sw = sx + kShrinkRows * 128u;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t a0[4] = {xv[0].x, xv[1].x, xv[0].y, xv[1].y}, a1[4] = {xv[0].z, xv[1].z, xv[0].w, xv[1].w};
-                const uint32_t c0[4] = {xv[2].x, xv[3].x, xv[2].y, xv[3].y}, c1[4] = {xv[2].z, xv[3].z, xv[2].w, xv[3].w};
-                const uint32_t* f = h == 0 ? (a0) : (c0);
-                const uint32_t* e = h == 0 ? (a1) : (c1);
+            for (uint32_t ks = 0; ks < 2; ++ks) {
+                const uint32_t u0 = 4u * khalf + 2u * ks;  // the k-step's first piece
+                uint32_t af[4];
+                const uint32_t ar = mrow + (lane & 15u);
+                ldmatrix4(af, sx + ar * 128u + (((u0 + (lane >> 4)) ^ (ar & 7u)) << 4));
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (8 * n >= r) continue;
-                    mma_bf16_16816(acc[h][n], f, wv[n].x, wv[n].y);
-                    mma_bf16_16816(acc[h][n], e, wv[n].z, wv[n].w);
+                for (int j = 0; j < NT; j += 2) {
+                    uint32_t bfr[4];
+                    // matrices: ranks 8 j.., pieces u0, u0 + 1; ranks 8 (j + 1).., the same
+                    const uint32_t br = 8u * j + ((lane >> 4) << 3) + (lane & 7u);
+                    const uint32_t row = NT == 1 ? (lane & 7u) : br;
+                    ldmatrix4(bfr, sw + row * 128u + (((u0 + ((lane >> 3) & 1u)) ^ (row & 7u)) << 4));
+                    mma_bf16_16816(acc[j], af, bfr[0], bfr[1]);
+                    if (NT > 1) mma_bf16_16816(acc[j + (NT > 1 ? 1 : 0)], af, bfr[2], bfr[3]);
                 }
             }
         }
-        __syncthreads();  // the previous adapter's sums are read
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float* d = s_sum + (warp * kTileRows + 16 * h + g) * LD + 8 * n + 2 * t;
-                d[0] = acc[h][n][0];
-                d[1] = acc[h][n][1];
-                d[8 * LD] = acc[h][n][2];
-                d[8 * LD + 1] = acc[h][n][3];
-            }
+        cp_wait<0>();
         __syncthreads();
-        const float sc = p.scales[a];
-        for (int32_t i = static_cast<int32_t>(tid); i < kTileRows * NT * 8; i += kLoraThreads) {
-            const int32_t row = i / (NT * 8), j = i % (NT * 8);
-            if (j >= r || m0 + row >= p.M) continue;
-            const int32_t ra = p.index[m0 + row];
-            if (ra != a) continue;
-            float v = 0.0f;
+        float* sums = reinterpret_cast<float*>(s_ring);  // [64][NT * 8]: the second half of K
+        if (khalf == 1) {
 #pragma unroll
-            for (int q = 0; q < kLoraWarps; ++q) v = __fadd_rn(v, s_sum[(q * kTileRows + row) * LD + j]);
-            p.t[(static_cast<int64_t>(split) * p.M + m0 + row) * p.rmax + j] = __fmul_rn(v, sc);
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sums[(mrow + g + 8 * (e >> 1)) * (NT * 8) + 8 * j + 2 * t + (e & 1)] = acc[j][e];
+        }
+        __syncthreads();
+        if (khalf == 0) {
+            const float sc = p.scales[a];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t row = mrow + g + 8 * (e >> 1);
+                    const int32_t c = 8 * j + 2 * static_cast<int32_t>(t) + (e & 1);
+                    if (c < r && s_a[row] == a)
+                        p.t[(static_cast<int64_t>(split) * p.M + m0 + row) * p.rmax + c] =
+                            __fmul_rn(__fadd_rn(acc[j][e], sums[row * (NT * 8) + c]), sc);
+                }
         }
     }
 }
 
-// y of 32 rows by `chunks` x 512 columns: each warp 64 adjacent columns at a
-// time.  t's parts are laid out as A fragments in shared memory.
+// y of 32 rows by `chunks` x 256 columns: each warp 32 adjacent columns at a
+// time.  t's parts are laid out as A fragments in shared memory; base and the
+// first weights of a chunk are fetched together.
 template <bool F32, bool VEC>
-__global__ void __launch_bounds__(kLoraThreads, 2) k_lora_expand_tile(const LoraParams p, int splits, int chunks, int groups) {
+__global__ void __launch_bounds__(kLoraThreads, F32 ? 2 : 3) k_lora_expand_tile(const LoraParams p, int splits, int chunks, int groups) {
     constexpr int PARTS = F32 ? 3 : 2;
+    constexpr int BW = F32 ? 8 : 4;  // words of base per lane and row
     extern __shared__ __align__(16) uint8_t s_raw[];
     uint4* s_t = reinterpret_cast<uint4*>(s_raw);  // [k-step pair][part][half of the rows][k-step][lane]
     __shared__ int32_t s_a[kTileRows];
@@ -291,7 +354,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_expand_tile(const Lora
         if (mine < 0 || mine >= p.nA) mine = -1;
     }
     if (warp == 0) s_a[lane] = mine;
-    const int64_t cbase = (static_cast<int64_t>(blockIdx.x % groups) * chunks * kLoraWarps + warp) * 64;
+    const int64_t cbase = (static_cast<int64_t>(blockIdx.x % groups) * chunks * kLoraWarps + warp) * 32;
     const int32_t first = next_adapter(mine, -1);
     const bool one = first == INT32_MAX || next_adapter(mine, first) == INT32_MAX;  // a single adapter: lay t out once
     pdl_wait();
@@ -341,9 +404,41 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_expand_tile(const Lora
         __syncthreads();
     }
     for (int c = 0; c < chunks; ++c) {
-        const int64_t n0 = cbase + static_cast<int64_t>(c) * kLoraWarps * 64;
-        // this lane's outputs: rows g + 8 i, columns n0 + 16 t + 0 .. 15 (n-tile e: columns 2 e, 2 e + 1)
-        float acc[2][8][4] = {};
+        const int64_t n0 = cbase + static_cast<int64_t>(c) * kLoraWarps * 32;
+        // this lane's outputs: rows g + 8 i, columns n0 + 8 t + 0 .. 7 (n-tile e: columns 2 e, 2 e + 1)
+        const int64_t nl = n0 + 8 * t;
+        uint32_t bw[4][BW];  // base
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = m0 + g + 8 * i;
+#pragma unroll
+            for (int q = 0; q < BW; ++q) bw[i][q] = 0u;
+            if (m < p.M) {
+                const int64_t o = m * p.N + nl;
+                if constexpr (F32) {
+                    const uint32_t* b = static_cast<const uint32_t*>(p.base) + o;
+                    if constexpr (VEC) {
+#pragma unroll
+                        for (int q = 0; q < 8; q += 4)
+                            if (nl + q < p.N) *reinterpret_cast<uint4*>(&bw[i][q]) = *reinterpret_cast<const uint4*>(b + q);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            if (nl + q < p.N) bw[i][q] = b[q];
+                    }
+                } else {
+                    const uint16_t* b = static_cast<const uint16_t*>(p.base) + o;
+                    if constexpr (VEC) {
+                        if (nl < p.N) *reinterpret_cast<uint4*>(&bw[i][0]) = *reinterpret_cast<const uint4*>(b);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            if (nl + q < p.N) bw[i][q / 2] |= static_cast<uint32_t>(b[q]) << (16 * (q & 1));
+                    }
+                }
+            }
+        }
+        float acc[2][4][4] = {};
         for (int32_t a = first; a != INT32_MAX; a = next_adapter(mine, a)) {
             const int32_t r = rank_of(p, a);
             if (!one) {
@@ -352,11 +447,11 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_expand_tile(const Lora
                 __syncthreads();
             }
             for (int32_t pr = 0; 32 * pr < r; ++pr) {
-                uint4 wv[8];
-                // column of B's fragment n-tile e, index g: n0 + 16 (g / 2) + 2 e + g % 2
+                uint4 wv[4];
+                // column of B's fragment n-tile e, index g: n0 + 8 (g / 2) + 2 e + g % 2
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int64_t n = n0 + 16 * (g >> 1) + 2 * e + (g & 1u);
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t n = n0 + 8 * (g >> 1) + 2 * e + (g & 1u);
                     const int32_t j = 32 * pr + 8 * static_cast<int32_t>(t);
                     wv[e] = make_uint4(0u, 0u, 0u, 0u);
                     if (n < p.N && j < r) {
@@ -378,62 +473,47 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_expand_tile(const Lora
                         const uint4 f1 = s_t[(((pr * PARTS + part) * 2 + half) * 2 + 1) * 32 + lane];
                         const uint32_t a0[4] = {f0.x, f0.y, f0.z, f0.w}, a1[4] = {f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            mma_bf16_16816(acc[half][e], a0, wv[e].x, wv[e].y);
-                            mma_bf16_16816(acc[half][e], a1, wv[e].z, wv[e].w);
-                        }
+                        for (int e = 0; e < 4; ++e) mma_bf16_16816(acc[half][e], a0, wv[e].x, wv[e].y);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mma_bf16_16816(acc[half][e], a1, wv[e].z, wv[e].w);
                     }
             }
         }
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = m0 + g + 8 * i;
+            if (m >= p.M) continue;
+            const int64_t o = m * p.N + nl;
+            const int half = i >> 1, c0 = 2 * (i & 1);
+            if constexpr (F32) {
+                float* y = static_cast<float*>(p.y) + o;
+                float v[8];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int64_t m = m0 + 16 * half + g + 8 * i, n = n0 + 16 * t;
-                if (m >= p.M) continue;
-                const int64_t o = m * p.N + n;
-                if constexpr (F32) {
-                    const float* b = static_cast<const float*>(p.base) + o;
-                    float* y = static_cast<float*>(p.y) + o;
-                    if constexpr (VEC) {
+                for (int q = 0; q < 8; ++q) v[q] = __fadd_rn(__uint_as_float(bw[i][q]), acc[half][q >> 1][c0 + (q & 1)]);
+                if constexpr (VEC) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (n + 4 * e < p.N) {
-                                float4 v = *reinterpret_cast<const float4*>(b + 4 * e);
-                                v.x = __fadd_rn(v.x, acc[half][2 * e][2 * i]);
-                                v.y = __fadd_rn(v.y, acc[half][2 * e][2 * i + 1]);
-                                v.z = __fadd_rn(v.z, acc[half][2 * e + 1][2 * i]);
-                                v.w = __fadd_rn(v.w, acc[half][2 * e + 1][2 * i + 1]);
-                                *reinterpret_cast<float4*>(y + 4 * e) = v;
-                            }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (n + e < p.N) y[e] = __fadd_rn(b[e], acc[half][e >> 1][2 * i + (e & 1)]);
-                    }
+                    for (int q = 0; q < 8; q += 4)
+                        if (nl + q < p.N) *reinterpret_cast<float4*>(y + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
                 } else {
-                    const uint16_t* b = static_cast<const uint16_t*>(p.base) + o;
-                    uint16_t* y = static_cast<uint16_t*>(p.y) + o;
-                    if constexpr (VEC) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (n + 8 * e < p.N) {
-                                uint4 v = *reinterpret_cast<const uint4*>(b + 8 * e);
-                                uint32_t* u = &v.x;
+                    for (int q = 0; q < 8; ++q)
+                        if (nl + q < p.N) y[q] = v[q];
+                }
+            } else {
+                uint16_t* y = static_cast<uint16_t*>(p.y) + o;
+                uint32_t v[4];
 #pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    u[q] = pack_bf16(__fadd_rn(bf_lo(u[q]), acc[half][4 * e + q][2 * i]),
-                                                     __fadd_rn(bf_hi(u[q]), acc[half][4 * e + q][2 * i + 1]));
-                                *reinterpret_cast<uint4*>(y + 8 * e) = v;
-                            }
-                    } else {
+                for (int q = 0; q < 4; ++q)
+                    v[q] = pack_bf16(__fadd_rn(bf_lo(bw[i][q]), acc[half][q][c0]), __fadd_rn(bf_hi(bw[i][q]), acc[half][q][c0 + 1]));
+                if constexpr (VEC) {
+                    if (nl < p.N) *reinterpret_cast<uint4*>(y) = make_uint4(v[0], v[1], v[2], v[3]);
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (n + e < p.N)
-                                y[e] = static_cast<uint16_t>(pack_bf16(__fadd_rn(bf(b[e]), acc[half][e >> 1][2 * i + (e & 1)]), 0.0f));
-                    }
+                    for (int q = 0; q < 8; ++q)
+                        if (nl + q < p.N) y[q] = static_cast<uint16_t>(v[q / 2] >> (16 * (q & 1)));
                 }
             }
+        }
     }
 }
 
@@ -445,7 +525,7 @@ constexpr int64_t kTileMinRows = 96;
 
 // K splits: enough CTAs for two on each SM, at least 512 of K each.
 int shrink_splits(int64_t M, int64_t K) {
-    const int64_t tiles = (M + kTileRows - 1) / kTileRows;
+    const int64_t tiles = (M + kShrinkRows - 1) / kShrinkRows;
     int64_t s = (2 * 152 + tiles - 1) / tiles;
     if (s > K / 512) s = K / 512;
     if (s > kMaxSplit) s = kMaxSplit;
@@ -467,13 +547,18 @@ cudaLaunchConfig_t behind(cudaLaunchAttribute* attr, dim3 grid, size_t smem, cud
 
 template <int NT>
 cudaError_t shrink_tile(const LoraParams& p, int splits, cudaStream_t st) {
-    constexpr int smem = kLoraWarps * kTileRows * (NT * 8 + 4) * 4;
-    if constexpr (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(k_lora_shrink_tile<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    constexpr int smem = ShrinkSmem<NT>::kBytes;
+    static bool ready[64];  // (concurrent first calls set the same attribute)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute(k_lora_shrink_tile<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
+        ready[dev] = true;
     }
-    const dim3 grid(static_cast<unsigned>((p.M + kTileRows - 1) / kTileRows), static_cast<unsigned>(splits));
+    const dim3 grid(static_cast<unsigned>((p.M + kShrinkRows - 1) / kShrinkRows), static_cast<unsigned>(splits));
     k_lora_shrink_tile<NT><<<grid, kLoraThreads, smem, st>>>(p, splits);
     return cudaGetLastError();
 }
@@ -481,12 +566,12 @@ cudaError_t shrink_tile(const LoraParams& p, int splits, cudaStream_t st) {
 }  // namespace
 
 // Room for any M' <= M: M' * splits is at most 8 M' and, splits being
-// (304 + tiles - 1) / tiles, at most 32 (304 + tiles).
+// (304 + tiles - 1) / tiles, at most 64 (304 + tiles).
 size_t lora_workspace_bytes(int64_t M, int64_t rmax, int64_t K) {
     if (M < 1) M = 1;
     int64_t s = K / 512 < kMaxSplit ? K / 512 : kMaxSplit;
     if (s < 1) s = 1;
-    const int64_t bound = kTileRows * (2 * 152 + (M + kTileRows - 1) / kTileRows);
+    const int64_t bound = kShrinkRows * (2 * 152 + (M + kShrinkRows - 1) / kShrinkRows);
     const int64_t rows = M * s < bound || bound < M ? M * s : bound;
     return static_cast<size_t>(rows) * static_cast<size_t>(rmax) * 4u + 16u;
 }
@@ -506,9 +591,9 @@ int launch_lora(const LoraParams& p, bool out_f32, void* stream) {
         else e = shrink_tile<16>(p, splits, st);
         if (e != cudaSuccess) return static_cast<int>(e);
         const bool vec_y = p.N % (out_f32 ? 4 : 8) == 0 && aligned16(p.base) && aligned16(p.y);
-        const int64_t tiles = (p.M + kTileRows - 1) / kTileRows, cols = (p.N + kLoraWarps * 64 - 1) / (kLoraWarps * 64);
-        // column chunks per CTA: t is laid out once for all of them, as long as every SM has two CTAs
-        int64_t chunks = tiles * cols / (4 * 152);
+        const int64_t tiles = (p.M + kTileRows - 1) / kTileRows, cols = (p.N + kLoraWarps * 32 - 1) / (kLoraWarps * 32);
+        // column chunks per CTA: t is laid out once for all of them, as long as there are enough CTAs to go round
+        int64_t chunks = tiles * cols / (6 * 152);
         chunks = chunks < 1 ? 1 : (chunks > 8 ? 8 : chunks);
         const int64_t groups = (cols + chunks - 1) / chunks;
         const size_t smem = static_cast<size_t>((p.rmax + 31) / 32) * (out_f32 ? 3 : 2) * 4 * 32 * 16;
