@@ -173,7 +173,7 @@ __device__ __forceinline__ float2 widen(uint32_t w) {
 
 // Four values over s, rounded to nearest even and saturated: the codes.
 template <bool E4M3>
-__device__ __forceinline__ uint32_t encode4(float4 v, float s) {
+__device__ __noinline__ uint32_t encode4(float4 v, float s) {
     if (!(s > 0.0f)) return 0u;
     v.x = __fdiv_rn(v.x, s);
     v.y = __fdiv_rn(v.y, s);
@@ -214,12 +214,25 @@ __device__ __forceinline__ uint32_t round4(float a, float b, float c, float d) {
     }
 }
 
-// encode4 for finite values of at most Q s: lo and hi enclose 1 / s.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 pair_mul(uint64_t a, uint64_t b) {
+    float2 r;
+    asm("{\n.reg .b64 m;\nmul.rn.f32x2 m, %2, %3;\nmov.b64 {%0, %1}, m;\n}" : "=f"(r.x), "=f"(r.y) : "l"(a), "l"(b));
+    return r;
+}
+
+// encode4 for finite values of at most Q s: the pairs lo and hi enclose 1 / s.
 template <bool E4M3>
-__device__ __forceinline__ uint32_t encode4_fast(float4 v, float s, float lo, float hi) {
-    const uint32_t a = round4<E4M3>(__fmul_rn(v.x, lo), __fmul_rn(v.y, lo), __fmul_rn(v.z, lo), __fmul_rn(v.w, lo));
-    const uint32_t b = round4<E4M3>(__fmul_rn(v.x, hi), __fmul_rn(v.y, hi), __fmul_rn(v.z, hi), __fmul_rn(v.w, hi));
-    return a == b ? a : encode4<E4M3>(v, s);
+__device__ __forceinline__ uint32_t encode4_fast(float2 v, float2 w, float s, uint64_t lo, uint64_t hi) {
+    const uint64_t pv = pair(v.x, v.y), pw = pair(w.x, w.y);
+    const float2 a0 = pair_mul(pv, lo), a1 = pair_mul(pw, lo), b0 = pair_mul(pv, hi), b1 = pair_mul(pw, hi);
+    const uint32_t a = round4<E4M3>(a0.x, a0.y, a1.x, a1.y), b = round4<E4M3>(b0.x, b0.y, b1.x, b1.y);
+    if (a == b) return a;
+    return encode4<E4M3>(make_float4(v.x, v.y, w.x, w.y), s);
 }
 
 template <bool E4M3>
@@ -248,7 +261,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
     constexpr int LPR = D / 4;              // lanes per row, four values each
     constexpr int RPP = TEAM * 32 / LPR;    // rows per pass of the team
     constexpr float kQmax = E4M3 ? 448.0f : 127.0f;
-    __shared__ float s_max[kAppendWarps];
+    __shared__ uint32_t s_max[kAppendWarps];
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const int units = 2 * p.c.heads;
     const int64_t team = TEAM == 1 ? static_cast<int64_t>(blockIdx.x) * kAppendWarps + warp : blockIdx.x;
@@ -280,13 +293,15 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
         const int64_t t0 = w0 + li;
         const int64_t s0 = __shfl_sync(0xffffffffu, slot, li);
         const int64_t blk = s0 >> bl;
-        // the run's length: up to bs tokens of the same block
+        // the run's length: up to bs tokens of the same block; dense: at adjacent slots, as a plan gives them
         int cnt = 0;
+        bool dense = true;
         for (int i0 = 0; i0 < bs; i0 += 32) {
             const int64_t t = t0 + i0 + lane;
-            const bool same = t < p.n_tokens && (p.slots[t] >> bl) == blk;
-            const uint32_t m = __ballot_sync(0xffffffffu, same);
+            const int64_t st = t < p.n_tokens ? p.slots[t] : -1;
+            const uint32_t m = __ballot_sync(0xffffffffu, (st >> bl) == blk);
             const int k = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+            dense = dense && __all_sync(0xffffffffu, static_cast<int>(lane) >= k || st == s0 + i0 + static_cast<int64_t>(lane));
             cnt += k;
             if (k < 32) break;
         }
@@ -294,41 +309,40 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
         const int n_old = static_cast<int>(s0 & (bs - 1));
         const int64_t unit = blk * p.c.heads + h;
         const float old = n_old > 0 ? scales[unit] : 0.0f;
+        const uint16_t* src = in + t0 * stride + col;
+        // magnitudes compare as 16-bit integers, infinity and NaN above all numbers
         uint2 held[kAppendHeld];
-        float amax = 0.0f;
-        bool odd = false;  // an infinity or NaN among the values
-        auto look = [&](const uint2& w) {
-            const float2 a = widen<BF16>(w.x), b = widen<BF16>(w.y);
-            const float m = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y)));
-            // (the sum is NaN or infinite if one of them is)
-            if (!(fabsf(a.x) + fabsf(a.y) + (fabsf(b.x) + fabsf(b.y)) <= FLT_MAX)) {
-                odd = true;
-                amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(a.x), finite_abs(a.y)), fmaxf(finite_abs(b.x), finite_abs(b.y))));
-            } else {
-                amax = fmaxf(amax, m);
-            }
-        };
+        uint32_t top = 0u;
 #pragma unroll
         for (int i = 0; i < kAppendHeld; ++i) {
             const int r = i * RPP + row;
             held[i] = make_uint2(0u, 0u);
-            if (r < cnt) held[i] = *reinterpret_cast<const uint2*>(in + (t0 + r) * stride + col);
+            if (r < cnt) held[i] = *reinterpret_cast<const uint2*>(src + r * stride);
         }
 #pragma unroll
-        for (int i = 0; i < kAppendHeld; ++i)
-            if (i * RPP < cnt) look(held[i]);
+        for (int i = 0; i < kAppendHeld; ++i) top = __vmaxu2(top, __vmaxu2(held[i].x & 0x7fff7fffu, held[i].y & 0x7fff7fffu));
 #pragma unroll 4
-        for (int r = kAppendHeld * RPP + row; r < cnt; r += RPP) look(*reinterpret_cast<const uint2*>(in + (t0 + r) * stride + col));
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+        for (int r = kAppendHeld * RPP + row; r < cnt; r += RPP) {
+            const uint2 w = *reinterpret_cast<const uint2*>(src + r * stride);
+            top = __vmaxu2(top, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu));
+        }
+        top = __reduce_max_sync(0xffffffffu, top >> 16 > (top & 0xffffu) ? top >> 16 : top & 0xffffu);
         if constexpr (TEAM > 1) {  // (also: every thread has read the old scale before it is written)
             __syncthreads();
-            if (lane == 0) s_max[warp] = amax;
-            odd = __syncthreads_or(odd);
+            if (lane == 0) s_max[warp] = top;
+            __syncthreads();
 #pragma unroll
-            for (int w = 0; w < TEAM; ++w) amax = fmaxf(amax, s_max[w]);
-        } else {
-            odd = __any_sync(0xffffffffu, odd);
+            for (int w = 0; w < TEAM; ++w) top = s_max[w] > top ? s_max[w] : top;
+        }
+        const bool odd = top >= (BF16 ? 0x7f80u : 0x7c00u);
+        float amax = widen<BF16>(top).x;
+        if (odd) {  // the largest finite magnitude, then (rare)
+            amax = 0.0f;
+            for (int r = 0; r < cnt; ++r)
+                for (int d = 0; d < D; d += 2) {
+                    const float2 a = widen<BF16>(*reinterpret_cast<const uint32_t*>(in + (t0 + r) * stride + d));
+                    amax = fmaxf(amax, fmaxf(finite_abs(a.x), finite_abs(a.y)));
+                }
         }
         float fresh = 0.0f;
         if (amax > 0.0f) fresh = fminf(fmaxf(__fdiv_rn(amax, kQmax), 0x1p-100f), 0x1p100f);
@@ -337,10 +351,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
         const bool fast = !odd && s > 0.0f && s < 0x1p100f;
         const float y = fast ? __fdividef(1.0f, s) : 0.0f;
         const float lo = __fmul_rn(y, 1.0f - 0x1p-21f), hi = __fmul_rn(y, 1.0f + 0x1p-21f);
-        auto encode = [&](const float4& v) { return fast ? encode4_fast<E4M3>(v, s, lo, hi) : encode4<E4M3>(v, s); };
+        const uint64_t lo2 = pair(lo, lo), hi2 = pair(hi, hi);
         uint8_t* out = codes + (unit << bl) * D + col;
         if (old > 0.0f && s > old) {  // the earlier tokens' codes under the grown scale
-#pragma unroll 4
+#pragma unroll 2
             for (int r = row; r < n_old; r += RPP) {
                 uint32_t* w = reinterpret_cast<uint32_t*>(out + r * D);
                 float4 v = decode4<E4M3>(*w);
@@ -353,16 +367,17 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
         }
         auto put = [&](const uint2& w, int r) {
             const float2 a = widen<BF16>(w.x), b = widen<BF16>(w.y);
-            const int o = static_cast<int>(p.slots[t0 + r] & (bs - 1));
-            *reinterpret_cast<uint32_t*>(out + o * D) = encode(make_float4(a.x, a.y, b.x, b.y));
+            const int o = dense ? n_old + r : static_cast<int>(p.slots[t0 + r] & (bs - 1));
+            *reinterpret_cast<uint32_t*>(out + o * D) =
+                fast ? encode4_fast<E4M3>(a, b, s, lo2, hi2) : encode4<E4M3>(make_float4(a.x, a.y, b.x, b.y), s);
         };
 #pragma unroll
         for (int i = 0; i < kAppendHeld; ++i) {
             const int r = i * RPP + row;
             if (r < cnt) put(held[i], r);
         }
-#pragma unroll 4
-        for (int r = kAppendHeld * RPP + row; r < cnt; r += RPP) put(*reinterpret_cast<const uint2*>(in + (t0 + r) * stride + col), r);
+#pragma unroll 2
+        for (int r = kAppendHeld * RPP + row; r < cnt; r += RPP) put(*reinterpret_cast<const uint2*>(src + r * stride), r);
         __syncwarp();  // every lane has read the old scale
         if (idx == 0) scales[unit] = s;
     }

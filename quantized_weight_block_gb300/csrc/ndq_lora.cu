@@ -79,11 +79,11 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_shrink_rows(const LoraPar
     const int64_t m = blockIdx.x / groups;
     const int32_t j0 = static_cast<int32_t>(blockIdx.x % groups) * kShrinkJ;
     const int32_t a = p.index[m];
-    const int32_t r = rank_of(p, a);
-    if (j0 >= r) return;
+    if (a < 0 || a >= p.nA) return;
     const uint16_t* x = p.x + m * p.K;
     const uint16_t* w = p.a + (static_cast<int64_t>(a) * p.rmax + j0) * p.K;
-    const int32_t nj = r - j0 < kShrinkJ ? r - j0 : kShrinkJ;
+    const int32_t have = static_cast<int32_t>(p.rmax) - j0 < kShrinkJ ? static_cast<int32_t>(p.rmax) - j0 : kShrinkJ;
+    const int32_t nj = rank_of(p, a) - j0;  // (the weights are fetched before it is known: rows beyond the rank exist)
     float s[kShrinkJ] = {};
     if constexpr (VEC) {
         const int64_t K8 = p.K >> 3;
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_shrink_rows(const LoraPar
             uint4 wv[kShrinkJ];
 #pragma unroll
             for (int j = 0; j < kShrinkJ; ++j)
-                wv[j] = j < nj ? __ldg(reinterpret_cast<const uint4*>(w + j * p.K) + i) : make_uint4(0u, 0u, 0u, 0u);
+                wv[j] = j < have ? __ldg(reinterpret_cast<const uint4*>(w + j * p.K) + i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int j = 0; j < kShrinkJ; ++j) s[j] = dot8(xv, wv[j], s[j]);
         }
@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_shrink_rows(const LoraPar
                 if (j < nj) s[j] = __fmaf_rn(xv, bf(w[j * p.K + k]), s[j]);
         }
     }
+    if (nj <= 0) return;
 #pragma unroll
     for (int j = 0; j < kShrinkJ; ++j)
 #pragma unroll
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_shrink_rows(const LoraPar
         for (int j = 0; j < kShrinkJ; ++j) s_part[warp][j] = s[j];
     }
     __syncthreads();
-    if (threadIdx.x < nj) {
+    if (threadIdx.x < kShrinkJ && static_cast<int32_t>(threadIdx.x) < nj) {
         float v = 0.0f;
 #pragma unroll
         for (int q = 0; q < kLoraWarps; ++q) v = __fadd_rn(v, s_part[q][threadIdx.x]);
@@ -132,37 +133,46 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_expand_rows(const LoraPar
     bool waited = false;
     for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
         const int32_t a = p.index[m];
-        const int32_t r = rank_of(p, a);
+        const bool has = a >= 0 && a < p.nA;
         const int64_t o = m * p.N + n;
-        float b = 0.0f;
+        const uint16_t* w = p.b + (static_cast<int64_t>(has ? a : 0) * p.N + n) * p.rmax;
+        const float* t = p.t + m * p.rmax;
+        float b = 0.0f, s = 0.0f;
         if (in) {
             if constexpr (F32) b = static_cast<const float*>(p.base)[o];
             else b = bf(static_cast<const uint16_t*>(p.base)[o]);
         }
-        const uint16_t* w = p.b + (static_cast<int64_t>(a) * p.N + n) * p.rmax;  // (not read where r is 0)
-        const float* t = p.t + m * p.rmax;
-        float s = 0.0f;
         if constexpr (VEC) {
-            uint4 v[2] = {};
+            uint4 v[2] = {};  // 16 ranks of the output's weights, fetched beside the adapter's rank
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (in && 8 * i < r) v[i] = __ldg(reinterpret_cast<const uint4*>(w) + i);
+                if (in && has && 8 * i < p.rmax) v[i] = __ldg(reinterpret_cast<const uint4*>(w) + i);
+            const int32_t r = rank_of(p, a);
             if (!waited) pdl_wait();
             waited = true;
             for (int32_t j0 = 0; j0 < r; j0 += 16) {
+                float4 tv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tv[i] = j0 + 4 * i < r ? __ldcg(reinterpret_cast<const float4*>(t + j0) + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                uint4 u[2] = {v[0], v[1]};
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (in && j0 + 16 + 8 * i < r) v[i] = __ldg(reinterpret_cast<const uint4*>(w + j0 + 16) + i);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    const uint32_t c[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                    const float f[8] = {tv[2 * i].x, tv[2 * i].y, tv[2 * i].z, tv[2 * i].w,
+                                        tv[2 * i + 1].x, tv[2 * i + 1].y, tv[2 * i + 1].z, tv[2 * i + 1].w};
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const int32_t j = j0 + 8 * i + e;
                         const float wv = (e & 1) ? bf_hi(c[e >> 1]) : bf_lo(c[e >> 1]);
-                        if (j < r) s = __fmaf_rn(__ldcg(t + j), wv, s);
+                        if (j0 + 8 * i + e < r) s = __fmaf_rn(f[e], wv, s);  // (t and weights beyond the rank are not defined)
                     }
-                    if (in && j0 + 16 + 8 * i < r) v[i] = __ldg(reinterpret_cast<const uint4*>(w + j0 + 16) + i);
                 }
             }
         } else {
+            const int32_t r = rank_of(p, a);
             if (!waited) pdl_wait();
             waited = true;
             if (in)
@@ -399,12 +409,14 @@ __global__ void __launch_bounds__(kLoraThreads, F32 ? 2 : 3) k_lora_expand_tile(
             }
         }
     };
+    const int32_t first_rank = first != INT32_MAX ? rank_of(p, first) : 0;
     if (one && first != INT32_MAX) {
-        lay(first, rank_of(p, first));
+        lay(first, first_rank);
         __syncthreads();
     }
     for (int c = 0; c < chunks; ++c) {
         const int64_t n0 = cbase + static_cast<int64_t>(c) * kLoraWarps * 32;
+        if (one && n0 >= p.N) break;
         // this lane's outputs: rows g + 8 i, columns n0 + 8 t + 0 .. 7 (n-tile e: columns 2 e, 2 e + 1)
         const int64_t nl = n0 + 8 * t;
         uint32_t bw[4][BW];  // base
@@ -439,44 +451,55 @@ __global__ void __launch_bounds__(kLoraThreads, F32 ? 2 : 3) k_lora_expand_tile(
             }
         }
         float acc[2][4][4] = {};
-        for (int32_t a = first; a != INT32_MAX; a = next_adapter(mine, a)) {
-            const int32_t r = rank_of(p, a);
-            if (!one) {
-                __syncthreads();
-                lay(a, r);
-                __syncthreads();
-            }
+        // adds adapter a's part (its t laid out): column of B's fragment n-tile e, index g: n0 + 8 (g / 2) + 2 e + g % 2
+        auto add = [&](int32_t a, int32_t r) {
+            const int64_t n = n0 + 8 * (g >> 1) + (g & 1u);
+            const uint16_t* w = p.b + (static_cast<int64_t>(a) * p.N + n) * p.rmax + 8 * t;
+            const bool whole = n0 + 32 <= p.N;
             for (int32_t pr = 0; 32 * pr < r; ++pr) {
                 uint4 wv[4];
-                // column of B's fragment n-tile e, index g: n0 + 8 (g / 2) + 2 e + g % 2
+                if (whole && 32 * pr + 32 <= r) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int64_t n = n0 + 8 * (g >> 1) + 2 * e + (g & 1u);
-                    const int32_t j = 32 * pr + 8 * static_cast<int32_t>(t);
-                    wv[e] = make_uint4(0u, 0u, 0u, 0u);
-                    if (n < p.N && j < r) {
-                        wv[e] = __ldg(reinterpret_cast<const uint4*>(p.b + (static_cast<int64_t>(a) * p.N + n) * p.rmax + j));
-                        if (j + 8 > r) {  // ranks beyond the adapter's: not 0 * garbage
-                            const int32_t left = r - j;
-                            wv[e].x = left >= 2 ? wv[e].x : wv[e].x & 0xffffu;
-                            wv[e].y = left >= 4 ? wv[e].y : (left >= 3 ? wv[e].y & 0xffffu : 0u);
-                            wv[e].z = left >= 6 ? wv[e].z : (left >= 5 ? wv[e].z & 0xffffu : 0u);
-                            wv[e].w = left >= 7 ? wv[e].w & 0xffffu : 0u;
+                    for (int e = 0; e < 4; ++e) wv[e] = __ldg(reinterpret_cast<const uint4*>(w + 2 * e * p.rmax + 32 * pr));
+                } else {
+                    const int32_t left = r - 32 * pr - 8 * static_cast<int32_t>(t);  // ranks of this lane's piece
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        wv[e] = make_uint4(0u, 0u, 0u, 0u);
+                        if (n + 2 * e < p.N && left > 0) {
+                            wv[e] = __ldg(reinterpret_cast<const uint4*>(w + 2 * e * p.rmax + 32 * pr));
+                            if (left < 8) {  // beyond the adapter's rank: not 0 * garbage
+                                wv[e].x = left >= 2 ? wv[e].x : wv[e].x & 0xffffu;
+                                wv[e].y = left >= 4 ? wv[e].y : (left >= 3 ? wv[e].y & 0xffffu : 0u);
+                                wv[e].z = left >= 6 ? wv[e].z : (left >= 5 ? wv[e].z & 0xffffu : 0u);
+                                wv[e].w = left >= 7 ? wv[e].w & 0xffffu : 0u;
+                            }
                         }
                     }
                 }
+                const uint4* f = s_t + pr * (PARTS * 128) + lane;
 #pragma unroll
                 for (int part = 0; part < PARTS; ++part)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        const uint4 f0 = s_t[(((pr * PARTS + part) * 2 + half) * 2 + 0) * 32 + lane];
-                        const uint4 f1 = s_t[(((pr * PARTS + part) * 2 + half) * 2 + 1) * 32 + lane];
+                        const uint4 f0 = f[(part * 2 + half) * 64], f1 = f[(part * 2 + half) * 64 + 32];
                         const uint32_t a0[4] = {f0.x, f0.y, f0.z, f0.w}, a1[4] = {f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) mma_bf16_16816(acc[half][e], a0, wv[e].x, wv[e].y);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) mma_bf16_16816(acc[half][e], a1, wv[e].z, wv[e].w);
                     }
+            }
+        };
+        if (one) {
+            if (first_rank > 0) add(first, first_rank);
+        } else {
+            for (int32_t a = first; a != INT32_MAX; a = next_adapter(mine, a)) {
+                const int32_t r = rank_of(p, a);
+                __syncthreads();
+                lay(a, r);
+                __syncthreads();
+                add(a, r);
             }
         }
 #pragma unroll
