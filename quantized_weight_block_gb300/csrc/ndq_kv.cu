@@ -72,17 +72,31 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const PlanParams p) {
     const uint32_t n_tokens = static_cast<uint32_t>(p.n_tokens);
     const uint32_t t1 = t0 + kPlanTokens < n_tokens ? t0 + kPlanTokens : n_tokens;
     const int32_t count = *p.free_count;
+    const bool vec = ((reinterpret_cast<uintptr_t>(p.cached) | reinterpret_cast<uintptr_t>(p.fresh)) & 15u) == 0;
     uint32_t run_q = 0, run_n = 0;
     for (int64_t r0 = 0; r0 < p.n_req && (blockIdx.x == 0 || run_q < t1); r0 += kPlanChunk) {
         const int64_t rt = r0 + static_cast<int64_t>(tid) * kPlanPer;
         uint32_t q[kPlanPer], nb[kPlanPer], kv[kPlanPer], sq = 0, sn = 0;
+        int32_t cv[kPlanPer], fv[kPlanPer];
+        if (vec && rt + kPlanPer <= p.n_req) {
+#pragma unroll
+            for (int i = 0; i < kPlanPer; i += 4) {
+                *reinterpret_cast<int4*>(cv + i) = *reinterpret_cast<const int4*>(p.cached + rt + i);
+                *reinterpret_cast<int4*>(fv + i) = *reinterpret_cast<const int4*>(p.fresh + rt + i);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPlanPer; ++i) {
+                cv[i] = fv[i] = 0;
+                if (rt + i < p.n_req) {
+                    cv[i] = p.cached[rt + i];
+                    fv[i] = p.fresh[rt + i];
+                }
+            }
+        }
 #pragma unroll
         for (int i = 0; i < kPlanPer; ++i) {
-            int32_t c = 0, f = 0;
-            if (rt + i < p.n_req) {
-                c = p.cached[rt + i];
-                f = p.fresh[rt + i];
-            }
+            const int32_t c = cv[i], f = fv[i];
             const uint32_t cu = c > 0 ? static_cast<uint32_t>(c) : 0u, fu = f > 0 ? static_cast<uint32_t>(f) : 0u;
             q[i] = sq;
             nb[i] = sn;
@@ -107,30 +121,50 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const PlanParams p) {
         if (tid == 0) s_q[kPlanChunk] = run_q + tq;
         __syncthreads();
         const uint32_t end = run_q + tq;
-        for (uint32_t t = t0 + tid; t < t1; t += kPlanThreads) {
-            if (t < run_q || t >= end) continue;
-            uint32_t lo = 0, hi = kPlanChunk;  // the last request that starts at or before t
-            while (hi - lo > 1u) {
-                const uint32_t mid = (lo + hi) >> 1;
-                if (s_q[mid] <= t) lo = mid;
-                else hi = mid;
-            }
-            const int64_t r = r0 + lo;
-            const int32_t c = p.cached[r];
-            const uint32_t cu = c > 0 ? static_cast<uint32_t>(c) : 0u;
-            const uint32_t pos = cu + (t - s_q[lo]), blk = pos >> bl, had = (cu + bs - 1u) >> bl;
-            int32_t id = -1;
-            if (blk < p.width) {
-                if (blk >= had) {
-                    const uint32_t i = static_cast<uint32_t>(count - 1) - (s_n[lo] + blk - had);
-                    if (count > 0 && i < static_cast<uint32_t>(count)) id = p.free_blocks[i];
-                    if ((pos & (bs - 1u)) == 0u) p.table[r * p.width + blk] = id;
-                } else {
-                    id = p.table[r * p.width + blk];
+        if (t0 < end && run_q < t1) {
+            constexpr int PT = kPlanTokens / kPlanThreads;  // tokens per thread, looked up side by side
+            uint32_t lo[PT] = {}, cu[PT];
+#pragma unroll
+            for (uint32_t half = kPlanChunk / 2; half > 0; half >>= 1)
+#pragma unroll
+                for (int i = 0; i < PT; ++i)  // the last request that starts at or before the token
+                    if (s_q[lo[i] + half] <= t0 + tid + kPlanThreads * i) lo[i] += half;
+#pragma unroll
+            for (int i = 0; i < PT; ++i) {
+                const uint32_t t = t0 + tid + kPlanThreads * i;
+                cu[i] = 0u;
+                if (t >= run_q && t < end && t < t1) {
+                    const int32_t c = p.cached[r0 + lo[i]];
+                    cu[i] = c > 0 ? static_cast<uint32_t>(c) : 0u;
                 }
             }
-            p.positions[t] = static_cast<int32_t>(pos);
-            p.slots[t] = id >= 0 ? (static_cast<int64_t>(id) << bl) + (pos & (bs - 1u)) : -1;
+            int32_t id[PT];
+#pragma unroll
+            for (int i = 0; i < PT; ++i) {
+                const uint32_t t = t0 + tid + kPlanThreads * i;
+                id[i] = -1;
+                if (t >= run_q && t < end && t < t1) {
+                    const uint32_t pos = cu[i] + (t - s_q[lo[i]]), blk = pos >> bl, had = (cu[i] + bs - 1u) >> bl;
+                    if (blk < p.width) {
+                        if (blk >= had) {
+                            const uint32_t k = static_cast<uint32_t>(count - 1) - (s_n[lo[i]] + blk - had);
+                            if (count > 0 && k < static_cast<uint32_t>(count)) id[i] = p.free_blocks[k];
+                        } else {
+                            id[i] = p.table[(r0 + lo[i]) * p.width + blk];
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < PT; ++i) {
+                const uint32_t t = t0 + tid + kPlanThreads * i;
+                if (t >= run_q && t < end && t < t1) {
+                    const uint32_t pos = cu[i] + (t - s_q[lo[i]]), blk = pos >> bl, had = (cu[i] + bs - 1u) >> bl;
+                    if (blk >= had && blk < p.width && (pos & (bs - 1u)) == 0u) p.table[(r0 + lo[i]) * p.width + blk] = id[i];
+                    p.positions[t] = static_cast<int32_t>(pos);
+                    p.slots[t] = id[i] >= 0 ? (static_cast<int64_t>(id[i]) << bl) + (pos & (bs - 1u)) : -1;
+                }
+            }
         }
         run_q = end;
         run_n += tn;
@@ -293,6 +327,16 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
         const int64_t t0 = w0 + li;
         const int64_t s0 = __shfl_sync(0xffffffffu, slot, li);
         const int64_t blk = s0 >> bl;
+        // the first passes of rows, fetched before the run's length is known (all of them are tokens of the call)
+        const uint16_t* src = in + t0 * stride + col;
+        const int most = p.n_tokens - t0 < bs ? static_cast<int>(p.n_tokens - t0) : bs;
+        uint2 held[kAppendHeld];
+#pragma unroll
+        for (int i = 0; i < kAppendHeld; ++i) {
+            const int r = i * RPP + row;
+            held[i] = make_uint2(0u, 0u);
+            if (r < most) held[i] = *reinterpret_cast<const uint2*>(src + r * stride);
+        }
         // the run's length: up to bs tokens of the same block; dense: at adjacent slots, as a plan gives them
         int cnt = 0;
         bool dense = true;
@@ -309,18 +353,11 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
         const int n_old = static_cast<int>(s0 & (bs - 1));
         const int64_t unit = blk * p.c.heads + h;
         const float old = n_old > 0 ? scales[unit] : 0.0f;
-        const uint16_t* src = in + t0 * stride + col;
         // magnitudes compare as 16-bit integers, infinity and NaN above all numbers
-        uint2 held[kAppendHeld];
         uint32_t top = 0u;
 #pragma unroll
-        for (int i = 0; i < kAppendHeld; ++i) {
-            const int r = i * RPP + row;
-            held[i] = make_uint2(0u, 0u);
-            if (r < cnt) held[i] = *reinterpret_cast<const uint2*>(src + r * stride);
-        }
-#pragma unroll
-        for (int i = 0; i < kAppendHeld; ++i) top = __vmaxu2(top, __vmaxu2(held[i].x & 0x7fff7fffu, held[i].y & 0x7fff7fffu));
+        for (int i = 0; i < kAppendHeld; ++i)
+            if (i * RPP + row < cnt) top = __vmaxu2(top, __vmaxu2(held[i].x & 0x7fff7fffu, held[i].y & 0x7fff7fffu));
 #pragma unroll 4
         for (int r = kAppendHeld * RPP + row; r < cnt; r += RPP) {
             const uint2 w = *reinterpret_cast<const uint2*>(src + r * stride);

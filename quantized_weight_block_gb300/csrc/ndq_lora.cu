@@ -347,12 +347,22 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_shrink_tile(const Lora
 }
 
 // y of 32 rows by `chunks` x 256 columns: each warp 32 adjacent columns at a
-// time.  t's parts are laid out as A fragments in shared memory; base and the
-// first weights of a chunk are fetched together.
+// time.  t's parts are laid out as A fragments in shared memory.  The usual
+// tile (one adapter, VEC, all 32 columns inside) fetches base and weights
+// `stages` chunks ahead through asynchronous copies private to the lane that
+// consumes them; loaded into registers chunk by chunk the same tiles took
+// twice the time, waiting.
+__host__ __device__ constexpr int expand_parts(bool f32) { return f32 ? 3 : 2; }
+__host__ __device__ constexpr int expand_t_bytes(bool f32, int rmax) { return (rmax + 31) / 32 * expand_parts(f32) * 4 * 32 * 16; }
+__host__ __device__ constexpr int expand_stage_bytes(bool f32, int rmax) {  // of one warp: base 4 rows, weights 4 pieces per 32 ranks
+    return 32 * 16 * ((f32 ? 8 : 4) + 4 * ((rmax + 31) / 32));
+}
+
 template <bool F32, bool VEC>
-__global__ void __launch_bounds__(kLoraThreads, F32 ? 2 : 3) k_lora_expand_tile(const LoraParams p, int splits, int chunks, int groups) {
-    constexpr int PARTS = F32 ? 3 : 2;
+__global__ void __launch_bounds__(kLoraThreads, 2) k_lora_expand_tile(const LoraParams p, int splits, int chunks, int groups, int stages) {
+    constexpr int PARTS = expand_parts(F32);
     constexpr int BW = F32 ? 8 : 4;  // words of base per lane and row
+    constexpr int BP = F32 ? 8 : 4;  // 16-byte pieces of base per lane
     extern __shared__ __align__(16) uint8_t s_raw[];
     uint4* s_t = reinterpret_cast<uint4*>(s_raw);  // [k-step pair][part][half of the rows][k-step][lane]
     __shared__ int32_t s_a[kTileRows];
@@ -375,20 +385,32 @@ __global__ void __launch_bounds__(kLoraThreads, F32 ? 2 : 3) k_lora_expand_tile(
         for (int32_t i = static_cast<int32_t>(tid); i < pairs * 2 * 2 * 32; i += kLoraThreads) {
             const int32_t ln = i & 31, ks = (i >> 5) & 1, half = (i >> 6) & 1, pr = i >> 7;
             const int32_t gg = ln >> 2, tt = ln & 3;
-            float v[2][4];
+            // the splits' sums, in order; all loads go out before the first addition
+            const int32_t j = 32 * pr + 8 * tt + 4 * ks;
+            float v[2][4] = {};
+            float4 ld[2][kMaxSplit];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int32_t row = 16 * half + gg + 8 * e;
-                const bool ok = s_a[row] == a;
+                const bool ok = s_a[row] == a && j < r;
+                const float* src = p.t + (m0 + row) * p.rmax + j;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int32_t j = 32 * pr + 8 * tt + 4 * ks + c;
-                    float s = 0.0f;
-                    if (ok && j < r)
-                        for (int32_t q = 0; q < splits; ++q)
-                            s = __fadd_rn(s, __ldcg(p.t + (static_cast<int64_t>(q) * p.M + m0 + row) * p.rmax + j));
-                    v[e][c] = s;
+                for (int q = 0; q < kMaxSplit; ++q)
+                    ld[e][q] = ok && q < splits ? __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(q) * p.M * p.rmax))
+                                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int q = 0; q < kMaxSplit; ++q) {
+                    v[e][0] = __fadd_rn(v[e][0], ld[e][q].x);
+                    v[e][1] = __fadd_rn(v[e][1], ld[e][q].y);
+                    v[e][2] = __fadd_rn(v[e][2], ld[e][q].z);
+                    v[e][3] = __fadd_rn(v[e][3], ld[e][q].w);
                 }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (j + c >= r) v[e][c] = 0.0f;  // (t beyond the rank is not written)
             }
 #pragma unroll
             for (int part = 0; part < PARTS; ++part) {
@@ -414,7 +436,112 @@ __global__ void __launch_bounds__(kLoraThreads, F32 ? 2 : 3) k_lora_expand_tile(
         lay(first, first_rank);
         __syncthreads();
     }
-    for (int c = 0; c < chunks; ++c) {
+    int c0 = 0;  // chunks done by the ring
+    if constexpr (VEC) {
+        int full = 0;  // chunks of this warp with all their columns inside
+        while (full < chunks && cbase + static_cast<int64_t>(full) * kLoraWarps * 32 + 32 <= p.N) ++full;
+        if (one && first_rank > 0 && stages > 1) {
+            c0 = full;
+            const int32_t r = first_rank, pairs = (r + 31) / 32;
+            const uint32_t stage = static_cast<uint32_t>(expand_stage_bytes(F32, static_cast<int>(p.rmax)));
+            const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(s_raw)) +
+                                  static_cast<uint32_t>(expand_t_bytes(F32, static_cast<int>(p.rmax))) +
+                                  warp * static_cast<uint32_t>(stages) * stage + lane * 16u;
+            const size_t el = F32 ? 4 : 2;
+            const uint8_t* bsrc = static_cast<const uint8_t*>(p.base) + ((m0 + g) * p.N + cbase + 8 * t) * el;
+            const uint16_t* wsrc = p.b + (static_cast<int64_t>(first) * p.N + cbase + 8 * (g >> 1) + (g & 1u)) * p.rmax + 8 * t;
+            const uint32_t wbytes[4] = {8u * t < static_cast<uint32_t>(r) ? 16u : 0u, 32u + 8u * t < static_cast<uint32_t>(r) ? 16u : 0u,
+                                        64u + 8u * t < static_cast<uint32_t>(r) ? 16u : 0u, 96u + 8u * t < static_cast<uint32_t>(r) ? 16u : 0u};
+            auto issue = [&](int c) {
+                if (c < full) {
+                    uint32_t d = ring + static_cast<uint32_t>(c % stages) * stage;
+                    const uint8_t* b = bsrc + static_cast<int64_t>(c) * (kLoraWarps * 32) * el;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool in = m0 + g + 8 * i < p.M;
+                        const uint8_t* row = b + 8 * i * p.N * el;
+#pragma unroll
+                        for (int q = 0; q < BP / 4; ++q, d += 512u)
+                            cp_async16(d, in ? row + 16 * q : static_cast<const uint8_t*>(p.base), in ? 16u : 0u);
+                    }
+                    const uint16_t* w = wsrc + static_cast<int64_t>(c) * (kLoraWarps * 32) * p.rmax;
+#pragma unroll
+                    for (int pr = 0; pr < 4; ++pr)
+                        if (pr < pairs) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e, d += 512u)
+                                cp_async16(d, wbytes[pr] ? w + 2 * e * p.rmax + 32 * pr : p.b, wbytes[pr]);
+                        }
+                }
+                cp_commit();
+            };
+            for (int c = 0; c < stages - 1; ++c) issue(c);
+            for (int c = 0; c < full; ++c) {
+                issue(c + stages - 1);
+                if (stages == 4) cp_wait<3>();
+                else if (stages == 3) cp_wait<2>();
+                else cp_wait<1>();
+                const uint8_t* st = s_raw + expand_t_bytes(F32, static_cast<int>(p.rmax)) +
+                                    (warp * static_cast<uint32_t>(stages) + static_cast<uint32_t>(c % stages)) * stage + lane * 16u;
+                float acc[2][4][4] = {};
+#pragma unroll 1
+                for (int32_t pr = 0; pr < pairs; ++pr) {
+                    uint4 wv[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) wv[e] = *reinterpret_cast<const uint4*>(st + (BP + 4 * pr + e) * 512);
+                    const int32_t left = r - 32 * pr - 8 * static_cast<int32_t>(t);
+                    if (left > 0 && left < 8) {  // beyond the adapter's rank: not 0 * garbage
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            wv[e].x = left >= 2 ? wv[e].x : wv[e].x & 0xffffu;
+                            wv[e].y = left >= 4 ? wv[e].y : (left >= 3 ? wv[e].y & 0xffffu : 0u);
+                            wv[e].z = left >= 6 ? wv[e].z : (left >= 5 ? wv[e].z & 0xffffu : 0u);
+                            wv[e].w = left >= 7 ? wv[e].w & 0xffffu : 0u;
+                        }
+                    }
+                    const uint4* f = s_t + pr * (PARTS * 128) + lane;
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint4 f0 = f[(part * 2 + half) * 64], f1 = f[(part * 2 + half) * 64 + 32];
+                            const uint32_t a0[4] = {f0.x, f0.y, f0.z, f0.w}, a1[4] = {f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) mma_bf16_16816(acc[half][e], a0, wv[e].x, wv[e].y);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) mma_bf16_16816(acc[half][e], a1, wv[e].z, wv[e].w);
+                        }
+                }
+                uint8_t* yb = static_cast<uint8_t*>(p.y) + ((m0 + g) * p.N + cbase + static_cast<int64_t>(c) * (kLoraWarps * 32) + 8 * t) * el;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (m0 + g + 8 * i >= p.M) continue;
+                    uint8_t* y = yb + 8 * i * p.N * el;
+                    const int half = i >> 1, k = 2 * (i & 1);
+                    if constexpr (F32) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            float4 v = *reinterpret_cast<const float4*>(st + (2 * i + q) * 512);
+                            v.x = __fadd_rn(v.x, acc[half][2 * q][k]);
+                            v.y = __fadd_rn(v.y, acc[half][2 * q][k + 1]);
+                            v.z = __fadd_rn(v.z, acc[half][2 * q + 1][k]);
+                            v.w = __fadd_rn(v.w, acc[half][2 * q + 1][k + 1]);
+                            *reinterpret_cast<float4*>(y + 16 * q) = v;
+                        }
+                    } else {
+                        uint4 v = *reinterpret_cast<const uint4*>(st + i * 512);
+                        uint32_t* u = &v.x;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            u[q] = pack_bf16(__fadd_rn(bf_lo(u[q]), acc[half][q][k]), __fadd_rn(bf_hi(u[q]), acc[half][q][k + 1]));
+                        *reinterpret_cast<uint4*>(y) = v;
+                    }
+                }
+            }
+            cp_wait<0>();
+        }
+    }
+    for (int c = c0; c < chunks; ++c) {
         const int64_t n0 = cbase + static_cast<int64_t>(c) * kLoraWarps * 32;
         if (one && n0 >= p.N) break;
         // this lane's outputs: rows g + 8 i, columns n0 + 8 t + 0 .. 7 (n-tile e: columns 2 e, 2 e + 1)
@@ -568,6 +695,22 @@ cudaLaunchConfig_t behind(cudaLaunchAttribute* attr, dim3 grid, size_t smem, cud
     return cfg;
 }
 
+cudaError_t expand_ready() {
+    static bool ready[64];  // (concurrent first calls set the same attributes)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (ready[dev]) return cudaSuccess;
+    for (const void* fn : {reinterpret_cast<const void*>(k_lora_expand_tile<true, true>), reinterpret_cast<const void*>(k_lora_expand_tile<true, false>),
+                           reinterpret_cast<const void*>(k_lora_expand_tile<false, true>), reinterpret_cast<const void*>(k_lora_expand_tile<false, false>)}) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+        if (e != cudaSuccess) return e;
+    }
+    ready[dev] = true;
+    return cudaSuccess;
+}
+
 template <int NT>
 cudaError_t shrink_tile(const LoraParams& p, int splits, cudaStream_t st) {
     constexpr int smem = ShrinkSmem<NT>::kBytes;
@@ -615,17 +758,28 @@ int launch_lora(const LoraParams& p, bool out_f32, void* stream) {
         if (e != cudaSuccess) return static_cast<int>(e);
         const bool vec_y = p.N % (out_f32 ? 4 : 8) == 0 && aligned16(p.base) && aligned16(p.y);
         const int64_t tiles = (p.M + kTileRows - 1) / kTileRows, cols = (p.N + kLoraWarps * 32 - 1) / (kLoraWarps * 32);
-        // column chunks per CTA: t is laid out once for all of them, as long as there are enough CTAs to go round
-        int64_t chunks = tiles * cols / (6 * 152);
-        chunks = chunks < 1 ? 1 : (chunks > 8 ? 8 : chunks);
+        // the ring: as many stages (2 to 4) as fit two CTAs on an SM, or else one
+        const int rm = static_cast<int>(p.rmax), tb = expand_t_bytes(out_f32, rm), sb = expand_stage_bytes(out_f32, rm) * kLoraWarps;
+        int stages = 4, per_sm = 2;
+        while (stages > 2 && tb + stages * sb > 110 * 1024) --stages;
+        if (tb + stages * sb > 110 * 1024) {
+            per_sm = 1;
+            stages = 4;
+            while (stages > 2 && tb + stages * sb > 220 * 1024) --stages;
+        }
+        const size_t smem = static_cast<size_t>(tb + stages * sb);
+        // column chunks per CTA: t is laid out once for all of them, as long as there are CTAs for three rounds
+        int64_t chunks = tiles * cols / (3 * 152 * per_sm);
+        chunks = chunks < 1 ? 1 : (chunks > 16 ? 16 : chunks);
         const int64_t groups = (cols + chunks - 1) / chunks;
-        const size_t smem = static_cast<size_t>((p.rmax + 31) / 32) * (out_f32 ? 3 : 2) * 4 * 32 * 16;
+        e = expand_ready();
+        if (e != cudaSuccess) return static_cast<int>(e);
         cudaLaunchConfig_t cfg = behind(attr, dim3(static_cast<unsigned>(tiles * groups)), smem, st);
         const int ch = static_cast<int>(chunks), cg = static_cast<int>(groups);
-        if (out_f32) e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, true>, p, splits, ch, cg)
-                               : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, false>, p, splits, ch, cg);
-        else e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, true>, p, splits, ch, cg)
-                       : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, false>, p, splits, ch, cg);
+        if (out_f32) e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, true>, p, splits, ch, cg, stages)
+                               : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, false>, p, splits, ch, cg, stages);
+        else e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, true>, p, splits, ch, cg, stages)
+                       : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, false>, p, splits, ch, cg, stages);
         return static_cast<int>(e);
     }
     if (p.nA > 0) {
