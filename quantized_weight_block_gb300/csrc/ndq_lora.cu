@@ -12,8 +12,8 @@
 //   of one pass over the adapters' weights.  A CTA takes one row and
 //   kShrinkJ ranks over all of K; a thread of the expansion one or more
 //   outputs.
-// * many rows (k_lora_shrink_tile, k_lora_expand_tile): tiles of 64 and 32
-//   rows on the tensor cores (mma.sync m16n8k16: the operator is bound by reading x
+// * many rows (k_lora_shrink_tile, k_lora_expand_tile): tiles of 64 rows on
+//   the tensor cores (mma.sync m16n8k16: the operator is bound by reading x
 //   and base and writing y, and its products need a fraction of even that
 //   rate).  A tile goes through the adapters of its rows one by one, with the
 //   other adapters' rows as zeros, so any row order is right and adjacent
@@ -21,10 +21,9 @@
 //   the shrink's products are exact; t enters the expansion as a sum of
 //   bfloat16 parts: three for a binary32 result (2^-24 of t is left), two
 //   for a bfloat16 one (2^-16, under the result's own rounding of 2^-9).
-//   The expansion's weights are loaded from global memory in the order of the
-//   fragments: the k-index is permuted so that a lane's 16-byte load is its
-//   part of two k-steps, the output columns so that a lane holds 8 adjacent
-//   ones.
+//   In the expansion the k-index is permuted so that a lane's 16 bytes are
+//   its part of two k-steps, the output columns so that a lane holds 8
+//   adjacent ones.
 //
 // Any other alignment (K or max_rank not a multiple of 8, buffers off 16
 // bytes) takes the few-row kernels with scalar loads.
@@ -34,6 +33,7 @@
 
 #include <cstdint>
 
+#include "ndq_device.cuh"
 #include "ndq_serve.h"
 
 namespace ndq {
@@ -42,7 +42,6 @@ namespace {
 constexpr int kShrinkJ = 4;          // ranks per CTA of k_lora_shrink_rows
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
-constexpr int kTileRows = 32;        // rows of a tensor-core tile
 constexpr int kMaxSplit = 8;         // K splits of k_lora_shrink_tile at most
 
 __device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
@@ -195,19 +194,6 @@ __device__ __forceinline__ void mma_bf16_16816(float* c, const uint32_t* a, uint
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// The next adapter of a tile after `prev` (rows' adapters in s_a; lanes are
-// rows), or INT32_MAX: ascending, so each comes once.
-__device__ __forceinline__ int32_t next_adapter(int32_t mine, int32_t prev) {
-    int32_t c = mine > prev ? mine : INT32_MAX;
-    return __reduce_min_sync(0xffffffffu, c);
-}
-
 // Sums t over a K split: CTA (tile of 64 rows, split), NT = max_rank / 8 rounded
 // up.  x and the adapter's rows of A come through a ring of asynchronous
 // copies in shared memory, 64 of K a stage, 16-byte pieces exchanged by row
@@ -346,57 +332,221 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_shrink_tile(const Lora
     }
 }
 
-// y of 32 rows by `chunks` x 256 columns: each warp 32 adjacent columns at a
-// time.  t's parts are laid out as A fragments in shared memory.  The usual
-// tile (one adapter, VEC, all 32 columns inside) fetches base and weights
-// `stages` chunks ahead through asynchronous copies private to the lane that
-// consumes them; loaded into registers chunk by chunk the same tiles took
-// twice the time, waiting.
+// Expansion of tiles of 64 rows, 256 columns (128 for wide binary32 cases) at a
+// time.  t's parts are laid out once a tile as A fragments in shared memory.
+// Warp 16 brings base (one bulk copy of a row's columns each: 16-byte loads
+// scattered over 64 rows read HBM at 2 TB/s) and the adapter's weights (one
+// piece of memory) into a ring; warps 0-15, 2 row halves by 8 column groups,
+// multiply, add and store.  A CTA's part of a tile is gone through once for
+// each adapter of its rows (and once for rows without one), with those rows
+// alone; so the order of (tile, columns) is divided over the CTAs by weight, a
+// tile counting as often as the adapter changes along its rows.  Without
+// VEC (N or a buffer off the 16-byte grid) base and weights are loaded directly.
+constexpr int kExpandRows = 64;
+constexpr int kExpandWarps = 16;
+constexpr int kExpandThreads = (kExpandWarps + 1) * 32;
+constexpr int kExpandStages = 4;  // at most
+constexpr int kExpandTiles = 2048;  // tiles whose weights are counted
+constexpr uint32_t kLoraFault = 16u;  // bit of the device fault word
+
 __host__ __device__ constexpr int expand_parts(bool f32) { return f32 ? 3 : 2; }
-__host__ __device__ constexpr int expand_t_bytes(bool f32, int rmax) { return (rmax + 31) / 32 * expand_parts(f32) * 4 * 32 * 16; }
-__host__ __device__ constexpr int expand_stage_bytes(bool f32, int rmax) {  // of one warp: base 4 rows, weights 4 pieces per 32 ranks
-    return 32 * 16 * ((f32 ? 8 : 4) + 4 * ((rmax + 31) / 32));
+__host__ __device__ constexpr int expand_t_bytes(bool f32, int rmax) { return (rmax + 31) / 32 * expand_parts(f32) * 8 * 32 * 16; }
+__host__ __device__ constexpr int expand_stage_bytes(bool f32, int rmax, int cols) {
+    return kExpandRows * cols * (f32 ? 4 : 2) + cols * rmax * 2;
+}
+
+// Splits 8 values of t into PARTS bfloat16 A fragments: rows g (v[0]) and g + 8 (v[1]) of four adjacent ranks.
+template <int PARTS>
+__device__ __forceinline__ void lay_parts(float (&v)[2][4], uint4* dst, int stride) {
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part) {
+        uint4 f;
+        f.x = pack_bf16(v[0][0], v[0][1]);
+        f.y = pack_bf16(v[1][0], v[1][1]);
+        f.z = pack_bf16(v[0][2], v[0][3]);
+        f.w = pack_bf16(v[1][2], v[1][3]);
+        dst[part * stride] = f;
+        v[0][0] = __fsub_rn(v[0][0], bf_lo(f.x));
+        v[0][1] = __fsub_rn(v[0][1], bf_hi(f.x));
+        v[1][0] = __fsub_rn(v[1][0], bf_lo(f.y));
+        v[1][1] = __fsub_rn(v[1][1], bf_hi(f.y));
+        v[0][2] = __fsub_rn(v[0][2], bf_lo(f.z));
+        v[0][3] = __fsub_rn(v[0][3], bf_hi(f.z));
+        v[1][2] = __fsub_rn(v[1][2], bf_lo(f.w));
+        v[1][3] = __fsub_rn(v[1][3], bf_hi(f.w));
+    }
+}
+
+// Ranks beyond the adapter's in a piece of 8 of which `left` (1 .. 7) count: not 0 * garbage.
+__device__ __forceinline__ void cut_ranks(uint4& w, int32_t left) {
+    w.x = left >= 2 ? w.x : w.x & 0xffffu;
+    w.y = left >= 4 ? w.y : (left >= 3 ? w.y & 0xffffu : 0u);
+    w.z = left >= 6 ? w.z : (left >= 5 ? w.z & 0xffffu : 0u);
+    w.w = left >= 7 ? w.w & 0xffffu : 0u;
 }
 
 template <bool F32, bool VEC>
-__global__ void __launch_bounds__(kLoraThreads, 2) k_lora_expand_tile(const LoraParams p, int splits, int chunks, int groups, int stages) {
+__global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const LoraParams p, int splits, int cols, int stages) {
     constexpr int PARTS = expand_parts(F32);
-    constexpr int BW = F32 ? 8 : 4;  // words of base per lane and row
-    constexpr int BP = F32 ? 8 : 4;  // 16-byte pieces of base per lane
-    extern __shared__ __align__(16) uint8_t s_raw[];
-    uint4* s_t = reinterpret_cast<uint4*>(s_raw);  // [k-step pair][part][half of the rows][k-step][lane]
-    __shared__ int32_t s_a[kTileRows];
+    constexpr int EL = F32 ? 4 : 2;
+    extern __shared__ __align__(128) uint8_t s_buf[];
+    __shared__ uint64_t s_full[kExpandStages], s_empty[kExpandStages];
+    __shared__ int32_t s_a[kExpandRows];
+    __shared__ uint32_t s_fault;
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x / groups) * kTileRows;
-    int32_t mine = -1;
-    if (m0 + lane < p.M) {
-        mine = p.index[m0 + lane];
-        if (mine < 0 || mine >= p.nA) mine = -1;
-    }
-    if (warp == 0) s_a[lane] = mine;
-    const int64_t cbase = (static_cast<int64_t>(blockIdx.x % groups) * chunks * kLoraWarps + warp) * 32;
-    const int32_t first = next_adapter(mine, -1);
-    const bool one = first == INT32_MAX || next_adapter(mine, first) == INT32_MAX;  // a single adapter: lay t out once
-    pdl_wait();
+    const int rmax = static_cast<int>(p.rmax);
+    const uint32_t tbytes = static_cast<uint32_t>(expand_t_bytes(F32, rmax)), stage = static_cast<uint32_t>(expand_stage_bytes(F32, rmax, cols));
+    uint4* s_t = reinterpret_cast<uint4*>(s_buf);  // [k-step pair][part][16 rows][k-step][lane]
+    uint8_t* ring = s_buf + tbytes;
+    const int64_t tiles = (p.M + kExpandRows - 1) / kExpandRows, per = (p.N + cols - 1) / cols;
+    __shared__ uint32_t s_w[kExpandTiles + 1];  // weights of the tiles before each
+    __shared__ uint32_t s_run[kExpandWarps];
+    const int32_t nw = tiles <= kExpandTiles ? static_cast<int32_t>(tiles) : 0;  // (more: all alike)
+    if (warp < kExpandWarps)
+        for (int32_t i = static_cast<int32_t>(warp); i < nw; i += kExpandWarps) {
+            uint32_t changes = 0;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t m = static_cast<int64_t>(i) * kExpandRows + lane + 32 * q;
+                const bool diff = m < p.M && (lane + q) > 0 && p.index[m] != p.index[m - 1];
+                changes += __popc(__ballot_sync(0xffffffffu, diff));
+            }
+            if (lane == 0) s_w[i] = changes + 1u;
+        }
     __syncthreads();
+    if (warp < kExpandWarps) {  // exclusive prefix sums, kExpandTiles / 512 tiles a thread
+        constexpr int TPT = kExpandTiles / (kExpandWarps * 32);
+        uint32_t v[TPT], sum = 0;
+#pragma unroll
+        for (int q = 0; q < TPT; ++q) {
+            const int32_t i = static_cast<int32_t>(tid) * TPT + q;
+            v[q] = sum;
+            sum += i < nw ? s_w[i] : 0u;
+        }
+        uint32_t incl = sum;
+#pragma unroll
+        for (uint32_t d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += y;
+        }
+        if (lane == 31u) s_run[warp] = incl;
+        asm volatile("barrier.cta.sync 1, %0;" ::"n"(kExpandWarps * 32) : "memory");
+        uint32_t before = incl - sum;
+        for (uint32_t q = 0; q < warp; ++q) before += s_run[q];
+#pragma unroll
+        for (int q = 0; q < TPT; ++q) {
+            const int32_t i = static_cast<int32_t>(tid) * TPT + q;
+            if (i <= nw) s_w[i] = before + v[q];
+        }
+        if (static_cast<int32_t>(tid) * TPT + TPT == nw) s_w[nw] = before + sum;
+    }
+    __syncthreads();
+    // this CTA's columns: from (tile, chunk) to (tile, chunk), in chunks from the first tile on
+    auto place = [&](int64_t b) -> int64_t {
+        if (nw == 0) return tiles * per * b / gridDim.x;
+        const int64_t u = static_cast<int64_t>(s_w[nw]) * per * b / gridDim.x;  // in weighted chunks
+        int32_t lo = 0, hi = nw;
+        while (hi - lo > 1) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (static_cast<int64_t>(s_w[mid]) * per <= u) lo = mid;
+            else hi = mid;
+        }
+        if (u >= static_cast<int64_t>(s_w[nw]) * per) return tiles * per;
+        return lo * per + (u - static_cast<int64_t>(s_w[lo]) * per) / (s_w[lo + 1] - s_w[lo]);
+    };
+    const int64_t w0 = place(blockIdx.x), w1 = place(blockIdx.x + 1);
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], kExpandWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        s_fault = 0u;
+    }
+    __syncthreads();
+    // the adapters of a tile, by lane: rows lane and lane + 32 (-1: none; INT32_MAX: no row)
+    auto rows_of = [&](int64_t tile, int32_t (&mine)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t m = tile * kExpandRows + lane + 32 * i;
+            mine[i] = INT32_MAX;
+            if (m < p.M) {
+                const int32_t a = p.index[m];
+                mine[i] = a >= 0 && a < p.nA ? a : -1;
+            }
+        }
+    };
+    auto next = [&](const int32_t (&mine)[2], int32_t prev) {  // ascending, INT32_MAX at the end
+        const int32_t c0 = mine[0] > prev ? mine[0] : INT32_MAX, c1 = mine[1] > prev ? mine[1] : INT32_MAX;
+        return __reduce_min_sync(0xffffffffu, c0 < c1 ? c0 : c1);
+    };
+
+    if (warp == kExpandWarps) {
+        // ---- loader
+        int issued = 0;
+        bool ok = true;
+        for (int64_t w = w0; VEC && w < w1 && ok;) {
+            const int64_t tile = w / per, m0 = tile * kExpandRows;
+            const int64_t end = (tile + 1) * per < w1 ? (tile + 1) * per : w1;
+            int32_t mine[2];
+            rows_of(tile, mine);
+            for (int32_t a = next(mine, -2); a != INT32_MAX && ok; a = next(mine, a)) {
+                const uint32_t nr = __popc(__ballot_sync(0xffffffffu, mine[0] == a)) + __popc(__ballot_sync(0xffffffffu, mine[1] == a));
+                const bool weights = rank_of(p, a) > 0;
+                for (int64_t c = w; c < end; ++c) {
+                    const int64_t n0 = c % per * cols;
+                    const int st = issued % stages;
+                    if (issued >= stages) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_empty[st], static_cast<uint32_t>((issued / stages - 1) & 1)));
+                    if (!ok) break;
+                    const uint32_t nc = static_cast<uint32_t>(p.N - n0 < cols ? p.N - n0 : cols);
+                    const uint32_t wb = weights ? nc * static_cast<uint32_t>(rmax) * 2u : 0u;
+                    uint8_t* d = ring + static_cast<uint32_t>(st) * stage;
+                    if (lane == 0) mbar_arrive_expect_tx(&s_full[st], nr * nc * EL + wb);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (mine[i] == a)
+                            bulk_load(d + (lane + 32 * i) * static_cast<uint32_t>(cols) * EL,
+                                      static_cast<const uint8_t*>(p.base) + ((m0 + lane + 32 * i) * p.N + n0) * EL, nc * EL, &s_full[st]);
+                    if (weights && lane == 0)
+                        bulk_load(d + kExpandRows * static_cast<uint32_t>(cols) * EL, p.b + (static_cast<int64_t>(a) * p.N + n0) * p.rmax, wb, &s_full[st]);
+                    ++issued;
+                }
+            }
+            w = end;
+        }
+        if (!ok) {  // its own copies in flight land before the block ends
+            if (lane == 0) {
+                atomicOr(&s_fault, 1u);
+                atomicOr(p.fault, kLoraFault);
+            }
+            for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+                mbar_wait_bounded(&s_full[i % stages], static_cast<uint32_t>((i / stages) & 1));
+        }
+        __syncthreads();
+        return;
+    }
+
+    // ---- compute: rows 32 rh .. of the tile, columns 32 cg .. of the chunk
+    const uint32_t rh = warp >> 3, cg = warp & 7u;
+    pdl_wait();
     // lays adapter a's t out: rows of other adapters and ranks beyond r as zeros
-    auto lay = [&](int32_t a, int32_t r) {
+    auto lay = [&](int64_t m0, int32_t a, int32_t r) {
         const int32_t pairs = (r + 31) / 32;
-        for (int32_t i = static_cast<int32_t>(tid); i < pairs * 2 * 2 * 32; i += kLoraThreads) {
-            const int32_t ln = i & 31, ks = (i >> 5) & 1, half = (i >> 6) & 1, pr = i >> 7;
-            const int32_t gg = ln >> 2, tt = ln & 3;
+        for (int32_t i = static_cast<int32_t>(tid); i < pairs * 4 * 2 * 32; i += kExpandWarps * 32) {
+            const int32_t ln = i & 31, ks = (i >> 5) & 1, quarter = (i >> 6) & 3, pr = i >> 8;
+            const int32_t gg = ln >> 2, j = 32 * pr + 8 * (ln & 3) + 4 * ks;
             // the splits' sums, in order; all loads go out before the first addition
-            const int32_t j = 32 * pr + 8 * tt + 4 * ks;
             float v[2][4] = {};
             float4 ld[2][kMaxSplit];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int32_t row = 16 * half + gg + 8 * e;
-                const bool ok = s_a[row] == a && j < r;
+                const int32_t row = 16 * quarter + gg + 8 * e;
+                const bool in = s_a[row] == a && j < r;
                 const float* src = p.t + (m0 + row) * p.rmax + j;
 #pragma unroll
                 for (int q = 0; q < kMaxSplit; ++q)
-                    ld[e][q] = ok && q < splits ? __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(q) * p.M * p.rmax))
+                    ld[e][q] = in && q < splits ? __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(q) * p.M * p.rmax))
                                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
 #pragma unroll
@@ -412,264 +562,133 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_expand_tile(const Lora
                 for (int c = 0; c < 4; ++c)
                     if (j + c >= r) v[e][c] = 0.0f;  // (t beyond the rank is not written)
             }
-#pragma unroll
-            for (int part = 0; part < PARTS; ++part) {
-                uint4 f;
-                f.x = pack_bf16(v[0][0], v[0][1]);
-                f.y = pack_bf16(v[1][0], v[1][1]);
-                f.z = pack_bf16(v[0][2], v[0][3]);
-                f.w = pack_bf16(v[1][2], v[1][3]);
-                s_t[(((pr * PARTS + part) * 2 + half) * 2 + ks) * 32 + ln] = f;
-                v[0][0] = __fsub_rn(v[0][0], bf_lo(f.x));
-                v[0][1] = __fsub_rn(v[0][1], bf_hi(f.x));
-                v[1][0] = __fsub_rn(v[1][0], bf_lo(f.y));
-                v[1][1] = __fsub_rn(v[1][1], bf_hi(f.y));
-                v[0][2] = __fsub_rn(v[0][2], bf_lo(f.z));
-                v[0][3] = __fsub_rn(v[0][3], bf_hi(f.z));
-                v[1][2] = __fsub_rn(v[1][2], bf_lo(f.w));
-                v[1][3] = __fsub_rn(v[1][3], bf_hi(f.w));
-            }
+            lay_parts<PARTS>(v, s_t + (pr * PARTS * 8 + quarter * 2 + ks) * 32 + ln, 8 * 32);
         }
     };
-    const int32_t first_rank = first != INT32_MAX ? rank_of(p, first) : 0;
-    if (one && first != INT32_MAX) {
-        lay(first, first_rank);
-        __syncthreads();
-    }
-    int c0 = 0;  // chunks done by the ring
-    if constexpr (VEC) {
-        int full = 0;  // chunks of this warp with all their columns inside
-        while (full < chunks && cbase + static_cast<int64_t>(full) * kLoraWarps * 32 + 32 <= p.N) ++full;
-        if (one && first_rank > 0 && stages > 1) {
-            c0 = full;
-            const int32_t r = first_rank, pairs = (r + 31) / 32;
-            const uint32_t stage = static_cast<uint32_t>(expand_stage_bytes(F32, static_cast<int>(p.rmax)));
-            const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(s_raw)) +
-                                  static_cast<uint32_t>(expand_t_bytes(F32, static_cast<int>(p.rmax))) +
-                                  warp * static_cast<uint32_t>(stages) * stage + lane * 16u;
-            const size_t el = F32 ? 4 : 2;
-            const uint8_t* bsrc = static_cast<const uint8_t*>(p.base) + ((m0 + g) * p.N + cbase + 8 * t) * el;
-            const uint16_t* wsrc = p.b + (static_cast<int64_t>(first) * p.N + cbase + 8 * (g >> 1) + (g & 1u)) * p.rmax + 8 * t;
-            const uint32_t wbytes[4] = {8u * t < static_cast<uint32_t>(r) ? 16u : 0u, 32u + 8u * t < static_cast<uint32_t>(r) ? 16u : 0u,
-                                        64u + 8u * t < static_cast<uint32_t>(r) ? 16u : 0u, 96u + 8u * t < static_cast<uint32_t>(r) ? 16u : 0u};
-            auto issue = [&](int c) {
-                if (c < full) {
-                    uint32_t d = ring + static_cast<uint32_t>(c % stages) * stage;
-                    const uint8_t* b = bsrc + static_cast<int64_t>(c) * (kLoraWarps * 32) * el;
+    // one k-step pair: A fragments of this warp's 32 rows times the pieces wv
+    auto multiply = [&](float (&acc)[2][4][4], int32_t pr, const uint4 (&wv)[4]) {
+        const uint4* f = s_t + (pr * PARTS * 8 + rh * 4) * 32 + lane;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool in = m0 + g + 8 * i < p.M;
-                        const uint8_t* row = b + 8 * i * p.N * el;
+        for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-                        for (int q = 0; q < BP / 4; ++q, d += 512u)
-                            cp_async16(d, in ? row + 16 * q : static_cast<const uint8_t*>(p.base), in ? 16u : 0u);
-                    }
-                    const uint16_t* w = wsrc + static_cast<int64_t>(c) * (kLoraWarps * 32) * p.rmax;
+            for (int half = 0; half < 2; ++half) {
+                const uint4 f0 = f[(part * 8 + half * 2) * 32], f1 = f[(part * 8 + half * 2 + 1) * 32];
+                const uint32_t a0[4] = {f0.x, f0.y, f0.z, f0.w}, a1[4] = {f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-                    for (int pr = 0; pr < 4; ++pr)
-                        if (pr < pairs) {
+                for (int e = 0; e < 4; ++e) mma_bf16_16816(acc[half][e], a0, wv[e].x, wv[e].y);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e, d += 512u)
-                                cp_async16(d, wbytes[pr] ? w + 2 * e * p.rmax + 32 * pr : p.b, wbytes[pr]);
-                        }
-                }
-                cp_commit();
-            };
-            for (int c = 0; c < stages - 1; ++c) issue(c);
-            for (int c = 0; c < full; ++c) {
-                issue(c + stages - 1);
-                if (stages == 4) cp_wait<3>();
-                else if (stages == 3) cp_wait<2>();
-                else cp_wait<1>();
-                const uint8_t* st = s_raw + expand_t_bytes(F32, static_cast<int>(p.rmax)) +
-                                    (warp * static_cast<uint32_t>(stages) + static_cast<uint32_t>(c % stages)) * stage + lane * 16u;
+                for (int e = 0; e < 4; ++e) mma_bf16_16816(acc[half][e], a1, wv[e].z, wv[e].w);
+            }
+    };
+    auto meet = [&]() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kExpandWarps * 32) : "memory"); };
+
+    int used = 0;
+    bool ok = true;  // (a warp whose wait ran out goes on without working: the others meet it)
+    for (int64_t w = w0; w < w1;) {
+        const int64_t tile = w / per, m0 = tile * kExpandRows;
+        const int64_t end = (tile + 1) * per < w1 ? (tile + 1) * per : w1;
+        int32_t mine[2];
+        rows_of(tile, mine);
+        meet();  // every warp is done with the previous tile
+        if (warp == 0) {
+            s_a[lane] = mine[0];
+            s_a[lane + 32] = mine[1];
+        }
+        for (int32_t a = next(mine, -2); a != INT32_MAX; a = next(mine, a)) {
+            const int32_t r = rank_of(p, a);
+            meet();  // s_a is there, and every warp is done with the previous adapter's t
+            lay(m0, a, r);
+            meet();
+            for (int64_t c = w; c < end; ++c) {
+                const int64_t n0 = c % per * cols;
+                const int64_t nl = n0 + 32 * cg + 8 * t;  // this lane's 8 columns (n-tile e: columns 2 e, 2 e + 1)
                 float acc[2][4][4] = {};
+                const uint8_t* sb = nullptr;
+                if constexpr (VEC) {
+                    const int st = used % stages;
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[st], static_cast<uint32_t>((used / stages) & 1)));
+                    sb = ring + static_cast<uint32_t>(st) * stage;
+                }
+                if (ok && static_cast<int>(32 * cg) < cols) {
+                    // column of B's fragment n-tile e, index g: 32 cg + 8 (g / 2) + 2 e + g % 2
+                    const int32_t nb = static_cast<int32_t>(32 * cg + 8 * (g >> 1) + (g & 1u));
+                    const uint8_t* sw = sb + kExpandRows * cols * EL + (nb * rmax + 8 * static_cast<int>(t)) * 2;
+                    const uint16_t* src = p.b + (static_cast<int64_t>(a < 0 ? 0 : a) * p.N + n0 + nb) * p.rmax + 8 * t;
 #pragma unroll 1
-                for (int32_t pr = 0; pr < pairs; ++pr) {
-                    uint4 wv[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) wv[e] = *reinterpret_cast<const uint4*>(st + (BP + 4 * pr + e) * 512);
-                    const int32_t left = r - 32 * pr - 8 * static_cast<int32_t>(t);
-                    if (left > 0 && left < 8) {  // beyond the adapter's rank: not 0 * garbage
+                    for (int32_t pr = 0; 32 * pr < r; ++pr) {
+                        uint4 wv[4];
+                        const int32_t left = r - 32 * pr - 8 * static_cast<int32_t>(t);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            wv[e].x = left >= 2 ? wv[e].x : wv[e].x & 0xffffu;
-                            wv[e].y = left >= 4 ? wv[e].y : (left >= 3 ? wv[e].y & 0xffffu : 0u);
-                            wv[e].z = left >= 6 ? wv[e].z : (left >= 5 ? wv[e].z & 0xffffu : 0u);
-                            wv[e].w = left >= 7 ? wv[e].w & 0xffffu : 0u;
-                        }
-                    }
-                    const uint4* f = s_t + pr * (PARTS * 128) + lane;
-#pragma unroll
-                    for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const uint4 f0 = f[(part * 2 + half) * 64], f1 = f[(part * 2 + half) * 64 + 32];
-                            const uint32_t a0[4] = {f0.x, f0.y, f0.z, f0.w}, a1[4] = {f1.x, f1.y, f1.z, f1.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) mma_bf16_16816(acc[half][e], a0, wv[e].x, wv[e].y);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) mma_bf16_16816(acc[half][e], a1, wv[e].z, wv[e].w);
-                        }
-                }
-                uint8_t* yb = static_cast<uint8_t*>(p.y) + ((m0 + g) * p.N + cbase + static_cast<int64_t>(c) * (kLoraWarps * 32) + 8 * t) * el;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (m0 + g + 8 * i >= p.M) continue;
-                    uint8_t* y = yb + 8 * i * p.N * el;
-                    const int half = i >> 1, k = 2 * (i & 1);
-                    if constexpr (F32) {
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            float4 v = *reinterpret_cast<const float4*>(st + (2 * i + q) * 512);
-                            v.x = __fadd_rn(v.x, acc[half][2 * q][k]);
-                            v.y = __fadd_rn(v.y, acc[half][2 * q][k + 1]);
-                            v.z = __fadd_rn(v.z, acc[half][2 * q + 1][k]);
-                            v.w = __fadd_rn(v.w, acc[half][2 * q + 1][k + 1]);
-                            *reinterpret_cast<float4*>(y + 16 * q) = v;
-                        }
-                    } else {
-                        uint4 v = *reinterpret_cast<const uint4*>(st + i * 512);
-                        uint32_t* u = &v.x;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            u[q] = pack_bf16(__fadd_rn(bf_lo(u[q]), acc[half][q][k]), __fadd_rn(bf_hi(u[q]), acc[half][q][k + 1]));
-                        *reinterpret_cast<uint4*>(y) = v;
-                    }
-                }
-            }
-            cp_wait<0>();
-        }
-    }
-    for (int c = c0; c < chunks; ++c) {
-        const int64_t n0 = cbase + static_cast<int64_t>(c) * kLoraWarps * 32;
-        if (one && n0 >= p.N) break;
-        // this lane's outputs: rows g + 8 i, columns n0 + 8 t + 0 .. 7 (n-tile e: columns 2 e, 2 e + 1)
-        const int64_t nl = n0 + 8 * t;
-        uint32_t bw[4][BW];  // base
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t m = m0 + g + 8 * i;
-#pragma unroll
-            for (int q = 0; q < BW; ++q) bw[i][q] = 0u;
-            if (m < p.M) {
-                const int64_t o = m * p.N + nl;
-                if constexpr (F32) {
-                    const uint32_t* b = static_cast<const uint32_t*>(p.base) + o;
-                    if constexpr (VEC) {
-#pragma unroll
-                        for (int q = 0; q < 8; q += 4)
-                            if (nl + q < p.N) *reinterpret_cast<uint4*>(&bw[i][q]) = *reinterpret_cast<const uint4*>(b + q);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            if (nl + q < p.N) bw[i][q] = b[q];
-                    }
-                } else {
-                    const uint16_t* b = static_cast<const uint16_t*>(p.base) + o;
-                    if constexpr (VEC) {
-                        if (nl < p.N) *reinterpret_cast<uint4*>(&bw[i][0]) = *reinterpret_cast<const uint4*>(b);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            if (nl + q < p.N) bw[i][q / 2] |= static_cast<uint32_t>(b[q]) << (16 * (q & 1));
-                    }
-                }
-            }
-        }
-        float acc[2][4][4] = {};
-        // adds adapter a's part (its t laid out): column of B's fragment n-tile e, index g: n0 + 8 (g / 2) + 2 e + g % 2
-        auto add = [&](int32_t a, int32_t r) {
-            const int64_t n = n0 + 8 * (g >> 1) + (g & 1u);
-            const uint16_t* w = p.b + (static_cast<int64_t>(a) * p.N + n) * p.rmax + 8 * t;
-            const bool whole = n0 + 32 <= p.N;
-            for (int32_t pr = 0; 32 * pr < r; ++pr) {
-                uint4 wv[4];
-                if (whole && 32 * pr + 32 <= r) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) wv[e] = __ldg(reinterpret_cast<const uint4*>(w + 2 * e * p.rmax + 32 * pr));
-                } else {
-                    const int32_t left = r - 32 * pr - 8 * static_cast<int32_t>(t);  // ranks of this lane's piece
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        wv[e] = make_uint4(0u, 0u, 0u, 0u);
-                        if (n + 2 * e < p.N && left > 0) {
-                            wv[e] = __ldg(reinterpret_cast<const uint4*>(w + 2 * e * p.rmax + 32 * pr));
-                            if (left < 8) {  // beyond the adapter's rank: not 0 * garbage
-                                wv[e].x = left >= 2 ? wv[e].x : wv[e].x & 0xffffu;
-                                wv[e].y = left >= 4 ? wv[e].y : (left >= 3 ? wv[e].y & 0xffffu : 0u);
-                                wv[e].z = left >= 6 ? wv[e].z : (left >= 5 ? wv[e].z & 0xffffu : 0u);
-                                wv[e].w = left >= 7 ? wv[e].w & 0xffffu : 0u;
+                            wv[e] = make_uint4(0u, 0u, 0u, 0u);
+                            if constexpr (VEC) {
+                                if (left > 0) wv[e] = *reinterpret_cast<const uint4*>(sw + (2 * e * rmax + 32 * pr) * 2);
+                            } else {
+                                if (left > 0 && n0 + nb + 2 * e < p.N) wv[e] = __ldg(reinterpret_cast<const uint4*>(src + 2 * e * p.rmax + 32 * pr));
                             }
+                            if (left > 0 && left < 8) cut_ranks(wv[e], left);
+                        }
+                        multiply(acc, pr, wv);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int32_t row = static_cast<int32_t>(32 * rh + g) + 8 * i;
+                        if (s_a[row] != a) continue;  // (also rows beyond M)
+                        const int half = i >> 1, k = 2 * (i & 1);
+                        const int64_t o = (m0 + row) * p.N + nl;
+                        if constexpr (!VEC) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                if (nl + q >= p.N) continue;
+                                const float v = acc[half][q >> 1][k + (q & 1)];
+                                if constexpr (F32) static_cast<float*>(p.y)[o + q] = __fadd_rn(static_cast<const float*>(p.base)[o + q], v);
+                                else static_cast<uint16_t*>(p.y)[o + q] =
+                                    static_cast<uint16_t>(pack_bf16(__fadd_rn(bf(static_cast<const uint16_t*>(p.base)[o + q]), v), 0.0f));
+                            }
+                            continue;
+                        }
+                        uint8_t* y = static_cast<uint8_t*>(p.y) + o * EL;
+                        const uint8_t* b = sb + (row * cols + 32 * static_cast<int>(cg) + 8 * static_cast<int>(t)) * EL;
+                        if constexpr (F32) {
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                if (nl + 4 * q >= p.N) continue;
+                                float4 v = *reinterpret_cast<const float4*>(b + 16 * q);
+                                v.x = __fadd_rn(v.x, acc[half][2 * q][k]);
+                                v.y = __fadd_rn(v.y, acc[half][2 * q][k + 1]);
+                                v.z = __fadd_rn(v.z, acc[half][2 * q + 1][k]);
+                                v.w = __fadd_rn(v.w, acc[half][2 * q + 1][k + 1]);
+                                *reinterpret_cast<float4*>(y + 16 * q) = v;
+                            }
+                        } else if (nl < p.N) {
+                            uint4 v = *reinterpret_cast<const uint4*>(b);
+                            uint32_t* u = &v.x;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                u[q] = pack_bf16(__fadd_rn(bf_lo(u[q]), acc[half][q][k]), __fadd_rn(bf_hi(u[q]), acc[half][q][k + 1]));
+                            *reinterpret_cast<uint4*>(y) = v;
                         }
                     }
                 }
-                const uint4* f = s_t + pr * (PARTS * 128) + lane;
-#pragma unroll
-                for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint4 f0 = f[(part * 2 + half) * 64], f1 = f[(part * 2 + half) * 64 + 32];
-                        const uint32_t a0[4] = {f0.x, f0.y, f0.z, f0.w}, a1[4] = {f1.x, f1.y, f1.z, f1.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) mma_bf16_16816(acc[half][e], a0, wv[e].x, wv[e].y);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) mma_bf16_16816(acc[half][e], a1, wv[e].z, wv[e].w);
-                    }
-            }
-        };
-        if (one) {
-            if (first_rank > 0) add(first, first_rank);
-        } else {
-            for (int32_t a = first; a != INT32_MAX; a = next_adapter(mine, a)) {
-                const int32_t r = rank_of(p, a);
-                __syncthreads();
-                lay(a, r);
-                __syncthreads();
-                add(a, r);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t m = m0 + g + 8 * i;
-            if (m >= p.M) continue;
-            const int64_t o = m * p.N + nl;
-            const int half = i >> 1, c0 = 2 * (i & 1);
-            if constexpr (F32) {
-                float* y = static_cast<float*>(p.y) + o;
-                float v[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] = __fadd_rn(__uint_as_float(bw[i][q]), acc[half][q >> 1][c0 + (q & 1)]);
                 if constexpr (VEC) {
-#pragma unroll
-                    for (int q = 0; q < 8; q += 4)
-                        if (nl + q < p.N) *reinterpret_cast<float4*>(y + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (nl + q < p.N) y[q] = v[q];
-                }
-            } else {
-                uint16_t* y = static_cast<uint16_t*>(p.y) + o;
-                uint32_t v[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    v[q] = pack_bf16(__fadd_rn(bf_lo(bw[i][q]), acc[half][q][c0]), __fadd_rn(bf_hi(bw[i][q]), acc[half][q][c0 + 1]));
-                if constexpr (VEC) {
-                    if (nl < p.N) *reinterpret_cast<uint4*>(y) = make_uint4(v[0], v[1], v[2], v[3]);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (nl + q < p.N) y[q] = static_cast<uint16_t>(v[q / 2] >> (16 * (q & 1)));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_empty[used % stages]);
+                    ++used;
                 }
             }
         }
+        w = end;
     }
+    if (!ok && lane == 0) {
+        atomicOr(&s_fault, 1u);
+        atomicOr(p.fault, kLoraFault);
+    }
+    __syncthreads();
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Rows from which the tensor-core tiles are taken (rule: where a 32-row tile
+// Rows from which the tensor-core tiles are taken (rule: where a 64-row tile
 // is worth its pass over the adapters of its rows).
 constexpr int64_t kTileMinRows = 96;
 
@@ -695,16 +714,15 @@ cudaLaunchConfig_t behind(cudaLaunchAttribute* attr, dim3 grid, size_t smem, cud
     return cfg;
 }
 
-cudaError_t expand_ready() {
+constexpr int kExpandSmem = 212 * 1024;  // (beside 10 KB of static shared memory)
+
+cudaError_t expand_ready(int dev) {
     static bool ready[64];  // (concurrent first calls set the same attributes)
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (ready[dev]) return cudaSuccess;
     for (const void* fn : {reinterpret_cast<const void*>(k_lora_expand_tile<true, true>), reinterpret_cast<const void*>(k_lora_expand_tile<true, false>),
                            reinterpret_cast<const void*>(k_lora_expand_tile<false, true>), reinterpret_cast<const void*>(k_lora_expand_tile<false, false>)}) {
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem);
         if (e != cudaSuccess) return e;
     }
     ready[dev] = true;
@@ -757,29 +775,27 @@ int launch_lora(const LoraParams& p, bool out_f32, void* stream) {
         else e = shrink_tile<16>(p, splits, st);
         if (e != cudaSuccess) return static_cast<int>(e);
         const bool vec_y = p.N % (out_f32 ? 4 : 8) == 0 && aligned16(p.base) && aligned16(p.y);
-        const int64_t tiles = (p.M + kTileRows - 1) / kTileRows, cols = (p.N + kLoraWarps * 32 - 1) / (kLoraWarps * 32);
-        // the ring: as many stages (2 to 4) as fit two CTAs on an SM, or else one
-        const int rm = static_cast<int>(p.rmax), tb = expand_t_bytes(out_f32, rm), sb = expand_stage_bytes(out_f32, rm) * kLoraWarps;
-        int stages = 4, per_sm = 2;
-        while (stages > 2 && tb + stages * sb > 110 * 1024) --stages;
-        if (tb + stages * sb > 110 * 1024) {
-            per_sm = 1;
-            stages = 4;
-            while (stages > 2 && tb + stages * sb > 220 * 1024) --stages;
-        }
-        const size_t smem = static_cast<size_t>(tb + stages * sb);
-        // column chunks per CTA: t is laid out once for all of them, as long as there are CTAs for three rounds
-        int64_t chunks = tiles * cols / (3 * 152 * per_sm);
-        chunks = chunks < 1 ? 1 : (chunks > 16 ? 16 : chunks);
-        const int64_t groups = (cols + chunks - 1) / chunks;
-        e = expand_ready();
+        // chunks of 256 columns, or of 128 when two stages of 256 do not fit; then up to four stages
+        const int rm = static_cast<int>(p.rmax), tb = expand_t_bytes(out_f32, rm);
+        const int cols = tb + 2 * expand_stage_bytes(out_f32, rm, 256) <= kExpandSmem ? 256 : 128;
+        int stages = kExpandStages;
+        while (stages > 1 && tb + stages * expand_stage_bytes(out_f32, rm, cols) > kExpandSmem) --stages;
+        const size_t smem = static_cast<size_t>(tb + stages * expand_stage_bytes(out_f32, rm, cols));
+        int dev = 0;
+        e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return static_cast<int>(e);
-        cudaLaunchConfig_t cfg = behind(attr, dim3(static_cast<unsigned>(tiles * groups)), smem, st);
-        const int ch = static_cast<int>(chunks), cg = static_cast<int>(groups);
-        if (out_f32) e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, true>, p, splits, ch, cg, stages)
-                               : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, false>, p, splits, ch, cg, stages);
-        else e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, true>, p, splits, ch, cg, stages)
-                       : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, false>, p, splits, ch, cg, stages);
+        LoraParams q = p;
+        const IqGrids* grids = nullptr;
+        if (const int rc = device_symbols(dev, &q.fault, &grids)) return rc;
+        e = expand_ready(dev);
+        if (e != cudaSuccess) return static_cast<int>(e);
+        const int64_t work = (p.M + kExpandRows - 1) / kExpandRows * ((p.N + cols - 1) / cols);
+        cudaLaunchConfig_t cfg = behind(attr, dim3(static_cast<unsigned>(work < 152 ? work : 152)), smem, st);
+        cfg.blockDim = dim3(kExpandThreads);
+        if (out_f32) e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, true>, q, splits, cols, stages)
+                               : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, false>, q, splits, cols, stages);
+        else e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, true>, q, splits, cols, stages)
+                       : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, false>, q, splits, cols, stages);
         return static_cast<int>(e);
     }
     if (p.nA > 0) {

@@ -104,6 +104,7 @@ struct LoraParams {
     void* y;
     float* t;  // workspace
     int64_t M, K, N, nA, rmax;
+    unsigned int* fault;  // device fault word (set by the launcher)
 };
 size_t lora_workspace_bytes(int64_t M, int64_t rmax, int64_t K);
 int launch_lora(const LoraParams& p, bool out_f32, void* stream);
