@@ -8,7 +8,7 @@
 // a code is read once for all of them.  With few rows the operator is bound
 // by reading the cache: 2 D bytes a token and head.
 //
-// Work.  The unit is 128 tokens of one (request, cache head, row tile).  The
+// Work.  The unit is 256 tokens of one (request, cache head, row tile).  The
 // units of all requests, laid end to end, are divided evenly over the CTAs,
 // whatever the lengths: a CTA finds its share from the lengths (a block scan
 // over the requests) and walks it segment by segment, a segment being its
@@ -17,10 +17,10 @@
 // arrives last joins them in CTA order, so the result does not depend on
 // timing.
 //
-// Inside a CTA each warp takes every eighth tile of 16 tokens.  A tile's
-// codes come through a ring of asynchronous copies in shared memory that is
-// private to the lane which consumes them (the copies only hide latency:
-// nothing is exchanged), are widened to binary16 in registers (exact) and go
+// Inside a CTA each warp takes every eighth pair of tiles of 16 tokens.  Their
+// codes come, K and V by turns, through a ring of asynchronous copies in shared
+// memory that is private to the lane which consumes them (the copies only hide
+// latency: nothing is exchanged), are widened to binary16 in registers (exact) and go
 // through mma.sync m16n8k16 with the tokens on the 16-row side and 8 (or
 // twice 8) query rows on the other: S^T = K Q^T with the head dimension
 // permuted so that a lane's 16-byte copy is its operand, then O^T += V^T P^T
@@ -31,10 +31,10 @@
 // a score passes it by 8 (weights up to 2^8: far from binary16's limit), so
 // most tiles need no exchange between lanes at all.
 //
-// Scales.  K's scale multiplies a tile's scores.  V's scale f * 2^e (f in
-// [1, 2)) joins the exponent, t = s + e, so that the weights 2^(t - m) f
-// which go to binary16 are at most 2 and lose nothing to a V of small scale;
-// the denominator sums 2^(t - m) 2^-e.
+// Scales.  K's scale multiplies a tile's scores; the logarithm of V's joins
+// the exponent, t = s ks + log2(vs), so that the weights 2^(t - m) which go to
+// binary16 lose nothing to a V of small scale; the denominator sums
+// 2^(t - m) / vs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -48,8 +48,9 @@ namespace {
 
 constexpr int kRowWarps = 8;
 constexpr int kRowThreads = kRowWarps * 32;
-constexpr int kRowTile = 16;                       // tokens per warp tile
-constexpr int kRowUnit = kRowWarps * kRowTile;     // tokens per unit of work
+constexpr int kRowTile = 16;                       // tokens per tile (within a block)
+constexpr int kRowPair = 2 * kRowTile;             // tokens per step of a warp
+constexpr int kRowUnit = kRowWarps * kRowPair;     // tokens per unit of work
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -112,8 +113,8 @@ template <int D, int NT>
 struct RowSmem {
     static constexpr int kRows = 8 * NT;
     static constexpr int kCtas = NT * D <= 128 ? 2 : 1;
-    static constexpr int kStages = D == 64 ? 6 : (kCtas == 2 ? 3 : 6);
-    static constexpr int kStage = 2 * kRowTile * D;                          // one warp's K and V tile
+    static constexpr int kStages = D == 64 || kCtas == 1 ? 5 : 3;            // (odd: K and V alternate)
+    static constexpr int kStage = kRowPair * D;                              // one warp's K or V of a pair of tiles
     static constexpr int kRing = kRowWarps * kStages * kStage;
     static constexpr int kMerge = kRowWarps * kRows * (D + 4) * 4;           // one partial per warp
     static constexpr int kBytes = kRing > kMerge ? kRing : kMerge;
@@ -201,52 +202,84 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         const int32_t any_hi = x.kv - x.n + qb + 1, all_hi = x.kv - x.n + qa + 1;
         const int32_t any_lo = p.window > 0 ? all_hi - p.window : 0, all_lo = p.window > 0 ? any_hi - p.window : 0;
 
-        // this warp's tiles: base token x.lo + 16 (8 c + warp), c = ca .. cb - 1
-        int32_t tok = x.lo + ca * kRowUnit + static_cast<int32_t>(warp) * kRowTile;
+        // this warp's pairs: base token x.lo + 32 (8 c + warp), c = ca .. cb - 1
+        int32_t tok = x.lo + ca * kRowUnit + static_cast<int32_t>(warp) * kRowPair;
         const int32_t seg_end = x.lo + cb * kRowUnit;
         const int32_t tok_end = seg_end < any_hi ? seg_end : any_hi;
-        while (tok + kRowTile <= any_lo && tok < tok_end) tok += kRowUnit;
-        const int32_t ntile = tok < tok_end ? (tok_end - tok + kRowUnit - 1) / kRowUnit : 0;
-        const int32_t* table = p.table + r * p.width;
-        // lane i holds the block id (-1: none) of tile 32 b + i
-        auto ids_of = [&](int32_t b) -> int32_t {
-            const int32_t i = 32 * b + static_cast<int32_t>(lane);
-            if (i >= ntile) return -1;
-            const int32_t id = table[(tok + i * kRowUnit) >> bl];
-            return id >= 0 && id < p.c.num_blocks ? id : -1;
+        while (tok + kRowPair <= any_lo && tok < tok_end) tok += kRowUnit;
+        const int32_t npair = tok < tok_end ? (tok_end - tok + kRowUnit - 1) / kRowUnit : 0;
+        // lane 2 i + s: tile s of pair 16 b + i: the offset of its codes (all ones: no such block), its scales
+        struct Lane {
+            uint64_t off;
+            float ks, vs;
         };
-        int32_t ids = ids_of(0), ids_next = -1;
-        auto issue = [&](int32_t i, int32_t id) {  // tile i into stage i % ST
-            if (id >= 0) {
-                const uint64_t unit = static_cast<uint64_t>(id) * p.c.heads + static_cast<uint32_t>(h);
-                const uint64_t off = ((unit << bl) + ((tok + i * kRowUnit) & ((1 << bl) - 1))) * D;
-                const uint8_t* k = p.c.k + off + g * D + t * 16;
-                const uint8_t* v = p.c.v + off + 2 * t * D + g * VB;
-                const uint32_t d = my_ring + static_cast<uint32_t>(i % ST) * Sm::kStage;
+        auto tiles_of = [&](int32_t b) {
+            Lane l{~0ull, 0.0f, 0.0f};
+            const int32_t i = 16 * b + static_cast<int32_t>(lane >> 1);
+            const int32_t tk = tok + i * kRowUnit + static_cast<int32_t>(lane & 1u) * kRowTile;
+            if (i < npair && tk < any_hi && tk + kRowTile > any_lo) {
+                const int32_t id = p.table[r * p.width + (tk >> bl)];
+                if (id >= 0 && id < p.c.num_blocks) {
+                    const uint64_t unit = static_cast<uint64_t>(id) * p.c.heads + static_cast<uint32_t>(h);
+                    l.off = ((unit << bl) + static_cast<uint32_t>(tk & ((1 << bl) - 1))) * D;
+                    l.ks = p.c.ks[unit];
+                    l.vs = p.c.vs[unit];
+                }
+            }
+            return l;
+        };
+        int32_t cur_block = 0;  // `now` holds pairs 16 cur_block .., `then` the next 16
+        Lane now = tiles_of(0), then = tiles_of(1);
+        // copies K (part 0) or V (part 1) of pair i into a ring slot
+        auto issue = [&](int32_t i, int part, uint32_t slot) {
+            if (i < npair) {
+                const bool far = (i >> 4) != (cur_block);
 #pragma unroll
-                for (int a = 0; a < 2; ++a)
+                for (int s = 0; s < 2; ++s) {
+                    const int src = 2 * (i & 15) + s;
+                    const uint32_t lo = __shfl_sync(0xffffffffu, static_cast<uint32_t>(far ? then.off : now.off), src);
+                    const uint32_t hi = __shfl_sync(0xffffffffu, static_cast<uint32_t>((far ? then.off : now.off) >> 32), src);
+                    if (hi == 0xffffffffu) continue;
+                    const uint64_t off = (static_cast<uint64_t>(hi) << 32) | lo;
+                    if (part == 0) {
+                        const uint8_t* k = p.c.k + off + g * D + t * 16;
+                        const uint32_t d = slot + s * (2 * KC * 512);
 #pragma unroll
-                    for (int c = 0; c < KC; ++c) cp_async16(d + (a * KC + c) * 512, k + a * 8 * D + c * 64);
+                        for (int a = 0; a < 2; ++a)
 #pragma unroll
-                for (int a = 0; a < 4; ++a) {  // tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-                    const uint8_t* src = v + ((a >> 1) * 8 + (a & 1)) * D;
-                    if constexpr (D == 128) cp_async16(d + (2 * KC + a) * 512, src);
-                    else cp_async8(d + 2 * KC * 512 + a * 256 - lane * 8, src);
+                            for (int c = 0; c < KC; ++c) cp_async16(d + (a * KC + c) * 512, k + a * 8 * D + c * 64);
+                    } else {
+                        const uint8_t* v = p.c.v + off + 2 * t * D + g * VB;
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {  // tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+                            const uint8_t* from = v + ((a >> 1) * 8 + (a & 1)) * D;
+                            if constexpr (D == 128) cp_async16(slot + (s * 4 + a) * 512, from);
+                            else cp_async8(slot + (s * 4 + a) * 256 - lane * 8, from);
+                        }
+                    }
                 }
             }
             cp_commit();
         };
+        // the ring position of K of pair i is 2 i, of V 2 i + 1; slots are taken in turn
+        auto next_slot = [&](uint32_t slot) { return slot + Sm::kStage == my_ring + ST * Sm::kStage ? my_ring : slot + Sm::kStage; };
+        uint32_t put = my_ring, get = my_ring;
 #pragma unroll
-        for (int i = 0; i < ST - 1; ++i) issue(i, __shfl_sync(0xffffffffu, ids, i));
-        float ks_l = 0.0f, vs_l = 0.0f;  // lane i: the scales of tile 32 b + i
-        auto scales_of = [&](int32_t id) {
-            if (id >= 0) {
-                const uint64_t unit = static_cast<uint64_t>(id) * p.c.heads + static_cast<uint32_t>(h);
-                ks_l = p.c.ks[unit];
-                vs_l = p.c.vs[unit];
-            }
+        for (int n = 0; n < ST - 1; ++n) {
+            issue(n >> 1, n & 1, put);
+            put = next_slot(put);
+        }
+        // lane i: K's scale, log2 of V's and its reciprocal (V of scale 0: its codes are taken as zeros)
+        float ks_l, ve_l, vinv_l;
+        auto scales = [&]() {
+            float f, e, inv, lg;
+            split_scale(now.vs, f, e, inv);
+            asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(now.vs == 0.0f ? 1.0f : f));
+            ks_l = now.ks;
+            ve_l = e + lg;
+            vinv_l = now.vs == 0.0f ? 1.0f : __fdividef(1.0f, now.vs);
         };
-        scales_of(ids);
+        scales();
 
         uint32_t qf[NT][KS][2];
         float frow[NT][2];  // rows 8 nt + 2 t and + 1: what turns a sum of products into a base-2 score, but for K's scale
@@ -303,45 +336,69 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                 ms[nt][e] = sum[nt][e] = 0.0f;
             }
 
-        for (int32_t i = 0; i < ntile; ++i) {
-            const int32_t i32 = i & 31;
-            if (i32 == 0) {
-                if (i > 0) {
-                    ids = ids_next;
-                    scales_of(ids);
-                }
-                ids_next = ids_of((i >> 5) + 1);
+        for (int32_t i = 0; i < npair; ++i) {
+            if ((i & 15) == 0 && i > 0) {
+                now = then;
+                cur_block = i >> 4;
+                then = tiles_of(cur_block + 1);
+                scales();
             }
-            {
-                const int32_t q = i + ST - 1;
-                issue(q, __shfl_sync(0xffffffffu, (q >> 5) == (i >> 5) ? ids : ids_next, q & 31));
+            issue(i + (ST - 1) / 2, 0, put);
+            put = next_slot(put);
+            // the two tiles' constants
+            float ks[2], ve[2], vinv[2];
+            bool live[2], zero[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int src = 2 * (i & 15) + s;
+                live[s] = __shfl_sync(0xffffffffu, static_cast<uint32_t>(now.off >> 32), src) != 0xffffffffu;
+                ks[s] = __shfl_sync(0xffffffffu, ks_l, src);
+                ve[s] = __shfl_sync(0xffffffffu, ve_l, src);
+                vinv[s] = __shfl_sync(0xffffffffu, vinv_l, src);
+                zero[s] = __shfl_sync(0xffffffffu, now.vs, src) == 0.0f;
             }
             cp_wait<ST - 1>();
-            if (__shfl_sync(0xffffffffu, ids, i32) < 0) continue;
-            const float ks = __shfl_sync(0xffffffffu, ks_l, i32);
-            float vf, ve, vinv;
-            split_scale(__shfl_sync(0xffffffffu, vs_l, i32), vf, ve, vinv);
-            const uint32_t d = my_ring + static_cast<uint32_t>(i % ST) * Sm::kStage;
-            // scores: sc[nt][0..1] token g, rows 2 t, 2 t + 1; [2..3] token g + 8
-            float sc[NT][4];
+            // scores: sc[s][nt][0..1] token g of tile s, rows 2 t, 2 t + 1; [2..3] token g + 8
+            float sc[2][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) sc[s][nt][0] = sc[s][nt][1] = sc[s][nt][2] = sc[s][nt][3] = 0.0f;
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
-                const uint4 w0 = lds128(d + c * 512), w1 = lds128(d + (KC + c) * 512);
-                const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+                uint4 w[2][2];
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    uint32_t a[4];
-                    widen4<E4M3>(x0[s], a[0], a[2]);
-                    widen4<E4M3>(x1[s], a[1], a[3]);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], a, qf[nt][c * 4 + s][0], qf[nt][c * 4 + s][1]);
+                for (int s = 0; s < 2; ++s) {
+                    w[s][0] = lds128(get + (s * 2 * KC + c) * 512);
+                    w[s][1] = lds128(get + (s * 2 * KC + KC + c) * 512);
                 }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t x0 = k == 0 ? w[s][0].x : k == 1 ? w[s][0].y : k == 2 ? w[s][0].z : w[s][0].w;
+                        const uint32_t x1 = k == 0 ? w[s][1].x : k == 1 ? w[s][1].y : k == 2 ? w[s][1].z : w[s][1].w;
+                        uint32_t a[4];
+                        widen4<E4M3>(x0, a[0], a[2]);
+                        widen4<E4M3>(x1, a[1], a[3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816(sc[s][nt], a, qf[nt][c * 4 + k][0], qf[nt][c * 4 + k][1]);
+                    }
             }
+            get = next_slot(get);
+            issue(i + (ST - 1) / 2, 1, put);
+            put = next_slot(put);
             const int32_t tb = tok + i * kRowUnit;
-            const bool masked = tb + kRowTile > all_hi || tb < all_lo;
-            uint32_t hidden = 0u;  // bit 4 nt + e: score e is not seen
+            const bool masked = tb + kRowPair > all_hi || tb < all_lo || !live[0] || !live[1];
+            // exponents relative to the running maximum
+            float ex[2][NT][4];
+            bool grow = false;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ex[s][nt][e] = __fmaf_rn(sc[s][nt][e], frow[nt][e & 1] * ks[s], ve[s] - ms[nt][e & 1]);
             if (masked) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -349,34 +406,32 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                     for (int e = 0; e < 2; ++e) {
                         int32_t lo, hi;
                         sees(8 * nt + 2 * static_cast<int32_t>(t) + e, lo, hi);
-                        const int32_t pos = tb + static_cast<int32_t>(g);
-                        if (pos < lo || pos >= hi) hidden |= 1u << (4 * nt + e);
-                        if (pos + 8 < lo || pos + 8 >= hi) hidden |= 4u << (4 * nt + e);
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const int32_t pos = tb + s * kRowTile + static_cast<int32_t>(g);
+                            if (pos < lo || pos >= hi || !live[s]) ex[s][nt][e] = -INFINITY;
+                            if (pos + 8 < lo || pos + 8 >= hi || !live[s]) ex[s][nt][e + 2] = -INFINITY;
+                        }
                     }
             }
-            // exponents relative to the running maximum
-            float ex[NT][4];
-            bool grow = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float y = __fmaf_rn(sc[nt][e], frow[nt][e & 1] * ks, ve - ms[nt][e & 1]);
-                    ex[nt][e] = (hidden >> (4 * nt + e)) & 1u ? -INFINITY : y;
-                    grow |= ex[nt][e] > (mx[nt][e & 1] == -INFINITY ? -INFINITY : 8.0f);
+                for (int e = 0; e < 2; ++e) {
+                    const float top = fmaxf(fmaxf(ex[0][nt][e], ex[0][nt][e + 2]), fmaxf(ex[1][nt][e], ex[1][nt][e + 2]));
+                    grow |= top > (mx[nt][e] == -INFINITY ? -INFINITY : 8.0f);
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float tm = fmaxf(ex[nt][e], ex[nt][e + 2]);
+                        float tm = fmaxf(fmaxf(ex[0][nt][e], ex[0][nt][e + 2]), fmaxf(ex[1][nt][e], ex[1][nt][e + 2]));
                         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 4));
                         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 8));
                         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
                         // (relative to ms: the new maximum is ms + tm where it grew)
                         if (mx[nt][e] == -INFINITY ? tm > -INFINITY : tm > 0.0f) {
-                            const float mn = ms[nt][e] + tm;
                             const float al = mx[nt][e] == -INFINITY ? 0.0f : exp2_fast(-tm);
                             sum[nt][e] *= al;
 #pragma unroll
@@ -384,102 +439,116 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                                 o[nt][s][e] *= al;
                                 o[nt][s][e + 2] *= al;
                             }
-                            ex[nt][e] -= tm;
-                            ex[nt][e + 2] -= tm;
-                            mx[nt][e] = ms[nt][e] = mn;
-                        }
-                    }
-            }
-            uint32_t pf[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float p0 = exp2_fast(ex[nt][0]), p1 = exp2_fast(ex[nt][1]);
-                const float p2 = exp2_fast(ex[nt][2]), p3 = exp2_fast(ex[nt][3]);
-                sum[nt][0] = __fmaf_rn(p0 + p2, vinv, sum[nt][0]);
-                sum[nt][1] = __fmaf_rn(p1 + p3, vinv, sum[nt][1]);
-                pf[nt][0] = transpose8x8(pack_half2(p0 * vf, p1 * vf));
-                pf[nt][1] = transpose8x8(pack_half2(p2 * vf, p3 * vf));
-            }
-            // O^T += V^T P^T
-            uint32_t vw[4][VB / 4];
-#pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                if constexpr (D == 128) {
-                    const uint4 w = lds128(d + (2 * KC + a) * 512);
-                    vw[a][0] = w.x;
-                    vw[a][1] = w.y;
-                    vw[a][2] = w.z;
-                    vw[a][3] = w.w;
-                } else {
-                    const uint2 w = lds64(d + 2 * KC * 512 + a * 256 - lane * 8);
-                    vw[a][0] = w.x;
-                    vw[a][1] = w.y;
-                }
-            }
-            if (masked) {
-                // a token that no row sees contributes nothing, whatever it
-                // holds; one that only some rows see may hold NaN codes
-                bool odd = false;
-#pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    const int32_t pos = tb + (a >> 1) * 8 + 2 * static_cast<int32_t>(t) + (a & 1);
-                    const bool dead = pos >= any_hi || pos < any_lo;
-#pragma unroll
-                    for (int w = 0; w < VB / 4; ++w) {
-                        if (dead) vw[a][w] = 0u;
-                        if constexpr (E4M3) odd |= nan_bytes(vw[a][w]) != 0u;
-                    }
-                }
-                if (E4M3 && __any_sync(0xffffffffu, odd)) {
-                    // NaN codes count only for the rows that see them: a product of
-                    // "is NaN" with "sees" marks those outputs, the codes become 0
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        int32_t lo, hi;
-                        sees(8 * nt + static_cast<int32_t>(g), lo, hi);
-                        uint32_t seen[2];
-#pragma unroll
-                        for (int a = 0; a < 2; ++a) {
-                            const int32_t pos = tb + a * 8 + 2 * static_cast<int32_t>(t);
-                            seen[a] = (pos >= lo && pos < hi ? 0x3c00u : 0u) | (pos + 1 >= lo && pos + 1 < hi ? 0x3c000000u : 0u);
-                        }
-#pragma unroll
-                        for (int s = 0; s < KS; ++s) {
-                            uint32_t n[4];  // [position 2 s, 2 s + 1 of the lane's bytes] x [tokens 2 t.., 2 t + 8..]
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int byte = 2 * s + (e & 1), w = byte >> 2, sh = 8 * (byte & 3) + 7, a = e & 2;
-                                n[e] = ((nan_bytes(vw[a][w]) >> sh) & 1u) * 0x3c00u | ((nan_bytes(vw[a + 1][w]) >> sh) & 1u) * 0x3c000000u;
+                            for (int s = 0; s < 2; ++s) {
+                                ex[s][nt][e] -= tm;
+                                ex[s][nt][e + 2] -= tm;
                             }
-                            float cnt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma16816(cnt, n, seen[0], seen[1]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (cnt[e] > 0.0f) o[nt][s][e] = __int_as_float(0x7fffffff);
+                            mx[nt][e] = ms[nt][e] = ms[nt][e] + tm;
                         }
                     }
-#pragma unroll
-                    for (int a = 0; a < 4; ++a)
-#pragma unroll
-                        for (int w = 0; w < VB / 4; ++w) vw[a][w] &= ~((nan_bytes(vw[a][w]) >> 7) * 0xffu);
-                }
             }
+            uint32_t pf[2][NT][2];
 #pragma unroll
-            for (int w = 0; w < VB / 4; ++w) {
-                // (token, next token) pairs of the word's four head positions
-                const uint32_t x01 = __byte_perm(vw[0][w], vw[1][w], 0x5140), y01 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-                const uint32_t x23 = __byte_perm(vw[2][w], vw[3][w], 0x5140), y23 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-                uint32_t a0[4], a1[4];
-                widen4<E4M3>(x01, a0[0], a0[1]);
-                widen4<E4M3>(x23, a0[2], a0[3]);
-                widen4<E4M3>(y01, a1[0], a1[1]);
-                widen4<E4M3>(y23, a1[2], a1[3]);
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma16816(o[nt][2 * w], a0, pf[nt][0], pf[nt][1]);
-                    mma16816(o[nt][2 * w + 1], a1, pf[nt][0], pf[nt][1]);
+                    const float p0 = exp2_fast(ex[s][nt][0]), p1 = exp2_fast(ex[s][nt][1]);
+                    const float p2 = exp2_fast(ex[s][nt][2]), p3 = exp2_fast(ex[s][nt][3]);
+                    sum[nt][0] = __fmaf_rn(p0 + p2, vinv[s], sum[nt][0]);
+                    sum[nt][1] = __fmaf_rn(p1 + p3, vinv[s], sum[nt][1]);
+                    pf[s][nt][0] = transpose8x8(pack_half2(p0, p1));
+                    pf[s][nt][1] = transpose8x8(pack_half2(p2, p3));
+                }
+            // O^T += V^T P^T
+            cp_wait<ST - 1>();
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                uint32_t vw[4][VB / 4];
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    if constexpr (D == 128) {
+                        const uint4 w = lds128(get + (s * 4 + a) * 512);
+                        vw[a][0] = w.x;
+                        vw[a][1] = w.y;
+                        vw[a][2] = w.z;
+                        vw[a][3] = w.w;
+                    } else {
+                        const uint2 w = lds64(get + (s * 4 + a) * 256 - lane * 8);
+                        vw[a][0] = w.x;
+                        vw[a][1] = w.y;
+                    }
+                }
+                if (masked || zero[s]) {
+                    // a token that no row sees contributes nothing, whatever it
+                    // holds; one that only some rows see may hold NaN codes
+                    bool odd = false;
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) {
+                        const int32_t pos = tb + s * kRowTile + (a >> 1) * 8 + 2 * static_cast<int32_t>(t) + (a & 1);
+                        const bool dead = pos >= any_hi || pos < any_lo || !live[s] || zero[s];
+#pragma unroll
+                        for (int w = 0; w < VB / 4; ++w) {
+                            if (dead) vw[a][w] = 0u;
+                            if constexpr (E4M3) odd |= nan_bytes(vw[a][w]) != 0u;
+                        }
+                    }
+                    if (E4M3 && __any_sync(0xffffffffu, odd)) {
+                        // NaN codes count only for the rows that see them: a product of
+                        // "is NaN" with "sees" marks those outputs, the codes become 0
+#pragma unroll 1
+                        for (int nt = 0; nt < NT; ++nt) {
+                            int32_t lo, hi;
+                            sees(8 * nt + static_cast<int32_t>(g), lo, hi);
+                            uint32_t seen[2];
+#pragma unroll
+                            for (int a = 0; a < 2; ++a) {
+                                const int32_t pos = tb + s * kRowTile + a * 8 + 2 * static_cast<int32_t>(t);
+                                seen[a] = (pos >= lo && pos < hi ? 0x3c00u : 0u) | (pos + 1 >= lo && pos + 1 < hi ? 0x3c000000u : 0u);
+                            }
+#pragma unroll
+                            for (int m = 0; m < KS; ++m) {
+                                uint32_t n[4];  // [position 2 m, 2 m + 1 of the lane's bytes] x [tokens 2 t.., 2 t + 8..]
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int byte = 2 * m + (e & 1), w = byte >> 2, sh = 8 * (byte & 3) + 7, a = e & 2;
+                                    n[e] = ((nan_bytes(vw[a][w]) >> sh) & 1u) * 0x3c00u | ((nan_bytes(vw[a + 1][w]) >> sh) & 1u) * 0x3c000000u;
+                                }
+                                float cnt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                mma16816(cnt, n, seen[0], seen[1]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (cnt[e] > 0.0f) {
+#pragma unroll
+                                        for (int q = 0; q < NT; ++q)
+                                            if (q == nt) o[q][m][e] = __int_as_float(0x7fffffff);
+                                    }
+                            }
+                        }
+#pragma unroll
+                        for (int a = 0; a < 4; ++a)
+#pragma unroll
+                            for (int w = 0; w < VB / 4; ++w) vw[a][w] &= ~((nan_bytes(vw[a][w]) >> 7) * 0xffu);
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < VB / 4; ++w) {
+                    // (token, next token) pairs of the word's four head positions
+                    const uint32_t x01 = __byte_perm(vw[0][w], vw[1][w], 0x5140), y01 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+                    const uint32_t x23 = __byte_perm(vw[2][w], vw[3][w], 0x5140), y23 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+                    uint32_t a0[4], a1[4];
+                    widen4<E4M3>(x01, a0[0], a0[1]);
+                    widen4<E4M3>(x23, a0[2], a0[3]);
+                    widen4<E4M3>(y01, a1[0], a1[1]);
+                    widen4<E4M3>(y23, a1[2], a1[3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma16816(o[nt][2 * w], a0, pf[s][nt][0], pf[s][nt][1]);
+                        mma16816(o[nt][2 * w + 1], a1, pf[s][nt][0], pf[s][nt][1]);
+                    }
                 }
             }
+            get = next_slot(get);
         }
         cp_wait<0>();
 #pragma unroll
