@@ -18,9 +18,8 @@
 // timing.
 //
 // Inside a CTA each warp takes every eighth pair of tiles of 16 tokens.  Their
-// codes come, K and V by turns, through a ring of asynchronous copies in shared
-// memory that is private to the lane which consumes them (the copies only hide
-// latency: nothing is exchanged), are widened to binary16 in registers (exact) and go
+// codes come, K and V by turns, through the warp's own ring in shared memory,
+// one bulk copy for a tile (16 tokens of a head lie together), and are widened to binary16 in registers (exact) and go
 // through mma.sync m16n8k16 with the tokens on the 16-row side and 8 (or
 // twice 8) query rows on the other: S^T = K Q^T with the head dimension
 // permuted so that a lane's 16-byte copy is its operand, then O^T += V^T P^T
@@ -42,6 +41,7 @@
 #include <cstdint>
 
 #include "ndq_attn.cuh"
+#include "ndq_device.cuh"
 
 namespace ndq {
 namespace {
@@ -51,18 +51,7 @@ constexpr int kRowThreads = kRowWarps * 32;
 constexpr int kRowTile = 16;                       // tokens per tile (within a block)
 constexpr int kRowPair = 2 * kRowTile;             // tokens per step of a warp
 constexpr int kRowUnit = kRowWarps * kRowPair;     // tokens per unit of work
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+constexpr uint32_t kRowFault = 4u;                 // bit of the device fault word
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -139,8 +128,12 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
     __shared__ int64_t s_r, s_base;
     __shared__ float s_m[kRowWarps][kRows], s_l[kRowWarps][kRows];
     __shared__ uint32_t s_last;
+    __shared__ uint64_t s_bar[kRowWarps][ST];  // a ring slot's copies have landed
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
     const int bl = p.c.bs_log2;
+
+    if (lane < ST) mbar_init(&s_bar[warp][lane], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
     // this CTA's share of the units
     uint64_t mine = 0;
@@ -179,7 +172,10 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
     int64_t r = s_r;
     uint64_t base = static_cast<uint64_t>(s_base);  // first unit of request r
 
-    const uint32_t my_ring = smem_u32(ring) + warp * ST * Sm::kStage + lane * 16;
+    const uint32_t my_ring = smem_u32(ring) + warp * ST * Sm::kStage;
+    // the ring goes on from segment to segment: slot and phase of the next copy and of the next to be read
+    uint32_t put = 0, get = 0, get_phase = 0, flying = 0;
+    bool ok = true;  // false once a wait ran out: nothing more is copied or read
     while (u < u_end) {
         const Req x = request<kRows>(p, r);
         const uint64_t ru = static_cast<uint64_t>(x.tiles) * p.c.heads * x.units;
@@ -230,45 +226,34 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         };
         int32_t cur_block = 0;  // `now` holds pairs 16 cur_block .., `then` the next 16
         Lane now = tiles_of(0), then = tiles_of(1);
-        // copies K (part 0) or V (part 1) of pair i into a ring slot
-        auto issue = [&](int32_t i, int part, uint32_t slot) {
-            if (i < npair) {
-                const bool far = (i >> 4) != (cur_block);
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int src = 2 * (i & 15) + s;
-                    const uint32_t lo = __shfl_sync(0xffffffffu, static_cast<uint32_t>(far ? then.off : now.off), src);
-                    const uint32_t hi = __shfl_sync(0xffffffffu, static_cast<uint32_t>((far ? then.off : now.off) >> 32), src);
-                    if (hi == 0xffffffffu) continue;
-                    const uint64_t off = (static_cast<uint64_t>(hi) << 32) | lo;
-                    if (part == 0) {
-                        const uint8_t* k = p.c.k + off + g * D + t * 16;
-                        const uint32_t d = slot + s * (2 * KC * 512);
-#pragma unroll
-                        for (int a = 0; a < 2; ++a)
-#pragma unroll
-                            for (int c = 0; c < KC; ++c) cp_async16(d + (a * KC + c) * 512, k + a * 8 * D + c * 64);
-                    } else {
-                        const uint8_t* v = p.c.v + off + 2 * t * D + g * VB;
-#pragma unroll
-                        for (int a = 0; a < 4; ++a) {  // tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-                            const uint8_t* from = v + ((a >> 1) * 8 + (a & 1)) * D;
-                            if constexpr (D == 128) cp_async16(slot + (s * 4 + a) * 512, from);
-                            else cp_async8(slot + (s * 4 + a) * 256 - lane * 8, from);
-                        }
-                    }
-                }
-            }
-            cp_commit();
+        // copies K (part 0) or V (part 1) of pair i into the next ring slot, which every lane has read
+        auto issue = [&](int32_t i, int part) {
+            if (i >= npair || !ok) return;
+            const uint64_t off = (i >> 4) != cur_block ? then.off : now.off;
+            const bool mine = static_cast<int32_t>(lane >> 1) == (i & 15) && off != ~0ull;
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));  // (also: every lane is here)
+            if (lane == 0) mbar_arrive_expect_tx(&s_bar[warp][put], n * static_cast<uint32_t>(kRowTile * D));
+            __syncwarp();
+            if (mine)
+                bulk_load(ring + (warp * ST + put) * Sm::kStage + (lane & 1u) * (kRowTile * D), (part ? p.c.v : p.c.k) + off, kRowTile * D,
+                          &s_bar[warp][put]);
+            put = put + 1 == ST ? 0 : put + 1;
+            ++flying;
         };
-        // the ring position of K of pair i is 2 i, of V 2 i + 1; slots are taken in turn
-        auto next_slot = [&](uint32_t slot) { return slot + Sm::kStage == my_ring + ST * Sm::kStage ? my_ring : slot + Sm::kStage; };
-        uint32_t put = my_ring, get = my_ring;
+        // waits for the next slot; its address
+        auto arrived = [&]() -> uint32_t {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_bar[warp][get], get_phase));
+            return my_ring + get * Sm::kStage;
+        };
+        auto taken = [&]() {
+            --flying;
+            if (++get == ST) {
+                get = 0;
+                get_phase ^= 1u;
+            }
+        };
 #pragma unroll
-        for (int n = 0; n < ST - 1; ++n) {
-            issue(n >> 1, n & 1, put);
-            put = next_slot(put);
-        }
+        for (int n = 0; n < ST - 1; ++n) issue(n >> 1, n & 1);
         // lane i: K's scale, log2 of V's and its reciprocal (V of scale 0: its codes are taken as zeros)
         float ks_l, ve_l, vinv_l;
         auto scales = [&]() {
@@ -343,8 +328,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                 then = tiles_of(cur_block + 1);
                 scales();
             }
-            issue(i + (ST - 1) / 2, 0, put);
-            put = next_slot(put);
+            issue(i + (ST - 1) / 2, 0);
             // the two tiles' constants
             float ks[2], ve[2], vinv[2];
             bool live[2], zero[2];
@@ -357,7 +341,8 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                 vinv[s] = __shfl_sync(0xffffffffu, vinv_l, src);
                 zero[s] = __shfl_sync(0xffffffffu, now.vs, src) == 0.0f;
             }
-            cp_wait<ST - 1>();
+            const uint32_t kat = arrived() + g * D + t * 16;
+            if (!ok) break;
             // scores: sc[s][nt][0..1] token g of tile s, rows 2 t, 2 t + 1; [2..3] token g + 8
             float sc[2][NT][4];
 #pragma unroll
@@ -369,8 +354,8 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                 uint4 w[2][2];
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    w[s][0] = lds128(get + (s * 2 * KC + c) * 512);
-                    w[s][1] = lds128(get + (s * 2 * KC + KC + c) * 512);
+                    w[s][0] = lds128(kat + s * kRowTile * D + c * 64);
+                    w[s][1] = lds128(kat + (s * kRowTile + 8) * D + c * 64);
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -385,9 +370,8 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                         for (int nt = 0; nt < NT; ++nt) mma16816(sc[s][nt], a, qf[nt][c * 4 + k][0], qf[nt][c * 4 + k][1]);
                     }
             }
-            get = next_slot(get);
-            issue(i + (ST - 1) / 2, 1, put);
-            put = next_slot(put);
+            taken();
+            issue(i + (ST - 1) / 2, 1);
             const int32_t tb = tok + i * kRowUnit;
             const bool masked = tb + kRowPair > all_hi || tb < all_lo || !live[0] || !live[1];
             // exponents relative to the running maximum
@@ -461,20 +445,21 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                     pf[s][nt][1] = transpose8x8(pack_half2(p2, p3));
                 }
             // O^T += V^T P^T
-            cp_wait<ST - 1>();
+            const uint32_t vat = arrived() + 2 * t * D + g * VB;
+            if (!ok) break;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 uint32_t vw[4][VB / 4];
 #pragma unroll
                 for (int a = 0; a < 4; ++a) {
                     if constexpr (D == 128) {
-                        const uint4 w = lds128(get + (s * 4 + a) * 512);
+                        const uint4 w = lds128(vat + (s * kRowTile + (a >> 1) * 8 + (a & 1)) * D);
                         vw[a][0] = w.x;
                         vw[a][1] = w.y;
                         vw[a][2] = w.z;
                         vw[a][3] = w.w;
                     } else {
-                        const uint2 w = lds64(get + (s * 4 + a) * 256 - lane * 8);
+                        const uint2 w = lds64(vat + (s * kRowTile + (a >> 1) * 8 + (a & 1)) * D);
                         vw[a][0] = w.x;
                         vw[a][1] = w.y;
                     }
@@ -548,9 +533,15 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                     }
                 }
             }
-            get = next_slot(get);
+            taken();
         }
-        cp_wait<0>();
+        if (!ok) {  // what is still in flight lands before the ring is used for anything else
+            if (lane == 0) atomicOr(p.fault, kRowFault);
+            while (flying > 0) {
+                mbar_wait_bounded(&s_bar[warp][get], get_phase);
+                taken();
+            }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -653,7 +644,8 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
             if (p.lse && d0 == 0)
                 p.lse[at] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : (L == L ? -INFINITY : L);
         }
-        __syncthreads();  // s_m, s_l, the ring and s_last are free again
+        fence_proxy_async_smem();  // (the ring was written and read by threads; copies come next)
+        __syncthreads();           // s_m, s_l, the ring and s_last are free again
         u += static_cast<uint64_t>(cb - ca);
     }
 }
@@ -698,6 +690,8 @@ int launch_attention(AttnParams p, int head_dim, bool e4m3, bool bf16, void* str
     }
     const int sms = sms_of[dev];
     if (p.max_q > p.n_tokens) p.max_q = p.n_tokens;
+    const IqGrids* grids = nullptr;
+    if (const int rc = device_symbols(dev, &p.fault, &grids)) return rc;
     // Requests with more than 16 rows go to the prompt kernel, which is not
     // launched when there can be none; the others to this one.  (The host does
     // not know the lengths, so this one always runs.)

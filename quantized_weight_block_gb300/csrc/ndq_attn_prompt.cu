@@ -805,9 +805,6 @@ int launch_typed(const AttnParams& p, unsigned grid, int dev, void* stream) {
 }  // namespace
 
 int launch_attention_prompt(AttnParams p, int head_dim, bool e4m3, bool bf16, int dev, int sms, void* stream) {
-    const IqGrids* grids = nullptr;
-    int e = device_symbols(dev, &p.fault, &grids);
-    if (e != 0) return e;
     // units at most: a request's last unit may be partial, and has at least prompt_rows rows
     const int64_t rows = p.n_tokens * p.group;
     const int64_t reqs = rows / p.prompt_rows < p.n_req ? rows / p.prompt_rows : p.n_req;
