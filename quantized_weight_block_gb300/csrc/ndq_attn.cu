@@ -71,6 +71,11 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     return v;
 }
 
+// a / b: the 32-bit division where it will do (the 64-bit one takes hundreds of cycles).
+__device__ __forceinline__ uint64_t udiv(uint64_t a, uint64_t b) {
+    return ((a | b) >> 32) != 0 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+
 // What a CTA knows of one request.
 struct Req {
     int64_t q0;    // its first query row
@@ -80,6 +85,11 @@ struct Req {
     int32_t units; // units of one row tile (at least one, so that empty rows are written)
     int32_t tiles; // row tiles per cache head
 };
+
+// The query of a row: the group is a power of two more often than not.
+__device__ __forceinline__ int32_t query_of(const AttnParams& p, int32_t row) {
+    return p.group_shift >= 0 ? row >> p.group_shift : row / p.group;
+}
 
 template <int ROWS>
 __device__ __forceinline__ Req request(const AttnParams& p, int64_t r) {
@@ -122,7 +132,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
     constexpr int KS = D / 16;       // k-steps of a score, m-tiles of a head
     constexpr int KC = D / 64;       // 16-byte pieces of a token's K per lane
     constexpr int VB = D / 8;        // bytes of a token's V per lane
-    constexpr uint64_t kSlot = kAttnRows * (D + 2);  // attn_slot_floats(D)
+    constexpr uint64_t kSlot = NDQ_ROWS_SLOT(D);
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ uint64_t s_sum[kRowWarps];
     __shared__ int64_t s_r, s_base;
@@ -135,42 +145,78 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
     if (lane < ST) mbar_init(&s_bar[warp][lane], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
-    // this CTA's share of the units
-    uint64_t mine = 0;
-    const int64_t per = (p.n_req + kRowThreads - 1) / kRowThreads;
-    for (int64_t i = 0; i < per; ++i) {
-        const int64_t r = tid * per + i;
-        if (r < p.n_req) {
-            const Req x = request<kRows>(p, r);
-            mine += static_cast<uint64_t>(x.tiles) * p.c.heads * x.units;
+    // this CTA's share of the units: the units of requests 0, 1, ... end to end
+    uint64_t total = 0, base = 0, u = 0, u_end = 0, ctas = 0;  // base: first unit of request r
+    int64_t r = 0;
+    auto share = [&]() {  // false: none
+        ctas = gridDim.x < total ? gridDim.x : total;
+        if (blockIdx.x >= ctas) return false;
+        const uint64_t q = udiv(total, ctas);
+        const uint32_t rem = static_cast<uint32_t>(total - q * ctas), n = static_cast<uint32_t>(ctas);
+        u = q * blockIdx.x + rem * blockIdx.x / n;  // total * b / ctas
+        u_end = q * (blockIdx.x + 1) + rem * (blockIdx.x + 1) / n;
+        return true;
+    };
+    bool some = true;
+    if (p.n_req <= 32) {  // every warp for itself
+        uint64_t mine = 0;
+        if (lane < p.n_req) {
+            const Req x = request<kRows>(p, lane);
+            mine = static_cast<uint64_t>(x.tiles) * p.c.heads * x.units;
+        }
+        uint64_t incl = mine;
+#pragma unroll
+        for (uint32_t d = 1; d < 32; d <<= 1) {
+            if (d >= p.n_req) break;
+            const uint64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += y;
+        }
+        total = __shfl_sync(0xffffffffu, incl, static_cast<int>(p.n_req) - 1);
+        some = share();
+        if (some) {
+            r = __ffs(__ballot_sync(0xffffffffu, lane < p.n_req && u < incl)) - 1;
+            base = __shfl_sync(0xffffffffu, incl - mine, static_cast<int>(r));
+        }
+        __syncthreads();  // (the barriers of the ring are initialised)
+    } else {
+        uint64_t mine = 0;
+        const int64_t per = (p.n_req + kRowThreads - 1) / kRowThreads;
+        for (int64_t i = 0; i < per; ++i) {
+            const int64_t q = tid * per + i;
+            if (q < p.n_req) {
+                const Req x = request<kRows>(p, q);
+                mine += static_cast<uint64_t>(x.tiles) * p.c.heads * x.units;
+            }
+        }
+        uint64_t incl = mine;
+#pragma unroll
+        for (uint32_t d = 1; d < 32; d <<= 1) {
+            const uint64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += y;
+        }
+        if (lane == 31u) s_sum[warp] = incl;
+        __syncthreads();
+        uint64_t before = incl - mine;
+#pragma unroll
+        for (uint32_t w = 0; w < kRowWarps; ++w) {
+            if (w < warp) before += s_sum[w];
+            total += s_sum[w];
+        }
+        some = share();
+        if (some) {  // (uniform)
+            if (before <= u && u < before + mine) {
+                s_r = tid * per;
+                s_base = static_cast<int64_t>(before);
+            }
+            __syncthreads();
+            r = s_r;
+            base = static_cast<uint64_t>(s_base);
         }
     }
-    uint64_t incl = mine;
-#pragma unroll
-    for (uint32_t d = 1; d < 32; d <<= 1) {
-        const uint64_t y = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += y;
+    if (!some) {
+        if (p.prompt_rows > 0) attn_pdl_wait();
+        return;
     }
-    if (lane == 31u) s_sum[warp] = incl;
-    __syncthreads();
-    uint64_t total = 0, before = incl - mine;
-#pragma unroll
-    for (uint32_t w = 0; w < kRowWarps; ++w) {
-        if (w < warp) before += s_sum[w];
-        total += s_sum[w];
-    }
-    if (total == 0) return;
-    const uint64_t ctas = gridDim.x < total ? gridDim.x : total;
-    if (blockIdx.x >= ctas) return;
-    uint64_t u = total * blockIdx.x / ctas;
-    const uint64_t u_end = total * (blockIdx.x + 1) / ctas;
-    if (before <= u && u < before + mine) {
-        s_r = tid * per;
-        s_base = static_cast<int64_t>(before);
-    }
-    __syncthreads();
-    int64_t r = s_r;
-    uint64_t base = static_cast<uint64_t>(s_base);  // first unit of request r
 
     const uint32_t my_ring = smem_u32(ring) + warp * ST * Sm::kStage;
     // the ring goes on from segment to segment: slot and phase of the next copy and of the next to be read
@@ -184,17 +230,17 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
             ++r;
             continue;
         }
-        const uint64_t hj = (u - base) / x.units;
-        const int32_t ca = static_cast<int32_t>((u - base) % x.units);
+        const uint64_t hj = udiv(u - base, static_cast<uint32_t>(x.units));
+        const int32_t ca = static_cast<int32_t>(u - base - hj * x.units);
         const int32_t cb = static_cast<int32_t>(x.units - ca < u_end - u ? x.units : ca + (u_end - u));
-        const int32_t h = static_cast<int32_t>(hj / x.tiles), j = static_cast<int32_t>(hj % x.tiles);
+        const int32_t h = static_cast<int32_t>(udiv(hj, static_cast<uint32_t>(x.tiles))), j = static_cast<int32_t>(hj) - h * x.tiles;
 
         // the tokens some row of the tile sees / every row sees; row i of the
         // tile is (query, head) = divmod(row0 + i, group)
         const int32_t row0 = j * kRows;
         const int32_t rows_left = x.n * p.group - row0;
         const int32_t nrows = rows_left < kRows ? rows_left : kRows;
-        const int32_t qa = row0 / p.group, qb = (row0 + nrows - 1) / p.group;
+        const int32_t qa = query_of(p, row0), qb = query_of(p, row0 + nrows - 1);
         const int32_t any_hi = x.kv - x.n + qb + 1, all_hi = x.kv - x.n + qa + 1;
         const int32_t any_lo = p.window > 0 ? all_hi - p.window : 0, all_lo = p.window > 0 ? any_hi - p.window : 0;
 
@@ -272,7 +318,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         for (int nt = 0; nt < NT; ++nt) {
             const int32_t i = 8 * nt + static_cast<int32_t>(g);
             const bool ok = i < nrows;
-            const int32_t qi = (row0 + (ok ? i : 0)) / p.group, qh = (row0 + (ok ? i : 0)) % p.group;
+            const int32_t qi = query_of(p, row0 + (ok ? i : 0)), qh = row0 + (ok ? i : 0) - qi * p.group;
             const uint16_t* src = p.q + (x.q0 + qi) * p.q_stride + static_cast<int64_t>(h * p.group + qh) * D + t * 16;
             float v[KC * 16];
 #pragma unroll
@@ -302,7 +348,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         }
         // the tokens row i of the tile sees: [lo, hi)
         auto sees = [&](int32_t i, int32_t& lo, int32_t& hi) {
-            const int32_t pos = x.kv - x.n + (row0 + i) / p.group;
+            const int32_t pos = x.kv - x.n + query_of(p, row0 + i);
             hi = i < nrows && pos >= 0 ? pos + 1 : 0;
             lo = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
         };
@@ -575,24 +621,29 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         constexpr int EPT = D / TPR;              // head positions per thread
         const int32_t row = static_cast<int32_t>(tid / TPR);
         const int32_t d0 = static_cast<int32_t>(tid % TPR) * EPT;
-        float M = -INFINITY, L = 0.0f, acc[EPT];
+        float M = -INFINITY, L = 0.0f, acc[EPT], mw[kRowWarps], lw[kRowWarps];
 #pragma unroll
         for (int e = 0; e < EPT; ++e) acc[e] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, s_m[w][row]);
+        for (int w = 0; w < kRowWarps; ++w) {
+            mw[w] = s_m[w][row];
+            lw[w] = s_l[w][row];
+        }
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, mw[w]);
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) {
-            const float mw = s_m[w][row];
-            const float f = mw == -INFINITY ? (s_l[w][row] == s_l[w][row] ? 0.0f : 1.0f) : exp2_fast(mw - M);
-            if (f == 0.0f) continue;  // a warp that saw nothing of this row
-            L = __fmaf_rn(s_l[w][row], f, L);
+            // (a warp that saw nothing of this row has 0 for everything, or NaN that must stay)
+            const float f = mw[w] == -INFINITY ? 1.0f : exp2_fast(mw[w] - M);
+            L = __fmaf_rn(lw[w], f, L);
+            const float* v = part + (w * kRows + row) * PS + d0;
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) acc[e] = __fmaf_rn(part[(w * kRows + row) * PS + d0 + e], f, acc[e]);
+            for (int e = 0; e < EPT; ++e) acc[e] = __fmaf_rn(v[e], f, acc[e]);
         }
         bool write = true;
         if (ca > 0 || cb < x.units) {  // part of a row tile: leave a partial, the last CTA to arrive joins them
             const uint64_t s0 = u - ca, s1 = s0 + x.units;
-            const uint64_t c0 = ((s0 + 1) * ctas - 1) / total, c1 = (s1 * ctas - 1) / total;
+            const uint64_t c0 = udiv((s0 + 1) * ctas - 1, total), c1 = udiv(s1 * ctas - 1, total);
             float* slot = p.parts + (2 * blockIdx.x + (ca == 0 ? 1 : 0)) * kSlot;
             if (d0 == 0) {
                 slot[row] = M;
@@ -634,7 +685,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
             }
         }
         if (write && row < nrows) {
-            const int32_t qi = (row0 + row) / p.group, qh = h * p.group + (row0 + row) % p.group;
+            const int32_t qi = query_of(p, row0 + row), qh = h * p.group + row0 + row - qi * p.group;
             const int64_t at = (x.q0 + qi) * p.q_heads + qh;
             const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : (L == L ? 0.0f : L);
             uint16_t* dst = static_cast<uint16_t*>(p.out) + at * D + d0;
@@ -648,6 +699,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         __syncthreads();           // s_m, s_l, the ring and s_last are free again
         u += static_cast<uint64_t>(cb - ca);
     }
+    if (p.prompt_rows > 0) attn_pdl_wait();  // (this launch ends no earlier than the prompt kernel that it runs beside)
 }
 
 constexpr int kMaxDevices = 64;
@@ -664,8 +716,19 @@ int launch_rows(const AttnParams& p, int dev, int sms, void* stream) {
     }
     int grid = sms * Sm::kCtas;
     if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
-    fn<<<grid, kRowThreads, Sm::kBytes, static_cast<cudaStream_t>(stream)>>>(p);
-    return static_cast<int>(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.dynamicSmemBytes = Sm::kBytes;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    // beside the prompt kernel of the same call: the two share inputs, and
+    // write different rows and different parts of the workspace
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.prompt_rows > 0 ? 1 : 0;
+    return static_cast<int>(cudaLaunchKernelEx(&cfg, fn, p));
 }
 
 template <int D, bool E4M3, bool BF16>
@@ -692,13 +755,24 @@ int launch_attention(AttnParams p, int head_dim, bool e4m3, bool bf16, void* str
     if (p.max_q > p.n_tokens) p.max_q = p.n_tokens;
     const IqGrids* grids = nullptr;
     if (const int rc = device_symbols(dev, &p.fault, &grids)) return rc;
-    // Requests with more than 16 rows go to the prompt kernel, which is not
-    // launched when there can be none; the others to this one.  (The host does
-    // not know the lengths, so this one always runs.)
-    if (p.max_q * p.group > kAttnRows) {
-        p.prompt_rows = kAttnRows + 1;
-        const int rc = launch_attention_prompt(p, head_dim, e4m3, bf16, dev, sms, stream);
+    // Requests with more than 32 rows go to the prompt kernel, which is not
+    // launched when there can be none; the others to this one, 16 rows at a
+    // time.  (The second 16 read the cache again, from L2: about what the 128
+    // rows of the prompt kernel's tile cost, and tens of microseconds less
+    // where the work is small.  The host does not know the lengths, so this
+    // kernel always runs.)
+    uint32_t* counters = p.counters;
+    float* parts = p.parts;
+    if (p.max_q * p.group > 2 * kAttnRows) {
+        p.prompt_rows = 2 * kAttnRows + 1;
+        p.counters = counters + kAttnMaxCtas;
+        p.parts = parts + 2 * static_cast<size_t>(kAttnMaxCtas) * NDQ_ROWS_SLOT(head_dim);
+        bool launched = false;
+        const int rc = launch_attention_prompt(p, head_dim, e4m3, bf16, dev, sms, stream, &launched);
         if (rc != 0) return rc;
+        if (!launched) p.prompt_rows = 0;
+        p.counters = counters;
+        p.parts = parts;
     }
     if (head_dim == 64) {
         if (e4m3) return bf16 ? launch_typed<64, true, true>(p, dev, sms, stream) : launch_typed<64, true, false>(p, dev, sms, stream);

@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     PrShared& S = *reinterpret_cast<PrShared*>(base + 7 * kTile);
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
     const int bl = p.c.bs_log2;
+    attn_pdl_launch();  // (the kernel for the other requests may start)
 
     // which unit: blockIdx.x counts (unit, split), units ordered by request,
     // then row tile (the last, longest, first), then head
@@ -741,30 +742,24 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             __threadfence();
         }
         meet<kMeetRows, 256>();
-        if (S.last && !fault && has_row) {
-            const uint32_t prow = wg * 128u + wrow;
+        if (S.last && !fault) {  // a thread per row and 8 head positions
             const float* first = p.parts + unit * static_cast<uint64_t>(p.splits) * NDQ_PROMPT_SLOT(D);
-            float M = -INFINITY, L = 0.0f;
-            for (int s = 0; s < p.splits; ++s) M = fmaxf(M, __ldcg(first + s * NDQ_PROMPT_SLOT(D) + prow));
-            auto weight = [&](int s, float& l) {
-                const float m = __ldcg(first + s * NDQ_PROMPT_SLOT(D) + prow);
-                l = __ldcg(first + s * NDQ_PROMPT_SLOT(D) + kPromptRows + prow);
-                return m == -INFINITY ? (l == l ? 0.0f : 1.0f) : exp2_fast(m - M);
-            };
-            for (int s = 0; s < p.splits; ++s) {
-                float l;
-                const float f = weight(s, l);
-                if (f != 0.0f) L = __fmaf_rn(l, f, L);
-            }
-            const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : (L == L ? 0.0f : L);
-            for (int c = 0; c < D / 8; ++c) {
+            for (int32_t i = static_cast<int32_t>(tid); i < nrows * (D / 8); i += 256) {
+                const int32_t prow = i % nrows, c = i / nrows;
+                float M = -INFINITY, L = 0.0f;
+#pragma unroll
+                for (int s = 0; s < kPromptMaxSplits; ++s)
+                    if (s < p.splits) M = fmaxf(M, __ldcg(first + s * NDQ_PROMPT_SLOT(D) + prow));
                 float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
-                for (int s = 0; s < p.splits; ++s) {
-                    float l;
-                    const float f = weight(s, l);
-                    if (f == 0.0f) continue;
+#pragma unroll 4
+                for (int s = 0; s < kPromptMaxSplits; ++s) {
+                    if (s >= p.splits) break;
                     const float4* q = reinterpret_cast<const float4*>(first + s * NDQ_PROMPT_SLOT(D) + 2 * kPromptRows);
                     const float4 x = __ldcg(q + (2 * c) * kPromptRows + prow), y = __ldcg(q + (2 * c + 1) * kPromptRows + prow);
+                    const float mm = __ldcg(first + s * NDQ_PROMPT_SLOT(D) + prow), ll = __ldcg(first + s * NDQ_PROMPT_SLOT(D) + kPromptRows + prow);
+                    const float f = mm == -INFINITY ? (ll == ll ? 0.0f : 1.0f) : exp2_fast(mm - M);
+                    if (f == 0.0f) continue;
+                    L = __fmaf_rn(ll, f, L);
                     a.x = __fmaf_rn(x.x, f, a.x);
                     a.y = __fmaf_rn(x.y, f, a.y);
                     a.z = __fmaf_rn(x.z, f, a.z);
@@ -774,11 +769,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     b.z = __fmaf_rn(y.z, f, b.z);
                     b.w = __fmaf_rn(y.w, f, b.w);
                 }
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(at) * D + 8 * c) =
+                const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : (L == L ? 0.0f : L);
+                const int32_t to = static_cast<int32_t>((q0 + (row0 + prow) / p.group) * p.q_heads) + h * p.group + (row0 + prow) % p.group;
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(to) * D + 8 * c) =
                     make_uint4(narrow2<BF16>(a.x * inv, a.y * inv), narrow2<BF16>(a.z * inv, a.w * inv),
                                narrow2<BF16>(b.x * inv, b.y * inv), narrow2<BF16>(b.z * inv, b.w * inv));
+                if (p.lse && c == 0) p.lse[to] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : (L == L ? -INFINITY : L);
             }
-            if (p.lse) p.lse[at] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : (L == L ? -INFINITY : L);
         }
     }
 }
@@ -804,11 +801,13 @@ int launch_typed(const AttnParams& p, unsigned grid, int dev, void* stream) {
 
 }  // namespace
 
-int launch_attention_prompt(AttnParams p, int head_dim, bool e4m3, bool bf16, int dev, int sms, void* stream) {
+int launch_attention_prompt(AttnParams p, int head_dim, bool e4m3, bool bf16, int dev, int sms, void* stream,
+                            bool* launched) {
     // units at most: a request's last unit may be partial, and has at least prompt_rows rows
     const int64_t rows = p.n_tokens * p.group;
     const int64_t reqs = rows / p.prompt_rows < p.n_req ? rows / p.prompt_rows : p.n_req;
     const int64_t units = (rows / kPromptRows + reqs) * p.c.heads;
+    *launched = units > 0;
     if (units == 0) return 0;
     // too few units to fill the GPU: split their tokens, four tiles to a part at least
     const int64_t most = (p.width << p.c.bs_log2) / (4 * 128);

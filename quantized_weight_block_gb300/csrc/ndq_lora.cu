@@ -225,6 +225,7 @@ __device__ __forceinline__ void ldmatrix4(uint32_t* r, uint32_t addr) {
 
 template <int NT>
 __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_shrink_tile(const LoraParams p, int splits) {
+    // (blockIdx.z of gridDim.z: every gridDim.z-th of the tile's adapters)
     using Sm = ShrinkSmem<NT>;
     constexpr int ST = Sm::kStages;
     extern __shared__ __align__(128) uint8_t s_ring[];
@@ -253,7 +254,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_shrink_tile(const Lora
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(s_ring));
     const uint32_t piece = tid & 7u, crow = tid >> 3;  // this thread copies piece `piece` of rows crow, crow + 32, ...
     const uint32_t mrow = 16u * (warp & 3u), khalf = warp >> 2;
+    uint32_t turn = 0;
     for (int32_t a = next(-1); a != INT32_MAX; a = next(a)) {
+        if (turn++ % gridDim.z != blockIdx.z) continue;
         const int32_t r = rank_of(p, a);
         if (r == 0) continue;
         const bool live0 = s_a[crow] == a, live1 = s_a[crow + 32] == a;
@@ -742,7 +745,12 @@ cudaError_t shrink_tile(const LoraParams& p, int splits, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         ready[dev] = true;
     }
-    const dim3 grid(static_cast<unsigned>((p.M + kShrinkRows - 1) / kShrinkRows), static_cast<unsigned>(splits));
+    // what is left of the GPU goes to a tile's adapters (CTAs beyond their number end at once)
+    const int64_t tiles = (p.M + kShrinkRows - 1) / kShrinkRows;
+    int64_t z = 2 * 152 / (tiles * splits);
+    z = z < 1 ? 1 : (z > 16 ? 16 : z);
+    if (z > p.nA) z = p.nA;
+    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(splits), static_cast<unsigned>(z));
     k_lora_shrink_tile<NT><<<grid, kLoraThreads, smem, st>>>(p, splits);
     return cudaGetLastError();
 }

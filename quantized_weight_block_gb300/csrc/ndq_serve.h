@@ -49,22 +49,22 @@ struct AppendParams {
 };
 int launch_kv_append(const AppendParams& p, int head_dim, bool e4m3, bool bf16, void* stream);
 
-// The attention workspace: arrival counters (zero between calls), then partial
-// results.  Few rows: CTAs of a launch at most, each leaving up to two
-// partials of 16 rows.  Prompts: units of 256 rows whose tokens are split over
-// at most one CTA per SM in all, each leaving one partial.
+// The attention workspace: arrival counters (zero between calls), then the
+// partial results of the two kernels, which may run side by side.  Few rows:
+// CTAs of a launch at most, each leaving up to two partials of 16 rows.
+// Prompts: units of 256 rows whose tokens are split over at most one CTA per
+// SM in all, each leaving one partial.
 constexpr int kAttnMaxCtas = 512;
-constexpr size_t kAttnCounterBytes = 4096;
 constexpr int kAttnRows = 16;
 constexpr int kPromptRows = 256;
 constexpr int kPromptMaxSplits = 16;
 constexpr int kPromptMaxParts = 192;  // (units * splits <= SMs when splits > 1)
-constexpr size_t attn_slot_floats(int head_dim) { return static_cast<size_t>(kAttnRows) * (head_dim + 2); }
+constexpr size_t kAttnCounterBytes = 4096;
+static_assert((kAttnMaxCtas + kPromptMaxParts) * 4 <= kAttnCounterBytes, "counters");
+#define NDQ_ROWS_SLOT(D) (static_cast<size_t>(ndq::kAttnRows) * ((D) + 2))     // floats of a partial
 #define NDQ_PROMPT_SLOT(D) (static_cast<size_t>(ndq::kPromptRows) * ((D) + 2))
 constexpr size_t attn_workspace_bytes(int head_dim) {
-    return kAttnCounterBytes + 4u * (2u * kAttnMaxCtas * attn_slot_floats(head_dim) > kPromptMaxParts * NDQ_PROMPT_SLOT(head_dim)
-                                         ? 2u * kAttnMaxCtas * attn_slot_floats(head_dim)
-                                         : kPromptMaxParts * NDQ_PROMPT_SLOT(head_dim));
+    return kAttnCounterBytes + 4u * (2u * kAttnMaxCtas * NDQ_ROWS_SLOT(head_dim) + kPromptMaxParts * NDQ_PROMPT_SLOT(head_dim));
 }
 
 struct AttnParams {
@@ -75,7 +75,7 @@ struct AttnParams {
     const int32_t* table;
     const int32_t* kv_len;
     const int32_t* q_start;  // or nullptr: one query per request
-    uint32_t* counters;
+    uint32_t* counters;  // of the kernel that is launched
     float* parts;
     int64_t n_tokens;
     int64_t n_req;
@@ -85,12 +85,14 @@ struct AttnParams {
     int64_t max_q;
     int32_t q_heads;
     int32_t group;   // query heads per cache head
+    int32_t group_shift;  // its logarithm, or -1
     float scale_log2;  // scale * log2(e)
     unsigned int* fault;  // device fault word (set by the launcher)
     int32_t splits;       // prompts: CTAs per unit (set by the launcher)
     int32_t prompt_rows;  // > 0: requests with at least this many rows are left to the prompt kernel
 };
-int launch_attention_prompt(AttnParams p, int head_dim, bool e4m3, bool bf16, int dev, int sms, void* stream);
+int launch_attention_prompt(AttnParams p, int head_dim, bool e4m3, bool bf16, int dev, int sms, void* stream,
+                            bool* launched);
 int launch_attention(AttnParams p, int head_dim, bool e4m3, bool bf16, void* stream);
 
 struct LoraParams {

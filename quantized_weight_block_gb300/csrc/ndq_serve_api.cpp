@@ -157,6 +157,9 @@ int ndq_attention_kv8(const ndq_kv_cache* cache, const void* q, int dtype, int64
     p.max_q = q_start ? max_q : 1;
     p.q_heads = q_heads;
     p.group = q_heads / cache->kv_heads;
+    p.group_shift = -1;
+    for (int i = 0; i < 13; ++i)
+        if (p.group == 1 << i) p.group_shift = i;
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     return ndq::launch_attention(p, cache->head_dim, cache->code_type == NDQ_FLOAT8E4M3FN, dtype == NDQ_BFLOAT16,
                                  stream) == 0
