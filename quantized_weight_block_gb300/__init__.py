@@ -370,11 +370,30 @@ def ndq_lora_add(x: int, M: int, K: int, lora_a: int, lora_b: int, n_adapters: i
                              workspace, ws_bytes, stream)
 
 
+class _Torch:
+    """What the wrappers of short launches look up in torch, once."""
+
+    def __init__(self):
+        torch = _torch()
+        self.f32, self.bf16, self.i32, self.i64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.code = {torch.float32: NDQ_FLOAT, torch.float16: NDQ_FLOAT16, torch.bfloat16: NDQ_BFLOAT16}
+
+
+_T = None
+
+
+def _consts() -> _Torch:
+    global _T
+    _T = _Torch()
+    return _T
+
+
 def _raw_stream(stream, device) -> int:
     # (the handle alone: building a torch.cuda.Stream for each call costs microseconds)
     if stream is not None:
         return int(stream.cuda_stream)
-    return _torch()._C._cuda_getCurrentRawStream(device.index)
+    return (_T or _consts()).raw_stream(device.index)
 
 
 def _check(name, x, dtype, shape, device):
@@ -414,12 +433,19 @@ class KvCache:
 
 
 class KvPlan:
-    """Outputs of kv_plan: q_start [R + 1], kv_len [R], positions [T] (int32),
-    slots [T] (int64), free_left [1] (int32)."""
-    __slots__ = ("q_start", "kv_len", "positions", "slots", "free_left")
+    """Output buffers of kv_plan: q_start [R + 1], kv_len [R], positions [T]
+    (int32), slots [T] (int64), free_left [1] (int32).  Keeps the tensors and
+    the arguments that name them to the library."""
 
     def __init__(self, q_start, kv_len, positions, slots, free_left):
+        torch = _torch()
+        R, T, device = kv_len.shape[0], slots.shape[0], kv_len.device
+        for name, x, dtype, n in (("q_start", q_start, torch.int32, R + 1), ("kv_len", kv_len, torch.int32, R),
+                                  ("positions", positions, torch.int32, T), ("slots", slots, torch.int64, T),
+                                  ("free_left", free_left, torch.int32, 1)):
+            _check(name, x, dtype, (n,), device)
         self.q_start, self.kv_len, self.positions, self.slots, self.free_left = q_start, kv_len, positions, slots, free_left
+        self.pointers = (q_start.data_ptr(), kv_len.data_ptr(), positions.data_ptr(), slots.data_ptr(), T, free_left.data_ptr())
 
 
 def kv_plan_buffers(n_req: int, n_tokens: int, device="cuda") -> KvPlan:
@@ -435,13 +461,12 @@ def kv_plan(cached, fresh, block_size: int, free_blocks, free_count, block_table
     [R], free_blocks [F], free_count [1] and block_table [R, width] are CUDA
     int32 tensors; block_table is written in place.  `out` holds the outputs,
     or `n_tokens` says how many tokens to allow for.  Returns the KvPlan."""
-    torch = _torch()
-    i32 = torch.int32
-    if (cached.dtype != i32 or fresh.dtype != i32 or free_blocks.dtype != i32 or free_count.dtype != i32
-            or block_table.dtype != i32):
+    i32 = (_T or _consts()).i32
+    if (cached.dtype is not i32 or fresh.dtype is not i32 or free_blocks.dtype is not i32 or free_count.dtype is not i32
+            or block_table.dtype is not i32):
         raise ValueError("kv_plan takes int32 tensors")
-    R = cached.shape[0]
-    if fresh.shape[0] != R or block_table.dim() != 2 or block_table.shape[0] != R or free_count.numel() != 1:
+    R, width = block_table.shape
+    if len(cached) != R or len(fresh) != R or free_count.numel() != 1:
         raise ValueError("cached [R], fresh [R], block_table [R, width] and free_count [1] must agree")
     if not (cached.is_contiguous() and fresh.is_contiguous() and free_blocks.is_contiguous()
             and block_table.is_contiguous()):
@@ -450,37 +475,38 @@ def kv_plan(cached, fresh, block_size: int, free_blocks, free_count, block_table
         if n_tokens is None:
             raise ValueError("kv_plan needs `out` or `n_tokens`")
         out = kv_plan_buffers(R, n_tokens, cached.device)
-    elif out.q_start.shape[0] != R + 1 or out.kv_len.shape[0] != R or out.positions.shape != out.slots.shape:
+    elif len(out.kv_len) != R:
         raise ValueError("out does not fit the requests")
     rc = _lib.ndq_kv_plan(cached.data_ptr(), fresh.data_ptr(), R, block_size, free_blocks.data_ptr(),
-                          free_count.data_ptr(), block_table.data_ptr(), block_table.shape[1], out.q_start.data_ptr(),
-                          out.kv_len.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(), out.slots.shape[0],
-                          out.free_left.data_ptr(), _raw_stream(stream, cached.device))
+                          free_count.data_ptr(), block_table.data_ptr(), width, *out.pointers, _raw_stream(stream, cached.device))
     if rc:
         raise NdqError(rc, "kv_plan")
     return out
 
 
 def _row_stride(name, x, heads, dim):
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
+    """Elements from one token's row [heads, dim] of x to the next."""
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name} must be [tokens, {heads}, {dim}]")
     st = x.stride()
     if st[2] != 1 or (st[1] != dim and heads > 1):
         raise ValueError(f"{name} must have dense heads")
-    return st[0] if x.shape[0] > 1 else heads * dim
+    return st[0] if shape[0] > 1 else heads * dim
 
 
 def kv_append(cache: KvCache, k, v, slots, stream=None) -> None:
     """Quantise the rows k, v [T, kv_heads, head_dim] (bfloat16 or float16;
     token strides of any multiple of 8) into `cache` at slots [T] (int64, as
     kv_plan writes them)."""
-    torch = _torch()
-    ks, vs = (_row_stride(n, x, cache.kv_heads, cache.head_dim) for n, x in (("k", k), ("v", v)))
-    T = k.shape[0]
-    if k.dtype != v.dtype or v.shape[0] != T or slots.dtype != torch.int64 or slots.shape != (T,) or not slots.is_contiguous():
-        raise ValueError("k and v must have the same type and tokens, and slots one int64 for each")
-    rc = _lib.ndq_kv_append(cache.desc, k.data_ptr(), v.data_ptr(), out_dtype_code(k.dtype), ks, vs, slots.data_ptr(), T,
-                            _raw_stream(stream, k.device))
+    c = _T or _consts()
+    heads, dim, code = cache.kv_heads, cache.head_dim, c.code.get(k.dtype)
+    T = len(k)
+    if (k.dtype is not v.dtype or code is None or len(v) != T or slots.dtype is not c.i64 or slots.dim() != 1 or len(slots) != T
+            or not slots.is_contiguous()):
+        raise ValueError("k and v must have the same type (bfloat16 or float16) and tokens, and slots one int64 for each")
+    rc = _lib.ndq_kv_append(cache.desc, k.data_ptr(), v.data_ptr(), code, _row_stride("k", k, heads, dim),
+                            _row_stride("v", v, heads, dim), slots.data_ptr(), T, _raw_stream(stream, cache.device))
     if rc:
         raise NdqError(rc, "kv_append")
 
@@ -502,31 +528,31 @@ def attention_kv8(q, cache: KvCache, block_table, kv_len, q_start=None, max_q=No
     q_start [R + 1] are CUDA int32 tensors, q_start None when every request has
     one query.  max_q bounds the queries of one request (default: T, or 1).
     Returns out [T, q_heads, head_dim]; lse [T, q_heads] is written if given."""
-    torch = _torch()
-    if q.dim() != 3:
-        raise ValueError("q must be [tokens, q_heads, head_dim]")
+    c = _T or _consts()
+    i32, code = c.i32, c.code.get(q.dtype)
+    if q.dim() != 3 or code is None:
+        raise ValueError("q must be [tokens, q_heads, head_dim], bfloat16 or float16")
     T, H, D = q.shape
     qs = _row_stride("q", q, H, cache.head_dim)
-    R = kv_len.shape[0]
-    if (block_table.dtype != torch.int32 or kv_len.dtype != torch.int32 or block_table.dim() != 2
-            or block_table.shape[0] != R or not block_table.is_contiguous() or not kv_len.is_contiguous()):
+    R, width = block_table.shape
+    if (block_table.dtype is not i32 or kv_len.dtype is not i32 or len(kv_len) != R or not block_table.is_contiguous()
+            or not kv_len.is_contiguous()):
         raise ValueError("block_table must be int32 [R, width] and kv_len int32 [R]")
-    if q_start is not None and (q_start.dtype != torch.int32 or q_start.shape != (R + 1,) or not q_start.is_contiguous()):
+    if q_start is not None and (q_start.dtype is not i32 or len(q_start) != R + 1 or not q_start.is_contiguous()):
         raise ValueError("q_start must be int32 [R + 1]")
     if out is None:
-        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+        out = _torch().empty((T, H, D), dtype=q.dtype, device=q.device)
+    elif out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's shape and type")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not c.f32 or lse.shape != (T, H) or not lse.is_contiguous()):
         raise ValueError("lse must be float32 [tokens, q_heads]")
     if workspace is None:
         workspace = attention_workspace(R, T, H, cache)
     rc = _lib.ndq_attention_kv8(
-        cache.desc, q.data_ptr(), out_dtype_code(q.dtype), T, H, qs, block_table.data_ptr(), block_table.shape[1],
-        kv_len.data_ptr(), None if q_start is None else q_start.data_ptr(), R,
-        max_q if max_q is not None else (1 if q_start is None else T), D ** -0.5 if scale is None else scale, window,
-        out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        _raw_stream(stream, q.device))
+        cache.desc, q.data_ptr(), code, T, H, qs, block_table.data_ptr(), width, kv_len.data_ptr(),
+        None if q_start is None else q_start.data_ptr(), R, max_q if max_q is not None else (1 if q_start is None else T),
+        D ** -0.5 if scale is None else scale, window, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, q.device))
     if rc:
         raise NdqError(rc, "attention_kv8")
     return out
@@ -543,20 +569,20 @@ def lora_add(x, lora_a, lora_b, ranks, scales, index, base, out=None, workspace=
     (see ndq_lora_add): x bfloat16 [M, K], lora_a bfloat16 [n, rank, K], lora_b
     bfloat16 [n, N, rank], ranks int32 [n], scales float32 [n], index int32 [M],
     base float32 or bfloat16 [M, N].  out may be base.  Returns out."""
-    torch = _torch()
+    c = _T or _consts()
+    bf16, i32 = c.bf16, c.i32
     M, K = x.shape
-    nA, rank = lora_a.shape[0], lora_a.shape[1]
-    N = lora_b.shape[1]
-    bf16 = torch.bfloat16
-    if (x.dtype != bf16 or lora_a.dtype != bf16 or lora_b.dtype != bf16 or lora_a.shape != (nA, rank, K)
-            or lora_b.shape != (nA, N, rank) or base.shape != (M, N) or ranks.shape != (nA,) or scales.shape != (nA,)
-            or index.shape != (M,) or ranks.dtype != torch.int32 or index.dtype != torch.int32
-            or scales.dtype != torch.float32):
+    nA, rank, Ka = lora_a.shape
+    nB, N, rb = lora_b.shape
+    dtype = base.dtype
+    if (x.dtype is not bf16 or lora_a.dtype is not bf16 or lora_b.dtype is not bf16 or Ka != K or nB != nA or rb != rank
+            or base.shape != (M, N) or len(ranks) != nA or len(scales) != nA or len(index) != M or ranks.dtype is not i32
+            or index.dtype is not i32 or scales.dtype is not c.f32 or (dtype is not c.f32 and dtype is not bf16)):
         raise ValueError("lora_add: x [M, K], lora_a [n, r, K], lora_b [n, N, r] bfloat16, ranks [n], index [M] int32, "
-                         "scales [n] float32, base [M, N]")
+                         "scales [n] float32, base [M, N] float32 or bfloat16")
     if out is None:
-        out = torch.empty_like(base)
-    if out.dtype != base.dtype or out.shape != base.shape:
+        out = _torch().empty_like(base)
+    elif out.dtype is not dtype or out.shape != base.shape:
         raise ValueError("out must have base's shape and type")
     if not (x.is_contiguous() and lora_a.is_contiguous() and lora_b.is_contiguous() and base.is_contiguous()
             and out.is_contiguous() and ranks.is_contiguous() and scales.is_contiguous() and index.is_contiguous()):
@@ -564,8 +590,8 @@ def lora_add(x, lora_a, lora_b, ranks, scales, index, base, out=None, workspace=
     if workspace is None:
         workspace = lora_workspace(M, nA, rank, K, x.device)
     rc = _lib.ndq_lora_add(x.data_ptr(), M, K, lora_a.data_ptr(), lora_b.data_ptr(), nA, rank, N, ranks.data_ptr(),
-                           scales.data_ptr(), index.data_ptr(), base.data_ptr(), out_dtype_code(base.dtype),
-                           out.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, x.device))
+                           scales.data_ptr(), index.data_ptr(), base.data_ptr(), c.code[dtype], out.data_ptr(),
+                           workspace.data_ptr(), workspace.numel(), _raw_stream(stream, x.device))
     if rc:
         raise NdqError(rc, "lora_add")
     return out

@@ -4,15 +4,14 @@
 //     t[m, j] = scale[a] * sum_k x[m, k] A[a, j, k]          (shrink, j < rank)
 //     y[m, n] = base[m, n] + sum_j t[m, j] B[a, n, j]        (expand),  a = index[m]
 //
-// Two kernels, t in binary32 in the workspace; the second is launched
-// programmatically behind the first and reads what does not depend on it
-// before it waits.  There are two pairs:
+// t in binary32.  There are two ways:
 //
-// * few rows (k_lora_shrink_rows, k_lora_expand_rows): bound by the latency
-//   of one pass over the adapters' weights.  A CTA takes one row and
-//   kShrinkJ ranks over all of K; a thread of the expansion one or more
-//   outputs.
-// * many rows (k_lora_shrink_tile, k_lora_expand_tile): tiles of 64 rows on
+// * few rows (k_lora_rows): bound by the latency of one pass over the
+//   adapters' weights.  One launch, a cluster of CTAs to a row: each sums some
+//   of the ranks over all of K, and after an exchange of t through distributed
+//   shared memory expands some of the columns.
+// * many rows (k_lora_shrink_tile, k_lora_expand_tile; t in the workspace, the
+//   second launched programmatically behind the first): tiles of 64 rows on
 //   the tensor cores (mma.sync m16n8k16: the operator is bound by reading x
 //   and base and writing y, and its products need a fraction of even that
 //   rate).  A tile goes through the adapters of its rows one by one, with the
@@ -26,12 +25,15 @@
 //   adjacent ones.
 //
 // Any other alignment (K or max_rank not a multiple of 8, buffers off 16
-// bytes) takes the few-row kernels with scalar loads.
+// bytes) takes the few-row kernel with scalar loads.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cooperative_groups.h>
+
 #include <cstdint>
+#include <type_traits>
 
 #include "ndq_device.cuh"
 #include "ndq_serve.h"
@@ -39,7 +41,7 @@
 namespace ndq {
 namespace {
 
-constexpr int kShrinkJ = 4;          // ranks per CTA of k_lora_shrink_rows
+constexpr int kRowCtas = 8;          // CTAs to a row there
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
 constexpr int kMaxSplit = 8;         // K splits of k_lora_shrink_tile at most
@@ -69,120 +71,120 @@ __device__ __forceinline__ float dot8(const uint4& x, const uint4& w, float s) {
 
 // ---- few rows ----------------------------------------------------------------
 
-// One row and kShrinkJ ranks; the CTA's threads split K.
-template <bool VEC>
-__global__ void __launch_bounds__(kLoraThreads) k_lora_shrink_rows(const LoraParams p) {
-    __shared__ float s_part[kLoraWarps][kShrinkJ];
-    pdl_launch();
-    const int32_t groups = static_cast<int32_t>((p.rmax + kShrinkJ - 1) / kShrinkJ);
-    const int64_t m = blockIdx.x / groups;
-    const int32_t j0 = static_cast<int32_t>(blockIdx.x % groups) * kShrinkJ;
-    const int32_t a = p.index[m];
-    if (a < 0 || a >= p.nA) return;
-    const uint16_t* x = p.x + m * p.K;
-    const uint16_t* w = p.a + (static_cast<int64_t>(a) * p.rmax + j0) * p.K;
-    const int32_t have = static_cast<int32_t>(p.rmax) - j0 < kShrinkJ ? static_cast<int32_t>(p.rmax) - j0 : kShrinkJ;
-    const int32_t nj = rank_of(p, a) - j0;  // (the weights are fetched before it is known: rows beyond the rank exist)
-    float s[kShrinkJ] = {};
-    if constexpr (VEC) {
-        const int64_t K8 = p.K >> 3;
-#pragma unroll 2
-        for (int64_t i = threadIdx.x; i < K8; i += kLoraThreads) {
-            const uint4 xv = reinterpret_cast<const uint4*>(x)[i];
-            uint4 wv[kShrinkJ];
-#pragma unroll
-            for (int j = 0; j < kShrinkJ; ++j)
-                wv[j] = j < have ? __ldg(reinterpret_cast<const uint4*>(w + j * p.K) + i) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int j = 0; j < kShrinkJ; ++j) s[j] = dot8(xv, wv[j], s[j]);
-        }
-    } else {
-        for (int64_t k = threadIdx.x; k < p.K; k += kLoraThreads) {
-            const float xv = bf(x[k]);
-#pragma unroll
-            for (int j = 0; j < kShrinkJ; ++j)
-                if (j < nj) s[j] = __fmaf_rn(xv, bf(w[j * p.K + k]), s[j]);
-        }
-    }
-    if (nj <= 0) return;
-#pragma unroll
-    for (int j = 0; j < kShrinkJ; ++j)
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s[j] = __fadd_rn(s[j], __shfl_xor_sync(0xffffffffu, s[j], d));
-    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    if (lane == 0) {
-#pragma unroll
-        for (int j = 0; j < kShrinkJ; ++j) s_part[warp][j] = s[j];
-    }
-    __syncthreads();
-    if (threadIdx.x < kShrinkJ && static_cast<int32_t>(threadIdx.x) < nj) {
-        float v = 0.0f;
-#pragma unroll
-        for (int q = 0; q < kLoraWarps; ++q) v = __fadd_rn(v, s_part[q][threadIdx.x]);
-        p.t[m * p.rmax + j0 + threadIdx.x] = __fmul_rn(v, p.scales[a]);
-    }
-}
-
-// An output per thread; the weights of the first 16 ranks and base are
-// fetched before the wait for t.
-template <bool F32, bool VEC>
-__global__ void __launch_bounds__(kLoraThreads) k_lora_expand_rows(const LoraParams p) {
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * kLoraThreads + threadIdx.x;
-    const bool in = n < p.N;
-    bool waited = false;
-    for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
+// One row to a cluster of kRowCtas CTAs.  CTA c sums the ranks J c .. J c + J - 1,
+// J (c + 8) .. of t, its threads splitting K; the CTAs read each other's t
+// through distributed shared memory; then each expands its columns, the first
+// of which (weights of 16 ranks and base) it fetched at the start.
+template <bool F32, bool VEC_A, bool VEC_B, int J>
+__global__ void __cluster_dims__(kRowCtas, 1, 1) __launch_bounds__(kLoraThreads, 4) k_lora_rows(const LoraParams p) {
+    namespace cg = cooperative_groups;
+    __shared__ float s_part[kLoraWarps][J];
+    __shared__ float s_t[128];               // this CTA's ranks, at their index
+    __shared__ __align__(16) float s_all[128];
+    cg::cluster_group cluster = cg::this_cluster();
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, c = cluster.block_rank();
+    const int64_t step = static_cast<int64_t>(kRowCtas) * kLoraThreads;
+    for (int64_t m = blockIdx.x / kRowCtas; m < p.M; m += gridDim.x / kRowCtas) {
         const int32_t a = p.index[m];
         const bool has = a >= 0 && a < p.nA;
-        const int64_t o = m * p.N + n;
-        const uint16_t* w = p.b + (static_cast<int64_t>(has ? a : 0) * p.N + n) * p.rmax;
-        const float* t = p.t + m * p.rmax;
-        float b = 0.0f, s = 0.0f;
-        if (in) {
-            if constexpr (F32) b = static_cast<const float*>(p.base)[o];
-            else b = bf(static_cast<const uint16_t*>(p.base)[o]);
-        }
-        if constexpr (VEC) {
-            uint4 v[2] = {};  // 16 ranks of the output's weights, fetched beside the adapter's rank
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (in && has && 8 * i < p.rmax) v[i] = __ldg(reinterpret_cast<const uint4*>(w) + i);
-            const int32_t r = rank_of(p, a);
-            if (!waited) pdl_wait();
-            waited = true;
-            for (int32_t j0 = 0; j0 < r; j0 += 16) {
-                float4 tv[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tv[i] = j0 + 4 * i < r ? __ldcg(reinterpret_cast<const float4*>(t + j0) + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                uint4 u[2] = {v[0], v[1]};
+        const int64_t n0 = static_cast<int64_t>(c) * kLoraThreads + tid;
+        auto base_at = [&](int64_t n) -> float {
+            if constexpr (F32) return static_cast<const float*>(p.base)[m * p.N + n];
+            else return bf(static_cast<const uint16_t*>(p.base)[m * p.N + n]);
+        };
+        const uint16_t* wb = p.b + static_cast<int64_t>(has ? a : 0) * p.N * p.rmax;
+        float b0 = 0.0f;
+        uint4 v0[2] = {};
+        if (n0 < p.N) {
+            b0 = base_at(n0);
+            if constexpr (VEC_B) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    if (in && j0 + 16 + 8 * i < r) v[i] = __ldg(reinterpret_cast<const uint4*>(w + j0 + 16) + i);
+                    if (has && 8 * i < p.rmax) v0[i] = __ldg(reinterpret_cast<const uint4*>(wb + n0 * p.rmax) + i);
+            }
+        }
+        // (weights are fetched before the rank is known: the rows beyond it exist)
+        const int32_t r = rank_of(p, a);
+        const uint16_t* x = p.x + m * p.K;
+        for (int32_t j0 = static_cast<int32_t>(c) * J; has && j0 < p.rmax; j0 += kRowCtas * J) {
+            const uint16_t* w = p.a + (static_cast<int64_t>(a) * p.rmax + j0) * p.K;
+            const int32_t nj = static_cast<int32_t>(p.rmax) - j0 < J ? static_cast<int32_t>(p.rmax) - j0 : J;
+            float s[J] = {};
+            if constexpr (VEC_A) {
+                const int64_t K8 = p.K >> 3;
+#pragma unroll 2
+                for (int64_t i = tid; i < K8; i += kLoraThreads) {
+                    const uint4 xv = __ldg(reinterpret_cast<const uint4*>(x) + i);
+                    uint4 wv[J];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t c[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                    const float f[8] = {tv[2 * i].x, tv[2 * i].y, tv[2 * i].z, tv[2 * i].w,
-                                        tv[2 * i + 1].x, tv[2 * i + 1].y, tv[2 * i + 1].z, tv[2 * i + 1].w};
+                    for (int j = 0; j < J; ++j)
+                        wv[j] = j < nj ? __ldg(reinterpret_cast<const uint4*>(w + j * p.K) + i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float wv = (e & 1) ? bf_hi(c[e >> 1]) : bf_lo(c[e >> 1]);
-                        if (j0 + 8 * i + e < r) s = __fmaf_rn(f[e], wv, s);  // (t and weights beyond the rank are not defined)
-                    }
+                    for (int j = 0; j < J; ++j) s[j] = dot8(xv, wv[j], s[j]);
+                }
+            } else {
+                for (int64_t k = tid; k < p.K; k += kLoraThreads) {
+                    const float xv = bf(x[k]);
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+                        if (j < nj) s[j] = __fmaf_rn(xv, bf(w[j * p.K + k]), s[j]);
                 }
             }
-        } else {
-            const int32_t r = rank_of(p, a);
-            if (!waited) pdl_wait();
-            waited = true;
-            if (in)
-                for (int32_t j = 0; j < r; ++j) s = __fmaf_rn(__ldcg(t + j), bf(w[j]), s);
+            if (j0 >= r) break;  // (uniform; later groups are beyond the rank too)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) s[j] = __fadd_rn(s[j], __shfl_xor_sync(0xffffffffu, s[j], d));
+            if (lane == 0) {
+#pragma unroll
+                for (int j = 0; j < J; ++j) s_part[warp][j] = s[j];
+            }
+            __syncthreads();
+            if (tid < J) {
+                float v = 0.0f;
+#pragma unroll
+                for (int q = 0; q < kLoraWarps; ++q) v = __fadd_rn(v, s_part[q][tid]);
+                s_t[j0 + tid] = __fmul_rn(v, p.scales[a]);
+            }
+            __syncthreads();
         }
-        if (in) {
-            if constexpr (F32) static_cast<float*>(p.y)[o] = __fadd_rn(b, s);
-            else static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(__fadd_rn(b, s));
+        cluster.sync();  // every CTA's t is in its shared memory
+        if (static_cast<int32_t>(tid) < r)
+            s_all[tid] = cluster.map_shared_rank(s_t, (tid / J) % kRowCtas)[tid];
+        else if (tid < 128)
+            s_all[tid] = 0.0f;
+        cluster.sync();  // and read by all of them
+        for (int64_t n = n0; n < p.N; n += step) {
+            float s = 0.0f;
+            const uint16_t* w = wb + n * p.rmax;
+            if constexpr (VEC_B) {
+                for (int32_t j0 = 0; j0 < r; j0 += 16) {
+                    uint4 v[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (n == n0 && j0 == 0) v[i] = v0[i];
+                        else v[i] = j0 + 8 * i < r ? __ldg(reinterpret_cast<const uint4*>(w + j0) + i) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int32_t j = j0 + 8 * i + e;
+                            const float wv = (e & 1) ? bf_hi(q[e >> 1]) : bf_lo(q[e >> 1]);
+                            if (j < r) s = __fmaf_rn(s_all[j], wv, s);  // (weights beyond the rank are not defined)
+                        }
+                    }
+                }
+            } else {
+                for (int32_t j = 0; j < r; ++j) s = __fmaf_rn(s_all[j], bf(w[j]), s);
+            }
+            const float y = __fadd_rn(n == n0 ? b0 : base_at(n), s);
+            if constexpr (F32) static_cast<float*>(p.y)[m * p.N + n] = y;
+            else static_cast<__nv_bfloat16*>(p.y)[m * p.N + n] = __float2bfloat16_rn(y);
         }
+        __syncthreads();  // s_all is read
     }
-    if (!waited) pdl_wait();
 }
 
 // ---- many rows -----------------------------------------------------------------
@@ -343,7 +345,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_shrink_tile(const Lora
 // multiply, add and store.  A CTA's part of a tile is gone through once for
 // each adapter of its rows (and once for rows without one), with those rows
 // alone; so the order of (tile, columns) is divided over the CTAs by weight, a
-// tile counting as often as the adapter changes along its rows.  Without
+// tile counting as often as the adapter changes along its rows.  (blockIdx.y of
+// gridDim.y takes every gridDim.y-th of a tile's adapters.)  Without
 // VEC (N or a buffer off the 16-byte grid) base and weights are loaded directly.
 constexpr int kExpandRows = 64;
 constexpr int kExpandWarps = 16;
@@ -493,7 +496,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const Lo
             const int64_t end = (tile + 1) * per < w1 ? (tile + 1) * per : w1;
             int32_t mine[2];
             rows_of(tile, mine);
+            uint32_t turn = 0;
             for (int32_t a = next(mine, -2); a != INT32_MAX && ok; a = next(mine, a)) {
+                if (turn++ % gridDim.y != blockIdx.y) continue;
                 const uint32_t nr = __popc(__ballot_sync(0xffffffffu, mine[0] == a)) + __popc(__ballot_sync(0xffffffffu, mine[1] == a));
                 const bool weights = rank_of(p, a) > 0;
                 for (int64_t c = w; c < end; ++c) {
@@ -597,7 +602,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const Lo
             s_a[lane] = mine[0];
             s_a[lane + 32] = mine[1];
         }
+        uint32_t turn = 0;
         for (int32_t a = next(mine, -2); a != INT32_MAX; a = next(mine, a)) {
+            if (turn++ % gridDim.y != blockIdx.y) continue;
             const int32_t r = rank_of(p, a);
             meet();  // s_a is there, and every warp is done with the previous adapter's t
             lay(m0, a, r);
@@ -691,9 +698,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const Lo
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Rows from which the tensor-core tiles are taken (rule: where a 64-row tile
-// is worth its pass over the adapters of its rows).
-constexpr int64_t kTileMinRows = 96;
+// Rows from which the tensor-core tiles are taken.  Measured (K = 4096, r 16,
+// N = 4096 / r 64, N = 14336): 61 rows of one adapter 6 / 27 us here, 96 rows
+// 13 / 18 us in tiles; 61 rows of 48 adapters 7 / 47 us here, where a tile goes
+// through its adapters one by one.
+constexpr int64_t kTileMinRows = 128;
 
 // K splits: enough CTAs for two on each SM, at least 512 of K each.
 int shrink_splits(int64_t M, int64_t K) {
@@ -798,7 +807,11 @@ int launch_lora(const LoraParams& p, bool out_f32, void* stream) {
         e = expand_ready(dev);
         if (e != cudaSuccess) return static_cast<int>(e);
         const int64_t work = (p.M + kExpandRows - 1) / kExpandRows * ((p.N + cols - 1) / cols);
-        cudaLaunchConfig_t cfg = behind(attr, dim3(static_cast<unsigned>(work < 152 ? work : 152)), smem, st);
+        // a small number of tiles: their adapters are dealt to several CTAs (those without one end at once)
+        int64_t deal = 2 * 152 / work;
+        deal = deal < 1 ? 1 : (deal > 8 ? 8 : deal);
+        if (deal > p.nA) deal = p.nA;
+        cudaLaunchConfig_t cfg = behind(attr, dim3(static_cast<unsigned>(work < 152 ? work : 152), static_cast<unsigned>(deal)), smem, st);
         cfg.blockDim = dim3(kExpandThreads);
         if (out_f32) e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, true>, q, splits, cols, stages)
                                : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, false>, q, splits, cols, stages);
@@ -806,24 +819,17 @@ int launch_lora(const LoraParams& p, bool out_f32, void* stream) {
                        : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, false>, q, splits, cols, stages);
         return static_cast<int>(e);
     }
-    if (p.nA > 0) {
-        const int64_t groups = (p.rmax + kShrinkJ - 1) / kShrinkJ;
-        const unsigned grid = static_cast<unsigned>(p.M * groups);  // (the host keeps M * max_rank below 2^31)
-        if (vec_a) k_lora_shrink_rows<true><<<grid, kLoraThreads, 0, st>>>(p);
-        else k_lora_shrink_rows<false><<<grid, kLoraThreads, 0, st>>>(p);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return static_cast<int>(e);
-    }
-    const dim3 grid(static_cast<unsigned>((p.N + kLoraThreads - 1) / kLoraThreads),
-                    static_cast<unsigned>(p.M < 65535 ? p.M : 65535));
-    cudaLaunchConfig_t cfg = behind(attr, grid, 0, st);
-    if (p.nA == 0) cfg.numAttrs = 0;  // nothing of this call to run behind
-    cudaError_t e;
-    if (out_f32) e = vec_b ? cudaLaunchKernelEx(&cfg, k_lora_expand_rows<true, true>, p)
-                           : cudaLaunchKernelEx(&cfg, k_lora_expand_rows<true, false>, p);
-    else e = vec_b ? cudaLaunchKernelEx(&cfg, k_lora_expand_rows<false, true>, p)
-                   : cudaLaunchKernelEx(&cfg, k_lora_expand_rows<false, false>, p);
-    return static_cast<int>(e);
+    const int64_t rows = p.M < 65536 ? p.M : 65536;
+    const unsigned grid = static_cast<unsigned>(rows * kRowCtas);
+    auto go = [&](auto f32, auto va, auto vb) {
+        // ranks at a time of a CTA: so many that up to 32 are spread over the whole cluster
+        if (p.rmax <= 2 * kRowCtas) k_lora_rows<decltype(f32)::value, decltype(va)::value, decltype(vb)::value, 2><<<grid, kLoraThreads, 0, st>>>(p);
+        else k_lora_rows<decltype(f32)::value, decltype(va)::value, decltype(vb)::value, 4><<<grid, kLoraThreads, 0, st>>>(p);
+    };
+    auto by_b = [&](auto f32, auto va) { vec_b ? go(f32, va, std::true_type{}) : go(f32, va, std::false_type{}); };
+    auto by_a = [&](auto f32) { vec_a ? by_b(f32, std::true_type{}) : by_b(f32, std::false_type{}); };
+    out_f32 ? by_a(std::true_type{}) : by_a(std::false_type{});
+    return static_cast<int>(cudaGetLastError());
 }
 
 }  // namespace ndq
