@@ -230,24 +230,6 @@ __device__ __noinline__ uint32_t encode4(float4 v, float s) {
     }
 }
 
-// The codes of four values as four numbers already divided: no special cases.
-template <bool E4M3>
-__device__ __forceinline__ uint32_t round4(float a, float b, float c, float d) {
-    if constexpr (E4M3) {
-        uint32_t r;
-        asm("{\n.reg .b16 l, h;\ncvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\ncvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\nmov.b32 %0, {l, h};\n}"
-            : "=r"(r)
-            : "f"(a), "f"(b), "f"(c), "f"(d));
-        return r;
-    } else {
-        // to nearest even by adding 1.5 * 2^23: the low byte is the code (|quotient| < 128)
-        constexpr float kBig = 12582912.0f;
-        const uint32_t ab = __byte_perm(__float_as_uint(__fadd_rn(a, kBig)), __float_as_uint(__fadd_rn(b, kBig)), 0x0040);
-        const uint32_t cd = __byte_perm(__float_as_uint(__fadd_rn(c, kBig)), __float_as_uint(__fadd_rn(d, kBig)), 0x0040);
-        return __byte_perm(ab, cd, 0x5410);
-    }
-}
-
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -259,13 +241,36 @@ __device__ __forceinline__ float2 pair_mul(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ void pair_fma(uint64_t a, uint64_t b, uint64_t c, uint32_t& x, uint32_t& y) {
+    asm("{\n.reg .b64 m;\nfma.rn.f32x2 m, %2, %3, %4;\nmov.b64 {%0, %1}, m;\n}" : "=r"(x), "=r"(y) : "l"(a), "l"(b), "l"(c));
+}
+// Four quotients to E4M3 codes.
+__device__ __forceinline__ uint32_t round_e4m3(float2 a, float2 b) {
+    uint32_t r;
+    asm("{\n.reg .b16 l, h;\ncvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\ncvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\nmov.b32 %0, {l, h};\n}"
+        : "=r"(r)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
 // encode4 for finite values of at most Q s: the pairs lo and hi enclose 1 / s.
 template <bool E4M3>
 __device__ __forceinline__ uint32_t encode4_fast(float2 v, float2 w, float s, uint64_t lo, uint64_t hi) {
     const uint64_t pv = pair(v.x, v.y), pw = pair(w.x, w.y);
-    const float2 a0 = pair_mul(pv, lo), a1 = pair_mul(pw, lo), b0 = pair_mul(pv, hi), b1 = pair_mul(pw, hi);
-    const uint32_t a = round4<E4M3>(a0.x, a0.y, a1.x, a1.y), b = round4<E4M3>(b0.x, b0.y, b1.x, b1.y);
-    if (a == b) return a;
+    if constexpr (E4M3) {
+        const uint32_t a = round_e4m3(pair_mul(pv, lo), pair_mul(pw, lo)), b = round_e4m3(pair_mul(pv, hi), pair_mul(pw, hi));
+        if (a == b) return a;
+    } else {
+        // x / s + 1.5 * 2^23, rounded once to nearest even: the low byte is the code (|x / s| < 128)
+        const uint64_t big = pair(12582912.0f, 12582912.0f);
+        uint32_t a[4], b[4];
+        pair_fma(pv, lo, big, a[0], a[1]);
+        pair_fma(pw, lo, big, a[2], a[3]);
+        pair_fma(pv, hi, big, b[0], b[1]);
+        pair_fma(pw, hi, big, b[2], b[3]);
+        if (((a[0] ^ b[0]) | (a[1] ^ b[1]) | (a[2] ^ b[2]) | (a[3] ^ b[3])) == 0u)
+            return __byte_perm(__byte_perm(a[0], a[1], 0x0040), __byte_perm(a[2], a[3], 0x0040), 0x5410);
+    }
     return encode4<E4M3>(make_float4(v.x, v.y, w.x, w.y), s);
 }
 
@@ -291,7 +296,7 @@ __device__ __forceinline__ float finite_abs(float x) {
 // TEAM warps work on a run together.  win (at most 32): the tokens a team
 // searches for runs that start among them.
 template <int D, bool E4M3, bool BF16, int TEAM>
-__global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendParams p, int win) {
+__global__ void __launch_bounds__(kAppendWarps * 32, TEAM > 1 ? 6 : 4) k_kv_append(const AppendParams p, int win) {
     constexpr int LPR = D / 4;              // lanes per row, four values each
     constexpr int RPP = TEAM * 32 / LPR;    // rows per pass of the team
     constexpr float kQmax = E4M3 ? 448.0f : 127.0f;
@@ -340,14 +345,19 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
         // the run's length: up to bs tokens of the same block; dense: at adjacent slots, as a plan gives them
         int cnt = 0;
         bool dense = true;
-        for (int i0 = 0; i0 < bs; i0 += 32) {
-            const int64_t t = t0 + i0 + lane;
-            const int64_t st = t < p.n_tokens ? p.slots[t] : -1;
-            const uint32_t m = __ballot_sync(0xffffffffu, (st >> bl) == blk);
+        int64_t ahead[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t t = t0 + 32 * i + lane;
+            ahead[i] = 32 * i < bs && t < p.n_tokens ? p.slots[t] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (32 * i >= bs || cnt < 32 * i) break;
+            const uint32_t m = __ballot_sync(0xffffffffu, (ahead[i] >> bl) == blk);
             const int k = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
-            dense = dense && __all_sync(0xffffffffu, static_cast<int>(lane) >= k || st == s0 + i0 + static_cast<int64_t>(lane));
+            dense = dense && __all_sync(0xffffffffu, static_cast<int>(lane) >= k || ahead[i] == s0 + 32 * i + static_cast<int64_t>(lane));
             cnt += k;
-            if (k < 32) break;
         }
         if (cnt > bs) cnt = bs;
         const int n_old = static_cast<int>(s0 & (bs - 1));
@@ -386,20 +396,22 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_kv_append(const AppendPar
         const float s = fmaxf(old, fresh);
         // (a scale cut off at 2^100 leaves values beyond Q s: to be saturated)
         const bool fast = !odd && s > 0.0f && s < 0x1p100f;
-        const float y = fast ? __fdividef(1.0f, s) : 0.0f;
+        const float y = s > 0.0f ? __fdividef(1.0f, s) : 0.0f;
         const float lo = __fmul_rn(y, 1.0f - 0x1p-21f), hi = __fmul_rn(y, 1.0f + 0x1p-21f);
         const uint64_t lo2 = pair(lo, lo), hi2 = pair(hi, hi);
         uint8_t* out = codes + (unit << bl) * D + col;
         if (old > 0.0f && s > old) {  // the earlier tokens' codes under the grown scale
-#pragma unroll 2
+#pragma unroll 4
             for (int r = row; r < n_old; r += RPP) {
                 uint32_t* w = reinterpret_cast<uint32_t*>(out + r * D);
+                const bool far = !E4M3 && __vcmpeq4(*w, 0x80808080u) != 0u;  // a code of -128, beyond Q, is to be saturated
                 float4 v = decode4<E4M3>(*w);
                 v.x = __fmul_rn(v.x, old);
                 v.y = __fmul_rn(v.y, old);
                 v.z = __fmul_rn(v.z, old);
                 v.w = __fmul_rn(v.w, old);
-                *w = encode4<E4M3>(v, s);
+                // (below Q s, or NaN codes, which stay: the short way whatever the new values hold)
+                *w = s < 0x1p100f && !far ? encode4_fast<E4M3>(make_float2(v.x, v.y), make_float2(v.z, v.w), s, lo2, hi2) : encode4<E4M3>(v, s);
             }
         }
         auto put = [&](const uint2& w, int r) {

@@ -704,10 +704,11 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // through its adapters one by one.
 constexpr int64_t kTileMinRows = 128;
 
-// K splits: enough CTAs for two on each SM, at least 512 of K each.
+// K splits: as many CTAs as two on each SM make at most (one more would wait
+// for a whole other round), at least 512 of K each.
 int shrink_splits(int64_t M, int64_t K) {
     const int64_t tiles = (M + kShrinkRows - 1) / kShrinkRows;
-    int64_t s = (2 * 152 + tiles - 1) / tiles;
+    int64_t s = 2 * 152 / tiles;
     if (s > K / 512) s = K / 512;
     if (s > kMaxSplit) s = kMaxSplit;
     return s < 1 ? 1 : static_cast<int>(s);
@@ -766,8 +767,8 @@ cudaError_t shrink_tile(const LoraParams& p, int splits, cudaStream_t st) {
 
 }  // namespace
 
-// Room for any M' <= M: M' * splits is at most 8 M' and, splits being
-// (304 + tiles - 1) / tiles, at most 64 (304 + tiles).
+// Room for any M' <= M: M' * splits is at most 8 M' and, splits being 304 / tiles
+// or 1, at most 64 (304 + tiles).
 size_t lora_workspace_bytes(int64_t M, int64_t rmax, int64_t K) {
     if (M < 1) M = 1;
     int64_t s = K / 512 < kMaxSplit ? K / 512 : kMaxSplit;

@@ -227,6 +227,21 @@ def test_append_special_values(code):
     check_append(k, v, slots, kc, ks, vc, vs, bs, code)
 
 
+@pytest.mark.parametrize("grow", [1.0 + 2.0 ** -10, 1.01, 3.0])
+def test_append_rescales_every_code(grow):
+    # a block whose earlier tokens hold every code there is (also -128, and the NaN codes), under a scale that grows
+    bs, D = 16, 64
+    for code in ("int8", "e4m3"):
+        kc = torch.zeros(2, 1, bs, D, dtype=torch.int8, device=DEV)
+        kc[1, 0, :4] = torch.arange(-128, 128, dtype=torch.int8, device=DEV).reshape(4, D)
+        kc = kc.view(CODES[code])
+        ks = torch.full((2, 1), 0.0123, device=DEV)
+        x = torch.zeros(3, 1, D, device=DEV)
+        x[1, 0, 7] = -0.0123 * QMAX[code] * grow
+        x = x.to(torch.float16)
+        check_append(x, x, [16 + 4, 16 + 5, 16 + 6], kc, ks, kc.clone(), ks.clone(), bs, code)
+
+
 def test_append_rows_of_a_wider_buffer():
     bs, heads, D = 32, 4, 64
     buf = torch.randn(50, 3 * heads * D + 8, device=DEV).to(torch.float16)
