@@ -31,6 +31,8 @@
 #include <cuda_runtime.h>
 
 #include <cooperative_groups.h>
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include <cstdint>
 #include <type_traits>
@@ -339,9 +341,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2) k_lora_shrink_tile(const Lora
 
 // Expansion of tiles of 64 rows, 256 columns (128 for wide binary32 cases) at a
 // time.  t's parts are laid out once a tile as A fragments in shared memory.
-// Warp 16 brings base (one bulk copy of a row's columns each: 16-byte loads
-// scattered over 64 rows read HBM at 2 TB/s) and the adapter's weights (one
-// piece of memory) into a ring; warps 0-15, 2 row halves by 8 column groups,
+// Warp 16 brings base (one tensor copy of the tile's rows; a bulk copy per row
+// took 80 cycles each to issue, 16-byte loads scattered over the rows read HBM
+// at 2 TB/s) and the adapter's weights (one piece of memory) into a ring; warps 0-15, 2 row halves by 8 column groups,
 // multiply, add and store.  A CTA's part of a tile is gone through once for
 // each adapter of its rows (and once for rows without one), with those rows
 // alone; so the order of (tile, columns) is divided over the CTAs by weight, a
@@ -392,7 +394,8 @@ __device__ __forceinline__ void cut_ranks(uint4& w, int32_t left) {
 }
 
 template <bool F32, bool VEC>
-__global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const LoraParams p, int splits, int cols, int stages) {
+__global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const LoraParams p, const __grid_constant__ CUtensorMap base_map,
+                                                                        int splits, int cols, int stages) {
     constexpr int PARTS = expand_parts(F32);
     constexpr int EL = F32 ? 4 : 2;
     extern __shared__ __align__(128) uint8_t s_buf[];
@@ -499,7 +502,6 @@ __global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const Lo
             uint32_t turn = 0;
             for (int32_t a = next(mine, -2); a != INT32_MAX && ok; a = next(mine, a)) {
                 if (turn++ % gridDim.y != blockIdx.y) continue;
-                const uint32_t nr = __popc(__ballot_sync(0xffffffffu, mine[0] == a)) + __popc(__ballot_sync(0xffffffffu, mine[1] == a));
                 const bool weights = rank_of(p, a) > 0;
                 for (int64_t c = w; c < end; ++c) {
                     const int64_t n0 = c % per * cols;
@@ -509,15 +511,19 @@ __global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const Lo
                     const uint32_t nc = static_cast<uint32_t>(p.N - n0 < cols ? p.N - n0 : cols);
                     const uint32_t wb = weights ? nc * static_cast<uint32_t>(rmax) * 2u : 0u;
                     uint8_t* d = ring + static_cast<uint32_t>(st) * stage;
-                    if (lane == 0) mbar_arrive_expect_tx(&s_full[st], nr * nc * EL + wb);
+                    if (lane == 0) {
+                        // (all 64 rows, zeros past M and N: those of other adapters are not looked at)
+                        mbar_arrive_expect_tx(&s_full[st], kExpandRows * static_cast<uint32_t>(cols) * EL + wb);
+                        asm volatile(
+                            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+                                "r"(smem_addr(d)),
+                            "l"(reinterpret_cast<uint64_t>(&base_map)), "r"(static_cast<int32_t>(n0)), "r"(static_cast<int32_t>(m0)),
+                            "r"(smem_addr(&s_full[st]))
+                            : "memory");
+                        if (weights)
+                            bulk_load(d + kExpandRows * static_cast<uint32_t>(cols) * EL, p.b + (static_cast<int64_t>(a) * p.N + n0) * p.rmax, wb, &s_full[st]);
+                    }
                     __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (mine[i] == a)
-                            bulk_load(d + (lane + 32 * i) * static_cast<uint32_t>(cols) * EL,
-                                      static_cast<const uint8_t*>(p.base) + ((m0 + lane + 32 * i) * p.N + n0) * EL, nc * EL, &s_full[st]);
-                    if (weights && lane == 0)
-                        bulk_load(d + kExpandRows * static_cast<uint32_t>(cols) * EL, p.b + (static_cast<int64_t>(a) * p.N + n0) * p.rmax, wb, &s_full[st]);
                     ++issued;
                 }
             }
@@ -729,6 +735,18 @@ cudaLaunchConfig_t behind(cudaLaunchAttribute* attr, dim3 grid, size_t smem, cud
 
 constexpr int kExpandSmem = 212 * 1024;  // (beside 10 KB of static shared memory)
 
+PFN_cuTensorMapEncodeTiled_v12000 box_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;  // (benign race: same value)
+    if (!encode) {
+        void* fp = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fp, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fp) return nullptr;
+        encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fp);
+    }
+    return encode;
+}
+
 cudaError_t expand_ready(int dev) {
     static bool ready[64];  // (concurrent first calls set the same attributes)
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -814,10 +832,22 @@ int launch_lora(const LoraParams& p, bool out_f32, void* stream) {
         if (deal > p.nA) deal = p.nA;
         cudaLaunchConfig_t cfg = behind(attr, dim3(static_cast<unsigned>(work < 152 ? work : 152), static_cast<unsigned>(deal)), smem, st);
         cfg.blockDim = dim3(kExpandThreads);
-        if (out_f32) e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, true>, q, splits, cols, stages)
-                               : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, false>, q, splits, cols, stages);
-        else e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, true>, q, splits, cols, stages)
-                       : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, false>, q, splits, cols, stages);
+        CUtensorMap map = {};
+        if (vec_y) {  // base as [M, N], boxes of 64 rows by `cols`
+            const PFN_cuTensorMapEncodeTiled_v12000 encode = box_encoder();
+            if (!encode) return static_cast<int>(cudaErrorNotSupported);
+            const cuuint64_t gdim[2] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.M)};
+            const cuuint64_t gstride[1] = {static_cast<cuuint64_t>(p.N) * (out_f32 ? 4u : 2u)};
+            const cuuint32_t box[2] = {static_cast<cuuint32_t>(cols), kExpandRows}, estride[2] = {1u, 1u};
+            if (encode(&map, out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p.base), gdim,
+                       gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return static_cast<int>(cudaErrorInvalidValue);
+        }
+        if (out_f32) e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, true>, q, map, splits, cols, stages)
+                               : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<true, false>, q, map, splits, cols, stages);
+        else e = vec_y ? cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, true>, q, map, splits, cols, stages)
+                       : cudaLaunchKernelEx(&cfg, k_lora_expand_tile<false, false>, q, map, splits, cols, stages);
         return static_cast<int>(e);
     }
     const int64_t rows = p.M < 65536 ? p.M : 65536;
