@@ -2,9 +2,10 @@
 
 Argument marshalling only: every decode step runs in the library's CUDA
 kernels.  The ``ndq_*`` functions mirror the C ABI in ``include/ndq.h`` one
-to one (plain integers and pointers); ``dequantize_packed`` and
-``dequantize_packed_batched`` are conveniences that take torch CUDA tensors
-and the current torch stream.  There is no CPU fallback: importing this
+to one (plain integers and pointers); ``dequantize_packed``,
+``dequantize_packed_batched``, ``matmul_packed``, ``kv_plan``, ``kv_append``,
+``attention_kv8``, ``lora_add`` and the like are conveniences that take torch
+CUDA tensors and the current torch stream.  There is no CPU fallback: importing this
 module fails if the library has not been built
 (``python -m quantized_weight_block_gb300.build``).
 """
