@@ -399,7 +399,8 @@ int ndq_kv_plan(const int32_t *cached, const int32_t *fresh, int64_t n_req, int 
  *   code  = x / s rounded to nearest even and saturated (0 when s is 0); NaN
  *           becomes the NaN code in E4M3 and 0 in INT8
  * and when s > old > 0 the codes c of the block's earlier tokens become
- * (c * old) / s, rounded the same way.  n_tokens of 0 is valid. */
+ * (c * old) / s, rounded the same way.  n_tokens of 0 is valid;
+ * n_tokens * kv_heads is at most 2^33. */
 int ndq_kv_append(const ndq_kv_cache *cache, const void *k, const void *v, int in_dtype, int64_t k_stride,
                   int64_t v_stride, const int64_t *slots, int64_t n_tokens, void *stream);
 

@@ -92,7 +92,7 @@ int ndq_kv_append(const ndq_kv_cache* cache, const void* k, const void* v, int i
     int rc = check_cache(cache, &p.c);
     if (rc != NDQ_OK) return rc;
     if (n_tokens < 0) return NDQ_ERR_NEGATIVE_DIM;
-    if (n_tokens > INT32_MAX) return NDQ_ERR_BAD_ARG;
+    if (n_tokens > INT32_MAX || n_tokens > (INT64_C(1) << 33) / cache->kv_heads) return NDQ_ERR_BAD_ARG;  // (the launch's blocks)
     if (in_dtype != NDQ_BFLOAT16 && in_dtype != NDQ_FLOAT16) return NDQ_ERR_BAD_DTYPE;
     if (n_tokens == 0) return NDQ_OK;
     if (!k || !v || !slots) return NDQ_ERR_NULL;

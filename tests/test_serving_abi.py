@@ -109,3 +109,8 @@ def test_lora_refusals(kw, want):
 
 def test_descriptor_layout_matches_the_header():
     assert ctypes.sizeof(ndq.ndq_kv_cache) == 4 * 8 + 8 + 4 * 4
+
+
+def test_append_launch_limit():
+    rows = dict(k_stride=4096 * 128, v_stride=4096 * 128)
+    assert append(cache(kv_heads=4096), n_tokens=(1 << 21) + 1, **rows) == BAD_ARG
