@@ -308,12 +308,8 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         // lane i: K's scale, log2 of V's and its reciprocal (V of scale 0: its codes are taken as zeros)
         float ks_l, ve_l, vinv_l;
         auto scales = [&]() {
-            float f, e, inv, lg;
-            split_scale(now.vs, f, e, inv);
-            asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(now.vs == 0.0f ? 1.0f : f));
             ks_l = now.ks;
-            ve_l = e + lg;
-            vinv_l = now.vs == 0.0f ? 1.0f : __fdividef(1.0f, now.vs);
+            value_scale(now.vs, ve_l, vinv_l);
         };
         scales();
 

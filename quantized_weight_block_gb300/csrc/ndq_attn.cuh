@@ -87,19 +87,21 @@ __device__ __forceinline__ void row_scale(float amax, float& up, float& down) {
     down = __uint_as_float(static_cast<uint32_t>(127 + s) << 23);
 }
 
-// A cache scale as f * 2^e with f in [1, 2) (0: as 1, its codes count for
-// nothing or are scaled by f = 0), and 2^-e.
-__device__ __forceinline__ void split_scale(float s, float& f, float& e, float& inv) {
-    const uint32_t b = __float_as_uint(s);
-    if (!(s > 0.0f)) {  // zero (or NaN, which stays one)
-        f = s;
-        e = 0.0f;
-        inv = 1.0f;
+// log2 of V's scale and its reciprocal.  A block of scale 0 counts as zeros
+// under a scale of 2^-30: its weights add to the denominator alone, and with a
+// scale of 1 they could raise the maximum so far that binary16 loses the
+// weights of blocks of small values.  (NaN stays NaN.)
+__device__ __forceinline__ void value_scale(float s, float& lg, float& inv) {
+    if (s == 0.0f) {
+        lg = -30.0f;
+        inv = 0x1p30f;
         return;
     }
-    f = __uint_as_float((b & 0x007fffffu) | 0x3f800000u);
-    e = static_cast<float>(static_cast<int>(b >> 23) - 127);
-    inv = __uint_as_float((254u - (b >> 23)) << 23);
+    const uint32_t b = __float_as_uint(s);
+    const float f = s > 0.0f ? __uint_as_float((b & 0x007fffffu) | 0x3f800000u) : s;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(f));
+    lg += s > 0.0f ? static_cast<float>(static_cast<int>(b >> 23) - 127) : 0.0f;
+    inv = __fdividef(1.0f, s);
 }
 
 // Request r's first query row, queries and tokens, kept inside the buffers

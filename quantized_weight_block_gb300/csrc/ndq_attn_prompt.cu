@@ -69,6 +69,7 @@ struct PrShared {
     uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
     uint64_t sfull[2], pfull[2], odone[2];
     float4 cst[kPrCst][kPrGroups];  // per group: K's scale, log2 of V's scale, 1 / V's scale
+    uint32_t gap[kPrCst];           // a block of the tile is missing
     uint32_t tmem;
     uint32_t fault;
     uint32_t nan;   // V has NaN codes in a tile that some rows see only part of
@@ -449,20 +450,21 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                         const int32_t tk = tok0 + (j + static_cast<int32_t>(lane >> 3)) * kPrTokens + static_cast<int32_t>(gl) * 16;
                         off = ((u << bl) + (static_cast<uint32_t>(tk) & ((1u << bl) - 1u))) * D;
                         const float vs = p.c.vs[u];
-                        float f, e, inv, lg;
-                        split_scale(vs, f, e, inv);
-                        asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(vs == 0.0f ? 1.0f : f));
-                        // (a block of V of scale 0 counts as zeros)
-                        c = make_float4(p.c.ks[u], e + lg, vs == 0.0f ? 1.0f : __fdiv_rn(1.0f, vs), vs == 0.0f ? 0.0f : 1.0f);
+                        float lg, inv;
+                        value_scale(vs, lg, inv);
+                        c = make_float4(p.c.ks[u], lg, inv, vs == 0.0f ? 0.0f : 1.0f);
                     }
                 }
                 const bool mine = static_cast<int32_t>(lane >> 3) == (j & 3);
                 const uint32_t n16 = __popc(__ballot_sync(0xffffffffu, mine && ids >= 0));
+                const int32_t left = any_hi - (tok0 + j * kPrTokens);  // (of the tile's groups, those that some row sees)
+                const uint32_t seen = left >= kPrTokens ? kPrGroups : static_cast<uint32_t>(left + 15) >> 4;
                 for (int32_t half = 0; half < 2; ++half) {  // K, V
                     const uint32_t rs = static_cast<uint32_t>(half);
                     if (j >= 1) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.rawfree[rs], static_cast<uint32_t>((j - 1) & 1)));
                     if (!ok) break;
                     if (half == 0 && mine) S.cst[j % kPrCst][gl] = c;
+                    if (half == 0 && lane == 0) S.gap[j % kPrCst] = n16 < seen ? 1u : 0u;
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(&S.rawfull[rs], n16 * 16u * D);
                     __syncwarp();
@@ -567,9 +569,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         float ms = 0.0f;
         bool ok = true;
         uint32_t w[kPrTokens / 2];  // the row's weights of the tile, in pairs
-        // The weights relative to ms, their sum and the largest exponent.
-        auto weigh = [&](auto mask, const float4* cst, int32_t tb, float& ts, float& top) {
-            constexpr bool kMasked = decltype(mask)::value;
+        // The weights relative to ms (and less), their sum and the largest exponent.
+        auto weigh = [&](auto mask, auto again, float less, const float4* cst, int32_t tb, float& ts, float& top) {
+            constexpr bool kMasked = decltype(mask)::value, kAgain = decltype(again)::value;
             uint32_t v[2][16];
             ts = 0.0f;
             float tops[2] = {-INFINITY, -INFINITY};
@@ -589,7 +591,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 if constexpr (kMasked) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        if (pos + e < see_lo || pos + e >= see_hi) y[e] = -INFINITY;
+                        if (pos + e < see_lo || pos + e >= see_hi || k.y == -INFINITY) y[e] = -INFINITY;
+                }
+                if constexpr (kAgain) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) y[e] -= less;
                 }
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) tops[(e >> 1) & 1] = max3(tops[(e >> 1) & 1], y[e], y[e + 1]);
@@ -611,20 +617,17 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             if (!ok) break;
             tc_fence_after();
             const int32_t tb = tok0 + j * kPrTokens;
-            const bool masked = tb + kPrTokens > all_hi || tb < all_lo;
+            const bool masked = tb + kPrTokens > all_hi || tb < all_lo || S.gap[j % kPrCst] != 0u;
             const float4* cst = S.cst[j % kPrCst];
             float ts, top;
-            bool waited = false;
-            // (again when a row passed its maximum by 8: always for the first tile that it sees, rarely later)
-            for (int again = 0; again < 3; ++again) {
-                if (masked) weigh(std::true_type{}, cst, tb, ts, top);
-                else weigh(std::false_type{}, cst, tb, ts, top);
-                const bool grow = top > (mx == -INFINITY ? -INFINITY : 8.0f);
-                if (!__any_sync(0xffffffffu, grow)) break;
+            if (masked) weigh(std::true_type{}, std::false_type{}, 0.0f, cst, tb, ts, top);
+            else weigh(std::false_type{}, std::false_type{}, 0.0f, cst, tb, ts, top);
+            const bool grow = top > (mx == -INFINITY ? -INFINITY : 8.0f);
+            // a row passed its maximum by 8: always in the first tile that it sees, rarely later
+            if (__any_sync(0xffffffffu, grow)) {
                 const float al = !grow ? 1.0f : (mx == -INFINITY ? 0.0f : exp2_fast(-top));
                 if (j > 0) {  // O moves to the new maximum once the product before this one is done with it
-                    if (!waited) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((j - 1) & 1)));
-                    waited = true;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((j - 1) & 1)));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -639,9 +642,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     tmem_wait_st();
                 }
                 sum *= al;
-                if (grow) mx = ms = ms + top;
+                // the same exponents less the growth, so that the largest is 0 whatever ms + top is rounded to
+                const float less = grow ? top : 0.0f;
+                weigh(std::true_type{}, std::true_type{}, less, cst, tb, ts, top);
+                if (grow) mx = ms = ms + less;
             }
-            if (!ok) break;
             sum += ts;
             tmem_st32(tS, w);
             tmem_st32(tS + 32, w + 32);

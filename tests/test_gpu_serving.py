@@ -508,6 +508,57 @@ def test_attend_lengths_outside_the_buffers_are_cut():
     assert (guard[:2] == 5).all() and (guard[-2:] == 5).all()
 
 
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("n", [1, 4, 140])
+def test_attend_zero_blocks_beside_small_values(code, n):
+    # blocks of values 0 (scale 0) take nothing from the weights of small values
+    bs, D = 16, 128
+    kv = [400, 1200]
+    q, kc, ks, vc, vs, table, start = attend_case(kv, [n, n], 8, 2, D, bs, code, torch.bfloat16, 12)
+    vs *= 2.0 ** -14
+    vs[::5] = 0.0
+    want, bound, _ = attend_ref(q, kc, ks, vc, vs, table, kv, start, bs, D ** -0.5, 0, torch.bfloat16)
+    out = ndq.attention_kv8(q, ndq.KvCache(kc, vc, ks, vs), torch.from_numpy(table).to(DEV), dev32(kv), q_start=dev32(start))
+    err = (out.double() - want).abs()
+    assert (err <= bound).all(), float((err / bound).max())
+
+
+@pytest.mark.parametrize("scale", [1e6, -1e6, 1e9])
+@pytest.mark.parametrize("n", [1, 6, 150])
+def test_attend_scores_whose_roundings_pass_the_exponents(n, scale):
+    # scores 1e7 and more apart: the largest takes all, in every kernel, and
+    # its value (7 bits) is exact
+    bs, D, kv, H = 16, 128, 250, 2
+    nb = -(-kv // bs)
+    key = torch.from_numpy(np.random.default_rng(3).permutation(kv) - 125)
+    kc, vc = (torch.zeros(nb, H, bs, D, dtype=torch.int8) for _ in range(2))
+    g = torch.Generator().manual_seed(3)
+    v = torch.randint(-127, 128, (kv, H, D), generator=g)
+    for j in range(kv):
+        kc[j // bs, :, j % bs] = key[j]
+        vc[j // bs, :, j % bs] = v[j].to(torch.int8)
+    cache = ndq.KvCache(kc.to(DEV), vc.to(DEV), torch.ones(nb, H, device=DEV), torch.full((nb, H), 2.0 ** -6, device=DEV))
+    q = torch.ones(n, 4 * H, D, dtype=torch.bfloat16, device=DEV)
+    table = torch.arange(nb, dtype=torch.int32, device=DEV)[None]
+    out = ndq.attention_kv8(q, cache, table, dev32([kv]), q_start=dev32([0, n]), scale=scale).cpu()
+    for i in range(n):
+        seen = key[:kv - n + i + 1] * (1 if scale > 0 else -1)
+        want = v[int(seen.argmax())].to(torch.float32).repeat_interleave(4, 0) * 2.0 ** -6
+        assert torch.equal(out[i].float(), want), i
+
+
+@pytest.mark.parametrize("n", [1, 5, 150])
+def test_attend_nan_queries_that_see_nothing(n):
+    q, kc, ks, vc, vs, table, start = attend_case([400, 300], [n, n], 8, 2, 128, 16, "e4m3", torch.bfloat16, 13)
+    q[n:] = float("nan")
+    table[1] = -1
+    lse = torch.zeros(q.shape[:2], device=DEV)
+    out = ndq.attention_kv8(q, ndq.KvCache(kc, vc, ks, vs), torch.from_numpy(table).to(DEV), dev32([400, 300]),
+                            q_start=dev32(start), lse=lse)
+    assert torch.isfinite(out).all() and int(out[n:].count_nonzero()) == 0
+    assert torch.isfinite(lse[:n]).all() and (lse[n:] == -float("inf")).all()
+
+
 # ---- adapters ----------------------------------------------------------------------
 
 
