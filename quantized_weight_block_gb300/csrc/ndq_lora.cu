@@ -368,6 +368,10 @@ __host__ __device__ constexpr int expand_stage_bytes(bool f32, int rmax, int col
     return kExpandRows * cols * (f32 ? 4 : 2) + cols * rmax * 2;
 }
 
+// What a bfloat16 part leaves of v: at most 2^119.  The bounds are for infinite
+// parts, of which nothing is left: a finite rest (of NaN, too) keeps them what they are.
+__device__ __forceinline__ float rest(float v, float part) { return fminf(fmaxf(__fsub_rn(v, part), -0x1p119f), 0x1p119f); }
+
 // Splits 8 values of t into PARTS bfloat16 A fragments: rows g (v[0]) and g + 8 (v[1]) of four adjacent ranks.
 template <int PARTS>
 __device__ __forceinline__ void lay_parts(float (&v)[2][4], uint4* dst, int stride) {
@@ -379,14 +383,14 @@ __device__ __forceinline__ void lay_parts(float (&v)[2][4], uint4* dst, int stri
         f.z = pack_bf16(v[0][2], v[0][3]);
         f.w = pack_bf16(v[1][2], v[1][3]);
         dst[part * stride] = f;
-        v[0][0] = __fsub_rn(v[0][0], bf_lo(f.x));
-        v[0][1] = __fsub_rn(v[0][1], bf_hi(f.x));
-        v[1][0] = __fsub_rn(v[1][0], bf_lo(f.y));
-        v[1][1] = __fsub_rn(v[1][1], bf_hi(f.y));
-        v[0][2] = __fsub_rn(v[0][2], bf_lo(f.z));
-        v[0][3] = __fsub_rn(v[0][3], bf_hi(f.z));
-        v[1][2] = __fsub_rn(v[1][2], bf_lo(f.w));
-        v[1][3] = __fsub_rn(v[1][3], bf_hi(f.w));
+        v[0][0] = rest(v[0][0], bf_lo(f.x));
+        v[0][1] = rest(v[0][1], bf_hi(f.x));
+        v[1][0] = rest(v[1][0], bf_lo(f.y));
+        v[1][1] = rest(v[1][1], bf_hi(f.y));
+        v[0][2] = rest(v[0][2], bf_lo(f.z));
+        v[0][3] = rest(v[0][3], bf_hi(f.z));
+        v[1][2] = rest(v[1][2], bf_lo(f.w));
+        v[1][3] = rest(v[1][3], bf_hi(f.w));
     }
 }
 

@@ -644,3 +644,23 @@ def test_lora_unaligned_buffers():
         rows = (index == i).nonzero()[:, 0]
         want[rows] += (x[rows].double() @ a[i, :r].double().T * float(scales[i])) @ b[i, :, :r].double().T
     assert ((y.double() - want).abs() <= 2.0 ** -14 * want.abs().max()).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M", [3, 200])
+def test_lora_infinite_inputs(M, dtype):
+    # of rank 1, so that no two infinities meet: y is infinite with the sign of the product, NaN for NaN
+    g = torch.Generator(device=DEV).manual_seed(9)
+    K, N = 256, 512
+    x = torch.randn(M, K, device=DEV, generator=g).to(torch.bfloat16)
+    x[0, 5], x[1, 7], x[2, 9] = float("inf"), -float("inf"), float("nan")
+    a = torch.randn(1, 8, K, device=DEV, generator=g).to(torch.bfloat16)
+    b = torch.randn(1, N, 8, device=DEV, generator=g).to(torch.bfloat16)
+    a[a == 0], b[b == 0] = 1.0, 1.0
+    base = torch.randn(M, N, device=DEV, generator=g).to(dtype)
+    y = ndq.lora_add(x, a, b, dev32([1]), torch.ones(1, device=DEV), dev32([0] * M), base)
+    want = base.double() + (x.double() @ a[0, :1].double().T) @ b[0, :, :1].double().T
+    odd = ~torch.isfinite(want)
+    assert odd[:3].all() and not odd[3:].any()
+    assert torch.equal(y[:2].double(), want[:2]) and y[2].isnan().all()
+    assert torch.isfinite(y[3:]).all()
