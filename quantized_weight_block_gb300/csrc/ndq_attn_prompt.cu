@@ -28,8 +28,8 @@
 // is rescaled rarely; P is then at most 2^8.
 //
 // Measured: four chunks of 1200 to 4000 tokens over 2k to 8k earlier ones, 32
-// heads of 128 on 8 (1.19 TFLOP): 1.11-1.19 ms, 1.0-1.07 PFLOP/s, 0.55 of the
-// measured bfloat16 rate.  A product of 128 x 128 x 128 takes 810 cycles
+// heads of 128 on 8 (1.19 TFLOP): 1.11-1.23 ms, 0.97-1.07 PFLOP/s, 0.51-0.56 of
+// the measured bfloat16 rate.  A product of 128 x 128 x 128 takes 810 cycles
 // instead of 512: its operands and the converters together ask more of shared
 // memory than its 128 bytes a cycle.
 //
