@@ -421,8 +421,8 @@ int ndq_kv_append(const ndq_kv_cache *cache, const void *k, const void *v, int i
  *   q_start    device int32 [n_req + 1], or NULL when every request has
  *              exactly one query (n_tokens == n_req)
  *              (n_tokens * q_heads below 2^31)
- *   max_q      an upper bound of the queries of one request (host); queries
- *              beyond it are not computed
+ *   max_q      an upper bound of the queries of one request (host); of a
+ *              request with more, the first max_q are computed
  *   out        device [n_tokens, q_heads, head_dim] of dtype, dense
  *   lse        NULL, or device binary32 [n_tokens, q_heads]: the natural
  *              logarithm of the softmax denominator, -inf for an empty row
@@ -430,6 +430,10 @@ int ndq_kv_append(const ndq_kv_cache *cache, const void *k, const void *v, int i
  *              bytes, 16-byte aligned, its first 4096 bytes zeroed once before
  *              its first use (each call leaves them zero), not shared by
  *              calls that may overlap
+ * Rows of out and lse are written for the computed queries alone: not for
+ * those past max_q or n_tokens (a request that q_start lets pass n_tokens has
+ * its queries at the positions that all of them would have), nor for tokens
+ * of no request.
  * A query that sees nothing gives 0.  What is not seen has no influence,
  * whatever its codes stand for.  Scores, softmax statistics and sums are
  * binary32; query values and softmax weights enter the tensor cores as

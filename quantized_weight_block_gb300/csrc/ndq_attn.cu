@@ -85,7 +85,7 @@ __device__ __forceinline__ uint64_t udiv(uint64_t a, uint64_t b) {
 struct Req {
     int64_t q0;    // its first query row
     int32_t n;     // queries
-    int32_t kv;    // tokens
+    int32_t pos;   // position of the first one
     int32_t lo;    // first token any of its queries sees, a multiple of 16
     int32_t units; // units of one row tile (at least one, so that empty rows are written)
     int32_t tiles; // row tiles per cache head
@@ -99,14 +99,15 @@ __device__ __forceinline__ int32_t query_of(const AttnParams& p, int32_t row) {
 template <int ROWS>
 __device__ __forceinline__ Req request(const AttnParams& p, int64_t r) {
     Req x;
-    attn_request(p, r, x.q0, x.n, x.kv);
+    attn_request(p, r, x.q0, x.n, x.pos);
+    const int32_t end = x.pos + x.n;  // no query sees further
     if (p.prompt_rows > 0 && static_cast<int64_t>(x.n) * p.group >= p.prompt_rows) x.n = 0;  // the other kernel's
     x.lo = 0;
     if (p.window > 0) {
-        const int32_t first = x.kv - x.n + 1 - p.window;
+        const int32_t first = x.pos + 1 - p.window;
         x.lo = first > 0 ? first & ~(kRowTile - 1) : 0;
     }
-    x.units = x.kv > x.lo ? (x.kv - x.lo + kRowUnit - 1) / kRowUnit : 1;
+    x.units = end > x.lo ? (end - x.lo + kRowUnit - 1) / kRowUnit : 1;
     x.tiles = (x.n * p.group + ROWS - 1) / ROWS;
     return x;
 }
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         const int32_t rows_left = x.n * p.group - row0;
         const int32_t nrows = rows_left < kRows ? rows_left : kRows;
         const int32_t qa = query_of(p, row0), qb = query_of(p, row0 + nrows - 1);
-        const int32_t any_hi = x.kv - x.n + qb + 1, all_hi = x.kv - x.n + qa + 1;
+        const int32_t any_hi = x.pos + qb + 1, all_hi = x.pos + qa + 1;
         const int32_t any_lo = p.window > 0 ? all_hi - p.window : 0, all_lo = p.window > 0 ? any_hi - p.window : 0;
 
         // this warp's pairs: base token x.lo + 32 (8 c + warp), c = ca .. cb - 1
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         }
         // the tokens row i of the tile sees: [lo, hi)
         auto sees = [&](int32_t i, int32_t& lo, int32_t& hi) {
-            const int32_t pos = x.kv - x.n + query_of(p, row0 + i);
+            const int32_t pos = x.pos + query_of(p, row0 + i);
             hi = i < nrows && pos >= 0 ? pos + 1 : 0;
             lo = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
         };

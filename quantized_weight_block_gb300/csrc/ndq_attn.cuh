@@ -104,22 +104,25 @@ __device__ __forceinline__ void value_scale(float s, float& lg, float& inv) {
     inv = __fdividef(1.0f, s);
 }
 
-// Request r's first query row, queries and tokens, kept inside the buffers
-// whatever the device arrays hold.
-__device__ __forceinline__ void attn_request(const AttnParams& p, int64_t r, int64_t& q0, int32_t& n, int32_t& kv) {
-    int64_t a = r, b = r + 1;
+// Request r's first query row, the number of queries that are computed and the
+// position of the first one, kept inside the buffers whatever the device
+// arrays hold.  Queries past max_q or n_tokens are left out, but they count
+// for the positions: all of a request's queries are its last tokens.
+__device__ __forceinline__ void attn_request(const AttnParams& p, int64_t r, int64_t& q0, int32_t& n, int32_t& first) {
+    int64_t a = r, all = 1, room = 1;
     if (p.q_start) {
         a = p.q_start[r];
-        b = p.q_start[r + 1];
         a = a < 0 ? 0 : (a > p.n_tokens ? p.n_tokens : a);
-        b = b < a ? a : (b > p.n_tokens ? p.n_tokens : b);
+        all = p.q_start[r + 1] - a;
+        all = all < 0 ? 0 : all;
+        room = p.n_tokens - a < p.max_q ? p.n_tokens - a : p.max_q;
     }
     q0 = a;
-    n = static_cast<int32_t>(b - a < p.max_q ? b - a : p.max_q);
+    n = static_cast<int32_t>(all < room ? all : room);
     const int64_t most = p.width << p.c.bs_log2;
     int64_t len = p.kv_len[r];
     len = len < 0 ? 0 : (len > most ? most : len);
-    kv = static_cast<int32_t>(len);
+    first = static_cast<int32_t>(len - all > -(1 << 30) ? len - all : -(1 << 30));  // (before 0 in either case)
 }
 
 }  // namespace

@@ -188,8 +188,8 @@ __device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
 }
 
 // A request's units of 256 rows (0: left to the other kernel).
-__device__ __forceinline__ int64_t prompt_tiles(const AttnParams& p, int64_t r, int64_t& q0, int32_t& n, int32_t& kv) {
-    attn_request(p, r, q0, n, kv);
+__device__ __forceinline__ int64_t prompt_tiles(const AttnParams& p, int64_t r, int64_t& q0, int32_t& n, int32_t& pos0) {
+    attn_request(p, r, q0, n, pos0);
     const int64_t rows = static_cast<int64_t>(n) * p.group;
     return rows < p.prompt_rows ? 0 : (rows + kPromptRows - 1) / kPromptRows;
 }
@@ -218,11 +218,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     {
         const int64_t per = (p.n_req + kPrThreads - 1) / kPrThreads;
         int64_t q0;
-        int32_t n, kv;
+        int32_t n, pos0;
         uint64_t mine = 0;
         for (int64_t i = 0; i < per; ++i) {
             const int64_t r = tid * per + i;
-            if (r < p.n_req) mine += static_cast<uint64_t>(prompt_tiles(p, r, q0, n, kv)) * p.c.heads;
+            if (r < p.n_req) mine += static_cast<uint64_t>(prompt_tiles(p, r, q0, n, pos0)) * p.c.heads;
         }
         uint64_t incl = mine;
 #pragma unroll
@@ -268,13 +268,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     }
     __syncthreads();
     int64_t r = S.r, q0 = 0;
-    int32_t n = 0, kv = 0;
+    int32_t n = 0, pos0 = 0;  // queries and the position of the first
     uint64_t left = unit - static_cast<uint64_t>(S.base);
-    int64_t tiles = prompt_tiles(p, r, q0, n, kv);
+    int64_t tiles = prompt_tiles(p, r, q0, n, pos0);
     while (left >= static_cast<uint64_t>(tiles) * p.c.heads) {
         left -= static_cast<uint64_t>(tiles) * p.c.heads;
         ++r;
-        tiles = prompt_tiles(p, r, q0, n, kv);
+        tiles = prompt_tiles(p, r, q0, n, pos0);
     }
     const int32_t h = static_cast<int32_t>(left % p.c.heads);
     const int32_t row0 = static_cast<int32_t>(tiles - 1 - left / p.c.heads) * kPromptRows;
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     const int32_t nrows = rows_left < kPromptRows ? rows_left : kPromptRows;
     const int32_t nact = nrows > 128 ? 2 : 1;  // row tiles in use
     // tokens that some row / every row of the CTA sees
-    const int32_t first_pos = kv - n + row0 / p.group, last_pos = kv - n + (row0 + nrows - 1) / p.group;
+    const int32_t first_pos = pos0 + row0 / p.group, last_pos = pos0 + (row0 + nrows - 1) / p.group;
     const int32_t any_hi = last_pos + 1, cta_hi = first_pos + 1;
     const int32_t any_lo = p.window > 0 && first_pos + 1 > p.window ? first_pos + 1 - p.window : 0;
     const int32_t cta_lo = p.window > 0 ? last_pos + 1 - p.window : 0;
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             }
             *reinterpret_cast<uint4*>(dst + (c >> 3) * kAtom + sw128(wrow, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        const int32_t pos = kv - n + qi;
+        const int32_t pos = pos0 + qi;
         see_hi = has_row && pos >= 0 ? pos + 1 : 0;
         see_lo = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
         fence_proxy_async_smem();
@@ -564,8 +564,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         const uint32_t tS = tmem + 128u * wg + ((32u * (warp & 3u)) << 16), tO = tmem + kO + D * wg + ((32u * (warp & 3u)) << 16);
         const int32_t wrow0 = row0 + 128 * static_cast<int32_t>(wg);
         const int32_t wrows = nrows - 128 * static_cast<int32_t>(wg) < 128 ? nrows - 128 * static_cast<int32_t>(wg) : 128;
-        const int32_t all_hi = kv - n + wrow0 / p.group + 1;
-        const int32_t all_lo = p.window > 0 ? kv - n + (wrow0 + wrows - 1) / p.group + 1 - p.window : 0;
+        const int32_t all_hi = pos0 + wrow0 / p.group + 1;
+        const int32_t all_lo = p.window > 0 ? pos0 + (wrow0 + wrows - 1) / p.group + 1 - p.window : 0;
         float ms = 0.0f;
         bool ok = true;
         uint32_t w[kPrTokens / 2];  // the row's weights of the tile, in pairs

@@ -1,0 +1,62 @@
+"""GPU tests of the serving operators along the paths that only larger, cut or
+unusual calls take, with the definitions and bounds of test_gpu_serving.py.
+"""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_serving import DEV, attend_case, attend_ref, dev32, random_cache
+
+pytestmark = pytest.mark.gpu
+
+import quantized_weight_block_gb300 as ndq  # noqa: E402
+
+
+# ---- attention: calls that compute only some of a request's queries ----------------
+
+
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("n,most", [([3, 1, 2], 1), ([9, 2, 4], 4), ([300, 5, 70], 64), ([300, 150, 290], 260)])
+def test_attend_queries_beyond_max_q_leave_the_others_in_place(n, most, window):
+    # (the queries that are computed keep their positions, and the rest of out stays as it was)
+    kv, D, bs = [400, 333, 290], 128, 16
+    q, kc, ks, vc, vs, table, start = attend_case(kv, n, 8, 2, D, bs, "e4m3", torch.bfloat16, 71)
+    want, bound, lse_want = attend_ref(q, kc, ks, vc, vs, table, kv, start, bs, D ** -0.5, window, torch.bfloat16)
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device=DEV)
+    ndq.attention_kv8(q, ndq.KvCache(kc, vc, ks, vs), torch.from_numpy(table).to(DEV), dev32(kv), q_start=dev32(start),
+                      max_q=most, window=window, out=out, lse=lse)
+    for r, a in enumerate(start[:-1]):
+        c = a + min(n[r], most)
+        assert ((out[a:c].double() - want[a:c]).abs() <= bound[a:c]).all(), r
+        assert ((lse[a:c] - lse_want[a:c]).abs() <= 2.0 ** -13).all(), r
+        assert (out[c:start[r + 1]] == 7).all() and (lse[c:start[r + 1]] == 7).all(), r
+
+
+@pytest.mark.parametrize("fresh,n_tokens", [([1, 4, 3], 6), ([40, 2, 200], 100), ([700, 5], 512)])
+def test_plan_append_and_attention_with_room_for_fewer_tokens(fresh, n_tokens):
+    # a plan keeps the true lengths of a request that brings more tokens than there is room for
+    bs, H, D, cached = 16, 2, 64, [33, 0, 50][:len(fresh)]
+    R = len(fresh)
+    blocks = [-(-(c + f) // bs) for c, f in zip(cached, fresh)]
+    nb = sum(blocks) + 2
+    table = np.full((R, max(blocks) + 1), -1, dtype=np.int32)
+    at = 0
+    for r, c in enumerate(cached):
+        table[r, :-(-c // bs)] = np.arange(at, at - (-c // bs))
+        at += -(-c // bs)
+    tt = torch.from_numpy(table).to(DEV)
+    kc, ks = random_cache(nb, H, bs, D, "int8", 81)
+    vc, vs = random_cache(nb, H, bs, D, "int8", 82)
+    cache = ndq.KvCache(kc, vc, ks, vs)
+    plan = ndq.kv_plan(dev32(cached), dev32(fresh), bs, dev32(range(at, nb)), dev32([nb - at]), tt, n_tokens=n_tokens)
+    g = torch.Generator(device=DEV).manual_seed(83)
+    q = torch.randn(n_tokens, 4, D, device=DEV, generator=g).to(torch.bfloat16)
+    k, v = (torch.randn(n_tokens, H, D, device=DEV, generator=g).to(torch.bfloat16) for _ in range(2))
+    ndq.kv_append(cache, k, v, plan.slots)
+    out = ndq.attention_kv8(q, cache, tt, plan.kv_len, q_start=plan.q_start, max_q=max(fresh))
+    # the same rows as queries of requests of just so many tokens
+    start = [min(int(s), n_tokens) for s in plan.q_start.tolist()]
+    kv = [c + start[r + 1] - start[r] for r, c in enumerate(cached)]
+    want, bound, _ = attend_ref(q, kc, ks, vc, vs, tt.cpu().numpy(), kv, start, bs, D ** -0.5, 0, torch.bfloat16)
+    err = (out.double() - want).abs()
+    assert (err <= bound).all(), float((err / bound).max())
