@@ -333,6 +333,9 @@ def get_device_fault() -> int:
 
 
 # ---- serving operators ------------------------------------------------------
+# The tensor calls below launch on `stream` (a torch.cuda.Stream) or the current
+# one.  What a call is given must be ready on that stream; outputs and
+# workspaces that it is not given it makes on that stream.
 def ndq_kv_plan(cached: int, fresh: int, n_req: int, block_size: int, free_blocks: int, free_count: int,
                 block_table: int, table_width: int, q_start: int, kv_len: int, positions: int, slots: int,
                 n_tokens: int, free_left: int, stream: int = 0) -> int:
@@ -395,6 +398,24 @@ def _raw_stream(stream, device) -> int:
     if stream is not None:
         return int(stream.cuda_stream)
     return (_T or _consts()).raw_stream(device.index)
+
+
+def _made_for(stream, make):
+    """make()'s tensors for a call on `stream` (None: the current one): from
+    that stream's memory and filled in its order, so that what the call drops
+    is not used by other streams while its kernels still run."""
+    if stream is None:
+        return make()
+    with _torch().cuda.stream(stream):
+        return make()
+
+
+def _returned(stream, *tensors):
+    """Tensors of _made_for that the caller gets, and may use and drop on the
+    current stream."""
+    if stream is not None:
+        for x in tensors:
+            x.record_stream(_torch().cuda.current_stream(x.device))
 
 
 def _check(name, x, dtype, shape, device):
@@ -475,7 +496,8 @@ def kv_plan(cached, fresh, block_size: int, free_blocks, free_count, block_table
     if out is None:
         if n_tokens is None:
             raise ValueError("kv_plan needs `out` or `n_tokens`")
-        out = kv_plan_buffers(R, n_tokens, cached.device)
+        out = _made_for(stream, lambda: kv_plan_buffers(R, n_tokens, cached.device))
+        _returned(stream, out.q_start, out.kv_len, out.positions, out.slots, out.free_left)
     elif len(out.kv_len) != R:
         raise ValueError("out does not fit the requests")
     rc = _lib.ndq_kv_plan(cached.data_ptr(), fresh.data_ptr(), R, block_size, free_blocks.data_ptr(),
@@ -514,8 +536,9 @@ def kv_append(cache: KvCache, k, v, slots, stream=None) -> None:
 
 def attention_workspace(n_req: int, n_tokens: int, q_heads: int, cache: KvCache, max_q: int = 1):
     """A workspace for attention_kv8 calls on `cache`, of any size: its
-    counters are zeroed here and left so by every call.  (The sizes are
-    accepted so that a caller need not know that they do not matter.)"""
+    counters are zeroed here, on the current stream, and left so by every
+    call; calls that share it must not overlap.  (The sizes are accepted so
+    that a caller need not know that they do not matter.)"""
     torch = _torch()
     ws = torch.empty(ndq_attention_workspace_bytes(cache.head_dim), dtype=torch.uint8, device=cache.device)
     ws[:4096].zero_()
@@ -542,13 +565,14 @@ def attention_kv8(q, cache: KvCache, block_table, kv_len, q_start=None, max_q=No
     if q_start is not None and (q_start.dtype is not i32 or len(q_start) != R + 1 or not q_start.is_contiguous()):
         raise ValueError("q_start must be int32 [R + 1]")
     if out is None:
-        out = _torch().empty((T, H, D), dtype=q.dtype, device=q.device)
+        out = _made_for(stream, lambda: _torch().empty((T, H, D), dtype=q.dtype, device=q.device))
+        _returned(stream, out)
     elif out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's shape and type")
     if lse is not None and (lse.dtype is not c.f32 or lse.shape != (T, H) or not lse.is_contiguous()):
         raise ValueError("lse must be float32 [tokens, q_heads]")
     if workspace is None:
-        workspace = attention_workspace(R, T, H, cache)
+        workspace = _made_for(stream, lambda: attention_workspace(R, T, H, cache))
     rc = _lib.ndq_attention_kv8(
         cache.desc, q.data_ptr(), code, T, H, qs, block_table.data_ptr(), width, kv_len.data_ptr(),
         None if q_start is None else q_start.data_ptr(), R, max_q if max_q is not None else (1 if q_start is None else T),
@@ -582,14 +606,15 @@ def lora_add(x, lora_a, lora_b, ranks, scales, index, base, out=None, workspace=
         raise ValueError("lora_add: x [M, K], lora_a [n, r, K], lora_b [n, N, r] bfloat16, ranks [n], index [M] int32, "
                          "scales [n] float32, base [M, N] float32 or bfloat16")
     if out is None:
-        out = _torch().empty_like(base)
+        out = _made_for(stream, lambda: _torch().empty_like(base))
+        _returned(stream, out)
     elif out.dtype is not dtype or out.shape != base.shape:
         raise ValueError("out must have base's shape and type")
     if not (x.is_contiguous() and lora_a.is_contiguous() and lora_b.is_contiguous() and base.is_contiguous()
             and out.is_contiguous() and ranks.is_contiguous() and scales.is_contiguous() and index.is_contiguous()):
         raise ValueError("lora_add takes contiguous tensors")
     if workspace is None:
-        workspace = lora_workspace(M, nA, rank, K, x.device)
+        workspace = _made_for(stream, lambda: lora_workspace(M, nA, rank, K, x.device))
     rc = _lib.ndq_lora_add(x.data_ptr(), M, K, lora_a.data_ptr(), lora_b.data_ptr(), nA, rank, N, ranks.data_ptr(),
                            scales.data_ptr(), index.data_ptr(), base.data_ptr(), c.code[dtype], out.data_ptr(),
                            workspace.data_ptr(), workspace.numel(), _raw_stream(stream, x.device))

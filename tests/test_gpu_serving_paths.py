@@ -60,3 +60,62 @@ def test_plan_append_and_attention_with_room_for_fewer_tokens(fresh, n_tokens):
     want, bound, _ = attend_ref(q, kc, ks, vc, vs, tt.cpu().numpy(), kv, start, bs, D ** -0.5, 0, torch.bfloat16)
     err = (out.double() - want).abs()
     assert (err <= bound).all(), float((err / bound).max())
+
+
+# ---- what a call on another stream makes for itself --------------------------------
+
+
+def side_calls():
+    """Calls without outputs or workspaces, each as (call, the library's
+    function, which of its arguments is the workspace)."""
+    bs, D, kv, n = 16, 128, [5000, 41], [2, 60]
+    q, kc, ks, vc, vs, table, start = attend_case(kv, n, 8, 2, D, bs, "e4m3", torch.bfloat16, 91)
+    cache, tt, kl, qs = ndq.KvCache(kc, vc, ks, vs), torch.from_numpy(table).to(DEV), dev32(kv), dev32(start)
+    g = torch.Generator(device=DEV).manual_seed(92)
+    x, a, b = (torch.randn(s, device=DEV, generator=g).to(torch.bfloat16) for s in ((300, 1024), (2, 16, 1024), (2, 512, 16)))
+    base, index = torch.randn(300, 512, device=DEV, generator=g), dev32([i % 2 for i in range(300)])
+    ranks, scales = dev32([16, 16]), torch.ones(2, device=DEV)
+    plan = (dev32([3, 40]), dev32([700, 1]), bs, dev32(range(60)), dev32([60]), torch.arange(100, dtype=torch.int32, device=DEV).reshape(2, 50))
+
+    return {
+        "attention": (lambda **kw: ndq.attention_kv8(q, cache, tt, kl, q_start=qs, max_q=60, **kw), "ndq_attention_kv8", 16),
+        "adapters": (lambda **kw: ndq.lora_add(x, a, b, ranks, scales, index, base, **kw), "ndq_lora_add", 14),
+        "plan": (lambda **kw: ndq.kv_plan(*plan, n_tokens=701, **kw), "ndq_kv_plan", None),
+    }
+
+
+def values(y):
+    return y if isinstance(y, torch.Tensor) else torch.cat([z.long() for z in (y.q_start, y.kv_len, y.positions, y.slots, y.free_left)])
+
+
+@pytest.mark.parametrize("name", ["attention", "adapters", "plan"])
+def test_a_call_on_another_stream_owns_what_it_makes(name, monkeypatch):
+    call, fn, ws_arg = side_calls()[name]
+    want = values(call())
+    seen = []
+    raw = getattr(ndq._lib, fn)
+    monkeypatch.setattr(ndq._lib, fn, lambda *args: (seen.append(args), raw(*args))[1])
+    side = torch.cuda.Stream()
+    # freed memory of every size on the current stream, still to be written there
+    torch.cuda.synchronize()
+    sizes = [1 << i for i in range(9, 26)] + [ndq.ndq_attention_workspace_bytes(128)]
+    junk = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(3)]
+    torch.cuda._sleep(100_000_000)
+    for z in junk:
+        z.fill_(255)
+    del junk
+    got = call(stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(values(got), want)
+    # the workspace, while the call's kernels have not run: not for the current stream
+    if ws_arg is not None:
+        seen.clear()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)
+        got = call(stream=side)
+        at, nbytes = seen[0][ws_arg], seen[0][ws_arg + 1]
+        later = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in sizes + [nbytes] for _ in range(3)]
+        assert all(z.data_ptr() + z.numel() <= at or z.data_ptr() >= at + nbytes for z in later)
+        torch.cuda.current_stream().synchronize()
+        side.synchronize()
+        assert torch.equal(got, want)
