@@ -393,11 +393,18 @@ def _consts() -> _Torch:
     return _T
 
 
-def _raw_stream(stream, device) -> int:
+def _raw_stream(stream, device: int) -> int:
     # (the handle alone: building a torch.cuda.Stream for each call costs microseconds)
     if stream is not None:
         return int(stream.cuda_stream)
-    return (_T or _consts()).raw_stream(device.index)
+    return (_T or _consts()).raw_stream(device)
+
+
+def _same_device(what, device: int, *tensors):
+    """Every tensor lies on GPU `device` (an index; -1, the host's, is none)."""
+    for x in tensors:
+        if x.get_device() != device or device < 0:
+            raise ValueError(f"{what} takes CUDA tensors on one device")
 
 
 def _made_for(stream, make):
@@ -423,6 +430,11 @@ def _check(name, x, dtype, shape, device):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
+def _check_workspace(x, device: int):
+    if x.get_device() != device or not x.is_contiguous():
+        raise ValueError("the workspace must be contiguous, on the other tensors' device")
+
+
 class KvCache:
     """An 8-bit key/value cache: codes k, v [blocks, kv_heads, block_size,
     head_dim] (torch.float8_e4m3fn or torch.int8) and binary32 scales k_scale,
@@ -439,7 +451,7 @@ class KvCache:
         _check("v_scale", v_scale, torch.float32, k.shape[:2], k.device)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_blocks, self.kv_heads, self.block_size, self.head_dim = k.shape
-        self.device = k.device
+        self.device, self.gpu = k.device, k.get_device()
         self.desc = ndq_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.num_blocks,
                                  self.kv_heads, self.block_size, self.head_dim, code)
 
@@ -462,6 +474,7 @@ class KvPlan:
     def __init__(self, q_start, kv_len, positions, slots, free_left):
         torch = _torch()
         R, T, device = kv_len.shape[0], slots.shape[0], kv_len.device
+        self.gpu = kv_len.get_device()
         for name, x, dtype, n in (("q_start", q_start, torch.int32, R + 1), ("kv_len", kv_len, torch.int32, R),
                                   ("positions", positions, torch.int32, T), ("slots", slots, torch.int64, T),
                                   ("free_left", free_left, torch.int32, 1)):
@@ -488,8 +501,10 @@ def kv_plan(cached, fresh, block_size: int, free_blocks, free_count, block_table
             or block_table.dtype is not i32):
         raise ValueError("kv_plan takes int32 tensors")
     R, width = block_table.shape
-    if len(cached) != R or len(fresh) != R or free_count.numel() != 1:
-        raise ValueError("cached [R], fresh [R], block_table [R, width] and free_count [1] must agree")
+    if cached.shape != (R,) or fresh.shape != (R,) or free_blocks.dim() != 1 or free_count.numel() != 1:
+        raise ValueError("cached [R], fresh [R], block_table [R, width], free_blocks [F] and free_count [1] must agree")
+    gpu = cached.get_device()
+    _same_device("kv_plan", gpu, fresh, free_blocks, free_count, block_table)
     if not (cached.is_contiguous() and fresh.is_contiguous() and free_blocks.is_contiguous()
             and block_table.is_contiguous()):
         raise ValueError("kv_plan takes contiguous tensors")
@@ -498,10 +513,10 @@ def kv_plan(cached, fresh, block_size: int, free_blocks, free_count, block_table
             raise ValueError("kv_plan needs `out` or `n_tokens`")
         out = _made_for(stream, lambda: kv_plan_buffers(R, n_tokens, cached.device))
         _returned(stream, out.q_start, out.kv_len, out.positions, out.slots, out.free_left)
-    elif len(out.kv_len) != R:
+    elif out.kv_len.shape[0] != R or out.gpu != gpu:
         raise ValueError("out does not fit the requests")
     rc = _lib.ndq_kv_plan(cached.data_ptr(), fresh.data_ptr(), R, block_size, free_blocks.data_ptr(),
-                          free_count.data_ptr(), block_table.data_ptr(), width, *out.pointers, _raw_stream(stream, cached.device))
+                          free_count.data_ptr(), block_table.data_ptr(), width, *out.pointers, _raw_stream(stream, gpu))
     if rc:
         raise NdqError(rc, "kv_plan")
     return out
@@ -524,12 +539,13 @@ def kv_append(cache: KvCache, k, v, slots, stream=None) -> None:
     kv_plan writes them)."""
     c = _T or _consts()
     heads, dim, code = cache.kv_heads, cache.head_dim, c.code.get(k.dtype)
-    T = len(k)
-    if (k.dtype is not v.dtype or code is None or len(v) != T or slots.dtype is not c.i64 or slots.dim() != 1 or len(slots) != T
+    T = k.shape[0] if k.dim() else -1
+    if (k.dtype is not v.dtype or code is None or v.shape != k.shape or slots.dtype is not c.i64 or slots.shape != (T,)
             or not slots.is_contiguous()):
         raise ValueError("k and v must have the same type (bfloat16 or float16) and tokens, and slots one int64 for each")
+    _same_device("kv_append", cache.gpu, k, v, slots)
     rc = _lib.ndq_kv_append(cache.desc, k.data_ptr(), v.data_ptr(), code, _row_stride("k", k, heads, dim),
-                            _row_stride("v", v, heads, dim), slots.data_ptr(), T, _raw_stream(stream, cache.device))
+                            _row_stride("v", v, heads, dim), slots.data_ptr(), T, _raw_stream(stream, cache.gpu))
     if rc:
         raise NdqError(rc, "kv_append")
 
@@ -559,25 +575,30 @@ def attention_kv8(q, cache: KvCache, block_table, kv_len, q_start=None, max_q=No
     T, H, D = q.shape
     qs = _row_stride("q", q, H, cache.head_dim)
     R, width = block_table.shape
-    if (block_table.dtype is not i32 or kv_len.dtype is not i32 or len(kv_len) != R or not block_table.is_contiguous()
+    if (block_table.dtype is not i32 or kv_len.dtype is not i32 or kv_len.shape != (R,) or not block_table.is_contiguous()
             or not kv_len.is_contiguous()):
         raise ValueError("block_table must be int32 [R, width] and kv_len int32 [R]")
-    if q_start is not None and (q_start.dtype is not i32 or len(q_start) != R + 1 or not q_start.is_contiguous()):
-        raise ValueError("q_start must be int32 [R + 1]")
+    gpu = cache.gpu
+    _same_device("attention_kv8", gpu, q, block_table, kv_len)
+    if q_start is not None and (q_start.dtype is not i32 or q_start.shape != (R + 1,) or not q_start.is_contiguous()
+                                or q_start.get_device() != gpu):
+        raise ValueError("q_start must be int32 [R + 1], on q's device")
     if out is None:
         out = _made_for(stream, lambda: _torch().empty((T, H, D), dtype=q.dtype, device=q.device))
         _returned(stream, out)
-    elif out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out must be contiguous, of q's shape and type")
-    if lse is not None and (lse.dtype is not c.f32 or lse.shape != (T, H) or not lse.is_contiguous()):
-        raise ValueError("lse must be float32 [tokens, q_heads]")
-    if workspace is None:
+    elif out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous() or out.get_device() != gpu:
+        raise ValueError("out must be contiguous, of q's shape and type and on its device")
+    if lse is not None and (lse.dtype is not c.f32 or lse.shape != (T, H) or not lse.is_contiguous() or lse.get_device() != gpu):
+        raise ValueError("lse must be float32 [tokens, q_heads], on q's device")
+    if workspace is not None:
+        _check_workspace(workspace, gpu)
+    else:
         workspace = _made_for(stream, lambda: attention_workspace(R, T, H, cache))
     rc = _lib.ndq_attention_kv8(
         cache.desc, q.data_ptr(), code, T, H, qs, block_table.data_ptr(), width, kv_len.data_ptr(),
         None if q_start is None else q_start.data_ptr(), R, max_q if max_q is not None else (1 if q_start is None else T),
         D ** -0.5 if scale is None else scale, window, out.data_ptr(), None if lse is None else lse.data_ptr(),
-        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, q.device))
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, gpu))
     if rc:
         raise NdqError(rc, "attention_kv8")
     return out
@@ -601,23 +622,27 @@ def lora_add(x, lora_a, lora_b, ranks, scales, index, base, out=None, workspace=
     nB, N, rb = lora_b.shape
     dtype = base.dtype
     if (x.dtype is not bf16 or lora_a.dtype is not bf16 or lora_b.dtype is not bf16 or Ka != K or nB != nA or rb != rank
-            or base.shape != (M, N) or len(ranks) != nA or len(scales) != nA or len(index) != M or ranks.dtype is not i32
+            or base.shape != (M, N) or ranks.shape != (nA,) or scales.shape != (nA,) or index.shape != (M,) or ranks.dtype is not i32
             or index.dtype is not i32 or scales.dtype is not c.f32 or (dtype is not c.f32 and dtype is not bf16)):
         raise ValueError("lora_add: x [M, K], lora_a [n, r, K], lora_b [n, N, r] bfloat16, ranks [n], index [M] int32, "
                          "scales [n] float32, base [M, N] float32 or bfloat16")
+    gpu = x.get_device()
+    _same_device("lora_add", gpu, lora_a, lora_b, ranks, scales, index, base)
     if out is None:
         out = _made_for(stream, lambda: _torch().empty_like(base))
         _returned(stream, out)
-    elif out.dtype is not dtype or out.shape != base.shape:
-        raise ValueError("out must have base's shape and type")
+    elif out.dtype is not dtype or out.shape != base.shape or out.get_device() != gpu:
+        raise ValueError("out must have base's shape and type, on its device")
     if not (x.is_contiguous() and lora_a.is_contiguous() and lora_b.is_contiguous() and base.is_contiguous()
             and out.is_contiguous() and ranks.is_contiguous() and scales.is_contiguous() and index.is_contiguous()):
         raise ValueError("lora_add takes contiguous tensors")
-    if workspace is None:
+    if workspace is not None:
+        _check_workspace(workspace, gpu)
+    else:
         workspace = _made_for(stream, lambda: lora_workspace(M, nA, rank, K, x.device))
     rc = _lib.ndq_lora_add(x.data_ptr(), M, K, lora_a.data_ptr(), lora_b.data_ptr(), nA, rank, N, ranks.data_ptr(),
                            scales.data_ptr(), index.data_ptr(), base.data_ptr(), c.code[dtype], out.data_ptr(),
-                           workspace.data_ptr(), workspace.numel(), _raw_stream(stream, x.device))
+                           workspace.data_ptr(), workspace.numel(), _raw_stream(stream, gpu))
     if rc:
         raise NdqError(rc, "lora_add")
     return out
