@@ -375,7 +375,10 @@ typedef struct ndq_kv_cache {
  * tokens from n_tokens on are left out, with the table entries of blocks
  * that start there.  The table is written in place and the stack is not
  * popped: the next step starts from free_left (a second call with the same
- * inputs writes the same values).  free_left must not alias free_count.
+ * inputs writes the same values).  No output may overlap an input or another
+ * output (kv_len as the next step's cached, too, needs two buffers taken in
+ * turn): that is refused with NDQ_ERR_BAD_ARG, but for the part of
+ * free_blocks above its first id, whose length the host does not know.
  * The sum of the lengths must stay below 2^31.  n_req or n_tokens of 0 is
  * valid (q_start[0] = 0 and free_left are still written). */
 int ndq_kv_plan(const int32_t *cached, const int32_t *fresh, int64_t n_req, int block_size,

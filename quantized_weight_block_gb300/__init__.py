@@ -495,7 +495,9 @@ def kv_plan(cached, fresh, block_size: int, free_blocks, free_count, block_table
     """Block tables and slot maps of one step (see ndq_kv_plan): cached, fresh
     [R], free_blocks [F], free_count [1] and block_table [R, width] are CUDA
     int32 tensors; block_table is written in place.  `out` holds the outputs,
-    or `n_tokens` says how many tokens to allow for.  Returns the KvPlan."""
+    or `n_tokens` says how many tokens to allow for.  Returns the KvPlan.  Its
+    kv_len and free_left may be the next step's cached and free_count, with
+    other buffers for that step's outputs."""
     i32 = (_T or _consts()).i32
     if (cached.dtype is not i32 or fresh.dtype is not i32 or free_blocks.dtype is not i32 or free_count.dtype is not i32
             or block_table.dtype is not i32):

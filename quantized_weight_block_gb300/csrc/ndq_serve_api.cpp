@@ -40,6 +40,16 @@ int check_cache(const ndq_kv_cache* c, ndq::KvCache* d) {
     return NDQ_OK;
 }
 
+// A piece of memory, of `bytes` (0: none).
+struct Piece {
+    const void* p;
+    int64_t bytes;
+};
+bool overlap(const Piece& a, const Piece& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < static_cast<uintptr_t>(a.bytes) : x - y < static_cast<uintptr_t>(b.bytes));
+}
+
 // Rows of dense heads, 16-byte aligned, `stride` elements of 2 bytes apart.
 int check_rows(const void* p, int64_t stride, int64_t row) {
     if (stride < row || stride > (int64_t(1) << 40)) return NDQ_ERR_BAD_ARG;
@@ -68,6 +78,18 @@ int ndq_kv_plan(const int32_t* cached, const int32_t* fresh, int64_t n_req, int 
         !aligned(block_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(positions, 4) ||
         !aligned(slots, 8) || !aligned(free_left, 4))
         return NDQ_ERR_MISALIGNED;
+    // The CTAs read the inputs while others write: an output may be neither an
+    // input nor another output.  (Of the stack only the bottom is known here.)
+    const int64_t entries = n_req * table_width;  // (below 2^62)
+    const Piece out[] = {{block_table, 4 * (entries < INT64_C(1) << 60 ? entries : INT64_C(1) << 60)}, {q_start, 4 * (n_req + 1)},
+                         {kv_len, 4 * n_req}, {positions, 4 * n_tokens}, {slots, 8 * n_tokens}, {free_left, 4}};
+    const Piece in[] = {{cached, 4 * n_req}, {fresh, 4 * n_req}, {free_blocks, n_req > 0 ? 4 : 0}, {free_count, 4}};
+    for (int i = 0; i < 6; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return NDQ_ERR_BAD_ARG;
+        for (const Piece& x : in)
+            if (overlap(out[i], x)) return NDQ_ERR_BAD_ARG;
+    }
     ndq::PlanParams p{};
     p.cached = cached;
     p.fresh = fresh;

@@ -119,3 +119,31 @@ def test_a_call_on_another_stream_owns_what_it_makes(name, monkeypatch):
         torch.cuda.current_stream().synchronize()
         side.synchronize()
         assert torch.equal(got, want)
+
+
+# ---- block tables: outputs beside the inputs ---------------------------------------
+
+
+def test_plan_outputs_next_to_its_inputs():
+    # arrays that touch without overlapping are taken; kv_len and free_left go on as the next step's cached and count
+    R, T, bs, W = 3, 6, 16, 4
+    buf = torch.zeros(200, dtype=torch.int32, device=DEV)
+    parts, at = {}, 0
+    for name, n in (("slots", 2 * T), ("cached", R), ("kv_len", R), ("fresh", R), ("q_start", R + 1), ("free", 20), ("table", R * W),
+                    ("count", 1), ("positions", T), ("left", 1)):
+        parts[name] = buf[at:at + n]
+        at += n
+    parts["cached"].copy_(dev32([15, 0, 40])), parts["fresh"].copy_(dev32([2, 3, 1]))
+    parts["free"].copy_(torch.arange(20, device=DEV)), parts["count"].fill_(20)
+    parts["table"].view(R, W)[:] = dev32([[30, -1, -1, -1], [-1] * 4, [31, 32, 33, -1]])
+    out = ndq.KvPlan(parts["q_start"], parts["kv_len"], parts["positions"], parts["slots"].view(torch.int64), parts["left"])
+    table = parts["table"].view(R, W)
+    ndq.kv_plan(parts["cached"], parts["fresh"], bs, parts["free"], parts["count"], table, out=out)
+    assert out.q_start.tolist() == [0, 2, 5, 6] and out.kv_len.tolist() == [17, 3, 41] and out.free_left.tolist() == [18]
+    assert out.slots.tolist() == [30 * 16 + 15, 19 * 16, 18 * 16, 18 * 16 + 1, 18 * 16 + 2, 33 * 16 + 8]
+    with pytest.raises(ndq.NdqError):
+        ndq.kv_plan(out.kv_len, parts["fresh"], bs, parts["free"], parts["count"], table, out=out)
+    second = ndq.kv_plan(out.kv_len, parts["fresh"], bs, parts["free"], out.free_left, table, n_tokens=T)
+    assert second.kv_len.tolist() == [19, 6, 42] and second.positions.tolist() == [17, 18, 3, 4, 5, 41]
+    assert second.slots.tolist() == [19 * 16 + 1, 19 * 16 + 2, 18 * 16 + 3, 18 * 16 + 4, 18 * 16 + 5, 33 * 16 + 9]
+    assert second.free_left.tolist() == [18]

@@ -114,3 +114,20 @@ def test_descriptor_layout_matches_the_header():
 def test_append_launch_limit():
     rows = dict(k_stride=4096 * 128, v_stride=4096 * 128)
     assert append(cache(kv_heads=4096), n_tokens=(1 << 21) + 1, **rows) == BAD_ARG
+
+
+PLAN_PARTS = {"cached": 12, "fresh": 12, "free_blocks": 4, "free_count": 4, "block_table": 48, "q_start": 16, "kv_len": 12, "positions": 20,
+              "slots": 40, "free_left": 4}  # bytes, for 3 requests, a table of width 4 and 5 tokens
+PLAN_OUTPUTS = ("block_table", "q_start", "kv_len", "positions", "slots", "free_left")
+
+
+@pytest.mark.parametrize("out", PLAN_OUTPUTS)
+@pytest.mark.parametrize("other", PLAN_PARTS)
+def test_plan_outputs_over_other_arrays_are_refused(out, other):
+    if out == other:
+        return
+    apart = {n: P * (i + 1) for i, n in enumerate(PLAN_PARTS)}
+    step = 8 if "slots" in (out, other) else 4
+    # the same place, the output's last element on the other's first, its first on the other's last
+    for shift in (0, -(PLAN_PARTS[out] - step) // step * step, (PLAN_PARTS[other] - 1) // step * step):
+        assert plan(n_req=3, table_width=4, n_tokens=5, **(apart | {out: apart[other] + shift})) == BAD_ARG
