@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_serving import DEV, attend_case, attend_ref, dev32, random_cache
+from test_gpu_serving import CODES, DEV, attend_case, attend_ref, check_append, check_attend, check_lora, dev32, random_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -147,3 +147,163 @@ def test_plan_outputs_next_to_its_inputs():
     assert second.kv_len.tolist() == [19, 6, 42] and second.positions.tolist() == [17, 18, 3, 4, 5, 41]
     assert second.slots.tolist() == [19 * 16 + 1, 19 * 16 + 2, 18 * 16 + 3, 18 * 16 + 4, 18 * 16 + 5, 33 * 16 + 9]
     assert second.free_left.tolist() == [18]
+
+
+# ---- append: calls of more tokens, heads, K and V than one warp each (7296) ---------
+
+
+def append_slots(spans, bs, skip=()):
+    """Slots of requests of (tokens before, new tokens); those in `skip` have none."""
+    blocks = [-(-(a + n) // bs) for a, n in spans]
+    ids = np.random.default_rng(bs + len(spans)).permutation(sum(blocks) + 3)
+    slots, at = [], 0
+    for i, ((a, n), nb) in enumerate(zip(spans, blocks)):
+        slots += [-1 if i in skip else int(ids[at + p // bs]) * bs + p % bs for p in range(a, a + n)]
+        at += nb
+    return slots, len(ids)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype,D,bs", [(torch.bfloat16, 64, 16), (torch.float16, 128, 32), (torch.float16, 64, 64), (torch.bfloat16, 128, 128)])
+@pytest.mark.parametrize("spans,skip", [
+    ([(5, 220), (0, 129), (127, 1), (70, 200)] + [(i * 17 % 200, 1) for i in range(30)], (1, 9)),  # prompts and steps
+    ([(i * 37 % 300, 1) for i in range(470)], (0, 17, 18, 469)),                                   # steps alone
+    ([(i % 41, 1 + i % 7) for i in range(130)], (3,))])                                             # a few tokens each
+def test_append_many(code, dtype, D, bs, spans, skip):
+    heads = 8
+    slots, nb = append_slots(spans, bs, skip)
+    assert len(slots) * 2 * heads > 7296
+    g = torch.Generator(device=DEV).manual_seed(D + bs)
+    rows = torch.randn(len(slots), 2, heads, D, device=DEV, generator=g)
+    rows = (rows * torch.exp(torch.randn(len(slots), 2, heads, 1, device=DEV, generator=g))).to(dtype)
+    kc, ks = random_cache(nb, heads, bs, D, code, 101)
+    vc, vs = random_cache(nb, heads, bs, D, code, 102, 0.2)
+    check_append(rows[:, 0], rows[:, 1], slots, kc, ks, vc, vs, bs, code)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("bs", [16, 128])
+def test_append_many_special_values(code, bs):
+    heads, D = 8, 128
+    slots, nb = append_slots([(5, 300), (40, 60), (0, 128)], bs)
+    k, v = (torch.randn(len(slots), heads, D, device=DEV).to(torch.bfloat16) for _ in range(2))
+    k[0, 0, 5], k[1, 0, 7], k[100, 1, 0], k[200, 1, 127], k[310, 7, 3] = float("nan"), float("inf"), -float("inf"), 3e38, -3e38
+    v[20:60], v[330:] = 0.0, 0.0
+    v[70, 2] = float("inf")
+    v[100:140, 3], k[350:, 4] = 1e-38, float("nan")
+    kc, ks = random_cache(nb, heads, bs, D, code, 103)
+    vc, vs = random_cache(nb, heads, bs, D, code, 104)
+    vs[::3] = 0.0
+    vc.view(torch.int8)[::3] = 0
+    check_append(k, v, slots, kc, ks, vc, vs, bs, code)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("growth", [0.0, 0.15])
+def test_tokens_appended_one_by_one_stay_near_their_values(code, growth):
+    # Every append of a larger value rounds the block's codes again.  A rounding
+    # adds half a step: s / 2 (INT8); 2^-4 of the value, or 2^-10 s if that is
+    # more (E4M3).  (2^-18 of it for the products and quotients in binary32.)
+    bs, heads, D = 32, 2, 64
+    g = torch.Generator(device=DEV).manual_seed(105)
+    x = torch.randn(2, bs, heads, D, device=DEV, generator=g) * torch.exp(growth * torch.arange(bs, device=DEV))[:, None, None]
+    x = x.to(torch.bfloat16)
+    cache = ndq.KvCache.empty(2, heads, bs, D, CODES[code], DEV)
+    err = torch.zeros(2, heads, bs, D, dtype=torch.float64, device=DEV)
+    before = torch.zeros(2, heads, dtype=torch.float64, device=DEV)
+    for i in range(bs):
+        ndq.kv_append(cache, x[0, i:i + 1], x[1, i:i + 1], torch.tensor([bs + i], device=DEV))
+        scale = torch.stack([cache.k_scale[1], cache.v_scale[1]]).double()
+        rounded = torch.zeros_like(err, dtype=torch.bool)
+        rounded[:, :, :i] = (scale > before)[:, :, None, None]
+        rounded[:, :, i] = True
+        s = scale[:, :, None, None]
+        size = x.double().transpose(1, 2).abs() + err
+        step = s / 2 if code == "int8" else torch.maximum(size * 2.0 ** -4, s * 2.0 ** -10)
+        err += torch.where(rounded, step * (1 + 2.0 ** -18) + size * 2.0 ** -18, 0.0)
+        before = scale
+    got = torch.stack([cache.k[1].double() * cache.k_scale[1, :, None, None].double(), cache.v[1].double() * cache.v_scale[1, :, None, None].double()])
+    assert ((got - x.double().transpose(1, 2)).abs() <= err).all()
+
+
+# ---- attention: long shares, long prompts --------------------------------------------
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads,n", [((8, 2), 1), ((32, 2), 1), ((8, 2), 4)])
+def test_attend_shares_of_many_tiles(code, D, heads, n):
+    # more than 4096 tokens of a request to a CTA, blocks missing far behind
+    bs, R, L = 32, 40, 21000
+    kv = [L - 37 * i for i in range(R)]
+    q, kc, ks, vc, vs, table, start = attend_case(kv, [n] * R, *heads, D, bs, code, torch.bfloat16, 111)
+    table[3, 400:420] = -1
+    table[7, 150] = 1 << 30
+    table[11, 17::50] = -5
+    want, bound, _ = attend_ref(q, kc, ks, vc, vs, table, kv, start, bs, D ** -0.5, 0, torch.bfloat16)
+    out = ndq.attention_kv8(q, ndq.KvCache(kc, vc, ks, vs), torch.from_numpy(table).to(DEV), dev32(kv), q_start=dev32(start), max_q=n)
+    err = (out.double() - want).abs()
+    assert (err <= bound).all(), float((err / bound).max())
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 1700])
+@pytest.mark.parametrize("kv,n,heads", [([3000, 2500, 90], [300, 1100, 1], (32, 8)),   # as many units as SMs: one CTA each
+                                        ([40000], [64], (8, 2))])                       # few: their tokens split
+def test_attend_long_prompts(code, D, window, kv, n, heads):
+    bs = 16
+    q, kc, ks, vc, vs, table, start = attend_case(kv, n, *heads, D, bs, code, torch.bfloat16, 121)
+    table[0, 100:104] = -1
+    want, bound, lse_want = attend_ref(q, kc, ks, vc, vs, table, kv, start, bs, D ** -0.5, window, torch.bfloat16)
+    lse = torch.empty(q.shape[:2], device=DEV)
+    out = ndq.attention_kv8(q, ndq.KvCache(kc, vc, ks, vs), torch.from_numpy(table).to(DEV), dev32(kv), q_start=dev32(start), max_q=max(n),
+                            window=window, lse=lse)
+    err = (out.double() - want).abs()
+    assert (err <= bound).all(), float((err / bound).max())
+    assert ((lse - lse_want).abs() <= 2.0 ** -13).all()
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_attend_steps_and_prompts_together(code, dtype):
+    n = [1] * 30 + [400] + [1] * 7 + [5, 0, 33]
+    kv = [100 * i + 7 for i in range(30)] + [3000] + [50 * i for i in range(7)] + [900, 44, 33]
+    check_attend(kv, n, 32, 8, 128, 16, code, dtype, seed=131)
+
+
+# ---- adapters: many tiles to a CTA -----------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,K,N,nA,rank", [(2000, 512, 8192, 5, 16), (1500, 256, 8200, 3, 64), (1999, 64, 4099, 4, 8), (700, 128, 6000, 6, 128)])
+def test_lora_many_tiles(dtype, M, K, N, nA, rank):
+    rng = np.random.default_rng(M)
+    runs = np.sort(rng.integers(-1, nA, M)).tolist()
+    check_lora(M, K, N, nA, rank, dtype, runs)
+    check_lora(M, K, N, nA, rank, dtype, rng.permutation(runs).tolist(), seed=1)
+    check_lora(M, K, N, nA, rank, dtype, [(i // 23) % (nA + 1) - 1 for i in range(M)], seed=2, inplace=True)
+
+
+def test_lora_more_tiles_than_are_weighed():
+    check_lora(140000, 64, 264, 3, 8, torch.bfloat16, [(i // 999) % 4 - 1 for i in range(140000)])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("which", ["base", "out", "both"])
+def test_lora_tiles_with_outputs_off_16_bytes(dtype, which):
+    M, K, N, nA, rank = 500, 256, 1024, 3, 16
+    g = torch.Generator(device=DEV).manual_seed(141)
+    x, a, b = (torch.randn(s, device=DEV, generator=g).to(torch.bfloat16) for s in ((M, K), (nA, rank, K), (nA, N, rank)))
+    base = torch.randn(M, N, device=DEV, generator=g).to(dtype)
+    index, ranks, scales = dev32([i * 5 // M - 1 for i in range(M)]), dev32([16, 9, 16]), torch.tensor([1.0, 0.5, 2.0], device=DEV)
+    want = ndq.lora_add(x, a, b, ranks, scales, index, base)
+
+    def off(t):
+        buf = torch.zeros(M * N + 1, dtype=dtype, device=DEV)
+        buf[1:] = t.flatten()
+        return buf[1:].view(M, N)
+
+    out = off(torch.zeros_like(base)) if which != "base" else torch.zeros_like(base)
+    ndq.lora_add(x, a, b, ranks, scales, index, off(base) if which != "out" else base, out=out)
+    assert torch.equal(out, want)  # (the same products in the same order)
