@@ -677,8 +677,9 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                     float v[EPT];
 #pragma unroll
                     for (int e = 0; e < EPT; ++e) v[e] = __ldcg(q + 2 * kAttnRows + row * D + d0 + e);
-                    const float f = mw == -INFINITY ? (lw == lw ? 0.0f : 1.0f) : exp2_fast(mw - M);
-                    if (f != 0.0f) {
+                    // (a part that saw nothing is left out; one whose weights vanish may hold a NaN that must stay)
+                    if (mw != -INFINITY || lw != lw) {
+                        const float f = mw == -INFINITY ? 1.0f : exp2_fast(mw - M);
                         L = __fmaf_rn(lw, f, L);
 #pragma unroll
                         for (int e = 0; e < EPT; ++e) acc[e] = __fmaf_rn(v[e], f, acc[e]);

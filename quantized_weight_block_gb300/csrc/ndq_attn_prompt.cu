@@ -768,8 +768,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     const float4* q = reinterpret_cast<const float4*>(first + s * NDQ_PROMPT_SLOT(D) + 2 * kPromptRows);
                     const float4 x = __ldcg(q + (2 * c) * kPromptRows + prow), y = __ldcg(q + (2 * c + 1) * kPromptRows + prow);
                     const float mm = __ldcg(first + s * NDQ_PROMPT_SLOT(D) + prow), ll = __ldcg(first + s * NDQ_PROMPT_SLOT(D) + kPromptRows + prow);
-                    const float f = mm == -INFINITY ? (ll == ll ? 0.0f : 1.0f) : exp2_fast(mm - M);
-                    if (f == 0.0f) continue;
+                    // (a part that saw nothing is left out; one whose weights vanish may hold a NaN that must stay)
+                    if (mm == -INFINITY && ll == ll) continue;
+                    const float f = mm == -INFINITY ? 1.0f : exp2_fast(mm - M);
                     L = __fmaf_rn(ll, f, L);
                     a.x = __fmaf_rn(x.x, f, a.x);
                     a.y = __fmaf_rn(x.y, f, a.y);

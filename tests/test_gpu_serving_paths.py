@@ -307,3 +307,20 @@ def test_lora_tiles_with_outputs_off_16_bytes(dtype, which):
     out = off(torch.zeros_like(base)) if which != "base" else torch.zeros_like(base)
     ndq.lora_add(x, a, b, ranks, scales, index, off(base) if which != "out" else base, out=out)
     assert torch.equal(out, want)  # (the same products in the same order)
+
+
+@pytest.mark.parametrize("n", [1, 64])
+def test_attend_nan_far_below_the_largest_score(n):
+    # split over CTAs: a part whose weights vanish beside the others' still holds its NaN
+    bs, D, kv = 16, 64, [20000]
+    q, kc, ks, vc, vs, table, start = attend_case(kv, [n], 2, 1, D, bs, "e4m3", torch.bfloat16, 171)
+    ks[torch.from_numpy(table[0, :1200].astype(np.int64)).to(DEV)] = 0.0  # score 0
+    q[:] = 8.0
+    late = torch.from_numpy(table[0, 1200:1250].astype(np.int64)).to(DEV)
+    kc[late] = torch.full((), 256.0, device=DEV).to(torch.float8_e4m3fn)
+    ks[late] = 1.0
+    vc.view(torch.int8)[int(table[0, 2]), 0, 5, 33] = 0x7f
+    out = ndq.attention_kv8(q, ndq.KvCache(kc, vc, ks, vs), torch.from_numpy(table).to(DEV), dev32(kv), q_start=dev32(start))
+    expect = torch.zeros_like(out, dtype=torch.bool)
+    expect[:, :, 33] = True
+    assert torch.equal(out.isnan(), expect)
