@@ -439,9 +439,13 @@ int ndq_kv_append(const ndq_kv_cache *cache, const void *k, const void *v, int i
  * of no request.
  * A query that sees nothing gives 0.  What is not seen has no influence,
  * whatever its codes stand for.  Scores, softmax statistics and sums are
- * binary32; query values and softmax weights enter the tensor cores as
- * binary16 scaled by powers of two (the codes are exact there).  Repeated
- * calls give identical bits. */
+ * binary32.  The tensor cores take codes exactly and the rest in binary16:
+ * query values scaled by a power of two per row (those below 2^-24 of the
+ * row's largest are lost), and weights p vs, with p the softmax weight and vs
+ * V's scale, relative to a row's largest (2^-11 of each, and 2^-25 of the
+ * largest).  Every token counts in the denominator, whatever the scales
+ * (where all are near 2^-100, of up to 2^20 tokens).  Repeated calls give
+ * identical bits. */
 size_t ndq_attention_workspace_bytes(int head_dim);
 int ndq_attention_kv8(const ndq_kv_cache *cache, const void *q, int dtype, int64_t n_tokens, int q_heads,
                       int64_t q_stride, const int32_t *block_table, int64_t table_width, const int32_t *kv_len,

@@ -33,7 +33,7 @@
 // Scales.  K's scale multiplies a tile's scores; the logarithm of V's joins
 // the exponent, t = s ks + log2(vs), so that the weights 2^(t - m) which go to
 // binary16 lose nothing to a V of small scale; the denominator sums
-// 2^(t - m) / vs.
+// 2^(t - m) / vs, or 2^(s ks - m) where vs lies far below others (kScaleSpread).
 // Measured: 8 requests with 16k to 131k tokens, 64 heads on 8 (1.23 GB): 215 us,
 // 5.7 TB/s, 0.84 of the measured copy bandwidth; 64 requests of up to 8k
 // tokens, 32 heads on 8 (553 MB): 113-122 us, 4.5-4.9 TB/s; one request of 777
@@ -308,11 +308,14 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         for (int n = 0; n < ST - 1; ++n) issue(n >> 1, n & 1);
         // lane i: K's scale, log2 of V's and its reciprocal (V of scale 0: its codes are taken as zeros)
         float ks_l, ve_l, vinv_l;
+        int32_t v_top = kNoScale;  // the largest exponent of V's scales in this warp's tiles so far
         auto scales = [&]() {
             ks_l = now.ks;
             value_scale(now.vs, ve_l, vinv_l);
+            const int32_t e = __reduce_max_sync(0xffffffffu, scale_exponent(now.vs));
+            v_top = e > v_top ? e : v_top;
+            if (now.off != ~0ull && ve_l < static_cast<float>(v_top) - kScaleSpread) vinv_l = 0.0f;  // far below: see kScaleSpread
         };
-        scales();
 
         uint32_t qf[NT][KS][2];
         float frow[NT][2];  // rows 8 nt + 2 t and + 1: what turns a sum of products into a base-2 score, but for K's scale
@@ -348,6 +351,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                 qf[nt][s][1] = pack_half2(v[s * 4 + 2] * up, v[s * 4 + 3] * up);
             }
         }
+        scales();  // (here, so that the loads of Q go out before V's scales are there)
         // the tokens row i of the tile sees: [lo, hi)
         auto sees = [&](int32_t i, int32_t& lo, int32_t& hi) {
             const int32_t pos = x.pos + query_of(p, row0 + i);
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
             const bool masked = tb + kRowPair > all_hi || tb < all_lo || !live[0] || !live[1];
             // exponents relative to the running maximum
             float ex[2][NT][4];
-            bool grow = false;
+            bool grow = vinv[0] == 0.0f || vinv[1] == 0.0f;  // (rare, and dealt with there, too)
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                         // (relative to ms: the new maximum is ms + tm where it grew)
                         if (mx[nt][e] == -INFINITY ? tm > -INFINITY : tm > 0.0f) {
                             const float al = mx[nt][e] == -INFINITY ? 0.0f : exp2_fast(-tm);
-                            sum[nt][e] *= al;
+                            sum[nt][e] = mx[nt][e] == -INFINITY ? sum[nt][e] * 0.0f : add_scaled(0.0f, sum[nt][e], tm);
 #pragma unroll
                             for (int s = 0; s < KS; ++s) {
                                 o[nt][s][e] *= al;
@@ -478,6 +482,14 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                             }
                             mx[nt][e] = ms[nt][e] = ms[nt][e] + tm;
                         }
+                    }
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    if (vinv[s] == 0.0f) {  // V's scale far below others'
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sum[nt][e & 1] += exp2_fast(ex[s][nt][e] - ve[s]);
                     }
             }
             uint32_t pf[2][NT][2];
@@ -519,10 +531,11 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
 #pragma unroll
                     for (int a = 0; a < 4; ++a) {
                         const int32_t pos = tb + s * kRowTile + (a >> 1) * 8 + 2 * static_cast<int32_t>(t) + (a & 1);
-                        const bool dead = pos >= any_hi || pos < any_lo || !live[s] || zero[s];
+                        const bool dead = pos >= any_hi || pos < any_lo || !live[s];
 #pragma unroll
                         for (int w = 0; w < VB / 4; ++w) {
                             if (dead) vw[a][w] = 0u;
+                            else if (zero[s]) vw[a][w] = nan_codes<E4M3>(vw[a][w]);
                             if constexpr (E4M3) odd |= nan_bytes(vw[a][w]) != 0u;
                         }
                     }
@@ -636,8 +649,9 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) {
             // (a warp that saw nothing of this row has 0 for everything, or NaN that must stay)
-            const float f = mw[w] == -INFINITY ? 1.0f : exp2_fast(mw[w] - M);
-            L = __fmaf_rn(lw[w], f, L);
+            // (by halves of the exponent: lw may be large where 2^(mw - M) vanishes)
+            const float hf = mw[w] == -INFINITY ? 1.0f : exp2_fast(0.5f * (mw[w] - M)), f = hf * hf;
+            L = __fmaf_rn(lw[w] * hf, hf, L);
             const float* v = part + (w * kRows + row) * PS + d0;
 #pragma unroll
             for (int e = 0; e < EPT; ++e) acc[e] = __fmaf_rn(v[e], f, acc[e]);
@@ -679,8 +693,8 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                     for (int e = 0; e < EPT; ++e) v[e] = __ldcg(q + 2 * kAttnRows + row * D + d0 + e);
                     // (a part that saw nothing is left out; one whose weights vanish may hold a NaN that must stay)
                     if (mw != -INFINITY || lw != lw) {
-                        const float f = mw == -INFINITY ? 1.0f : exp2_fast(mw - M);
-                        L = __fmaf_rn(lw, f, L);
+                        const float hf = mw == -INFINITY ? 1.0f : exp2_fast(0.5f * (mw - M)), f = hf * hf;
+                        L = __fmaf_rn(lw * hf, hf, L);
 #pragma unroll
                         for (int e = 0; e < EPT; ++e) acc[e] = __fmaf_rn(v[e], f, acc[e]);
                     }

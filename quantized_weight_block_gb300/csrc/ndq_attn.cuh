@@ -88,13 +88,13 @@ __device__ __forceinline__ void row_scale(float amax, float& up, float& down) {
 }
 
 // log2 of V's scale and its reciprocal.  A block of scale 0 counts as zeros
-// under a scale of 2^-30: its weights add to the denominator alone, and with a
-// scale of 1 they could raise the maximum so far that binary16 loses the
-// weights of blocks of small values.  (NaN stays NaN.)
+// under the smallest scale there is: its weights add to the denominator alone,
+// and under a larger one they could raise the maximum so far that binary16
+// loses the weights of blocks of small values.  (NaN stays NaN.)
 __device__ __forceinline__ void value_scale(float s, float& lg, float& inv) {
     if (s == 0.0f) {
-        lg = -30.0f;
-        inv = 0x1p30f;
+        lg = -100.0f;
+        inv = 0x1p100f;
         return;
     }
     const uint32_t b = __float_as_uint(s);
@@ -102,6 +102,35 @@ __device__ __forceinline__ void value_scale(float s, float& lg, float& inv) {
     asm("lg2.approx.f32 %0, %1;" : "=f"(lg) : "f"(f));
     lg += s > 0.0f ? static_cast<float>(static_cast<int>(b >> 23) - 127) : 0.0f;
     inv = __fdividef(1.0f, s);
+}
+
+// V's scales far apart.  The weights are p = 2^(s + lg - m), the denominator
+// sums p / 2^lg.  A token whose p vanishes adds nothing to the values beside
+// the largest one's, but with lg far below that one's it may add to the
+// denominator: where lg lies more than kScaleSpread below the largest so far,
+// 2^(s - m) is taken by itself.  (Elsewhere a p that vanishes, below 2^-126,
+// belongs to an s at least 65 below the largest one's.)
+constexpr float kScaleSpread = 60.0f;
+constexpr int32_t kNoScale = -1000;
+
+// floor(log2(s)) of a scale above 0, else kNoScale.
+__device__ __forceinline__ int32_t scale_exponent(float s) {
+    return s > 0.0f && s < INFINITY ? static_cast<int32_t>(__float_as_uint(s) >> 23) - 127 : kNoScale;
+}
+
+// What of four codes of V a block of scale 0 keeps: E4M3's NaN.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+    if constexpr (E4M3) return w & ((nan_bytes(w) >> 7) * 0xffu);
+    else return 0u;
+}
+
+// sum + x 2^-d, d >= 0.  Denominators span more than 2^126, so that a large
+// one times a vanishing 2^-d may count.
+__device__ __forceinline__ float add_scaled(float sum, float x, float d) {
+    if (d < 120.0f) return __fmaf_rn(x, exp2_fast(-d), sum);
+    const float h = exp2_fast(-0.5f * d);
+    return __fmaf_rn(x * h, h, sum);
 }
 
 // Request r's first query row, the number of queries that are computed and the

@@ -23,7 +23,8 @@
 // the other's exponentials are taken.
 //
 // Scales as in ndq_attn.cu: t = s ks + log2(vs), P = 2^(t - m), the
-// denominator sums P / vs per group; Q is scaled by a power of two per row.
+// denominator sums P / vs per group (or takes 2^(s ks - m) by itself, with V's
+// scales far apart); Q is scaled by a power of two per row.
 // The maximum m moves only when a row passes it by 8, so O in tensor memory
 // is rescaled rarely; P is then at most 2^8.
 //
@@ -68,8 +69,8 @@ struct PrShared {
     uint64_t rawfull[kPrRaw], rawfree[kPrRaw];
     uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
     uint64_t sfull[2], pfull[2], odone[2];
-    float4 cst[kPrCst][kPrGroups];  // per group: K's scale, log2 of V's scale, 1 / V's scale
-    uint32_t gap[kPrCst];           // a block of the tile is missing
+    float4 cst[kPrCst][kPrGroups];  // per group: K's scale, log2 of V's scale, 1 / V's scale (0: far below others'), 0 for V of scale 0
+    uint32_t gap[kPrCst];           // a block of the tile is missing, or V's scale far below others'
     uint32_t tmem;
     uint32_t fault;
     uint32_t nan;   // V has NaN codes in a tile that some rows see only part of
@@ -368,9 +369,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const float4 c = S.cst[j % kPrCst][cw + 4 * q];
-                if (c.w == 0.0f && (is_v || c.y == -INFINITY)) {
+                if (c.y == -INFINITY) {
 #pragma unroll
                     for (int i = 0; i < ITS; ++i) x[q][i] = make_uint2(0u, 0u);
+                } else if (is_v && c.w == 0.0f) {
+#pragma unroll
+                    for (int i = 0; i < ITS; ++i) x[q][i] = make_uint2(nan_codes<E4M3>(x[q][i].x), nan_codes<E4M3>(x[q][i].y));
                 }
             }
             if (part) {
@@ -438,6 +442,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             };
             bool ok = true;
             int32_t ids = -1, ids_next = ids_of(0), issued = 0;
+            int32_t v_top = kNoScale;  // the largest exponent of V's scales so far
             uint64_t off = 0;
             float4 c = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
             for (int32_t j = 0; j < nt && ok; ++j) {
@@ -445,18 +450,23 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     ids = ids_next;
                     ids_next = ids_of((j >> 2) + 1);
                     c = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);  // a missing block: weight 0
+                    float vs = 0.0f;
                     if (ids >= 0) {
                         const uint64_t u = static_cast<uint64_t>(ids) * p.c.heads + static_cast<uint32_t>(h);
                         const int32_t tk = tok0 + (j + static_cast<int32_t>(lane >> 3)) * kPrTokens + static_cast<int32_t>(gl) * 16;
                         off = ((u << bl) + (static_cast<uint32_t>(tk) & ((1u << bl) - 1u))) * D;
-                        const float vs = p.c.vs[u];
+                        vs = p.c.vs[u];
                         float lg, inv;
                         value_scale(vs, lg, inv);
                         c = make_float4(p.c.ks[u], lg, inv, vs == 0.0f ? 0.0f : 1.0f);
                     }
+                    const int32_t e = __reduce_max_sync(0xffffffffu, scale_exponent(vs));
+                    v_top = e > v_top ? e : v_top;
+                    if (c.y < static_cast<float>(v_top) - kScaleSpread) c.z = 0.0f;  // far below: see kScaleSpread
                 }
                 const bool mine = static_cast<int32_t>(lane >> 3) == (j & 3);
                 const uint32_t n16 = __popc(__ballot_sync(0xffffffffu, mine && ids >= 0));
+                const bool far = __any_sync(0xffffffffu, mine && ids >= 0 && c.z == 0.0f);
                 const int32_t left = any_hi - (tok0 + j * kPrTokens);  // (of the tile's groups, those that some row sees)
                 const uint32_t seen = left >= kPrTokens ? kPrGroups : static_cast<uint32_t>(left + 15) >> 4;
                 for (int32_t half = 0; half < 2; ++half) {  // K, V
@@ -464,7 +474,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     if (j >= 1) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.rawfree[rs], static_cast<uint32_t>((j - 1) & 1)));
                     if (!ok) break;
                     if (half == 0 && mine) S.cst[j % kPrCst][gl] = c;
-                    if (half == 0 && lane == 0) S.gap[j % kPrCst] = n16 < seen ? 1u : 0u;
+                    if (half == 0 && lane == 0) S.gap[j % kPrCst] = n16 < seen || far ? 1u : 0u;
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(&S.rawfull[rs], n16 * 16u * D);
                     __syncwarp();
@@ -599,6 +609,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 }
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) tops[(e >> 1) & 1] = max3(tops[(e >> 1) & 1], y[e], y[e + 1]);
+                if constexpr (kMasked) {
+                    if (k.z == 0.0f) {  // (rare: V's scale far below others', or a missing block)
+                        float d = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) d += y[e] == -INFINITY ? 0.0f : exp2_fast(y[e] - k.y);
+                        ts += d;
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) y[e] = exp2_fast(y[e]);
                 uint64_t s2[2] = {pair(y[0], y[1]), pair(y[2], y[3])};
@@ -641,7 +659,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     }
                     tmem_wait_st();
                 }
-                sum *= al;
+                if (grow) sum = mx == -INFINITY ? sum * 0.0f : add_scaled(0.0f, sum, top);
                 // the same exponents less the growth, so that the largest is 0 whatever ms + top is rounded to
                 const float less = grow ? top : 0.0f;
                 weigh(std::true_type{}, std::true_type{}, less, cst, tb, ts, top);
@@ -681,7 +699,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     const int32_t id = table[tk >> bl];
                     if (id < 0 || id >= p.c.num_blocks) continue;
                     const uint64_t u = static_cast<uint64_t>(id) * p.c.heads + static_cast<uint32_t>(h);
-                    if (p.c.vs[u] == 0.0f) continue;
                     const uint32_t* v = reinterpret_cast<const uint32_t*>(
                         p.c.v + ((u << bl) + (static_cast<uint32_t>(tk) & ((1u << bl) - 1u))) * D);
 #pragma unroll
@@ -771,7 +788,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     // (a part that saw nothing is left out; one whose weights vanish may hold a NaN that must stay)
                     if (mm == -INFINITY && ll == ll) continue;
                     const float f = mm == -INFINITY ? 1.0f : exp2_fast(mm - M);
-                    L = __fmaf_rn(ll, f, L);
+                    L = add_scaled(L, ll, mm == -INFINITY ? 0.0f : M - mm);
                     a.x = __fmaf_rn(x.x, f, a.x);
                     a.y = __fmaf_rn(x.y, f, a.y);
                     a.z = __fmaf_rn(x.z, f, a.z);

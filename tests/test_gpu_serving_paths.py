@@ -309,6 +309,60 @@ def test_lora_tiles_with_outputs_off_16_bytes(dtype, which):
     assert torch.equal(out, want)  # (the same products in the same order)
 
 
+# ---- attention: V's scales over their whole range ------------------------------------
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("n", [1, 4, 140])
+@pytest.mark.parametrize("spread", ["random", "rising", "falling", "small with zeros", "large with zeros", "zeros first", "zeros"])
+def test_attend_scales_of_v_over_their_range(code, n, spread):
+    # A block counts in the denominator whatever its scale, and blocks of zeros
+    # take no bits from the others.  (In tiles of 128 tokens and in small ones.)
+    bs, D = 16, 128
+    kv = [700, 3500]
+    q, kc, ks, vc, vs, table, start = attend_case(kv, [n, n], 8, 2, D, bs, code, torch.bfloat16, 151)
+    g = torch.Generator(device=DEV).manual_seed(152)
+    nb = vs.shape[0]
+    where = torch.full((nb,), -1.0, device=DEV)  # a block's place in its request, 0 .. 1
+    for r in range(2):
+        m = -(-kv[r] // bs)
+        where[torch.from_numpy(table[r, :m].astype(np.int64)).to(DEV)] = torch.linspace(0, 1, m, device=DEV)
+    one = torch.rand(vs.shape, device=DEV, generator=g) + 0.5
+    power = {"random": torch.randint(-99, 99, vs.shape, device=DEV, generator=g).float(), "rising": (198 * where - 99).round()[:, None],
+             "falling": (99 - 198 * where).round()[:, None], "small with zeros": -80.0, "large with zeros": 98.0, "zeros first": -70.0,
+             "zeros": 0.0}[spread]
+    vs.copy_(torch.ldexp(one, torch.as_tensor(power, device=DEV).int()))
+    if spread.endswith("with zeros"):
+        vs[::3] = 0.0
+    elif spread == "zeros first":
+        vs[where < 0.6] = 0.0
+    elif spread == "zeros":
+        vs.zero_()
+    if code == "e4m3":  # codes of blocks of zeros may be anything but NaN
+        vc.view(torch.int8)[(vc.view(torch.int8) & 0x7f) == 0x7f] = 0x11
+    want, bound, lse_want = attend_ref(q, kc, ks, vc, vs, table, kv, start, bs, D ** -0.5, 0, torch.bfloat16)
+    lse = torch.empty(q.shape[:2], device=DEV)
+    out = ndq.attention_kv8(q, ndq.KvCache(kc, vc, ks, vs), torch.from_numpy(table).to(DEV), dev32(kv), q_start=dev32(start), lse=lse)
+    err = (out.double() - want).abs()
+    assert (err <= bound).all(), float((err / bound).max())
+    # (the logarithm's parts are of up to 108, in binary32)
+    assert ((lse - lse_want).abs() <= 2.0 ** -13).all()
+
+
+@pytest.mark.parametrize("n", [1, 4, 140])
+def test_attend_nan_in_a_block_of_small_scale(n):
+    bs, D, kv = 16, 128, [600]
+    q, kc, ks, vc, vs, table, start = attend_case(kv, [n], 8, 2, D, bs, "e4m3", torch.bfloat16, 161)
+    b = int(table[0, 9])
+    vs[b] = 2.0 ** -95
+    vc.view(torch.int8)[b, 1, 3, 17] = -1
+    vc.view(torch.int8)[b, 1, 12, 80] = 0x7f
+    out = ndq.attention_kv8(q, ndq.KvCache(kc, vc, ks, vs), torch.from_numpy(table).to(DEV), dev32(kv), q_start=dev32(start))
+    expect = torch.zeros_like(out, dtype=torch.bool)
+    expect[:, 4:, 17] = expect[:, 4:, 80] = True
+    assert torch.equal(out.isnan(), expect)
+
+
 @pytest.mark.parametrize("n", [1, 64])
 def test_attend_nan_far_below_the_largest_score(n):
     # split over CTAs: a part whose weights vanish beside the others' still holds its NaN
