@@ -418,9 +418,9 @@ int ndq_kv_append(const ndq_kv_cache *cache, const void *k, const void *v, int i
  *              NDQ_FLOAT16), rows q_stride elements apart, heads dense, base
  *              and rows 16-byte aligned
  *   block_table, table_width   as for ndq_kv_plan; tokens of an id outside
- *              [0, num_blocks) are not seen
- *   kv_len     device int32 [n_req] (at most table_width * block_size each,
- *              which is at most 2^30)
+ *              [0, num_blocks) are not seen, nor those past table_width *
+ *              block_size, which is at most 2^30
+ *   kv_len     device int32 [n_req]
  *   q_start    device int32 [n_req + 1], or NULL when every request has
  *              exactly one query (n_tokens == n_req)
  *              (n_tokens * q_heads below 2^31)

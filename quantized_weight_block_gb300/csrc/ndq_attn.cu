@@ -100,12 +100,12 @@ template <int ROWS>
 __device__ __forceinline__ Req request(const AttnParams& p, int64_t r) {
     Req x;
     attn_request(p, r, x.q0, x.n, x.pos);
-    const int32_t end = x.pos + x.n;  // no query sees further
+    const int32_t most = table_tokens(p), end = x.pos + x.n < most ? x.pos + x.n : most;  // no query sees further
     if (p.prompt_rows > 0 && static_cast<int64_t>(x.n) * p.group >= p.prompt_rows) x.n = 0;  // the other kernel's
     x.lo = 0;
     if (p.window > 0) {
         const int32_t first = x.pos + 1 - p.window;
-        x.lo = first > 0 ? first & ~(kRowTile - 1) : 0;
+        x.lo = first > 0 ? (first < most ? first & ~(kRowTile - 1) : most) : 0;
     }
     x.units = end > x.lo ? (end - x.lo + kRowUnit - 1) / kRowUnit : 1;
     x.tiles = (x.n * p.group + ROWS - 1) / ROWS;
@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         const int32_t rows_left = x.n * p.group - row0;
         const int32_t nrows = rows_left < kRows ? rows_left : kRows;
         const int32_t qa = query_of(p, row0), qb = query_of(p, row0 + nrows - 1);
-        const int32_t any_hi = x.pos + qb + 1, all_hi = x.pos + qa + 1;
-        const int32_t any_lo = p.window > 0 ? all_hi - p.window : 0, all_lo = p.window > 0 ? any_hi - p.window : 0;
+        const int32_t end = x.pos + qb + 1, all_hi = x.pos + qa + 1, any_hi = end < table_tokens(p) ? end : table_tokens(p);
+        const int32_t any_lo = p.window > 0 ? all_hi - p.window : 0, all_lo = p.window > 0 ? end - p.window : 0;
 
         // this warp's pairs: base token x.lo + 32 (8 c + warp), c = ca .. cb - 1
         int32_t tok = x.lo + ca * kRowUnit + static_cast<int32_t>(warp) * kRowPair;

@@ -133,10 +133,14 @@ __device__ __forceinline__ float add_scaled(float sum, float x, float d) {
     return __fmaf_rn(x * h, h, sum);
 }
 
+// Tokens that the block table has room for (at most 2^30).
+__device__ __forceinline__ int32_t table_tokens(const AttnParams& p) { return static_cast<int32_t>(p.width << p.c.bs_log2); }
+
 // Request r's first query row, the number of queries that are computed and the
 // position of the first one, kept inside the buffers whatever the device
-// arrays hold.  Queries past max_q or n_tokens are left out, but they count
-// for the positions: all of a request's queries are its last tokens.
+// arrays hold.  Queries past max_q or n_tokens are left out, and tokens past
+// the table are not seen, but both count for the positions: all of a request's
+// queries are its last tokens.
 __device__ __forceinline__ void attn_request(const AttnParams& p, int64_t r, int64_t& q0, int32_t& n, int32_t& first) {
     int64_t a = r, all = 1, room = 1;
     if (p.q_start) {
@@ -148,9 +152,7 @@ __device__ __forceinline__ void attn_request(const AttnParams& p, int64_t r, int
     }
     q0 = a;
     n = static_cast<int32_t>(all < room ? all : room);
-    const int64_t most = p.width << p.c.bs_log2;
-    int64_t len = p.kv_len[r];
-    len = len < 0 ? 0 : (len > most ? most : len);
+    const int64_t len = p.kv_len[r] > 0 ? p.kv_len[r] : 0;
     first = static_cast<int32_t>(len - all > -(1 << 30) ? len - all : -(1 << 30));  // (before 0 in either case)
 }
 

@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     const int32_t nact = nrows > 128 ? 2 : 1;  // row tiles in use
     // tokens that some row / every row of the CTA sees
     const int32_t first_pos = pos0 + row0 / p.group, last_pos = pos0 + (row0 + nrows - 1) / p.group;
-    const int32_t any_hi = last_pos + 1, cta_hi = first_pos + 1;
+    const int32_t most = table_tokens(p), any_hi = last_pos < most ? last_pos + 1 : most, cta_hi = first_pos + 1;
     const int32_t any_lo = p.window > 0 && first_pos + 1 > p.window ? first_pos + 1 - p.window : 0;
     const int32_t cta_lo = p.window > 0 ? last_pos + 1 - p.window : 0;
     const int32_t lo16 = any_lo & ~15;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             *reinterpret_cast<uint4*>(dst + (c >> 3) * kAtom + sw128(wrow, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         const int32_t pos = pos0 + qi;
-        see_hi = has_row && pos >= 0 ? pos + 1 : 0;
+        see_hi = has_row && pos >= 0 ? (pos < most ? pos + 1 : most) : 0;
         see_lo = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
         fence_proxy_async_smem();
     }
@@ -467,14 +467,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 const bool mine = static_cast<int32_t>(lane >> 3) == (j & 3);
                 const uint32_t n16 = __popc(__ballot_sync(0xffffffffu, mine && ids >= 0));
                 const bool far = __any_sync(0xffffffffu, mine && ids >= 0 && c.z == 0.0f);
-                const int32_t left = any_hi - (tok0 + j * kPrTokens);  // (of the tile's groups, those that some row sees)
-                const uint32_t seen = left >= kPrTokens ? kPrGroups : static_cast<uint32_t>(left + 15) >> 4;
                 for (int32_t half = 0; half < 2; ++half) {  // K, V
                     const uint32_t rs = static_cast<uint32_t>(half);
                     if (j >= 1) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.rawfree[rs], static_cast<uint32_t>((j - 1) & 1)));
                     if (!ok) break;
                     if (half == 0 && mine) S.cst[j % kPrCst][gl] = c;
-                    if (half == 0 && lane == 0) S.gap[j % kPrCst] = n16 < seen || far ? 1u : 0u;
+                    if (half == 0 && lane == 0) S.gap[j % kPrCst] = n16 < kPrGroups || far ? 1u : 0u;
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(&S.rawfull[rs], n16 * 16u * D);
                     __syncwarp();

@@ -62,6 +62,33 @@ def test_plan_append_and_attention_with_room_for_fewer_tokens(fresh, n_tokens):
     assert (err <= bound).all(), float((err / bound).max())
 
 
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("window", [0, 90])
+@pytest.mark.parametrize("n,over", [([1, 1, 1], 1), ([4, 3, 1], 2), ([4, 4, 4], 40), ([200, 130, 70], 60), ([300, 40, 300], 500)])
+def test_attend_tokens_past_the_table_are_not_seen(code, window, n, over):
+    # (a plan whose table is too narrow: such tokens have no blocks, and the queries keep their positions)
+    bs, D, W = 16, 128, 30
+    kv = [W * bs + over, 300, W * bs + 2 * over]
+    q, kc, ks, vc, vs, table, start = attend_case(kv, n, 8, 2, D, bs, code, torch.bfloat16, 181)
+    narrow = np.ascontiguousarray(table[:, :W])
+    hidden = table.copy()
+    hidden[:, W:] = -1
+    want, bound, lse_want = attend_ref(q, kc, ks, vc, vs, hidden, kv, start, bs, D ** -0.5, window, torch.bfloat16)
+    if code == "e4m3":  # a NaN at the table's end reaches those that see it
+        vc.view(torch.int8)[int(table[0, W - 1]), 0, bs - 1, 3] = 0x7f
+    lse = torch.empty(q.shape[:2], device=DEV)
+    out = ndq.attention_kv8(q, ndq.KvCache(kc, vc, ks, vs), torch.from_numpy(narrow).to(DEV), dev32(kv), q_start=dev32(start), window=window, lse=lse)
+    nan = torch.zeros_like(out, dtype=torch.bool)
+    if code == "e4m3":
+        pos = torch.arange(kv[0] - n[0], kv[0], device=DEV)
+        sees = (pos >= W * bs - 1) & ((pos < W * bs - 1 + window) if window else True)
+        nan[:n[0], :4, 3] = sees[:, None]
+    assert torch.equal(out.isnan(), nan)
+    assert (((out.double() - want).abs() <= bound) | nan).all()
+    none = torch.isinf(lse_want)
+    assert torch.equal(torch.isinf(lse), none) and ((lse - lse_want)[~none].abs() <= 2.0 ** -13).all()
+
+
 # ---- what a call on another stream makes for itself --------------------------------
 
 
