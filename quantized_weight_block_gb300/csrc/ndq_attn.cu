@@ -468,8 +468,8 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
                         // (relative to ms: the new maximum is ms + tm where it grew)
                         if (mx[nt][e] == -INFINITY ? tm > -INFINITY : tm > 0.0f) {
-                            const float al = mx[nt][e] == -INFINITY ? 0.0f : exp2_fast(-tm);
-                            sum[nt][e] = mx[nt][e] == -INFINITY ? sum[nt][e] * 0.0f : add_scaled(0.0f, sum[nt][e], tm);
+                            const float ah = mx[nt][e] == -INFINITY ? 0.0f : exp2_fast(-0.5f * tm), al = ah * ah;
+                            sum[nt][e] = sum[nt][e] * ah * ah;
 #pragma unroll
                             for (int s = 0; s < KS; ++s) {
                                 o[nt][s][e] *= al;
@@ -649,7 +649,6 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) {
             // (a warp that saw nothing of this row has 0 for everything, or NaN that must stay)
-            // (by halves of the exponent: lw may be large where 2^(mw - M) vanishes)
             const float hf = mw[w] == -INFINITY ? 1.0f : exp2_fast(0.5f * (mw[w] - M)), f = hf * hf;
             L = __fmaf_rn(lw[w] * hf, hf, L);
             const float* v = part + (w * kRows + row) * PS + d0;

@@ -109,7 +109,9 @@ __device__ __forceinline__ void value_scale(float s, float& lg, float& inv) {
 // the largest one's, but with lg far below that one's it may add to the
 // denominator: where lg lies more than kScaleSpread below the largest so far,
 // 2^(s - m) is taken by itself.  (Elsewhere a p that vanishes, below 2^-126,
-// belongs to an s at least 65 below the largest one's.)
+// belongs to an s at least 65 below the largest one's.)  Denominators span more
+// than 2^126, so one that counts may be large where the factor that it is to be
+// scaled by vanishes: it is scaled by halves of the exponent.
 constexpr float kScaleSpread = 60.0f;
 constexpr int32_t kNoScale = -1000;
 
@@ -123,14 +125,6 @@ template <bool E4M3>
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
     if constexpr (E4M3) return w & ((nan_bytes(w) >> 7) * 0xffu);
     else return 0u;
-}
-
-// sum + x 2^-d, d >= 0.  Denominators span more than 2^126, so that a large
-// one times a vanishing 2^-d may count.
-__device__ __forceinline__ float add_scaled(float sum, float x, float d) {
-    if (d < 120.0f) return __fmaf_rn(x, exp2_fast(-d), sum);
-    const float h = exp2_fast(-0.5f * d);
-    return __fmaf_rn(x * h, h, sum);
 }
 
 // Tokens that the block table has room for (at most 2^30).

@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             const bool grow = top > (mx == -INFINITY ? -INFINITY : 8.0f);
             // a row passed its maximum by 8: always in the first tile that it sees, rarely later
             if (__any_sync(0xffffffffu, grow)) {
-                const float al = !grow ? 1.0f : (mx == -INFINITY ? 0.0f : exp2_fast(-top));
+                const float ah = !grow ? 1.0f : (mx == -INFINITY ? 0.0f : exp2_fast(-0.5f * top)), al = ah * ah;
                 if (j > 0) {  // O moves to the new maximum once the product before this one is done with it
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((j - 1) & 1)));
                     if (!ok) break;
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     }
                     tmem_wait_st();
                 }
-                if (grow) sum = mx == -INFINITY ? sum * 0.0f : add_scaled(0.0f, sum, top);
+                sum = sum * ah * ah;
                 // the same exponents less the growth, so that the largest is 0 whatever ms + top is rounded to
                 const float less = grow ? top : 0.0f;
                 weigh(std::true_type{}, std::true_type{}, less, cst, tb, ts, top);
@@ -785,8 +785,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     const float mm = __ldcg(first + s * NDQ_PROMPT_SLOT(D) + prow), ll = __ldcg(first + s * NDQ_PROMPT_SLOT(D) + kPromptRows + prow);
                     // (a part that saw nothing is left out; one whose weights vanish may hold a NaN that must stay)
                     if (mm == -INFINITY && ll == ll) continue;
-                    const float f = mm == -INFINITY ? 1.0f : exp2_fast(mm - M);
-                    L = add_scaled(L, ll, mm == -INFINITY ? 0.0f : M - mm);
+                    const float hf = mm == -INFINITY ? 1.0f : exp2_fast(0.5f * (mm - M)), f = hf * hf;
+                    L = __fmaf_rn(ll * hf, hf, L);
                     a.x = __fmaf_rn(x.x, f, a.x);
                     a.y = __fmaf_rn(x.y, f, a.y);
                     a.z = __fmaf_rn(x.z, f, a.z);
