@@ -492,6 +492,17 @@ int ndq_lora_add(const void *x_bf16, int64_t M, int64_t K, const void *lora_a, c
  * 2000000. */
 int ndq_test_withhold_copy(int64_t tile, uint32_t wait_limit_us);
 
+/* The same for the serving operators: the NEXT ndq_attention_kv8 or
+ * ndq_lora_add launched by the calling host thread waits for 16 bytes more
+ * than each of its staged copies brings, as if none had landed, and for at
+ * most `wait_limit_us` microseconds (1000 to 2000000) instead of 2 s.  Its
+ * waits run out, its kernels set their bits in the fault word (8: prompt
+ * attention, 16: adapter tiles, 32: few-row attention) and end; its outputs
+ * are unspecified, its workspace stays fit for use.  (Few rows of adapters
+ * have no staged copies.)  0 cancels the request.  Returns NDQ_ERR_BAD_COUNT
+ * for other values. */
+int ndq_test_lose_copies(uint32_t wait_limit_us);
+
 /* Read and clear the library's device fault word on the current device.
  * A kernel sets a nonzero bit when one of its bounded waits for staged
  * payload data gives up (it then stops decoding instead of hanging the GPU).

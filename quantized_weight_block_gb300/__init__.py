@@ -90,6 +90,7 @@ _lib.ndq_dequantize_packed_batched.argtypes = [_c.POINTER(ndq_tensor_desc), _c.c
                                                _c.c_void_p]
 _lib.ndq_get_device_fault.argtypes = [_c.POINTER(_c.c_uint32)]
 _lib.ndq_test_withhold_copy.argtypes = [_c.c_int64, _c.c_uint32]
+_lib.ndq_test_lose_copies.argtypes = [_c.c_uint32]
 _lib.ndq_dequantize_packed_batched_noalloc.argtypes = [_c.POINTER(ndq_tensor_desc), _c.c_int, _c.c_void_p]
 _lib.ndq_matmul_packed.argtypes = [_c.c_int, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_size_t, _c.c_void_p,
                                    _c.c_int64, _c.c_int, _c.c_int, _c.c_void_p, _c.c_void_p]
@@ -114,7 +115,7 @@ EXPORTS = (
     "ndq_dequantize_packed_batched", "ndq_get_device_fault", "ndq_dequantize_packed_batched_noalloc",
     "ndq_matmul_packed", "ndq_test_withhold_copy", "ndq_matmul_packed_batched",
     "ndq_kv_plan", "ndq_kv_append", "ndq_attention_workspace_bytes", "ndq_attention_kv8",
-    "ndq_lora_workspace_bytes", "ndq_lora_add",
+    "ndq_lora_workspace_bytes", "ndq_lora_add", "ndq_test_lose_copies",
 )
 
 
@@ -200,6 +201,13 @@ def ndq_test_withhold_copy(tile: int, wait_limit_us: int) -> int:
     tile's staging copy (a check of the device-side failure path); returns
     the status code."""
     return _lib.ndq_test_withhold_copy(tile, wait_limit_us)
+
+
+def ndq_test_lose_copies(wait_limit_us: int) -> int:
+    """Raw call: the next attention or adapter launch of this host thread sees
+    none of its staged copies land (a check of the device-side failure path);
+    returns the status code."""
+    return _lib.ndq_test_lose_copies(wait_limit_us)
 
 
 def ndq_get_device_fault() -> int:

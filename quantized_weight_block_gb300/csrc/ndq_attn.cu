@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
             const uint64_t off = (i >> 4) != cur_block ? then.off : now.off;
             const bool mine = static_cast<int32_t>(lane >> 1) == (i & 15) && off != ~0ull;
             const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));  // (also: every lane is here)
-            if (lane == 0) mbar_arrive_expect_tx(&s_bar[warp][put], n * static_cast<uint32_t>(kRowTile * D));
+            if (lane == 0) mbar_arrive_expect_tx(&s_bar[warp][put], n * static_cast<uint32_t>(kRowTile * D) + p.waits.beyond);
             __syncwarp();
             if (mine)
                 bulk_load(ring + (warp * ST + put) * Sm::kStage + (lane & 1u) * (kRowTile * D), (part ? p.c.v : p.c.k) + off, kRowTile * D,
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         };
         // waits for the next slot; its address
         auto arrived = [&]() -> uint32_t {
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_bar[warp][get], get_phase));
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_bar[warp][get], get_phase, p.waits.limit_ns));
             return my_ring + get * Sm::kStage;
         };
         auto taken = [&]() {
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         if (!ok) {  // what is still in flight lands before the ring is used for anything else
             if (lane == 0) atomicOr(p.fault, kRowFault);
             while (flying > 0) {
-                mbar_wait_bounded(&s_bar[warp][get], get_phase);
+                mbar_wait_bounded(&s_bar[warp][get], get_phase, p.waits.limit_ns);
                 taken();
             }
         }

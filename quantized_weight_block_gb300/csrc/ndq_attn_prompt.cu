@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             fence_proxy_async_smem();
             __syncwarp();
         };
-        auto wait = [&](uint64_t* b, int32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(b, static_cast<uint32_t>(parity & 1))); };
+        auto wait = [&](uint64_t* b, int32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(b, static_cast<uint32_t>(parity & 1), p.waits.limit_ns)); };
         for (int32_t j = 0; j < nt; ++j) {
             const uint32_t st = static_cast<uint32_t>(j & 1);
             ok = wait(&S.rawfull[0], j) && (j < 2 || wait(&S.kfree[st], (j >> 1) - 1));
@@ -469,12 +469,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 const bool far = __any_sync(0xffffffffu, mine && ids >= 0 && c.z == 0.0f);
                 for (int32_t half = 0; half < 2; ++half) {  // K, V
                     const uint32_t rs = static_cast<uint32_t>(half);
-                    if (j >= 1) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.rawfree[rs], static_cast<uint32_t>((j - 1) & 1)));
+                    if (j >= 1) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.rawfree[rs], static_cast<uint32_t>((j - 1) & 1), p.waits.limit_ns));
                     if (!ok) break;
                     if (half == 0 && mine) S.cst[j % kPrCst][gl] = c;
                     if (half == 0 && lane == 0) S.gap[j % kPrCst] = n16 < kPrGroups || far ? 1u : 0u;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_expect_tx(&S.rawfull[rs], n16 * 16u * D);
+                    if (lane == 0) mbar_arrive_expect_tx(&S.rawfull[rs], n16 * 16u * D + p.waits.beyond);
                     __syncwarp();
                     if (mine && ids >= 0)
                         bulk_load(sRaw + rs * (kTile / 2) + gl * 16u * D, (half ? p.c.v : p.c.k) + off, 16u * D, &S.rawfull[rs]);
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             if (!ok) {  // its own copies in flight land before the block ends
                 if (lane == 0) atomicOr(&S.fault, 1u);
                 for (int32_t i = issued > kPrRaw ? issued - kPrRaw : 0; i < issued; ++i)
-                    mbar_wait_bounded(&S.rawfull[i & 1], static_cast<uint32_t>((i >> 1) & 1));
+                    mbar_wait_bounded(&S.rawfull[i & 1], static_cast<uint32_t>((i >> 1) & 1), p.waits.limit_ns);
             }
             meet<kMeetAll, kPrThreads>();
             return;
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         bool ok = true;
         int32_t issued[2] = {0, 0};  // PV products of each row tile
         int32_t scored[2] = {0, 0};  // score products of each row tile
-        auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(b, parity)); };
+        auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(b, parity, p.waits.limit_ns)); };
         auto scores = [&](int32_t i, int32_t j) {  // S_i = Q_i K_j^T
             const uint64_t a0 = dq + static_cast<uint32_t>(i) * (kTile >> 4), b0 = dk + static_cast<uint32_t>(j & 1) * (kTile >> 4);
             if (elect_one()) {
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             top = fmaxf(tops[0], tops[1]);
         };
         for (int32_t j = 0; j < nt; ++j) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.sfull[wg], static_cast<uint32_t>(j & 1)));
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.sfull[wg], static_cast<uint32_t>(j & 1), p.waits.limit_ns));
             if (!ok) break;
             tc_fence_after();
             const int32_t tb = tok0 + j * kPrTokens;
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             if (__any_sync(0xffffffffu, grow)) {
                 const float ah = !grow ? 1.0f : (mx == -INFINITY ? 0.0f : exp2_fast(-0.5f * top)), al = ah * ah;
                 if (j > 0) {  // O moves to the new maximum once the product before this one is done with it
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((j - 1) & 1)));
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((j - 1) & 1), p.waits.limit_ns));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             if (lane == 0) mbar_arrive(&S.pfull[wg]);
         }
         if (ok && nt > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((nt - 1) & 1)));
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((nt - 1) & 1), p.waits.limit_ns));
             tc_fence_after();
         }
         if (!ok && lane == 0) atomicOr(&S.fault, 1u);

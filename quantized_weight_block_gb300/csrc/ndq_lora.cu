@@ -515,14 +515,14 @@ __global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const Lo
                 for (int64_t c = w; c < end; ++c) {
                     const int64_t n0 = c % per * cols;
                     const int st = issued % stages;
-                    if (issued >= stages) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_empty[st], static_cast<uint32_t>((issued / stages - 1) & 1)));
+                    if (issued >= stages) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_empty[st], static_cast<uint32_t>((issued / stages - 1) & 1), p.waits.limit_ns));
                     if (!ok) break;
                     const uint32_t nc = static_cast<uint32_t>(p.N - n0 < cols ? p.N - n0 : cols);
                     const uint32_t wb = weights ? nc * static_cast<uint32_t>(rmax) * 2u : 0u;
                     uint8_t* d = ring + static_cast<uint32_t>(st) * stage;
                     if (lane == 0) {
                         // (all 64 rows, zeros past M and N: those of other adapters are not looked at)
-                        mbar_arrive_expect_tx(&s_full[st], kExpandRows * static_cast<uint32_t>(cols) * EL + wb);
+                        mbar_arrive_expect_tx(&s_full[st], kExpandRows * static_cast<uint32_t>(cols) * EL + wb + p.waits.beyond);
                         asm volatile(
                             "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
                                 "r"(smem_addr(d)),
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const Lo
                 atomicOr(p.fault, kLoraFault);
             }
             for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
-                mbar_wait_bounded(&s_full[i % stages], static_cast<uint32_t>((i / stages) & 1));
+                mbar_wait_bounded(&s_full[i % stages], static_cast<uint32_t>((i / stages) & 1), p.waits.limit_ns);
         }
         __syncthreads();
         return;
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const Lo
     auto meet = [&]() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kExpandWarps * 32) : "memory"); };
 
     int used = 0;
-    bool ok = true;  // (a warp whose wait ran out goes on without working: the others meet it)
+    bool ok = true;  // (a warp whose wait ran out goes on without working: the others meet it; the loader's wait for it runs out)
     for (int64_t w = w0; w < w1;) {
         const int64_t tile = w / per, m0 = tile * kExpandRows;
         const int64_t end = (tile + 1) * per < w1 ? (tile + 1) * per : w1;
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const Lo
                 const uint8_t* sb = nullptr;
                 if constexpr (VEC) {
                     const int st = used % stages;
-                    ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[st], static_cast<uint32_t>((used / stages) & 1)));
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[st], static_cast<uint32_t>((used / stages) & 1), p.waits.limit_ns));
                     sb = ring + static_cast<uint32_t>(st) * stage;
                 }
                 if (ok && static_cast<int>(32 * cg) < cols) {
@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const Lo
                 }
                 if constexpr (VEC) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_empty[used % stages]);
+                    if (lane == 0 && ok) mbar_arrive(&s_empty[used % stages]);  // (a stage that did not land is not filled again)
                     ++used;
                 }
             }

@@ -9,6 +9,15 @@
 
 namespace ndq {
 
+// What the kernels wait with: the limit of a wait, and the bytes that every
+// staged copy is waited for beyond those it brings (0; else a requested check
+// of the failure path: no copy is ever seen to land).
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
+struct Waits {
+    uint64_t limit_ns = kWaitNs;
+    uint32_t beyond = 0;
+};
+
 struct PlanParams {
     const int32_t* cached;
     const int32_t* fresh;
@@ -88,6 +97,7 @@ struct AttnParams {
     int32_t group_shift;  // its logarithm, or -1
     float scale_log2;  // scale * log2(e)
     unsigned int* fault;  // device fault word (set by the launcher)
+    Waits waits;
     int32_t splits;       // prompts: CTAs per unit (set by the launcher)
     int32_t prompt_rows;  // > 0: requests with at least this many rows are left to the prompt kernel
 };
@@ -107,6 +117,7 @@ struct LoraParams {
     float* t;  // workspace
     int64_t M, K, N, nA, rmax;
     unsigned int* fault;  // device fault word (set by the launcher)
+    Waits waits;
 };
 size_t lora_workspace_bytes(int64_t M, int64_t rmax, int64_t K);
 int launch_lora(const LoraParams& p, bool out_f32, void* stream);

@@ -9,6 +9,15 @@
 
 namespace {
 
+// A failure-path check requested for this host thread's next call with copies.
+thread_local ndq::Waits t_waits;
+
+ndq::Waits take_waits() {
+    const ndq::Waits w = t_waits;
+    t_waits = ndq::Waits{};
+    return w;
+}
+
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 int block_log2(int bs) {
@@ -183,6 +192,7 @@ int ndq_attention_kv8(const ndq_kv_cache* cache, const void* q, int dtype, int64
     for (int i = 0; i < 13; ++i)
         if (p.group == 1 << i) p.group_shift = i;
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    p.waits = take_waits();
     return ndq::launch_attention(p, cache->head_dim, cache->code_type == NDQ_FLOAT8E4M3FN, dtype == NDQ_BFLOAT16,
                                  stream) == 0
                ? NDQ_OK
@@ -227,7 +237,18 @@ int ndq_lora_add(const void* x_bf16, int64_t M, int64_t K, const void* lora_a, c
     p.N = N;
     p.nA = n_adapters;
     p.rmax = max_rank;
+    p.waits = take_waits();
     return ndq::launch_lora(p, dtype == NDQ_FLOAT, stream) == 0 ? NDQ_OK : NDQ_ERR_CUDA;
+}
+
+int ndq_test_lose_copies(uint32_t wait_limit_us) {
+    if (wait_limit_us > 2000000u || (wait_limit_us > 0 && wait_limit_us < 1000u)) return NDQ_ERR_BAD_COUNT;
+    t_waits = ndq::Waits{};
+    if (wait_limit_us > 0) {
+        t_waits.limit_ns = static_cast<uint64_t>(wait_limit_us) * 1000u;
+        t_waits.beyond = 16u;
+    }
+    return NDQ_OK;
 }
 
 }  // extern "C"

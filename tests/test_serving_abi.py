@@ -131,3 +131,9 @@ def test_plan_outputs_over_other_arrays_are_refused(out, other):
     # the same place, the output's last element on the other's first, its first on the other's last
     for shift in (0, -(PLAN_PARTS[out] - step) // step * step, (PLAN_PARTS[other] - 1) // step * step):
         assert plan(n_req=3, table_width=4, n_tokens=5, **(apart | {out: apart[other] + shift})) == BAD_ARG
+
+
+def test_failure_path_requests():
+    for limit in (1, 999, 2000001):
+        assert ndq.ndq_test_lose_copies(limit) == 13
+    assert ndq.ndq_test_lose_copies(1000) == OK and ndq.ndq_test_lose_copies(0) == OK  # (cancelled)
