@@ -609,10 +609,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 for (int e = 0; e < 16; e += 2) tops[(e >> 1) & 1] = max3(tops[(e >> 1) & 1], y[e], y[e + 1]);
                 if constexpr (kMasked) {
                     if (k.z == 0.0f) {  // (rare: V's scale far below others', or a missing block)
-                        float d = 0.0f;
+                        const float up = k.y == -INFINITY ? 0.0f : k.y;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) d += y[e] == -INFINITY ? 0.0f : exp2_fast(y[e] - k.y);
-                        ts += d;
+                        for (int e = 0; e < 16; ++e) ts += exp2_fast(y[e] - up);
                     }
                 }
 #pragma unroll
