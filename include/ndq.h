@@ -467,8 +467,11 @@ int ndq_attention_kv8(const ndq_kv_cache *cache, const void *q, int dtype, int64
  *   workspace  device buffer of ndq_lora_workspace_bytes(...) bytes, 16-byte
  *           aligned; not shared by calls that may overlap
  * 1 <= max_rank <= 128, M * max_rank below 2^31.  A workspace sized for some
- * M, max_rank and K serves smaller ones.  Products are exact and sums binary32 in a fixed
- * order; y is rounded once.  Rows of one adapter run fastest when adjacent,
+ * M, max_rank and K serves smaller ones.  x A^T has exact products and
+ * binary32 sums in a fixed order.  Beside few rows the second product is
+ * binary32, too; beside 128 and more it takes the scaled x A^T as a sum of
+ * bfloat16 parts, to 2^-24 of it for binary32 results and to 2^-16 for bfloat16
+ * ones.  y is rounded once at the end.  Rows of one adapter run fastest when adjacent,
  * any order is right.  M, N, K or n_adapters of 0 is valid. */
 size_t ndq_lora_workspace_bytes(int64_t M, int64_t max_rank, int64_t K);
 int ndq_lora_add(const void *x_bf16, int64_t M, int64_t K, const void *lora_a, const void *lora_b,

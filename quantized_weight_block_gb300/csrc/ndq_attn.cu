@@ -34,11 +34,11 @@
 // the exponent, t = s ks + log2(vs), so that the weights 2^(t - m) which go to
 // binary16 lose nothing to a V of small scale; the denominator sums
 // 2^(t - m) / vs, or 2^(s ks - m) where vs lies far below others (kScaleSpread).
-// Measured: 8 requests with 16k to 131k tokens, 64 heads on 8 (1.23 GB): 215 us,
-// 5.7 TB/s, 0.84 of the measured copy bandwidth; 64 requests of up to 8k
-// tokens, 32 heads on 8 (553 MB): 113-122 us, 4.5-4.9 TB/s; one request of 777
-// tokens: 9.4 us, latency (3500 cycles until the first copy, 3000 a step, 3000
-// for the join across CTAs).
+// Measured: 8 requests with 16k to 131k tokens, 64 heads on 8 (1.23 GB): 217-222
+// us, 5.6 TB/s, 0.82-0.83 of the measured copy bandwidth; 64 requests of up to
+// 8k tokens, 32 heads on 8 (553 MB): 112-120 us, 4.6-4.9 TB/s; one request of
+// 777 tokens: 9.4 us, latency (3500 cycles until the first copy, 3000 a step,
+// 3000 for the join across CTAs).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

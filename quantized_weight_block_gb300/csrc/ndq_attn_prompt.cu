@@ -29,10 +29,14 @@
 // is rescaled rarely; P is then at most 2^8.
 //
 // Measured: four chunks of 1200 to 4000 tokens over 2k to 8k earlier ones, 32
-// heads of 128 on 8 (1.19 TFLOP): 1.11-1.23 ms, 0.97-1.07 PFLOP/s, 0.51-0.56 of
-// the measured bfloat16 rate.  A product of 128 x 128 x 128 takes 810 cycles
-// instead of 512: its operands and the converters together ask more of shared
-// memory than its 128 bytes a cycle.
+// heads of 128 on 8 (1.19 TFLOP): 1.22-1.25 ms, 0.95-0.98 PFLOP/s, 0.50-0.51 of
+// the measured bfloat16 rate.  What bounds it is a row tile's chain: P lies in
+// its scores' columns, so the next scores wait for the value product, which
+// waits for all of the softmax.  That is 810 + 810 + 2035 cycles of the 4690
+// per 128 tokens, the rest handing over; the other row tile fills only part of
+// the gaps.  (Shared memory moves 320 KB a tile, 2560 of the cycles: the score
+// products' operands 2 x 64 KB, the value products' 2 x 32 KB, converters and
+// copies 128 KB.)
 //
 // What a tile's rows do not all see is masked per element.  Tokens that no
 // row of the CTA sees enter as zeros; a NaN code of V that only some rows see

@@ -442,9 +442,15 @@ template <int D, bool E4M3>
 int append_typed(const AppendParams& p, bool bf16, void* stream) {
     const int64_t units = 2 * static_cast<int64_t>(p.c.heads);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // A warp per token, head and K or V while all of them are resident at once
-    // (a step: latency).  More tokens are prompts, whose runs are blocks: a
-    // CTA per 32 tokens works on the runs that start there.
+    // A warp per token, head and K or V while all of them are resident at once;
+    // beyond, a CTA per 32 tokens, which works on the runs that start there.
+    // What decides is the length of the runs, which the host does not know:
+    // the number of tokens stands for it.  Measured (INT8, heads of 128, blocks
+    // of 64; by warps / by CTAs, us): one token each of 64, 400, 1024 requests,
+    // 8 heads: 3.5 / 47, 8.4 / 50, 17 / 68; one prompt of 450 tokens, 8 heads:
+    // 24 / 4.8; of 1024, 8 heads: 28 / 8.0; of 3600, one head: 12 / 5.0.  So
+    // steps of more than 456 requests at 8 heads, and prompts below as many
+    // tokens, take the slower form.
     if (p.n_tokens * units <= 152 * 48) {
         const unsigned grid = static_cast<unsigned>((p.n_tokens * units + kAppendWarps - 1) / kAppendWarps);
         if (bf16) k_kv_append<D, E4M3, true, 1><<<grid, kAppendWarps * 32, 0, st>>>(p, 1);

@@ -27,10 +27,10 @@
 // Any other alignment (K or max_rank not a multiple of 8, buffers off 16
 // bytes) takes the few-row kernel with scalar loads.
 //
-// Measured: 61 rows, 48 adapters of rank 16, K = N = 4096: 5.8 us (8.2 us a call
-// from Python); 5003 rows of six requests, rank 64, K = 4096, N = 14336,
-// bfloat16: 27 us for the shrink, 118 us for the expansion (288 MB: 2.4 TB/s; its
-// mma.sync products alone are 46 us of every SM's time).
+// Measured: 61 rows, 48 adapters of rank 16, K = N = 4096: 5.8 us (8.1-8.9 us a
+// call from Python); 5003 rows of six requests, rank 64, K = 4096, N = 14336,
+// bfloat16: 124-128 us, 28 for the shrink and 98 for the expansion (288 MB: 2.9
+// TB/s; its mma.sync products alone are 46 us of every SM's time).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -713,10 +713,15 @@ __global__ void __launch_bounds__(kExpandThreads, 1) k_lora_expand_tile(const Lo
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Rows from which the tensor-core tiles are taken.  Measured (K = 4096, r 16,
-// N = 4096 / r 64, N = 14336): 61 rows of one adapter 6 / 27 us here, 96 rows
-// 13 / 18 us in tiles; 61 rows of 48 adapters 7 / 47 us here, where a tile goes
-// through its adapters one by one.
+// Rows from which the tensor-core tiles are taken.  What decides is the rows of
+// an adapter, which the host does not know: the number of rows stands for it.
+// Measured (K = 4096, bfloat16; row by row / in tiles, us), at rank 16, N = 4096
+// one adapter: 61 rows 6.1 / 10, 128 rows 10 / 10, 512 rows 34 / 14; rows dealt to
+// 48 adapters in turn: 61 rows 6.4 / 41, 128 rows 11 / 69, 512 rows 36 / 180.  At
+// rank 64, N = 14336 one adapter: 61 rows 45 / 17, 150 rows 101 / 18, 512 rows
+// 298 / 24; 48 adapters: 61 rows 47 / 123, 150 rows 120 / 231, 512 rows 342 / 465.
+// So many rows of as many adapters take the slower form, and wide projections
+// beside fewer than 128 rows of one adapter, too.
 constexpr int64_t kTileMinRows = 128;
 
 // K splits: as many CTAs as two on each SM make at most (one more would wait
