@@ -7,7 +7,9 @@ the [128256,4096] embedding in gguf:q8_0) from HBM-resident payloads into
 bf16, i.e. every row of the decode path: validation, block staging, scale
 decode, code unpack, FP32 arithmetic, RNE cast and the batched launcher.
 
-Printed (rank 0, one JSON line on stdout):
+Printed (rank 0): one JSON line on stdout, kept below 2500 characters, and
+before it, on stderr, one line "[bench] details" with the JSON of everything
+measured.  In the line:
   value         dequant GB/s = (payload bytes + output bytes) / step time,
                 whole job (all ranks), inputs resident in HBM;
   e2e           the same metric through the public API with host buffers:
@@ -15,6 +17,8 @@ Printed (rank 0, one JSON line on stdout):
                 decodes, and copies the decoded bf16 weights device->host;
   roofline      the decode kernel against the measured HBM copy bandwidth;
   cpu_baseline  the CPU oracle on a bounded sample of the same workload;
+  parity        the timed launch's whole output against the oracle's.
+In the details also:
   per_workload  the single-format workloads (q8_0, q4_0, q4_g64, q4_k, q6_k,
                 nvfp4, mxfp4, iq4_nl), each timed back to back over buffer
                 sets larger than L2 and as one launch after an L2 eviction;
@@ -89,6 +93,34 @@ def parse_args():
     ap.add_argument("--only", default=None,
                     help="time one single-format workload (a label of synth.WORKLOADS) for --steps steps and exit")
     return ap.parse_args()
+
+
+# What the line on stdout holds of each part (None: all of it).
+LINE_PARTS = {
+    "config": None, "clocks": None,
+    "roofline": ("bound", "achieved", "peak", "unit", "frac", "traffic", "peak_source"),
+    "parity": ("bit_exact", "elements", "mismatches", "tensors"),
+    "payload_sha256": ("whole_model",),
+    "cpu_baseline": ("value", "unit", "cores", "kind", "elements/s", "seconds", "sample"),
+    "e2e": ("value", "unit", "ms_per_step", "steps", "h2d_bytes_per_step", "d2h_bytes_per_step", "gpu_launches_per_step"),
+}
+LINE_MAX = 2500
+
+
+def result_line(res):
+    """The JSON line for the measured result: its numbers, and of its parts what
+    LINE_PARTS names; the tables are left to the details."""
+    out = {}
+    for k, v in res.items():
+        if not isinstance(v, dict):
+            out[k] = v
+        elif k in LINE_PARTS:
+            keep = LINE_PARTS[k]
+            out[k] = {x: y for x, y in v.items() if keep is None or x in keep}
+    line = json.dumps(out)
+    if len(line) >= LINE_MAX:
+        raise RuntimeError(f"the result line has {len(line)} characters, {LINE_MAX} or more")
+    return line
 
 
 def log(*a):
@@ -927,7 +959,8 @@ def run_ours(args, rank, world, local_rank):
     if world > 1:
         torch.distributed.destroy_process_group()
     if rank == 0:
-        print(json.dumps(res), flush=True)
+        log("[bench] details " + json.dumps(res))
+        print(result_line(res), flush=True)
 
 
 # --------------------------------------------------------------------------
