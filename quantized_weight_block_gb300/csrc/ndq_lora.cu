@@ -29,7 +29,7 @@
 //
 // Measured: 61 rows, 48 adapters of rank 16, K = N = 4096: 5.8 us (8.1-8.9 us a
 // call from Python); 5003 rows of six requests, rank 64, K = 4096, N = 14336,
-// bfloat16: 124-128 us, 28 for the shrink and 98 for the expansion (288 MB: 2.9
+// bfloat16: 123-128 us, 28 for the shrink and 98 for the expansion (288 MB: 2.9
 // TB/s; its mma.sync products alone are 46 us of every SM's time).
 
 #include <cuda_bf16.h>
