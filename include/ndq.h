@@ -59,6 +59,10 @@ extern "C" {
 #define NDQ_DOUBLE 11
 #define NDQ_BFLOAT16 16
 
+/* Index types of token ids (again the ONNX data-type numbers). */
+#define NDQ_INT32 6
+#define NDQ_INT64 7
+
 /* Cache code types (again the ONNX data-type numbers). */
 #define NDQ_INT8 3
 #define NDQ_FLOAT8E4M3FN 17
@@ -266,6 +270,25 @@ typedef struct ndq_matmul_desc {
 int ndq_matmul_packed_batched(const ndq_matmul_desc *descs, int count, int64_t K, const void *x_bf16, int64_t M,
                               int weight_dtype, int out_dtype, void *stream);
 
+/* Rows of a packed table, decoded and scaled (the token embedding of a model
+ * whose table is packed like its other weights):
+ *     y[t] = scale * W[ids[t]]        W [V, K]
+ *   format_id, w, w_len   the table's payload, under the same length rule as
+ *              ndq_dequantize_packed (the fp8 row formats need K % 16 == 0)
+ *   ids        device [n_tokens] of ids_dtype (NDQ_INT32 or NDQ_INT64); an id
+ *              outside [0, V) gives a row of zeros
+ *   y          device rows of out_dtype (NDQ_FLOAT, NDQ_FLOAT16 or
+ *              NDQ_BFLOAT16), y_stride >= K elements apart; what lies between
+ *              rows stays as it was.  Rows 16-byte aligned take the bulk
+ *              store, others element stores.
+ * Each value is the binary32 decode of ndq_dequantize_packed, times scale
+ * (finite; one binary32 rounding, none for 1), rounded once to out_dtype.
+ * Only the rows that are asked for are read.  Same ownership, asynchrony and
+ * error rules as ndq_dequantize_packed; y may overlap neither w nor ids.
+ * V, K or n_tokens of 0 is valid; n_tokens * ceil(K / 256) is below 2^31. */
+int ndq_embed_packed(int format_id, int64_t V, int64_t K, const uint8_t *w, size_t w_len, const void *ids, int ids_dtype,
+                     int64_t n_tokens, float scale, int out_dtype, void *y, int64_t y_stride, void *stream);
+
 /* Device workspace bytes the batched call needs for n tensors (a table of
  * per-tensor launch descriptors), or 0 when n < 0. */
 size_t ndq_batched_workspace_bytes(int n);
@@ -322,11 +345,12 @@ int ndq_dequantize_packed_batched_noalloc(const ndq_tensor_desc *descs, int n, v
 /* ------------------------------------------------------------------------ */
 /* Serving operators: what a generation step over packed weights needs        */
 /* beside its products.  (No counterpart on the pages.)  A step calls         */
-/* ndq_kv_plan, then for every layer ndq_matmul_packed[_batched] (+           */
-/* ndq_lora_add), ndq_kv_append and ndq_attention_kv8.  Like the calls above  */
-/* they allocate nothing, validate on the host before any launch and run      */
-/* asynchronously on `stream`; lengths, tables and slots stay on the device   */
-/* and are never read by the host.                                            */
+/* ndq_kv_plan and ndq_embed_packed, then for every layer                     */
+/* ndq_matmul_packed[_batched] (+ ndq_lora_add), ndq_qk_norm_rope,            */
+/* ndq_kv_append and ndq_attention_kv8.  Like the calls above they allocate   */
+/* nothing, validate on the host before any launch and run asynchronously on  */
+/* `stream`; lengths, tables and slots stay on the device and are never read  */
+/* by the host.                                                               */
 /* ------------------------------------------------------------------------ */
 
 /* A key/value cache in 8-bit codes with one binary32 scale for each block of
@@ -451,6 +475,34 @@ int ndq_attention_kv8(const ndq_kv_cache *cache, const void *q, int dtype, int64
                       int64_t q_stride, const int32_t *block_table, int64_t table_width, const int32_t *kv_len,
                       const int32_t *q_start, int64_t n_req, int64_t max_q, float scale, int64_t window, void *out,
                       float *lse, void *workspace, size_t ws_bytes, void *stream);
+
+/* Norms of query and key heads and their rotation by position, in one pass:
+ *     z = x / sqrt(mean(x^2) + eps) * weight     (z = x without a weight)
+ *     (a, b) -> (a cos f - b sin f, a sin f + b cos f),   f = positions[t] * inv_freq[i]
+ * for pair i < rot_dim / 2 of a head's first rot_dim values: z[i] and
+ * z[i + rot_dim / 2], or z[2 i] and z[2 i + 1] when interleaved is 1.
+ *   q, k       device rows [n_tokens, heads, head_dim] of in_dtype (NDQ_FLOAT,
+ *              NDQ_BFLOAT16 or NDQ_FLOAT16), q_stride / k_stride elements
+ *              apart, heads dense; parts of one row of a fused projection will do
+ *   head_dim   a multiple of 16, 16 to 256; rot_dim a multiple of 16, 0 to
+ *              head_dim (the other values are only normed)
+ *   positions  device int32 [n_tokens], as ndq_kv_plan writes them; rows of a
+ *              token whose position is negative are not written
+ *   inv_freq   device binary32 [rot_dim / 2], magnitudes up to 1
+ *   q_weight, k_weight   device binary32 [head_dim], or NULL: no norm
+ *   eps        finite, 0 or more
+ *   q_out, k_out   device rows of out_dtype (NDQ_BFLOAT16 or NDQ_FLOAT16);
+ *              q_out may be q (k_out k) with the same type and stride, and
+ *              otherwise no output may overlap an input or the other output
+ * Bases are 16-byte aligned and strides multiples of 8.  Heads of 0 are valid
+ * (then that side's pointers are not looked at).  Angles are exact to 2^-31 of
+ * a turn at every position; norms, products and sums are binary32 (squares
+ * that would overflow or vanish are scaled first), each result is rounded once
+ * to out_dtype. */
+int ndq_qk_norm_rope(const void *q, int q_heads, int64_t q_stride, const void *k, int k_heads, int64_t k_stride, int in_dtype,
+                     int64_t n_tokens, int head_dim, int rot_dim, int interleaved, const int32_t *positions,
+                     const float *inv_freq, const float *q_weight, const float *k_weight, float eps, void *q_out,
+                     int64_t q_out_stride, void *k_out, int64_t k_out_stride, int out_dtype, void *stream);
 
 /* Low-rank adapters of many requests beside a shared projection:
  *   y[m] = base[m] + scales[a] * (x[m] A[a]^T) B[a]^T,   a = index[m]

@@ -35,6 +35,7 @@ STATUS = {
 }
 NDQ_FLOAT, NDQ_FLOAT16, NDQ_DOUBLE, NDQ_BFLOAT16 = 1, 10, 11, 16
 NDQ_INT8, NDQ_FLOAT8E4M3FN = 3, 17
+NDQ_INT32, NDQ_INT64 = 6, 7
 NDQ_MAX_RANK = 8
 NDQ_NUM_FORMATS = 36
 NDQ_NOALLOC_MAX_TENSORS = 1024
@@ -103,6 +104,10 @@ _lib.ndq_attention_workspace_bytes.argtypes = [_c.c_int]
 _lib.ndq_attention_workspace_bytes.restype = _c.c_size_t
 _lib.ndq_attention_kv8.argtypes = [_c.POINTER(ndq_kv_cache), _p, _c.c_int, _i64, _c.c_int, _i64, _p, _i64, _p, _p, _i64,
                                    _i64, _c.c_float, _i64, _p, _p, _p, _c.c_size_t, _p]
+_lib.ndq_embed_packed.argtypes = [_c.c_int, _i64, _i64, _p, _c.c_size_t, _p, _c.c_int, _i64, _c.c_float, _c.c_int, _p, _i64,
+                                  _p]
+_lib.ndq_qk_norm_rope.argtypes = [_p, _c.c_int, _i64, _p, _c.c_int, _i64, _c.c_int, _i64, _c.c_int, _c.c_int, _c.c_int, _p, _p,
+                                  _p, _p, _c.c_float, _p, _i64, _p, _i64, _c.c_int, _p]
 _lib.ndq_lora_workspace_bytes.argtypes = [_i64, _i64, _i64]
 _lib.ndq_lora_workspace_bytes.restype = _c.c_size_t
 _lib.ndq_lora_add.argtypes = [_p, _i64, _i64, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _c.c_int, _p, _p, _c.c_size_t,
@@ -116,6 +121,7 @@ EXPORTS = (
     "ndq_matmul_packed", "ndq_test_withhold_copy", "ndq_matmul_packed_batched",
     "ndq_kv_plan", "ndq_kv_append", "ndq_attention_workspace_bytes", "ndq_attention_kv8",
     "ndq_lora_workspace_bytes", "ndq_lora_add", "ndq_test_lose_copies",
+    "ndq_embed_packed", "ndq_qk_norm_rope",
 )
 
 
@@ -370,6 +376,22 @@ def ndq_attention_kv8(cache, q: int, dtype: int, n_tokens: int, q_heads: int, q_
                                   q_start, n_req, max_q, scale, window, out, lse, workspace, ws_bytes, stream)
 
 
+def ndq_embed_packed(format_id: int, V: int, K: int, w: int, w_len: int, ids: int, ids_dtype: int, n_tokens: int, scale: float,
+                     out_dtype: int, y: int, y_stride: int, stream: int = 0) -> int:
+    """Raw call (device pointers as integers); returns the status code."""
+    return _lib.ndq_embed_packed(format_id, V, K, w, w_len, ids, ids_dtype, n_tokens, scale, out_dtype, y, y_stride, stream)
+
+
+def ndq_qk_norm_rope(q: int, q_heads: int, q_stride: int, k: int, k_heads: int, k_stride: int, in_dtype: int, n_tokens: int,
+                     head_dim: int, rot_dim: int, interleaved: int, positions: int, inv_freq: int, q_weight: int, k_weight: int,
+                     eps: float, q_out: int, q_out_stride: int, k_out: int, k_out_stride: int, out_dtype: int,
+                     stream: int = 0) -> int:
+    """Raw call (device pointers as integers); returns the status code."""
+    return _lib.ndq_qk_norm_rope(q, q_heads, q_stride, k, k_heads, k_stride, in_dtype, n_tokens, head_dim, rot_dim, interleaved,
+                                 positions, inv_freq, q_weight, k_weight, eps, q_out, q_out_stride, k_out, k_out_stride,
+                                 out_dtype, stream)
+
+
 def ndq_lora_workspace_bytes(M: int, max_rank: int, K: int) -> int:
     return _lib.ndq_lora_workspace_bytes(M, max_rank, K)
 
@@ -388,6 +410,7 @@ class _Torch:
     def __init__(self):
         torch = _torch()
         self.f32, self.bf16, self.i32, self.i64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
+        self.u8, self.f16 = torch.uint8, torch.float16
         self.raw_stream = torch._C._cuda_getCurrentRawStream
         self.code = {torch.float32: NDQ_FLOAT, torch.float16: NDQ_FLOAT16, torch.bfloat16: NDQ_BFLOAT16}
 
@@ -441,6 +464,34 @@ def _check(name, x, dtype, shape, device):
 def _check_workspace(x, device: int):
     if x.get_device() != device or not x.is_contiguous():
         raise ValueError("the workspace must be contiguous, on the other tensors' device")
+
+
+def embed_packed(fmt, w, V: int, K: int, ids, scale: float = 1.0, out_dtype=None, out=None, stream=None):
+    """scale * W[ids] with the table W [V, K] packed in the CUDA uint8 payload
+    `w` (see ndq_embed_packed): ids int32 or int64 [T]; an id outside the table
+    gives zeros.  out [T, K] (float32, float16 or bfloat16, dense rows) or
+    out_dtype (default bfloat16).  Returns out."""
+    c = _T or _consts()
+    if w.dtype is not c.u8 or not w.is_contiguous() or ids.dim() != 1 or not ids.is_contiguous():
+        raise ValueError("embed_packed: w must be a contiguous uint8 payload and ids contiguous [tokens]")
+    idt = NDQ_INT32 if ids.dtype is c.i32 else NDQ_INT64 if ids.dtype is c.i64 else None
+    if idt is None:
+        raise ValueError("ids must be int32 or int64")
+    gpu, T = w.get_device(), ids.shape[0]
+    if out is None:
+        out = _made_for(stream, lambda: _torch().empty((T, K), dtype=out_dtype or c.bf16, device=w.device))
+        _returned(stream, out)
+    elif out.shape != (T, K) or (out_dtype is not None and out.dtype is not out_dtype) or (K > 1 and out.stride(1) != 1):
+        raise ValueError("out must be [tokens, K] of out_dtype, with dense rows")
+    code = c.code.get(out.dtype)
+    if code is None:
+        raise ValueError("embed_packed writes float32, float16 or bfloat16")
+    _same_device("embed_packed", gpu, ids, out)
+    rc = _lib.ndq_embed_packed(fmt if isinstance(fmt, int) else format_id(fmt), V, K, w.data_ptr(), w.numel(), ids.data_ptr(), idt,
+                               T, scale, code, out.data_ptr(), out.stride(0) if T > 1 else K, _raw_stream(stream, gpu))
+    if rc:
+        raise NdqError(rc, "embed_packed")
+    return out
 
 
 class KvCache:
@@ -612,6 +663,65 @@ def attention_kv8(q, cache: KvCache, block_table, kv_len, q_start=None, max_q=No
     if rc:
         raise NdqError(rc, "attention_kv8")
     return out
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                 q_out=None, k_out=None, out_dtype=None, stream=None):
+    """Norm (with a weight) and rotation of the heads q [T, q_heads, D] and k
+    [T, k_heads, D] by positions [T] (see ndq_qk_norm_rope): float32, bfloat16
+    or float16, token strides of any multiple of 8; either may be None.
+    inv_freq float32 [rot_dim / 2] says how much of a head is rotated, weights
+    are float32 [D].  The outputs are bfloat16 or float16 (default: the inputs'
+    type, bfloat16 for float32), and may be q and k themselves.  Rows of
+    negative positions are not written (and zero in outputs made here).
+    Returns (q_out, k_out)."""
+    c = _T or _consts()
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("qk_norm_rope needs q or k")
+    if first.dim() != 3 or positions.dim() != 1 or inv_freq.dim() != 1:
+        raise ValueError("q and k must be [tokens, heads, head_dim], positions [tokens] and inv_freq [rot_dim / 2]")
+    T, D, dtype = first.shape[0], first.shape[2], first.dtype
+    code = c.code.get(dtype)
+    if code is None:
+        raise ValueError("q and k must be float32, bfloat16 or float16")
+    if (positions.dtype is not c.i32 or positions.shape[0] != T or not positions.is_contiguous() or inv_freq.dtype is not c.f32
+            or not inv_freq.is_contiguous()):
+        raise ValueError("positions must be int32 [tokens] and inv_freq float32 [rot_dim / 2], both contiguous")
+    gpu = first.get_device()
+    _same_device("qk_norm_rope", gpu, first, positions, inv_freq)
+    given = q_out if q_out is not None else k_out
+    odt = out_dtype or (given.dtype if given is not None else dtype if dtype is not c.f32 else c.bf16)
+    if odt is not c.bf16 and odt is not c.f16:
+        raise ValueError("qk_norm_rope writes bfloat16 or float16")
+    args, outs = [], []
+    for name, x, y, w in (("q", q, q_out, q_weight), ("k", k, k_out, k_weight)):
+        if x is None:
+            if y is not None or w is not None:
+                raise ValueError(f"{name}_out and {name}_weight need {name}")
+            args.append((None, 0, 0, None, None, 0))
+            outs.append(None)
+            continue
+        if x.dtype is not dtype or x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or x.get_device() != gpu:
+            raise ValueError("q and k must have the same type, tokens and head_dim, on one device")
+        H = x.shape[1]
+        if w is not None and (w.dtype is not c.f32 or w.shape != (D,) or not w.is_contiguous() or w.get_device() != gpu):
+            raise ValueError(f"{name}_weight must be float32 [head_dim], contiguous, on {name}'s device")
+        if y is None:
+            y = _made_for(stream, lambda shape=x.shape: _torch().zeros(shape, dtype=odt, device=first.device))
+            _returned(stream, y)
+        elif y.dtype is not odt or y.shape != x.shape or y.get_device() != gpu:
+            raise ValueError(f"{name}_out must be {odt}, of {name}'s shape, on its device")
+        args.append((x.data_ptr(), H, _row_stride(name, x, H, D), None if w is None else w.data_ptr(), y.data_ptr(),
+                     _row_stride(name + "_out", y, H, D)))
+        outs.append(y)
+    (qp, qh, qs, qw, qo, qos), (kp, kh, ks, kw, ko, kos) = args
+    rc = _lib.ndq_qk_norm_rope(qp, qh, qs, kp, kh, ks, code, T, D, 2 * inv_freq.shape[0], 1 if interleaved else 0,
+                               positions.data_ptr(), inv_freq.data_ptr(), qw, kw, eps, qo, qos, ko, kos, c.code[odt],
+                               _raw_stream(stream, gpu))
+    if rc:
+        raise NdqError(rc, "qk_norm_rope")
+    return tuple(outs)
 
 
 def lora_workspace(M: int, n_adapters: int, max_rank: int, K: int, device="cuda"):

@@ -10,11 +10,13 @@
 
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <vector>
 
 #include "ndq.h"
+#include "ndq_embed.h"
 #include "ndq_fused.h"
 #include "ndq_internal.h"
 
@@ -429,6 +431,47 @@ int ndq_matmul_packed_batched(const ndq_matmul_desc* descs, int count, int64_t K
         if (rc != NDQ_OK) return rc;
     }
     return NDQ_OK;
+}
+
+int ndq_embed_packed(int format_id, int64_t V, int64_t K, const uint8_t* w, size_t w_len, const void* ids, int ids_dtype,
+                     int64_t n_tokens, float scale, int out_dtype, void* y, int64_t y_stride, void* stream) {
+    if (!valid_id(format_id)) return NDQ_ERR_UNKNOWN_FORMAT;
+    if (V < 0 || K < 0 || n_tokens < 0) return NDQ_ERR_NEGATIVE_DIM;
+    if ((out_dtype != NDQ_FLOAT && out_dtype != NDQ_FLOAT16 && out_dtype != NDQ_BFLOAT16) ||
+        (ids_dtype != NDQ_INT32 && ids_dtype != NDQ_INT64))
+        return NDQ_ERR_BAD_DTYPE;
+    // (the fp8 row formats decode in 16-code units, which must not cross rows here)
+    if (fp8_row(format_id) && K % 16 != 0) return NDQ_ERR_NOT_BLOCK_ALIGNED;
+    const int64_t shape[2] = {V, K};
+    ndq::EmbedParams p;
+    std::memset(&p, 0, sizeof(p));
+    Geometry g;
+    // (the descriptor's output pointer is unused by the kernel)
+    const int rc = prepare(format_id, shape, 2, NDQ_FLOAT, w, w_len, const_cast<uint8_t*>(w), &p.w, &g);
+    if (rc != NDQ_OK) return rc;
+    if (!std::isfinite(scale) || n_tokens > INT32_MAX || y_stride < K || y_stride > (INT64_C(1) << 40)) return NDQ_ERR_BAD_ARG;
+    if (n_tokens == 0 || K == 0) return NDQ_OK;
+    if (!ids || !y) return NDQ_ERR_NULL;
+    const uintptr_t el = out_dtype == NDQ_FLOAT ? 4 : 2, ib = ids_dtype == NDQ_INT32 ? 4 : 8;
+    if (reinterpret_cast<uintptr_t>(y) % el != 0 || reinterpret_cast<uintptr_t>(ids) % ib != 0) return NDQ_ERR_MISALIGNED;
+    if (V == 0) {  // (every id is outside the table, which has no payload to describe)
+        p.w.fmt = kFormats[format_id].kfmt;
+        p.w.B = static_cast<uint16_t>(fp8_row(format_id) ? 16 : kFormats[format_id].B);
+        p.w.S = static_cast<uint16_t>(fp8_row(format_id) ? 16 : kFormats[format_id].S);
+    }
+    p.ids = ids;
+    p.y = y;
+    p.y_stride = static_cast<uint64_t>(y_stride);
+    p.n_rows = static_cast<uint64_t>(V);
+    p.K = static_cast<uint64_t>(K);
+    p.bpr = V > 0 ? p.w.nblocks / static_cast<uint64_t>(V) : 0;
+    p.n_tokens = static_cast<uint32_t>(n_tokens);
+    p.out = out_dtype == NDQ_FLOAT ? ndq::KO_F32 : out_dtype == NDQ_FLOAT16 ? ndq::KO_F16 : ndq::KO_BF16;
+    p.ids64 = ids_dtype == NDQ_INT64;
+    p.scale = scale;
+    p.yvec = (reinterpret_cast<uintptr_t>(y) & 15u) == 0 && (n_tokens == 1 || static_cast<uint64_t>(y_stride) * el % 16 == 0);
+    const int e = ndq::launch_embed(p, stream);
+    return e == 0 ? NDQ_OK : e < 0 ? NDQ_ERR_BAD_ARG : NDQ_ERR_CUDA;
 }
 
 size_t ndq_batched_workspace_bytes(int n) {

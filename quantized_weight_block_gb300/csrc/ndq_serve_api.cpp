@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "ndq.h"
+#include "ndq_rope.h"
 #include "ndq_serve.h"
 
 namespace {
@@ -195,6 +196,65 @@ int ndq_attention_kv8(const ndq_kv_cache* cache, const void* q, int dtype, int64
     p.waits = take_waits();
     return ndq::launch_attention(p, cache->head_dim, cache->code_type == NDQ_FLOAT8E4M3FN, dtype == NDQ_BFLOAT16,
                                  stream) == 0
+               ? NDQ_OK
+               : NDQ_ERR_CUDA;
+}
+
+int ndq_qk_norm_rope(const void* q, int q_heads, int64_t q_stride, const void* k, int k_heads, int64_t k_stride, int in_dtype,
+                     int64_t n_tokens, int head_dim, int rot_dim, int interleaved, const int32_t* positions,
+                     const float* inv_freq, const float* q_weight, const float* k_weight, float eps, void* q_out,
+                     int64_t q_out_stride, void* k_out, int64_t k_out_stride, int out_dtype, void* stream) {
+    if (n_tokens < 0 || q_heads < 0 || k_heads < 0) return NDQ_ERR_NEGATIVE_DIM;
+    if ((in_dtype != NDQ_FLOAT && in_dtype != NDQ_BFLOAT16 && in_dtype != NDQ_FLOAT16) ||
+        (out_dtype != NDQ_BFLOAT16 && out_dtype != NDQ_FLOAT16))
+        return NDQ_ERR_BAD_DTYPE;
+    if (n_tokens > INT32_MAX || q_heads > 4096 || k_heads > 4096 || head_dim < 16 || head_dim > 256 || head_dim % 16 != 0 ||
+        rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0 || !std::isfinite(eps) || eps < 0.0f ||
+        (interleaved != 0 && interleaved != 1))
+        return NDQ_ERR_BAD_ARG;
+    if (n_tokens == 0 || q_heads + k_heads == 0) return NDQ_OK;
+    if (!positions || (rot_dim > 0 && !inv_freq) || (q_heads > 0 && (!q || !q_out)) || (k_heads > 0 && (!k || !k_out)))
+        return NDQ_ERR_NULL;
+    if (!aligned(positions, 4) || !aligned(inv_freq, 4) || !aligned(q_weight, 4) || !aligned(k_weight, 4))
+        return NDQ_ERR_MISALIGNED;
+    struct Side {
+        const void* x;
+        int heads;
+        int64_t stride;
+        void* y;
+        int64_t y_stride;
+    };
+    const Side sides[] = {{q, q_heads, q_stride, q_out, q_out_stride}, {k, k_heads, k_stride, k_out, k_out_stride}};
+    for (const Side& s : sides) {
+        if (s.heads == 0) continue;
+        const int64_t row = static_cast<int64_t>(s.heads) * head_dim;
+        // (rows of 4-byte values are 16-byte aligned every fourth; one rule for all types)
+        int rc = check_rows(s.x, s.stride, row);
+        if (rc == NDQ_OK) rc = check_rows(s.y, s.y_stride, row);
+        if (rc != NDQ_OK) return rc;
+        if (s.x == s.y && (in_dtype != out_dtype || s.stride != s.y_stride)) return NDQ_ERR_BAD_ARG;
+    }
+    ndq::RopeParams p{};
+    p.q = q;
+    p.k = k;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.q_weight = q_weight;
+    p.k_weight = k_weight;
+    p.inv_freq = inv_freq;
+    p.positions = positions;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_out_stride = k_out_stride;
+    p.n_tokens = n_tokens;
+    p.q_heads = q_heads;
+    p.k_heads = k_heads;
+    p.head_dim = head_dim;
+    p.rot_dim = rot_dim;
+    p.interleaved = interleaved;
+    p.eps = eps;
+    return ndq::launch_rope(p, in_dtype == NDQ_FLOAT ? 0 : in_dtype == NDQ_BFLOAT16 ? 1 : 2, out_dtype == NDQ_BFLOAT16, stream) == 0
                ? NDQ_OK
                : NDQ_ERR_CUDA;
 }

@@ -1,0 +1,115 @@
+"""Refusals of the packed embedding lookup and of the norm and rotation of
+heads: what the host checks before any launch, so these run without a GPU."""
+import pytest
+import torch
+
+import quantized_weight_block_gb300 as ndq
+from test_serving_binding import On, on_gpu
+
+OK, NULL, UNKNOWN, NEGATIVE, BLOCKS, LENGTH, BAD_DTYPE, BAD_ARG, MISALIGNED = 0, 1, 2, 5, 6, 7, 9, 15, 16
+F32, F16, BF16, DOUBLE = ndq.NDQ_FLOAT, ndq.NDQ_FLOAT16, ndq.NDQ_BFLOAT16, ndq.NDQ_DOUBLE
+P = 4096  # a pointer that is never followed
+Q8, FP8 = ndq.format_id("gguf:q8_0"), ndq.format_id("fp8_e4m3fn_row_bf16")
+
+
+def embed(**kw):
+    a = dict(format_id=Q8, V=10, K=64, w=P, w_len=10 * 2 * 34, ids=P, ids_dtype=ndq.NDQ_INT32, n_tokens=3, scale=1.0,
+             out_dtype=BF16, y=P, y_stride=64) | kw
+    return ndq.ndq_embed_packed(**a)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(format_id=99), UNKNOWN), (dict(format_id=-1), UNKNOWN), (dict(V=-1), NEGATIVE), (dict(K=-32), NEGATIVE),
+    (dict(n_tokens=-1), NEGATIVE), (dict(K=48), BLOCKS), (dict(w_len=679), LENGTH), (dict(V=11), LENGTH),
+    (dict(format_id=FP8, K=24, w_len=10 * 26), BLOCKS), (dict(out_dtype=DOUBLE), BAD_DTYPE), (dict(out_dtype=0), BAD_DTYPE),
+    (dict(ids_dtype=F32), BAD_DTYPE), (dict(w=0), NULL), (dict(ids=0), NULL), (dict(y=0), NULL), (dict(y_stride=63), BAD_ARG),
+    (dict(y_stride=-64), BAD_ARG), (dict(y_stride=1 << 41), BAD_ARG), (dict(scale=float("nan")), BAD_ARG),
+    (dict(scale=float("inf")), BAD_ARG), (dict(n_tokens=1 << 31), BAD_ARG), (dict(y=P + 1), MISALIGNED),
+    (dict(out_dtype=F32, y=P + 2), MISALIGNED), (dict(ids=P + 2), MISALIGNED), (dict(ids_dtype=ndq.NDQ_INT64, ids=P + 4), MISALIGNED),
+    (dict(n_tokens=0), OK), (dict(K=0, w_len=0, y_stride=0), OK), (dict(n_tokens=0, ids=0, y=0), OK)])
+def test_embed_refusals(kw, want):
+    assert embed(**kw) == want
+
+
+def rope(**kw):
+    a = dict(q=P, q_heads=8, q_stride=1024, k=P, k_heads=2, k_stride=256, in_dtype=BF16, n_tokens=3, head_dim=128, rot_dim=128,
+             interleaved=0, positions=P, inv_freq=P, q_weight=P, k_weight=P, eps=1e-6, q_out=2 * P, q_out_stride=1024,
+             k_out=2 * P, k_out_stride=256, out_dtype=BF16) | kw
+    return ndq.ndq_qk_norm_rope(**a)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(n_tokens=-1), NEGATIVE), (dict(q_heads=-1), NEGATIVE), (dict(k_heads=-1), NEGATIVE), (dict(in_dtype=DOUBLE), BAD_DTYPE),
+    (dict(out_dtype=F32), BAD_DTYPE), (dict(head_dim=0), BAD_ARG), (dict(head_dim=120), BAD_ARG), (dict(head_dim=272), BAD_ARG),
+    (dict(rot_dim=-16), BAD_ARG), (dict(rot_dim=144), BAD_ARG), (dict(rot_dim=24), BAD_ARG), (dict(interleaved=2), BAD_ARG),
+    (dict(eps=-1e-6), BAD_ARG), (dict(eps=float("nan")), BAD_ARG), (dict(n_tokens=1 << 31), BAD_ARG), (dict(q_heads=4097), BAD_ARG),
+    (dict(q=0), NULL), (dict(k=0), NULL), (dict(q_out=0), NULL), (dict(k_out=0), NULL), (dict(positions=0), NULL),
+    (dict(inv_freq=0), NULL), (dict(q_stride=1016), BAD_ARG), (dict(k_out_stride=255), BAD_ARG), (dict(q_stride=1028), MISALIGNED),
+    (dict(k=P + 8), MISALIGNED), (dict(q_out=P + 2), MISALIGNED), (dict(positions=P + 2), MISALIGNED),
+    (dict(k_weight=P + 1), MISALIGNED), (dict(in_dtype=F32, q_out=P), BAD_ARG), (dict(k_out=P, k_out_stride=512), BAD_ARG),
+    (dict(n_tokens=0), OK), (dict(q_heads=0, k_heads=0, q=0, k=0), OK)])
+def test_rope_refusals(kw, want):
+    assert rope(**kw) == want
+
+
+# ---- the tensor calls -----------------------------------------------------------
+
+BF, I32 = torch.bfloat16, torch.int32
+
+
+def embed_args():
+    return dict(fmt="gguf:q8_0", w=torch.zeros(680, dtype=torch.uint8), V=10, K=64, ids=torch.zeros(3, dtype=I32), out=torch.zeros(3, 64))
+
+
+def rope_args():
+    return dict(q=torch.zeros(3, 4, 64, dtype=BF), k=torch.zeros(3, 2, 64, dtype=BF), positions=torch.zeros(3, dtype=I32),
+                inv_freq=torch.zeros(32), q_weight=torch.ones(64), k_weight=torch.ones(64), q_out=torch.zeros(3, 4, 64, dtype=BF),
+                k_out=torch.zeros(3, 2, 64, dtype=BF))
+
+
+CALLS = {"embed_packed": embed_args, "qk_norm_rope": rope_args}
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """The library's calls, which must not come."""
+    seen = []
+    for name in CALLS:
+        monkeypatch.setattr(ndq._lib, "ndq_" + name, lambda *a, name=name: (seen.append(name), 0)[1])
+    monkeypatch.setattr(ndq, "_raw_stream", lambda stream, device: 0)
+    return seen
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_tensors_on_the_device_are_taken(name, launches):
+    getattr(ndq, name)(**on_gpu(CALLS[name]()))
+    assert launches == [name]
+
+
+@pytest.mark.parametrize("elsewhere", [-1, 1])
+@pytest.mark.parametrize("name,arg", [(n, a) for n, f in CALLS.items() for a, v in f().items() if isinstance(v, torch.Tensor)])
+def test_a_tensor_elsewhere_is_refused(name, arg, elsewhere, launches):
+    args = on_gpu(CALLS[name]())
+    args[arg] = On.at(args[arg], elsewhere)
+    with pytest.raises(ValueError):
+        getattr(ndq, name)(**args)
+    assert launches == []
+
+
+@pytest.mark.parametrize("name,change", [
+    ("embed_packed", dict(ids=torch.zeros(3, 1, dtype=I32))), ("embed_packed", dict(ids=torch.zeros(3))),
+    ("embed_packed", dict(ids=torch.zeros(6, dtype=I32)[::2])), ("embed_packed", dict(out=torch.zeros(2, 64))),
+    ("embed_packed", dict(out=torch.zeros(64, 3).t())), ("embed_packed", dict(out=torch.zeros(3, 64, dtype=torch.float64))),
+    ("embed_packed", dict(w=torch.zeros(680, dtype=torch.int8))), ("embed_packed", dict(out_dtype=BF)),
+    ("qk_norm_rope", dict(q=torch.zeros(3, 4, 64))), ("qk_norm_rope", dict(k=torch.zeros(4, 2, 64, dtype=BF))),
+    ("qk_norm_rope", dict(k=torch.zeros(3, 2, 128, dtype=BF))), ("qk_norm_rope", dict(q=torch.zeros(3, 64, 4, dtype=BF).transpose(1, 2))),
+    ("qk_norm_rope", dict(positions=torch.zeros(3, dtype=torch.int64))), ("qk_norm_rope", dict(positions=torch.zeros(2, dtype=I32))),
+    ("qk_norm_rope", dict(inv_freq=torch.zeros(32, dtype=torch.float64))), ("qk_norm_rope", dict(q_weight=torch.ones(64, dtype=BF))),
+    ("qk_norm_rope", dict(k_weight=torch.ones(32))), ("qk_norm_rope", dict(q_out=torch.zeros(3, 4, 64))),
+    ("qk_norm_rope", dict(k_out=torch.zeros(3, 2, 32, dtype=BF))), ("qk_norm_rope", dict(k=None)),
+    ("qk_norm_rope", dict(q=None, k=None))])
+def test_other_tensors_are_refused(name, change, launches):
+    args = on_gpu(CALLS[name]() | change)
+    with pytest.raises(ValueError):
+        getattr(ndq, name)(**args)
+    assert launches == []
