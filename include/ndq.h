@@ -347,10 +347,11 @@ int ndq_dequantize_packed_batched_noalloc(const ndq_tensor_desc *descs, int n, v
 /* beside its products.  (No counterpart on the pages.)  A step calls         */
 /* ndq_kv_plan and ndq_embed_packed, then for every layer                     */
 /* ndq_matmul_packed[_batched] (+ ndq_lora_add), ndq_qk_norm_rope,            */
-/* ndq_kv_append and ndq_attention_kv8.  Like the calls above they allocate   */
-/* nothing, validate on the host before any launch and run asynchronously on  */
-/* `stream`; lengths, tables and slots stay on the device and are never read  */
-/* by the host.                                                               */
+/* ndq_kv_append and ndq_attention_kv8, or ndq_attention_prefix_kv8 where     */
+/* requests share a long prefix.  Like the calls above they allocate nothing, */
+/* validate on the host before any launch and run asynchronously on `stream`; */
+/* lengths, tables and slots stay on the device and are never read by the     */
+/* host.                                                                      */
 /* ------------------------------------------------------------------------ */
 
 /* A key/value cache in 8-bit codes with one binary32 scale for each block of
@@ -475,6 +476,36 @@ int ndq_attention_kv8(const ndq_kv_cache *cache, const void *q, int dtype, int64
                       int64_t q_stride, const int32_t *block_table, int64_t table_width, const int32_t *kv_len,
                       const int32_t *q_start, int64_t n_req, int64_t max_q, float scale, int64_t window, void *out,
                       float *lse, void *workspace, size_t ws_bytes, void *stream);
+
+/* Attention over the cache for requests that share long prefixes (a system
+ * prompt, a document, the prompt of several sampled answers): the result of
+ * ndq_attention_kv8, with the shared tokens read once for all requests of a
+ * group instead of once for each.
+ *   group_start   device int32 [n_groups + 1], ascending: group g has the
+ *                 requests group_start[g] .. group_start[g + 1] - 1; requests
+ *                 outside every group share nothing
+ *   prefix_len    device int32 [n_groups]: the requests of group g hold the
+ *                 same first prefix_len[g] tokens, in the same blocks: the
+ *                 whole blocks among them are shared (the others, and what
+ *                 lies beyond the table, are taken as each request's own)
+ * The block ids of the shared blocks are read from the row of the group's first
+ * request, which must hold them; the other rows must agree, and need not when
+ * no query of theirs sees that block.  Queries may sit inside the prefix and
+ * windows end in it.  The other arguments, and what the outputs hold, are
+ * ndq_attention_kv8's; the two parts are joined in binary32.  A group of one,
+ * prefixes of 0 and n_groups of 0 are valid.
+ *   workspace  device buffer of ndq_attention_prefix_workspace_bytes(head_dim,
+ *              n_tokens, q_heads, kv_heads) bytes or more, 256-byte aligned,
+ *              its first 4096 bytes zeroed once before its first use (each call
+ *              leaves them zero), not shared by calls that may overlap; one
+ *              sized for some n_tokens and heads serves any call that needs no
+ *              more bytes.  (0 bytes: the sizes are refused.) */
+size_t ndq_attention_prefix_workspace_bytes(int head_dim, int64_t n_tokens, int q_heads, int kv_heads);
+int ndq_attention_prefix_kv8(const ndq_kv_cache *cache, const void *q, int dtype, int64_t n_tokens, int q_heads,
+                             int64_t q_stride, const int32_t *block_table, int64_t table_width, const int32_t *kv_len,
+                             const int32_t *q_start, int64_t n_req, int64_t max_q, const int32_t *group_start,
+                             const int32_t *prefix_len, int64_t n_groups, float scale, int64_t window, void *out,
+                             float *lse, void *workspace, size_t ws_bytes, void *stream);
 
 /* Norms of query and key heads and their rotation by position, in one pass:
  *     z = x / sqrt(mean(x^2) + eps) * weight     (z = x without a weight)

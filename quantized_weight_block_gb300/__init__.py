@@ -104,6 +104,10 @@ _lib.ndq_attention_workspace_bytes.argtypes = [_c.c_int]
 _lib.ndq_attention_workspace_bytes.restype = _c.c_size_t
 _lib.ndq_attention_kv8.argtypes = [_c.POINTER(ndq_kv_cache), _p, _c.c_int, _i64, _c.c_int, _i64, _p, _i64, _p, _p, _i64,
                                    _i64, _c.c_float, _i64, _p, _p, _p, _c.c_size_t, _p]
+_lib.ndq_attention_prefix_workspace_bytes.argtypes = [_c.c_int, _i64, _c.c_int, _c.c_int]
+_lib.ndq_attention_prefix_workspace_bytes.restype = _c.c_size_t
+_lib.ndq_attention_prefix_kv8.argtypes = [_c.POINTER(ndq_kv_cache), _p, _c.c_int, _i64, _c.c_int, _i64, _p, _i64, _p, _p, _i64,
+                                          _i64, _p, _p, _i64, _c.c_float, _i64, _p, _p, _p, _c.c_size_t, _p]
 _lib.ndq_embed_packed.argtypes = [_c.c_int, _i64, _i64, _p, _c.c_size_t, _p, _c.c_int, _i64, _c.c_float, _c.c_int, _p, _i64,
                                   _p]
 _lib.ndq_qk_norm_rope.argtypes = [_p, _c.c_int, _i64, _p, _c.c_int, _i64, _c.c_int, _i64, _c.c_int, _c.c_int, _c.c_int, _p, _p,
@@ -121,7 +125,7 @@ EXPORTS = (
     "ndq_matmul_packed", "ndq_test_withhold_copy", "ndq_matmul_packed_batched",
     "ndq_kv_plan", "ndq_kv_append", "ndq_attention_workspace_bytes", "ndq_attention_kv8",
     "ndq_lora_workspace_bytes", "ndq_lora_add", "ndq_test_lose_copies",
-    "ndq_embed_packed", "ndq_qk_norm_rope",
+    "ndq_embed_packed", "ndq_qk_norm_rope", "ndq_attention_prefix_workspace_bytes", "ndq_attention_prefix_kv8",
 )
 
 
@@ -376,6 +380,20 @@ def ndq_attention_kv8(cache, q: int, dtype: int, n_tokens: int, q_heads: int, q_
                                   q_start, n_req, max_q, scale, window, out, lse, workspace, ws_bytes, stream)
 
 
+def ndq_attention_prefix_workspace_bytes(head_dim: int, n_tokens: int, q_heads: int, kv_heads: int) -> int:
+    return _lib.ndq_attention_prefix_workspace_bytes(head_dim, n_tokens, q_heads, kv_heads)
+
+
+def ndq_attention_prefix_kv8(cache, q: int, dtype: int, n_tokens: int, q_heads: int, q_stride: int, block_table: int,
+                             table_width: int, kv_len: int, q_start: int, n_req: int, max_q: int, group_start: int,
+                             prefix_len: int, n_groups: int, scale: float, window: int, out: int, lse: int, workspace: int,
+                             ws_bytes: int, stream: int = 0) -> int:
+    """Raw call; `cache` is an ndq_kv_cache; returns the status code."""
+    return _lib.ndq_attention_prefix_kv8(cache, q, dtype, n_tokens, q_heads, q_stride, block_table, table_width, kv_len, q_start,
+                                         n_req, max_q, group_start, prefix_len, n_groups, scale, window, out, lse, workspace,
+                                         ws_bytes, stream)
+
+
 def ndq_embed_packed(format_id: int, V: int, K: int, w: int, w_len: int, ids: int, ids_dtype: int, n_tokens: int, scale: float,
                      out_dtype: int, y: int, y_stride: int, stream: int = 0) -> int:
     """Raw call (device pointers as integers); returns the status code."""
@@ -622,13 +640,8 @@ def attention_workspace(n_req: int, n_tokens: int, q_heads: int, cache: KvCache,
     return ws
 
 
-def attention_kv8(q, cache: KvCache, block_table, kv_len, q_start=None, max_q=None, scale=None, window: int = 0,
-                  out=None, lse=None, workspace=None, stream=None):
-    """Causal attention of q [T, q_heads, head_dim] (bfloat16 or float16) over
-    `cache` (see ndq_attention_kv8): block_table [R, width], kv_len [R] and
-    q_start [R + 1] are CUDA int32 tensors, q_start None when every request has
-    one query.  max_q bounds the queries of one request (default: T, or 1).
-    Returns out [T, q_heads, head_dim]; lse [T, q_heads] is written if given."""
+def _attention_args(q, cache, block_table, kv_len, q_start, out, lse, stream, what):
+    """The checks that the attention calls share; (T, H, D, R, width, row stride, type code, out)."""
     c = _T or _consts()
     i32, code = c.i32, c.code.get(q.dtype)
     if q.dim() != 3 or code is None:
@@ -640,7 +653,7 @@ def attention_kv8(q, cache: KvCache, block_table, kv_len, q_start=None, max_q=No
             or not kv_len.is_contiguous()):
         raise ValueError("block_table must be int32 [R, width] and kv_len int32 [R]")
     gpu = cache.gpu
-    _same_device("attention_kv8", gpu, q, block_table, kv_len)
+    _same_device(what, gpu, q, block_table, kv_len)
     if q_start is not None and (q_start.dtype is not i32 or q_start.shape != (R + 1,) or not q_start.is_contiguous()
                                 or q_start.get_device() != gpu):
         raise ValueError("q_start must be int32 [R + 1], on q's device")
@@ -651,6 +664,18 @@ def attention_kv8(q, cache: KvCache, block_table, kv_len, q_start=None, max_q=No
         raise ValueError("out must be contiguous, of q's shape and type and on its device")
     if lse is not None and (lse.dtype is not c.f32 or lse.shape != (T, H) or not lse.is_contiguous() or lse.get_device() != gpu):
         raise ValueError("lse must be float32 [tokens, q_heads], on q's device")
+    return T, H, D, R, width, qs, code, out
+
+
+def attention_kv8(q, cache: KvCache, block_table, kv_len, q_start=None, max_q=None, scale=None, window: int = 0,
+                  out=None, lse=None, workspace=None, stream=None):
+    """Causal attention of q [T, q_heads, head_dim] (bfloat16 or float16) over
+    `cache` (see ndq_attention_kv8): block_table [R, width], kv_len [R] and
+    q_start [R + 1] are CUDA int32 tensors, q_start None when every request has
+    one query.  max_q bounds the queries of one request (default: T, or 1).
+    Returns out [T, q_heads, head_dim]; lse [T, q_heads] is written if given."""
+    T, H, D, R, width, qs, code, out = _attention_args(q, cache, block_table, kv_len, q_start, out, lse, stream, "attention_kv8")
+    gpu = cache.gpu
     if workspace is not None:
         _check_workspace(workspace, gpu)
     else:
@@ -662,6 +687,47 @@ def attention_kv8(q, cache: KvCache, block_table, kv_len, q_start=None, max_q=No
         workspace.data_ptr(), workspace.numel(), _raw_stream(stream, gpu))
     if rc:
         raise NdqError(rc, "attention_kv8")
+    return out
+
+
+def attention_prefix_workspace(cache: KvCache, n_tokens: int, q_heads: int):
+    """A workspace for attention_prefix_kv8 calls on `cache` of up to n_tokens
+    queries and q_heads: its counters are zeroed here, on the current stream,
+    and left so by every call; calls that share it must not overlap."""
+    torch = _torch()
+    nbytes = ndq_attention_prefix_workspace_bytes(cache.head_dim, n_tokens, q_heads, cache.kv_heads)
+    if nbytes == 0:
+        raise ValueError("no such call: q_heads must be a multiple of the cache's heads, and n_tokens * q_heads below 2^31")
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+    ws[:4096].zero_()
+    return ws
+
+
+def attention_prefix_kv8(q, cache: KvCache, block_table, kv_len, group_start, prefix_len, q_start=None, max_q=None, scale=None,
+                         window: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """attention_kv8 of requests that share prefixes, which are read once for
+    all of them (see ndq_attention_prefix_kv8): requests group_start[g] ..
+    group_start[g + 1] - 1 hold the same first prefix_len[g] tokens in the same
+    blocks; group_start [G + 1] and prefix_len [G] are CUDA int32 tensors, the
+    workspace one of attention_prefix_workspace, everything else as there."""
+    T, H, D, R, width, qs, code, out = _attention_args(q, cache, block_table, kv_len, q_start, out, lse, stream,
+                                                       "attention_prefix_kv8")
+    gpu, i32, G = cache.gpu, _T.i32, prefix_len.shape[0] if prefix_len.dim() else -1
+    if (group_start.dtype is not i32 or prefix_len.dtype is not i32 or prefix_len.shape != (G,) or group_start.shape != (G + 1,)
+            or not group_start.is_contiguous() or not prefix_len.is_contiguous()):
+        raise ValueError("group_start must be int32 [G + 1] and prefix_len int32 [G]")
+    _same_device("attention_prefix_kv8", gpu, group_start, prefix_len)
+    if workspace is not None:
+        _check_workspace(workspace, gpu)
+    else:
+        workspace = _made_for(stream, lambda: attention_prefix_workspace(cache, T, H))
+    rc = _lib.ndq_attention_prefix_kv8(
+        cache.desc, q.data_ptr(), code, T, H, qs, block_table.data_ptr(), width, kv_len.data_ptr(),
+        None if q_start is None else q_start.data_ptr(), R, max_q if max_q is not None else (1 if q_start is None else T),
+        group_start.data_ptr(), prefix_len.data_ptr(), G, D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, gpu))
+    if rc:
+        raise NdqError(rc, "attention_prefix_kv8")
     return out
 
 

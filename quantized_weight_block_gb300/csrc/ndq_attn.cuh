@@ -150,5 +150,98 @@ __device__ __forceinline__ void attn_request(const AttnParams& p, int64_t r, int
     first = static_cast<int32_t>(len - all > -(1 << 30) ? len - all : -(1 << 30));  // (before 0 in either case)
 }
 
+// ---- requests that share prefixes ---------------------------------------------
+
+// What an attention kernel computes: all that its rows see; the shared prefix
+// of groups of requests; or the rest, joined with that.
+enum AttnMode : int { kAttnAll = 0, kAttnShared = 1, kAttnOwn = 2 };
+template <int MODE>
+struct AttnArgs {
+    using type = PrefixParams;
+};
+template <>
+struct AttnArgs<kAttnAll> {
+    using type = AttnParams;
+};
+
+// Group g's requests and the tokens that they share: whole blocks, and no
+// more than the table has room for.
+struct Group {
+    int64_t begin, end;
+    int32_t tokens;
+};
+__device__ __forceinline__ Group attn_group(const PrefixParams& p, int64_t g) {
+    Group x;
+    x.begin = p.group_start[g];
+    x.begin = x.begin < 0 ? 0 : (x.begin > p.n_req ? p.n_req : x.begin);
+    x.end = p.group_start[g + 1];
+    x.end = x.end < x.begin ? x.begin : (x.end > p.n_req ? p.n_req : x.end);
+    const int32_t most = table_tokens(p), n = p.prefix_len[g] < most ? p.prefix_len[g] : most;
+    x.tokens = n > 0 ? n & ~((1 << p.c.bs_log2) - 1) : 0;
+    return x;
+}
+
+// The tokens that request r shares with its group.
+__device__ __forceinline__ int32_t shared_tokens(const PrefixParams& p, int64_t r) {
+    int64_t a = 0, b = p.n_groups;  // the last group that starts at r or before
+    while (b - a > 1) {
+        const int64_t m = (a + b) >> 1;
+        if (p.group_start[m] <= r) a = m;
+        else b = m;
+    }
+    const Group x = attn_group(p, a);
+    return x.begin <= r && r < x.end ? x.tokens : 0;
+}
+
+// The parts that the prefix's kernel left of one row.
+template <int D>
+struct RowParts {
+    const float* first;
+    uint32_t pad, n, row;
+
+    __device__ __forceinline__ RowParts(const PrefixParams& p, int64_t at) {
+        const uint4 x = __ldcg(static_cast<const uint4*>(p.records) + at);
+        pad = x.y;
+        n = x.z;
+        row = x.w;
+        // (whatever a record holds, no read leaves the slots)
+        if (pad > kPromptRows || row >= pad || n > kPrefixMaxParts || x.x + static_cast<uint64_t>(n) * pad > static_cast<uint64_t>(p.slot_rows)) n = 0;
+        first = p.slots + static_cast<uint64_t>(x.x) * (D + 2);
+    }
+    __device__ __forceinline__ const float* slot(uint32_t k) const { return first + static_cast<uint64_t>(k) * pad * (D + 2); }
+    __device__ __forceinline__ float top(uint32_t k) const { return __ldcg(slot(k) + row); }
+    __device__ __forceinline__ float sum(uint32_t k) const { return __ldcg(slot(k) + pad + row); }
+    // head positions 4 c .. 4 c + 3
+    __device__ __forceinline__ float4 values(uint32_t k, uint32_t c) const {
+        return __ldcg(reinterpret_cast<const float4*>(slot(k) + 2 * pad) + static_cast<uint64_t>(c) * pad + row);
+    }
+    // N (2, or a multiple of 4) of them from d on
+    template <int N>
+    __device__ __forceinline__ void load(uint32_t k, uint32_t d, float* v) const {
+        if constexpr (N == 2) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(slot(k) + 2 * pad + (static_cast<uint64_t>(d >> 2) * pad + row) * 4 + (d & 2u)));
+            v[0] = x.x;
+            v[1] = x.y;
+        } else {
+#pragma unroll
+            for (int c = 0; c < N / 4; ++c) {
+                const float4 x = values(k, d / 4 + c);
+                v[4 * c] = x.x;
+                v[4 * c + 1] = x.y;
+                v[4 * c + 2] = x.z;
+                v[4 * c + 3] = x.w;
+            }
+        }
+    }
+    __device__ __forceinline__ float largest(float M) const {
+        for (uint32_t k = 0; k < n; ++k) M = fmaxf(M, top(k));
+        return M;
+    }
+};
+
+// What a part counts for beside the maximum M, as a root (see kScaleSpread).
+// A part that saw nothing has 0 for everything, or a NaN that must stay.
+__device__ __forceinline__ float part_root(float m, float M) { return m == -INFINITY ? 1.0f : exp2_fast(0.5f * (m - M)); }
+
 }  // namespace
 }  // namespace ndq

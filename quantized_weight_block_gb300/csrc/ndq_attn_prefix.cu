@@ -1,0 +1,49 @@
+// ndq_attn_prefix.cu -- attention of requests that share prefixes: the kernel of
+// the shared prefixes, and the launcher of all three.
+#include "ndq_attn_prompt.cuh"
+
+namespace ndq {
+
+int launch_prefix_shared(const PrefixParams& p, int head_dim, bool e4m3, bool bf16, int dev, void* stream) {
+    // units at most: a group's last one may be partial, and every group in use has a token
+    const int64_t groups = p.n_groups < p.n_tokens ? p.n_groups : p.n_tokens;
+    const int64_t grid = (p.n_tokens * p.group / kPromptRows + groups) * p.c.heads + kPrefixMaxExtra;
+    if (grid > INT32_MAX) return static_cast<int>(cudaErrorInvalidValue);
+    return launch_prompt_of<kAttnShared>(p, head_dim, e4m3, bf16, static_cast<unsigned>(grid), dev, stream);
+}
+
+int launch_attention_prefix(PrefixParams p, int head_dim, bool e4m3, bool bf16, void* stream) {
+    static int sms_of[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    if (dev < 0 || dev >= 64) return static_cast<int>(cudaErrorInvalidDevice);
+    if (sms_of[dev] == 0) {
+        int sms = 0;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return static_cast<int>(e);
+        sms_of[dev] = sms;
+    }
+    p.sms = sms_of[dev] < kPrefixMaxExtra ? sms_of[dev] : kPrefixMaxExtra;
+    if (p.max_q > p.n_tokens) p.max_q = p.n_tokens;
+    const IqGrids* grids = nullptr;
+    if (const int rc = device_symbols(dev, &p.fault, &grids)) return rc;
+    p.splits = 1;
+    if (const int rc = launch_prefix_shared(p, head_dim, e4m3, bf16, dev, stream)) return rc;
+    // the requests' own tokens, by their rows as in launch_attention
+    uint32_t* counters = p.counters;
+    float* parts = p.parts;
+    if (p.max_q * p.group > 2 * kAttnRows) {
+        p.prompt_rows = 2 * kAttnRows + 1;
+        p.counters = counters + kAttnMaxCtas;
+        p.parts = parts + 2 * static_cast<size_t>(kAttnMaxCtas) * NDQ_ROWS_SLOT(head_dim);
+        bool launched = false;
+        if (const int rc = launch_prefix_own_prompt(p, head_dim, e4m3, bf16, dev, stream, &launched)) return rc;
+        if (!launched) p.prompt_rows = 0;
+        p.counters = counters;
+        p.parts = parts;
+    }
+    return launch_prefix_own_rows(p, head_dim, e4m3, bf16, dev, stream);
+}
+
+}  // namespace ndq

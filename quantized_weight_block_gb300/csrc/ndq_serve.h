@@ -105,6 +105,43 @@ int launch_attention_prompt(AttnParams p, int head_dim, bool e4m3, bool bf16, in
                             bool* launched);
 int launch_attention(AttnParams p, int head_dim, bool e4m3, bool bf16, void* stream);
 
+// Attention of requests that share prefixes, in two parts: the prefix of each
+// group of requests, read once for the rows of all of them (k_attn_prompt),
+// and every request's own tokens, whose kernels join the two.
+//
+// The prefix part is laid out in slots: a unit (256 rows of a group and cache
+// head at most) leaves one slot for each CTA that shares its tokens, a slot
+// holding `pad` rows (its rows, rounded up to four): pad maxima, pad sums,
+// then head positions by fours, [D / 4][pad][4].  A row finds its slots by its
+// record, (first slot's offset in rows, pad, slots, row in the slot).
+constexpr int kPrefixMaxParts = 64;   // CTAs of a unit at most
+constexpr int kPrefixMaxExtra = 192;  // CTAs beyond one per unit at most (no more than SMs)
+constexpr int64_t prefix_slot_rows(int64_t n_tokens, int64_t q_heads, int64_t kv_heads) {
+    return n_tokens * (q_heads + 3 * kv_heads) + static_cast<int64_t>(kPrefixMaxExtra) * kPromptRows;
+}
+constexpr size_t prefix_records_at(int head_dim) { return (attn_workspace_bytes(head_dim) + 255) / 256 * 256; }
+constexpr size_t prefix_slots_at(int head_dim, int64_t n_tokens, int64_t q_heads) {
+    return (prefix_records_at(head_dim) + 16 * static_cast<size_t>(n_tokens * q_heads) + 255) / 256 * 256;
+}
+constexpr size_t prefix_workspace_bytes(int head_dim, int64_t n_tokens, int64_t q_heads, int64_t kv_heads) {
+    return prefix_slots_at(head_dim, n_tokens, q_heads) +
+           4 * static_cast<size_t>(head_dim + 2) * static_cast<size_t>(prefix_slot_rows(n_tokens, q_heads, kv_heads));
+}
+struct PrefixParams : AttnParams {
+    const int32_t* group_start;
+    const int32_t* prefix_len;
+    int64_t n_groups;
+    void* records;      // uint4 [n_tokens, q_heads]
+    float* slots;
+    int64_t slot_rows;  // rows that the slots have room for
+    int32_t sms;        // (set by the launcher)
+};
+int launch_attention_prefix(PrefixParams p, int head_dim, bool e4m3, bool bf16, void* stream);
+// The three kernels' launches (each in its own translation unit).
+int launch_prefix_shared(const PrefixParams& p, int head_dim, bool e4m3, bool bf16, int dev, void* stream);
+int launch_prefix_own_prompt(PrefixParams p, int head_dim, bool e4m3, bool bf16, int dev, void* stream, bool* launched);
+int launch_prefix_own_rows(const PrefixParams& p, int head_dim, bool e4m3, bool bf16, int dev, void* stream);
+
 struct LoraParams {
     const uint16_t* x;
     const uint16_t* a;

@@ -67,6 +67,54 @@ int check_rows(const void* p, int64_t stride, int64_t row) {
     return NDQ_OK;
 }
 
+// What the attention calls have in common: their checks and the launch
+// descriptor, but for the workspace.  empty: there is nothing to compute.
+int check_attention(const ndq_kv_cache* cache, const void* q, int dtype, int64_t n_tokens, int q_heads, int64_t q_stride,
+                    const int32_t* block_table, int64_t table_width, const int32_t* kv_len, const int32_t* q_start,
+                    int64_t n_req, int64_t max_q, float scale, int64_t window, void* out, float* lse, ndq::AttnParams* d,
+                    bool* empty) {
+    ndq::AttnParams& p = *d;
+    int rc = check_cache(cache, &p.c);
+    if (rc != NDQ_OK) return rc;
+    if (n_tokens < 0 || n_req < 0 || max_q < 0 || table_width < 0 || window < 0) return NDQ_ERR_NEGATIVE_DIM;
+    if (dtype != NDQ_BFLOAT16 && dtype != NDQ_FLOAT16) return NDQ_ERR_BAD_DTYPE;
+    if (n_tokens > INT32_MAX / 2 || n_req > INT32_MAX / 2 ||
+        table_width > (INT64_C(1) << 30) / cache->block_size)
+        return NDQ_ERR_BAD_ARG;
+    if (q_heads < 1 || q_heads > 4096 || q_heads % cache->kv_heads != 0 ||
+        n_tokens > INT32_MAX / q_heads)
+        return NDQ_ERR_BAD_ARG;
+    if (!std::isfinite(scale)) return NDQ_ERR_BAD_ARG;
+    *empty = n_tokens == 0 || n_req == 0 || max_q == 0;
+    if (*empty) return NDQ_OK;
+    if (!q_start && n_tokens != n_req) return NDQ_ERR_BAD_ARG;
+    if (!q || !out || !kv_len || (table_width > 0 && !block_table)) return NDQ_ERR_NULL;
+    const int64_t row = static_cast<int64_t>(q_heads) * cache->head_dim;
+    if ((rc = check_rows(q, q_stride, row)) != NDQ_OK) return rc;
+    if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(kv_len, 4) ||
+        !aligned(q_start, 4))
+        return NDQ_ERR_MISALIGNED;
+    p.q = static_cast<const uint16_t*>(q);
+    p.out = out;
+    p.lse = lse;
+    p.table = block_table;
+    p.kv_len = kv_len;
+    p.q_start = q_start;
+    p.n_tokens = n_tokens;
+    p.n_req = n_req;
+    p.q_stride = q_stride;
+    p.width = table_width;
+    p.window = window > (INT64_C(1) << 30) ? 0 : static_cast<int32_t>(window);  // (no table is that long)
+    p.max_q = q_start ? max_q : 1;
+    p.q_heads = q_heads;
+    p.group = q_heads / cache->kv_heads;
+    p.group_shift = -1;
+    for (int i = 0; i < 13; ++i)
+        if (p.group == 1 << i) p.group_shift = i;
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    return NDQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -152,52 +200,59 @@ int ndq_attention_kv8(const ndq_kv_cache* cache, const void* q, int dtype, int64
                       const int32_t* q_start, int64_t n_req, int64_t max_q, float scale, int64_t window, void* out,
                       float* lse, void* workspace, size_t ws_bytes, void* stream) {
     ndq::AttnParams p{};
-    int rc = check_cache(cache, &p.c);
-    if (rc != NDQ_OK) return rc;
-    if (n_tokens < 0 || n_req < 0 || max_q < 0 || table_width < 0 || window < 0) return NDQ_ERR_NEGATIVE_DIM;
-    if (dtype != NDQ_BFLOAT16 && dtype != NDQ_FLOAT16) return NDQ_ERR_BAD_DTYPE;
-    if (n_tokens > INT32_MAX / 2 || n_req > INT32_MAX / 2 ||
-        table_width > (INT64_C(1) << 30) / cache->block_size)
-        return NDQ_ERR_BAD_ARG;
-    if (q_heads < 1 || q_heads > 4096 || q_heads % cache->kv_heads != 0 ||
-        n_tokens > INT32_MAX / q_heads)
-        return NDQ_ERR_BAD_ARG;
-    if (!std::isfinite(scale)) return NDQ_ERR_BAD_ARG;
-    if (n_tokens == 0 || n_req == 0 || max_q == 0) return NDQ_OK;
-    if (!q_start && n_tokens != n_req) return NDQ_ERR_BAD_ARG;
-    if (!q || !out || !kv_len || (table_width > 0 && !block_table)) return NDQ_ERR_NULL;
-    const int64_t row = static_cast<int64_t>(q_heads) * cache->head_dim;
-    if ((rc = check_rows(q, q_stride, row)) != NDQ_OK) return rc;
-    if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(kv_len, 4) ||
-        !aligned(q_start, 4))
-        return NDQ_ERR_MISALIGNED;
+    bool empty = false;
+    const int rc = check_attention(cache, q, dtype, n_tokens, q_heads, q_stride, block_table, table_width, kv_len, q_start, n_req,
+                                   max_q, scale, window, out, lse, &p, &empty);
+    if (rc != NDQ_OK || empty) return rc;
     if (!workspace || !aligned(workspace, 16) || ws_bytes < ndq::attn_workspace_bytes(cache->head_dim))
         return NDQ_ERR_WORKSPACE;
-    p.q = static_cast<const uint16_t*>(q);
-    p.out = out;
-    p.lse = lse;
-    p.table = block_table;
-    p.kv_len = kv_len;
-    p.q_start = q_start;
     p.counters = static_cast<uint32_t*>(workspace);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ndq::kAttnCounterBytes);
-    p.n_tokens = n_tokens;
-    p.n_req = n_req;
-    p.q_stride = q_stride;
-    p.width = table_width;
-    p.window = window > (INT64_C(1) << 30) ? 0 : static_cast<int32_t>(window);  // (no table is that long)
-    p.max_q = q_start ? max_q : 1;
-    p.q_heads = q_heads;
-    p.group = q_heads / cache->kv_heads;
-    p.group_shift = -1;
-    for (int i = 0; i < 13; ++i)
-        if (p.group == 1 << i) p.group_shift = i;
-    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.waits = take_waits();
     return ndq::launch_attention(p, cache->head_dim, cache->code_type == NDQ_FLOAT8E4M3FN, dtype == NDQ_BFLOAT16,
                                  stream) == 0
                ? NDQ_OK
                : NDQ_ERR_CUDA;
+}
+
+size_t ndq_attention_prefix_workspace_bytes(int head_dim, int64_t n_tokens, int q_heads, int kv_heads) {
+    if ((head_dim != 64 && head_dim != 128) || n_tokens < 0 || n_tokens > INT32_MAX / 2 || kv_heads < 1 || q_heads < 1 ||
+        q_heads > 4096 || q_heads % kv_heads != 0 || n_tokens > INT32_MAX / q_heads)
+        return 0;
+    return ndq::prefix_workspace_bytes(head_dim, n_tokens, q_heads, kv_heads);
+}
+
+int ndq_attention_prefix_kv8(const ndq_kv_cache* cache, const void* q, int dtype, int64_t n_tokens, int q_heads,
+                             int64_t q_stride, const int32_t* block_table, int64_t table_width, const int32_t* kv_len,
+                             const int32_t* q_start, int64_t n_req, int64_t max_q, const int32_t* group_start,
+                             const int32_t* prefix_len, int64_t n_groups, float scale, int64_t window, void* out,
+                             float* lse, void* workspace, size_t ws_bytes, void* stream) {
+    ndq::PrefixParams p{};
+    bool empty = false;
+    if (n_groups < 0) return NDQ_ERR_NEGATIVE_DIM;
+    const int rc = check_attention(cache, q, dtype, n_tokens, q_heads, q_stride, block_table, table_width, kv_len, q_start, n_req,
+                                   max_q, scale, window, out, lse, &p, &empty);
+    if (rc != NDQ_OK) return rc;
+    if (n_groups > INT32_MAX / 2) return NDQ_ERR_BAD_ARG;
+    if (empty) return NDQ_OK;
+    if (n_groups > 0 && (!group_start || !prefix_len)) return NDQ_ERR_NULL;
+    if (!aligned(group_start, 4) || !aligned(prefix_len, 4)) return NDQ_ERR_MISALIGNED;
+    const int D = cache->head_dim;
+    if (!workspace || !aligned(workspace, 256) || ws_bytes < ndq::prefix_workspace_bytes(D, n_tokens, q_heads, cache->kv_heads))
+        return NDQ_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.counters = static_cast<uint32_t*>(workspace);
+    p.parts = reinterpret_cast<float*>(ws + ndq::kAttnCounterBytes);
+    p.group_start = group_start;
+    p.prefix_len = prefix_len;
+    p.n_groups = n_groups;
+    p.records = ws + ndq::prefix_records_at(D);
+    p.slots = reinterpret_cast<float*>(ws + ndq::prefix_slots_at(D, n_tokens, q_heads));
+    p.slot_rows = ndq::prefix_slot_rows(n_tokens, q_heads, cache->kv_heads);
+    p.waits = take_waits();
+    const bool e4m3 = cache->code_type == NDQ_FLOAT8E4M3FN, bf16 = dtype == NDQ_BFLOAT16;
+    const int e = n_groups == 0 ? ndq::launch_attention(p, D, e4m3, bf16, stream) : ndq::launch_attention_prefix(p, D, e4m3, bf16, stream);
+    return e == 0 ? NDQ_OK : NDQ_ERR_CUDA;
 }
 
 int ndq_qk_norm_rope(const void* q, int q_heads, int64_t q_stride, const void* k, int k_heads, int64_t k_stride, int in_dtype,

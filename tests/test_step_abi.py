@@ -1,12 +1,14 @@
-"""Refusals of the packed embedding lookup and of the norm and rotation of
-heads: what the host checks before any launch, so these run without a GPU."""
+"""Refusals of the packed embedding lookup, of the norm and rotation of heads
+and of attention behind shared prefixes: what the host checks before any launch,
+so these run without a GPU."""
 import pytest
 import torch
 
 import quantized_weight_block_gb300 as ndq
-from test_serving_binding import On, on_gpu
+from test_serving_abi import BAD_CACHES, cache
+from test_serving_binding import On, attend_args, on_gpu
 
-OK, NULL, UNKNOWN, NEGATIVE, BLOCKS, LENGTH, BAD_DTYPE, BAD_ARG, MISALIGNED = 0, 1, 2, 5, 6, 7, 9, 15, 16
+OK, NULL, UNKNOWN, NEGATIVE, BLOCKS, LENGTH, BAD_DTYPE, WORKSPACE, BAD_ARG, MISALIGNED = 0, 1, 2, 5, 6, 7, 9, 10, 15, 16
 F32, F16, BF16, DOUBLE = ndq.NDQ_FLOAT, ndq.NDQ_FLOAT16, ndq.NDQ_BFLOAT16, ndq.NDQ_DOUBLE
 P = 4096  # a pointer that is never followed
 Q8, FP8 = ndq.format_id("gguf:q8_0"), ndq.format_id("fp8_e4m3fn_row_bf16")
@@ -52,6 +54,42 @@ def test_rope_refusals(kw, want):
     assert rope(**kw) == want
 
 
+def bytes_for(n=3, heads=8, kv=2, D=128):
+    return ndq.ndq_attention_prefix_workspace_bytes(D, n, heads, kv)
+
+
+def prefix(c=None, **kw):
+    a = dict(q=P, dtype=BF16, n_tokens=3, q_heads=8, q_stride=1024, block_table=P, table_width=4, kv_len=P, q_start=P, n_req=2, max_q=3,
+             group_start=P, prefix_len=P, n_groups=1, scale=1.0, window=0, out=P, lse=0, workspace=P, ws_bytes=bytes_for()) | kw
+    return ndq.ndq_attention_prefix_kv8(c or cache(), **a)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(q=0), NULL), (dict(out=0), NULL), (dict(kv_len=0), NULL), (dict(block_table=0), NULL), (dict(group_start=0), NULL),
+    (dict(prefix_len=0), NULL), (dict(n_groups=-1), NEGATIVE), (dict(n_groups=1 << 31), BAD_ARG), (dict(dtype=F32), BAD_DTYPE),
+    (dict(n_tokens=-1), NEGATIVE), (dict(n_req=-1), NEGATIVE), (dict(max_q=-1), NEGATIVE), (dict(window=-1), NEGATIVE),
+    (dict(table_width=-1), NEGATIVE), (dict(q_heads=0), BAD_ARG), (dict(q_heads=7), BAD_ARG), (dict(table_width=1 << 27), BAD_ARG),
+    (dict(n_tokens=1 << 29), BAD_ARG), (dict(scale=float("nan")), BAD_ARG), (dict(q_start=0), BAD_ARG), (dict(q_stride=1016), BAD_ARG),
+    (dict(q_stride=1028), MISALIGNED), (dict(q=P + 2), MISALIGNED), (dict(out=P + 8), MISALIGNED), (dict(lse=P + 2), MISALIGNED),
+    (dict(group_start=P + 2), MISALIGNED), (dict(prefix_len=P + 1), MISALIGNED), (dict(workspace=0), WORKSPACE),
+    (dict(workspace=P + 128), WORKSPACE), (dict(ws_bytes=bytes_for() - 1), WORKSPACE), (dict(n_tokens=0), OK), (dict(n_req=0), OK),
+    (dict(max_q=0), OK)])
+def test_prefix_refusals(kw, want):
+    assert prefix(**kw) == want
+
+
+@pytest.mark.parametrize("kw,want", BAD_CACHES)
+def test_prefix_cache_refusals(kw, want):
+    assert prefix(cache(**kw)) == want
+
+
+def test_prefix_workspace_sizes():
+    assert bytes_for(D=96) == bytes_for(n=-1) == bytes_for(heads=0) == bytes_for(kv=0) == bytes_for(heads=7) == bytes_for(n=1 << 29) == 0
+    assert ndq.ndq_attention_workspace_bytes(128) < bytes_for(n=0) < bytes_for(n=1) < bytes_for(n=2)
+    # records and parts of every row, and of 192 units more
+    assert bytes_for(n=1000) >= 1000 * 8 * (16 + 130 * 4) + 192 * 256 * 130 * 4
+
+
 # ---- the tensor calls -----------------------------------------------------------
 
 BF, I32 = torch.bfloat16, torch.int32
@@ -67,7 +105,11 @@ def rope_args():
                 k_out=torch.zeros(3, 2, 64, dtype=BF))
 
 
-CALLS = {"embed_packed": embed_args, "qk_norm_rope": rope_args}
+def prefix_args():
+    return attend_args() | dict(group_start=torch.tensor([0, 2], dtype=I32), prefix_len=torch.tensor([16], dtype=I32))
+
+
+CALLS = {"embed_packed": embed_args, "qk_norm_rope": rope_args, "attention_prefix_kv8": prefix_args}
 
 
 @pytest.fixture
@@ -107,7 +149,11 @@ def test_a_tensor_elsewhere_is_refused(name, arg, elsewhere, launches):
     ("qk_norm_rope", dict(inv_freq=torch.zeros(32, dtype=torch.float64))), ("qk_norm_rope", dict(q_weight=torch.ones(64, dtype=BF))),
     ("qk_norm_rope", dict(k_weight=torch.ones(32))), ("qk_norm_rope", dict(q_out=torch.zeros(3, 4, 64))),
     ("qk_norm_rope", dict(k_out=torch.zeros(3, 2, 32, dtype=BF))), ("qk_norm_rope", dict(k=None)),
-    ("qk_norm_rope", dict(q=None, k=None))])
+    ("qk_norm_rope", dict(q=None, k=None)), ("attention_prefix_kv8", dict(group_start=torch.zeros(3, dtype=I32))),
+    ("attention_prefix_kv8", dict(group_start=torch.zeros(2, dtype=torch.int64))), ("attention_prefix_kv8", dict(prefix_len=torch.tensor(16, dtype=I32))),
+    ("attention_prefix_kv8", dict(prefix_len=torch.zeros(1, 1, dtype=I32))), ("attention_prefix_kv8", dict(prefix_len=torch.zeros(1))),
+    ("attention_prefix_kv8", dict(group_start=torch.zeros(4, dtype=I32)[::2])), ("attention_prefix_kv8", dict(lse=torch.zeros(3, 5))),
+    ("attention_prefix_kv8", dict(workspace=torch.zeros(64, dtype=torch.uint8)[::2]))])
 def test_other_tensors_are_refused(name, change, launches):
     args = on_gpu(CALLS[name]() | change)
     with pytest.raises(ValueError):
