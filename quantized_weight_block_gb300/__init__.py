@@ -745,49 +745,52 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     first = q if q is not None else k
     if first is None:
         raise ValueError("qk_norm_rope needs q or k")
-    if first.dim() != 3 or positions.dim() != 1 or inv_freq.dim() != 1:
+    shape = first.shape
+    if len(shape) != 3 or positions.dim() != 1 or inv_freq.dim() != 1:
         raise ValueError("q and k must be [tokens, heads, head_dim], positions [tokens] and inv_freq [rot_dim / 2]")
-    T, D, dtype = first.shape[0], first.shape[2], first.dtype
+    T, H, D = shape
+    dtype, gpu = first.dtype, first.get_device()
     code = c.code.get(dtype)
     if code is None:
         raise ValueError("q and k must be float32, bfloat16 or float16")
-    if (positions.dtype is not c.i32 or positions.shape[0] != T or not positions.is_contiguous() or inv_freq.dtype is not c.f32
+    if (positions.dtype is not c.i32 or positions.numel() != T or not positions.is_contiguous() or inv_freq.dtype is not c.f32
             or not inv_freq.is_contiguous()):
         raise ValueError("positions must be int32 [tokens] and inv_freq float32 [rot_dim / 2], both contiguous")
-    gpu = first.get_device()
-    _same_device("qk_norm_rope", gpu, first, positions, inv_freq)
-    given = q_out if q_out is not None else k_out
-    odt = out_dtype or (given.dtype if given is not None else dtype if dtype is not c.f32 else c.bf16)
-    if odt is not c.bf16 and odt is not c.f16:
+    _same_device("qk_norm_rope", gpu, positions, inv_freq)
+    if out_dtype is None:
+        given = q_out if q_out is not None else k_out
+        out_dtype = given.dtype if given is not None else dtype if dtype is not c.f32 else c.bf16
+    if out_dtype is not c.bf16 and out_dtype is not c.f16:
         raise ValueError("qk_norm_rope writes bfloat16 or float16")
-    args, outs = [], []
-    for name, x, y, w in (("q", q, q_out, q_weight), ("k", k, k_out, k_weight)):
+
+    def side(name, x, y, w):
+        """The arguments of q or k: pointer, heads, stride, weight, output, its stride; and the output."""
         if x is None:
             if y is not None or w is not None:
                 raise ValueError(f"{name}_out and {name}_weight need {name}")
-            args.append((None, 0, 0, None, None, 0))
-            outs.append(None)
-            continue
-        if x.dtype is not dtype or x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or x.get_device() != gpu:
+            return None, 0, 0, None, None, 0, None
+        shape = x.shape
+        if x.dtype is not dtype or len(shape) != 3 or shape[0] != T or shape[2] != D or x.get_device() != gpu:
             raise ValueError("q and k must have the same type, tokens and head_dim, on one device")
-        H = x.shape[1]
+        H = shape[1]
         if w is not None and (w.dtype is not c.f32 or w.shape != (D,) or not w.is_contiguous() or w.get_device() != gpu):
             raise ValueError(f"{name}_weight must be float32 [head_dim], contiguous, on {name}'s device")
         if y is None:
-            y = _made_for(stream, lambda shape=x.shape: _torch().zeros(shape, dtype=odt, device=first.device))
+            y = _made_for(stream, lambda: _torch().zeros(shape, dtype=out_dtype, device=x.device))
             _returned(stream, y)
-        elif y.dtype is not odt or y.shape != x.shape or y.get_device() != gpu:
-            raise ValueError(f"{name}_out must be {odt}, of {name}'s shape, on its device")
-        args.append((x.data_ptr(), H, _row_stride(name, x, H, D), None if w is None else w.data_ptr(), y.data_ptr(),
-                     _row_stride(name + "_out", y, H, D)))
-        outs.append(y)
-    (qp, qh, qs, qw, qo, qos), (kp, kh, ks, kw, ko, kos) = args
-    rc = _lib.ndq_qk_norm_rope(qp, qh, qs, kp, kh, ks, code, T, D, 2 * inv_freq.shape[0], 1 if interleaved else 0,
-                               positions.data_ptr(), inv_freq.data_ptr(), qw, kw, eps, qo, qos, ko, kos, c.code[odt],
+        elif y.dtype is not out_dtype or y.shape != shape or y.get_device() != gpu:
+            raise ValueError(f"{name}_out must be {out_dtype}, of {name}'s shape, on its device")
+        return (x.data_ptr(), H, _row_stride(name, x, H, D), None if w is None else w.data_ptr(), y.data_ptr(),
+                _row_stride(name, y, H, D), y)
+
+    qp, qh, qs, qw, qo, qos, q_out = side("q", q, q_out, q_weight)
+    kp, kh, ks, kw, ko, kos, k_out = side("k", k, k_out, k_weight)
+    rc = _lib.ndq_qk_norm_rope(qp, qh, qs, kp, kh, ks, code, T, D, 2 * inv_freq.numel(), 1 if interleaved else 0,
+                               positions.data_ptr(), inv_freq.data_ptr(), qw, kw, eps, qo, qos, ko, kos, c.code[out_dtype],
                                _raw_stream(stream, gpu))
     if rc:
         raise NdqError(rc, "qk_norm_rope")
-    return tuple(outs)
+    return q_out, k_out
 
 
 def lora_workspace(M: int, n_adapters: int, max_rank: int, K: int, device="cuda"):

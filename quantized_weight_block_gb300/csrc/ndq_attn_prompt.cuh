@@ -167,7 +167,7 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t* v) {
 // Barriers by number: every thread of the roles that meet there, and no other.
 template <int ID, int THREADS>
 __device__ __forceinline__ void meet() { asm volatile("barrier.cta.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory"); }
-constexpr int kMeetAll = 1, kMeetEnd = 2, kMeetRows = 3;
+constexpr int kMeetAll = 1, kMeetEnd = 2, kMeetRows = 3, kMeetQ = 4;
 
 template <int N>
 __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -228,8 +228,6 @@ __device__ __forceinline__ SharedUnits shared_units(const PrefixParams& p, const
     x.tiles = (g.tokens + kPrTokens - 1) / kPrTokens;
     return x;
 }
-__device__ __forceinline__ int64_t pad4(int64_t rows) { return (rows + 3) & ~static_cast<int64_t>(3); }
-
 // The sum over the block's threads before this one, and of all of them.
 __device__ __forceinline__ uint64_t block_scan(uint64_t mine, uint64_t* warps, uint64_t& total) {
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
@@ -271,61 +269,95 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     // then row tile (the last, longest, first), then head
     const uint64_t unit = blockIdx.x / static_cast<uint32_t>(p.splits);
     const uint32_t split = blockIdx.x % static_cast<uint32_t>(p.splits);
-    int64_t slot_row = 0;       // (kAttnShared) this CTA's slot, and the parts of its unit
-    uint32_t pad = 0, parts = 1, part = 0;
+    int64_t slot_row = 0;  // (kAttnShared) this CTA's slot, and the parts of its unit
+    uint32_t parts = 1, part = 0;
     if constexpr (MODE == kAttnShared) {
         // Every CTA counts the groups' units and tiles, from these how many
         // tiles a CTA is to take, and then finds its unit and part.
-        const int64_t per = (p.n_groups + kPrThreads - 1) / kPrThreads;
-        uint64_t units = 0, work = 0, all_units = 0, all_work = 0;
-        for (int64_t i = 0; i < per; ++i) {
-            const int64_t g = tid * per + i;
-            if (g < p.n_groups) {
-                const SharedUnits x = shared_units(p, attn_group(p, g));
-                units += static_cast<uint64_t>(x.units);
-                work += static_cast<uint64_t>(x.units) * static_cast<uint64_t>(x.tiles);
-            }
-        }
-        block_scan(units, S.sum, all_units);
-        block_scan(work, S.tot, all_work);
-        // CTAs beyond one per unit number at most work / chunk, no more than the SMs
-        const uint64_t sms = static_cast<uint64_t>(p.sms);
-        const uint64_t spare = all_units + sms / 4 < sms ? sms - all_units : (sms + 3) / 4;
-        uint64_t chunk = (all_work + spare - 1) / spare;
-        chunk = chunk < 4 ? 4 : chunk;
+        uint64_t chunk = 1;
         auto parts_of = [&](int32_t tiles) {
-            const uint64_t n = (static_cast<uint64_t>(tiles) + chunk - 1) / chunk;
+            const uint64_t n = chunk >= static_cast<uint64_t>(tiles) ? 1 : (static_cast<uint32_t>(tiles) + static_cast<uint32_t>(chunk) - 1) / static_cast<uint32_t>(chunk);
             return static_cast<int64_t>(n > kPrefixMaxParts ? kPrefixMaxParts : n);
         };
-        auto ctas_of = [&](const SharedUnits& x) { return x.units * parts_of(x.tiles); };
-        auto slots_of = [&](const SharedUnits& x) {
-            return (x.rows / kPromptRows * kPromptRows + pad4(x.rows % kPromptRows)) * p.c.heads * parts_of(x.tiles);
+        auto set_chunk = [&](uint64_t units, uint64_t work) {
+            // CTAs beyond one per unit number at most work / chunk, no more than the SMs
+            const uint64_t sms = static_cast<uint64_t>(p.sms);
+            const uint64_t spare = units + sms / 4 < sms ? sms - units : (sms + 3) / 4;
+            chunk = (work >> 32) != 0 ? (work + spare - 1) / spare : static_cast<uint32_t>(work + spare - 1) / static_cast<uint32_t>(spare);
+            chunk = chunk < kPrefixMinTiles ? kPrefixMinTiles : chunk;
         };
-        uint64_t ctas = 0, rows = 0, all_ctas = 0, all_rows = 0;
-        for (int64_t i = 0; i < per; ++i) {
-            const int64_t g = tid * per + i;
-            if (g < p.n_groups) {
-                const SharedUnits x = shared_units(p, attn_group(p, g));
-                ctas += static_cast<uint64_t>(ctas_of(x));
-                rows += static_cast<uint64_t>(slots_of(x));
-            }
-        }
-        __syncthreads();  // (the sums above are read)
-        const uint64_t ctas_before = block_scan(ctas, S.sum, all_ctas), rows_before = block_scan(rows, S.tot, all_rows);
-        if (blockIdx.x >= all_ctas || all_rows > static_cast<uint64_t>(p.slot_rows)) return;  // (never the latter)
-        if (ctas_before <= blockIdx.x && blockIdx.x < ctas_before + ctas) {
-            uint64_t c = ctas_before, n = rows_before;
-            int64_t g = tid * per;
-            SharedUnits x = shared_units(p, attn_group(p, g));
-            while (blockIdx.x >= c + static_cast<uint64_t>(ctas_of(x))) {
-                c += static_cast<uint64_t>(ctas_of(x));
-                n += static_cast<uint64_t>(slots_of(x));
-                x = shared_units(p, attn_group(p, ++g));
-            }
+        auto ctas_of = [&](const SharedUnits& x) { return static_cast<uint64_t>(x.units * parts_of(x.tiles)); };
+        auto slots_of = [&](const SharedUnits& x) { return static_cast<uint64_t>(x.rows * p.c.heads * parts_of(x.tiles)); };
+        auto mine = [&](int64_t g, uint64_t c, uint64_t n, int64_t parts_here) {
             S.r = g;
             S.base = static_cast<int64_t>(blockIdx.x - c);
             S.slot = static_cast<int64_t>(n);
-            S.parts = static_cast<uint32_t>(parts_of(x.tiles));
+            S.parts = static_cast<uint32_t>(parts_here);
+        };
+        if (p.n_groups <= 32) {  // every warp for itself
+            SharedUnits x{};
+            if (lane < p.n_groups) x = shared_units(p, attn_group(p, lane));
+            uint64_t units = static_cast<uint64_t>(x.units), work = units * static_cast<uint64_t>(x.tiles);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                if (d >= p.n_groups) break;
+                units += __shfl_xor_sync(0xffffffffu, units, d);
+                work += __shfl_xor_sync(0xffffffffu, work, d);
+            }
+            units = __shfl_sync(0xffffffffu, units, 0);
+            set_chunk(units, __shfl_sync(0xffffffffu, work, 0));
+            const uint64_t ctas = x.units > 0 ? ctas_of(x) : 0, rows = x.units > 0 ? slots_of(x) : 0;
+            uint64_t ci = ctas, ri = rows;
+#pragma unroll
+            for (uint32_t d = 1; d < 32; d <<= 1) {
+                if (d >= p.n_groups) break;
+                const uint64_t a = __shfl_up_sync(0xffffffffu, ci, d), b = __shfl_up_sync(0xffffffffu, ri, d);
+                if (lane >= d) {
+                    ci += a;
+                    ri += b;
+                }
+            }
+            const uint32_t here = __ballot_sync(0xffffffffu, blockIdx.x < ci && blockIdx.x >= ci - ctas);
+            const uint64_t all_rows = __shfl_sync(0xffffffffu, ri, static_cast<int>(p.n_groups) - 1);
+            if (here == 0u || all_rows > static_cast<uint64_t>(p.slot_rows)) return;  // (the latter never)
+            if (warp == 0 && lane == static_cast<uint32_t>(__ffs(here)) - 1u) mine(lane, ci - ctas, ri - rows, parts_of(x.tiles));
+        } else {
+            const int64_t per = (p.n_groups + kPrThreads - 1) / kPrThreads;
+            uint64_t units = 0, work = 0, all_units = 0, all_work = 0;
+            for (int64_t i = 0; i < per; ++i) {
+                const int64_t g = tid * per + i;
+                if (g < p.n_groups) {
+                    const SharedUnits x = shared_units(p, attn_group(p, g));
+                    units += static_cast<uint64_t>(x.units);
+                    work += static_cast<uint64_t>(x.units) * static_cast<uint64_t>(x.tiles);
+                }
+            }
+            block_scan(units, S.sum, all_units);
+            block_scan(work, S.tot, all_work);
+            set_chunk(all_units, all_work);
+            uint64_t ctas = 0, rows = 0, all_ctas = 0, all_rows = 0;
+            for (int64_t i = 0; i < per; ++i) {
+                const int64_t g = tid * per + i;
+                if (g < p.n_groups) {
+                    const SharedUnits x = shared_units(p, attn_group(p, g));
+                    ctas += ctas_of(x);
+                    rows += slots_of(x);
+                }
+            }
+            __syncthreads();  // (the sums above are read)
+            const uint64_t ctas_before = block_scan(ctas, S.sum, all_ctas), rows_before = block_scan(rows, S.tot, all_rows);
+            if (blockIdx.x >= all_ctas || all_rows > static_cast<uint64_t>(p.slot_rows)) return;
+            if (ctas_before <= blockIdx.x && blockIdx.x < ctas_before + ctas) {
+                uint64_t c = ctas_before, n = rows_before;
+                int64_t g = tid * per;
+                SharedUnits x = shared_units(p, attn_group(p, g));
+                while (blockIdx.x >= c + ctas_of(x)) {
+                    c += ctas_of(x);
+                    n += slots_of(x);
+                    x = shared_units(p, attn_group(p, ++g));
+                }
+                mine(g, c, n, parts_of(x.tiles));
+            }
         }
     } else {
         const int64_t per = (p.n_req + kPrThreads - 1) / kPrThreads;
@@ -406,8 +438,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         row0 = static_cast<int32_t>(tile) * kPromptRows;
         const int64_t rows_left = x.rows - row0;
         nrows = static_cast<int32_t>(rows_left < kPromptRows ? rows_left : kPromptRows);
-        pad = static_cast<uint32_t>(pad4(nrows));
-        slot_row = S.slot + (tile * kPromptRows * p.c.heads + static_cast<int64_t>(h) * pad) * parts + static_cast<int64_t>(part) * pad;
+        slot_row = S.slot + (tile * kPromptRows * p.c.heads + static_cast<int64_t>(h) * nrows) * parts + static_cast<int64_t>(part) * nrows;
     } else {
         uint64_t left = unit - static_cast<uint64_t>(S.base);
         int64_t tiles = prompt_tiles(p, r, q0, n, pos0);
@@ -440,6 +471,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         const int32_t j0 = all_tiles * static_cast<int32_t>(split) / p.splits;
         nt = all_tiles * static_cast<int32_t>(split + 1) / p.splits - j0;
         tok0 = lo16 + j0 * kPrTokens;
+    } else {  // (with a window, see below)
+        const int32_t tiles = (own + kPrTokens - 1) / kPrTokens;
+        const int32_t j0 = tiles * static_cast<int32_t>(part) / static_cast<int32_t>(parts);
+        nt = tiles * static_cast<int32_t>(part + 1) / static_cast<int32_t>(parts) - j0;
+        tok0 = j0 * kPrTokens;
+        any_lo = 0;
+        any_hi = own;
     }
 
     // Q: one row per softmax thread, scaled, as a 128-byte-swizzled operand
@@ -448,34 +486,94 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     int32_t see_lo = 0, see_hi = 0;
     int32_t at = 0;  // index of the row's output (n_tokens * q_heads is below 2^31)
     bool has_row = false;
-    if (warp < kPrConvWarp) {
+    // without a window the loader has all that it needs: it goes ahead
+    const bool ahead = MODE == kAttnShared && p.window == 0;
+    if (MODE == kAttnShared && warp < kPrConvWarp) {
+        // The rows' loads first, by D / 8 lanes a row (a thread that read its
+        // own row would fetch every line by sixteenths); whose they are and
+        // where they sit meanwhile.
+        constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per load
         const int32_t i = static_cast<int32_t>(wg * 128u + wrow);
+        const int32_t mine = row0 + (i < nrows ? i : 0);
+        const int32_t qi = mine / p.group, qh = h * p.group + mine % p.group;
+        at = static_cast<int32_t>((q0 + qi) * p.q_heads) + qh;
+        const int64_t off = (q0 + qi) * p.q_stride + static_cast<int64_t>(qh) * D;
+        uint4 x[32 / RPI];
+#pragma unroll
+        for (int c = 0; c < 32 / RPI; ++c) {
+            const int64_t o = __shfl_sync(0xffffffffu, off, c * RPI + static_cast<int>(lane) / LPR);
+            x[c] = *reinterpret_cast<const uint4*>(p.q + o + (lane % LPR) * 8);
+        }
         has_row = i < nrows;
         int32_t pos = 0;
-        if constexpr (MODE == kAttnShared) {  // whose query this is, and where it sits
-            if (has_row) {
-                const int64_t t = q0 + (row0 + i) / p.group;
-                int64_t rq = t, a0 = t;
-                int32_t an = 1;
-                if (p.q_start) {
-                    // requests of one length, mostly; else the last that starts at t or before
-                    rq = r + (t - q0) / ((n + (group_end - r) - 1) / (group_end - r));
-                    if (!(p.q_start[rq] <= t && t < p.q_start[rq + 1])) {
-                        int64_t a = r, b = group_end;
-                        while (b - a > 1) {
-                            const int64_t m = (a + b) >> 1;
-                            if (p.q_start[m] <= t) a = m;
-                            else b = m;
-                        }
-                        rq = a;
+        if (has_row) {
+            const int64_t t = q0 + qi;
+            int64_t rq = t, a0 = t;
+            int32_t an = 1;
+            if (p.q_start) {
+                // requests of one length, mostly; else the last that starts at t or before
+                const int32_t reqs = static_cast<int32_t>(group_end - r);
+                rq = r + qi / ((n + reqs - 1) / reqs);
+                if (!(p.q_start[rq] <= t && t < p.q_start[rq + 1])) {
+                    int64_t a = r, b = group_end;
+                    while (b - a > 1) {
+                        const int64_t m = (a + b) >> 1;
+                        if (p.q_start[m] <= t) a = m;
+                        else b = m;
                     }
+                    rq = a;
                 }
-                attn_request(p, rq, a0, an, pos);
-                has_row = a0 <= t && t < a0 + an;
-                pos += static_cast<int32_t>(t - a0);
             }
+            attn_request(p, rq, a0, an, pos);
+            has_row = a0 <= t && t < a0 + an;
+            pos += static_cast<int32_t>(t - a0);
         }
-        const int32_t qi = (row0 + (i < nrows ? i : 0)) / p.group, qh = h * p.group + (row0 + (i < nrows ? i : 0)) % p.group;
+        see_hi = has_row && pos >= 0 ? (pos < most ? pos + 1 : most) : 0;
+        see_hi = see_hi < own ? see_hi : own;
+        see_lo = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
+        const uint32_t rows_here = __ballot_sync(0xffffffffu, has_row);
+        uint8_t* dst = sQ + wg * kTile;
+        const uint32_t piece = lane % LPR;
+#pragma unroll
+        for (int c = 0; c < 32 / RPI; ++c) {
+            const uint32_t rl = c * RPI + lane / LPR;  // the row among the warp's 32
+            const bool in = (rows_here >> rl & 1u) != 0u;
+            const uint32_t ww[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+            float f[8], amax = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                widen2<BF16>(in ? ww[e] : 0u, f[2 * e], f[2 * e + 1]);
+                amax = max3(amax, fabsf(f[2 * e]), fabsf(f[2 * e + 1]));
+            }
+#pragma unroll
+            for (int e = 1; e < LPR; e <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, e));
+            float up, down;
+            row_scale(amax, up, down);
+            if (p.scale_log2 < 0.0f) {  // (a negative scale goes into Q: K's scale then keeps the order of scores)
+                up = -up;
+                down = -down;
+            }
+            // (the row's owner, lane rl, is served by the lanes of its row)
+            const float fr = __shfl_sync(0xffffffffu, down * p.scale_log2, (static_cast<int>(lane) % RPI) * LPR);
+            if (lane / RPI == static_cast<uint32_t>(c)) frow = fr;
+            *reinterpret_cast<uint4*>(dst + (piece >> 3) * kAtom + sw128(32u * (warp & 3u) + rl, piece & 7u)) =
+                make_uint4(pack_half2(f[0] * up, f[1] * up), pack_half2(f[2] * up, f[3] * up), pack_half2(f[4] * up, f[5] * up),
+                           pack_half2(f[6] * up, f[7] * up));
+        }
+        const int32_t l0 = __reduce_min_sync(0xffffffffu, has_row ? see_lo : INT32_MAX), l1 = __reduce_max_sync(0xffffffffu, has_row ? see_lo : 0);
+        const int32_t h0 = __reduce_min_sync(0xffffffffu, has_row ? see_hi : INT32_MAX), h1 = __reduce_max_sync(0xffffffffu, see_hi);
+        if (lane == 0) {
+            atomicMin(&S.lo_min, l0);
+            atomicMax(&S.lo_max, l1);
+            atomicMin(&S.hi_min, h0);
+            atomicMax(&S.hi_max, h1);
+        }
+        fence_proxy_async_smem();
+    }
+    if (MODE != kAttnShared && warp < kPrConvWarp) {
+        const int32_t i = static_cast<int32_t>(wg * 128u + wrow);
+        has_row = i < nrows;
+        const int32_t qi = (row0 + (has_row ? i : 0)) / p.group, qh = h * p.group + (row0 + (has_row ? i : 0)) % p.group;
         at = static_cast<int32_t>((q0 + qi) * p.q_heads) + qh;
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (q0 + qi) * p.q_stride + static_cast<int64_t>(qh) * D);
         float amax = 0.0f;
@@ -511,38 +609,32 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             }
             *reinterpret_cast<uint4*>(dst + (c >> 3) * kAtom + sw128(wrow, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        if constexpr (MODE != kAttnShared) pos = pos0 + qi;
+        const int32_t pos = pos0 + qi;
         see_hi = has_row && pos >= 0 ? (pos < most ? pos + 1 : most) : 0;
         see_lo = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
         if constexpr (MODE == kAttnOwn) see_lo = see_lo > own ? see_lo : own;
-        if constexpr (MODE == kAttnShared) {
-            see_hi = see_hi < own ? see_hi : own;
-            const int32_t l0 = __reduce_min_sync(0xffffffffu, has_row ? see_lo : INT32_MAX), l1 = __reduce_max_sync(0xffffffffu, has_row ? see_lo : 0);
-            const int32_t h0 = __reduce_min_sync(0xffffffffu, has_row ? see_hi : INT32_MAX), h1 = __reduce_max_sync(0xffffffffu, see_hi);
-            if (lane == 0) {
-                atomicMin(&S.lo_min, l0);
-                atomicMax(&S.lo_max, l1);
-                atomicMin(&S.hi_min, h0);
-                atomicMax(&S.hi_max, h1);
-            }
-        }
         fence_proxy_async_smem();
     }
     tc_fence_before();
-    __syncthreads();
+    if (!ahead) __syncthreads();
+    else if (warp <= kPrMmaWarp) meet<kMeetQ, (kPrMmaWarp + 1) * 32>();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    if constexpr (MODE == kAttnShared) {  // the rows are of many requests: what they see is known now
-        any_lo = S.lo_min;
-        cta_lo = S.lo_max;
-        any_hi = S.hi_max;
-        cta_hi = S.hi_min;
-        const int64_t tiles = (own + kPrTokens - 1) / kPrTokens;
-        int32_t j0 = static_cast<int32_t>(tiles * part / parts), j1 = static_cast<int32_t>(tiles * (part + 1) / parts);
-        if (any_hi > any_lo) {
-            j0 = j0 > any_lo / kPrTokens ? j0 : any_lo / kPrTokens;
-            j1 = j1 < (any_hi + kPrTokens - 1) / kPrTokens ? j1 : (any_hi + kPrTokens - 1) / kPrTokens;
-            nt = j1 > j0 ? j1 - j0 : 0;
+    if constexpr (MODE == kAttnShared) {
+        // the rows are of many requests: what they see is known now (the
+        // loader that went ahead brings the tiles of all of the prefix)
+        if (!ahead || warp <= kPrMmaWarp) {
+            any_lo = S.lo_min;
+            cta_lo = S.lo_max;
+            any_hi = S.hi_max;
+            cta_hi = S.hi_min;
+        }
+        if (!ahead) {  // tiles before and behind the windows are left out
+            int32_t j0 = tok0 / kPrTokens, j1 = j0 + nt;
+            const int32_t first = any_lo / kPrTokens, end = (any_hi + kPrTokens - 1) / kPrTokens;
+            j0 = j0 > first ? j0 : first;
+            j1 = j1 < end ? j1 : end;
+            nt = any_hi > any_lo && j1 > j0 ? j1 - j0 : 0;
             tok0 = j0 * kPrTokens;
         }
     }
@@ -782,16 +874,18 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         bool ok = true;
         uint32_t w[kPrTokens / 2];  // the row's weights of the tile, in pairs
         // The weights relative to ms (and less), their sum and the largest exponent.
-        auto weigh = [&](auto mask, auto again, float less, const float4* cst, int32_t tb, float& ts, float& top) {
+        auto weigh = [&](auto mask, auto again, bool read, float less, const float4* cst, int32_t tb, float& ts, float& top) {
             constexpr bool kMasked = decltype(mask)::value, kAgain = decltype(again)::value;
             uint32_t v[2][16];
             ts = 0.0f;
             float tops[2] = {-INFINITY, -INFINITY};
-            tmem_ld16(tS, v[0]);
+            if (MODE == kAttnAll || read) tmem_ld16(tS, v[0]);
 #pragma unroll
             for (int q = 0; q < kPrGroups; ++q) {  // a group of 16 tokens; the next one's scores load meanwhile
-                tmem_wait_ld16(v[q & 1]);
-                if (q + 1 < kPrGroups) tmem_ld16(tS + 16 * (q + 1), v[(q + 1) & 1]);
+                if (MODE == kAttnAll || read) {
+                    tmem_wait_ld16(v[q & 1]);
+                    if (q + 1 < kPrGroups) tmem_ld16(tS + 16 * (q + 1), v[(q + 1) & 1]);
+                }
                 const uint32_t* x = v[q & 1];
                 const float4 k = cst[q];
                 const uint64_t f2 = pair(frow * k.x, frow * k.x), c2 = pair(k.y - ms, k.y - ms);
@@ -831,18 +925,56 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             }
             top = fmaxf(tops[0], tops[1]);
         };
-        for (int32_t j = 0; j < nt; ++j) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.sfull[wg], static_cast<uint32_t>(j & 1), p.waits.limit_ns));
-            if (!ok) break;
-            tc_fence_after();
-            const int32_t tb = tok0 + j * kPrTokens;
-            const bool masked = tb + kPrTokens > all_hi || tb < all_lo || S.gap[j % kPrCst] != 0u;
-            const float4* cst = S.cst[j % kPrCst];
+        // The first tile's maximum, in a small loop: without it the weights
+        // would be taken twice there.
+        auto first_top = [&](const float4* cst, int32_t tb) {
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < kPrGroups; ++q) {
+                uint32_t v[16];
+                tmem_ld16(tS + 16 * q, v);
+                tmem_wait_ld16(v);
+                const float4 k = cst[q];
+                const float f = frow * k.x;
+                const int32_t pos = tb + 16 * q;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float y = __fmaf_rn(__uint_as_float(v[e]), f, k.y);
+                    if (pos + e >= see_lo && pos + e < see_hi) top = fmaxf(top, y);
+                }
+            }
+            return top;
+        };
+        // Pass -1 takes weights of nothing, while the first codes are on their
+        // way: it brings the code of the loop, 9 KB, to the SM, which cost 14000
+        // cycles of the first tile (33000 on all SMs at once).
+        for (int32_t j = MODE != kAttnAll && nt > 0 ? -1 : 0; j < nt; ++j) {
+            bool masked = false;
+            int32_t tb = 0;
+            if (MODE == kAttnAll || j >= 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.sfull[wg], static_cast<uint32_t>(j & 1), p.waits.limit_ns));
+                if (!ok) break;
+                tc_fence_after();
+                tb = tok0 + j * kPrTokens;
+                masked = tb + kPrTokens > all_hi || tb < all_lo || S.gap[j % kPrCst] != 0u;
+                if (MODE != kAttnAll && __any_sync(0xffffffffu, mx == -INFINITY && see_lo < tb + kPrTokens && see_hi > tb)) {
+                    const float top = first_top(S.cst[j % kPrCst], tb);
+                    if (mx == -INFINITY) ms = top > -INFINITY && top < INFINITY ? top : 0.0f;
+                }
+            }
+            const float4* cst = S.cst[MODE == kAttnAll || j >= 0 ? j % kPrCst : 0];
             float ts, top;
-            if (masked) weigh(std::true_type{}, std::false_type{}, 0.0f, cst, tb, ts, top);
-            else weigh(std::false_type{}, std::false_type{}, 0.0f, cst, tb, ts, top);
-            const bool grow = top > (mx == -INFINITY ? -INFINITY : 8.0f);
-            // a row passed its maximum by 8: always in the first tile that it sees, rarely later
+            if (masked) weigh(std::true_type{}, std::false_type{}, j >= 0, 0.0f, cst, tb, ts, top);
+            else weigh(std::false_type{}, std::false_type{}, j >= 0, 0.0f, cst, tb, ts, top);
+            if (MODE != kAttnAll && j < 0) continue;
+            bool grow = top > (mx == -INFINITY ? -INFINITY : 8.0f);
+            if constexpr (MODE != kAttnAll) {
+                if (mx == -INFINITY && top >= -8.0f && top <= 8.0f) {  // ms is the maximum, but for roundings
+                    mx = ms;
+                    grow = false;
+                }
+            }
+            // a row passed its maximum by 8: always in the first tile that it sees (or where that is not known before), rarely later
             if (__any_sync(0xffffffffu, grow)) {
                 const float ah = !grow ? 1.0f : (mx == -INFINITY ? 0.0f : exp2_fast(-0.5f * top)), al = ah * ah;
                 if (j > 0) {  // O moves to the new maximum once the product before this one is done with it
@@ -863,7 +995,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 sum = sum * ah * ah;
                 // the same exponents less the growth, so that the largest is 0 whatever ms + top is rounded to
                 const float less = grow ? top : 0.0f;
-                weigh(std::true_type{}, std::true_type{}, less, cst, tb, ts, top);
+                weigh(std::true_type{}, std::true_type{}, true, less, cst, tb, ts, top);
                 if (grow) mx = ms = ms + less;
             }
             sum += ts;
@@ -915,18 +1047,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         const bool leaves = MODE == kAttnShared || p.splits > 1;
         const uint32_t prow = wg * 128u + wrow;
         float* slot = p.parts + static_cast<uint64_t>(blockIdx.x) * NDQ_PROMPT_SLOT(D);
-        uint32_t slot_pad = kPromptRows;
-        bool stays = leaves;
+        float4* staged = reinterpret_cast<float4*>(base) + prow * (D / 4 + 1);  // (kAttnShared) the row on its way to its slot
         if constexpr (MODE == kAttnShared) {
-            slot = p.slots + slot_row * (D + 2);
-            slot_pad = pad;
-            stays = static_cast<int32_t>(prow) < nrows;
+            staged[D / 4] = make_float4(mx, sum, 0.0f, 0.0f);
             if (part == 0 && has_row)
-                static_cast<uint4*>(p.records)[at] = make_uint4(static_cast<uint32_t>(slot_row), pad, parts, prow);
-        }
-        if (stays) {
+                static_cast<uint4*>(p.records)[at] = make_uint4(static_cast<uint32_t>(slot_row), static_cast<uint32_t>(nrows), parts, prow);
+        } else if (leaves) {
             slot[prow] = mx;
-            slot[slot_pad + prow] = sum;
+            slot[kPromptRows + prow] = sum;
         }
         // what the prefix adds to the row, if this kernel finishes it
         constexpr bool kJoin = MODE == kAttnOwn;
@@ -940,10 +1068,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 self = hs * hs;
                 sum = sum * hs * hs;
                 for (uint32_t k = 0; k < rp.n; ++k) {
-                    const float mk = rp.top(k), lk = rp.sum(k);
-                    if (mk == -INFINITY && lk == lk) continue;
-                    const float hf = part_root(mk, top);
-                    sum = __fmaf_rn(lk * hf, hf, sum);
+                    const float2 x = rp.stat(k);
+                    if (x.x == -INFINITY && x.y == x.y) continue;
+                    const float hf = part_root(x.x, top);
+                    sum = __fmaf_rn(x.y * hf, hf, sum);
                 }
             }
         }
@@ -973,9 +1101,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * self);
                     for (uint32_t k = 0; k < rp.n; ++k) {
-                        const float mk = rp.top(k), lk = rp.sum(k);
-                        if (mk == -INFINITY && lk == lk) continue;
-                        const float hf = part_root(mk, mx), f = hf * hf;
+                        const float2 st = rp.stat(k);
+                        if (st.x == -INFINITY && st.y == st.y) continue;
+                        const float hf = part_root(st.x, mx), f = hf * hf;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const float4 x = rp.values(k, static_cast<uint32_t>(8 * c + e));
@@ -987,11 +1115,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     }
                 }
             }
-            if (stays) {
-                float4* d = reinterpret_cast<float4*>(slot + 2 * slot_pad);
+            if constexpr (MODE == kAttnShared) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    d[(8 * c + e) * slot_pad + prow] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                    staged[8 * c + e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
+                                                    __uint_as_float(v[4 * e + 3]));
+            } else if (leaves) {
+                float4* d = reinterpret_cast<float4*>(slot + 2 * kPromptRows);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    d[(8 * c + e) * kPromptRows + prow] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
                                                                      __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
             } else if (!leaves && has_row) {
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(at) * D + 32 * c);
@@ -1004,6 +1137,18 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                         o[q] = sum == 0.0f ? 0u : narrow2<BF16>(__uint_as_float(v[8 * e + 2 * q]) * inv, __uint_as_float(v[8 * e + 2 * q + 1]) * inv);
                     dst[e] = make_uint4(o[0], o[1], o[2], o[3]);
                 }
+            }
+        }
+        if constexpr (MODE == kAttnShared) {
+            // the warp's rows, one bulk store (K's, V's and the codes' memory is free: every product is done)
+            fence_proxy_async_smem();
+            __syncwarp();
+            const int32_t mine = nrows - 32 * static_cast<int32_t>(warp);
+            if (lane == 0 && mine > 0) {
+                bulk_store(p.slots + (slot_row + 32 * warp) * (D + 4), reinterpret_cast<float4*>(base) + 32 * warp * (D / 4 + 1),
+                           static_cast<uint32_t>(mine < 32 ? mine : 32) * (D + 4) * 4u);
+                bulk_commit();
+                bulk_wait_all();
             }
         }
         if (!leaves && p.lse && has_row)
@@ -1060,11 +1205,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                         a = make_float4(a.x * fs, a.y * fs, a.z * fs, a.w * fs);
                         b = make_float4(b.x * fs, b.y * fs, b.z * fs, b.w * fs);
                         for (uint32_t k = 0; k < rp.n; ++k) {
-                            const float mk = rp.top(k), lk = rp.sum(k);
-                            if (mk == -INFINITY && lk == lk) continue;
-                            const float hf = part_root(mk, M), f = hf * hf;
+                            const float2 st = rp.stat(k);
+                            if (st.x == -INFINITY && st.y == st.y) continue;
+                            const float hf = part_root(st.x, M), f = hf * hf;
                             const float4 x = rp.values(k, static_cast<uint32_t>(2 * c)), y = rp.values(k, static_cast<uint32_t>(2 * c + 1));
-                            L = __fmaf_rn(lk * hf, hf, L);
+                            L = __fmaf_rn(st.y * hf, hf, L);
                             a = make_float4(__fmaf_rn(x.x, f, a.x), __fmaf_rn(x.y, f, a.y), __fmaf_rn(x.z, f, a.z), __fmaf_rn(x.w, f, a.w));
                             b = make_float4(__fmaf_rn(y.x, f, b.x), __fmaf_rn(y.y, f, b.y), __fmaf_rn(y.z, f, b.z), __fmaf_rn(y.w, f, b.w));
                         }

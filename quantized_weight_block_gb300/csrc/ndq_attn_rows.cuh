@@ -717,31 +717,16 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                 attn_pdl_wait();
                 joins = true;
             }
+            if (write && x.own > 0) {  // join the prefix's parts
+                const int32_t i = row < nrows ? row : 0, qi = query_of(p, row0 + i);
+                RowParts<D> parts(p, (x.q0 + qi) * p.q_heads + h * p.group + row0 + i - qi * p.group);
+                if (row >= nrows) parts.n = 0;
+                parts.template join<TPR, EPT>(static_cast<uint32_t>(tid % TPR), static_cast<uint32_t>(d0), M, L, acc);
+            }
         }
         if (write && row < nrows) {
             const int32_t qi = query_of(p, row0 + row), qh = h * p.group + row0 + row - qi * p.group;
             const int64_t at = (x.q0 + qi) * p.q_heads + qh;
-            if constexpr (MODE == kAttnOwn) {
-                if (x.own > 0) {  // join the prefix's parts, in their order
-                    const RowParts<D> parts(p, at);
-                    const float top = parts.largest(M), hs = part_root(M, top), fs = hs * hs;
-                    M = top;
-                    L = L * hs * hs;
-#pragma unroll
-                    for (int e = 0; e < EPT; ++e) acc[e] *= fs;
-#pragma unroll 4
-                    for (uint32_t k = 0; k < parts.n; ++k) {
-                        const float mk = parts.top(k), lk = parts.sum(k);
-                        float v[EPT];
-                        parts.template load<EPT>(k, static_cast<uint32_t>(d0), v);
-                        if (mk == -INFINITY && lk == lk) continue;
-                        const float hf = part_root(mk, M), f = hf * hf;
-                        L = __fmaf_rn(lk * hf, hf, L);
-#pragma unroll
-                        for (int e = 0; e < EPT; ++e) acc[e] = __fmaf_rn(v[e], f, acc[e]);
-                    }
-                }
-            }
             const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : (L == L ? 0.0f : L);
             uint16_t* dst = static_cast<uint16_t*>(p.out) + at * D + d0;
 #pragma unroll

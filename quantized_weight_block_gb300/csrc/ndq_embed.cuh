@@ -8,10 +8,10 @@
 //
 // Work.  The unit is a segment of 32 chunks of one token's row (512 elements,
 // 256 of nvfp4), a chunk to a lane; warps take the segments of all tokens in
-// turn.  A warp is on its own: it copies its next segment's 16-byte lines to
-// shared memory while it decodes this one, and leaves the outputs to one bulk
-// store (lanes that store their own 32 bytes fill half sectors, which caps the
-// write rate), so that nothing waits for another warp.
+// turn.  A warp is on its own: it keeps the 16-byte lines of its next three
+// segments on their way to shared memory while it decodes this one, and leaves
+// the outputs to one bulk store (lanes that store their own 32 bytes fill half
+// sectors, which caps the write rate), so that nothing waits for another warp.
 #pragma once
 
 #include "ndq_device.cuh"
@@ -21,6 +21,7 @@ namespace ndq {
 namespace {
 
 constexpr int kEmbedWarps = 8;
+constexpr int kEmbedStages = 4;  // packed segments of a warp in shared memory
 
 template <int F>
 struct EmbedSeg {
@@ -37,7 +38,7 @@ __global__ void __launch_bounds__(kEmbedWarps * 32) k_embed(const __grid_constan
     using Sg = EmbedSeg<F>;
     constexpr int CE = Fm::CE;
     __shared__ SmemHdr H;  // the decoders' 16-entry tables
-    __shared__ __align__(16) uint8_t s_in[kEmbedWarps][2][Sg::kStage];
+    __shared__ __align__(16) uint8_t s_in[kEmbedWarps][kEmbedStages][Sg::kStage];
     __shared__ __align__(16) uint8_t s_out[kEmbedWarps][Sg::kElems * 4];
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
     if (tid < 16) {
@@ -70,27 +71,30 @@ __global__ void __launch_bounds__(kEmbedWarps * 32) k_embed(const __grid_constan
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    uint32_t u = blockIdx.x * kEmbedWarps + warp, buf = 0;
-    int64_t id = row_of(u), id_next = row_of(u + step);
-    fetch(u, id, 0);
+    uint32_t u = blockIdx.x * kEmbedWarps + warp, buf = 0, half = 0;
+    int64_t id[kEmbedStages];  // rows of this unit and the next ones
+#pragma unroll
+    for (int i = 0; i < kEmbedStages; ++i) id[i] = row_of(u + i * step);
+#pragma unroll
+    for (int i = 0; i < kEmbedStages - 1; ++i) fetch(u + i * step, id[i], i);
     Ctx x{&H, nullptr, t.divs, 0, t.blocks_per_div, p.grids, code_count(t), 0, 0};
-    for (; u < p.units; u += step, buf ^= 1u) {
-        const int64_t id_after = row_of(u + 2u * step);
-        fetch(u + step, id_next, buf ^ 1u);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    for (; u < p.units; u += step, buf = (buf + 1) % kEmbedStages) {
+        const int64_t id_after = row_of(u + kEmbedStages * step);
+        fetch(u + (kEmbedStages - 1) * step, id[kEmbedStages - 1], (buf + kEmbedStages - 1) % kEmbedStages);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kEmbedStages - 1) : "memory");
         __syncwarp();
         const uint32_t seg = u % p.segs;
         const uint64_t e0 = static_cast<uint64_t>(seg) * Sg::kElems, e = e0 + lane * CE;
         const bool ok = e < p.K;
         float v[CE];
-        if (ok && id >= 0) {
-            x.row0 = static_cast<uint64_t>(id);
+        if (ok && id[0] >= 0) {
+            x.row0 = static_cast<uint64_t>(id[0]);
             x.col0 = e0;
-            x.block0 = static_cast<uint64_t>(id) * p.bpr + seg * (Sg::kElems / Fm::B);
+            x.block0 = static_cast<uint64_t>(id[0]) * p.bpr + seg * (Sg::kElems / Fm::B);
             if (p.aligned)
                 Fm::template chunk<false>(s_in[warp][buf], 0u, lane, v, x);
             else
-                Fm::template chunk<true>(s_in[warp][buf], static_cast<uint32_t>(reinterpret_cast<uintptr_t>(source(u, id)) & 15u),
+                Fm::template chunk<true>(s_in[warp][buf], static_cast<uint32_t>(reinterpret_cast<uintptr_t>(source(u, id[0])) & 15u),
                                          lane, v, x);
 #pragma unroll
             for (int i = 0; i < CE; ++i) v[i] = __fmul_rn(v[i], p.scale);
@@ -100,9 +104,14 @@ __global__ void __launch_bounds__(kEmbedWarps * 32) k_embed(const __grid_constan
         }
         const uint64_t at = static_cast<uint64_t>(u / p.segs) * p.y_stride;
         if (p.yvec) {
-            if (lane == 0) bulk_wait_read<0>();  // the last bulk store has read the buffer
+            // the last bulk store from here has read it (16-bit outputs fill the halves by turns)
+            if (lane == 0) {
+                if (p.out == KO_F32) bulk_wait_read<0>();
+                else bulk_wait_read<1>();
+            }
             __syncwarp();
-            uint4* o = reinterpret_cast<uint4*>(s_out[warp] + lane * CE * (p.out == KO_F32 ? 4 : 2));
+            uint8_t* so = s_out[warp] + half;
+            uint4* o = reinterpret_cast<uint4*>(so + lane * CE * (p.out == KO_F32 ? 4 : 2));
             if (p.out == KO_F32) {
 #pragma unroll
                 for (int i = 0; i < CE / 4; ++i)
@@ -121,18 +130,20 @@ __global__ void __launch_bounds__(kEmbedWarps * 32) k_embed(const __grid_constan
             if (lane == 0) {
                 const uint32_t el = p.out == KO_F32 ? 4u : 2u;
                 const uint64_t left = p.K - e0;
-                bulk_store(static_cast<uint8_t*>(p.y) + (at + e0) * el, s_out[warp],
+                bulk_store(static_cast<uint8_t*>(p.y) + (at + e0) * el, so,
                            (left < Sg::kElems ? static_cast<uint32_t>(left) : Sg::kElems) * el);
                 bulk_commit();
             }
+            if (p.out != KO_F32) half ^= Sg::kElems * 2;
         } else if (ok) {
             if (p.out == KO_F32) store_chunk<KO_F32, CE>(p.y, at + e, v, false);
             else if (p.out == KO_BF16) store_chunk<KO_BF16, CE>(p.y, at + e, v, false);
             else store_chunk<KO_F16, CE>(p.y, at + e, v, false);
         }
         __syncwarp();  // every lane has read the packed segment
-        id = id_next;
-        id_next = id_after;
+#pragma unroll
+        for (int i = 0; i + 1 < kEmbedStages; ++i) id[i] = id[i + 1];
+        id[kEmbedStages - 1] = id_after;
     }
     if (lane == 0) bulk_wait_all();
 }

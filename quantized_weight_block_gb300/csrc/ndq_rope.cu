@@ -37,7 +37,7 @@ constexpr int kRopeMaxDim = 256;
 
 struct RopeShared {
     uint64_t turn[kRopeMaxDim / 2];  // turns per position, in units of 2^-64
-    float w[2][kRopeMaxDim];
+    alignas(16) float w[2][kRopeMaxDim];
 };
 
 // inv_freq / (2 pi) modulo 1 in units of 2^-64.  For magnitudes up to 1 the
@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant_
     constexpr int G = 32 / L;               // heads at a time
     constexpr int R = IN == 0 ? 2 : 1;      // 16-byte words of eight inputs
     constexpr int C = (8 + G - 1) / G;      // cosines that a lane computes
+    constexpr int N = IN == 0 ? 1 : 2;      // rounds of heads whose loads are under way
     __shared__ RopeShared S;
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
     const int g = static_cast<int>(lane) / L, j = static_cast<int>(lane) % L;
@@ -142,32 +143,25 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant_
         // heads [h0, h1) of the queries, then of the keys
         auto heads = [&](const void* x, int64_t x_stride, void* y, int64_t y_stride, int h0, int h1, const float* w, bool norm) {
             if (h0 >= h1) return;
-            float wa[8], wb[8];
-            if (norm) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    wa[e] = w[8 * pa + e];
-                    wb[e] = w[8 * pb + e];
-                }
-            }
             const int64_t xa = static_cast<int64_t>(t) * x_stride, ya = static_cast<int64_t>(t) * y_stride;
-            uint4 ra[R], rb[R];
-            auto load = [&](int h) {
+            uint4 ra[N][R], rb[N][R];
+            auto load = [&](int h, int i) {
                 const bool in = live && h < h1;
 #pragma unroll
-                for (int r = 0; r < R; ++r) ra[r] = rb[r] = make_uint4(0u, 0u, 0u, 0u);
+                for (int r = 0; r < R; ++r) ra[i][r] = rb[i][r] = make_uint4(0u, 0u, 0u, 0u);
                 if (in) {
-                    load8<IN>(x, xa + static_cast<int64_t>(h) * D + 8 * pa, ra);
-                    load8<IN>(x, xa + static_cast<int64_t>(h) * D + 8 * pb, rb);
+                    load8<IN>(x, xa + static_cast<int64_t>(h) * D + 8 * pa, ra[i]);
+                    load8<IN>(x, xa + static_cast<int64_t>(h) * D + 8 * pb, rb[i]);
                 }
             };
-            load(h0 + g);
-            for (int hb = h0; hb < h1; hb += G) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) load(h0 + i * G + g, i);
+            auto round = [&](int hb, int i) {
                 const int h = hb + g;
                 float a[8], b[8];
-                widen8<IN>(ra, a);
-                widen8<IN>(rb, b);
-                if (hb + G < h1) load(h + G);
+                widen8<IN>(ra[i], a);
+                widen8<IN>(rb[i], b);
+                if (hb + N * G < h1) load(h + N * G, i);
                 if (norm) {
                     float s2[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -210,10 +204,19 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant_
                         for (int d = 1; d < L; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                     }
                     const float r = rsqrtf(__fmaf_rn(sum, inv_dim, eps));
+                    const float4* wa = reinterpret_cast<const float4*>(w + 8 * pa);
+                    const float4* wb = reinterpret_cast<const float4*>(w + 8 * pb);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        a[e] = a[e] * r * wa[e];
-                        b[e] = b[e] * r * wb[e];
+                    for (int e = 0; e < 2; ++e) {
+                        const float4 f = wa[e], g4 = wb[e];
+                        a[4 * e] = a[4 * e] * r * f.x;
+                        a[4 * e + 1] = a[4 * e + 1] * r * f.y;
+                        a[4 * e + 2] = a[4 * e + 2] * r * f.z;
+                        a[4 * e + 3] = a[4 * e + 3] * r * f.w;
+                        b[4 * e] = b[4 * e] * r * g4.x;
+                        b[4 * e + 1] = b[4 * e + 1] * r * g4.y;
+                        b[4 * e + 2] = b[4 * e + 2] * r * g4.z;
+                        b[4 * e + 3] = b[4 * e + 3] * r * g4.w;
                     }
                 }
                 if (turned) {
@@ -242,6 +245,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant_
                     *reinterpret_cast<uint4*>(dst + 8 * pb) =
                         make_uint4(narrow2<BF16>(b[0], b[1]), narrow2<BF16>(b[2], b[3]), narrow2<BF16>(b[4], b[5]), narrow2<BF16>(b[6], b[7]));
                 }
+            };
+            for (int hb = h0; hb < h1; hb += N * G) {
+                round(hb, 0);
+                if (N == 2 && hb + G < h1) round(hb + G, N - 1);
             }
         };
         const int H = p.q_heads + p.k_heads;

@@ -110,22 +110,23 @@ int launch_attention(AttnParams p, int head_dim, bool e4m3, bool bf16, void* str
 // and every request's own tokens, whose kernels join the two.
 //
 // The prefix part is laid out in slots: a unit (256 rows of a group and cache
-// head at most) leaves one slot for each CTA that shares its tokens, a slot
-// holding `pad` rows (its rows, rounded up to four): pad maxima, pad sums,
-// then head positions by fours, [D / 4][pad][4].  A row finds its slots by its
-// record, (first slot's offset in rows, pad, slots, row in the slot).
+// head at most) leaves one slot for each CTA that shares its tokens, of one
+// row of D + 4 floats for each of its own (values, maximum, sum).  A row finds
+// its slots by its record: the first slot's offset in rows, the rows of a
+// slot, the slots, the row in the slot.
 constexpr int kPrefixMaxParts = 64;   // CTAs of a unit at most
+constexpr uint64_t kPrefixMinTiles = 2;  // tiles of 128 tokens of a CTA at least
 constexpr int kPrefixMaxExtra = 192;  // CTAs beyond one per unit at most (no more than SMs)
-constexpr int64_t prefix_slot_rows(int64_t n_tokens, int64_t q_heads, int64_t kv_heads) {
-    return n_tokens * (q_heads + 3 * kv_heads) + static_cast<int64_t>(kPrefixMaxExtra) * kPromptRows;
+constexpr int64_t prefix_slot_rows(int64_t n_tokens, int64_t q_heads) {
+    return n_tokens * q_heads + static_cast<int64_t>(kPrefixMaxExtra) * kPromptRows;
 }
 constexpr size_t prefix_records_at(int head_dim) { return (attn_workspace_bytes(head_dim) + 255) / 256 * 256; }
 constexpr size_t prefix_slots_at(int head_dim, int64_t n_tokens, int64_t q_heads) {
     return (prefix_records_at(head_dim) + 16 * static_cast<size_t>(n_tokens * q_heads) + 255) / 256 * 256;
 }
-constexpr size_t prefix_workspace_bytes(int head_dim, int64_t n_tokens, int64_t q_heads, int64_t kv_heads) {
+constexpr size_t prefix_workspace_bytes(int head_dim, int64_t n_tokens, int64_t q_heads) {
     return prefix_slots_at(head_dim, n_tokens, q_heads) +
-           4 * static_cast<size_t>(head_dim + 2) * static_cast<size_t>(prefix_slot_rows(n_tokens, q_heads, kv_heads));
+           4 * static_cast<size_t>(head_dim + 4) * static_cast<size_t>(prefix_slot_rows(n_tokens, q_heads));
 }
 struct PrefixParams : AttnParams {
     const int32_t* group_start;
