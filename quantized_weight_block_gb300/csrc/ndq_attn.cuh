@@ -209,7 +209,7 @@ struct RowParts {
         rows = x.y;
         n = x.z;
         // (whatever a record holds, no read leaves the slots)
-        if (rows > kPromptRows || x.w >= rows || n > kPrefixMaxParts || x.x + static_cast<uint64_t>(n) * rows > static_cast<uint64_t>(p.slot_rows)) n = 0;
+        if (rows > kPromptRows || x.w >= rows || n > 2 * kPrefixMaxParts || x.x + static_cast<uint64_t>(n) * rows > static_cast<uint64_t>(p.slot_rows)) n = 0;
         first = p.slots + (static_cast<uint64_t>(x.x) + x.w) * (D + 4);
     }
     __device__ __forceinline__ const float* part(uint32_t k) const { return first + static_cast<uint64_t>(k) * rows * (D + 4); }
@@ -217,72 +217,6 @@ struct RowParts {
     __device__ __forceinline__ float2 stat(uint32_t k) const { return __ldcg(reinterpret_cast<const float2*>(part(k) + D)); }
     // head positions 4 c .. 4 c + 3, by a thread that reads the ones beside them, too
     __device__ __forceinline__ float4 values(uint32_t k, uint32_t c) const { return reinterpret_cast<const float4*>(part(k))[c]; }
-    // N (2, or a multiple of 4) of them from d on
-    template <int N>
-    __device__ __forceinline__ void load(uint32_t k, uint32_t d, float* v) const {
-        if constexpr (N == 2) {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(part(k) + d));
-            v[0] = x.x;
-            v[1] = x.y;
-        } else {
-#pragma unroll
-            for (int c = 0; c < N / 4; ++c) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(part(k) + d) + c);
-                v[4 * c] = x.x;
-                v[4 * c + 1] = x.y;
-                v[4 * c + 2] = x.z;
-                v[4 * c + 3] = x.w;
-            }
-        }
-    }
-    // The row's own maximum, sum and values from d on joined with the parts, by
-    // the LANES lanes that hold its values: each takes the weights of every
-    // LANES-th part, and all take the values part by part, several parts' loads
-    // at a time.  Every lane of the warp calls it.
-    template <int LANES, int N>
-    __device__ __forceinline__ void join(uint32_t lane, uint32_t d, float& M, float& L, float* acc) const {
-        float top = M;
-        for (uint32_t k = lane; k < n; k += LANES) top = fmaxf(top, stat(k).x);
-#pragma unroll
-        for (int e = 1; e < LANES; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
-        constexpr uint32_t B = N > 4 ? 4 : 8;
-        const float hs = part_root(M, top), fs = hs * hs;
-        M = top;
-#pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] *= fs;
-        float more = 0.0f;  // this lane's parts' sums
-        const uint32_t most = __reduce_max_sync(0xffffffffu, n);
-        for (uint32_t k0 = 0; k0 < most; k0 += LANES) {
-            float f = -1.0f;  // (left out: it saw nothing, or is none)
-            if (k0 + lane < n) {
-                const float2 x = stat(k0 + lane);
-                if (x.x != -INFINITY || x.y != x.y) {
-                    const float hf = part_root(x.x, top);
-                    f = hf * hf;
-                    more = __fmaf_rn(x.y * hf, hf, more);
-                }
-            }
-            const uint32_t here = most - k0 < LANES ? most - k0 : LANES;
-            for (uint32_t j = 0; j < here; j += B) {
-                float v[B][N], w[B];
-#pragma unroll
-                for (uint32_t i = 0; i < B; ++i) {
-                    w[i] = __shfl_sync(0xffffffffu, f, static_cast<int>((j + i) & (LANES - 1)), LANES);
-                    if (j + i >= here) w[i] = -1.0f;
-                    if (w[i] >= 0.0f) load<N>(k0 + j + i, d, v[i]);
-                }
-#pragma unroll
-                for (uint32_t i = 0; i < B; ++i)
-                    if (w[i] >= 0.0f) {
-#pragma unroll
-                        for (int e = 0; e < N; ++e) acc[e] = __fmaf_rn(v[i][e], w[i], acc[e]);
-                    }
-            }
-        }
-#pragma unroll
-        for (int e = 1; e < LANES; e <<= 1) more += __shfl_xor_sync(0xffffffffu, more, e);
-        L = __fmaf_rn(L * hs, hs, more);
-    }
     __device__ __forceinline__ float largest(float M) const {
 #pragma unroll 4
         for (uint32_t k = 0; k < n; ++k) M = fmaxf(M, stat(k).x);

@@ -1,5 +1,5 @@
 // ndq_attn_prefix.cu -- attention of requests that share prefixes: the kernel of
-// the shared prefixes, and the launcher of all three.
+// the shared prefixes, and the launcher of all.
 #include "ndq_attn_prompt.cuh"
 
 namespace ndq {
@@ -43,7 +43,8 @@ int launch_attention_prefix(PrefixParams p, int head_dim, bool e4m3, bool bf16, 
         p.counters = counters;
         p.parts = parts;
     }
-    return launch_prefix_own_rows(p, head_dim, e4m3, bf16, dev, stream);
+    if (const int rc = launch_prefix_own_rows(p, head_dim, e4m3, bf16, dev, stream)) return rc;
+    return launch_prefix_join(p, head_dim, bf16, stream);
 }
 
 }  // namespace ndq

@@ -1,5 +1,5 @@
 // ndq_attn_prefix_rows.cu -- launcher of the few-row kernel over requests' own
-// tokens, joined with the prefixes that they share.
+// tokens, whose parts are joined with those of the prefixes that they share.
 #include "ndq_attn_rows.cuh"
 
 namespace ndq {

@@ -271,6 +271,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     const uint32_t split = blockIdx.x % static_cast<uint32_t>(p.splits);
     int64_t slot_row = 0;  // (kAttnShared) this CTA's slot, and the parts of its unit
     uint32_t parts = 1, part = 0;
+    // (kAttnShared) At most 128 rows: both row tiles are these rows, and take
+    // the tokens' tiles by turns, each leaving a part.  (One row tile alone
+    // waits for its own chain of products and softmax.)
+    bool dual = false;
     if constexpr (MODE == kAttnShared) {
         // Every CTA counts the groups' units and tiles, from these how many
         // tiles a CTA is to take, and then finds its unit and part.
@@ -287,7 +291,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             chunk = chunk < kPrefixMinTiles ? kPrefixMinTiles : chunk;
         };
         auto ctas_of = [&](const SharedUnits& x) { return static_cast<uint64_t>(x.units * parts_of(x.tiles)); };
-        auto slots_of = [&](const SharedUnits& x) { return static_cast<uint64_t>(x.rows * p.c.heads * parts_of(x.tiles)); };
+        auto slots_of = [&](const SharedUnits& x) {  // (few rows leave two rows each, see `dual`)
+            const int64_t last = x.rows % kPromptRows;
+            return static_cast<uint64_t>((x.rows + (last <= kPromptRows / 2 ? last : 0)) * p.c.heads * parts_of(x.tiles));
+        };
         auto mine = [&](int64_t g, uint64_t c, uint64_t n, int64_t parts_here) {
             S.r = g;
             S.base = static_cast<int64_t>(blockIdx.x - c);
@@ -305,7 +312,22 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 work += __shfl_xor_sync(0xffffffffu, work, d);
             }
             units = __shfl_sync(0xffffffffu, units, 0);
-            set_chunk(units, __shfl_sync(0xffffffffu, work, 0));
+            work = __shfl_sync(0xffffffffu, work, 0);
+            set_chunk(units, work);
+            // the smallest chunk whose CTAs still are one wave
+            const uint64_t sms = static_cast<uint64_t>(p.sms);
+            if (units < sms && (work >> 31) == 0) {
+                uint32_t lo = static_cast<uint32_t>(work) / static_cast<uint32_t>(sms), hi = static_cast<uint32_t>(chunk);  // lo: too small, hi: will do
+                lo = lo < kPrefixMinTiles - 1 ? static_cast<uint32_t>(kPrefixMinTiles) - 1 : lo;
+                while (lo + 1 < hi) {
+                    const uint32_t mid = (lo + hi) >> 1;
+                    chunk = mid;
+                    const uint64_t c = x.units > 0 ? ctas_of(x) : 0;
+                    if (__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(c < sms ? c : sms + 1)) <= sms) hi = mid;
+                    else lo = mid;
+                }
+                chunk = hi;
+            }
             const uint64_t ctas = x.units > 0 ? ctas_of(x) : 0, rows = x.units > 0 ? slots_of(x) : 0;
             uint64_t ci = ctas, ri = rows;
 #pragma unroll
@@ -438,7 +460,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         row0 = static_cast<int32_t>(tile) * kPromptRows;
         const int64_t rows_left = x.rows - row0;
         nrows = static_cast<int32_t>(rows_left < kPromptRows ? rows_left : kPromptRows);
-        slot_row = S.slot + (tile * kPromptRows * p.c.heads + static_cast<int64_t>(h) * nrows) * parts + static_cast<int64_t>(part) * nrows;
+        dual = nrows <= kPromptRows / 2;
+        const int64_t left = dual ? 2 * nrows : nrows;  // rows that a CTA of this unit leaves
+        slot_row = S.slot + (tile * kPromptRows * p.c.heads + h * left) * parts + part * left;
     } else {
         uint64_t left = unit - static_cast<uint64_t>(S.base);
         int64_t tiles = prompt_tiles(p, r, q0, n, pos0);
@@ -453,7 +477,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         nrows = rows_left < kPromptRows ? rows_left : kPromptRows;
         if constexpr (MODE == kAttnOwn) own = shared_tokens(p, r);
     }
-    const int32_t nact = nrows > 128 ? 2 : 1;  // row tiles in use
+    const int32_t nact = nrows > 128 || dual ? 2 : 1;  // row tiles in use
     // tokens that some row / every row of the CTA sees
     const int32_t first_pos = pos0 + row0 / p.group, last_pos = pos0 + (row0 + nrows - 1) / p.group;
     const int32_t most = table_tokens(p);
@@ -493,7 +517,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         // own row would fetch every line by sixteenths); whose they are and
         // where they sit meanwhile.
         constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per load
-        const int32_t i = static_cast<int32_t>(wg * 128u + wrow);
+        const int32_t i = static_cast<int32_t>(dual ? wrow : wg * 128u + wrow);
         const int32_t mine = row0 + (i < nrows ? i : 0);
         const int32_t qi = mine / p.group, qh = h * p.group + mine % p.group;
         at = static_cast<int32_t>((q0 + qi) * p.q_heads) + qh;
@@ -802,35 +826,58 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     mma_bf16(tmem + 128u * i, a0 + (((s >> 2) * kAtom + (s & 3u) * 32u) >> 4),
                              b0 + (((s >> 2) * kAtom + (s & 3u) * 32u) >> 4), kIdQ, s > 0 ? 1u : 0u);
                 mma_commit(&S.sfull[i]);
-                if (i == nact - 1) mma_commit(&S.kfree[j & 1]);
+                if (i == nact - 1 || dual) mma_commit(&S.kfree[j & 1]);
             }
             __syncwarp();
             ++scored[i];
         };
-        if (nt > 0) {
+        auto values = [&](int32_t i, int32_t j) {  // O_i += P_i V_j
+            const uint64_t b0 = dv + static_cast<uint32_t>(j & 1) * (kTile >> 4);
+            const bool more = issued[i] > 0;
+            if (elect_one()) {
+#pragma unroll
+                for (uint32_t s = 0; s < kPrTokens / 16; ++s)
+                    mma_ts(tmem + kO + D * i, tmem + 128u * i + 8u * s, b0 + s * (2048u >> 4), kIdP, more || s > 0 ? 1u : 0u);
+                mma_commit(&S.odone[i]);
+                if (i == nact - 1 || dual) mma_commit(&S.vfree[j & 1]);
+            }
+            __syncwarp();
+            ++issued[i];
+        };
+        if (MODE == kAttnShared && dual) {  // tile j is row tile j & 1's, in the stage j & 1 of K and V
+            for (int32_t j = 0; j < 2 && j < nt && ok; ++j) {
+                ok = wait(&S.kfull[j], 0u);
+                if (!ok) break;
+                tc_fence_after();
+                scores(j, j);
+            }
+            for (int32_t j = 0; j < nt && ok; ++j) {
+                const uint32_t turn = static_cast<uint32_t>((j >> 1) & 1);
+                ok = wait(&S.vfull[j & 1], turn) && wait(&S.pfull[j & 1], turn);
+                if (!ok) break;
+                tc_fence_after();
+                values(j & 1, j);
+                if (j + 2 < nt) {
+                    ok = wait(&S.kfull[j & 1], turn ^ 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(j & 1, j + 2);
+                }
+            }
+        } else if (nt > 0) {
             ok = wait(&S.kfull[0], 0u);
             if (ok) {
                 tc_fence_after();
                 for (int32_t i = 0; i < nact; ++i) scores(i, 0);
             }
         }
-        for (int32_t j = 0; j < nt && ok; ++j) {
+        for (int32_t j = 0; j < nt && ok && !dual; ++j) {
             ok = wait(&S.vfull[j & 1], static_cast<uint32_t>((j >> 1) & 1));
             for (int32_t i = 0; i < nact && ok; ++i) {
                 ok = wait(&S.pfull[i], static_cast<uint32_t>(j & 1));
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t b0 = dv + static_cast<uint32_t>(j & 1) * (kTile >> 4);
-                if (elect_one()) {
-#pragma unroll
-                    for (uint32_t s = 0; s < kPrTokens / 16; ++s)
-                        mma_ts(tmem + kO + D * i, tmem + 128u * i + 8u * s, b0 + s * (2048u >> 4), kIdP,
-                               j > 0 || s > 0 ? 1u : 0u);
-                    mma_commit(&S.odone[i]);
-                    if (i == nact - 1) mma_commit(&S.vfree[j & 1]);
-                }
-                __syncwarp();
-                ++issued[i];
+                values(i, j);
                 if (j + 1 < nt) {
                     if (i == 0) {
                         ok = wait(&S.kfull[(j + 1) & 1], static_cast<uint32_t>(((j + 1) >> 1) & 1));
@@ -872,6 +919,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         }
         float ms = 0.0f;
         bool ok = true;
+        const int32_t turns = dual ? (nt + 1 - static_cast<int32_t>(wg)) >> 1 : nt;  // tiles of this row tile
         uint32_t w[kPrTokens / 2];  // the row's weights of the tile, in pairs
         // The weights relative to ms (and less), their sum and the largest exponent.
         auto weigh = [&](auto mask, auto again, bool read, float less, const float4* cst, int32_t tb, float& ts, float& top) {
@@ -948,11 +996,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         // Pass -1 takes weights of nothing, while the first codes are on their
         // way: it brings the code of the loop, 9 KB, to the SM, which cost 14000
         // cycles of the first tile (33000 on all SMs at once).
-        for (int32_t j = MODE != kAttnAll && nt > 0 ? -1 : 0; j < nt; ++j) {
+        for (int32_t n = MODE != kAttnAll && nt > 0 ? -1 : 0; n < turns; ++n) {
+            const int32_t j = MODE == kAttnShared && dual && n >= 0 ? 2 * n + static_cast<int32_t>(wg) : n;  // the tile
             bool masked = false;
             int32_t tb = 0;
-            if (MODE == kAttnAll || j >= 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.sfull[wg], static_cast<uint32_t>(j & 1), p.waits.limit_ns));
+            if (MODE == kAttnAll || n >= 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.sfull[wg], static_cast<uint32_t>(n & 1), p.waits.limit_ns));
                 if (!ok) break;
                 tc_fence_after();
                 tb = tok0 + j * kPrTokens;
@@ -962,11 +1011,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     if (mx == -INFINITY) ms = top > -INFINITY && top < INFINITY ? top : 0.0f;
                 }
             }
-            const float4* cst = S.cst[MODE == kAttnAll || j >= 0 ? j % kPrCst : 0];
+            const float4* cst = S.cst[MODE == kAttnAll || n >= 0 ? j % kPrCst : 0];
             float ts, top;
-            if (masked) weigh(std::true_type{}, std::false_type{}, j >= 0, 0.0f, cst, tb, ts, top);
-            else weigh(std::false_type{}, std::false_type{}, j >= 0, 0.0f, cst, tb, ts, top);
-            if (MODE != kAttnAll && j < 0) continue;
+            if (masked) weigh(std::true_type{}, std::false_type{}, n >= 0, 0.0f, cst, tb, ts, top);
+            else weigh(std::false_type{}, std::false_type{}, n >= 0, 0.0f, cst, tb, ts, top);
+            if (MODE != kAttnAll && n < 0) continue;
             bool grow = top > (mx == -INFINITY ? -INFINITY : 8.0f);
             if constexpr (MODE != kAttnAll) {
                 if (mx == -INFINITY && top >= -8.0f && top <= 8.0f) {  // ms is the maximum, but for roundings
@@ -977,8 +1026,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             // a row passed its maximum by 8: always in the first tile that it sees (or where that is not known before), rarely later
             if (__any_sync(0xffffffffu, grow)) {
                 const float ah = !grow ? 1.0f : (mx == -INFINITY ? 0.0f : exp2_fast(-0.5f * top)), al = ah * ah;
-                if (j > 0) {  // O moves to the new maximum once the product before this one is done with it
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((j - 1) & 1), p.waits.limit_ns));
+                if (n > 0) {  // O moves to the new maximum once the product before this one is done with it
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((n - 1) & 1), p.waits.limit_ns));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -1006,8 +1055,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.pfull[wg]);
         }
-        if (ok && nt > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((nt - 1) & 1), p.waits.limit_ns));
+        if (ok && turns > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.odone[wg], static_cast<uint32_t>((turns - 1) & 1), p.waits.limit_ns));
             tc_fence_after();
         }
         if (!ok && lane == 0) atomicOr(&S.fault, 1u);
@@ -1050,8 +1099,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         float4* staged = reinterpret_cast<float4*>(base) + prow * (D / 4 + 1);  // (kAttnShared) the row on its way to its slot
         if constexpr (MODE == kAttnShared) {
             staged[D / 4] = make_float4(mx, sum, 0.0f, 0.0f);
-            if (part == 0 && has_row)
-                static_cast<uint4*>(p.records)[at] = make_uint4(static_cast<uint32_t>(slot_row), static_cast<uint32_t>(nrows), parts, prow);
+            if (part == 0 && has_row && !(dual && wg == 1))
+                static_cast<uint4*>(p.records)[at] =
+                    make_uint4(static_cast<uint32_t>(slot_row), static_cast<uint32_t>(nrows), dual ? 2 * parts : parts, prow);
         } else if (leaves) {
             slot[prow] = mx;
             slot[kPromptRows + prow] = sum;
@@ -1079,7 +1129,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
-            if (nt > 0) {
+            if (nt > (dual ? static_cast<int32_t>(wg) : 0)) {
                 tmem_ld32(tO + 32 * c, v);
                 tmem_wait_ld32(v);
             } else {
@@ -1143,9 +1193,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             // the warp's rows, one bulk store (K's, V's and the codes' memory is free: every product is done)
             fence_proxy_async_smem();
             __syncwarp();
-            const int32_t mine = nrows - 32 * static_cast<int32_t>(warp);
+            const uint32_t first = 32 * (dual ? warp & 3u : warp);  // the first of them among the unit's rows
+            const int32_t mine = nrows - static_cast<int32_t>(first);
             if (lane == 0 && mine > 0) {
-                bulk_store(p.slots + (slot_row + 32 * warp) * (D + 4), reinterpret_cast<float4*>(base) + 32 * warp * (D / 4 + 1),
+                bulk_store(p.slots + (slot_row + (dual ? wg * nrows : 0) + first) * (D + 4), reinterpret_cast<float4*>(base) + 32 * warp * (D / 4 + 1),
                            static_cast<uint32_t>(mine < 32 ? mine : 32) * (D + 4) * 4u);
                 bulk_commit();
                 bulk_wait_all();

@@ -92,6 +92,7 @@ struct Req {
     int32_t units; // units of one row tile (at least one, so that empty rows are written)
     int32_t tiles; // row tiles per cache head
     int32_t own;   // its first token that is not of a shared prefix (0 in kAttnAll)
+    int32_t tokens;  // from lo on
 };
 
 // The query of a row: the group is a power of two more often than not.
@@ -113,9 +114,35 @@ __device__ __forceinline__ Req request(const typename AttnArgs<MODE>::type& p, i
         x.lo = first > 0 ? (first < most ? first & ~(kRowTile - 1) : most) : 0;
     }
     if constexpr (MODE == kAttnOwn) x.lo = x.lo > x.own ? x.lo : x.own;
+    x.tokens = end > x.lo ? end - x.lo : 0;
     x.units = end > x.lo ? (end - x.lo + kRowUnit - 1) / kRowUnit : 1;
     x.tiles = (x.n * p.group + ROWS - 1) / ROWS;
     return x;
+}
+
+// (kAttnOwn) Parts that a row of the request leaves.
+__device__ __forceinline__ int32_t own_parts(const Req& x, int32_t chunk) { return x.tokens > chunk ? (x.tokens - 1) / chunk + 1 : 1; }
+constexpr int32_t kOwnMinTokens = 256;
+
+// The sum over the block's threads before this one, and of all of them.
+__device__ __forceinline__ uint64_t rows_scan(uint64_t mine, uint64_t* warps, uint64_t& total) {
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    uint64_t incl = mine;
+#pragma unroll
+    for (uint32_t d = 1; d < 32; d <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    if (lane == 31u) warps[warp] = incl;
+    __syncthreads();
+    uint64_t before = incl - mine;
+    total = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kRowWarps; ++w) {
+        if (w < warp) before += warps[w];
+        total += warps[w];
+    }
+    return before;
 }
 
 // NT: n-tiles of 8 rows.  Two CTAs on an SM where the accumulators (NT D / 8
@@ -147,6 +174,8 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
     constexpr uint64_t kSlot = NDQ_ROWS_SLOT(D);
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ uint64_t s_sum[kRowWarps];
+    __shared__ uint64_t s_sum2[MODE == kAttnOwn ? kRowWarps : 1];
+    __shared__ uint64_t s_units[MODE == kAttnOwn ? kRowThreads : 1], s_rows[MODE == kAttnOwn ? kRowThreads : 1];  // before each thread's requests
     __shared__ int64_t s_r, s_base;
     __shared__ float s_m[kRowWarps][kRows], s_l[kRowWarps][kRows];
     __shared__ uint32_t s_last;
@@ -154,12 +183,57 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
     const int bl = p.c.bs_log2;
 
+    constexpr int32_t kStep = MODE == kAttnOwn ? kRowPair : kRowUnit;  // from one of a warp's pairs of tiles to the next
     if (lane < ST) mbar_init(&s_bar[warp][lane], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
     // this CTA's share of the units: the units of requests 0, 1, ... end to end
     uint64_t total = 0, base = 0, u = 0, u_end = 0, ctas = 0;  // base: first unit of request r
     int64_t r = 0;
+    // (kAttnOwn) A unit is what one warp takes of a row tile, `chunk` tokens,
+    // and the warps take the units in turn.
+    int64_t per = 0;
+    int32_t chunk = kRowPair;
+    if constexpr (MODE == kAttnOwn) {
+        attn_pdl_launch();  // (the join's CTAs find their rows meanwhile)
+        // all requests' row tiles and tokens, from them the chunk, then every
+        // request's units and rows of parts; a thread sums up `per` requests
+        per = (p.n_req + kRowThreads - 1) / kRowThreads;
+        uint64_t tiles = 0, work = 0, all_tiles = 0, all_work = 0;
+        for (int64_t i = 0; i < per; ++i) {
+            const int64_t q = tid * per + i;
+            if (q < p.n_req) {
+                const Req x = request<kRows, MODE>(p, q);
+                const uint64_t n = static_cast<uint64_t>(x.tiles) * p.c.heads;
+                tiles += n;
+                work += n * static_cast<uint32_t>(x.tokens);
+            }
+        }
+        rows_scan(tiles, s_sum, all_tiles);
+        rows_scan(work, s_sum2, all_work);
+        const uint64_t warps = static_cast<uint64_t>(gridDim.x) * kRowWarps;
+        const uint64_t spare = all_tiles + warps / 4 < warps ? warps - all_tiles : warps / 4;  // units beyond one a row tile at most
+        uint64_t c = udiv(all_work, spare) + 1;
+        c = (c + kRowPair - 1) / kRowPair * kRowPair;
+        chunk = c < kOwnMinTokens ? kOwnMinTokens : (c > (1 << 30) ? (1 << 30) : static_cast<int32_t>(c));
+        uint64_t units = 0, rows = 0, all_rows = 0;
+        for (int64_t i = 0; i < per; ++i) {
+            const int64_t q = tid * per + i;
+            if (q < p.n_req) {
+                const Req x = request<kRows, MODE>(p, q);
+                const uint64_t n = static_cast<uint32_t>(own_parts(x, chunk));
+                units += static_cast<uint64_t>(x.tiles) * p.c.heads * n;
+                rows += static_cast<uint64_t>(x.n) * p.q_heads * n;
+            }
+        }
+        __syncthreads();  // (the sums above are read)
+        s_units[tid] = rows_scan(units, s_sum, total);
+        s_rows[tid] = rows_scan(rows, s_sum2, all_rows);
+        __syncthreads();
+        if (all_rows > static_cast<uint64_t>(p.own_rows)) total = 0;  // (never)
+        u = static_cast<uint64_t>(blockIdx.x) * kRowWarps + warp;
+        u_end = total;
+    } else {
     auto share = [&]() {  // false: none
         ctas = gridDim.x < total ? gridDim.x : total;
         if (blockIdx.x >= ctas) return false;
@@ -226,17 +300,46 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         }
     }
     if (!some) {
-        if (MODE == kAttnOwn || p.prompt_rows > 0) attn_pdl_wait();
+        if (p.prompt_rows > 0) attn_pdl_wait();
         return;
     }
-    bool joins = false;  // (kAttnOwn) the prefix's parts are there
+    }
 
     const uint32_t my_ring = smem_u32(ring) + warp * ST * Sm::kStage;
     // the ring goes on from segment to segment: slot and phase of the next copy and of the next to be read
     uint32_t put = 0, get = 0, get_phase = 0, flying = 0;
     bool ok = true;  // false once a wait ran out: nothing more is copied or read
     while (u < u_end) {
-        const Req x = request<kRows, MODE>(p, r);
+        Req x;
+        int32_t ca = 0, cb = 0, h, j;
+        uint64_t own_row = 0;  // (kAttnOwn) the first row of the request's parts
+        int32_t own_n = 1;     // its parts of a row
+        if constexpr (MODE == kAttnOwn) {
+            // the last thread whose requests start at u or before, then the request among them
+            int32_t lo = 0, hi = kRowThreads;
+            while (hi - lo > 1) {
+                const int32_t m = (lo + hi) >> 1;
+                if (s_units[m] <= u) lo = m;
+                else hi = m;
+            }
+            uint64_t first = s_units[lo];
+            own_row = s_rows[lo];
+            r = lo * per;
+            for (;;) {
+                x = request<kRows, MODE>(p, r);
+                own_n = own_parts(x, chunk);
+                const uint64_t n = static_cast<uint64_t>(x.tiles) * p.c.heads * static_cast<uint32_t>(own_n);
+                if (u < first + n || r + 1 >= p.n_req) break;
+                first += n;
+                own_row += static_cast<uint64_t>(x.n) * p.q_heads * static_cast<uint32_t>(own_n);
+                ++r;
+            }
+            const uint64_t hj = udiv(u - first, static_cast<uint32_t>(own_n));
+            ca = static_cast<int32_t>(u - first - hj * own_n);
+            h = static_cast<int32_t>(udiv(hj, static_cast<uint32_t>(x.tiles)));
+            j = static_cast<int32_t>(hj) - h * x.tiles;
+        } else {
+            x = request<kRows, MODE>(p, r);
         const uint64_t ru = static_cast<uint64_t>(x.tiles) * p.c.heads * x.units;
         if (u >= base + ru) {
             base += ru;
@@ -244,9 +347,11 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
             continue;
         }
         const uint64_t hj = udiv(u - base, static_cast<uint32_t>(x.units));
-        const int32_t ca = static_cast<int32_t>(u - base - hj * x.units);
-        const int32_t cb = static_cast<int32_t>(x.units - ca < u_end - u ? x.units : ca + (u_end - u));
-        const int32_t h = static_cast<int32_t>(udiv(hj, static_cast<uint32_t>(x.tiles))), j = static_cast<int32_t>(hj) - h * x.tiles;
+        ca = static_cast<int32_t>(u - base - hj * x.units);
+        cb = static_cast<int32_t>(x.units - ca < u_end - u ? x.units : ca + (u_end - u));
+        h = static_cast<int32_t>(udiv(hj, static_cast<uint32_t>(x.tiles)));
+        j = static_cast<int32_t>(hj) - h * x.tiles;
+        }
 
         // the tokens some row of the tile sees / every row sees; row i of the
         // tile is (query, head) = divmod(row0 + i, group)
@@ -262,11 +367,12 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         }
 
         // this warp's pairs: base token x.lo + 32 (8 c + warp), c = ca .. cb - 1
-        int32_t tok = x.lo + ca * kRowUnit + static_cast<int32_t>(warp) * kRowPair;
-        const int32_t seg_end = x.lo + cb * kRowUnit;
+        // (kAttnOwn: the chunk ca)
+        int32_t tok = MODE == kAttnOwn ? x.lo + ca * chunk : x.lo + ca * kRowUnit + static_cast<int32_t>(warp) * kRowPair;
+        const int32_t seg_end = MODE == kAttnOwn ? (x.tokens - ca * chunk > chunk ? tok + chunk : x.lo + x.tokens) : x.lo + cb * kRowUnit;
         const int32_t tok_end = seg_end < any_hi ? seg_end : any_hi;
-        while (tok + kRowPair <= any_lo && tok < tok_end) tok += kRowUnit;
-        const int32_t npair = tok < tok_end ? (tok_end - tok + kRowUnit - 1) / kRowUnit : 0;
+        while (tok + kRowPair <= any_lo && tok < tok_end) tok += kStep;
+        const int32_t npair = tok < tok_end ? (tok_end - tok + kStep - 1) / kStep : 0;
         // lane 2 i + s: tile s of pair 16 b + i: the offset of its codes (all ones: no such block), its scales
         struct Lane {
             uint64_t off;
@@ -275,7 +381,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         auto tiles_of = [&](int32_t b) {
             Lane l{~0ull, 0.0f, 0.0f};
             const int32_t i = 16 * b + static_cast<int32_t>(lane >> 1);
-            const int32_t tk = tok + i * kRowUnit + static_cast<int32_t>(lane & 1u) * kRowTile;
+            const int32_t tk = tok + i * kStep + static_cast<int32_t>(lane & 1u) * kRowTile;
             if (i < npair && tk < any_hi && tk + kRowTile > any_lo) {
                 const int32_t id = p.table[r * p.width + (tk >> bl)];
                 if (id >= 0 && id < p.c.num_blocks) {
@@ -436,7 +542,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
             }
             taken();
             issue(i + (ST - 1) / 2, 1);
-            const int32_t tb = tok + i * kRowUnit;
+            const int32_t tb = tok + i * kStep;
             const bool masked = tb + kRowPair > all_hi || tb < all_lo || !live[0] || !live[1];
             // exponents relative to the running maximum
             float ex[2][NT][4];
@@ -624,6 +730,30 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                 sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], 16);
             }
 
+        if constexpr (MODE == kAttnOwn) {  // the part of every row: values, maximum, sum
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int32_t row = 8 * nt + 2 * static_cast<int32_t>(t) + e;
+                    if (row >= nrows) continue;
+                    const uint64_t first = own_row + (static_cast<uint64_t>(h) * (x.n * p.group) + static_cast<uint32_t>(row0 + row)) * own_n;
+                    float* dst = p.own_slots + (first + ca) * (D + 4);
+                    if (g == 0) {
+                        *reinterpret_cast<float4*>(dst + D) = make_float4(mx[nt][e], sum[nt][e], 0.0f, 0.0f);
+                        const int32_t qi = query_of(p, row0 + row);
+                        if (ca == 0)
+                            static_cast<uint2*>(p.own_records)[(x.q0 + qi) * p.q_heads + h * p.group + row0 + row - qi * p.group] =
+                                make_uint2(static_cast<uint32_t>(first), static_cast<uint32_t>(own_n));
+                    }
+#pragma unroll
+                    for (int s = 0; s < KS; s += 2)
+                        *reinterpret_cast<float4*>(dst + g * VB + 2 * s) =
+                            make_float4(o[nt][s][e], o[nt][s][e + 2], o[nt][s + 1][e], o[nt][s + 1][e + 2]);
+                }
+            u += static_cast<uint64_t>(gridDim.x) * kRowWarps;
+            continue;
+        }
         // join the warps: row i's maximum, sum and values over the 8 warps in order
         __syncthreads();  // the ring is free
         float* part = reinterpret_cast<float*>(ring);
@@ -712,18 +842,6 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                 }
             }
         }
-        if constexpr (MODE == kAttnOwn) {
-            if (write && x.own > 0 && !joins) {
-                attn_pdl_wait();
-                joins = true;
-            }
-            if (write && x.own > 0) {  // join the prefix's parts
-                const int32_t i = row < nrows ? row : 0, qi = query_of(p, row0 + i);
-                RowParts<D> parts(p, (x.q0 + qi) * p.q_heads + h * p.group + row0 + i - qi * p.group);
-                if (row >= nrows) parts.n = 0;
-                parts.template join<TPR, EPT>(static_cast<uint32_t>(tid % TPR), static_cast<uint32_t>(d0), M, L, acc);
-            }
-        }
         if (write && row < nrows) {
             const int32_t qi = query_of(p, row0 + row), qh = h * p.group + row0 + row - qi * p.group;
             const int64_t at = (x.q0 + qi) * p.q_heads + qh;
@@ -739,7 +857,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         __syncthreads();           // s_m, s_l, the ring and s_last are free again
         u += static_cast<uint64_t>(cb - ca);
     }
-    if (MODE == kAttnOwn ? !joins : p.prompt_rows > 0) attn_pdl_wait();  // (this launch ends no earlier than the prompt kernel that it runs beside)
+    if (MODE == kAttnOwn || p.prompt_rows > 0) attn_pdl_wait();  // (this launch ends no earlier than the prompt kernel that it runs beside)
 }
 
 // ---- launching ---------------------------------------------------------------

@@ -105,43 +105,59 @@ int launch_attention_prompt(AttnParams p, int head_dim, bool e4m3, bool bf16, in
                             bool* launched);
 int launch_attention(AttnParams p, int head_dim, bool e4m3, bool bf16, void* stream);
 
-// Attention of requests that share prefixes, in two parts: the prefix of each
-// group of requests, read once for the rows of all of them (k_attn_prompt),
-// and every request's own tokens, whose kernels join the two.
+// Attention of requests that share prefixes: the prefix of each group of
+// requests, read once for the rows of all of them (k_attn_prompt), every
+// request's own tokens (k_attn_rows, in parts of one warp each; k_attn_prompt
+// for many rows, which finishes those), and the join of the parts of a row
+// (k_attn_join).
 //
-// The prefix part is laid out in slots: a unit (256 rows of a group and cache
-// head at most) leaves one slot for each CTA that shares its tokens, of one
-// row of D + 4 floats for each of its own (values, maximum, sum).  A row finds
-// its slots by its record: the first slot's offset in rows, the rows of a
-// slot, the slots, the row in the slot.
+// A part is a row of D + 4 floats: values, maximum, sum.  The prefix's parts
+// lie in slots: a unit (256 rows of a group and cache head at most) leaves one
+// slot, of a row for each of its own, for each CTA that shares its tokens (two
+// where it has 128 rows or fewer).  A row finds them by its record: the first
+// slot's offset in rows, the rows of a slot, the slots, the row in the slot.
+// The parts of its own tokens follow one another; their record is the first
+// one's row and their number.
 constexpr int kPrefixMaxParts = 64;   // CTAs of a unit at most
 constexpr uint64_t kPrefixMinTiles = 2;  // tiles of 128 tokens of a CTA at least
 constexpr int kPrefixMaxExtra = 192;  // CTAs beyond one per unit at most (no more than SMs)
 constexpr int64_t prefix_slot_rows(int64_t n_tokens, int64_t q_heads) {
-    return n_tokens * q_heads + static_cast<int64_t>(kPrefixMaxExtra) * kPromptRows;
+    return 2 * n_tokens * q_heads + static_cast<int64_t>(kPrefixMaxExtra) * kPromptRows;
 }
-constexpr size_t prefix_records_at(int head_dim) { return (attn_workspace_bytes(head_dim) + 255) / 256 * 256; }
-constexpr size_t prefix_slots_at(int head_dim, int64_t n_tokens, int64_t q_heads) {
-    return (prefix_records_at(head_dim) + 16 * static_cast<size_t>(n_tokens * q_heads) + 255) / 256 * 256;
+constexpr int64_t prefix_own_rows(int64_t n_tokens, int64_t q_heads) {  // units beyond one a row tile: no more than warps
+    return n_tokens * q_heads + static_cast<int64_t>(kAttnMaxCtas) * 8 * kAttnRows;
 }
-constexpr size_t prefix_workspace_bytes(int head_dim, int64_t n_tokens, int64_t q_heads) {
-    return prefix_slots_at(head_dim, n_tokens, q_heads) +
-           4 * static_cast<size_t>(head_dim + 4) * static_cast<size_t>(prefix_slot_rows(n_tokens, q_heads));
+struct PrefixLayout {  // bytes from the workspace's start
+    size_t records, own_records, slots, own_slots, bytes;
+};
+constexpr PrefixLayout prefix_layout(int head_dim, int64_t n_tokens, int64_t q_heads) {
+    const size_t rows = static_cast<size_t>(n_tokens * q_heads), row = 4 * static_cast<size_t>(head_dim + 4);
+    PrefixLayout x{};
+    x.records = (attn_workspace_bytes(head_dim) + 255) / 256 * 256;
+    x.own_records = (x.records + 16 * rows + 255) / 256 * 256;
+    x.slots = (x.own_records + 8 * rows + 255) / 256 * 256;
+    x.own_slots = (x.slots + row * static_cast<size_t>(prefix_slot_rows(n_tokens, q_heads)) + 255) / 256 * 256;
+    x.bytes = x.own_slots + row * static_cast<size_t>(prefix_own_rows(n_tokens, q_heads));
+    return x;
 }
 struct PrefixParams : AttnParams {
     const int32_t* group_start;
     const int32_t* prefix_len;
     int64_t n_groups;
     void* records;      // uint4 [n_tokens, q_heads]
+    void* own_records;  // uint2 [n_tokens, q_heads]
     float* slots;
-    int64_t slot_rows;  // rows that the slots have room for
+    float* own_slots;
+    int64_t slot_rows;  // rows that they have room for
+    int64_t own_rows;
     int32_t sms;        // (set by the launcher)
 };
 int launch_attention_prefix(PrefixParams p, int head_dim, bool e4m3, bool bf16, void* stream);
-// The three kernels' launches (each in its own translation unit).
+// The kernels' launches (each in its own translation unit).
 int launch_prefix_shared(const PrefixParams& p, int head_dim, bool e4m3, bool bf16, int dev, void* stream);
 int launch_prefix_own_prompt(PrefixParams p, int head_dim, bool e4m3, bool bf16, int dev, void* stream, bool* launched);
 int launch_prefix_own_rows(const PrefixParams& p, int head_dim, bool e4m3, bool bf16, int dev, void* stream);
+int launch_prefix_join(const PrefixParams& p, int head_dim, bool bf16, void* stream);
 
 struct LoraParams {
     const uint16_t* x;

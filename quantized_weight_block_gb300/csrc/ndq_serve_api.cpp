@@ -219,7 +219,7 @@ size_t ndq_attention_prefix_workspace_bytes(int head_dim, int64_t n_tokens, int 
     if ((head_dim != 64 && head_dim != 128) || n_tokens < 0 || n_tokens > INT32_MAX / 2 || kv_heads < 1 || q_heads < 1 ||
         q_heads > 4096 || q_heads % kv_heads != 0 || n_tokens > INT32_MAX / q_heads)
         return 0;
-    return ndq::prefix_workspace_bytes(head_dim, n_tokens, q_heads);
+    return ndq::prefix_layout(head_dim, n_tokens, q_heads).bytes;
 }
 
 int ndq_attention_prefix_kv8(const ndq_kv_cache* cache, const void* q, int dtype, int64_t n_tokens, int q_heads,
@@ -238,17 +238,20 @@ int ndq_attention_prefix_kv8(const ndq_kv_cache* cache, const void* q, int dtype
     if (n_groups > 0 && (!group_start || !prefix_len)) return NDQ_ERR_NULL;
     if (!aligned(group_start, 4) || !aligned(prefix_len, 4)) return NDQ_ERR_MISALIGNED;
     const int D = cache->head_dim;
-    if (!workspace || !aligned(workspace, 256) || ws_bytes < ndq::prefix_workspace_bytes(D, n_tokens, q_heads))
-        return NDQ_ERR_WORKSPACE;
+    const ndq::PrefixLayout at = ndq::prefix_layout(D, n_tokens, q_heads);
+    if (!workspace || !aligned(workspace, 256) || ws_bytes < at.bytes) return NDQ_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.counters = static_cast<uint32_t*>(workspace);
     p.parts = reinterpret_cast<float*>(ws + ndq::kAttnCounterBytes);
     p.group_start = group_start;
     p.prefix_len = prefix_len;
     p.n_groups = n_groups;
-    p.records = ws + ndq::prefix_records_at(D);
-    p.slots = reinterpret_cast<float*>(ws + ndq::prefix_slots_at(D, n_tokens, q_heads));
+    p.records = ws + at.records;
+    p.own_records = ws + at.own_records;
+    p.slots = reinterpret_cast<float*>(ws + at.slots);
+    p.own_slots = reinterpret_cast<float*>(ws + at.own_slots);
     p.slot_rows = ndq::prefix_slot_rows(n_tokens, q_heads);
+    p.own_rows = ndq::prefix_own_rows(n_tokens, q_heads);
     p.waits = take_waits();
     const bool e4m3 = cache->code_type == NDQ_FLOAT8E4M3FN, bf16 = dtype == NDQ_BFLOAT16;
     const int e = n_groups == 0 ? ndq::launch_attention(p, D, e4m3, bf16, stream) : ndq::launch_attention_prefix(p, D, e4m3, bf16, stream);
