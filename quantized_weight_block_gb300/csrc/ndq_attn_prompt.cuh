@@ -264,6 +264,27 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
     const int bl = p.c.bs_log2;
     attn_pdl_launch();  // (the kernel for the other requests may start)
+    if (tid == 32 * kPrMmaWarp) {  // (beside the loads below)
+        for (int i = 0; i < kPrRaw; ++i) {
+            mbar_init(&S.rawfull[i], 1);
+            mbar_init(&S.rawfree[i], kPrConv);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.vfull[i], kPrConv);
+            mbar_init(&S.vfree[i], 1);
+            mbar_init(&S.kfull[i], kPrConv);
+            mbar_init(&S.kfree[i], 1);
+            mbar_init(&S.sfull[i], 1);
+            mbar_init(&S.odone[i], 1);
+            mbar_init(&S.pfull[i], 4);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        S.fault = 0u;
+        S.nan = 0u;
+        S.last = 0u;
+        S.lo_min = S.hi_min = INT32_MAX;
+        S.lo_max = S.hi_max = 0;
+    }
 
     // which unit: blockIdx.x counts (unit, split), units ordered by request,
     // then row tile (the last, longest, first), then head
@@ -411,27 +432,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             S.r = tid * per;
             S.base = static_cast<int64_t>(before);
         }
-    }
-    if (tid == 0) {
-        for (int i = 0; i < kPrRaw; ++i) {
-            mbar_init(&S.rawfull[i], 1);
-            mbar_init(&S.rawfree[i], kPrConv);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&S.vfull[i], kPrConv);
-            mbar_init(&S.vfree[i], 1);
-            mbar_init(&S.kfull[i], kPrConv);
-            mbar_init(&S.kfree[i], 1);
-            mbar_init(&S.sfull[i], 1);
-            mbar_init(&S.odone[i], 1);
-            mbar_init(&S.pfull[i], 4);
-        }
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        S.fault = 0u;
-        S.nan = 0u;
-        S.last = 0u;
-        S.lo_min = S.hi_min = INT32_MAX;
-        S.lo_max = S.hi_max = 0;
     }
     if (warp == kPrMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&S.tmem)));

@@ -122,25 +122,36 @@ __device__ __forceinline__ Req request(const typename AttnArgs<MODE>::type& p, i
 
 // (kAttnOwn) Parts that a row of the request leaves.
 __device__ __forceinline__ int32_t own_parts(const Req& x, int32_t chunk) { return x.tokens > chunk ? (x.tokens - 1) / chunk + 1 : 1; }
-constexpr int32_t kOwnMinTokens = 256;
+constexpr int32_t kOwnMinTokens = 64;
 
-// The sum over the block's threads before this one, and of all of them.
-__device__ __forceinline__ uint64_t rows_scan(uint64_t mine, uint64_t* warps, uint64_t& total) {
+// Two sums over the block's threads before this one, and of all of them.
+struct RowSums {
+    uint64_t a, b;
+};
+__device__ __forceinline__ RowSums rows_scan(RowSums mine, RowSums* warps, RowSums& total) {
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    uint64_t incl = mine;
+    RowSums incl = mine;
 #pragma unroll
     for (uint32_t d = 1; d < 32; d <<= 1) {
-        const uint64_t y = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += y;
+        const uint64_t y = __shfl_up_sync(0xffffffffu, incl.a, d), z = __shfl_up_sync(0xffffffffu, incl.b, d);
+        if (lane >= d) {
+            incl.a += y;
+            incl.b += z;
+        }
     }
     if (lane == 31u) warps[warp] = incl;
     __syncthreads();
-    uint64_t before = incl - mine;
-    total = 0;
+    RowSums before{incl.a - mine.a, incl.b - mine.b};
+    total = {0, 0};
 #pragma unroll
     for (uint32_t w = 0; w < kRowWarps; ++w) {
-        if (w < warp) before += warps[w];
-        total += warps[w];
+        const RowSums x = warps[w];
+        if (w < warp) {
+            before.a += x.a;
+            before.b += x.b;
+        }
+        total.a += x.a;
+        total.b += x.b;
     }
     return before;
 }
@@ -174,8 +185,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
     constexpr uint64_t kSlot = NDQ_ROWS_SLOT(D);
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ uint64_t s_sum[kRowWarps];
-    __shared__ uint64_t s_sum2[MODE == kAttnOwn ? kRowWarps : 1];
-    __shared__ uint64_t s_units[MODE == kAttnOwn ? kRowThreads : 1], s_rows[MODE == kAttnOwn ? kRowThreads : 1];  // before each thread's requests
+    __shared__ RowSums s_own[2][MODE == kAttnOwn ? kRowWarps : 1], s_before[MODE == kAttnOwn ? kRowThreads : 1];  // (before each thread's requests)
     __shared__ int64_t s_r, s_base;
     __shared__ float s_m[kRowWarps][kRows], s_l[kRowWarps][kRows];
     __shared__ uint32_t s_last;
@@ -199,38 +209,35 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         // all requests' row tiles and tokens, from them the chunk, then every
         // request's units and rows of parts; a thread sums up `per` requests
         per = (p.n_req + kRowThreads - 1) / kRowThreads;
-        uint64_t tiles = 0, work = 0, all_tiles = 0, all_work = 0;
+        RowSums tiles{0, 0}, all{0, 0};  // row tiles, and tokens of them
         for (int64_t i = 0; i < per; ++i) {
             const int64_t q = tid * per + i;
             if (q < p.n_req) {
                 const Req x = request<kRows, MODE>(p, q);
                 const uint64_t n = static_cast<uint64_t>(x.tiles) * p.c.heads;
-                tiles += n;
-                work += n * static_cast<uint32_t>(x.tokens);
+                tiles.a += n;
+                tiles.b += n * static_cast<uint32_t>(x.tokens);
             }
         }
-        rows_scan(tiles, s_sum, all_tiles);
-        rows_scan(work, s_sum2, all_work);
+        rows_scan(tiles, s_own[0], all);
         const uint64_t warps = static_cast<uint64_t>(gridDim.x) * kRowWarps;
-        const uint64_t spare = all_tiles + warps / 4 < warps ? warps - all_tiles : warps / 4;  // units beyond one a row tile at most
-        uint64_t c = udiv(all_work, spare) + 1;
+        const uint64_t spare = all.a + warps / 4 < warps ? warps - all.a : warps / 4;  // units beyond one a row tile at most
+        uint64_t c = udiv(all.b, spare) + 1;
         c = (c + kRowPair - 1) / kRowPair * kRowPair;
         chunk = c < kOwnMinTokens ? kOwnMinTokens : (c > (1 << 30) ? (1 << 30) : static_cast<int32_t>(c));
-        uint64_t units = 0, rows = 0, all_rows = 0;
+        RowSums units{0, 0};  // units, and rows of parts
         for (int64_t i = 0; i < per; ++i) {
             const int64_t q = tid * per + i;
             if (q < p.n_req) {
                 const Req x = request<kRows, MODE>(p, q);
                 const uint64_t n = static_cast<uint32_t>(own_parts(x, chunk));
-                units += static_cast<uint64_t>(x.tiles) * p.c.heads * n;
-                rows += static_cast<uint64_t>(x.n) * p.q_heads * n;
+                units.a += static_cast<uint64_t>(x.tiles) * p.c.heads * n;
+                units.b += static_cast<uint64_t>(x.n) * p.q_heads * n;
             }
         }
-        __syncthreads();  // (the sums above are read)
-        s_units[tid] = rows_scan(units, s_sum, total);
-        s_rows[tid] = rows_scan(rows, s_sum2, all_rows);
+        s_before[tid] = rows_scan(units, s_own[1], all);
         __syncthreads();
-        if (all_rows > static_cast<uint64_t>(p.own_rows)) total = 0;  // (never)
+        total = all.b <= static_cast<uint64_t>(p.own_rows) ? all.a : 0;  // (always)
         u = static_cast<uint64_t>(blockIdx.x) * kRowWarps + warp;
         u_end = total;
     } else {
@@ -319,11 +326,11 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
             int32_t lo = 0, hi = kRowThreads;
             while (hi - lo > 1) {
                 const int32_t m = (lo + hi) >> 1;
-                if (s_units[m] <= u) lo = m;
+                if (s_before[m].a <= u) lo = m;
                 else hi = m;
             }
-            uint64_t first = s_units[lo];
-            own_row = s_rows[lo];
+            uint64_t first = s_before[lo].a;
+            own_row = s_before[lo].b;
             r = lo * per;
             for (;;) {
                 x = request<kRows, MODE>(p, r);
