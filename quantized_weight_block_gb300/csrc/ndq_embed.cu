@@ -26,7 +26,7 @@ int launch_embed(EmbedParams p, void* stream) {
         if (!fn) fn = family(p.w.fmt, &seg);
     if (!fn) return static_cast<int>(cudaErrorInvalidValue);
     EmbedDevice& di = g_embed_dev[dev];
-    constexpr int kThreadsPerCta = 256;
+    constexpr int kThreadsPerCta = 128;
     if (di.ctas[p.w.fmt] == 0) {  // (concurrent first calls find the same values)
         int sms = 0, ctas = 0;
         if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return static_cast<int>(e);
@@ -39,7 +39,7 @@ int launch_embed(EmbedParams p, void* stream) {
     p.segs = static_cast<uint32_t>(segs);
     p.units = static_cast<uint32_t>(units);
     p.aligned = (reinterpret_cast<uintptr_t>(p.w.x) & 15u) == 0 && p.bpr * p.w.S % 16u == 0 && seg / p.w.B * p.w.S % 16u == 0;
-    const uint64_t want = (units + 7) / 8, resident = static_cast<uint64_t>(di.sms) * static_cast<uint64_t>(di.ctas[p.w.fmt]);
+    const uint64_t want = (units + 3) / 4, resident = static_cast<uint64_t>(di.sms) * static_cast<uint64_t>(di.ctas[p.w.fmt]);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(want < resident ? want : resident));
     cfg.blockDim = dim3(kThreadsPerCta);

@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "ndq_attn.cuh"
+#include "ndq_device.cuh"
 #include "ndq_rope.h"
 
 namespace ndq {
@@ -34,6 +35,10 @@ namespace {
 
 constexpr int kRopeWarps = 4;
 constexpr int kRopeMaxDim = 256;
+// CTAs of an SM, and of the grid for each SM.  16001 tokens of 40 heads of 128,
+// bfloat16: 57.1 us with 6, 61.1 with 5, 65.7 as the compiler would have it (4),
+// and 59.5 against 61.1 when no CTA comes after the resident ones.
+constexpr int rope_ctas(int in) { return in == 0 ? 5 : 6; }
 
 struct RopeShared {
     uint64_t turn[kRopeMaxDim / 2];  // turns per position, in units of 2^-64
@@ -69,27 +74,23 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, uint4* r) {
     }
 }
 template <int IN>
-__device__ __forceinline__ void widen8(const uint4* r, float* v) {
+__device__ __forceinline__ void widen8(const uint4* r, float2* v) {
     if constexpr (IN == 0) {
-        v[0] = __uint_as_float(r[0].x);
-        v[1] = __uint_as_float(r[0].y);
-        v[2] = __uint_as_float(r[0].z);
-        v[3] = __uint_as_float(r[0].w);
-        v[4] = __uint_as_float(r[1].x);
-        v[5] = __uint_as_float(r[1].y);
-        v[6] = __uint_as_float(r[1].z);
-        v[7] = __uint_as_float(r[1].w);
+        v[0] = make_float2(__uint_as_float(r[0].x), __uint_as_float(r[0].y));
+        v[1] = make_float2(__uint_as_float(r[0].z), __uint_as_float(r[0].w));
+        v[2] = make_float2(__uint_as_float(r[1].x), __uint_as_float(r[1].y));
+        v[3] = make_float2(__uint_as_float(r[1].z), __uint_as_float(r[1].w));
     } else {
-        widen2<IN == 1>(r[0].x, v[0], v[1]);
-        widen2<IN == 1>(r[0].y, v[2], v[3]);
-        widen2<IN == 1>(r[0].z, v[4], v[5]);
-        widen2<IN == 1>(r[0].w, v[6], v[7]);
+        widen2<IN == 1>(r[0].x, v[0].x, v[0].y);
+        widen2<IN == 1>(r[0].y, v[1].x, v[1].y);
+        widen2<IN == 1>(r[0].z, v[2].x, v[2].y);
+        widen2<IN == 1>(r[0].w, v[3].x, v[3].y);
     }
 }
 
 // IN: the inputs' type; BF16: the outputs'; L: lanes of a head.
 template <int L, int IN, bool BF16>
-__global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas(IN)) k_rope(const __grid_constant__ RopeParams p) {
     constexpr int G = 32 / L;               // heads at a time
     constexpr int R = IN == 0 ? 2 : 1;      // 16-byte words of eight inputs
     constexpr int C = (8 + G - 1) / G;      // cosines that a lane computes
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant_
         const int32_t pos = p.positions[t];
         if (pos < 0) continue;  // padding: left as it was
         // the rotation of this lane's eight pairs
-        float cs[8], sn[8];
+        float2 cs[4], sn[4];
         if (rot > 0) {
             float c1[C], s1[C];
 #pragma unroll
@@ -135,9 +136,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant_
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                cs[i] = __shfl_sync(0xffffffffu, c1[i / G], (i % G) * L + j);
-                sn[i] = __shfl_sync(0xffffffffu, s1[i / G], (i % G) * L + j);
+            for (int i = 0; i < 4; ++i) {
+                cs[i].x = __shfl_sync(0xffffffffu, c1[2 * i / G], (2 * i % G) * L + j);
+                cs[i].y = __shfl_sync(0xffffffffu, c1[(2 * i + 1) / G], ((2 * i + 1) % G) * L + j);
+                sn[i].x = __shfl_sync(0xffffffffu, s1[2 * i / G], (2 * i % G) * L + j);
+                sn[i].y = __shfl_sync(0xffffffffu, s1[(2 * i + 1) / G], ((2 * i + 1) % G) * L + j);
             }
         }
         // heads [h0, h1) of the queries, then of the keys
@@ -158,27 +161,31 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant_
             for (int i = 0; i < N; ++i) load(h0 + i * G + g, i);
             auto round = [&](int hb, int i) {
                 const int h = hb + g;
-                float a[8], b[8];
+                float2 a[4], b[4];
                 widen8<IN>(ra[i], a);
                 widen8<IN>(rb[i], b);
                 if (hb + N * G < h1) load(h + N * G, i);
                 if (norm) {
-                    float s2[2] = {0.0f, 0.0f};
+                    auto squares = [&]() {
+                        float2 s2 = make_float2(0.0f, 0.0f), s3 = s2;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        s2[0] = __fmaf_rn(a[e], a[e], s2[0]);
-                        s2[1] = __fmaf_rn(b[e], b[e], s2[1]);
-                    }
-                    float sum = s2[0] + s2[1];
+                        for (int e = 0; e < 4; ++e) {
+                            s2 = fma2(a[e], a[e], s2);
+                            s3 = fma2(b[e], b[e], s3);
+                        }
+                        float sum = (s2.x + s2.y) + (s3.x + s3.y);
 #pragma unroll
-                    for (int d = 1; d < L; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                        for (int d = 1; d < L; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                        return sum;
+                    };
+                    float sum = squares(), eps = p.eps;
                     // Squares that overflow or vanish (rare): the row is scaled by a power of two first.
                     const bool odd = sum > 0x1p120f || (sum < 0x1p-90f && p.eps < 0x1p-60f);
-                    float eps = p.eps;
                     if (__any_sync(0xffffffffu, odd)) {
                         float top = 0.0f;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(a[e]), fabsf(b[e])));
+                        for (int e = 0; e < 4; ++e)
+                            top = fmaxf(top, fmaxf(fmaxf(fabsf(a[e].x), fabsf(a[e].y)), fmaxf(fabsf(b[e].x), fabsf(b[e].y))));
 #pragma unroll
                         for (int d = 1; d < L; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                         const int ex = static_cast<int>(__float_as_uint(top) >> 23);  // 0: vanishing, 255: infinite
@@ -187,68 +194,57 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant_
                             const int up = 127 - (ex > 1 ? ex : 1), u1 = up / 2, u2 = up - u1;
                             const float f1 = __uint_as_float(static_cast<uint32_t>(127 + u1) << 23), f2 = __uint_as_float(static_cast<uint32_t>(127 + u2) << 23);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                a[e] = a[e] * f1 * f2;
-                                b[e] = b[e] * f1 * f2;
+                            for (int e = 0; e < 4; ++e) {
+                                a[e] = make_float2(a[e].x * f1 * f2, a[e].y * f1 * f2);
+                                b[e] = make_float2(b[e].x * f1 * f2, b[e].y * f1 * f2);
                             }
                             eps = eps * f1 * f2 * f1 * f2;
                         }
-                        s2[0] = s2[1] = 0.0f;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            s2[0] = __fmaf_rn(a[e], a[e], s2[0]);
-                            s2[1] = __fmaf_rn(b[e], b[e], s2[1]);
-                        }
-                        sum = s2[0] + s2[1];
-#pragma unroll
-                        for (int d = 1; d < L; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                        sum = squares();
                     }
                     const float r = rsqrtf(__fmaf_rn(sum, inv_dim, eps));
+                    const float2 rr = make_float2(r, r);
                     const float4* wa = reinterpret_cast<const float4*>(w + 8 * pa);
                     const float4* wb = reinterpret_cast<const float4*>(w + 8 * pb);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float4 f = wa[e], g4 = wb[e];
-                        a[4 * e] = a[4 * e] * r * f.x;
-                        a[4 * e + 1] = a[4 * e + 1] * r * f.y;
-                        a[4 * e + 2] = a[4 * e + 2] * r * f.z;
-                        a[4 * e + 3] = a[4 * e + 3] * r * f.w;
-                        b[4 * e] = b[4 * e] * r * g4.x;
-                        b[4 * e + 1] = b[4 * e + 1] * r * g4.y;
-                        b[4 * e + 2] = b[4 * e + 2] * r * g4.z;
-                        b[4 * e + 3] = b[4 * e + 3] * r * g4.w;
+                        const float4 f = wa[e], k = wb[e];
+                        a[2 * e] = mul2(mul2(a[2 * e], rr), make_float2(f.x, f.y));
+                        a[2 * e + 1] = mul2(mul2(a[2 * e + 1], rr), make_float2(f.z, f.w));
+                        b[2 * e] = mul2(mul2(b[2 * e], rr), make_float2(k.x, k.y));
+                        b[2 * e + 1] = mul2(mul2(b[2 * e + 1], rr), make_float2(k.z, k.w));
                     }
                 }
                 if (turned) {
                     if (p.interleaved) {
+                        auto turn = [](float2& v, float c, float s) {
+                            v = make_float2(__fmaf_rn(-v.y, s, v.x * c), __fmaf_rn(v.y, c, v.x * s));
+                        };
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float a0 = a[2 * e], a1 = a[2 * e + 1], b0 = b[2 * e], b1 = b[2 * e + 1];
-                            a[2 * e] = __fmaf_rn(-a1, sn[e], a0 * cs[e]);
-                            a[2 * e + 1] = __fmaf_rn(a1, cs[e], a0 * sn[e]);
-                            b[2 * e] = __fmaf_rn(-b1, sn[e + 4], b0 * cs[e + 4]);
-                            b[2 * e + 1] = __fmaf_rn(b1, cs[e + 4], b0 * sn[e + 4]);
+                            turn(a[e], e & 1 ? cs[e / 2].y : cs[e / 2].x, e & 1 ? sn[e / 2].y : sn[e / 2].x);
+                            turn(b[e], e & 1 ? cs[2 + e / 2].y : cs[2 + e / 2].x, e & 1 ? sn[2 + e / 2].y : sn[2 + e / 2].x);
                         }
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float a0 = a[e], b0 = b[e];
-                            a[e] = __fmaf_rn(-b0, sn[e], a0 * cs[e]);
-                            b[e] = __fmaf_rn(b0, cs[e], a0 * sn[e]);
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 a0 = a[e], b0 = b[e];
+                            a[e] = fma2(make_float2(-b0.x, -b0.y), sn[e], mul2(a0, cs[e]));
+                            b[e] = fma2(b0, cs[e], mul2(a0, sn[e]));
                         }
                     }
                 }
                 if (live && h < h1) {
                     uint16_t* dst = static_cast<uint16_t*>(y) + ya + static_cast<int64_t>(h) * D;
                     *reinterpret_cast<uint4*>(dst + 8 * pa) =
-                        make_uint4(narrow2<BF16>(a[0], a[1]), narrow2<BF16>(a[2], a[3]), narrow2<BF16>(a[4], a[5]), narrow2<BF16>(a[6], a[7]));
+                        make_uint4(narrow2<BF16>(a[0].x, a[0].y), narrow2<BF16>(a[1].x, a[1].y), narrow2<BF16>(a[2].x, a[2].y), narrow2<BF16>(a[3].x, a[3].y));
                     *reinterpret_cast<uint4*>(dst + 8 * pb) =
-                        make_uint4(narrow2<BF16>(b[0], b[1]), narrow2<BF16>(b[2], b[3]), narrow2<BF16>(b[4], b[5]), narrow2<BF16>(b[6], b[7]));
+                        make_uint4(narrow2<BF16>(b[0].x, b[0].y), narrow2<BF16>(b[1].x, b[1].y), narrow2<BF16>(b[2].x, b[2].y), narrow2<BF16>(b[3].x, b[3].y));
                 }
             };
             for (int hb = h0; hb < h1; hb += N * G) {
                 round(hb, 0);
-                if (N == 2 && hb + G < h1) round(hb + G, N - 1);
+                if (N >= 2 && hb + G < h1) round(hb + G, N - 1);
             }
         };
         const int H = p.q_heads + p.k_heads;
@@ -298,7 +294,7 @@ int launch_rope(RopeParams p, int in, bool bf16, void* stream) {
     if (parts > rounds) parts = rounds;
     if (parts < 1) parts = 1;
     p.parts = static_cast<int32_t>(parts);
-    const int64_t want = (p.n_tokens * parts + kRopeWarps - 1) / kRopeWarps, most = static_cast<int64_t>(sms_of[dev]) * 16;
+    const int64_t want = (p.n_tokens * parts + kRopeWarps - 1) / kRopeWarps, most = static_cast<int64_t>(sms_of[dev]) * rope_ctas(in);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(want < most ? want : most));
     cfg.blockDim = dim3(kRopeWarps * 32);
