@@ -492,8 +492,11 @@ int ndq_attention_kv8(const ndq_kv_cache *cache, const void *q, int dtype, int64
  * request, which must hold them; the other rows must agree, and need not when
  * no query of theirs sees that block.  Queries may sit inside the prefix and
  * windows end in it.  The other arguments, and what the outputs hold, are
- * ndq_attention_kv8's; the two parts are joined in binary32.  A group of one,
- * prefixes of 0 and n_groups of 0 are valid.
+ * ndq_attention_kv8's; the parts are joined in binary32.  A group of one,
+ * prefixes of 0 and n_groups of 0 are valid.  Where sharing saves little (less
+ * than 128 MB if every request but one a group had a full table, or requests of
+ * 128 rows a cache head and more on average, whose products are the work) the
+ * call is ndq_attention_kv8's itself.
  *   workspace  device buffer of ndq_attention_prefix_workspace_bytes(head_dim,
  *              n_tokens, q_heads, kv_heads) bytes or more, 256-byte aligned,
  *              its first 4096 bytes zeroed once before its first use (each call

@@ -4,6 +4,9 @@
 
 namespace ndq {
 
+constexpr double kPrefixMinSaved = 128e6;  // bytes of the cache
+constexpr int64_t kPrefixMostRows = 128;   // rows of a request and cache head, on average
+
 int launch_prefix_shared(const PrefixParams& p, int head_dim, bool e4m3, bool bf16, int dev, void* stream) {
     // units at most: a group's last one may be partial, and every group in use has a token
     const int64_t groups = p.n_groups < p.n_tokens ? p.n_groups : p.n_tokens;
@@ -28,6 +31,16 @@ int launch_attention_prefix(PrefixParams p, int head_dim, bool e4m3, bool bf16, 
     if (p.max_q > p.n_tokens) p.max_q = p.n_tokens;
     const IqGrids* grids = nullptr;
     if (const int rc = device_symbols(dev, &p.fault, &grids)) return rc;
+    // Where sharing saves little: what it can save at most (what the host knows
+    // are the tables' widths), or requests whose own rows fill the prompt
+    // kernel's tiles, so that its products are the work.  Measured, shared beside
+    // not (32 heads of 128 on 8, steps): 16 requests behind 2000 tokens (saves
+    // 69 MB) 31 beside 27 us, behind 4000 (131 MB) 35 beside 35, 64 behind 1000
+    // (169 MB) 35 beside 40, behind 32000 106 beside 513; eight requests behind
+    // 4000 of 96 rows each 77 beside 86, of 256 106 beside 95, of 512 143 beside 100.
+    const int64_t groups = p.n_groups < p.n_req ? p.n_groups : p.n_req;
+    const double saved = static_cast<double>(p.n_req - groups) * static_cast<double>(p.width << p.c.bs_log2) * (2.0 * head_dim * p.c.heads);
+    if (saved < kPrefixMinSaved || p.n_tokens * p.group >= kPrefixMostRows * p.n_req) return launch_attention(p, head_dim, e4m3, bf16, stream);
     p.splits = 1;
     if (const int rc = launch_prefix_shared(p, head_dim, e4m3, bf16, dev, stream)) return rc;
     // the requests' own tokens, by their rows as in launch_attention
