@@ -69,10 +69,11 @@ constexpr int kPrThreads = 512;                 // four warpgroups; warps 14 and
 constexpr int kPrLaunchRegs = 128;
 constexpr int kPrTokens = 128;                  // tokens of a K / V tile
 constexpr int kPrGroups = kPrTokens / 16;
+constexpr float kStepCycles = 4400.0f, kFixedCycles = 30000.0f;  // (kAttnShared) of a tile, and before and after them
 constexpr uint32_t kPrFault = 8u;               // bit of the device fault word
 
 struct PrShared {
-    uint64_t rawfull[kPrRaw], rawfree[kPrRaw];
+    uint64_t rawfull[2 * kPrRaw], rawfree[2 * kPrRaw];  // (the second half: see `dual`)
     uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
     uint64_t sfull[2], pfull[2], odone[2];
     float4 cst[kPrCst][kPrGroups];  // per group: K's scale, log2 of V's scale, 1 / V's scale (0: far below others'), 0 for V of scale 0
@@ -89,6 +90,8 @@ struct PrShared {
     uint32_t parts;
     int32_t lo_min, lo_max, hi_min, hi_max;
 };
+
+static_assert(sizeof(PrShared) <= 2048, "beside seven tiles of 32 KB");
 
 template <int D>
 struct PrSmem {
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     const int bl = p.c.bs_log2;
     attn_pdl_launch();  // (the kernel for the other requests may start)
     if (tid == 32 * kPrMmaWarp) {  // (beside the loads below)
-        for (int i = 0; i < kPrRaw; ++i) {
+        for (int i = 0; i < 2 * kPrRaw; ++i) {
             mbar_init(&S.rawfull[i], 1);
             mbar_init(&S.rawfree[i], kPrConv);
         }
@@ -294,27 +297,33 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     uint32_t parts = 1, part = 0;
     // (kAttnShared) At most 128 rows: both row tiles are these rows, and take
     // the tokens' tiles by turns, each leaving a part.  (One row tile alone
-    // waits for its own chain of products and softmax.)
+    // waits for its own chain of products and softmax.)  There is one Q, and the
+    // other's memory holds a second pair of tiles of codes: one pair was
+    // brought, widened and given back in 3000 cycles, more than half of what the
+    // two row tiles then take.
     bool dual = false;
     if constexpr (MODE == kAttnShared) {
         // Every CTA counts the groups' units and tiles, from these how many
         // tiles a CTA is to take, and then finds its unit and part.
-        uint64_t chunk = 1;
-        auto parts_of = [&](int32_t tiles) {
-            const uint64_t n = chunk >= static_cast<uint64_t>(tiles) ? 1 : (static_cast<uint32_t>(tiles) + static_cast<uint32_t>(chunk) - 1) / static_cast<uint32_t>(chunk);
+        // (A unit of 128 rows or fewer goes through its tiles two at a time, see
+        // `dual`: they count half.)
+        uint64_t chunk = 1, sms = static_cast<uint64_t>(p.sms);
+        auto steps_of = [&](const SharedUnits& x) { return static_cast<uint32_t>(x.rows <= kPromptRows / 2 ? (x.tiles + 1) / 2 : x.tiles); };
+        auto parts_of = [&](const SharedUnits& x) {
+            const uint32_t steps = steps_of(x);
+            const uint64_t n = chunk >= steps ? 1 : (steps + static_cast<uint32_t>(chunk) - 1) / static_cast<uint32_t>(chunk);
             return static_cast<int64_t>(n > kPrefixMaxParts ? kPrefixMaxParts : n);
         };
         auto set_chunk = [&](uint64_t units, uint64_t work) {
             // CTAs beyond one per unit number at most work / chunk, no more than the SMs
-            const uint64_t sms = static_cast<uint64_t>(p.sms);
             const uint64_t spare = units + sms / 4 < sms ? sms - units : (sms + 3) / 4;
             chunk = (work >> 32) != 0 ? (work + spare - 1) / spare : static_cast<uint32_t>(work + spare - 1) / static_cast<uint32_t>(spare);
             chunk = chunk < kPrefixMinTiles ? kPrefixMinTiles : chunk;
         };
-        auto ctas_of = [&](const SharedUnits& x) { return static_cast<uint64_t>(x.units * parts_of(x.tiles)); };
+        auto ctas_of = [&](const SharedUnits& x) { return static_cast<uint64_t>(x.units * parts_of(x)); };
         auto slots_of = [&](const SharedUnits& x) {  // (few rows leave two rows each, see `dual`)
             const int64_t last = x.rows % kPromptRows;
-            return static_cast<uint64_t>((x.rows + (last <= kPromptRows / 2 ? last : 0)) * p.c.heads * parts_of(x.tiles));
+            return static_cast<uint64_t>((x.rows + (last <= kPromptRows / 2 ? last : 0)) * p.c.heads * parts_of(x));
         };
         auto mine = [&](int64_t g, uint64_t c, uint64_t n, int64_t parts_here) {
             S.r = g;
@@ -324,8 +333,28 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         };
         if (p.n_groups <= 32) {  // every warp for itself
             SharedUnits x{};
-            if (lane < p.n_groups) x = shared_units(p, attn_group(p, lane));
-            uint64_t units = static_cast<uint64_t>(x.units), work = units * static_cast<uint64_t>(x.tiles);
+            Group g{};
+            if (lane < p.n_groups) {
+                g = attn_group(p, lane);
+                x = shared_units(p, g);
+            }
+            uint64_t units = static_cast<uint64_t>(x.units), work = units * steps_of(x);
+            // All requests' tokens but the shared ones, for which the kernel after
+            // this one reads the cache meanwhile, on the SMs that are left to it.
+            uint64_t own = 0;
+            for (int64_t r = tid; r < p.n_req; r += kPrThreads) own += static_cast<uint32_t>(p.kv_len[r] > 0 ? p.kv_len[r] : 0);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) own += __shfl_xor_sync(0xffffffffu, own, d);
+            if (lane == 0) S.tot[warp] = own;
+            __syncthreads();
+            own = lane < kPrThreads / 32 ? S.tot[lane] : 0;
+            uint64_t common = lane < p.n_groups ? static_cast<uint64_t>(g.end - g.begin) * static_cast<uint32_t>(g.tokens) : 0;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) {
+                own += __shfl_xor_sync(0xffffffffu, own, d);
+                common += __shfl_xor_sync(0xffffffffu, common, d);
+            }
+            own = own > common ? own - common : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 if (d >= p.n_groups) break;
@@ -334,9 +363,17 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             }
             units = __shfl_sync(0xffffffffu, units, 0);
             work = __shfl_sync(0xffffffffu, work, 0);
+            {
+                // SMs in proportion: kStepCycles a tile and, beside it, D / 10 a
+                // token and row tile of the own ones (20 bytes a cycle and SM)
+                const float row_tiles = fmaxf(1.0f, static_cast<float>(p.n_tokens * p.group) / static_cast<float>(p.n_req * kAttnRows));
+                const float here = kFixedCycles * static_cast<float>(p.sms) * 0.5f + static_cast<float>(work) * kStepCycles;
+                const float there = static_cast<float>(own) * static_cast<float>(p.c.heads) * row_tiles * (D / 10.0f);
+                const uint32_t want = static_cast<uint32_t>(static_cast<float>(p.sms) * here / (here + there)) + 1u;
+                sms = want < p.sms / 2u ? p.sms / 2u : (want < static_cast<uint32_t>(p.sms) ? want : static_cast<uint32_t>(p.sms));
+            }
             set_chunk(units, work);
             // the smallest chunk whose CTAs still are one wave
-            const uint64_t sms = static_cast<uint64_t>(p.sms);
             if (units < sms && (work >> 31) == 0) {
                 uint32_t lo = static_cast<uint32_t>(work) / static_cast<uint32_t>(sms), hi = static_cast<uint32_t>(chunk);  // lo: too small, hi: will do
                 lo = lo < kPrefixMinTiles - 1 ? static_cast<uint32_t>(kPrefixMinTiles) - 1 : lo;
@@ -363,7 +400,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             const uint32_t here = __ballot_sync(0xffffffffu, blockIdx.x < ci && blockIdx.x >= ci - ctas);
             const uint64_t all_rows = __shfl_sync(0xffffffffu, ri, static_cast<int>(p.n_groups) - 1);
             if (here == 0u || all_rows > static_cast<uint64_t>(p.slot_rows)) return;  // (the latter never)
-            if (warp == 0 && lane == static_cast<uint32_t>(__ffs(here)) - 1u) mine(lane, ci - ctas, ri - rows, parts_of(x.tiles));
+            if (warp == 0 && lane == static_cast<uint32_t>(__ffs(here)) - 1u) mine(lane, ci - ctas, ri - rows, parts_of(x));
         } else {
             const int64_t per = (p.n_groups + kPrThreads - 1) / kPrThreads;
             uint64_t units = 0, work = 0, all_units = 0, all_work = 0;
@@ -372,7 +409,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 if (g < p.n_groups) {
                     const SharedUnits x = shared_units(p, attn_group(p, g));
                     units += static_cast<uint64_t>(x.units);
-                    work += static_cast<uint64_t>(x.units) * static_cast<uint64_t>(x.tiles);
+                    work += static_cast<uint64_t>(x.units) * steps_of(x);
                 }
             }
             block_scan(units, S.sum, all_units);
@@ -399,7 +436,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     n += slots_of(x);
                     x = shared_units(p, attn_group(p, ++g));
                 }
-                mine(g, c, n, parts_of(x.tiles));
+                mine(g, c, n, parts_of(x));
             }
         }
     } else {
@@ -580,7 +617,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             // (the row's owner, lane rl, is served by the lanes of its row)
             const float fr = __shfl_sync(0xffffffffu, down * p.scale_log2, (static_cast<int>(lane) % RPI) * LPR);
             if (lane / RPI == static_cast<uint32_t>(c)) frow = fr;
-            *reinterpret_cast<uint4*>(dst + (piece >> 3) * kAtom + sw128(32u * (warp & 3u) + rl, piece & 7u)) =
+            if (!(dual && wg == 1))
+                *reinterpret_cast<uint4*>(dst + (piece >> 3) * kAtom + sw128(32u * (warp & 3u) + rl, piece & 7u)) =
                 make_uint4(pack_half2(f[0] * up, f[1] * up), pack_half2(f[2] * up, f[3] * up), pack_half2(f[4] * up, f[5] * up),
                            pack_half2(f[6] * up, f[7] * up));
         }
@@ -663,6 +701,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         }
     }
     float mx = -INFINITY, sum = 0.0f;
+    // the codes of tile j, K (0) or V (1): their barrier, how often it has come round, and their place
+    const int32_t raws = MODE == kAttnShared && dual ? 2 : 1;
+    auto raw_bar = [&](int32_t j, uint32_t half) { return half + 2u * static_cast<uint32_t>(raws == 2 ? j & 1 : 0); };
+    auto raw_turn = [&](int32_t j) { return raws == 2 ? j >> 1 : j; };
+    auto raw_at = [&](int32_t j, uint32_t half) { return (raws == 2 && (j & 1) ? sQ + kTile : sRaw) + half * (kTile / 2); };
 
     if (warp >= kPrConvWarp && warp < kPrMmaWarp) {
         // ---- converters: groups cw and cw + 4 of every tile
@@ -722,19 +765,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         auto wait = [&](uint64_t* b, int32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(b, static_cast<uint32_t>(parity & 1), p.waits.limit_ns)); };
         for (int32_t j = 0; j < nt; ++j) {
             const uint32_t st = static_cast<uint32_t>(j & 1);
-            ok = wait(&S.rawfull[0], j) && (j < 2 || wait(&S.kfree[st], (j >> 1) - 1));
+            ok = wait(&S.rawfull[raw_bar(j, 0)], raw_turn(j)) && (j < 2 || wait(&S.kfree[st], (j >> 1) - 1));
             if (!ok) break;
-            convert(sRaw, sK + st * kTile, j, false);
+            convert(raw_at(j, 0), sK + st * kTile, j, false);
             if (lane == 0) {
                 mbar_arrive(&S.kfull[st]);
-                mbar_arrive(&S.rawfree[0]);
+                mbar_arrive(&S.rawfree[raw_bar(j, 0)]);
             }
-            ok = wait(&S.rawfull[1], j) && (j < 2 || wait(&S.vfree[st], (j >> 1) - 1));
+            ok = wait(&S.rawfull[raw_bar(j, 1)], raw_turn(j)) && (j < 2 || wait(&S.vfree[st], (j >> 1) - 1));
             if (!ok) break;
-            convert(sRaw + kTile / 2, sV + st * kTile, j, true);
+            convert(raw_at(j, 1), sV + st * kTile, j, true);
             if (lane == 0) {
                 mbar_arrive(&S.vfull[st]);
-                mbar_arrive(&S.rawfree[1]);
+                mbar_arrive(&S.rawfree[raw_bar(j, 1)]);
             }
         }
         if (!ok && lane == 0) atomicOr(&S.fault, 1u);
@@ -783,8 +826,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 const uint32_t n16 = __popc(__ballot_sync(0xffffffffu, mine && ids >= 0));
                 const bool far = __any_sync(0xffffffffu, mine && ids >= 0 && c.z == 0.0f);
                 for (int32_t half = 0; half < 2; ++half) {  // K, V
-                    const uint32_t rs = static_cast<uint32_t>(half);
-                    if (j >= 1) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.rawfree[rs], static_cast<uint32_t>((j - 1) & 1), p.waits.limit_ns));
+                    const uint32_t rs = raw_bar(j, static_cast<uint32_t>(half));
+                    if (j >= raws) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.rawfree[rs], static_cast<uint32_t>((raw_turn(j) - 1) & 1), p.waits.limit_ns));
                     if (!ok) break;
                     if (half == 0 && mine) S.cst[j % kPrCst][gl] = c;
                     if (half == 0 && lane == 0) S.gap[j % kPrCst] = n16 < kPrGroups || far ? 1u : 0u;
@@ -792,14 +835,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                     if (lane == 0) mbar_arrive_expect_tx(&S.rawfull[rs], n16 * 16u * D + p.waits.beyond);
                     __syncwarp();
                     if (mine && ids >= 0)
-                        bulk_load(sRaw + rs * (kTile / 2) + gl * 16u * D, (half ? p.c.v : p.c.k) + off, 16u * D, &S.rawfull[rs]);
+                        bulk_load(raw_at(j, static_cast<uint32_t>(half)) + gl * 16u * D, (half ? p.c.v : p.c.k) + off, 16u * D, &S.rawfull[rs]);
                     ++issued;
                 }
             }
             if (!ok) {  // its own copies in flight land before the block ends
                 if (lane == 0) atomicOr(&S.fault, 1u);
-                for (int32_t i = issued > kPrRaw ? issued - kPrRaw : 0; i < issued; ++i)
-                    mbar_wait_bounded(&S.rawfull[i & 1], static_cast<uint32_t>((i >> 1) & 1), p.waits.limit_ns);
+                for (int32_t i = issued > kPrRaw * raws ? issued - kPrRaw * raws : 0; i < issued; ++i)
+                    mbar_wait_bounded(&S.rawfull[raw_bar(i >> 1, static_cast<uint32_t>(i & 1))], static_cast<uint32_t>(raw_turn(i >> 1) & 1), p.waits.limit_ns);
             }
             meet<kMeetAll, kPrThreads>();
             return;
@@ -819,7 +862,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         int32_t scored[2] = {0, 0};  // score products of each row tile
         auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(b, parity, p.waits.limit_ns)); };
         auto scores = [&](int32_t i, int32_t j) {  // S_i = Q_i K_j^T
-            const uint64_t a0 = dq + static_cast<uint32_t>(i) * (kTile >> 4), b0 = dk + static_cast<uint32_t>(j & 1) * (kTile >> 4);
+            const uint64_t a0 = dq + (MODE == kAttnShared && dual ? 0u : static_cast<uint32_t>(i) * (kTile >> 4)), b0 = dk + static_cast<uint32_t>(j & 1) * (kTile >> 4);
             if (elect_one()) {
 #pragma unroll
                 for (uint32_t s = 0; s < D / 16; ++s)

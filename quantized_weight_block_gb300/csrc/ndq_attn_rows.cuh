@@ -200,10 +200,17 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
     // this CTA's share of the units: the units of requests 0, 1, ... end to end
     uint64_t total = 0, base = 0, u = 0, u_end = 0, ctas = 0;  // base: first unit of request r
     int64_t r = 0;
-    // (kAttnOwn) A unit is what one warp takes of a row tile, `chunk` tokens,
-    // and the warps take the units in turn.
+    // (kAttnOwn) A unit is what one warp takes of a row tile, `chunk` tokens.
+    // The warps take the next one from a counter: the CTAs start when SMs come
+    // free beside the prefix's kernel, the first ones long before the last.
+    // (What is computed does not depend on who computes it.)
     int64_t per = 0;
     int32_t chunk = kRowPair;
+    auto next_unit = [&]() -> uint64_t {
+        uint32_t n = 0;
+        if (lane == 0) n = atomicAdd(p.counters, 1u);
+        return __shfl_sync(0xffffffffu, n, 0);
+    };
     if constexpr (MODE == kAttnOwn) {
         attn_pdl_launch();  // (the join's CTAs find their rows meanwhile)
         // all requests' row tiles and tokens, from them the chunk, then every
@@ -238,7 +245,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         s_before[tid] = rows_scan(units, s_own[1], all);
         __syncthreads();
         total = all.b <= static_cast<uint64_t>(p.own_rows) ? all.a : 0;  // (always)
-        u = static_cast<uint64_t>(blockIdx.x) * kRowWarps + warp;
+        u = next_unit();
         u_end = total;
     } else {
     auto share = [&]() {  // false: none
@@ -758,7 +765,7 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
                         *reinterpret_cast<float4*>(dst + g * VB + 2 * s) =
                             make_float4(o[nt][s][e], o[nt][s][e + 2], o[nt][s + 1][e], o[nt][s + 1][e + 2]);
                 }
-            u += static_cast<uint64_t>(gridDim.x) * kRowWarps;
+            u = next_unit();
             continue;
         }
         // join the warps: row i's maximum, sum and values over the 8 warps in order
@@ -864,7 +871,15 @@ __global__ void __launch_bounds__(kRowThreads, RowSmem<D, NT>::kCtas) k_attn_row
         __syncthreads();           // s_m, s_l, the ring and s_last are free again
         u += static_cast<uint64_t>(cb - ca);
     }
-    if (MODE == kAttnOwn || p.prompt_rows > 0) attn_pdl_wait();  // (this launch ends no earlier than the prompt kernel that it runs beside)
+    if constexpr (MODE == kAttnOwn) {  // the last CTA to end leaves the counters zero
+        __syncthreads();
+        if (tid == 0 && atomicAdd(p.counters + 1, 1u) == gridDim.x - 1) {
+            p.counters[0] = 0u;
+            p.counters[1] = 0u;
+        }
+    }
+    // (kAttnOwn: one CTA waits for all, the others make room for those to come)
+    if (MODE == kAttnOwn ? blockIdx.x == 0 : p.prompt_rows > 0) attn_pdl_wait();  // (this launch ends no earlier than the prompt kernel that it runs beside)
 }
 
 // ---- launching ---------------------------------------------------------------
