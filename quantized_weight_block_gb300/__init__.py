@@ -731,6 +731,31 @@ def attention_prefix_kv8(q, cache: KvCache, block_table, kv_len, group_start, pr
     return out
 
 
+def _heads(name, x, y, w, T, D, dtype, out_dtype, gpu, stream):
+    """One side of qk_norm_rope: pointer, heads, stride, weight, output, its stride; and the output."""
+    if x is None:
+        if y is not None or w is not None:
+            raise ValueError(f"{name}_out and {name}_weight need {name}")
+        return None, 0, 0, None, None, 0, None
+    shape = x.shape
+    if x.dtype is not dtype or len(shape) != 3 or shape[0] != T or shape[2] != D or x.get_device() != gpu:
+        raise ValueError("q and k must have the same type, tokens and head_dim, on one device")
+    if w is not None:
+        if w.dtype is not _T.f32 or w.shape != (D,) or not w.is_contiguous() or w.get_device() != gpu:
+            raise ValueError(f"{name}_weight must be float32 [head_dim], contiguous, on {name}'s device")
+        w = w.data_ptr()
+    if y is None:
+        y = _made_for(stream, lambda: _torch().zeros(shape, dtype=out_dtype, device=x.device))
+        _returned(stream, y)
+    elif y.dtype is not out_dtype or y.shape != shape or y.get_device() != gpu:
+        raise ValueError(f"{name}_out must be {out_dtype}, of {name}'s shape, on its device")
+    H = shape[1]
+    xs, ys = x.stride(), y.stride()
+    if xs[2] != 1 or ys[2] != 1 or (H > 1 and (xs[1] != D or ys[1] != D)):
+        raise ValueError(f"{name} and {name}_out must have dense heads")
+    return (x.data_ptr(), H, xs[0] if T > 1 else H * D, w, y.data_ptr(), ys[0] if T > 1 else H * D, y)
+
+
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
                  q_out=None, k_out=None, out_dtype=None, stream=None):
     """Norm (with a weight) and rotation of the heads q [T, q_heads, D] and k
@@ -756,35 +781,16 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     if (positions.dtype is not c.i32 or positions.numel() != T or not positions.is_contiguous() or inv_freq.dtype is not c.f32
             or not inv_freq.is_contiguous()):
         raise ValueError("positions must be int32 [tokens] and inv_freq float32 [rot_dim / 2], both contiguous")
-    _same_device("qk_norm_rope", gpu, positions, inv_freq)
+    if gpu < 0 or positions.get_device() != gpu or inv_freq.get_device() != gpu:
+        raise ValueError("qk_norm_rope takes CUDA tensors on one device")
     if out_dtype is None:
         given = q_out if q_out is not None else k_out
         out_dtype = given.dtype if given is not None else dtype if dtype is not c.f32 else c.bf16
     if out_dtype is not c.bf16 and out_dtype is not c.f16:
         raise ValueError("qk_norm_rope writes bfloat16 or float16")
 
-    def side(name, x, y, w):
-        """The arguments of q or k: pointer, heads, stride, weight, output, its stride; and the output."""
-        if x is None:
-            if y is not None or w is not None:
-                raise ValueError(f"{name}_out and {name}_weight need {name}")
-            return None, 0, 0, None, None, 0, None
-        shape = x.shape
-        if x.dtype is not dtype or len(shape) != 3 or shape[0] != T or shape[2] != D or x.get_device() != gpu:
-            raise ValueError("q and k must have the same type, tokens and head_dim, on one device")
-        H = shape[1]
-        if w is not None and (w.dtype is not c.f32 or w.shape != (D,) or not w.is_contiguous() or w.get_device() != gpu):
-            raise ValueError(f"{name}_weight must be float32 [head_dim], contiguous, on {name}'s device")
-        if y is None:
-            y = _made_for(stream, lambda: _torch().zeros(shape, dtype=out_dtype, device=x.device))
-            _returned(stream, y)
-        elif y.dtype is not out_dtype or y.shape != shape or y.get_device() != gpu:
-            raise ValueError(f"{name}_out must be {out_dtype}, of {name}'s shape, on its device")
-        return (x.data_ptr(), H, _row_stride(name, x, H, D), None if w is None else w.data_ptr(), y.data_ptr(),
-                _row_stride(name, y, H, D), y)
-
-    qp, qh, qs, qw, qo, qos, q_out = side("q", q, q_out, q_weight)
-    kp, kh, ks, kw, ko, kos, k_out = side("k", k, k_out, k_weight)
+    qp, qh, qs, qw, qo, qos, q_out = _heads("q", q, q_out, q_weight, T, D, dtype, out_dtype, gpu, stream)
+    kp, kh, ks, kw, ko, kos, k_out = _heads("k", k, k_out, k_weight, T, D, dtype, out_dtype, gpu, stream)
     rc = _lib.ndq_qk_norm_rope(qp, qh, qs, kp, kh, ks, code, T, D, 2 * inv_freq.numel(), 1 if interleaved else 0,
                                positions.data_ptr(), inv_freq.data_ptr(), qw, kw, eps, qo, qos, ko, kos, c.code[out_dtype],
                                _raw_stream(stream, gpu))
