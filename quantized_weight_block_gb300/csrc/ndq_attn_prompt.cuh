@@ -38,6 +38,15 @@
 // products' operands 2 x 64 KB, the value products' 2 x 32 KB, converters and
 // copies 128 KB.)
 //
+// Modes.  kAttnAll: all that rows see, and the outputs.  kAttnShared: the tokens
+// that groups of requests share, for the rows of all requests of a group; units
+// are cut from a group's rows, every CTA plans the shares from the device's
+// arrays, whose row is whose and what it sees is looked up per row, and rows
+// leave parts.  kAttnOwn: requests' own tokens, joined with those parts.
+// Measured (kAttnShared, 256 rows a unit, 250 tiles, 8 heads, 144 CTAs of 14
+// tiles): 54 us, of 102000 cycles 25000 before the first scores, 8000 for the
+// first tile, 4400 for each other and 10000 for the parts' way out (135 KB a CTA).
+//
 // What a tile's rows do not all see is masked per element.  Tokens that no
 // row of the CTA sees enter as zeros; a NaN code of V that only some rows see
 // is taken out of the product and put into those rows at the end.
@@ -332,6 +341,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             S.parts = static_cast<uint32_t>(parts_here);
         };
         if (p.n_groups <= 32) {  // every warp for itself
+            // All requests' tokens but the shared ones, for which the kernel after
+            // this one reads the cache meanwhile, on the SMs that are left to it.
+            uint64_t own = 0;
+            for (int64_t r = tid; r < p.n_req; r += kPrThreads) own += static_cast<uint32_t>(p.kv_len[r] > 0 ? p.kv_len[r] : 0);
             SharedUnits x{};
             Group g{};
             if (lane < p.n_groups) {
@@ -339,10 +352,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 x = shared_units(p, g);
             }
             uint64_t units = static_cast<uint64_t>(x.units), work = units * steps_of(x);
-            // All requests' tokens but the shared ones, for which the kernel after
-            // this one reads the cache meanwhile, on the SMs that are left to it.
-            uint64_t own = 0;
-            for (int64_t r = tid; r < p.n_req; r += kPrThreads) own += static_cast<uint32_t>(p.kv_len[r] > 0 ? p.kv_len[r] : 0);
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) own += __shfl_xor_sync(0xffffffffu, own, d);
             if (lane == 0) S.tot[warp] = own;
@@ -374,7 +383,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             }
             set_chunk(units, work);
             // the smallest chunk whose CTAs still are one wave
-            if (units < sms && (work >> 31) == 0) {
+            if (p.n_groups == 1) {
+                const uint32_t ctas = units < sms ? static_cast<uint32_t>(sms) / static_cast<uint32_t>(units > 0 ? units : 1) : 1u, steps = __shfl_sync(0xffffffffu, steps_of(x), 0);
+                chunk = (steps + ctas - 1) / ctas;
+                chunk = chunk < kPrefixMinTiles ? kPrefixMinTiles : chunk;
+            } else if (units < sms && (work >> 31) == 0) {
                 uint32_t lo = static_cast<uint32_t>(work) / static_cast<uint32_t>(sms), hi = static_cast<uint32_t>(chunk);  // lo: too small, hi: will do
                 lo = lo < kPrefixMinTiles - 1 ? static_cast<uint32_t>(kPrefixMinTiles) - 1 : lo;
                 while (lo + 1 < hi) {

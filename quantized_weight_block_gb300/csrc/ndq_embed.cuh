@@ -12,6 +12,11 @@
 // segments on their way to shared memory while it decodes this one, and leaves
 // the outputs to one bulk store (lanes that store their own 32 bytes fill half
 // sectors, which caps the write rate), so that nothing waits for another warp.
+//
+// Measured: 16001 rows of 4096 values, q4_k to bfloat16: 37 us, 4.5 TB/s, 0.66
+// of the copy bandwidth, at 68 % issue: the decoders' instructions bound it (one
+// segment ahead, segments of 512 and divisions in every unit: 54 us).  One row:
+// 4.4 us, latency.
 #pragma once
 
 #include "ndq_device.cuh"
