@@ -285,7 +285,7 @@ int ndq_matmul_packed_batched(const ndq_matmul_desc *descs, int count, int64_t K
  * (finite; one binary32 rounding, none for 1), rounded once to out_dtype.
  * Only the rows that are asked for are read.  Same ownership, asynchrony and
  * error rules as ndq_dequantize_packed; y may overlap neither w nor ids.
- * V, K or n_tokens of 0 is valid; n_tokens * ceil(K / 256) is below 2^31. */
+ * V, K or n_tokens of 0 is valid; n_tokens * ceil(K / 1024) is below 2^31. */
 int ndq_embed_packed(int format_id, int64_t V, int64_t K, const uint8_t *w, size_t w_len, const void *ids, int ids_dtype,
                      int64_t n_tokens, float scale, int out_dtype, void *y, int64_t y_stride, void *stream);
 

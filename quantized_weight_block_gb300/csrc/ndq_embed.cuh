@@ -6,17 +6,19 @@
 // with the scale, one rounding to the output type.  Bound by bytes: a row's
 // payload read and its outputs written (2 or 4 bytes for about half a byte).
 //
-// Work.  The unit is a segment of 64 chunks of one token's row (1024 elements,
-// 512 of nvfp4), two chunks to a lane; warps take the segments of all tokens in
-// turn.  A warp is on its own: it keeps the 16-byte lines of its next three
-// segments on their way to shared memory while it decodes this one, and leaves
-// the outputs to one bulk store (lanes that store their own 32 bytes fill half
-// sectors, which caps the write rate), so that nothing waits for another warp.
+// Work.  The unit is a segment of 128 chunks of one token's row (2048 elements,
+// 1024 of nvfp4), four chunks to a lane; warps take the segments of all tokens in
+// turn.  A warp is on its own: it has the 16-byte lines of its next segment on
+// their way to shared memory while it decodes this one, and leaves the outputs to
+// one bulk store (lanes that store their own 32 bytes fill half sectors, which
+// caps the write rate), so that nothing waits for another warp.
 //
-// Measured: 16001 rows of 4096 values, q4_k to bfloat16: 37 us, 4.5 TB/s, 0.66
-// of the copy bandwidth, at 68 % issue: the decoders' instructions bound it (one
-// segment ahead, segments of 512 and divisions in every unit: 54 us).  One row:
-// 4.4 us, latency.
+// Measured: 16001 rows of 4096 values, q4_k to bfloat16: 31.7 us, 5.2 TB/s, 0.77
+// of the copy bandwidth; q8_0 36.5 us, 5.4 TB/s; q6_k 37.9 us, 4.8 TB/s.  What
+// bounds it is instructions: with one chunk to a lane it took 49.7 us, with two
+// 36.5 (68 % issue); divisions in every unit took 54 us before.  More segments on
+// their way (three, four) were slower: fewer CTAs fit an SM.  One row: 4.4 us,
+// latency.
 #pragma once
 
 #include "ndq_device.cuh"
@@ -26,8 +28,8 @@ namespace ndq {
 namespace {
 
 constexpr int kEmbedWarps = 4;
-constexpr int kEmbedChunks = 2;  // of a lane, in a segment
-constexpr int kEmbedStages = 4;  // packed segments of a warp in shared memory
+constexpr int kEmbedChunks = 4;  // of a lane, in a segment
+constexpr int kEmbedStages = 2;  // packed segments of a warp in shared memory
 
 template <int F>
 struct EmbedSeg {
