@@ -134,6 +134,16 @@ def test_step_groups_and_lengths(D, sizes, prefix, own):
     Case(sizes, prefix, own, [1] * len(own), 8, 2, D, 16).check()
 
 
+@pytest.mark.parametrize("groups,each,prefix", [(33, 2, 300), (40, 5, 700), (600, 3, 150)])
+@pytest.mark.parametrize("prompts", [False, True])
+def test_many_groups(groups, each, prefix, prompts):
+    # (more than 32 groups are planned by the whole block, more than 512 several to a thread; prefixes of 0 among them)
+    R = groups * each
+    lengths = [(37 * g) % prefix for g in range(groups)]
+    fresh = [40 if prompts and r % 50 == 7 else 1 for r in range(R)]
+    Case([each] * groups, lengths, own_lengths(R, 60), fresh, 8, 2, 64, 16, "int8").check()
+
+
 @pytest.mark.parametrize("heads", [(32, 8), (4, 4), (16, 1), (10, 2), (40, 1)])
 @pytest.mark.parametrize("code,D", [("e4m3", 128), ("int8", 64)])
 @pytest.mark.parametrize("sizes,prefix,own,fresh", [
