@@ -187,3 +187,18 @@ def test_on_another_stream():
     got, _ = ndq.qk_norm_rope(q, None, pos, f, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-36, 2.0 ** -100])
+@pytest.mark.parametrize("eps", [1e-19, 1e-20, 1e-24, 1e-40])
+def test_an_eps_far_above_the_squares(size, eps):
+    # (the squares vanish in binary32, the eps does not: it is the norm)
+    eps = torch.tensor(eps).item()
+    check(9, 6, 2, 128, 128, din=F32, size=size, eps=eps)
+    check(9, 6, 2, 64, 64, din=BF, size=size, eps=eps, interleaved=True)
+
+
+@pytest.mark.parametrize("size", [1e18, 1e30])
+def test_an_eps_beside_squares_that_overflow(size):
+    for eps in (1e-20, 1e30, 3e38):
+        check(9, 6, 2, 128, 128, din=F32, size=size, eps=torch.tensor(eps).item())
