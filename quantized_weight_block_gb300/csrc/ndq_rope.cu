@@ -18,9 +18,11 @@
 // Angles.  A binary32 product position * inv_freq is off by 2^-24 of itself:
 // radians, far out.  Here each frequency becomes a fraction of a turn in 64
 // bits (its mantissa times 2^64 / (2 pi), in integers), the product with the
-// position wraps by itself, and the top 32 bits are the angle to 2^-32 of a
-// turn for every position below 2^31.  The cosines of a token are computed once
-// a warp: its lane groups take different pairs and exchange them.
+// position wraps by itself, and the top 32 bits are the angle to 2^-31 of a
+// turn for every position below 2^31.  binary32 holds 24 of them: cosine and sine
+// are taken of the top ones and corrected by the rest (a + d: cos a - d sin a,
+// sin a + d cos a).  The cosines of a token are computed once a warp: its lane
+// groups take different pairs and exchange them.
 //
 // Measured: 16001 tokens of 40 heads of 128, bfloat16, with norms: 56 us, 5.9
 // TB/s, 0.86 of the copy bandwidth; 5003 tokens of 72 heads, binary32 in: 48 us,
@@ -38,6 +40,7 @@ namespace {
 
 constexpr int kRopeWarps = 4;
 constexpr int kRopeMaxDim = 256;
+constexpr float kRadians = 0x1.921fb6p-30f;  // 2 pi / 2^32
 // CTAs of an SM, and of the grid for each SM.  16001 tokens of 40 heads of 128,
 // bfloat16: 57.1 us with 6, 61.1 with 5, 65.7 as the compiler would have it (4),
 // and 59.5 against 61.1 when no CTA comes after the resident ones.
@@ -134,8 +137,15 @@ __global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas(IN)) k_rope(const _
                 c1[c] = 1.0f;
                 s1[c] = 0.0f;
                 if (turned && i < 8) {
-                    const uint64_t turn = S.turn[pair] * static_cast<uint32_t>(pos);
-                    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s1[c], &c1[c]);
+                    // 32 bits of a turn: the top 25 are the functions' angle (as binary32 exactly),
+                    // the other 7, at most 2^-26 of a turn, turn the result by themselves
+                    const uint32_t turn = static_cast<uint32_t>((S.turn[pair] * static_cast<uint32_t>(pos)) >> 32);
+                    const uint32_t top = (turn + 64u) & ~127u;
+                    const float rest = static_cast<float>(static_cast<int32_t>(turn - top)) * kRadians;
+                    float sf, cf;
+                    sincospif(static_cast<float>(static_cast<int32_t>(top)) * 0x1p-31f, &sf, &cf);
+                    c1[c] = __fmaf_rn(-sf, rest, cf);
+                    s1[c] = __fmaf_rn(cf, rest, sf);
                 }
             }
 #pragma unroll

@@ -202,3 +202,49 @@ def test_an_eps_far_above_the_squares(size, eps):
 def test_an_eps_beside_squares_that_overflow(size):
     for eps in (1e-20, 1e30, 3e38):
         check(9, 6, 2, 128, 128, din=F32, size=size, eps=torch.tensor(eps).item())
+
+
+def turns(pos, freq):
+    """pos * freq / (2 pi) modulo 1, in [-1/2, 1/2], rounded once to 64 bits (freq: a binary32 value)."""
+    one = 1 << 300
+
+    def atan_of_inverse(n):
+        term, total, i = one // n, 0, 0
+        while term:
+            total += (-1) ** i * (term // (2 * i + 1))
+            term //= n * n
+            i += 1
+        return total
+
+    pi = 4 * (4 * atan_of_inverse(5) - atan_of_inverse(239))
+    num, den = float(freq).as_integer_ratio()
+    t = pos * num * one * one // (den * 2 * pi) % one
+    return (t if t < one // 2 else t - one) / one
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_angles_next_to_multiples_of_a_quarter_turn(interleaved):
+    # Sines and cosines near 0 show the angle itself: with bfloat16 outputs they
+    # keep 2^-8 of themselves, the angle 2^-31 of a turn, and the functions,
+    # their correction and the rotation 2^-20 of the result.  The positions are numerators of
+    # convergents of pi (odd and even multiples of half a turn) and their multiples.
+    pos = [n * k for n in (355, 103993, 104348, 208341, 312689, 833719, 1146408, 4272943, 5419351, 80143857, 165707065, 245850922, 411557987) for k in (1, 2, 4)
+           if n * k < 1 << 31]
+    f = torch.tensor([s * 2.0 ** -i for i in range(16) for s in (1, -1)], device=DEV)
+    q = torch.zeros(len(pos), 1, 64, device=DEV)
+    q[..., 0:64:2] = 1.0
+    if not interleaved:
+        q = torch.cat([q[..., 0::2], q[..., 1::2]], -1).contiguous()
+    out, _ = ndq.qk_norm_rope(q, None, torch.tensor(pos, dtype=torch.int32, device=DEV), f, interleaved=interleaved, out_dtype=BF)
+    out = out[:, 0].double()
+    got_c, got_s = (out[:, 0::2], out[:, 1::2]) if interleaved else (out[:, :32], out[:, 32:])
+    t = torch.tensor([[turns(n, x) for x in f.tolist()] for n in pos], dtype=torch.float64, device=DEV)
+
+    def quarter(t):  # the sine of t turns, of the distance to the nearest half turn where that is small
+        n = (2 * t).round()
+        return torch.where(n % 2 == 0, 1.0, -1.0) * ((t - n / 2) * 2 * torch.pi).sin()
+
+    for got, want in ((got_s, quarter(t)), (got_c, quarter(t + 0.25))):
+        err = (got - want).abs()
+        bound = want.abs() * (2.0 ** -8 + 2.0 ** -20) + 2 * torch.pi * 2.0 ** -31
+        assert (err <= bound).all(), (float((err / bound).max()), (err > bound).nonzero()[:4].tolist())
