@@ -193,12 +193,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas(IN)) k_rope(const _
                     };
                     float sum = squares(), eps = p.eps;
                     // Squares that overflow or vanish (rare): the row is scaled by a power of two
-                    // first, so that the larger of its largest value and the root of eps, which
-                    // decide the norm, comes to [1, 2) (eps beside a vanishing row, scaled as the
-                    // row's largest value asks, would be infinite).
+                    // first, so that the larger of its largest value and the root of eps (by its
+                    // exponent), which decide the norm, comes to [1, 2) (eps beside a vanishing
+                    // row, scaled as the row's largest value asks, would be infinite).
                     const bool odd = sum > 0x1p120f || (sum < 0x1p-90f && p.eps < 0x1p-60f);
                     if (__any_sync(0xffffffffu, odd)) {
-                        float top = sqrtf(p.eps);
+                        float top = p.eps > 0.0f ? __uint_as_float((((__float_as_uint(p.eps) >> 23) + 127u) >> 1) << 23) : 0.0f;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             top = fmaxf(top, fmaxf(fmaxf(fabsf(a[e].x), fabsf(a[e].y)), fmaxf(fabsf(b[e].x), fabsf(b[e].y))));
