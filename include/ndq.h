@@ -284,7 +284,8 @@ int ndq_matmul_packed_batched(const ndq_matmul_desc *descs, int count, int64_t K
  * Each value is the binary32 decode of ndq_dequantize_packed, times scale
  * (finite; one binary32 rounding, none for 1), rounded once to out_dtype.
  * Only the rows that are asked for are read.  Same ownership, asynchrony and
- * error rules as ndq_dequantize_packed; y may overlap neither w nor ids.
+ * error rules as ndq_dequantize_packed; rows of y that overlap w or ids are
+ * refused with NDQ_ERR_BAD_ARG.
  * V, K or n_tokens of 0 is valid; n_tokens * ceil(K / 1024) is below 2^31. */
 int ndq_embed_packed(int format_id, int64_t V, int64_t K, const uint8_t *w, size_t w_len, const void *ids, int ids_dtype,
                      int64_t n_tokens, float scale, int out_dtype, void *y, int64_t y_stride, void *stream);
@@ -526,8 +527,9 @@ int ndq_attention_prefix_kv8(const ndq_kv_cache *cache, const void *q, int dtype
  *   q_weight, k_weight   device binary32 [head_dim], or NULL: no norm
  *   eps        finite, 0 or more
  *   q_out, k_out   device rows of out_dtype (NDQ_BFLOAT16 or NDQ_FLOAT16);
- *              q_out may be q (k_out k) with the same type and stride, and
- *              otherwise no output may overlap an input or the other output
+ *              q_out may be q (k_out k) with the same type and stride;
+ *              otherwise an output whose heads overlap an input or the other
+ *              output is refused with NDQ_ERR_BAD_ARG
  * Bases are 16-byte aligned and strides multiples of 8.  Heads of 0 are valid
  * (then that side's pointers are not looked at).  Angles are exact to 2^-31 of
  * a turn at every position; norms, products and sums are binary32 (squares

@@ -19,6 +19,7 @@
 #include "ndq_embed.h"
 #include "ndq_fused.h"
 #include "ndq_internal.h"
+#include "ndq_overlap.h"
 
 static_assert(NDQ_NOALLOC_MAX_TENSORS == ndq::kNoAllocMaxTensors, "no-allocation table size");
 
@@ -454,6 +455,9 @@ int ndq_embed_packed(int format_id, int64_t V, int64_t K, const uint8_t* w, size
     if (!ids || !y) return NDQ_ERR_NULL;
     const uintptr_t el = out_dtype == NDQ_FLOAT ? 4 : 2, ib = ids_dtype == NDQ_INT32 ? 4 : 8;
     if (reinterpret_cast<uintptr_t>(y) % el != 0 || reinterpret_cast<uintptr_t>(ids) % ib != 0) return NDQ_ERR_MISALIGNED;
+    const ndq::Rows out = {y, K * static_cast<int64_t>(el), n_tokens, y_stride * static_cast<int64_t>(el)};
+    if (overlap(out, ndq::Rows{w, static_cast<int64_t>(w_len)}) || overlap(out, ndq::Rows{ids, n_tokens * static_cast<int64_t>(ib)}))
+        return NDQ_ERR_BAD_ARG;
     if (V == 0) {  // (every id is outside the table, which has no payload to describe)
         p.w.fmt = kFormats[format_id].kfmt;
         p.w.B = static_cast<uint16_t>(fp8_row(format_id) ? 16 : kFormats[format_id].B);

@@ -1,0 +1,54 @@
+// ndq_overlap.h -- which memory of a call's arguments overlaps, for the host
+// checks.  Not part of the public ABI.
+#pragma once
+
+#include <cstdint>
+
+namespace ndq {
+
+// `rows` pieces of `bytes` each, one every `stride` bytes.
+struct Rows {
+    const void* p;
+    int64_t bytes;
+    int64_t rows = 1;
+    int64_t stride = 0;
+};
+
+namespace overlap_detail {
+using Wide = __int128;  // (strides of 2^42 bytes times 2^31 rows)
+
+inline Wide floor_div(Wide a, Wide b) { return a >= 0 ? a / b : -((-a + b - 1) / b); }
+
+// Rows a + i s (i < n, la bytes) and b + j s (j < m, lb bytes), d = a - b: with
+// k = i - j they overlap where -la < d + k s < lb.
+inline bool same_stride(Wide d, Wide s, int64_t n, int64_t la, int64_t m, int64_t lb) {
+    Wide k = s > 0 ? floor_div(-la - d, s) + 1 : 0;  // the first above -la
+    if (k < 1 - Wide(m)) k = 1 - Wide(m);
+    return k <= Wide(n) - 1 && d + k * s < lb && d + k * s > -la;
+}
+}  // namespace overlap_detail
+
+// Does a byte of a lie in b?  (Rows of one another's gaps do not.)
+inline bool overlap(const Rows& a, const Rows& b) {
+    using namespace overlap_detail;
+    if (a.bytes <= 0 || b.bytes <= 0 || a.rows <= 0 || b.rows <= 0) return false;
+    if (a.rows == 1 && b.rows == 1) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return x < y ? y - x < static_cast<uintptr_t>(a.bytes) : x - y < static_cast<uintptr_t>(b.bytes);
+    }
+    const Wide x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    const Wide x1 = x + Wide(a.rows - 1) * a.stride + a.bytes, y1 = y + Wide(b.rows - 1) * b.stride + b.bytes;
+    if (x1 <= y || y1 <= x) return false;
+    if (a.rows == 1 || b.rows == 1 || a.stride == b.stride)
+        return same_stride(x - y, a.rows == 1 ? b.stride : a.stride, a.rows, a.bytes, b.rows, b.bytes);
+    // strides apart: the rows of one against all of the other, from where they meet
+    const bool swap = a.rows > b.rows;
+    const Rows &u = swap ? b : a, &v = swap ? a : b;
+    const Wide u0 = swap ? y : x, v0 = swap ? x : y, v1 = swap ? x1 : y1;
+    Wide i = u0 + u.bytes > v0 ? 0 : floor_div(v0 - u0 - u.bytes, u.stride) + 1;
+    for (; i < u.rows && u0 + i * u.stride < v1; ++i)
+        if (same_stride(u0 + i * u.stride - v0, v.stride, 1, u.bytes, v.rows, v.bytes)) return true;
+    return false;
+}
+
+}  // namespace ndq

@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "ndq.h"
+#include "ndq_overlap.h"
 #include "ndq_rope.h"
 #include "ndq_serve.h"
 
@@ -48,16 +49,6 @@ int check_cache(const ndq_kv_cache* c, ndq::KvCache* d) {
     d->num_blocks = c->num_blocks;
     d->heads = c->kv_heads;
     return NDQ_OK;
-}
-
-// A piece of memory, of `bytes` (0: none).
-struct Piece {
-    const void* p;
-    int64_t bytes;
-};
-bool overlap(const Piece& a, const Piece& b) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < static_cast<uintptr_t>(a.bytes) : x - y < static_cast<uintptr_t>(b.bytes));
 }
 
 // Rows of dense heads, 16-byte aligned, `stride` elements of 2 bytes apart.
@@ -139,13 +130,13 @@ int ndq_kv_plan(const int32_t* cached, const int32_t* fresh, int64_t n_req, int 
     // The CTAs read the inputs while others write: an output may be neither an
     // input nor another output.  (Of the stack only the bottom is known here.)
     const int64_t entries = n_req * table_width;  // (below 2^62)
-    const Piece out[] = {{block_table, 4 * (entries < INT64_C(1) << 60 ? entries : INT64_C(1) << 60)}, {q_start, 4 * (n_req + 1)},
+    const ndq::Rows out[] = {{block_table, 4 * (entries < INT64_C(1) << 60 ? entries : INT64_C(1) << 60)}, {q_start, 4 * (n_req + 1)},
                          {kv_len, 4 * n_req}, {positions, 4 * n_tokens}, {slots, 8 * n_tokens}, {free_left, 4}};
-    const Piece in[] = {{cached, 4 * n_req}, {fresh, 4 * n_req}, {free_blocks, n_req > 0 ? 4 : 0}, {free_count, 4}};
+    const ndq::Rows in[] = {{cached, 4 * n_req}, {fresh, 4 * n_req}, {free_blocks, n_req > 0 ? 4 : 0}, {free_count, 4}};
     for (int i = 0; i < 6; ++i) {
         for (int j = 0; j < i; ++j)
             if (overlap(out[i], out[j])) return NDQ_ERR_BAD_ARG;
-        for (const Piece& x : in)
+        for (const ndq::Rows& x : in)
             if (overlap(out[i], x)) return NDQ_ERR_BAD_ARG;
     }
     ndq::PlanParams p{};
@@ -291,6 +282,24 @@ int ndq_qk_norm_rope(const void* q, int q_heads, int64_t q_stride, const void* k
         if (rc == NDQ_OK) rc = check_rows(s.y, s.y_stride, row);
         if (rc != NDQ_OK) return rc;
         if (s.x == s.y && (in_dtype != out_dtype || s.stride != s.y_stride)) return NDQ_ERR_BAD_ARG;
+    }
+    // An output may be its own input; otherwise it is read before and after it is
+    // written, by different warps.  (Rows that lie between one another's are apart:
+    // queries and keys of one fused projection.)
+    const int64_t el = in_dtype == NDQ_FLOAT ? 4 : 2;
+    ndq::Rows in[2], out[2];
+    for (int i = 0; i < 2; ++i) {
+        const int64_t row = static_cast<int64_t>(sides[i].heads) * head_dim, n = sides[i].heads > 0 ? n_tokens : 0;
+        in[i] = {sides[i].x, row * el, n, sides[i].stride * el};
+        out[i] = {sides[i].y, row * 2, n, sides[i].y_stride * 2};
+    }
+    const ndq::Rows small[] = {{positions, 4 * n_tokens}, {inv_freq, 2 * rot_dim}, {q_weight, q_heads > 0 && q_weight ? 4 * head_dim : 0},
+                               {k_weight, k_heads > 0 && k_weight ? 4 * head_dim : 0}};
+    if (overlap(out[0], out[1])) return NDQ_ERR_BAD_ARG;
+    for (int i = 0; i < 2; ++i) {
+        if ((in[i].p != out[i].p && overlap(out[i], in[i])) || overlap(out[i], in[1 - i])) return NDQ_ERR_BAD_ARG;
+        for (const ndq::Rows& x : small)
+            if (overlap(out[i], x)) return NDQ_ERR_BAD_ARG;
     }
     ndq::RopeParams p{};
     p.q = q;

@@ -248,3 +248,16 @@ def test_angles_next_to_multiples_of_a_quarter_turn(interleaved):
         err = (got - want).abs()
         bound = want.abs() * (2.0 ** -8 + 2.0 ** -20) + 2 * torch.pi * 2.0 ** -31
         assert (err <= bound).all(), (float((err / bound).max()), (err > bound).nonzero()[:4].tolist())
+
+
+def test_inputs_and_outputs_between_one_another_in_one_buffer():
+    g = torch.Generator(device=DEV).manual_seed(3)
+    row = torch.randn(33, 20, 64, device=DEV, generator=g).to(BF)
+    q, k, qo, ko = row[:, :6], row[:, 8:10], row[:, 10:16], row[:, 17:19]
+    pos, f, w = torch.arange(33, dtype=torch.int32, device=DEV), freqs(64), torch.ones(64, device=DEV)
+    want = ndq.qk_norm_rope(q.clone(), k.clone(), pos, f, w, w)
+    rest = row[:, [6, 7, 16, 19]].clone()
+    ndq.qk_norm_rope(q, k, pos, f, w, w, q_out=qo, k_out=ko)
+    assert torch.equal(qo, want[0]) and torch.equal(ko, want[1]) and torch.equal(row[:, [6, 7, 16, 19]], rest)
+    with pytest.raises(ndq.NdqError):
+        ndq.qk_norm_rope(q, k, pos, f, w, w, q_out=row[:, 4:10], k_out=ko)

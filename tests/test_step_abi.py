@@ -159,3 +159,38 @@ def test_other_tensors_are_refused(name, change, launches):
     with pytest.raises(ValueError):
         getattr(ndq, name)(**args)
     assert launches == []
+
+
+# ---- outputs over inputs: refused before any launch ------------------------------
+
+Q, K_, Q_OUT, K_OUT, POS, FREQ, QW, KW = (i << 20 for i in range(1, 9))  # far apart
+
+
+def apart(**kw):
+    return rope(**dict(q=Q, k=K_, q_out=Q_OUT, k_out=K_OUT, positions=POS, inv_freq=FREQ, q_weight=QW, k_weight=KW) | kw)
+
+
+ROW, KROW = 8 * 128 * 2, 2 * 128 * 2  # bytes of a token's heads
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_out=Q + 16), dict(q_out=Q + 3 * ROW - 16), dict(q_out=Q - 3 * ROW + 16), dict(q_out=K_), dict(q_out=K_ + 3 * KROW - 16),
+    dict(k_out=Q), dict(k_out=K_ + KROW), dict(k_out=Q_OUT), dict(k_out=Q_OUT + 3 * ROW - 16), dict(k_out=Q_OUT - 3 * KROW + 16),
+    dict(q_out=POS), dict(k_out=POS - 3 * KROW + 16), dict(q_out=FREQ + 240), dict(k_out=FREQ), dict(q_out=QW + 496), dict(k_out=QW), dict(q_out=KW),
+    dict(k_out=KW), dict(q_out=Q, in_dtype=F32, q_stride=2048), dict(q=Q, q_out=Q, k=Q + 16, k_out=K_OUT),
+    # rows of one buffer: the same stride and heads that meet, other strides
+    dict(q_stride=1536, k=Q + ROW - 16, k_stride=1536, q_out=Q, q_out_stride=1536), dict(q_stride=1536, q_out=Q + ROW, q_out_stride=1536),
+    dict(q_stride=4096, q_out=Q + ROW, q_out_stride=1536), dict(q_stride=4096, q_out=Q + ROW, q_out_stride=3584),
+    dict(in_dtype=F32, q_stride=2048, q_out=Q + 4096, q_out_stride=2048)])
+def test_rope_outputs_over_inputs_are_refused(kw):
+    assert apart(**kw) == BAD_ARG
+
+
+W, IDS, Y = 1 << 20, 2 << 20, 3 << 20
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=W), dict(y=W + 678), dict(y=W - 3 * 128 + 2), dict(y=IDS), dict(y=IDS - 126), dict(y=IDS + 8), dict(y=IDS - 256, y_stride=128, n_tokens=3),
+    dict(y=IDS - 2 * 65536 - 64, y_stride=32768), dict(y=IDS + 20, ids_dtype=ndq.NDQ_INT64), dict(out_dtype=F32, y=IDS - 764)])
+def test_embed_outputs_over_inputs_are_refused(kw):
+    assert embed(**dict(w=W, ids=IDS, y=Y) | kw) == BAD_ARG
