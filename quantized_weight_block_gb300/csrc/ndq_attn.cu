@@ -1,5 +1,6 @@
 // ndq_attn.cu -- launcher of attention over the 8-bit cache.
 #include "ndq_attn_rows.cuh"
+#include "ndq_once.h"
 
 namespace ndq {
 namespace {
@@ -9,18 +10,14 @@ constexpr int kMaxDevices = 64;
 }  // namespace
 
 int launch_attention(AttnParams p, int head_dim, bool e4m3, bool bf16, void* stream) {
-    static int sms_of[kMaxDevices];
+    static Once sms_of[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return static_cast<int>(e);
     if (dev < 0 || dev >= kMaxDevices) return static_cast<int>(cudaErrorInvalidDevice);
-    if (sms_of[dev] == 0) {
-        int sms = 0;
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return static_cast<int>(e);
-        sms_of[dev] = sms;
-    }
-    const int sms = sms_of[dev];
+    int sms = 0;
+    const int se = sms_of[dev].get([&](int* n) { return static_cast<int>(cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev)); }, &sms);
+    if (se != 0) return se;
     if (p.max_q > p.n_tokens) p.max_q = p.n_tokens;
     const IqGrids* grids = nullptr;
     if (const int rc = device_symbols(dev, &p.fault, &grids)) return rc;

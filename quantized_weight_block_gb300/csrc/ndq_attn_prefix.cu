@@ -1,6 +1,7 @@
 // ndq_attn_prefix.cu -- attention of requests that share prefixes: the kernel of
 // the shared prefixes, and the launcher of all.
 #include "ndq_attn_prompt.cuh"
+#include "ndq_once.h"
 
 namespace ndq {
 
@@ -16,18 +17,15 @@ int launch_prefix_shared(const PrefixParams& p, int head_dim, bool e4m3, bool bf
 }
 
 int launch_attention_prefix(PrefixParams p, int head_dim, bool e4m3, bool bf16, void* stream) {
-    static int sms_of[64];
+    static Once sms_of[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return static_cast<int>(e);
     if (dev < 0 || dev >= 64) return static_cast<int>(cudaErrorInvalidDevice);
-    if (sms_of[dev] == 0) {
-        int sms = 0;
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return static_cast<int>(e);
-        sms_of[dev] = sms;
-    }
-    p.sms = sms_of[dev] < kPrefixMaxExtra ? sms_of[dev] : kPrefixMaxExtra;
+    int sms = 0;
+    const int se = sms_of[dev].get([&](int* n) { return static_cast<int>(cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev)); }, &sms);
+    if (se != 0) return se;
+    p.sms = sms < kPrefixMaxExtra ? sms : kPrefixMaxExtra;
     if (p.max_q > p.n_tokens) p.max_q = p.n_tokens;
     const IqGrids* grids = nullptr;
     if (const int rc = device_symbols(dev, &p.fault, &grids)) return rc;

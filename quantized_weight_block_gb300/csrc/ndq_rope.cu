@@ -33,6 +33,7 @@
 
 #include "ndq_attn.cuh"
 #include "ndq_device.cuh"
+#include "ndq_once.h"
 #include "ndq_rope.h"
 
 namespace ndq {
@@ -284,16 +285,14 @@ RopeFn rope_of(int in, bool bf16) {
 }  // namespace
 
 int launch_rope(RopeParams p, int in, bool bf16, void* stream) {
-    static int sms_of[64];
+    static Once sms_of[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return static_cast<int>(e);
     if (dev < 0 || dev >= 64) return static_cast<int>(cudaErrorInvalidDevice);
-    if (sms_of[dev] == 0) {
-        int sms = 0;
-        if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return static_cast<int>(e);
-        sms_of[dev] = sms;
-    }
+    int sms = 0;
+    const int se = sms_of[dev].get([&](int* n) { return static_cast<int>(cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev)); }, &sms);
+    if (se != 0) return se;
     int L = 1;
     while (L * 16 < p.head_dim) L *= 2;
     RopeFn fn = nullptr;
@@ -305,12 +304,12 @@ int launch_rope(RopeParams p, int in, bool bf16, void* stream) {
         default: fn = rope_of<16>(in, bf16); break;
     }
     // few tokens: their heads over several warps, one round of a warp's heads to a warp at least
-    const int64_t warps = static_cast<int64_t>(sms_of[dev]) * 16, rounds = (p.q_heads + p.k_heads + 32 / L - 1) / (32 / L);
+    const int64_t warps = static_cast<int64_t>(sms) * 16, rounds = (p.q_heads + p.k_heads + 32 / L - 1) / (32 / L);
     int64_t parts = warps / p.n_tokens;
     if (parts > rounds) parts = rounds;
     if (parts < 1) parts = 1;
     p.parts = static_cast<int32_t>(parts);
-    const int64_t want = (p.n_tokens * parts + kRopeWarps - 1) / kRopeWarps, most = static_cast<int64_t>(sms_of[dev]) * rope_ctas(in);
+    const int64_t want = (p.n_tokens * parts + kRopeWarps - 1) / kRopeWarps, most = static_cast<int64_t>(sms) * rope_ctas(in);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(want < most ? want : most));
     cfg.blockDim = dim3(kRopeWarps * 32);

@@ -125,3 +125,48 @@ def test_on_another_stream(orc):
     y = ndq.embed_packed(fmt, w, V, K, ids, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert_bit_exact(words(y), words(expected(orc, fmt, (V, K), x, ids.cpu(), 1.0, "bfloat16")), "bfloat16")
+
+
+FIRST_CALLS = """
+import sys, threading
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch, synth
+import quantized_weight_block_gb300 as ndq
+from test_gpu_embed import FORMATS
+K, T, V = 4096, 300, 24
+work = []
+for fmt in FORMATS:
+    w = torch.from_numpy(synth.payload(fmt, (V, K), seed=1)).cuda()
+    work.append((fmt, w, torch.arange(T, device="cuda") % V))
+torch.cuda.synchronize()
+got, gate = [[None] * len(work) for _ in range(8)], threading.Barrier(8)
+
+def run(i):
+    for j, (fmt, w, ids) in enumerate(work):
+        gate.wait()
+        try:
+            got[i][j] = ndq.embed_packed(fmt, w, V, K, ids)
+        except Exception as e:
+            got[i][j] = e
+
+threads = [threading.Thread(target=run, args=(i,)) for i in range(8)]
+for t in threads: t.start()
+for t in threads: t.join()
+torch.cuda.synchronize()
+for j, (fmt, w, ids) in enumerate(work):
+    want = ndq.embed_packed(fmt, w, V, K, ids)
+    for i in range(8):
+        assert isinstance(got[i][j], torch.Tensor), (fmt, got[i][j])
+        assert torch.equal(got[i][j].view(torch.int16), want.view(torch.int16)), fmt
+print("ok")
+"""
+
+
+def test_first_calls_of_several_threads_at_once():
+    # (in a process of its own, where no format has been asked for yet)
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=os.path.dirname(tests), tests=tests)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout[-500:] + r.stderr[-1500:]
