@@ -380,3 +380,24 @@ def test_without_groups_it_is_attention_over_the_cache():
     a = ndq.attention_prefix_kv8(c.q, c.cache(), q_start=dev32(c.start), **args)
     b = ndq.attention_kv8(c.q, c.cache(), args["block_table"], args["kv_len"], q_start=dev32(c.start))
     assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_calls_of_different_shapes_take_turns_on_one_workspace():
+    # other tokens, heads and head sizes lay the workspace out anew: nothing that an earlier call left may be read
+    cases = [Case([4], [700], [300, 40, 0, 500], [1] * 4, 32, 8, 128, 16, seed=91),
+             Case([5, 2], [2000, 333], own_lengths(7, 400, 2), [3, 1, 4, 1, 30, 2, 6], 8, 2, 64, 32, "int8", F16, seed=92),
+             Case([40], [900], own_lengths(40, 200, 3), [1] * 40, 16, 1, 128, 64, seed=93),
+             Case([3], [1500], [5, 300, 0], [17, 40, 33], 10, 2, 128, 16, seed=94),
+             Case([1] * 35 + [3], [200 + 7 * g for g in range(36)], own_lengths(38, 50, 4), [1] * 38, 4, 4, 64, 16, seed=95)]
+    need = [ndq.ndq_attention_prefix_workspace_bytes(c.D, c.q.shape[0], c.Hq, c.kc.shape[1]) for c in cases]
+    ws = torch.full((max(need),), 0xff, dtype=torch.uint8, device=DEV)
+    ws[:4096] = 0
+    want = [c.reference() for c in cases]
+    caches, args = [c.cache() for c in cases], [c.args() for c in cases]
+    for i in (0, 1, 2, 3, 4, 3, 0, 4, 2, 1, 0, 0, 2):
+        c = cases[i]
+        lse = torch.zeros(c.q.shape[:2], device=DEV)
+        out = ndq.attention_prefix_kv8(c.q, caches[i], q_start=dev32(c.start), max_q=max(c.fresh), lse=lse, workspace=ws, **args[i])
+        assert ((out.double() - want[i][0]).abs() <= want[i][1]).all(), i
+        assert ((lse.double() - want[i][2]).abs() <= 2.0 ** -18 * (1 + want[i][2].abs()) + 2.0 ** -18 * 40).all(), i
+        assert int(ws[:4096].count_nonzero()) == 0

@@ -90,6 +90,19 @@ def test_prefix_workspace_sizes():
     assert bytes_for(n=1000) >= 1000 * 8 * (16 + 130 * 4) + 192 * 256 * 130 * 4
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,heads,kv", [(1, 1, 1), (7, 8, 2), (64, 32, 8), (1000, 40, 8), (16001, 64, 8)])
+def test_prefix_workspace_holds_every_part(D, n, heads, kv):
+    # a part: D values, maximum, sum and two words to make rows of 16 bytes; a
+    # record of 16 and one of 8 bytes a row.  Parts: two a row of the prefix (units of 128 rows and
+    # fewer), 256 rows for each of 192 CTAs beyond one a unit; one a row of the
+    # own tokens, 16 rows for each of 8 warps of 512 CTAs beyond one a row tile.
+    rows, part = n * heads, 4 * (D + 4)
+    need = rows * (16 + 8) + part * (2 * rows + 192 * 256) + part * (rows + 512 * 8 * 16)
+    got = ndq.ndq_attention_prefix_workspace_bytes(D, n, heads, kv)
+    assert 0 <= got - ndq.ndq_attention_workspace_bytes(D) - need <= 4 * 256  # (and each region on 256 bytes)
+
+
 # ---- the tensor calls -----------------------------------------------------------
 
 BF, I32 = torch.bfloat16, torch.int32
