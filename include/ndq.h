@@ -494,16 +494,23 @@ int ndq_attention_kv8(const ndq_kv_cache *cache, const void *q, int dtype, int64
  * no query of theirs sees that block.  Queries may sit inside the prefix and
  * windows end in it.  The other arguments, and what the outputs hold, are
  * ndq_attention_kv8's; the parts are joined in binary32.  A group of one,
- * prefixes of 0 and n_groups of 0 are valid.  Where sharing saves little (less
- * than 128 MB if every request but one a group had a full table, or requests of
- * 128 rows a cache head and more on average, whose products are the work) the
- * call is ndq_attention_kv8's itself.
+ * prefixes of 0 and n_groups of 0 are valid.
+ * The call is ndq_attention_kv8's itself where sharing would read less than
+ * 128 MB less if every request but one a group had a full table, and where the
+ * requests have 128 rows and more a cache head on average (n_tokens * q_heads /
+ * kv_heads / n_req), as prompt chunks do, whose products are the work.  The host
+ * knows neither lengths nor how the rows are dealt out, and windows are not
+ * looked at.  So a long chunk among many single tokens takes the sharing from all
+ * of them (in a call of its own it does not), and where windows are far shorter
+ * than the prefix, or tables far wider than the lengths, ndq_attention_kv8 is the
+ * faster call.
  *   workspace  device buffer of ndq_attention_prefix_workspace_bytes(head_dim,
  *              n_tokens, q_heads, kv_heads) bytes or more, 256-byte aligned,
  *              its first 4096 bytes zeroed once before its first use (each call
  *              leaves them zero), not shared by calls that may overlap; one
  *              sized for some n_tokens and heads serves any call that needs no
- *              more bytes.  (0 bytes: the sizes are refused.) */
+ *              more bytes, of the shared path, whichever the call takes.
+ *              (0 bytes: the sizes are refused.) */
 size_t ndq_attention_prefix_workspace_bytes(int head_dim, int64_t n_tokens, int q_heads, int kv_heads);
 int ndq_attention_prefix_kv8(const ndq_kv_cache *cache, const void *q, int dtype, int64_t n_tokens, int q_heads,
                              int64_t q_stride, const int32_t *block_table, int64_t table_width, const int32_t *kv_len,
@@ -525,7 +532,7 @@ int ndq_attention_prefix_kv8(const ndq_kv_cache *cache, const void *q, int dtype
  *              token whose position is negative are not written
  *   inv_freq   device binary32 [rot_dim / 2], magnitudes up to 1
  *   q_weight, k_weight   device binary32 [head_dim], or NULL: no norm
- *   eps        finite, 0 or more
+ *   eps        finite, 0 or more (with 0 a head of zeros gives NaN)
  *   q_out, k_out   device rows of out_dtype (NDQ_BFLOAT16 or NDQ_FLOAT16);
  *              q_out may be q (k_out k) with the same type and stride;
  *              otherwise an output whose heads overlap an input or the other
@@ -583,9 +590,9 @@ int ndq_lora_add(const void *x_bf16, int64_t M, int64_t K, const void *lora_a, c
  * 2000000. */
 int ndq_test_withhold_copy(int64_t tile, uint32_t wait_limit_us);
 
-/* The same for the serving operators: the NEXT ndq_attention_kv8 or
- * ndq_lora_add launched by the calling host thread waits for 16 bytes more
- * than each of its staged copies brings, as if none had landed, and for at
+/* The same for the serving operators: the NEXT ndq_attention_kv8,
+ * ndq_attention_prefix_kv8 or ndq_lora_add launched by the calling host thread
+ * waits for 16 bytes more than each of its staged copies brings, as if none had landed, and for at
  * most `wait_limit_us` microseconds (1000 to 2000000) instead of 2 s.  Its
  * waits run out, its kernels set their bits in the fault word (8: prompt
  * attention, 16: adapter tiles, 32: few-row attention) and end; its outputs

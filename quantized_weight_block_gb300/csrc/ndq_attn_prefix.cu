@@ -31,11 +31,18 @@ int launch_attention_prefix(PrefixParams p, int head_dim, bool e4m3, bool bf16, 
     if (const int rc = device_symbols(dev, &p.fault, &grids)) return rc;
     // Where sharing saves little: what it can save at most (what the host knows
     // are the tables' widths), or requests whose own rows fill the prompt
-    // kernel's tiles, so that its products are the work.  Measured, shared beside
-    // not (32 heads of 128 on 8, steps): 16 requests behind 2000 tokens (saves
-    // 69 MB) 31 beside 27 us, behind 4000 (131 MB) 35 beside 35, 64 behind 1000
-    // (169 MB) 35 beside 40, behind 32000 106 beside 513; eight requests behind
-    // 4000 of 96 rows each 77 beside 86, of 256 106 beside 95, of 512 143 beside 100.
+    // kernel's tiles, so that its products are the work.  Measured in us, shared
+    // beside not, of 32 heads of 128 on 8 | 64 of 64 on 8 | 8 of 128 on 8, steps:
+    // 16 requests behind 2000 tokens 34 beside 27 | 31 beside 22 | 32 beside 27,
+    // behind 4000 (131 | 66 | 131 MB to save at most) 36 beside 35 | 34 beside 27
+    // | 34 beside 35, 64 behind 1000 (169 | 85 | 169 MB) 35 beside 40 | 31 beside
+    // 33 | 33 beside 40, behind 32000 91 beside 519 | 88 beside 357 | 65 beside
+    // 503; eight requests behind 4000, 32 heads of 128 on 8, of 96 rows each 83
+    // beside 87, of 256 118 beside 101, of 512 150 beside 102.
+    // What the numbers do not tell: the rows are an average (64 single tokens and
+    // a chunk of 2048 behind 32000 take 1.92 ms, unshared, and 1.22 ms in two
+    // calls), and windows (64 behind 32000: with one of 500 tokens 51 beside 31,
+    // of 2048 137 beside 58, of 4096 116 beside 88, of 8192 139 beside 149).
     const int64_t groups = p.n_groups < p.n_req ? p.n_groups : p.n_req;
     const double saved = static_cast<double>(p.n_req - groups) * static_cast<double>(p.width << p.c.bs_log2) * (2.0 * head_dim * p.c.heads);
     if (saved < kPrefixMinSaved || p.n_tokens * p.group >= kPrefixMostRows * p.n_req) return launch_attention(p, head_dim, e4m3, bf16, stream);

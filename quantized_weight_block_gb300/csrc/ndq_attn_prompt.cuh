@@ -43,9 +43,10 @@
 // are cut from a group's rows, every CTA plans the shares from the device's
 // arrays, whose row is whose and what it sees is looked up per row, and rows
 // leave parts.  kAttnOwn: requests' own tokens, joined with those parts.
-// Measured (kAttnShared, 256 rows a unit, 250 tiles, 8 heads, 144 CTAs of 14
-// tiles): 54 us, of 102000 cycles 25000 before the first scores, 8000 for the
-// first tile, 4400 for each other and 10000 for the parts' way out (135 KB a CTA).
+// Measured (kAttnShared, 256 rows a unit, 250 tiles, 8 heads; 88 CTAs of 22 or 23
+// tiles, the other SMs left to the own tokens): 75 us with cold caches, 25600
+// cycles before the first scores, 7400 for the first tile, 4400 for each other
+// and 10000 for the parts' way out (135 KB a CTA).
 //
 // What a tile's rows do not all see is masked per element.  Tokens that no
 // row of the CTA sees enter as zeros; a NaN code of V that only some rows see

@@ -14,11 +14,12 @@
 // caps the write rate), so that nothing waits for another warp.
 //
 // Measured: 16001 rows of 4096 values, q4_k to bfloat16: 31.7 us, 5.2 TB/s, 0.77
-// of the copy bandwidth; q8_0 36.5 us, 5.4 TB/s; q6_k 37.9 us, 4.8 TB/s.  What
-// bounds it is instructions: with one chunk to a lane it took 49.7 us, with two
-// 36.5 (68 % issue); divisions in every unit took 54 us before.  More segments on
-// their way (three, four) were slower: fewer CTAs fit an SM.  One row: 4.4 us,
-// latency.
+// of the copy bandwidth; q8_0 36.6 us, 5.4 TB/s; q6_k 37.9 us, 4.8 TB/s; 8000
+// rows, q4_0 to binary32: 28.7 us, 5.2 TB/s.  What bounds it is instructions (22 M
+// of a warp, 62 % issue) beside the waits that 20 warps an SM leave open (five
+// CTAs of 45 KB): with one chunk to a lane it took 49.7 us, with two 36.5 (30 M,
+// 68 % issue); divisions in every unit took 54 us before.  More segments on their
+// way (three, four) were slower: fewer CTAs fit an SM.  One row: 4.4 us, latency.
 #pragma once
 
 #include "ndq_device.cuh"

@@ -24,8 +24,8 @@
 // sin a + d cos a).  The cosines of a token are computed once a warp: its lane
 // groups take different pairs and exchange them.
 //
-// Measured: 16001 tokens of 40 heads of 128, bfloat16, with norms: 56 us, 5.9
-// TB/s, 0.86 of the copy bandwidth; 5003 tokens of 72 heads, binary32 in: 48 us,
+// Measured: 16001 tokens of 40 heads of 128, bfloat16, with norms: 56.4 us, 5.8
+// TB/s, 0.86 of the copy bandwidth; 5003 tokens of 72 heads, binary32 in: 48.9 us,
 // 5.7 TB/s.  64 tokens: 5.4 us, latency.
 #include <cuda_runtime.h>
 
