@@ -44,6 +44,7 @@ class AttentionLayer:
         self.scales = torch.linspace(0.5, 1.5, adapters, device=device)
         self.cache = ndq.KvCache.empty(num_blocks, kv_heads, block_size, head_dim, code, device)
         self.workspace = ndq.attention_workspace(0, 0, q_heads, self.cache)
+        self.shared_workspace, self.shared_tokens = None, -1  # made for the largest step so far
         # rotation by position after the norms of the query and key heads
         self.inv_freq = None
         if rotate:
@@ -77,7 +78,11 @@ class AttentionLayer:
             o = ndq.attention_kv8(q, self.cache, block_table, plan.kv_len, q_start=plan.q_start, max_q=max_q,
                                   workspace=self.workspace).flatten(1)
         else:
-            o = ndq.attention_prefix_kv8(q, self.cache, block_table, plan.kv_len, *shared, q_start=plan.q_start, max_q=max_q).flatten(1)
+            if q.shape[0] > self.shared_tokens:
+                self.shared_workspace = ndq.attention_prefix_workspace(self.cache, q.shape[0], self.q_heads)
+                self.shared_tokens = q.shape[0]
+            o = ndq.attention_prefix_kv8(q, self.cache, block_table, plan.kv_len, *shared, q_start=plan.q_start, max_q=max_q,
+                                         workspace=self.shared_workspace).flatten(1)
         y = ndq.matmul_packed(self.fmt, self.w["o"], self.hidden, self.q_heads * self.head_dim, o)
         return self.project("o", y, o, adapter)
 

@@ -261,3 +261,16 @@ def test_inputs_and_outputs_between_one_another_in_one_buffer():
     assert torch.equal(qo, want[0]) and torch.equal(ko, want[1]) and torch.equal(row[:, [6, 7, 16, 19]], rest)
     with pytest.raises(ndq.NdqError):
         ndq.qk_norm_rope(q, k, pos, f, w, w, q_out=row[:, 4:10], k_out=ko)
+
+
+def test_a_head_of_zeros_without_eps():
+    q = torch.randn(3, 4, 128, device=DEV).to(BF)
+    q[1, 2] = 0.0
+    pos, f, w = torch.arange(3, dtype=torch.int32, device=DEV), freqs(128), torch.ones(128, device=DEV)
+    none, _ = ndq.qk_norm_rope(q, None, pos, f, w, eps=0.0)  # 0 / 0
+    nan = torch.zeros(3, 4, dtype=torch.bool, device=DEV)
+    nan[1, 2] = True
+    assert none[nan].isnan().all() and torch.isfinite(none[~nan]).all()
+    for eps in (1e-6, 1e-20, 1e-44):
+        some, _ = ndq.qk_norm_rope(q, None, pos, f, w, eps=eps)
+        assert not some[1, 2].any() and torch.isfinite(some).all()
